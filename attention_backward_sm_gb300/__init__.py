@@ -318,3 +318,7 @@ def backward_lse(q, k, v, o, do, lse, cu_q_dev, cu_kv_dev, cu_q_host, cu_kv_host
     if check:
         fa_check_device_status(stream)
     return dq, dk, dv
+
+
+from .paged import (FA_KV_BF16, FA_KV_E4M3, KvPlan, decode, fa_decode, fa_decode_workspace_size,  # noqa: E402,F401
+                    fa_kv_append, fa_kv_plan, kv_append, kv_plan)

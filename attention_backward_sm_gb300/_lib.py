@@ -16,6 +16,7 @@ _p = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 SIGNATURES = {
     "fa_fwd_stats": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p]),
     "fa_fwd_stats_gqa": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p]),
@@ -34,6 +35,11 @@ SIGNATURES = {
     "fa_bwd_dq_finalize": (_i, [_p, _p, _i, _i, _i, _f, _p]),
     "fa_bwd_noalloc": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p,
                             _i, _i, _i, _i, _i, _i, _f, _p]),
+    "fa_kv_plan": (_i, [_p, _ll, _i, _p, _p, _p, _i, _p, _i, _i, _i, _p, _p, _p, _p, _p, _p]),
+    "fa_kv_append": (_i, [_p, _p, _ll, _ll, _p, _i, _p, _p, _i, _p, _p, _ll, _ll, _ll, _i, _i, _i, _i, _p]),
+    "fa_decode_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "fa_decode": (_i, [_p, _ll, _p, _p, _i, _p, _p, _ll, _ll, _ll, _i, _i, _p, _ll, _i, _p, _i, _i, _i, _i, _i, _f,
+                       _p, _p, _p, _sz, _p]),
     "fa_selftest_wait_timeout": (_i, [_p]),
     "fa_check_device_status": (_i, [_p]),
     "fa_last_error": (ctypes.c_char_p, []),

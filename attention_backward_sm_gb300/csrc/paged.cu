@@ -1,0 +1,441 @@
+// Paged key/value cache: C entry points, and the kernels that give new
+// tokens their places in the cache (plan) and write them there (append).
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "../../include/fabwd.h"
+#include "internal.h"
+#include "paged.h"
+
+namespace {
+
+using fa::set_last_error;
+
+int ok() { return set_last_error(FA_OK, "%s", ""); }
+
+int cuda_fail(cudaError_t e, const char* where) {
+  return set_last_error(FA_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+int check_device() {
+  static std::atomic<unsigned long long> ok_mask{0};   // devices already found to be sm_103
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (bit && (ok_mask.load(std::memory_order_acquire) & bit)) return FA_OK;
+  int major = 0, minor = 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (major != 10 || minor != 3)
+    return set_last_error(FA_ERR_UNSUPPORTED, "this library is built for sm_103a; device %d is sm_%d%d", dev, major,
+                          minor);
+  if (bit) ok_mask.fetch_or(bit, std::memory_order_release);
+  return FA_OK;
+}
+
+// The cache's sizes, strides and types; pointers only where they are set.
+int check_cache(const fa::PagedCache& c, int kv_type) {
+  if (kv_type != FA_KV_BF16 && kv_type != FA_KV_E4M3)
+    return set_last_error(FA_ERR_INVALID_ARG, "kv_type must be 0 (bf16) or 1 (e4m3), got %d", kv_type);
+  if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
+    return set_last_error(FA_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256, got %d", c.head_dim);
+  if (c.heads_kv < 1) return set_last_error(FA_ERR_INVALID_ARG, "heads_kv must be >= 1, got %d", c.heads_kv);
+  if (c.num_pages < 0) return set_last_error(FA_ERR_INVALID_ARG, "num_pages must be >= 0, got %d", c.num_pages);
+  if (c.page_size < 1) return set_last_error(FA_ERR_INVALID_ARG, "page_size must be >= 1, got %d", c.page_size);
+  if (kv_type == FA_KV_BF16 && (c.k_scale || c.v_scale))
+    return set_last_error(FA_ERR_INVALID_ARG, "k_scale and v_scale belong to an e4m3 cache");
+  const long long unit = kv_type == FA_KV_E4M3 ? 16 : 8;   // elements in 16 bytes
+  const struct { const char* name; long long v; int n; } st[] = {
+      {"page_stride", c.page_stride, c.num_pages}, {"slot_stride", c.slot_stride, c.page_size},
+      {"head_stride", c.head_stride, c.heads_kv}};
+  for (const auto& s : st) {
+    if (s.n <= 1) continue;   // never multiplied by anything but 0
+    if (s.v < c.head_dim)
+      return set_last_error(FA_ERR_INVALID_ARG, "%s must be at least head_dim (%d elements), got %lld", s.name,
+                            c.head_dim, s.v);
+    if (s.v % unit)
+      return set_last_error(FA_ERR_INVALID_ARG, "%s must be a multiple of 16 bytes (%lld elements), got %lld", s.name,
+                            unit, s.v);
+  }
+  if (misaligned16(c.k) || misaligned16(c.v))
+    return set_last_error(FA_ERR_INVALID_ARG, "k_cache and v_cache must be 16-byte aligned");
+  if (misaligned4(c.k_scale) || misaligned4(c.v_scale))
+    return set_last_error(FA_ERR_INVALID_ARG, "k_scale and v_scale must be 4-byte aligned");
+  return FA_OK;
+}
+
+int check_row_stride(const char* name, long long stride, long long row, int rows) {
+  if (rows <= 1) return FA_OK;
+  if (stride < row || stride % 8)
+    return set_last_error(FA_ERR_INVALID_ARG,
+                          "%s must be a multiple of 8 elements and hold a whole row (%lld elements), got %lld", name,
+                          row, stride);
+  return FA_OK;
+}
+
+fa::PagedCache make_cache(const void* k, const void* v, int kv_type, const float* k_scale, const float* v_scale,
+                          long long page_stride, long long slot_stride, long long head_stride, int num_pages,
+                          int page_size, int heads_kv, int head_dim) {
+  fa::PagedCache c;
+  c.k = const_cast<void*>(k);
+  c.v = const_cast<void*>(v);
+  c.k_scale = k_scale;
+  c.v_scale = v_scale;
+  c.page_stride = page_stride;
+  c.slot_stride = slot_stride;
+  c.head_stride = head_stride;
+  c.e4m3 = kv_type == FA_KV_E4M3;
+  c.num_pages = num_pages;
+  c.page_size = page_size;
+  c.heads_kv = heads_kv;
+  c.head_dim = head_dim;
+  return c;
+}
+
+// ---------------------------------------------------------------- plan
+constexpr int kPlanThreads = 256;
+
+struct PlanParams {
+  int32_t* table;
+  long long table_stride;
+  int max_pages;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  const int32_t* free_pages;
+  int num_free;
+  const int32_t* free_start;
+  int page_size;
+  int batch;
+  int num_tokens;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* cu_new;
+  int32_t* seq_lens_out;
+  int32_t* free_next;
+};
+
+__device__ __forceinline__ int clamp_int(long long x) {
+  return static_cast<int>(x > 0x7fffffffll ? 0x7fffffffll : x);
+}
+
+struct Request {
+  int seq, fresh;     // tokens cached, tokens new
+  int have, take;     // pages held, pages to take
+};
+
+__device__ __forceinline__ Request load_request(const PlanParams& p, int b) {
+  Request r;
+  r.seq = max(p.seq_lens[b], 0);
+  r.fresh = max(p.new_lens[b], 0);
+  const long long after = static_cast<long long>(r.seq) + r.fresh;
+  const long long have = (static_cast<long long>(r.seq) + p.page_size - 1) / p.page_size;
+  const long long need = (after + p.page_size - 1) / p.page_size;
+  r.have = static_cast<int>(have < p.max_pages ? have : p.max_pages);
+  r.take = static_cast<int>(need < p.max_pages ? need : p.max_pages) - r.have;
+  return r;
+}
+
+// Every block sums the requests' new tokens and pages itself (a block scan
+// over runs of consecutive requests, one run per thread), then places its
+// own tokens; block 0 also writes what there is one of per request.  Nothing
+// is passed between blocks, so one launch is enough.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+  __shared__ long long run_tok[kPlanThreads + 1];   // new tokens before each thread's run
+  __shared__ long long run_page[kPlanThreads + 1];  // pages taken before it
+  const int t = threadIdx.x;
+  const int per = (p.batch + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(t * per, p.batch), b1 = min(b0 + per, p.batch);
+  long long tok = 0, page = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(p, b);
+    tok += r.fresh;
+    page += r.take;
+  }
+  run_tok[t + 1] = tok;
+  run_page[t + 1] = page;
+  if (t == 0) run_tok[0] = run_page[0] = 0;
+  __syncthreads();
+  for (int off = 1; off < kPlanThreads; off <<= 1) {
+    long long a = 0, c = 0;
+    if (t + 1 > off) {
+      a = run_tok[t + 1 - off];
+      c = run_page[t + 1 - off];
+    }
+    __syncthreads();
+    run_tok[t + 1] += a;
+    run_page[t + 1] += c;
+    __syncthreads();
+  }
+  const long long start = p.free_start ? max(*p.free_start, 0) : 0;
+  if (blockIdx.x == 0) {
+    long long at = run_tok[t];
+    for (int b = b0; b < b1; ++b) {
+      const Request r = load_request(p, b);
+      p.cu_new[b] = clamp_int(at);
+      p.seq_lens_out[b] = clamp_int(static_cast<long long>(r.seq) + r.fresh);
+      at += r.fresh;
+    }
+    if (t == 0) {
+      p.cu_new[p.batch] = clamp_int(run_tok[kPlanThreads]);
+      *p.free_next = clamp_int(start + run_page[kPlanThreads]);
+    }
+  }
+  const long long total = run_tok[kPlanThreads];
+  for (long long i = static_cast<long long>(blockIdx.x) * kPlanThreads + t; i < p.num_tokens;
+       i += static_cast<long long>(gridDim.x) * kPlanThreads) {
+    long long slot = -1;
+    int pos = 0;
+    if (i < total) {
+      int lo = 0, hi = kPlanThreads;   // run_tok[lo] <= i < run_tok[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (run_tok[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      long long at = run_tok[lo], taken = start + run_page[lo];
+      int b = min(lo * per, p.batch);
+      Request r = load_request(p, b);
+      while (at + r.fresh <= i) {
+        at += r.fresh;
+        taken += r.take;
+        r = load_request(p, ++b);
+      }
+      const long long place = static_cast<long long>(r.seq) + (i - at);
+      pos = clamp_int(place);
+      const long long pi = place / p.page_size;
+      const int in_page = static_cast<int>(place - pi * p.page_size);
+      if (pi < p.max_pages) {
+        int id;
+        if (pi < r.have) {
+          id = p.table[b * p.table_stride + pi];
+        } else {
+          const long long f = taken + (pi - r.have);
+          id = f < p.num_free ? p.free_pages[f] : -1;
+          if (in_page == 0) p.table[b * p.table_stride + pi] = id;
+        }
+        if (id >= 0) slot = static_cast<long long>(id) * p.page_size + in_page;
+      }
+    }
+    p.slots[i] = slot;
+    p.positions[i] = pos;
+  }
+}
+
+// ---------------------------------------------------------------- append
+constexpr int kAppendThreads = 256;
+
+struct AppendParams {
+  fa::PagedCache kv;
+  const uint16_t* k;
+  const uint16_t* v;
+  long long k_row_stride;
+  long long v_row_stride;
+  const int64_t* slots;
+  int num_tokens;
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// Two values to e4m3 (round to nearest even, saturating to +-448, NaN stays).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Eight bf16 values divided by `scale` (the correctly rounded quotient: a
+// product with a rounded reciprocal would put values next to a border of two
+// 8-bit numbers on the wrong side) and rounded to eight bytes.
+__device__ __forceinline__ uint2 quantise8(uint4 x, float scale) {
+  uint2 r;
+  r.x = e4m3x2(__fdiv_rn(bf_lo(x.x), scale), __fdiv_rn(bf_hi(x.x), scale)) |
+        e4m3x2(__fdiv_rn(bf_lo(x.y), scale), __fdiv_rn(bf_hi(x.y), scale)) << 16;
+  r.y = e4m3x2(__fdiv_rn(bf_lo(x.z), scale), __fdiv_rn(bf_hi(x.z), scale)) |
+        e4m3x2(__fdiv_rn(bf_lo(x.w), scale), __fdiv_rn(bf_hi(x.w), scale)) << 16;
+  return r;
+}
+
+// One thread per eight elements of a row of K and of V.
+template <bool E4M3>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+  const int per_head = p.kv.head_dim / 8;
+  const int per_row = p.kv.heads_kv * per_head;
+  const long long n = static_cast<long long>(p.num_tokens) * per_row;
+  const long long num_slots = static_cast<long long>(p.kv.num_pages) * p.kv.page_size;
+  for (long long i = static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * kAppendThreads) {
+    const long long row = i / per_row;
+    const int c = static_cast<int>(i - row * per_row);
+    const int h = c / per_head;
+    const long long slot = p.slots[row];
+    if (slot < 0 || slot >= num_slots) continue;
+    const long long page = slot / p.kv.page_size;
+    const long long at = page * p.kv.page_stride + (slot - page * p.kv.page_size) * p.kv.slot_stride +
+                         h * p.kv.head_stride + (c - h * per_head) * 8;
+    const uint4 k = *reinterpret_cast<const uint4*>(p.k + row * p.k_row_stride + c * 8);
+    const uint4 v = *reinterpret_cast<const uint4*>(p.v + row * p.v_row_stride + c * 8);
+    if constexpr (E4M3) {
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kv.k) + at) = quantise8(k, p.kv.k_scale ? p.kv.k_scale[h] : 1.f);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kv.v) + at) = quantise8(v, p.kv.v_scale ? p.kv.v_scale[h] : 1.f);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.k) + at) = k;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.v) + at) = v;
+    }
+  }
+}
+
+int blocks_for(long long items, int threads, int per_sm) {
+  const long long want = (items + threads - 1) / threads;
+  const long long cap = 152ll * per_sm;   // SMs of a GB300
+  return static_cast<int>(want < 1 ? 1 : (want > cap ? cap : want));
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_kv_plan(int32_t* block_table, long long table_stride, int max_pages, const int32_t* seq_lens,
+               const int32_t* new_lens, const int32_t* free_pages, int num_free, const int32_t* free_start,
+               int page_size, int batch, int num_tokens, int64_t* slots, int32_t* positions, int32_t* cu_new,
+               int32_t* seq_lens_out, int32_t* free_next, fa_stream_t stream) {
+  if (batch < 0 || num_tokens < 0 || num_free < 0 || max_pages < 0)
+    return set_last_error(FA_ERR_INVALID_ARG, "batch, num_tokens, num_free and max_pages must be >= 0");
+  if (page_size < 1) return set_last_error(FA_ERR_INVALID_ARG, "page_size must be >= 1, got %d", page_size);
+  if (batch > 1 && table_stride < max_pages)
+    return set_last_error(FA_ERR_INVALID_ARG, "table_stride must be at least max_pages (%d), got %lld", max_pages,
+                          table_stride);
+  if (!cu_new || !free_next || (batch > 0 && (!seq_lens || !new_lens || !seq_lens_out)) ||
+      (batch > 0 && max_pages > 0 && !block_table) || (num_free > 0 && !free_pages) ||
+      (num_tokens > 0 && (!slots || !positions)))
+    return set_last_error(FA_ERR_INVALID_ARG, "a device pointer is NULL");
+  if (batch > 0 && (seq_lens_out == seq_lens || seq_lens_out == new_lens))
+    return set_last_error(FA_ERR_INVALID_ARG, "seq_lens_out must not be seq_lens or new_lens");
+  if (free_next == free_start)
+    return set_last_error(FA_ERR_INVALID_ARG, "free_next must not be free_start");
+  const void* al[] = {block_table, seq_lens, new_lens, free_pages, free_start, positions, cu_new, seq_lens_out, free_next};
+  for (const void* ptr : al)
+    if (misaligned4(ptr)) return set_last_error(FA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(slots) & 7u)
+    return set_last_error(FA_ERR_INVALID_ARG, "slots must be 8-byte aligned");
+  int rc = check_device();
+  if (rc) return rc;
+  const PlanParams p{block_table, table_stride, max_pages,  seq_lens, new_lens,  free_pages, num_free,     free_start,
+                     page_size,   batch,        num_tokens, slots,    positions, cu_new,     seq_lens_out, free_next};
+  plan_kernel<<<blocks_for(num_tokens, kPlanThreads, 2), kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "plan launch");
+  return ok();
+}
+
+int fa_kv_append(const fa_bf16* k, const fa_bf16* v, long long k_row_stride, long long v_row_stride,
+                 const int64_t* slots, int num_tokens, void* k_cache, void* v_cache, int kv_type,
+                 const float* k_scale, const float* v_scale, long long page_stride, long long slot_stride,
+                 long long head_stride, int num_pages, int page_size, int heads_kv, int head_dim,
+                 fa_stream_t stream) {
+  AppendParams p;
+  p.kv = make_cache(k_cache, v_cache, kv_type, k_scale, v_scale, page_stride, slot_stride, head_stride, num_pages,
+                    page_size, heads_kv, head_dim);
+  int rc = check_cache(p.kv, kv_type);
+  if (rc) return rc;
+  if (num_tokens < 0) return set_last_error(FA_ERR_INVALID_ARG, "num_tokens must be >= 0, got %d", num_tokens);
+  const long long row = static_cast<long long>(heads_kv) * head_dim;
+  if ((rc = check_row_stride("k_row_stride", k_row_stride, row, num_tokens))) return rc;
+  if ((rc = check_row_stride("v_row_stride", v_row_stride, row, num_tokens))) return rc;
+  if (num_tokens == 0 || num_pages == 0) return ok();
+  if (!k || !v || !slots || !k_cache || !v_cache)
+    return set_last_error(FA_ERR_INVALID_ARG, "a device pointer is NULL");
+  if (misaligned16(k) || misaligned16(v))
+    return set_last_error(FA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(slots) & 7u)
+    return set_last_error(FA_ERR_INVALID_ARG, "slots must be 8-byte aligned");
+  if ((rc = check_device())) return rc;
+  p.k = k;
+  p.v = v;
+  p.k_row_stride = k_row_stride;
+  p.v_row_stride = v_row_stride;
+  p.slots = slots;
+  p.num_tokens = num_tokens;
+  const int grid = blocks_for(num_tokens * (row / 8), kAppendThreads, 8);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p.kv.e4m3) append_kernel<true><<<grid, kAppendThreads, 0, s>>>(p);
+  else append_kernel<false><<<grid, kAppendThreads, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "append launch");
+  return ok();
+}
+
+size_t fa_decode_workspace_size(int batch, int heads, int heads_kv, int head_dim) {
+  if (batch < 0 || heads_kv < 1 || heads < 1 || heads % heads_kv != 0) {
+    set_last_error(FA_ERR_INVALID_ARG,
+                   "need batch >= 0 and query heads (%d) a positive multiple of key/value heads (%d)", heads, heads_kv);
+    return 0;
+  }
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) {
+    set_last_error(FA_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256, got %d", head_dim);
+    return 0;
+  }
+  ok();
+  return fa::decode_workspace_bytes(batch, heads, heads_kv, head_dim);
+}
+
+int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, const void* v_cache, int kv_type,
+              const float* k_scale, const float* v_scale, long long page_stride, long long slot_stride,
+              long long head_stride, int num_pages, int page_size, const int32_t* block_table,
+              long long table_stride, int max_pages, const int32_t* seq_lens, int batch, int heads, int heads_kv,
+              int head_dim, int window, float scale, fa_bf16* o, float* lse, void* workspace,
+              size_t workspace_bytes, fa_stream_t stream) {
+  fa::DecodeParams p;
+  p.kv = make_cache(k_cache, v_cache, kv_type, k_scale, v_scale, page_stride, slot_stride, head_stride, num_pages,
+                    page_size, heads_kv, head_dim);
+  int rc = check_cache(p.kv, kv_type);
+  if (rc) return rc;
+  if (batch < 0) return set_last_error(FA_ERR_INVALID_ARG, "batch must be >= 0, got %d", batch);
+  if (heads < 1 || heads % heads_kv != 0)
+    return set_last_error(FA_ERR_INVALID_ARG, "query heads (%d) must be a positive multiple of key/value heads (%d)",
+                          heads, heads_kv);
+  if (window < 0) return set_last_error(FA_ERR_INVALID_ARG, "window must be >= 0, got %d", window);
+  if (!isfinite(scale)) return set_last_error(FA_ERR_INVALID_ARG, "scale must be finite");
+  if (max_pages < 0) return set_last_error(FA_ERR_INVALID_ARG, "max_pages must be >= 0, got %d", max_pages);
+  if (static_cast<long long>(max_pages) * page_size > 0x7fff0000ll)
+    return set_last_error(FA_ERR_UNSUPPORTED, "a block table of %d pages of %d slots is too long", max_pages, page_size);
+  if (batch > 1 && table_stride < 0)
+    return set_last_error(FA_ERR_INVALID_ARG, "table_stride must be >= 0, got %lld", table_stride);
+  if ((rc = check_row_stride("q_row_stride", q_row_stride, static_cast<long long>(heads) * head_dim, batch))) return rc;
+  if (batch == 0) return ok();
+  if (!q || !o || !seq_lens || (max_pages > 0 && !block_table) || (max_pages > 0 && num_pages > 0 && (!k_cache || !v_cache)))
+    return set_last_error(FA_ERR_INVALID_ARG, "a device pointer is NULL");
+  if (misaligned16(q) || misaligned16(o)) return set_last_error(FA_ERR_INVALID_ARG, "q and o must be 16-byte aligned");
+  if (misaligned4(block_table) || misaligned4(seq_lens) || misaligned4(lse))
+    return set_last_error(FA_ERR_INVALID_ARG, "block_table, seq_lens and lse must be 4-byte aligned");
+  const size_t need = fa::decode_workspace_bytes(batch, heads, heads_kv, head_dim);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return set_last_error(FA_ERR_INVALID_ARG, "workspace of %zu bytes needed, got %zu", need, workspace_bytes);
+  if (misaligned16(workspace)) return set_last_error(FA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  if ((rc = check_device())) return rc;
+  p.q = q;
+  p.q_row_stride = q_row_stride;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.seq_lens = seq_lens;
+  p.o = o;
+  p.lse = lse;
+  p.work = static_cast<float*>(workspace);
+  p.max_pages = max_pages;
+  p.batch = batch;
+  p.heads = heads;
+  p.window = window;
+  p.scale = scale;
+  cudaError_t e = fa::launch_decode(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "decode launch");
+  return ok();
+}
+
+}  // extern "C"

@@ -277,6 +277,94 @@ int fa_bwd_noalloc(const fa_bf16* q, const fa_bf16* k, const fa_bf16* v, const f
                    int batch, int total_q, int total_kv, int heads, int head_dim,
                    int causal, float scale, fa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key/value cache: the serving side of the forward above.
+ *
+ * Keys and values of past tokens live in pages of page_size slots, k_cache
+ * and v_cache apart but laid out alike: slot s of page p, key/value head h
+ * starts at element p * page_stride + s * slot_stride + h * head_stride, d
+ * elements long (strides in elements, multiples of 16 bytes).  The packed
+ * layout of the other entry points, [num_pages, page_size, Hkv, d], has
+ * strides (page_size * Hkv * d, Hkv * d, d); [num_pages, Hkv, page_size, d]
+ * and a cache that interleaves K and V pages are other strides of the same.
+ * A request's tokens 0, 1, ... occupy the slots of the pages its row of the
+ * block table names, in order; an entry that is no page of the cache
+ * (< 0 or >= num_pages) holds no keys.  A slot's number is
+ * page * page_size + place in the page.
+ *
+ * Device contents are not read on the host: lengths below 0 count as 0,
+ * and page and slot numbers are bounds-checked on the device.
+ * ------------------------------------------------------------------------ */
+enum fa_kv_type {
+    FA_KV_BF16 = 0,
+    FA_KV_E4M3 = 1    /* 8-bit floating point, value = element * scale of the key/value head */
+};
+
+/* Places for new tokens, built on the device from the requests' lengths.
+ * Request b has seq_lens[b] tokens in the cache and gets new_lens[b] more.
+ * Pages it needs beyond those it holds, ceil(seq_lens / page_size), are
+ * taken from free_pages in request order, from entry *free_start on
+ * (free_start NULL: 0), and entered into its row of block_table (rows
+ * table_stride entries apart, max_pages entries each; other entries are left
+ * as they were, so the same call made again gives the same result).
+ *   slots[num_tokens], positions[num_tokens]: slot and position in its
+ *     request of every new token, requests in order.  Rows past the last new
+ *     token (a padded batch) get slot -1, position 0.
+ *   cu_new[batch+1]: offsets of the requests' new tokens (the cu_q of a
+ *     following fa_fwd_* call);  seq_lens_out[batch] = seq_lens + new_lens;
+ *   free_next[1]: the first entry of free_pages not taken.
+ * A token for which the table row or the free list has no page gets slot -1
+ * (and the table entry -1); *free_next > num_free tells that the list ran
+ * out, cu_new[batch] > num_tokens that slots was too short (tokens past it
+ * get no place).  seq_lens_out must not overlap seq_lens or new_lens, and
+ * free_next not free_start; no other output may overlap an input. */
+int fa_kv_plan(int32_t* block_table, long long table_stride, int max_pages,
+               const int32_t* seq_lens, const int32_t* new_lens,
+               const int32_t* free_pages, int num_free, const int32_t* free_start,
+               int page_size, int batch, int num_tokens,
+               int64_t* slots, int32_t* positions, int32_t* cu_new,
+               int32_t* seq_lens_out, int32_t* free_next, fa_stream_t stream);
+
+/* Writes the new tokens' keys and values, k and v [num_tokens, Hkv, d] bf16
+ * (rows k_row_stride / v_row_stride elements apart, multiples of 8: slices
+ * of a fused projection need no copy), into the cache: row t goes to
+ * slots[t]; rows whose slot is outside the cache (-1) are skipped and slots
+ * that no row names are left as they were.  The slots of one call must
+ * differ from one another: of rows with the same slot any one may remain,
+ * or parts of several.  kv_type FA_KV_E4M3 stores
+ * e4m3(x / k_scale[head]) (v_scale for v; NULL: 1), round to nearest even,
+ * saturating at +-448; NaN stays NaN.  Scales: [Hkv] float32 on the device,
+ * positive; NULL with FA_KV_BF16. */
+int fa_kv_append(const fa_bf16* k, const fa_bf16* v, long long k_row_stride, long long v_row_stride,
+                 const int64_t* slots, int num_tokens,
+                 void* k_cache, void* v_cache, int kv_type, const float* k_scale, const float* v_scale,
+                 long long page_stride, long long slot_stride, long long head_stride,
+                 int num_pages, int page_size, int heads_kv, int head_dim, fa_stream_t stream);
+
+/* Bytes of device workspace fa_decode needs (an upper bound over all
+ * lengths).  Returns 0 and sets fa_last_error() on bad arguments. */
+size_t fa_decode_workspace_size(int batch, int heads, int heads_kv, int head_dim);
+
+/* Attention of one new token per request over the cache: q [batch, H, d]
+ * bf16 (rows q_row_stride elements apart, a multiple of 8), o [batch, H, d]
+ * bf16 contiguous, lse [batch, H] float32 (may be NULL), the values
+ * fa_fwd_lse gives for a query at position seq_lens[b] - 1 that sees keys
+ * [max(0, seq_lens[b] - window), seq_lens[b]) (window 0: all).  The new
+ * token's own key and value are in the cache already (fa_kv_append) and
+ * count in seq_lens.  Lengths are clamped to max_pages * page_size.  Query
+ * head h reads key/value head h / (H / Hkv).  A row that sees no key gets
+ * o = 0, lse = -inf.  Contents of slots that are not seen do not matter
+ * (NaN included).  workspace: fa_decode_workspace_size() bytes, 16-byte
+ * aligned, contents arbitrary; calls whose work overlaps on the GPU need one
+ * each.  Results do not depend on timing: the same call gives the same bits. */
+int fa_decode(const fa_bf16* q, long long q_row_stride,
+              const void* k_cache, const void* v_cache, int kv_type, const float* k_scale, const float* v_scale,
+              long long page_stride, long long slot_stride, long long head_stride,
+              int num_pages, int page_size, const int32_t* block_table, long long table_stride, int max_pages,
+              const int32_t* seq_lens, int batch, int heads, int heads_kv, int head_dim,
+              int window, float scale, fa_bf16* o, float* lse,
+              void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
 /* Diagnostic (the pages have no counterpart): launches one block that
  * waits, through the same bounded mbarrier wait the kernels use, on a
  * barrier nothing arrives on.  After its own short limit (1 s; the

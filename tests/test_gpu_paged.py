@@ -1,0 +1,466 @@
+"""Paged cache operators on the GPU against the fp64 oracle.
+
+Bounds for decode, per element (derived, not tuned): with u the unit
+roundoff of a stored type (bf16: 2^-8) and fp32 sums that may truncate
+(2^-23 per addition),
+  * a score of d products is off by at most delta = (d + 4) 2^-23 max|x|,
+    |x| the sum of the absolute products, so every weight by 2 delta;
+  * weights are rounded once to 16 bits (u) and summed over n keys
+    (n 2^-23), o is rounded to bf16 (u |o|):
+    |o - ref| <= u |o| + (1 + 2^-6) (u + 2 delta + (n + 32) 2^-23) sum p |v|
+  * |lse - ref| <= 2 delta + (n + 32) 2^-23 + 2^-22 |lse|.
+plan and append move whole numbers and bits: they are compared exactly."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import seeded_inputs as si
+from oracle import paged
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -8
+
+
+def fab():
+    import attention_backward_sm_gb300 as m
+    return m
+
+
+def strided(cache, layout):
+    """The same [pages, page, Hkv, d] contents in another memory layout."""
+    if layout == "heads_first":
+        return cache.transpose(1, 2).contiguous().transpose(1, 2)
+    if layout == "gaps":   # every second page and padded slots of a larger buffer
+        p, s, h, d = cache.shape
+        big = torch.full((p, 2, s, h + 1, d), 1.0).to(cache.dtype).to(cache.device)
+        big[:, 1, :, :h] = cache
+        return big[:, 1, :, :h]
+    return cache
+
+
+class Problem:
+    """Requests of given lengths over randomly placed pages.  Slots past a
+    request's last key and pages that nobody holds are NaN."""
+
+    def __init__(self, lens, heads, heads_kv, dim, page, kv="bf16", window=0, layout="plain", seed=0, q_scale=1.0,
+                 extra_width=1, bad=()):
+        g = torch.Generator().manual_seed(seed)
+        have = [-(-n // page) for n in lens]
+        width = max(have + [0]) + extra_width
+        pool = sum(have) + 3
+        order = torch.randperm(pool, generator=g)
+        self.table = torch.full((len(lens), width), -1, dtype=torch.int32)
+        at = 0
+        shape = (pool, page, heads_kv, dim)
+        k = torch.full(shape, float("nan"))
+        v = torch.full(shape, float("nan"))
+        for b, n in enumerate(lens):
+            pages = order[at:at + have[b]]
+            at += have[b]
+            self.table[b, :have[b]] = pages.int()
+            if n:
+                j = torch.arange(n)
+                k[pages[j // page], j % page] = torch.randn(n, heads_kv, dim, generator=g)
+                v[pages[j // page], j % page] = torch.randn(n, heads_kv, dim, generator=g)
+        for b, i, entry in bad:
+            self.table[b, i] = entry
+        self.k_scale = self.v_scale = None
+        if kv == "e4m3":
+            self.k_scale = 0.01 + 0.01 * torch.rand(heads_kv, generator=g)
+            self.v_scale = 0.01 + 0.01 * torch.rand(heads_kv, generator=g)
+            k = (k / self.k_scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+            v = (v / self.v_scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        else:
+            k, v = k.bfloat16(), v.bfloat16()
+        self.k, self.v = k, v
+        self.q = (q_scale * torch.randn(len(lens), heads, dim, generator=g)).bfloat16()
+        self.lens = torch.tensor(lens, dtype=torch.int32)
+        self.window, self.scale, self.layout = window, dim ** -0.5, layout
+
+    def device(self):
+        kc, vc = strided(self.k.to(DEV), self.layout), strided(self.v.to(DEV), self.layout)
+        on = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+        return dict(q=on(self.q), k_cache=kc, v_cache=vc, block_table=on(self.table), seq_lens=on(self.lens),
+                    scale=self.scale, window=self.window, k_scale=on(self.k_scale), v_scale=on(self.v_scale))
+
+    def run(self, **kw):
+        return fab().decode(**{**self.device(), **kw})
+
+    def check(self, o, lse, rows=None):
+        ref, rlse, pv, xa = paged.decode(self.q.float(), self.k.float(), self.v.float(), self.table.numpy(),
+                                         self.lens.numpy(), self.scale, self.window,
+                                         self.k_scale, self.v_scale)
+        o, lse = o.float().cpu().double().numpy(), lse.cpu().double().numpy()
+        d = o.shape[-1]
+        n = self.lens.clamp(min=0).numpy()[:, None]
+        if self.window:
+            n = np.minimum(n, self.window)
+        delta = (d + 4) * 2.0 ** -23 * xa
+        none = np.isneginf(rlse)
+        assert np.array_equal(np.isneginf(lse), none)
+        assert np.all(o[none] == 0)
+        rlse, lse = np.where(none, 0, rlse), np.where(none, 0, lse)
+        tol = 2 * delta + (n + 32) * 2.0 ** -23 + 2.0 ** -22 * np.abs(rlse)
+        assert np.all(np.abs(lse - rlse) <= tol), f"lse off by {np.abs(lse - rlse).max():.3e}"
+        tol = U * np.abs(ref) + (1 + 2.0 ** -6) * (U + 2 * delta + (n + 32) * 2.0 ** -23)[..., None] * pv
+        bad = np.abs(o - ref) > tol + 1e-30
+        assert not bad.any(), f"{bad.sum()} of {bad.size} outputs off, worst {np.abs(o - ref)[bad].max():.3e}"
+
+
+# ------------------------------------------------------------------ plan
+@pytest.mark.parametrize("batch,page,seq_hi,new_hi,width,free,pad,start", [
+    (1, 16, 0, 1, 4, 8, 0, 0), (3, 1, 5, 4, 16, 64, 3, 2), (64, 16, 500, 1, 40, 80, 0, 0),
+    (257, 7, 90, 3, 20, 300, 10, 5), (1000, 64, 0, 130, 4, 3100, 7, 0), (5, 16, 40, 60, 5, 9, 0, 0),
+    (1, 8, 3, 20000, 2600, 2600, 1, 0), (300, 16, 33, 0, 4, 0, 2, 0)])
+def test_plan_matches_the_oracle(batch, page, seq_hi, new_hi, width, free, pad, start):
+    rng = np.random.default_rng(batch * 1000 + page)
+    seq = rng.integers(0, seq_hi + 1, batch)
+    new = rng.integers(0, new_hi + 1, batch)
+    if batch > 2:
+        seq[1], new[2] = -4, -1          # lengths below 0 count as 0
+    table = np.full((batch, width), -1)
+    pages = rng.permutation(batch * width + free)
+    for b in range(batch):
+        have = min(-(-max(seq[b], 0) // page), width)
+        table[b, :have] = pages[b * width:b * width + have]
+    free_pages = pages[batch * width:]
+    tokens = int(np.maximum(new, 0).sum()) + pad
+    want = paged.plan(table, seq, new, free_pages, page, tokens, start)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).to(DEV)  # noqa: E731
+    wide = i32(np.concatenate([table, np.full((batch, 3), 77)], 1))   # rows further apart than they are long
+    args = (wide[:, :width], i32(seq), i32(new), i32(free_pages))
+    for call in range(2):                                             # the second changes nothing
+        got = fab().kv_plan(*args, page, tokens, free_start=i32([start]))
+        torch.cuda.synchronize()
+        for name, g, w in zip(("table", "slots", "positions", "cu_new", "seq_lens", "free_next"),
+                              (args[0], *got), (*want[:5], np.array([want[5]]))):
+            assert np.array_equal(g.cpu().numpy(), w), (name, call)
+        assert torch.all(wide[:, width:] == 77)
+
+
+def test_plan_too_few_slots_keeps_the_count():
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = torch.full((2, 4), -1, **i32)
+    p = fab().kv_plan(table, torch.zeros(2, **i32), torch.tensor([5, 3], **i32), torch.arange(8, **i32), 4, 6)
+    assert p.slots.tolist() == [0, 1, 2, 3, 4, 8] and p.cu_new.tolist() == [0, 5, 8] and p.free_next.tolist() == [3]
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("tokens,heads_kv,dim,page", [(1, 1, 64, 16), (7, 8, 128, 16), (333, 3, 64, 5), (129, 2, 256, 64)])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("layout", ["plain", "heads_first", "gaps"])
+def test_append_writes_named_slots_only(tokens, heads_kv, dim, page, kv, layout):
+    g = torch.Generator().manual_seed(tokens)
+    pool = -(-tokens // page) + 3
+    dtype = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    bits = torch.int16 if kv == "bf16" else torch.uint8
+    fused = (30 * torch.randn(tokens, 5 + 2 * heads_kv, dim, generator=g)).bfloat16()
+    fused[0, 5, :4] = torch.tensor([float("nan"), float("inf"), -float("inf"), 1e30])
+    fused[-1, -1, :3] = torch.tensor([-0.0, 1e-30, 448.5])
+    k, v = fused[:, 5:5 + heads_kv], fused[:, 5 + heads_kv:]
+    slots = torch.randperm(pool * page, generator=g)[:tokens]
+    if tokens > 3:
+        slots[1], slots[3] = -1, pool * page       # skipped
+    scale = None if kv == "bf16" else 0.05 + torch.rand(heads_kv, generator=g)
+    before = torch.randn(pool, page, heads_kv, dim, generator=g).to(dtype)
+    kc, vc = strided(before.to(DEV), layout), strided(before.clone().to(DEV), layout)
+    on = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    dev = fused.to(DEV)
+    fab().kv_append(dev[:, 5:5 + heads_kv], dev[:, 5 + heads_kv:], kc, vc, slots.to(DEV), on(scale), on(scale))
+    ok = (slots >= 0) & (slots < pool * page)
+    for got, new in ((kc, k), (vc, v)):
+        want = before.clone().view(bits).view(-1, heads_kv, dim)
+        row = new if scale is None else (new.float() / scale[:, None]).clamp(-448, 448).to(dtype)
+        want[slots[ok]] = row.contiguous().view(bits)[ok]
+        got, want = got.cpu().contiguous().view(dtype), want.view(dtype).view(before.shape)
+        nan = torch.isnan(want.float())
+        assert torch.equal(torch.isnan(got.float()), nan)
+        assert torch.equal(got.view(bits)[~nan], want.view(bits)[~nan])
+
+
+# ------------------------------------------------------------------ decode
+GROUPS = [(1, 1), (4, 4), (8, 2), (6, 2), (14, 2), (9, 1), (16, 1), (20, 1), (40, 1)]
+
+
+@pytest.mark.parametrize("heads,heads_kv", GROUPS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_decode_head_layouts(heads, heads_kv, dim, kv):
+    p = Problem([1, 0, 63, 64, 65, 130, 300], heads, heads_kv, dim, 16, kv, seed=heads * dim)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 24, 64, 100, 256])
+@pytest.mark.parametrize("window", [0, 1, 17, 64, 1000])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_decode_pages_and_windows(page, window, kv):
+    p = Problem([1, page, page + 1, 127, 128, 129, 517, 0, 16], 4, 2, 128, page, kv, window, seed=page + window)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("layout", ["plain", "heads_first", "gaps"])
+@pytest.mark.parametrize("dim,kv", [(64, "bf16"), (128, "e4m3"), (256, "bf16")])
+def test_decode_layouts_and_strided_queries(layout, dim, kv):
+    p = Problem([200, 33, 1, 90], 6, 3, dim, 16, kv, layout=layout, seed=dim)
+    fused = torch.full((4, 12, dim), float("nan"), dtype=torch.bfloat16)
+    fused[:, :6] = p.q
+    p.check(*p.run(q=fused.to(DEV)[:, :6]))
+
+
+@pytest.mark.parametrize("batch,hi,heads,heads_kv,dim,kv", [
+    (1, 20000, 8, 2, 128, "bf16"),        # one request over every SM
+    (1, 9000, 1, 1, 64, "e4m3"),
+    (300, 90, 4, 4, 64, "bf16"),          # many more requests than SMs
+    (33, 3000, 4, 1, 256, "bf16"),        # ragged
+    (40, 2500, 24, 1, 128, "e4m3")])
+def test_decode_splits(batch, hi, heads, heads_kv, dim, kv):
+    lens = [int(x) for x in np.random.default_rng(batch).integers(0, hi + 1, batch)]
+    lens[0] = hi
+    p = Problem(lens, heads, heads_kv, dim, 16, kv, seed=batch)
+    o, lse = p.run()
+    p.check(o, lse)
+    again = p.run()
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_decode_peaked_growing_and_shrinking_scores(kv):
+    """Weights on a few keys; the running maximum rises or falls all along."""
+    for q_scale in (30.0, 0.0):
+        p = Problem([700, 129], 4, 2, 128, 16, kv, q_scale=q_scale, seed=9)
+        p.check(*p.run())
+    for sign in (1, -1):
+        p = Problem([640, 640], 4, 1, 128, 16, seed=10)
+        ramp = torch.linspace(-4, 4, 640) * sign
+        j = torch.arange(640)
+        for b in range(2):
+            p.k[p.table[b].long()[j // 16], j % 16, 0, 0] = ramp.bfloat16()
+        p.q[..., 0] = 40.0
+        p.check(*p.run())
+
+
+def test_decode_bad_pages_are_not_seen():
+    p = Problem([70, 200, 40, 10], 4, 2, 128, 16, seed=12,
+                bad=[(0, 1, -1), (0, 4, 10 ** 9), (1, 0, -7), (1, 12, 2 ** 31 - 1), (3, 0, -1)])
+    o, lse = p.run()
+    p.check(o, lse)
+    assert torch.all(o[3] == 0) and torch.all(lse[3] == -float("inf"))
+
+
+def test_decode_lengths_are_clamped_to_the_table():
+    p = Problem([32, 20, 5], 4, 2, 64, 16, extra_width=0, seed=13)
+    p.lens[0], p.lens[2] = 2 ** 31 - 1, -3
+    o, lse = p.run()
+    p.lens[0], p.lens[2] = 32, 0
+    p.check(o, lse)
+
+
+def test_decode_visible_nan_and_inf_reach_the_output():
+    """A NaN key or value that is seen shows, in its request and head only."""
+    p = Problem([50, 50], 4, 2, 64, 16, seed=14)
+    clean = p.run()
+    p.v[p.table[0, 1].long(), 3, 0, 5] = float("nan")
+    p.k[p.table[1, 0].long(), 2, 1, 7] = float("nan")
+    o, lse = p.run()
+    assert torch.isnan(o[0, :2, 5]).all() and torch.isnan(o[1, 2:]).all() and torch.isnan(lse[1, 2:]).all()
+    assert torch.equal(o[0, 2:], clean[0][0, 2:]) and torch.equal(o[1, :2], clean[0][1, :2])
+    assert torch.equal(lse[0], clean[1][0])
+
+
+def test_decode_empty_table_and_no_lse():
+    f = fab()
+    p = Problem([3, 0], 4, 2, 64, 16, seed=15)
+    d = p.device()
+    o, lse = f.decode(**{**d, "block_table": d["block_table"][:, :0]})
+    assert torch.all(o == 0) and torch.all(lse == -float("inf"))
+    full, _ = f.decode(**d)
+    o = torch.empty_like(full)
+    ws = torch.empty(max(1, f.fa_decode_workspace_size(2, 4, 2, 64)), dtype=torch.uint8, device=DEV)
+    f.fa_decode(d["q"], d["k_cache"], d["v_cache"], d["block_table"], d["seq_lens"], o, None, p.scale, workspace=ws)
+    assert torch.equal(o, full)
+    o, lse = f.decode(**{**d, "q": d["q"][:0], "block_table": d["block_table"][:0], "seq_lens": d["seq_lens"][:0]})
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(kv):
+    """A cache of 2^31 + some elements: pages behind the 2^31st element are
+    written and read at their own place."""
+    f = fab()
+    page, heads_kv, dim = 64, 8, 128
+    pool = (1 << 31) // (page * heads_kv * dim) + 4
+    dtype = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    kc = torch.empty(pool, page, heads_kv, dim, dtype=dtype, device=DEV)
+    vc = torch.empty_like(kc)
+    p = Problem([150, 64], 8, heads_kv, dim, page, kv, seed=16)
+    where = torch.tensor([pool - 1, 0, pool - 2, 1, pool - 3, pool // 2, pool - 4, 2])[:p.k.shape[0]]
+    table = torch.where(p.table >= 0, where[p.table.clamp(min=0).long()].int(), -1)
+    for src, dst in ((p.k, kc), (p.v, vc)):
+        dst[where.to(DEV)] = src.to(DEV)
+    d = p.device()
+    small = f.decode(**d)
+    big = f.decode(**{**d, "k_cache": kc, "v_cache": vc, "block_table": table.to(DEV)})
+    assert torch.equal(small[0], big[0]) and torch.equal(small[1], big[1])
+    row = torch.randn(1, heads_kv, dim, device=DEV).bfloat16()
+    slot = torch.tensor([(pool - 1) * page + 5], device=DEV)
+    f.kv_append(row, row, kc, vc, slot)
+    assert torch.equal(kc[pool - 1, 5].float(), row[0].to(dtype).float())
+
+
+# ------------------------------------------------------------------ as a program uses them
+def test_prefill_then_decode_steps_match_the_forward():
+    """plan -> append -> forward over the prompts, then plan -> append ->
+    decode token by token: every step's row is the row that the packed causal
+    forward over all tokens gives (both within their bounds of the oracle)."""
+    f = fab()
+    H, Hkv, d, page, steps = 8, 2, 128, 16, 20
+    prompt, B = [37, 1, 64, 15], 4
+    total = [n + steps for n in prompt]
+    case = si.Case("serve", H, d, total, total, True, 77, heads_kv=Hkv)
+    q, k, v, _ = (t.to(DEV) for t in case.tensors())
+    cu = torch.from_numpy(case.cu_q).to(DEV)
+    full_o, full_lse = f.forward_lse(q, k, v, cu, cu, case.cu_q, case.cu_q, True, case.softmax_scale)
+    kc = torch.full((64, page, Hkv, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    vc = torch.full_like(kc, float("nan"))
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = torch.full((B, 8), -1, **i32)
+    free = torch.randperm(64, generator=torch.Generator().manual_seed(1)).int().to(DEV)
+    seq, start = torch.zeros(B, **i32), torch.zeros(1, **i32)
+    base = case.cu_q[:-1]
+    rows = np.concatenate([base[b] + np.arange(n) for b, n in enumerate(prompt)])
+    for step in range(steps + 1):
+        if step:
+            rows = np.array([base[b] + n + step - 1 for b, n in enumerate(prompt)])
+        at = torch.from_numpy(rows).to(DEV)
+        new = torch.tensor(prompt if step == 0 else [1] * B, **i32)
+        plan = f.kv_plan(table, seq, new, free, page, len(rows), free_start=start)
+        f.kv_append(k[at], v[at], kc, vc, plan.slots)
+        seq, start = plan.seq_lens, plan.free_next
+        last = at if step else torch.from_numpy(np.array([base[b] + n - 1 for b, n in enumerate(prompt)])).to(DEV)
+        o, lse = f.decode(q[last], kc, vc, table, seq, case.softmax_scale)
+        torch.testing.assert_close(lse, full_lse[last], rtol=2e-6, atol=1e-5)
+        # each side is within 2^-8 (|o| + sum p|v|) of the exact row; sum p|v| < 4 for these values
+        assert (o.float() - full_o[last].float()).abs().max().item() <= 2 * U * 8
+    assert start.item() == sum(-(-n // page) for n in total)
+    flat = kc.view(-1, Hkv, d)
+    for b, n in enumerate(total):
+        j = torch.arange(n, device=DEV)
+        slots = table[b].long()[j // page] * page + j % page
+        assert torch.equal(flat[slots], k[int(base[b]):int(base[b]) + n])
+
+
+def test_decode_loop_in_a_graph():
+    """One captured step (plan, append, decode, state copied forward) replayed:
+    the same as eager steps, while another graph with its own buffers replays
+    on a second stream."""
+    f = fab()
+    H, Hkv, d, page, B, steps = 8, 2, 64, 16, 3, 40
+
+    class Loop:
+        def __init__(self, seed):
+            g = torch.Generator(device=DEV).manual_seed(seed)
+            i32 = dict(dtype=torch.int32, device=DEV)
+            rnd = lambda *s: torch.randn(*s, device=DEV, generator=g).bfloat16()  # noqa: E731
+            self.qs, self.ks, self.vs = rnd(steps, B, H, d), rnd(steps, B, Hkv, d), rnd(steps, B, Hkv, d)
+            self.q, self.k, self.v = rnd(B, H, d), rnd(B, Hkv, d), rnd(B, Hkv, d)
+            self.kc, self.vc = rnd(16, page, Hkv, d), rnd(16, page, Hkv, d)
+            self.table, self.seq, self.start = torch.full((B, 4), -1, **i32), torch.zeros(B, **i32), torch.zeros(1, **i32)
+            self.new = torch.ones(B, **i32)
+            self.free = torch.arange(16, **i32)
+
+        def feed(self, i):
+            self.q.copy_(self.qs[i]), self.k.copy_(self.ks[i]), self.v.copy_(self.vs[i])
+
+        def step(self):
+            p = f.kv_plan(self.table, self.seq, self.new, self.free, page, B, free_start=self.start)
+            f.kv_append(self.k, self.v, self.kc, self.vc, p.slots)
+            out = f.decode(self.q, self.kc, self.vc, self.table, p.seq_lens, d ** -0.5)
+            self.seq.copy_(p.seq_lens), self.start.copy_(p.free_next)
+            return out
+
+        def reset(self):
+            self.table.fill_(-1), self.seq.zero_(), self.start.zero_()
+
+    loops = [Loop(1), Loop(2)]
+    want = []
+    for lp in loops:
+        got = []
+        for i in range(steps):
+            lp.feed(i)
+            got.append(tuple(t.clone() for t in lp.step()))
+        want.append(got)
+        lp.reset()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for lp in loops:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(lp.step())
+        graphs.append(g)
+        lp.reset()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in loops]
+    got = [[], []]
+    for i in range(steps):
+        for n in range(2):
+            with torch.cuda.stream(streams[n]):
+                loops[n].feed(i)
+                graphs[n].replay()
+                got[n].append(tuple(t.clone() for t in outs[n]))
+    torch.cuda.synchronize()
+    for n in range(2):
+        for a, b in zip(want[n], got[n]):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_decode_from_two_threads_on_two_streams():
+    """Calls in flight at once, each with its own workspace, give the bits of
+    a plain call; each caller's stream is ordered after its own."""
+    f = fab()
+    p = Problem([900, 5, 333, 64], 8, 2, 128, 16, seed=21)
+    args = p.device()
+    plain = f.decode(**args)
+    p.check(*plain)
+    torch.cuda.synchronize()
+    results, errors = {}, []
+
+    def worker(tid):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                results[tid] = [f.decode(**args) for _ in range(30)]
+            stream.synchronize()
+        except Exception as e:  # reported on the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for got in results.values():
+        for o, lse in got:
+            assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])
+
+
+def test_stream_argument():
+    """stream=: the work runs on it, after what is queued there."""
+    f = fab()
+    p = Problem([100, 40], 4, 2, 64, 16, seed=22)
+    args = p.device()
+    plain = f.decode(**args)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    late = args["q"].clone().zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(10_000_000)
+        late.copy_(args["q"])
+    o, lse = f.decode(**{**args, "q": late}, stream=stream)
+    stream.synchronize()
+    assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])

@@ -1,0 +1,215 @@
+"""Paged cache operators without a GPU: the oracle's pins, and the refusals
+of the C entry points and of the binding (all before anything touches the
+device)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import paged
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from attention_backward_sm_gb300 import build
+    build.build()
+    from attention_backward_sm_gb300 import _lib
+    return _lib.load()
+
+
+# ------------------------------------------------------------------ oracle
+def test_plan_worked_by_hand():
+    """Pages of 4: request 0 holds 5 tokens on pages 7, 2 and gets 4; request
+    1 is empty and gets none; request 2 is empty and gets 2."""
+    table = [[7, 2, -1], [-1, -1, -1], [-1, -1, -1]]
+    t, slots, pos, cu, after, nxt = paged.plan(table, [5, 0, 0], [4, 0, 2], [9, 4, 6], 4, 8)
+    assert slots.tolist() == [9, 10, 11, 36, 16, 17, -1, -1]
+    assert pos.tolist() == [5, 6, 7, 8, 0, 1, 0, 0]
+    assert cu.tolist() == [0, 4, 4, 6] and after.tolist() == [9, 0, 2] and nxt == 2
+    assert t.tolist() == [[7, 2, 9], [-1, -1, -1], [4, -1, -1]]
+
+
+def test_e4m3_matches_torch_on_every_border():
+    """All 8-bit values, the midpoints between neighbours and their float32
+    neighbours, against torch's conversion."""
+    v = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    v = v[torch.isfinite(v)].sort().values
+    mid = (v[1:] + v[:-1]) / 2
+    x = torch.cat([v, mid, torch.nextafter(mid, mid + 1), torch.nextafter(mid, mid - 1)])
+    want = x.clamp(-448, 448).to(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(paged.e4m3(x.double().numpy()), want)
+    assert paged.e4m3([1e9, -1e9, np.inf]).tolist() == [448, -448, 448] and np.isnan(paged.e4m3(np.nan))
+
+
+@pytest.mark.parametrize("window", [0, 5])
+def test_decode_is_the_last_row_of_the_forward(window):
+    """Over a permuted paged copy of packed K, V, single-token attention is
+    the last query row of the causal forward."""
+    rng = np.random.default_rng(3)
+    H, Hkv, d, ps = 4, 2, 8, 4
+    lens = [1, 4, 11]
+    width = 3
+    k_cache, v_cache = rng.normal(size=(2, 12, ps, Hkv, d))
+    order = rng.permutation(12)
+    table = order[:9].reshape(3, width)
+    q = rng.normal(size=(3, H, d))
+    o, lse, _, _ = paged.decode(q, k_cache, v_cache, table, lens, 0.3, window)
+    for b, n in enumerate(lens):
+        k = k_cache[table[b]].reshape(-1, Hkv, d)[:n]
+        v = v_cache[table[b]].reshape(-1, Hkv, d)[:n]
+        for h in range(H):
+            qs = np.zeros((n, d))
+            qs[-1] = q[b, h]
+            fo, m, l = oracle.forward_head(qs, k[:, h // 2], v[:, h // 2], 0.3, True, window)
+            assert np.allclose(o[b, h], fo[-1], atol=1e-12)
+            assert np.isclose(lse[b, h], m[-1] + np.log(l[-1]), atol=1e-12)
+
+
+def test_decode_rows_without_keys_and_bad_pages():
+    rng = np.random.default_rng(4)
+    k_cache, v_cache = rng.normal(size=(2, 3, 2, 1, 8))
+    q = rng.normal(size=(3, 1, 8))
+    o, lse, _, _ = paged.decode(q, k_cache, v_cache, [[0, 1], [-1, 3], [-1, 2]], [0, 4, 4], 1.0)
+    assert np.all(o[:2] == 0) and np.all(lse[:2] == -np.inf)
+    only = paged.decode(q[2:], k_cache, v_cache, [[2]], [2], 1.0)
+    assert np.allclose(o[2], only[0][0]) and np.isclose(lse[2, 0], only[1][0, 0])
+
+
+# ------------------------------------------------------------------ C refusals
+P = ctypes.c_void_p(16)   # never dereferenced: the checks fail first
+
+
+def _plan_rc(lib, **kw):
+    a = dict(table=P, stride=8, width=8, seq=P, new=ctypes.c_void_p(32), free=P, num_free=4, start=None, page=16,
+             batch=2, tokens=4, slots=P, pos=P, cu=P, out=ctypes.c_void_p(64), next=ctypes.c_void_p(96))
+    a.update(kw)
+    return lib.fa_kv_plan(a["table"], a["stride"], a["width"], a["seq"], a["new"], a["free"], a["num_free"],
+                          a["start"], a["page"], a["batch"], a["tokens"], a["slots"], a["pos"], a["cu"], a["out"],
+                          a["next"], None)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(page=0), b"page_size"), (dict(batch=-1), b"batch"), (dict(tokens=-1), b"num_tokens"),
+    (dict(num_free=-1), b"num_free"), (dict(width=-1), b"max_pages"), (dict(stride=7), b"table_stride"),
+    (dict(table=None), b"NULL"), (dict(seq=None), b"NULL"), (dict(free=None), b"NULL"), (dict(slots=None), b"NULL"),
+    (dict(cu=None), b"NULL"), (dict(next=None), b"NULL"), (dict(out=P), b"seq_lens_out"),
+    (dict(start=ctypes.c_void_p(96)), b"free_start"), (dict(slots=ctypes.c_void_p(20)), b"aligned"),
+    (dict(pos=ctypes.c_void_p(18)), b"aligned")])
+def test_plan_refusals(lib, kw, word):
+    assert _plan_rc(lib, **kw) == 1
+    assert word in lib.fa_last_error()
+
+
+def _append_rc(lib, **kw):
+    a = dict(k=P, v=P, ks=256, vs=256, slots=P, n=4, kc=P, vc=P, kind=0, k_scale=None, v_scale=None, page_stride=4096,
+             slot_stride=256, head_stride=128, pages=8, page=16, heads_kv=2, dim=128)
+    a.update(kw)
+    return lib.fa_kv_append(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(dim=96), 2, b"head_dim"), (dict(kind=2), 1, b"kv_type"), (dict(heads_kv=0), 1, b"heads_kv"),
+    (dict(pages=-1), 1, b"num_pages"), (dict(page=0), 1, b"page_size"), (dict(k_scale=P), 1, b"e4m3"),
+    (dict(page_stride=64), 1, b"page_stride"), (dict(slot_stride=260), 1, b"slot_stride"),
+    (dict(head_stride=0), 1, b"head_stride"), (dict(kind=1, head_stride=136), 1, b"head_stride"),
+    (dict(kc=ctypes.c_void_p(8)), 1, b"aligned"), (dict(n=-1), 1, b"num_tokens"), (dict(ks=128), 1, b"k_row_stride"),
+    (dict(vs=260), 1, b"v_row_stride"), (dict(k=None), 1, b"NULL"), (dict(slots=None), 1, b"NULL"),
+    (dict(v=ctypes.c_void_p(8)), 1, b"aligned"), (dict(slots=ctypes.c_void_p(4)), 1, b"aligned")])
+def test_append_refusals(lib, kw, code, word):
+    assert _append_rc(lib, **kw) == code
+    assert word in lib.fa_last_error()
+
+
+def test_append_of_nothing_succeeds(lib):
+    assert _append_rc(lib, n=0, k=None, v=None, slots=None) == 0
+    assert lib.fa_last_error() == b""
+
+
+def _decode_rc(lib, **kw):
+    a = dict(q=P, qs=512, kc=P, vc=P, kind=0, k_scale=None, v_scale=None, page_stride=4096, slot_stride=256,
+             head_stride=128, pages=8, page=16, table=P, table_stride=4, width=4, seq=P, batch=2, heads=4, heads_kv=2,
+             dim=128, window=0, scale=0.1, o=P, lse=P, ws=P, ws_bytes=1 << 40)
+    a.update(kw)
+    return lib.fa_decode(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(dim=32), 2, b"head_dim"), (dict(heads=3), 1, b"multiple"), (dict(heads=0), 1, b"multiple"),
+    (dict(batch=-1), 1, b"batch"), (dict(window=-1), 1, b"window"), (dict(scale=float("nan")), 1, b"scale"),
+    (dict(scale=float("inf")), 1, b"scale"), (dict(width=-1), 1, b"max_pages"),
+    (dict(width=1 << 20, page=1 << 20), 2, b"too long"), (dict(table_stride=-4), 1, b"table_stride"),
+    (dict(qs=256), 1, b"q_row_stride"), (dict(qs=516), 1, b"q_row_stride"), (dict(q=None), 1, b"NULL"),
+    (dict(seq=None), 1, b"NULL"), (dict(table=None), 1, b"NULL"), (dict(kc=None), 1, b"NULL"),
+    (dict(o=ctypes.c_void_p(8)), 1, b"aligned"), (dict(seq=ctypes.c_void_p(18)), 1, b"aligned"),
+    (dict(kind=0, v_scale=P), 1, b"e4m3"), (dict(slot_stride=100), 1, b"slot_stride")])
+def test_decode_refusals(lib, kw, code, word):
+    assert _decode_rc(lib, **kw) == code
+    assert word in lib.fa_last_error()
+
+
+def test_decode_workspace_size(lib):
+    assert lib.fa_decode_workspace_size(4, 6, 4, 128) == 0 and b"multiple" in lib.fa_last_error()
+    assert lib.fa_decode_workspace_size(4, 8, 4, 96) == 0 and b"head_dim" in lib.fa_last_error()
+    n = lib.fa_decode_workspace_size(64, 32, 8, 128)
+    assert lib.fa_last_error() == b""
+    if n:   # too little of it, none of it and a misaligned one are refused
+        kw = dict(batch=64, heads=32, heads_kv=8, page_stride=16384, slot_stride=1024, qs=4096)
+        assert _decode_rc(lib, ws_bytes=n - 1, **kw) == 1 and b"workspace" in lib.fa_last_error()
+        assert _decode_rc(lib, ws=None, **kw) == 1 and b"workspace" in lib.fa_last_error()
+        assert _decode_rc(lib, ws=ctypes.c_void_p(8), **kw) == 1 and b"workspace" in lib.fa_last_error()
+
+
+def test_decode_of_no_requests_succeeds(lib):
+    assert _decode_rc(lib, batch=0, q=None, o=None, seq=None, table=None) == 0
+
+
+# ------------------------------------------------------------------ binding refusals
+def _tensors():
+    return dict(q=torch.zeros(2, 4, 64, dtype=torch.bfloat16), k_cache=torch.zeros(6, 8, 2, 64, dtype=torch.bfloat16),
+                v_cache=torch.zeros(6, 8, 2, 64, dtype=torch.bfloat16),
+                block_table=torch.zeros(2, 3, dtype=torch.int32), seq_lens=torch.ones(2, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("change,word", [
+    ({}, "CUDA"),
+    (dict(q=torch.zeros(2, 4, 64)), "bfloat16"),
+    (dict(q=torch.zeros(2, 4, 32, dtype=torch.bfloat16)), "head_dim"),
+    (dict(q=torch.zeros(3, 4, 64, dtype=torch.bfloat16)), "q must"),
+    (dict(q=torch.zeros(2, 64, 4, dtype=torch.bfloat16).transpose(1, 2)), "packed"),
+    (dict(q=torch.zeros(2, 256, dtype=torch.bfloat16)), "q must"),
+    (dict(v_cache=torch.zeros(6, 8, 1, 64, dtype=torch.bfloat16)), "one shape"),
+    (dict(v_cache=torch.zeros(6, 8, 2, 64, dtype=torch.float16)), "float8"),
+    (dict(v_cache=torch.zeros(6, 2, 8, 64, dtype=torch.bfloat16).transpose(1, 2)), "strides"),
+    (dict(block_table=torch.zeros(2, 3, dtype=torch.int64)), "block_table"),
+    (dict(block_table=torch.zeros(3, 2, dtype=torch.int32).t()), "contiguous rows"),
+    (dict(seq_lens=torch.ones(3, dtype=torch.int32)), "seq_lens"),
+    (dict(seq_lens=torch.ones(2)), "seq_lens"),
+    (dict(k_scale=torch.ones(3)), "k_scale"),
+    (dict(v_scale=torch.ones(2, dtype=torch.float64)), "v_scale")])
+def test_decode_binding_refusals(lib, change, word):
+    import attention_backward_sm_gb300 as fab
+    with pytest.raises((ValueError, fab.FabwdError), match=word):
+        fab.decode(**{**_tensors(), **change}, scale=0.1)
+
+
+def test_append_and_plan_binding_refusals(lib):
+    import attention_backward_sm_gb300 as fab
+    t = _tensors()
+    k = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    slots = torch.zeros(5, dtype=torch.int64)
+    with pytest.raises(ValueError, match="CUDA"):
+        fab.kv_append(k, k, t["k_cache"], t["v_cache"], slots)
+    with pytest.raises(ValueError, match="slots"):
+        fab.kv_append(k, k, t["k_cache"], t["v_cache"], slots.int())
+    with pytest.raises(ValueError, match="k must"):
+        fab.kv_append(k[:4], k, t["k_cache"], t["v_cache"], slots)
+    i32 = dict(dtype=torch.int32)
+    args = [t["block_table"], t["seq_lens"], torch.ones(2, **i32), torch.zeros(4, **i32)]
+    with pytest.raises(ValueError, match="CUDA"):
+        fab.kv_plan(*args, 8, 2)
+    with pytest.raises(ValueError, match="new_lens"):
+        fab.kv_plan(*args[:2], torch.ones(3, **i32), args[3], 8, 2)
+    with pytest.raises(ValueError, match="free_start"):
+        fab.kv_plan(*args, 8, 2, free_start=torch.zeros(2, **i32))
