@@ -1,16 +1,34 @@
 // Attention of one new token per request over a paged key/value cache.
 //
-// For request b, query head h (key/value head h / (heads / heads_kv)) and
-// the visible cached keys j in [max(0, len - window), len):
+// For request b, query head h (key/value head h / G, G = heads / heads_kv)
+// and the visible cached keys j in [max(0, len - window), len):
 //     x_j = scale * q . k_j,  o = sum_j exp(x_j) v_j / sum_j exp(x_j),
 //     lse = ln sum_j exp(x_j)
-// in one pass over the keys with a running maximum and sum.  Keys whose
-// block-table entry is not a page of the cache are not seen; a row that sees
-// no key gets o = 0, lse = -inf.
-#include <cuda_fp16.h>
+// Keys whose block-table entry is not a page of the cache are not seen; a
+// row that sees no key gets o = 0, lse = -inf.
+//
+// The call has to read every visible key and value once and does 2 G
+// operations per cached bf16 byte: it is bound by HBM.  So
+//   * the G query heads of a key/value head share one pass over its keys: they
+//     are the rows of 16-row tensor-core products (S = Q K^T, O += P V), which
+//     keeps the arithmetic far below the time of the loads;
+//   * keys are taken in tiles of kTile; the tiles of all (request, key/value
+//     head) units, in order, are cut into equal runs, one per resident block.
+//     Ragged lengths, one long request and many short ones all load every SM
+//     alike, and a unit that lies in several runs leaves at most one partial
+//     result per run, which combine_kernel joins (fixed order: same bits on
+//     every call).  The host needs no lengths.
+//   * K and V rows come through cp.async into a ring of kStages tiles (any
+//     page size and strides; a TMA box would tie the tile to the page), the
+//     block-table entries one tile further ahead.
+// Each warp takes 16 keys of a tile at a time with a running maximum and sum
+// of its own; the warps' states are joined where a unit ends.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
+#include "internal.h"
 #include "paged.h"
 #include "sm103.cuh"
 
@@ -18,107 +36,736 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;         // query heads per block (rows of the tensor-core products)
+constexpr int kMaxBlocks = 608;   // upper bound of a launch's blocks: 4 on each of 152 SMs
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float2 e4m3_pair(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  return __half22float2(*reinterpret_cast<__half2*>(&h));
+template <int D, bool E4M3>
+struct Shape {
+  static constexpr int kElem = E4M3 ? 1 : 2;
+  static constexpr int kRowBytes = D * kElem;
+  // Keys per tile: K and V tiles together are at least the 4 * 16 * D floats
+  // that joining the warps takes (it reuses the stage just consumed).
+  static constexpr int kTile = E4M3 || D == 64 ? 128 : 64;
+  static constexpr int kTileBytes = kTile * kRowBytes;       // of K, and of V
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = 3;
+  // Blocks per SM: as many as the stages allow in 227 KB.
+  static constexpr int kBlocksPerSm = kStageBytes >= 65536 ? 1 : (kStageBytes >= 32768 ? 2 : 3);
+  static constexpr int kOffsets = kStages + 1;               // tiles whose row offsets are kept
+  static constexpr int kQBytes = kRows * D * 2;              // query rows of one unit (ring of kStages units)
+  static constexpr int kOffQ = kStages * kStageBytes;
+  static constexpr int kOffOffsets = kOffQ + kStages * kQBytes;
+  static constexpr int kOffSeen = kOffOffsets + kOffsets * kTile * 8;
+  static constexpr int kOffJoin = kOffSeen + kOffsets * (kTile / 32) * 4;
+  static constexpr int kOffScan = kOffJoin + 2 * kWarps * kRows * 4;
+  static constexpr int kSmem = kOffScan + 64;
+  static_assert(kStageBytes >= kWarps * kRows * D * 4, "join buffer");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+// A unit that is cut by the end of a block's run, seen from the block in
+// which it starts: blocks [this one, last] hold its partial results.
+struct Cut {
+  int unit;    // b * heads_kv + key/value head, or -1
+  int last;
+  int slot;    // of the first block's partial result
+  int pad;
+};
+
+struct Work {
+  float* parts;   // [blocks][2 slots][rows][D] sums of p v, then [rows] reference maxima, [rows] sums of p
+  Cut* cuts;      // [blocks]
+};
+
+struct Launch {
+  int rows;        // query heads per chunk (at most kRows)
+  int chunks;      // chunks of the G query heads of a key/value head
+  int blocks;      // blocks per chunk
+};
+
+__host__ __device__ inline size_t part_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;   // fewer source bytes than 16: the rest is zero-filled
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// c += a b, 16 x 8 x 16, fp32 accumulate; operands bf16 or fp16.
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two 8-bit values to two halves (exact), from bits 0-15 or 16-31.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+// Programmatic dependent launch: the next kernel of the stream may be set up
+// from here on; it waits for this one's end (and its writes) in pdl_wait.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Byte offset of 16-byte piece c of row r in a tile whose rows are RB bytes,
+// so that eight consecutive rows' pieces c lie in different banks.
+template <int RB>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  if constexpr (RB >= 128) return r * RB + ((c ^ (r & 7)) << 4);
+  else return r * RB + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// D / 32 consecutive elements of a cache row, as floats.
-template <int N, bool E4M3>
-__device__ __forceinline__ void load_row(const void* base, long long at, float (&x)[N]) {
+// ------------------------------------------------------------------ partition
+struct Lens {
+  const int32_t* seq;
+  int most;      // max_pages * page_size
+  int window;
+  __device__ __forceinline__ int len(int b) const { return min(max(__ldg(seq + b), 0), most); }
+  __device__ __forceinline__ int first(int len) const { return window > 0 ? max(0, len - window) : 0; }
+  // A request without keys has one (empty) tile: its row is written too.
+  template <int TILE>
+  __device__ __forceinline__ int tiles(int len) const {
+    return max(1, (len - first(len) + TILE - 1) / TILE);
+  }
+};
+
+// First tile of run c when `total` tiles are cut into n <= total runs (none
+// empty), and the run that holds tile x.
+__device__ __forceinline__ long long run_start(long long c, long long total, int n) { return c * total / n; }
+__device__ __forceinline__ int run_of(long long x, long long total, int n) {
+  return static_cast<int>(((x + 1) * n - 1) / total);
+}
+
+// A place in the list of tiles: tile t of nt of (request b, key/value head hk).
+template <int TILE>
+struct Place {
+  int b, hk, t, nt, first, len;
+  __device__ __forceinline__ void request(const Lens& L, int batch) {
+    if (b >= batch) return;
+    len = L.len(b);
+    first = L.first(len);
+    nt = L.tiles<TILE>(len);
+  }
+  __device__ __forceinline__ void next(const Lens& L, int batch, int heads_kv) {
+    if (++t < nt) return;
+    t = 0;
+    if (++hk < heads_kv) return;
+    hk = 0;
+    ++b;
+    request(L, batch);
+  }
+};
+
+// ------------------------------------------------------------------ main kernel
+template <int D, bool E4M3, bool HALF>   // HALF: at most 8 rows
+__global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
+    decode_kernel(const DecodeParams p, const Launch lc, const Work work) {
+  using S = Shape<D, E4M3>;
+  constexpr int TILE = S::kTile, RB = S::kRowBytes, ST = S::kStages;
+  constexpr int NR = HALF ? 1 : 2;   // groups of 8 rows with data
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint32_t sbase = smem_u32(smem);
+  long long* const offsets = reinterpret_cast<long long*>(smem + S::kOffOffsets);
+  uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + S::kOffSeen);
+  float* const join_m = reinterpret_cast<float*>(smem + S::kOffJoin);
+  float* const join_l = join_m + kWarps * kRows;
+  long long* const scan = reinterpret_cast<long long*>(smem + S::kOffScan);   // [kWarps]
+  int* const found = reinterpret_cast<int*>(scan + kWarps);                   // b, hk, t
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.heads / p.kv.heads_kv;
+  const int row0 = blockIdx.y * lc.rows;                 // first query head of this chunk within its group
+  const int rows = min(lc.rows, G - row0);
+  const int block = blockIdx.y * lc.blocks + blockIdx.x;
+  const Lens L{p.seq_lens, p.max_pages * p.kv.page_size, p.window};
+
+  // Rows past `rows` of the query tiles stay zero.
+  for (int i = tid; i < ST * S::kQBytes / 16; i += kThreads)
+    reinterpret_cast<uint4*>(smem + S::kOffQ)[i] = make_uint4(0, 0, 0, 0);
+
+  // The run of this block: every block counts all tiles (a scan over the
+  // requests), then finds where its share starts.
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += L.tiles<TILE>(L.len(b));
+  mine *= p.kv.heads_kv;
+  long long upto = mine;
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    if constexpr (E4M3) {
-      const float2 f = e4m3_pair(*reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(base) + at + i));
-      x[i] = f.x;
-      x[i + 1] = f.y;
-    } else {
-      const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + at + i);
-      x[i] = __uint_as_float(u << 16);
-      x[i + 1] = __uint_as_float(u & 0xFFFF0000u);
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += x;
+  }
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += scan[w];
+    total += scan[w];
+  }
+  const int runs = total < lc.blocks ? static_cast<int>(total) : lc.blocks;
+  if (static_cast<int>(blockIdx.x) >= runs) {
+    if (tid == 0) work.cuts[block].unit = -1;
+    return;
+  }
+  const long long start = run_start(blockIdx.x, total, runs);
+  const int n = static_cast<int>(run_start(blockIdx.x + 1, total, runs) - start);
+  if (start >= upto - mine && start < upto) {
+    long long at = upto - mine;
+    for (int b = b0; b < b1; ++b) {
+      const int nt = L.tiles<TILE>(L.len(b));
+      const long long all = static_cast<long long>(nt) * p.kv.heads_kv;
+      if (start < at + all) {
+        found[0] = b;
+        found[1] = static_cast<int>((start - at) / nt);
+        found[2] = static_cast<int>((start - at) % nt);
+        break;
+      }
+      at += all;
     }
   }
-}
-
-// One block per (request, query head); warp w takes keys w, w + kWarps, ...
-// and the warps' softmax states are joined at the end.
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(const DecodeParams p) {
-  constexpr int N = D / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-  const int b = blockIdx.x / p.heads, h = blockIdx.x % p.heads;
-  const int hk = h / (p.heads / p.kv.heads_kv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = min(max(p.seq_lens[b], 0), p.max_pages * p.kv.page_size);
-  const int first = p.window > 0 ? max(0, len - p.window) : 0;
-  const float ks = p.kv.k_scale ? p.kv.k_scale[hk] : 1.f, vs = p.kv.v_scale ? p.kv.v_scale[hk] : 1.f;
-  float q[N], o[N], m = -INFINITY, l = 0.f;
-  load_row<N, false>(p.q, b * p.q_row_stride + static_cast<long long>(h) * D + lane * N, q);
-#pragma unroll
-  for (int i = 0; i < N; ++i) o[i] = 0.f;
-  for (int j = first + warp; j < len; j += kWarps) {
-    const int page = p.table[b * p.table_stride + j / p.kv.page_size];
-    if (page < 0 || page >= p.kv.num_pages) continue;
-    const long long at = page * p.kv.page_stride + (j % p.kv.page_size) * p.kv.slot_stride + hk * p.kv.head_stride +
-                         lane * N;
-    float k[N], v[N];
-    load_row<N, E4M3>(p.kv.k, at, k);
-    load_row<N, E4M3>(p.kv.v, at, v);
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) x = fmaf(q[i], k[i], x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    x *= p.scale * ks * kLog2e;
-    const float top = fmaxf(m, x);
-    const float keep = exp2f(m - top), e = exp2f(x - top);
-    m = top;
-    l = l * keep + e;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fmaf(o[i], keep, e * v[i]);
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) s_o[warp][lane * N + i] = o[i];
   __syncthreads();
-  float top = -INFINITY;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  float total = 0.f;
-  for (int w = 0; w < kWarps; ++w)
-    if (s_l[w] != 0.f) total += s_l[w] * exp2f(s_m[w] - top);
-  const long long row = static_cast<long long>(b) * p.heads + h;
-  for (int c = threadIdx.x; c < D; c += kWarps * 32) {
-    float sum = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      if (s_l[w] != 0.f) sum += s_o[w][c] * exp2f(s_m[w] - top);
-    const float out = total == 0.f ? 0.f : sum / total * vs;
-    p.o[row * D + c] = static_cast<uint16_t>(pack_bf16x2(out, out) & 0xffffu);
+  Place<TILE> here;   // the tile being computed
+  here.b = found[0];
+  here.hk = found[1];
+  here.t = found[2];
+  here.request(L, p.batch);
+  Place<TILE> ahead = here;   // the next tile to load
+  pdl_launch();
+
+  // Page of this thread's key of a tile, and from it the row's offset (bytes,
+  // without the head's; -1: not seen) and the tile's bits of seen keys.
+  auto look_up = [&](const Place<TILE>& at) -> int {
+    const int key = at.first + at.t * TILE + tid;
+    if (tid >= TILE || key >= at.len) return -1;
+    return __ldg(p.table + at.b * p.table_stride + key / p.kv.page_size);
+  };
+  auto store_offset = [&](const Place<TILE>& at, int page, int ring) {
+    if (tid >= TILE) return;
+    const int key = at.first + at.t * TILE + tid;
+    const bool ok = key < at.len && page >= 0 && page < p.kv.num_pages;
+    offsets[ring * TILE + tid] =
+        ok ? (page * p.kv.page_stride + (key % p.kv.page_size) * p.kv.slot_stride) * S::kElem : -1;
+    const uint32_t bits = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) seen[ring * (TILE / 32) + warp] = bits;
+  };
+  constexpr int CPR = RB / 16, RPP = kThreads / CPR;   // 16-byte pieces per row, rows per pass
+  const int piece = tid % CPR, row_in_pass = tid / CPR;
+  auto load_tile = [&](const Place<TILE>& at, int ring, int stage, int q_slot, bool with_q) {
+    const long long head = at.hk * p.kv.head_stride * S::kElem + piece * 16;
+    const unsigned char* const kb = static_cast<const unsigned char*>(p.kv.k) + head;
+    const unsigned char* const vb = static_cast<const unsigned char*>(p.kv.v) + head;
+    const uint32_t dst = sbase + stage * S::kStageBytes;
+#pragma unroll
+    for (int i = 0; i < TILE / RPP; ++i) {
+      const int r = row_in_pass + i * RPP;
+      const long long off = offsets[ring * TILE + r];
+      const uint32_t to = dst + swizzled<RB>(r, piece);
+      const bool ok = off >= 0;   // unseen rows are zero-filled: nothing is read
+      cp_async16(to, ok ? static_cast<const void*>(kb + off) : p.q, ok);
+      cp_async16(to + S::kTileBytes, ok ? static_cast<const void*>(vb + off) : p.q, ok);
+    }
+    if (with_q) {
+      const uint16_t* const q = p.q + at.b * p.q_row_stride + (static_cast<long long>(at.hk) * G + row0) * D;
+      for (int i = tid; i < rows * (D / 8); i += kThreads) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        cp_async16(sbase + S::kOffQ + q_slot * S::kQBytes + swizzled<D * 2>(r, c), q + r * D + c * 8, true);
+      }
+    }
+  };
+
+  // Prologue: the first ST - 1 tiles are on their way before the loop.
+  int q_load = 0;                 // query slot of the unit being loaded
+  {
+    Place<TILE> load = here;
+    for (int i = 0; i < ST - 1; ++i) {
+      if (i < n) {
+        store_offset(ahead, look_up(ahead), i);
+        ahead.next(L, p.batch, p.kv.heads_kv);
+      }
+    }
+    __syncthreads();
+    for (int i = 0; i < ST - 1; ++i) {
+      if (i < n) {
+        const bool with_q = i == 0 || load.t == 0;
+        if (i > 0 && with_q) q_load = q_load + 1 == ST ? 0 : q_load + 1;
+        load_tile(load, i, i, q_load, with_q);
+        load.next(L, p.batch, p.kv.heads_kv);
+      }
+      cp_commit();
+    }
   }
-  if (p.lse && threadIdx.x == 0) p.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
+  int page_ahead = ST - 1 < n ? look_up(ahead) : -1;
+
+  uint32_t qa[D / 16][4];                   // query fragments (e4m3: fp16, rescaled per row)
+  float o[D / 8][4];
+  float m[NR], l[NR], row_scale[NR];
+  int stage = 0, ring = 0, q_slot = 0;
+  int load_stage = ST - 1, load_ring = ST - 1;
+  bool fresh = true, first_piece = true;
+  const int g = lane >> 2, quad = lane & 3;
+
+  for (int s = 0; s < n; ++s) {
+    cp_wait<ST - 2>();
+    const bool more = s + ST - 1 < n;
+    if (more) store_offset(ahead, page_ahead, load_ring);
+    __syncthreads();   // tile s has landed for every thread; tile s - 1's stage is free
+    if (more) {
+      const bool with_q = ahead.t == 0;
+      if (with_q) q_load = q_load + 1 == ST ? 0 : q_load + 1;
+      load_tile(ahead, load_ring, load_stage, q_load, with_q);
+      ahead.next(L, p.batch, p.kv.heads_kv);
+      if (s + ST < n) page_ahead = look_up(ahead);
+      load_stage = load_stage + 1 == ST ? 0 : load_stage + 1;
+      load_ring = load_ring + 1 == S::kOffsets ? 0 : load_ring + 1;
+    }
+    cp_commit();
+
+    if (fresh) {
+      fresh = false;
+      const uint32_t qb = sbase + S::kOffQ + q_slot * S::kQBytes;
+      const float ks = p.kv.k_scale ? __ldg(p.kv.k_scale + here.hk) : 1.f;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        row_scale[r] = p.scale * kLog2e * ks;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+      if constexpr (!E4M3) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) ldsm4(qa[j], qb + swizzled<D * 2>(lane & 15, 2 * j + (lane >> 4)));
+      } else {
+        // A thread's four bytes of a K row are four consecutive dimensions;
+        // they serve as the products' k = 2 quad, + 1, + 8, + 9, and the query
+        // is laid out alike.  It is held in fp16, which its bf16 values fit once
+        // each row is scaled by a power of two that brings its largest element
+        // to [2^14, 2^15): exact but for elements 2^-28 below the largest.
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (r < NR) {
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              const uint32_t a = qb + swizzled<D * 2>(g + 8 * r, 2 * j + (quad >> 1)) + (quad & 1) * 8;
+              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(qa[j][r]), "=r"(qa[j][2 + r]) : "r"(a) : "memory");
+              top = fmaxf(top, fmaxf(fmaxf(fabsf(bf_lo(qa[j][r])), fabsf(bf_hi(qa[j][r]))),
+                                     fmaxf(fabsf(bf_lo(qa[j][2 + r])), fabsf(bf_hi(qa[j][2 + r])))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = static_cast<int>(__float_as_uint(top) >> 23);
+            const int up = e == 255 ? 127 : min(268 - max(e, 1), 253);   // biased exponent of the factor
+            const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+            row_scale[r < NR ? r : 0] *= __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              qa[j][r] = pack_f16x2(bf_lo(qa[j][r]) * f, bf_hi(qa[j][r]) * f);
+              qa[j][2 + r] = pack_f16x2(bf_lo(qa[j][2 + r]) * f, bf_hi(qa[j][2 + r]) * f);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) qa[j][r] = qa[j][2 + r] = 0u;
+          }
+        }
+      }
+    }
+
+    const uint32_t kt = sbase + stage * S::kStageBytes, vt = kt + S::kTileBytes;
+#pragma unroll
+    for (int kgi = 0; kgi < TILE / 16 / kWarps; ++kgi) {
+      const int kg = kgi * kWarps + warp;
+      // S = Q K^T for 16 keys
+      float x[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+      const int kr = kg * 16 + (lane & 7) + ((lane >> 4) << 3);
+      if constexpr (!E4M3) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t b[4];
+          ldsm4(b, kt + swizzled<RB>(kr, 2 * j + ((lane >> 3) & 1)));
+          mma<false>(x[0], qa[j], b[0], b[1]);
+          mma<false>(x[1], qa[j], b[2], b[3]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2) {
+          uint32_t b[4];
+          ldsm4(b, kt + swizzled<RB>(kr, j + ((lane >> 3) & 1)));
+          mma<true>(x[0], qa[j], e4m3_lo(b[0]), e4m3_hi(b[0]));
+          mma<true>(x[1], qa[j], e4m3_lo(b[2]), e4m3_hi(b[2]));
+          mma<true>(x[0], qa[j + 1], e4m3_lo(b[1]), e4m3_hi(b[1]));
+          mma<true>(x[1], qa[j + 1], e4m3_lo(b[3]), e4m3_hi(b[3]));
+        }
+      }
+      // scores in units of log 2, unseen keys at -inf
+      const uint32_t bits = seen[ring * (TILE / 32) + (kg >> 1)] >> ((kg & 1) * 16);
+      const bool all = (bits & 0xffffu) == 0xffffu;
+      float top[NR];
+      bool rise = false;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float& v = x[i][2 * r + c];
+            v *= row_scale[r];
+            if (!all && !((bits >> (i * 8 + 2 * quad + c)) & 1u)) v = -INFINITY;
+          }
+        top[r] = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+        rise |= top[r] > m[r];
+      }
+      if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float up = fmaxf(m[r], top[r]);
+          const float keep = up == m[r] ? 1.f : ex2_approx(m[r] - up);
+          m[r] = up;
+          l[r] *= keep;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][2 * r] *= keep;
+            o[i][2 * r + 1] *= keep;
+          }
+        }
+      }
+      // P: rounded to 16 bits for the second product, summed in 32.  In fp16
+      // (e4m3 caches) the weights carry a factor 2^8 so that none above 2^-22
+      // of the largest is subnormal.
+      uint32_t pa[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float ref = (m[r] == -INFINITY ? 0.f : m[r]) - (E4M3 ? 8.f : 0.f);
+        float e[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) e[i][c] = ex2_approx(x[i][2 * r + c] - ref);
+        l[r] += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          pa[2 * i + r] = E4M3 ? pack_f16x2(e[i][0], e[i][1]) : pack_bf16x2(e[i][0], e[i][1]);
+      }
+      // O += P V
+      const int vr = kg * 16 + (lane & 15);
+      if constexpr (!E4M3) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t b[4];
+          ldsm4t(b, vt + swizzled<RB>(vr, 2 * j + (lane >> 4)));
+          mma<false>(o[2 * j], pa, b[0], b[1]);
+          mma<false>(o[2 * j + 1], pa, b[2], b[3]);
+        }
+      } else {
+        // Transposed as 16-bit units, a register holds two keys' bytes of two
+        // neighbouring dimensions: even and odd dimensions become the two
+        // products' columns.
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2) {
+          uint32_t b[4];
+          ldsm4t(b, vt + swizzled<RB>(vr, j + (lane >> 4)));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t even = __byte_perm(b[2 * i], b[2 * i + 1], 0x6420);
+            const uint32_t odd = __byte_perm(b[2 * i], b[2 * i + 1], 0x7531);
+            mma<true>(o[2 * (j + i)], pa, e4m3_lo(even), e4m3_hi(even));
+            mma<true>(o[2 * (j + i) + 1], pa, e4m3_lo(odd), e4m3_hi(odd));
+          }
+        }
+      }
+    }
+
+    const bool unit_done = here.t + 1 == here.nt;
+    if (unit_done || s + 1 == n) {
+      // Join the warps' states in the stage just consumed.
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (quad == 0) {
+          join_m[warp * kRows + g + 8 * r] = m[r];
+          join_l[warp * kRows + g + 8 * r] = l[r];
+        }
+      }
+      __syncthreads();   // every warp has read the stage
+      float* const buf = reinterpret_cast<float*>(smem + stage * S::kStageBytes);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const int row = g + 8 * r;
+        float* const to = buf + (warp * kRows + row) * D;   // groups of 8 columns, swizzled by row
+        if (row < rows) {
+          if constexpr (!E4M3) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+              *reinterpret_cast<float2*>(to + ((i ^ g) * 8 + 2 * quad)) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+              *reinterpret_cast<float4*>(to + (((2 * j + (quad >> 1)) ^ g) * 8 + 4 * (quad & 1))) =
+                  make_float4(o[2 * j][2 * r], o[2 * j + 1][2 * r], o[2 * j][2 * r + 1], o[2 * j + 1][2 * r + 1]);
+          }
+        }
+      }
+      __syncthreads();
+      const bool starts_here = here.t <= s;   // the unit's first tile is in this run
+      const bool whole = unit_done && starts_here;
+      const int slot = first_piece ? 0 : 1;
+      float* const part = work.parts + (static_cast<size_t>(block) * 2 + slot) * part_floats(lc.rows, D);
+      for (int i = tid; i < rows * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), c4 = i % (D / 4);
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, join_m[w * kRows + row]);
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float lw = join_l[w * kRows + row];
+          const float f = lw == 0.f ? 0.f : ex2_approx(join_m[w * kRows + row] - top);
+          const float4 v = *reinterpret_cast<const float4*>(
+              buf + (w * kRows + row) * D + (((c4 >> 1) ^ (row & 7)) * 8 + (c4 & 1) * 4));
+          sum = fmaf(f, lw, sum);
+          acc.x = fmaf(f, v.x, acc.x);
+          acc.y = fmaf(f, v.y, acc.y);
+          acc.z = fmaf(f, v.z, acc.z);
+          acc.w = fmaf(f, v.w, acc.w);
+        }
+        if (whole) {
+          const float vs = p.kv.v_scale ? __ldg(p.kv.v_scale + here.hk) : 1.f;
+          const float inv = sum == 0.f ? 0.f : vs / sum;
+          const long long at = static_cast<long long>(here.b) * p.heads + here.hk * G + row0 + row;
+          uint2 out;
+          out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+          out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+          *reinterpret_cast<uint2*>(p.o + at * D + c4 * 4) = out;
+          if (p.lse && c4 == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top - (E4M3 ? 8.f : 0.f) + __log2f(sum)) * kLn2;
+        } else {
+          *reinterpret_cast<float2*>(part + row * D + c4 * 4) = make_float2(acc.x, acc.y);
+          *reinterpret_cast<float2*>(part + row * D + c4 * 4 + 2) = make_float2(acc.z, acc.w);
+          if (c4 == 0) {
+            part[lc.rows * D + row] = top;
+            part[lc.rows * D + lc.rows + row] = sum;
+          }
+        }
+      }
+      if (s + 1 == n && tid == 0) {
+        Cut cut;
+        cut.unit = !unit_done && starts_here ? here.b * p.kv.heads_kv + here.hk : -1;
+        cut.last = run_of(start + s - here.t + here.nt - 1, total, runs);
+        cut.slot = slot;
+        cut.pad = 0;
+        work.cuts[block] = cut;
+      }
+      fresh = true;
+      first_piece = false;
+      q_slot = q_slot + 1 == ST ? 0 : q_slot + 1;
+    }
+    here.next(L, p.batch, p.kv.heads_kv);
+    stage = stage + 1 == ST ? 0 : stage + 1;
+    ring = ring + 1 == S::kOffsets ? 0 : ring + 1;
+  }
 }
 
+// ------------------------------------------------------------------ combine
+// One block per (cut unit, query head): joins the partial results of the
+// runs the unit lies in, in the order of the runs.
 template <int D>
-cudaError_t launch_d(const DecodeParams& p, cudaStream_t s) {
-  const int grid = p.batch * p.heads;
-  if (p.kv.e4m3) decode_kernel<D, true><<<grid, kWarps * 32, 0, s>>>(p);
-  else decode_kernel<D, false><<<grid, kWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+__global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeParams p, const Launch lc, const Work work) {
+  constexpr int COLS = D / 4, GROUPS = kThreads / COLS;
+  __shared__ float weight[kMaxBlocks];
+  __shared__ float s_top[kWarps], s_sum[kWarps];
+  __shared__ float4 s_acc[kThreads];
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int chunk = blockIdx.y / lc.rows, row = blockIdx.y % lc.rows;
+  const int G = p.heads / p.kv.heads_kv;
+  if (chunk * lc.rows + row >= G) return;
+  const int c0 = blockIdx.x;
+  const Cut cut = work.cuts[chunk * lc.blocks + c0];
+  if (cut.unit < 0) return;
+  const int n = cut.last - c0 + 1;
+  const size_t pf = part_floats(lc.rows, D);
+  auto part = [&](int i) {
+    return work.parts + (static_cast<size_t>(chunk * lc.blocks + c0 + i) * 2 + (i == 0 ? cut.slot : 0)) * pf;
+  };
+  float top = -INFINITY;
+  for (int i = tid; i < n; i += kThreads) top = fmaxf(top, part(i)[lc.rows * D + row]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+  float sum = 0.f;
+  for (int i = tid; i < n; i += kThreads) {
+    const float li = part(i)[lc.rows * D + lc.rows + row];
+    const float f = li == 0.f ? 0.f : ex2_approx(part(i)[lc.rows * D + row] - top);
+    weight[i] = f;
+    sum = fmaf(f, li, sum);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+  const int col = tid % COLS, group = tid / COLS;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = group; i < n; i += GROUPS) {
+    const float2* const from = reinterpret_cast<const float2*>(part(i) + row * D + col * 4);
+    const float2 a = from[0], b = from[1];
+    const float f = weight[i];
+    acc.x = fmaf(f, a.x, acc.x);
+    acc.y = fmaf(f, a.y, acc.y);
+    acc.z = fmaf(f, b.x, acc.z);
+    acc.w = fmaf(f, b.y, acc.w);
+  }
+  s_acc[tid] = acc;
+  __syncthreads();
+  if (tid >= COLS) return;
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) {
+    const float4 a = s_acc[i * COLS + tid];
+    acc.x += a.x;
+    acc.y += a.y;
+    acc.z += a.z;
+    acc.w += a.w;
+  }
+  const int b = cut.unit / p.kv.heads_kv, hk = cut.unit % p.kv.heads_kv;
+  const float inv = sum == 0.f ? 0.f : (p.kv.v_scale ? __ldg(p.kv.v_scale + hk) : 1.f) / sum;
+  const long long at = static_cast<long long>(b) * p.heads + hk * G + chunk * lc.rows + row;
+  uint2 out;
+  out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.o + at * D + tid * 4) = out;
+  if (p.lse && tid == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top - (p.kv.e4m3 ? 8.f : 0.f) + __log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------------ launch
+Launch split_heads(int heads, int heads_kv) {
+  const int G = heads / heads_kv;
+  Launch lc;
+  lc.chunks = (G + kRows - 1) / kRows;
+  lc.rows = (G + lc.chunks - 1) / lc.chunks;
+  lc.chunks = (G + lc.rows - 1) / lc.rows;
+  lc.blocks = 0;
+  return lc;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    n = 152;
+  return n;
+}
+
+template <int D, bool E4M3, bool HALF>
+cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
+  using Sh = Shape<D, E4M3>;
+  static std::atomic<unsigned long long> smem_done{0};
+  auto* const kernel = decode_kernel<D, E4M3, HALF>;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), Sh::kSmem, smem_done);
+  if (e != cudaSuccess) return e;
+  // At most one block per tile, at most the blocks that are resident at once.
+  int longest = p.max_pages * p.kv.page_size;
+  if (p.window > 0 && p.window < longest) longest = p.window;
+  const long long unit_tiles = longest > Sh::kTile ? (longest + static_cast<long long>(Sh::kTile) - 1) / Sh::kTile : 1;
+  const long long tiles = unit_tiles * p.batch * p.kv.heads_kv;
+  long long blocks = Sh::kBlocksPerSm * sm_count();
+  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
+  blocks = blocks / lc.chunks > 1 ? blocks / lc.chunks : 1;
+  lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
+  Work work;
+  const size_t all = static_cast<size_t>(lc.blocks) * lc.chunks;
+  work.cuts = reinterpret_cast<Cut*>(p.work);
+  work.parts = reinterpret_cast<float*>(work.cuts + all);
+  kernel<<<dim3(lc.blocks, lc.chunks), kThreads, Sh::kSmem, s>>>(p, lc, work);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(lc.blocks, lc.chunks * lc.rows);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p, lc, work);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_rows(const DecodeParams& p, cudaStream_t s) {
+  const Launch lc = split_heads(p.heads, p.kv.heads_kv);
+  return lc.rows <= 8 ? launch_shape<D, E4M3, true>(p, lc, s) : launch_shape<D, E4M3, false>(p, lc, s);
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes(int, int, int, int) { return 0; }
+size_t decode_workspace_bytes(int batch, int heads, int heads_kv, int head_dim) {
+  if (batch == 0) return 0;
+  const Launch lc = split_heads(heads, heads_kv);
+  const size_t blocks = lc.chunks > kMaxBlocks ? lc.chunks : kMaxBlocks;
+  const size_t bytes = blocks * (sizeof(Cut) + 2 * part_floats(lc.rows, head_dim) * sizeof(float));
+  return (bytes + 255) / 256 * 256;
+}
 
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t s) {
-  if (p.kv.head_dim == 64) return launch_d<64>(p, s);
-  if (p.kv.head_dim == 128) return launch_d<128>(p, s);
-  return launch_d<256>(p, s);
+  switch (p.kv.head_dim) {
+    case 64: return p.kv.e4m3 ? launch_rows<64, true>(p, s) : launch_rows<64, false>(p, s);
+    case 128: return p.kv.e4m3 ? launch_rows<128, true>(p, s) : launch_rows<128, false>(p, s);
+    default: return p.kv.e4m3 ? launch_rows<256, true>(p, s) : launch_rows<256, false>(p, s);
+  }
 }
 
 }  // namespace fa
