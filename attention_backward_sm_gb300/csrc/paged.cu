@@ -401,6 +401,8 @@ int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
   if (heads < 1 || heads % heads_kv != 0)
     return set_last_error(FA_ERR_INVALID_ARG, "query heads (%d) must be a positive multiple of key/value heads (%d)",
                           heads, heads_kv);
+  if (static_cast<long long>(heads) * head_dim > 65535 * 64)
+    return set_last_error(FA_ERR_UNSUPPORTED, "heads * head_dim too large (%d * %d)", heads, head_dim);
   if (window < 0) return set_last_error(FA_ERR_INVALID_ARG, "window must be >= 0, got %d", window);
   if (!isfinite(scale)) return set_last_error(FA_ERR_INVALID_ARG, "scale must be finite");
   if (max_pages < 0) return set_last_error(FA_ERR_INVALID_ARG, "max_pages must be >= 0, got %d", max_pages);
@@ -415,6 +417,12 @@ int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
   if (misaligned16(q) || misaligned16(o)) return set_last_error(FA_ERR_INVALID_ARG, "q and o must be 16-byte aligned");
   if (misaligned4(block_table) || misaligned4(seq_lens) || misaligned4(lse))
     return set_last_error(FA_ERR_INVALID_ARG, "block_table, seq_lens and lse must be 4-byte aligned");
+  // Blocks that share a row write o while others still read q.
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+  const uintptr_t row = 2ull * heads * head_dim;
+  const uintptr_t q_bytes = (batch - 1) * 2ull * (batch > 1 ? q_row_stride : 0) + row;
+  if (q0 < o0 + batch * row && o0 < q0 + q_bytes)
+    return set_last_error(FA_ERR_INVALID_ARG, "o must not overlap q");
   const size_t need = fa::decode_workspace_bytes(batch, heads, heads_kv, head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return set_last_error(FA_ERR_INVALID_ARG, "workspace of %zu bytes needed, got %zu", need, workspace_bytes);

@@ -354,7 +354,7 @@ size_t fa_decode_workspace_size(int batch, int heads, int heads_kv, int head_dim
  * count in seq_lens.  Lengths are clamped to max_pages * page_size.  Query
  * head h reads key/value head h / (H / Hkv).  A row that sees no key gets
  * o = 0, lse = -inf.  Contents of slots that are not seen do not matter
- * (NaN included).  workspace: fa_decode_workspace_size() bytes, 16-byte
+ * (NaN included).  o must not overlap q.  workspace: fa_decode_workspace_size() bytes, 16-byte
  * aligned, contents arbitrary; calls whose work overlaps on the GPU need one
  * each.  Results do not depend on timing: the same call gives the same bits. */
 int fa_decode(const fa_bf16* q, long long q_row_stride,

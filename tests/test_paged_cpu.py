@@ -130,7 +130,7 @@ def test_append_of_nothing_succeeds(lib):
 def _decode_rc(lib, **kw):
     a = dict(q=P, qs=512, kc=P, vc=P, kind=0, k_scale=None, v_scale=None, page_stride=4096, slot_stride=256,
              head_stride=128, pages=8, page=16, table=P, table_stride=4, width=4, seq=P, batch=2, heads=4, heads_kv=2,
-             dim=128, window=0, scale=0.1, o=P, lse=P, ws=P, ws_bytes=1 << 40)
+             dim=128, window=0, scale=0.1, o=ctypes.c_void_p(1 << 20), lse=P, ws=P, ws_bytes=1 << 40)
     a.update(kw)
     return lib.fa_decode(*a.values(), None)
 
@@ -143,6 +143,8 @@ def _decode_rc(lib, **kw):
     (dict(qs=256), 1, b"q_row_stride"), (dict(qs=516), 1, b"q_row_stride"), (dict(q=None), 1, b"NULL"),
     (dict(seq=None), 1, b"NULL"), (dict(table=None), 1, b"NULL"), (dict(kc=None), 1, b"NULL"),
     (dict(o=ctypes.c_void_p(8)), 1, b"aligned"), (dict(seq=ctypes.c_void_p(18)), 1, b"aligned"),
+    (dict(o=P), 1, b"overlap"), (dict(o=ctypes.c_void_p(16 + 1024)), 1, b"overlap"),
+    (dict(heads=1 << 20, qs=1 << 27), 2, b"too large"),
     (dict(kind=0, v_scale=P), 1, b"e4m3"), (dict(slot_stride=100), 1, b"slot_stride")])
 def test_decode_refusals(lib, kw, code, word):
     assert _decode_rc(lib, **kw) == code
