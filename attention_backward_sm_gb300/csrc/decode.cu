@@ -35,8 +35,7 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 4;         // warps over the keys of a tile
 constexpr int kRows = 16;         // query heads per block (rows of the tensor-core products)
 constexpr int kMaxBlocks = 608;   // upper bound of a launch's blocks: 4 on each of 152 SMs
 constexpr float kLog2e = 1.4426950408889634f;
@@ -44,11 +43,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D, bool E4M3>
 struct Shape {
+  // Warps side by side over the same keys, each with a part of O's columns
+  // (the scores are computed by each): at head_dim 256 one block fills an SM's
+  // shared memory, and 4 warps would hold 192 registers of O and Q each.
+  static constexpr int kSplit = D == 256 ? 2 : 1;
+  static constexpr int kThreads = kWarps * kSplit * 32;
   static constexpr int kElem = E4M3 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
   // Keys per tile: K and V tiles together are at least the 4 * 16 * D floats
   // that joining the warps takes (it reuses the stage just consumed).
   static constexpr int kTile = E4M3 || D == 64 ? 128 : 64;
+  static constexpr int kKeys = kTile / kWarps;                // of a warp
   static constexpr int kTileBytes = kTile * kRowBytes;       // of K, and of V
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kStages = 3;
@@ -61,8 +66,10 @@ struct Shape {
   static constexpr int kOffSeen = kOffOffsets + kOffsets * kTile * 8;
   static constexpr int kOffJoin = kOffSeen + kOffsets * (kTile / 32) * 4;
   static constexpr int kOffScan = kOffJoin + 2 * kWarps * kRows * 4;
-  static constexpr int kSmem = kOffScan + 64;
+  static constexpr int kSmem = kOffScan + kThreads / 32 * 8 + 16;
   static_assert(kStageBytes >= kWarps * kRows * D * 4, "join buffer");
+  static_assert(kKeys == 16 || kKeys == 32, "a word of seen keys");
+  static_assert(kTile <= kThreads, "a thread per key looks up its page");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -198,10 +205,12 @@ struct Place {
 
 // ------------------------------------------------------------------ main kernel
 template <int D, bool E4M3, bool HALF>   // HALF: at most 8 rows
-__global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
+__global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlocksPerSm)
     decode_kernel(const DecodeParams p, const Launch lc, const Work work) {
   using S = Shape<D, E4M3>;
-  constexpr int TILE = S::kTile, RB = S::kRowBytes, ST = S::kStages;
+  constexpr int TILE = S::kTile, RB = S::kRowBytes, ST = S::kStages, kThreads = S::kThreads;
+  constexpr int NT = S::kKeys / 8;   // a warp's score columns, in groups of 8 keys
+  constexpr int DO = D / S::kSplit;  // columns of O of a warp
   constexpr int NR = HALF ? 1 : 2;   // groups of 8 rows with data
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -209,10 +218,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
   uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + S::kOffSeen);
   float* const join_m = reinterpret_cast<float*>(smem + S::kOffJoin);
   float* const join_l = join_m + kWarps * kRows;
-  long long* const scan = reinterpret_cast<long long*>(smem + S::kOffScan);   // [kWarps]
-  int* const found = reinterpret_cast<int*>(scan + kWarps);                   // b, hk, t
+  long long* const scan = reinterpret_cast<long long*>(smem + S::kOffScan);   // [warps]
+  int* const found = reinterpret_cast<int*>(scan + kThreads / 32);            // b, hk, t
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kwarp = warp % kWarps, c0 = warp / kWarps * DO;   // its part of a tile's keys, its first column of O
   const int G = p.heads / p.kv.heads_kv;
   const int row0 = blockIdx.y * lc.rows;                 // first query head of this chunk within its group
   const int rows = min(lc.rows, G - row0);
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) upto += scan[w];
     total += scan[w];
   }
@@ -339,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
   int page_ahead = ST - 1 < n ? look_up(ahead) : -1;
 
   uint32_t qa[D / 16][4];                   // query fragments (e4m3: fp16, rescaled per row)
-  float o[D / 8][4];
+  float o[DO / 8][4];
   float m[NR], l[NR], row_scale[NR];
   int stage = 0, ring = 0, q_slot = 0;
   int load_stage = ST - 1, load_ring = ST - 1;
@@ -373,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
         row_scale[r] = p.scale * kLog2e * ks;
       }
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int i = 0; i < DO / 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
       if constexpr (!E4M3) {
@@ -416,113 +426,123 @@ __global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
     }
 
     const uint32_t kt = sbase + stage * S::kStageBytes, vt = kt + S::kTileBytes;
+    // S = Q K^T for the warp's keys
+    const int key0 = kwarp * S::kKeys;
+    float x[NT][4];
 #pragma unroll
-    for (int kgi = 0; kgi < TILE / 16 / kWarps; ++kgi) {
-      const int kg = kgi * kWarps + warp;
-      // S = Q K^T for 16 keys
-      float x[2][4];
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+    const int kr = key0 + (lane & 7) + ((lane >> 4) << 3);
+    if constexpr (!E4M3) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
-      const int kr = kg * 16 + (lane & 7) + ((lane >> 4) << 3);
-      if constexpr (!E4M3) {
+      for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
+        for (int i = 0; i < NT; i += 2) {
           uint32_t b[4];
-          ldsm4(b, kt + swizzled<RB>(kr, 2 * j + ((lane >> 3) & 1)));
-          mma<false>(x[0], qa[j], b[0], b[1]);
-          mma<false>(x[1], qa[j], b[2], b[3]);
+          ldsm4(b, kt + swizzled<RB>(kr + 8 * i, 2 * j + ((lane >> 3) & 1)));
+          mma<false>(x[i], qa[j], b[0], b[1]);
+          mma<false>(x[i + 1], qa[j], b[2], b[3]);
         }
-      } else {
+    } else {
 #pragma unroll
-        for (int j = 0; j < D / 16; j += 2) {
+      for (int j = 0; j < D / 16; j += 2)
+#pragma unroll
+        for (int i = 0; i < NT; i += 2) {
           uint32_t b[4];
-          ldsm4(b, kt + swizzled<RB>(kr, j + ((lane >> 3) & 1)));
-          mma<true>(x[0], qa[j], e4m3_lo(b[0]), e4m3_hi(b[0]));
-          mma<true>(x[1], qa[j], e4m3_lo(b[2]), e4m3_hi(b[2]));
-          mma<true>(x[0], qa[j + 1], e4m3_lo(b[1]), e4m3_hi(b[1]));
-          mma<true>(x[1], qa[j + 1], e4m3_lo(b[3]), e4m3_hi(b[3]));
+          ldsm4(b, kt + swizzled<RB>(kr + 8 * i, j + ((lane >> 3) & 1)));
+          mma<true>(x[i], qa[j], e4m3_lo(b[0]), e4m3_hi(b[0]));
+          mma<true>(x[i + 1], qa[j], e4m3_lo(b[2]), e4m3_hi(b[2]));
+          mma<true>(x[i], qa[j + 1], e4m3_lo(b[1]), e4m3_hi(b[1]));
+          mma<true>(x[i + 1], qa[j + 1], e4m3_lo(b[3]), e4m3_hi(b[3]));
         }
-      }
-      // scores in units of log 2, unseen keys at -inf
-      const uint32_t bits = seen[ring * (TILE / 32) + (kg >> 1)] >> ((kg & 1) * 16);
-      const bool all = (bits & 0xffffu) == 0xffffu;
-      float top[NR];
-      bool rise = false;
+    }
+    // scores in units of log 2, unseen keys at -inf
+    uint32_t bits = seen[ring * (TILE / 32) + (key0 >> 5)] >> (key0 & 31);
+    if constexpr (S::kKeys == 16) bits |= 0xffff0000u;
+    float top[NR];
+    bool rise = false;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      top[r] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float& v = x[i][2 * r + c];
+          v *= row_scale[r];
+          if (bits != 0xffffffffu && !((bits >> (i * 8 + 2 * quad + c)) & 1u)) v = -INFINITY;
+          top[r] = fmaxf(top[r], v);
+        }
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+      rise |= top[r] > m[r];
+    }
+    if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
+        const float up = fmaxf(m[r], top[r]);
+        const float keep = up == m[r] ? 1.f : ex2_approx(m[r] - up);
+        m[r] = up;
+        l[r] *= keep;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float& v = x[i][2 * r + c];
-            v *= row_scale[r];
-            if (!all && !((bits >> (i * 8 + 2 * quad + c)) & 1u)) v = -INFINITY;
-          }
-        top[r] = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-        rise |= top[r] > m[r];
-      }
-      if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float up = fmaxf(m[r], top[r]);
-          const float keep = up == m[r] ? 1.f : ex2_approx(m[r] - up);
-          m[r] = up;
-          l[r] *= keep;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][2 * r] *= keep;
-            o[i][2 * r + 1] *= keep;
-          }
+        for (int i = 0; i < DO / 8; ++i) {
+          o[i][2 * r] *= keep;
+          o[i][2 * r + 1] *= keep;
         }
       }
-      // P: rounded to 16 bits for the second product, summed in 32.  In fp16
-      // (e4m3 caches) the weights carry a factor 2^8 so that none above 2^-22
-      // of the largest is subnormal.
-      uint32_t pa[4] = {0u, 0u, 0u, 0u};
+    }
+    // P: rounded to 16 bits for the second product, summed in 32.  In fp16
+    // (e4m3 caches) the weights carry a factor 2^8 so that none above 2^-22
+    // of the largest is subnormal.
+    uint32_t pa[NT / 2][4];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
+    for (int r = 0; r < 2; ++r) {
+      if (r < NR) {
         const float ref = (m[r] == -INFINITY ? 0.f : m[r]) - (E4M3 ? 8.f : 0.f);
-        float e[2][2];
+        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) e[i][c] = ex2_approx(x[i][2 * r + c] - ref);
-        l[r] += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          pa[2 * i + r] = E4M3 ? pack_f16x2(e[i][0], e[i][1]) : pack_bf16x2(e[i][0], e[i][1]);
-      }
-      // O += P V
-      const int vr = kg * 16 + (lane & 15);
-      if constexpr (!E4M3) {
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          uint32_t b[4];
-          ldsm4t(b, vt + swizzled<RB>(vr, 2 * j + (lane >> 4)));
-          mma<false>(o[2 * j], pa, b[0], b[1]);
-          mma<false>(o[2 * j + 1], pa, b[2], b[3]);
+        for (int i = 0; i < NT; ++i) {
+          const float e0 = ex2_approx(x[i][2 * r] - ref), e1 = ex2_approx(x[i][2 * r + 1] - ref);
+          sum += e0 + e1;
+          pa[i / 2][2 * (i & 1) + r] = E4M3 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
         }
+        l[r < NR ? r : 0] += sum;
       } else {
-        // Transposed as 16-bit units, a register holds two keys' bytes of two
-        // neighbouring dimensions: even and odd dimensions become the two
-        // products' columns.
 #pragma unroll
-        for (int j = 0; j < D / 16; j += 2) {
+        for (int i = 0; i < NT; ++i) pa[i / 2][2 * (i & 1) + r] = 0u;
+      }
+    }
+    // O += P V
+    const int vr = key0 + (lane & 15);
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int i = 0; i < NT / 2; ++i)
+#pragma unroll
+        for (int j = 0; j < DO / 16; ++j) {
           uint32_t b[4];
-          ldsm4t(b, vt + swizzled<RB>(vr, j + (lane >> 4)));
+          ldsm4t(b, vt + swizzled<RB>(vr + 16 * i, c0 / 8 + 2 * j + (lane >> 4)));
+          mma<false>(o[2 * j], pa[i], b[0], b[1]);
+          mma<false>(o[2 * j + 1], pa[i], b[2], b[3]);
+        }
+    } else {
+      // Transposed as 16-bit units, a register holds two keys' bytes of two
+      // neighbouring dimensions: even and odd dimensions become the two
+      // products' columns.
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t even = __byte_perm(b[2 * i], b[2 * i + 1], 0x6420);
-            const uint32_t odd = __byte_perm(b[2 * i], b[2 * i + 1], 0x7531);
-            mma<true>(o[2 * (j + i)], pa, e4m3_lo(even), e4m3_hi(even));
-            mma<true>(o[2 * (j + i) + 1], pa, e4m3_lo(odd), e4m3_hi(odd));
+      for (int i = 0; i < NT / 2; ++i)
+#pragma unroll
+        for (int j = 0; j < DO / 16; j += 2) {
+          uint32_t b[4];
+          ldsm4t(b, vt + swizzled<RB>(vr + 16 * i, c0 / 16 + j + (lane >> 4)));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t even = __byte_perm(b[2 * u], b[2 * u + 1], 0x6420);
+            const uint32_t odd = __byte_perm(b[2 * u], b[2 * u + 1], 0x7531);
+            mma<true>(o[2 * (j + u)], pa[i], e4m3_lo(even), e4m3_hi(even));
+            mma<true>(o[2 * (j + u) + 1], pa[i], e4m3_lo(odd), e4m3_hi(odd));
           }
         }
-      }
     }
 
     const bool unit_done = here.t + 1 == here.nt;
@@ -533,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         if (quad == 0) {
-          join_m[warp * kRows + g + 8 * r] = m[r];
-          join_l[warp * kRows + g + 8 * r] = l[r];
+          join_m[kwarp * kRows + g + 8 * r] = m[r];
+          join_l[kwarp * kRows + g + 8 * r] = l[r];
         }
       }
       __syncthreads();   // every warp has read the stage
@@ -542,15 +562,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const int row = g + 8 * r;
-        float* const to = buf + (warp * kRows + row) * D;   // groups of 8 columns, swizzled by row
+        float* const to = buf + (kwarp * kRows + row) * D + c0;   // groups of 8 columns, swizzled by row
         if (row < rows) {
           if constexpr (!E4M3) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
+            for (int i = 0; i < DO / 8; ++i)
               *reinterpret_cast<float2*>(to + ((i ^ g) * 8 + 2 * quad)) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
           } else {
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j)
+            for (int j = 0; j < DO / 16; ++j)
               *reinterpret_cast<float4*>(to + (((2 * j + (quad >> 1)) ^ g) * 8 + 4 * (quad & 1))) =
                   make_float4(o[2 * j][2 * r], o[2 * j + 1][2 * r], o[2 * j][2 * r + 1], o[2 * j + 1][2 * r + 1]);
           }
@@ -618,15 +638,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, E4M3>::kBlocksPerSm)
 
 // ------------------------------------------------------------------ combine
 // One block per (cut unit, query head): joins the partial results of the
-// runs the unit lies in, in the order of the runs.
+// runs the unit lies in, group g of its threads those of runs g, g + GROUPS,
+// ... in one pass with a running maximum, then the groups in order.
+constexpr int kJoinThreads = 128;
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeParams p, const Launch lc, const Work work) {
-  constexpr int COLS = D / 4, GROUPS = kThreads / COLS;
-  __shared__ float weight[kMaxBlocks];
-  __shared__ float s_top[kWarps], s_sum[kWarps];
-  __shared__ float4 s_acc[kThreads];
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParams p, const Launch lc,
+                                                               const Work work) {
+  constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
+  __shared__ float s_top[GROUPS], s_sum[GROUPS];
+  __shared__ float4 s_acc[kJoinThreads];
   pdl_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int chunk = blockIdx.y / lc.rows, row = blockIdx.y % lc.rows;
   const int G = p.heads / p.kv.heads_kv;
   if (chunk * lc.rows + row >= G) return;
@@ -635,50 +658,46 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const DecodeParams p,
   if (cut.unit < 0) return;
   const int n = cut.last - c0 + 1;
   const size_t pf = part_floats(lc.rows, D);
-  auto part = [&](int i) {
-    return work.parts + (static_cast<size_t>(chunk * lc.blocks + c0 + i) * 2 + (i == 0 ? cut.slot : 0)) * pf;
-  };
-  float top = -INFINITY;
-  for (int i = tid; i < n; i += kThreads) top = fmaxf(top, part(i)[lc.rows * D + row]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
-  float sum = 0.f;
-  for (int i = tid; i < n; i += kThreads) {
-    const float li = part(i)[lc.rows * D + lc.rows + row];
-    const float f = li == 0.f ? 0.f : ex2_approx(part(i)[lc.rows * D + row] - top);
-    weight[i] = f;
-    sum = fmaf(f, li, sum);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
   const int col = tid % COLS, group = tid / COLS;
+  float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = group; i < n; i += GROUPS) {
-    const float2* const from = reinterpret_cast<const float2*>(part(i) + row * D + col * 4);
+    const float* const part =
+        work.parts + (static_cast<size_t>(chunk * lc.blocks + c0 + i) * 2 + (i == 0 ? cut.slot : 0)) * pf;
+    const float2* const from = reinterpret_cast<const float2*>(part + row * D + col * 4);
     const float2 a = from[0], b = from[1];
-    const float f = weight[i];
-    acc.x = fmaf(f, a.x, acc.x);
-    acc.y = fmaf(f, a.y, acc.y);
-    acc.z = fmaf(f, b.x, acc.z);
-    acc.w = fmaf(f, b.y, acc.w);
+    const float mi = part[lc.rows * D + row], li = part[lc.rows * D + lc.rows + row];
+    const float up = fmaxf(top, mi);
+    const float keep = up == top ? 1.f : ex2_approx(top - up);
+    const float f = li == 0.f ? 0.f : ex2_approx(mi - up);
+    top = up;
+    sum = fmaf(sum, keep, f * li);
+    acc.x = fmaf(acc.x, keep, f * a.x);
+    acc.y = fmaf(acc.y, keep, f * a.y);
+    acc.z = fmaf(acc.z, keep, f * b.x);
+    acc.w = fmaf(acc.w, keep, f * b.y);
   }
   s_acc[tid] = acc;
+  if (col == 0) {
+    s_top[group] = top;
+    s_sum[group] = sum;
+  }
   __syncthreads();
   if (tid >= COLS) return;
 #pragma unroll
-  for (int i = 1; i < GROUPS; ++i) {
+  for (int i = 1; i < GROUPS; ++i) top = fmaxf(top, s_top[i]);
+  sum = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < GROUPS; ++i) {
+    const float f = s_sum[i] == 0.f ? 0.f : ex2_approx(s_top[i] - top);
     const float4 a = s_acc[i * COLS + tid];
-    acc.x += a.x;
-    acc.y += a.y;
-    acc.z += a.z;
-    acc.w += a.w;
+    sum = fmaf(f, s_sum[i], sum);
+    acc.x = fmaf(f, a.x, acc.x);
+    acc.y = fmaf(f, a.y, acc.y);
+    acc.z = fmaf(f, a.z, acc.z);
+    acc.w = fmaf(f, a.w, acc.w);
   }
   const int b = cut.unit / p.kv.heads_kv, hk = cut.unit % p.kv.heads_kv;
   const float inv = sum == 0.f ? 0.f : (p.kv.v_scale ? __ldg(p.kv.v_scale + hk) : 1.f) / sum;
@@ -729,12 +748,12 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   const size_t all = static_cast<size_t>(lc.blocks) * lc.chunks;
   work.cuts = reinterpret_cast<Cut*>(p.work);
   work.parts = reinterpret_cast<float*>(work.cuts + all);
-  kernel<<<dim3(lc.blocks, lc.chunks), kThreads, Sh::kSmem, s>>>(p, lc, work);
+  kernel<<<dim3(lc.blocks, lc.chunks), Sh::kThreads, Sh::kSmem, s>>>(p, lc, work);
   e = cudaGetLastError();
   if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(lc.blocks, lc.chunks * lc.rows);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
