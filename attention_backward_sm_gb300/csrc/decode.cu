@@ -41,7 +41,7 @@ constexpr int kMaxBlocks = 608;   // upper bound of a launch's blocks: 4 on each
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool HALF>   // HALF: at most 8 rows
 struct Shape {
   // Warps side by side over the same keys, each with a part of O's columns
   // (the scores are computed by each): at head_dim 256 one block fills an SM's
@@ -60,21 +60,21 @@ struct Shape {
   // Blocks per SM: as many as the stages allow in 227 KB.
   static constexpr int kBlocksPerSm = kStageBytes >= 65536 ? 1 : (kStageBytes >= 32768 ? 2 : 3);
   static constexpr int kOffsets = kStages + 1;               // tiles whose row offsets are kept
-  static constexpr int kQBytes = kRows * D * 2;              // query rows of one unit (ring of kStages units)
+  static constexpr int kQBytes = (HALF ? 8 : kRows) * D * 2; // query rows of one unit (ring of kStages units)
   static constexpr int kOffQ = kStages * kStageBytes;
   static constexpr int kOffOffsets = kOffQ + kStages * kQBytes;
   static constexpr int kOffSeen = kOffOffsets + kOffsets * kTile * 8;
   static constexpr int kOffJoin = kOffSeen + kOffsets * (kTile / 32) * 4;
   static constexpr int kOffScan = kOffJoin + 2 * kWarps * kRows * 4;
-  static constexpr int kSmem = kOffScan + kThreads / 32 * 8 + 16;
+  static constexpr int kSmem = kOffScan + kThreads / 32 * 4 + 16;
   static_assert(kStageBytes >= kWarps * kRows * D * 4, "join buffer");
   static_assert(kKeys == 16 || kKeys == 32, "a word of seen keys");
   static_assert(kTile <= kThreads, "a thread per key looks up its page");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// A unit that is cut by the end of a block's run, seen from the block in
-// which it starts: blocks [this one, last] hold its partial results.
+// The unit that the end of a block's run cuts, if it starts in that run:
+// blocks [this one, last] hold its partial results.
 struct Cut {
   int unit;    // b * heads_kv + key/value head, or -1
   int last;
@@ -82,16 +82,17 @@ struct Cut {
   int pad;
 };
 
-struct Work {
-  float* parts;   // [blocks][2 slots][rows][D] sums of p v, then [rows] reference maxima, [rows] sums of p
-  Cut* cuts;      // [blocks]
-};
-
 struct Launch {
   int rows;        // query heads per chunk (at most kRows)
   int chunks;      // chunks of the G query heads of a key/value head
   int blocks;      // blocks per chunk
 };
+
+// Workspace: [blocks] cuts, then partial results [blocks][2 slots]: [rows][D]
+// sums of p v, [rows] reference maxima and [rows] sums of p.
+__host__ __device__ inline float* parts_of(float* work, size_t blocks) {
+  return reinterpret_cast<float*>(reinterpret_cast<Cut*>(work) + blocks);
+}
 
 __host__ __device__ inline size_t part_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
 
@@ -110,6 +111,9 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a)
                : "memory");
+}
+__device__ __forceinline__ void ldsm2(uint32_t& r0, uint32_t& r1, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(a) : "memory");
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -176,20 +180,78 @@ struct Lens {
   }
 };
 
-// First tile of run c when `total` tiles are cut into n <= total runs (none
-// empty), and the run that holds tile x.
-__device__ __forceinline__ long long run_start(long long c, long long total, int n) { return c * total / n; }
-__device__ __forceinline__ int run_of(long long x, long long total, int n) {
-  return static_cast<int>(((x + 1) * n - 1) / total);
-}
+// The list of all tiles (requests in order, the key/value heads of each, the
+// tiles of each) cut into `runs` runs, none empty, that differ by one at most.
+struct Runs {
+  int total, runs, base, rem;
+  __device__ __forceinline__ Runs(int total_, int blocks) : total(total_), runs(min(total_, blocks)) {
+    base = static_cast<unsigned>(total) / static_cast<unsigned>(runs);
+    rem = total - base * runs;
+  }
+  __device__ __forceinline__ int start(int c) const { return c * base + min(c, rem); }
+  // The run that holds tile x.
+  __device__ __forceinline__ int of(int x) const {
+    const int y = x - rem * (base + 1);
+    return y < 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(base + 1)
+                 : rem + static_cast<unsigned>(y) / static_cast<unsigned>(base);
+  }
+};
+
+// Tiles of all requests before those of this thread, of its own (requests
+// [b0, b1)) and in all, by a scan over the block.  scan: a word per warp.
+template <int TILE, int THREADS>
+struct Scan {
+  int b0, b1, before, mine, total;
+  __device__ __forceinline__ Scan(const Lens& L, int batch, int heads_kv, int* scan) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (batch + THREADS - 1) / THREADS;
+    b0 = min(tid * per, batch);
+    b1 = min(b0 + per, batch);
+    mine = 0;
+    for (int b = b0; b < b1; ++b) mine += L.tiles<TILE>(L.len(b));
+    mine *= heads_kv;
+    int upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += x;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) upto += scan[w];
+      total += scan[w];
+    }
+    before = upto - mine;
+  }
+  // The thread whose requests hold tile x writes the tile's request, key/value
+  // head, place and the request's length to found[4].
+  __device__ __forceinline__ void find(const Lens& L, int heads_kv, int x, int* found) const {
+    if (x < before || x >= before + mine) return;
+    int at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int len = L.len(b), nt = L.tiles<TILE>(len);
+      if (x < at + nt * heads_kv) {
+        const unsigned in = x - at;
+        found[0] = b;
+        found[1] = in / static_cast<unsigned>(nt);
+        found[2] = in % static_cast<unsigned>(nt);
+        found[3] = len;
+        return;
+      }
+      at += nt * heads_kv;
+    }
+  }
+};
 
 // A place in the list of tiles: tile t of nt of (request b, key/value head hk).
 template <int TILE>
 struct Place {
   int b, hk, t, nt, first, len;
-  __device__ __forceinline__ void request(const Lens& L, int batch) {
-    if (b >= batch) return;
-    len = L.len(b);
+  __device__ __forceinline__ void request(const Lens& L, int length) {
+    len = length;
     first = L.first(len);
     nt = L.tiles<TILE>(len);
   }
@@ -198,16 +260,15 @@ struct Place {
     t = 0;
     if (++hk < heads_kv) return;
     hk = 0;
-    ++b;
-    request(L, batch);
+    if (++b < batch) request(L, L.len(b));
   }
 };
 
 // ------------------------------------------------------------------ main kernel
-template <int D, bool E4M3, bool HALF>   // HALF: at most 8 rows
-__global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlocksPerSm)
-    decode_kernel(const DecodeParams p, const Launch lc, const Work work) {
-  using S = Shape<D, E4M3>;
+template <int D, bool E4M3, bool HALF>
+__global__ void __launch_bounds__(Shape<D, E4M3, HALF>::kThreads, Shape<D, E4M3, HALF>::kBlocksPerSm)
+    decode_kernel(const DecodeParams p, const Launch lc) {
+  using S = Shape<D, E4M3, HALF>;
   constexpr int TILE = S::kTile, RB = S::kRowBytes, ST = S::kStages, kThreads = S::kThreads;
   constexpr int NT = S::kKeys / 8;   // a warp's score columns, in groups of 8 keys
   constexpr int DO = D / S::kSplit;  // columns of O of a warp
@@ -218,8 +279,8 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
   uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + S::kOffSeen);
   float* const join_m = reinterpret_cast<float*>(smem + S::kOffJoin);
   float* const join_l = join_m + kWarps * kRows;
-  long long* const scan = reinterpret_cast<long long*>(smem + S::kOffScan);   // [warps]
-  int* const found = reinterpret_cast<int*>(scan + kThreads / 32);            // b, hk, t
+  int* const scan = reinterpret_cast<int*>(smem + S::kOffScan);   // [warps]
+  int* const found = scan + kThreads / 32;                        // b, hk, t, length
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kwarp = warp % kWarps, c0 = warp / kWarps * DO;   // its part of a tile's keys, its first column of O
@@ -233,54 +294,23 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
   for (int i = tid; i < ST * S::kQBytes / 16; i += kThreads)
     reinterpret_cast<uint4*>(smem + S::kOffQ)[i] = make_uint4(0, 0, 0, 0);
 
-  // The run of this block: every block counts all tiles (a scan over the
-  // requests), then finds where its share starts.
-  const int per = (p.batch + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += L.tiles<TILE>(L.len(b));
-  mine *= p.kv.heads_kv;
-  long long upto = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += x;
-  }
-  if (lane == 31) scan[warp] = upto;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) upto += scan[w];
-    total += scan[w];
-  }
-  const int runs = total < lc.blocks ? static_cast<int>(total) : lc.blocks;
-  if (static_cast<int>(blockIdx.x) >= runs) {
-    if (tid == 0) work.cuts[block].unit = -1;
+  // The run of this block: every block counts all tiles, then finds where
+  // its share starts.
+  const Scan<TILE, kThreads> tiles(L, p.batch, p.kv.heads_kv, scan);
+  const Runs runs(tiles.total, lc.blocks);
+  Cut* const cut = reinterpret_cast<Cut*>(p.work) + block;
+  if (static_cast<int>(blockIdx.x) >= runs.runs) {
+    if (tid == 0) cut->unit = -1;
     return;
   }
-  const long long start = run_start(blockIdx.x, total, runs);
-  const int n = static_cast<int>(run_start(blockIdx.x + 1, total, runs) - start);
-  if (start >= upto - mine && start < upto) {
-    long long at = upto - mine;
-    for (int b = b0; b < b1; ++b) {
-      const int nt = L.tiles<TILE>(L.len(b));
-      const long long all = static_cast<long long>(nt) * p.kv.heads_kv;
-      if (start < at + all) {
-        found[0] = b;
-        found[1] = static_cast<int>((start - at) / nt);
-        found[2] = static_cast<int>((start - at) % nt);
-        break;
-      }
-      at += all;
-    }
-  }
+  const int start = runs.start(blockIdx.x), n = runs.start(blockIdx.x + 1) - start;
+  tiles.find(L, p.kv.heads_kv, start, found);
   __syncthreads();
   Place<TILE> here;   // the tile being computed
   here.b = found[0];
   here.hk = found[1];
   here.t = found[2];
-  here.request(L, p.batch);
+  here.request(L, found[3]);
   Place<TILE> ahead = here;   // the next tile to load
   pdl_launch();
 
@@ -289,14 +319,14 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
   auto look_up = [&](const Place<TILE>& at) -> int {
     const int key = at.first + at.t * TILE + tid;
     if (tid >= TILE || key >= at.len) return -1;
-    return __ldg(p.table + at.b * p.table_stride + key / p.kv.page_size);
+    return __ldg(p.table + at.b * p.table_stride + static_cast<unsigned>(key) / static_cast<unsigned>(p.kv.page_size));
   };
   auto store_offset = [&](const Place<TILE>& at, int page, int ring) {
     if (tid >= TILE) return;
     const int key = at.first + at.t * TILE + tid;
     const bool ok = key < at.len && page >= 0 && page < p.kv.num_pages;
     offsets[ring * TILE + tid] =
-        ok ? (page * p.kv.page_stride + (key % p.kv.page_size) * p.kv.slot_stride) * S::kElem : -1;
+        ok ? (page * p.kv.page_stride + (static_cast<unsigned>(key) % static_cast<unsigned>(p.kv.page_size)) * p.kv.slot_stride) * S::kElem : -1;
     const uint32_t bits = __ballot_sync(0xffffffffu, ok);
     if (lane == 0) seen[ring * (TILE / 32) + warp] = bits;
   };
@@ -307,14 +337,22 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
     const unsigned char* const kb = static_cast<const unsigned char*>(p.kv.k) + head;
     const unsigned char* const vb = static_cast<const unsigned char*>(p.kv.v) + head;
     const uint32_t dst = sbase + stage * S::kStageBytes;
-#pragma unroll
-    for (int i = 0; i < TILE / RPP; ++i) {
-      const int r = row_in_pass + i * RPP;
+    auto load_row = [&](int r) {
       const long long off = offsets[ring * TILE + r];
       const uint32_t to = dst + swizzled<RB>(r, piece);
       const bool ok = off >= 0;   // unseen rows are zero-filled: nothing is read
       cp_async16(to, ok ? static_cast<const void*>(kb + off) : p.q, ok);
       cp_async16(to + S::kTileBytes, ok ? static_cast<const void*>(vb + off) : p.q, ok);
+    };
+    // Of a tile that is not full, rows are filled up to the end of the last
+    // warp's share that has a key; warps without one skip the tile.
+    const int keys = at.len - at.first - at.t * TILE;
+    if (keys >= TILE) {
+#pragma unroll
+      for (int i = 0; i < TILE / RPP; ++i) load_row(row_in_pass + i * RPP);
+    } else {
+      const int end = (keys + S::kKeys - 1) / S::kKeys * S::kKeys;
+      for (int r = row_in_pass; r < end; r += RPP) load_row(r);
     }
     if (with_q) {
       const uint16_t* const q = p.q + at.b * p.q_row_stride + (static_cast<long long>(at.hk) * G + row0) * D;
@@ -329,10 +367,21 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
   int q_load = 0;                 // query slot of the unit being loaded
   {
     Place<TILE> load = here;
+    int pages[ST - 1];   // looked up together: one trip to memory
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) {
+      pages[i] = -1;
+      if (i < n) {
+        pages[i] = look_up(ahead);
+        ahead.next(L, p.batch, p.kv.heads_kv);
+      }
+    }
+    Place<TILE> at = here;
+#pragma unroll
     for (int i = 0; i < ST - 1; ++i) {
       if (i < n) {
-        store_offset(ahead, look_up(ahead), i);
-        ahead.next(L, p.batch, p.kv.heads_kv);
+        store_offset(at, pages[i], i);
+        at.next(L, p.batch, p.kv.heads_kv);
       }
     }
     __syncthreads();
@@ -388,7 +437,14 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
       if constexpr (!E4M3) {
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) ldsm4(qa[j], qb + swizzled<D * 2>(lane & 15, 2 * j + (lane >> 4)));
+        for (int j = 0; j < D / 16; ++j) {
+          if constexpr (HALF) {
+            ldsm2(qa[j][0], qa[j][2], qb + swizzled<D * 2>(lane & 7, 2 * j + ((lane >> 3) & 1)));
+            qa[j][1] = qa[j][3] = 0u;
+          } else {
+            ldsm4(qa[j], qb + swizzled<D * 2>(lane & 15, 2 * j + (lane >> 4)));
+          }
+        }
       } else {
         // A thread's four bytes of a K row are four consecutive dimensions;
         // they serve as the products' k = 2 quad, + 1, + 8, + 9, and the query
@@ -426,123 +482,126 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
     }
 
     const uint32_t kt = sbase + stage * S::kStageBytes, vt = kt + S::kTileBytes;
-    // S = Q K^T for the warp's keys
     const int key0 = kwarp * S::kKeys;
-    float x[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
-    const int kr = key0 + (lane & 7) + ((lane >> 4) << 3);
-    if constexpr (!E4M3) {
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-        for (int i = 0; i < NT; i += 2) {
-          uint32_t b[4];
-          ldsm4(b, kt + swizzled<RB>(kr + 8 * i, 2 * j + ((lane >> 3) & 1)));
-          mma<false>(x[i], qa[j], b[0], b[1]);
-          mma<false>(x[i + 1], qa[j], b[2], b[3]);
-        }
-    } else {
-#pragma unroll
-      for (int j = 0; j < D / 16; j += 2)
-#pragma unroll
-        for (int i = 0; i < NT; i += 2) {
-          uint32_t b[4];
-          ldsm4(b, kt + swizzled<RB>(kr + 8 * i, j + ((lane >> 3) & 1)));
-          mma<true>(x[i], qa[j], e4m3_lo(b[0]), e4m3_hi(b[0]));
-          mma<true>(x[i + 1], qa[j], e4m3_lo(b[2]), e4m3_hi(b[2]));
-          mma<true>(x[i], qa[j + 1], e4m3_lo(b[1]), e4m3_hi(b[1]));
-          mma<true>(x[i + 1], qa[j + 1], e4m3_lo(b[3]), e4m3_hi(b[3]));
-        }
-    }
-    // scores in units of log 2, unseen keys at -inf
     uint32_t bits = seen[ring * (TILE / 32) + (key0 >> 5)] >> (key0 & 31);
-    if constexpr (S::kKeys == 16) bits |= 0xffff0000u;
-    float top[NR];
-    bool rise = false;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      top[r] = -INFINITY;
+    if constexpr (S::kKeys == 16) bits &= 0xffffu;
+    if (bits != 0u) {
+      // S = Q K^T for the warp's keys
+      float x[NT][4];
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float& v = x[i][2 * r + c];
-          v *= row_scale[r];
-          if (bits != 0xffffffffu && !((bits >> (i * 8 + 2 * quad + c)) & 1u)) v = -INFINITY;
-          top[r] = fmaxf(top[r], v);
-        }
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      rise |= top[r] > m[r];
-    }
-    if (__any_sync(0xffffffffu, rise)) {
+        for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+      const int kr = key0 + (lane & 7) + ((lane >> 4) << 3);
+      if constexpr (!E4M3) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const float up = fmaxf(m[r], top[r]);
-        const float keep = up == m[r] ? 1.f : ex2_approx(m[r] - up);
-        m[r] = up;
-        l[r] *= keep;
+        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int i = 0; i < DO / 8; ++i) {
-          o[i][2 * r] *= keep;
-          o[i][2 * r + 1] *= keep;
-        }
-      }
-    }
-    // P: rounded to 16 bits for the second product, summed in 32.  In fp16
-    // (e4m3 caches) the weights carry a factor 2^8 so that none above 2^-22
-    // of the largest is subnormal.
-    uint32_t pa[NT / 2][4];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (r < NR) {
-        const float ref = (m[r] == -INFINITY ? 0.f : m[r]) - (E4M3 ? 8.f : 0.f);
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const float e0 = ex2_approx(x[i][2 * r] - ref), e1 = ex2_approx(x[i][2 * r + 1] - ref);
-          sum += e0 + e1;
-          pa[i / 2][2 * (i & 1) + r] = E4M3 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
-        }
-        l[r < NR ? r : 0] += sum;
+          for (int i = 0; i < NT; i += 2) {
+            uint32_t b[4];
+            ldsm4(b, kt + swizzled<RB>(kr + 8 * i, 2 * j + ((lane >> 3) & 1)));
+            mma<false>(x[i], qa[j], b[0], b[1]);
+            mma<false>(x[i + 1], qa[j], b[2], b[3]);
+          }
       } else {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) pa[i / 2][2 * (i & 1) + r] = 0u;
+        for (int j = 0; j < D / 16; j += 2)
+#pragma unroll
+          for (int i = 0; i < NT; i += 2) {
+            uint32_t b[4];
+            ldsm4(b, kt + swizzled<RB>(kr + 8 * i, j + ((lane >> 3) & 1)));
+            mma<true>(x[i], qa[j], e4m3_lo(b[0]), e4m3_hi(b[0]));
+            mma<true>(x[i + 1], qa[j], e4m3_lo(b[2]), e4m3_hi(b[2]));
+            mma<true>(x[i], qa[j + 1], e4m3_lo(b[1]), e4m3_hi(b[1]));
+            mma<true>(x[i + 1], qa[j + 1], e4m3_lo(b[3]), e4m3_hi(b[3]));
+          }
       }
-    }
-    // O += P V
-    const int vr = key0 + (lane & 15);
-    if constexpr (!E4M3) {
+      // scores in units of log 2, unseen keys at -inf
+      if constexpr (S::kKeys == 16) bits |= 0xffff0000u;
+      float top[NR];
+      bool rise = false;
 #pragma unroll
-      for (int i = 0; i < NT / 2; ++i)
+      for (int r = 0; r < NR; ++r) {
+        top[r] = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < DO / 16; ++j) {
-          uint32_t b[4];
-          ldsm4t(b, vt + swizzled<RB>(vr + 16 * i, c0 / 8 + 2 * j + (lane >> 4)));
-          mma<false>(o[2 * j], pa[i], b[0], b[1]);
-          mma<false>(o[2 * j + 1], pa[i], b[2], b[3]);
-        }
-    } else {
-      // Transposed as 16-bit units, a register holds two keys' bytes of two
-      // neighbouring dimensions: even and odd dimensions become the two
-      // products' columns.
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int i = 0; i < NT / 2; ++i)
+          for (int c = 0; c < 2; ++c) {
+            float& v = x[i][2 * r + c];
+            v *= row_scale[r];
+            if (bits != 0xffffffffu && !((bits >> (i * 8 + 2 * quad + c)) & 1u)) v = -INFINITY;
+            top[r] = fmaxf(top[r], v);
+          }
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+        rise |= top[r] > m[r];
+      }
+      if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-        for (int j = 0; j < DO / 16; j += 2) {
-          uint32_t b[4];
-          ldsm4t(b, vt + swizzled<RB>(vr + 16 * i, c0 / 16 + j + (lane >> 4)));
+        for (int r = 0; r < NR; ++r) {
+          const float up = fmaxf(m[r], top[r]);
+          const float keep = up == m[r] ? 1.f : ex2_approx(m[r] - up);
+          m[r] = up;
+          l[r] *= keep;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t even = __byte_perm(b[2 * u], b[2 * u + 1], 0x6420);
-            const uint32_t odd = __byte_perm(b[2 * u], b[2 * u + 1], 0x7531);
-            mma<true>(o[2 * (j + u)], pa[i], e4m3_lo(even), e4m3_hi(even));
-            mma<true>(o[2 * (j + u) + 1], pa[i], e4m3_lo(odd), e4m3_hi(odd));
+          for (int i = 0; i < DO / 8; ++i) {
+            o[i][2 * r] *= keep;
+            o[i][2 * r + 1] *= keep;
           }
         }
+      }
+      // P: rounded to 16 bits for the second product, summed in 32.  In fp16
+      // (e4m3 caches) the weights carry a factor 2^8 so that none above 2^-22
+      // of the largest is subnormal.
+      uint32_t pa[NT / 2][4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (r < NR) {
+          const float ref = (m[r] == -INFINITY ? 0.f : m[r]) - (E4M3 ? 8.f : 0.f);
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const float e0 = ex2_approx(x[i][2 * r] - ref), e1 = ex2_approx(x[i][2 * r + 1] - ref);
+            sum += e0 + e1;
+            pa[i / 2][2 * (i & 1) + r] = E4M3 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+          }
+          l[r < NR ? r : 0] += sum;
+        } else {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) pa[i / 2][2 * (i & 1) + r] = 0u;
+        }
+      }
+      // O += P V
+      const int vr = key0 + (lane & 15);
+      if constexpr (!E4M3) {
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i)
+#pragma unroll
+          for (int j = 0; j < DO / 16; ++j) {
+            uint32_t b[4];
+            ldsm4t(b, vt + swizzled<RB>(vr + 16 * i, c0 / 8 + 2 * j + (lane >> 4)));
+            mma<false>(o[2 * j], pa[i], b[0], b[1]);
+            mma<false>(o[2 * j + 1], pa[i], b[2], b[3]);
+          }
+      } else {
+        // Transposed as 16-bit units, a register holds two keys' bytes of two
+        // neighbouring dimensions: even and odd dimensions become the two
+        // products' columns.
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i)
+#pragma unroll
+          for (int j = 0; j < DO / 16; j += 2) {
+            uint32_t b[4];
+            ldsm4t(b, vt + swizzled<RB>(vr + 16 * i, c0 / 16 + j + (lane >> 4)));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t even = __byte_perm(b[2 * u], b[2 * u + 1], 0x6420);
+              const uint32_t odd = __byte_perm(b[2 * u], b[2 * u + 1], 0x7531);
+              mma<true>(o[2 * (j + u)], pa[i], e4m3_lo(even), e4m3_hi(even));
+              mma<true>(o[2 * (j + u) + 1], pa[i], e4m3_lo(odd), e4m3_hi(odd));
+            }
+          }
+      }
     }
 
     const bool unit_done = here.t + 1 == here.nt;
@@ -580,7 +639,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
       const bool starts_here = here.t <= s;   // the unit's first tile is in this run
       const bool whole = unit_done && starts_here;
       const int slot = first_piece ? 0 : 1;
-      float* const part = work.parts + (static_cast<size_t>(block) * 2 + slot) * part_floats(lc.rows, D);
+      float* const part = parts_of(p.work, gridDim.x * gridDim.y) + (static_cast<size_t>(block) * 2 + slot) * part_floats(lc.rows, D);
       for (int i = tid; i < rows * (D / 4); i += kThreads) {
         const int row = i / (D / 4), c4 = i % (D / 4);
         float top = -INFINITY;
@@ -619,12 +678,8 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
         }
       }
       if (s + 1 == n && tid == 0) {
-        Cut cut;
-        cut.unit = !unit_done && starts_here ? here.b * p.kv.heads_kv + here.hk : -1;
-        cut.last = run_of(start + s - here.t + here.nt - 1, total, runs);
-        cut.slot = slot;
-        cut.pad = 0;
-        work.cuts[block] = cut;
+        const int unit = !unit_done && starts_here ? here.b * p.kv.heads_kv + here.hk : -1;
+        *reinterpret_cast<int4*>(cut) = make_int4(unit, runs.of(start + s - here.t + here.nt - 1), slot, 0);
       }
       fresh = true;
       first_piece = false;
@@ -637,26 +692,27 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, Shape<D, E4M3>::kBlo
 }
 
 // ------------------------------------------------------------------ combine
-// One block per (cut unit, query head): joins the partial results of the
-// runs the unit lies in, group g of its threads those of runs g, g + GROUPS,
-// ... in one pass with a running maximum, then the groups in order.
-constexpr int kJoinThreads = 128;
+// One block per (run, query head), for the unit that the run's end cuts, if
+// it starts in that run: joins the partial results of the runs the unit lies
+// in, group g of its threads those of runs g, g + GROUPS, ... in one pass
+// with a running maximum, then the groups in order.
+constexpr int kJoinThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParams p, const Launch lc,
-                                                               const Work work) {
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParams p, const Launch lc) {
   constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
   __shared__ float s_top[GROUPS], s_sum[GROUPS];
   __shared__ float4 s_acc[kJoinThreads];
-  pdl_wait();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, run = blockIdx.x;
   const int chunk = blockIdx.y / lc.rows, row = blockIdx.y % lc.rows;
   const int G = p.heads / p.kv.heads_kv;
+  pdl_wait();
   if (chunk * lc.rows + row >= G) return;
-  const int c0 = blockIdx.x;
-  const Cut cut = work.cuts[chunk * lc.blocks + c0];
-  if (cut.unit < 0) return;
-  const int n = cut.last - c0 + 1;
+  const int4 cut = *(reinterpret_cast<const int4*>(p.work) + chunk * lc.blocks + run);
+  if (cut.x < 0) return;
+  const int b = cut.x / p.kv.heads_kv, hk = cut.x % p.kv.heads_kv;
+  const int n = cut.y - run + 1, first_slot = cut.z;
+  const float* const parts = parts_of(p.work, static_cast<size_t>(lc.blocks) * lc.chunks);
   const size_t pf = part_floats(lc.rows, D);
   const int col = tid % COLS, group = tid / COLS;
   float top = -INFINITY, sum = 0.f;
@@ -664,7 +720,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
 #pragma unroll 4
   for (int i = group; i < n; i += GROUPS) {
     const float* const part =
-        work.parts + (static_cast<size_t>(chunk * lc.blocks + c0 + i) * 2 + (i == 0 ? cut.slot : 0)) * pf;
+        parts + (static_cast<size_t>(chunk * lc.blocks + run + i) * 2 + (i == 0 ? first_slot : 0)) * pf;
     const float2* const from = reinterpret_cast<const float2*>(part + row * D + col * 4);
     const float2 a = from[0], b = from[1];
     const float mi = part[lc.rows * D + row], li = part[lc.rows * D + lc.rows + row];
@@ -699,7 +755,6 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
     acc.z = fmaf(f, a.z, acc.z);
     acc.w = fmaf(f, a.w, acc.w);
   }
-  const int b = cut.unit / p.kv.heads_kv, hk = cut.unit % p.kv.heads_kv;
   const float inv = sum == 0.f ? 0.f : (p.kv.v_scale ? __ldg(p.kv.v_scale + hk) : 1.f) / sum;
   const long long at = static_cast<long long>(b) * p.heads + hk * G + chunk * lc.rows + row;
   uint2 out;
@@ -730,7 +785,7 @@ int sm_count() {
 
 template <int D, bool E4M3, bool HALF>
 cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
-  using Sh = Shape<D, E4M3>;
+  using Sh = Shape<D, E4M3, HALF>;
   static std::atomic<unsigned long long> smem_done{0};
   auto* const kernel = decode_kernel<D, E4M3, HALF>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), Sh::kSmem, smem_done);
@@ -744,11 +799,7 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   if (blocks > kMaxBlocks) blocks = kMaxBlocks;
   blocks = blocks / lc.chunks > 1 ? blocks / lc.chunks : 1;
   lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
-  Work work;
-  const size_t all = static_cast<size_t>(lc.blocks) * lc.chunks;
-  work.cuts = reinterpret_cast<Cut*>(p.work);
-  work.parts = reinterpret_cast<float*>(work.cuts + all);
-  kernel<<<dim3(lc.blocks, lc.chunks), Sh::kThreads, Sh::kSmem, s>>>(p, lc, work);
+  kernel<<<dim3(lc.blocks, lc.chunks), Sh::kThreads, Sh::kSmem, s>>>(p, lc);
   e = cudaGetLastError();
   if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
   cudaLaunchConfig_t cfg = {};
@@ -760,7 +811,7 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p, lc, work);
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p, lc);
 }
 
 template <int D, bool E4M3>
