@@ -9,8 +9,9 @@
 //
 // The call has to read every visible key and value once and does 2 G
 // operations per cached bf16 byte: it is bound by HBM.  So
-//   * the G query heads of a key/value head share one pass over its keys: they
-//     are the rows of 16-row tensor-core products (S = Q K^T, O += P V), which
+//   * the G query heads of a key/value head share one pass over its keys.  They
+//     are the columns of 16 x 8 tensor-core products S^T = K Q^T, O^T += V^T P^T
+//     (keys and dimensions in the rows, so that few heads waste little), which
 //     keeps the arithmetic far below the time of the loads;
 //   * keys are taken in tiles of kTile; the tiles of all (request, key/value
 //     head) units, in order, are cut into equal runs, one per resident block.
@@ -21,7 +22,7 @@
 //   * K and V rows come through cp.async into a ring of kStages tiles (any
 //     page size and strides; a TMA box would tie the tile to the page), the
 //     block-table entries one tile further ahead.
-// Each warp takes 16 keys of a tile at a time with a running maximum and sum
+// Each warp takes its 16 or 32 keys of a tile with a running reference and sum
 // of its own; the warps' states are joined where a unit ends.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -35,42 +36,49 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;         // warps over the keys of a tile
-constexpr int kRows = 16;         // query heads per block (rows of the tensor-core products)
-constexpr int kMaxBlocks = 608;   // upper bound of a launch's blocks: 4 on each of 152 SMs
+constexpr int kMaxBlocks = 304;   // upper bound of a launch's blocks: 2 on each of 152 SMs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// A warp's reference for the exponents moves only when a score exceeds it by
+// more than kSlack (units of log 2): weights are at most 2^kSlack, and the
+// maximum over the warp is taken a few times per unit instead of every tile.
+constexpr float kSlack = 8.f;
 
-template <int D, bool E4M3, bool HALF>   // HALF: at most 8 rows
+// NH: groups of 8 query heads.
+template <int D, bool E4M3, int NH>
 struct Shape {
-  // Warps side by side over the same keys, each with a part of O's columns
-  // (the scores are computed by each): at head_dim 256 one block fills an SM's
-  // shared memory, and 4 warps would hold 192 registers of O and Q each.
-  static constexpr int kSplit = D == 256 ? 2 : 1;
-  static constexpr int kThreads = kWarps * kSplit * 32;
   static constexpr int kElem = E4M3 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
-  // Keys per tile: K and V tiles together are at least the 4 * 16 * D floats
-  // that joining the warps takes (it reuses the stage just consumed).
-  static constexpr int kTile = E4M3 || D == 64 ? 128 : 64;
-  static constexpr int kKeys = kTile / kWarps;                // of a warp
+  static constexpr int kTile = E4M3 || D == 64 ? 128 : 64;   // keys
   static constexpr int kTileBytes = kTile * kRowBytes;       // of K, and of V
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = 3;
-  // Blocks per SM: as many as the stages allow in 227 KB.
-  static constexpr int kBlocksPerSm = kStageBytes >= 65536 ? 1 : (kStageBytes >= 32768 ? 2 : 3);
+  // Two blocks per SM where two rings of stages and queries fit; with 8 warps
+  // each where the fragments of O and Q fit 128 registers.
+  static constexpr int kBlocksPerSm =
+      kStageBytes >= 65536 || (kStageBytes >= 32768 && NH > (E4M3 ? 1 : 2)) ? 1 : 2;
+  static constexpr int kStages = kStageBytes >= 65536 || (kStageBytes >= 32768 && kBlocksPerSm == 2) ? 3 : 5;
+  static constexpr int kKeyWarps = kTile == 64 || (kBlocksPerSm == 2 && NH > 2) ? 4 : 8;
+  // Warps over the same keys, each with a part of O's columns (and all of the
+  // scores), where 4 warps would be all that an SM runs.
+  static constexpr int kSplit = kTile == 64 && kBlocksPerSm == 1 ? 2 : 1;
+  static constexpr int kThreads = kKeyWarps * kSplit * 32;
+  static constexpr int kKeys = kTile / kKeyWarps;            // of a warp
+  static constexpr int kHeads = 8 * NH;
   static constexpr int kOffsets = kStages + 1;               // tiles whose row offsets are kept
-  static constexpr int kQBytes = (HALF ? 8 : kRows) * D * 2; // query rows of one unit (ring of kStages units)
+  static constexpr int kQBytes = kHeads * D * 2;             // queries of one unit (ring of kStages units)
+  // The warps' O are joined in the stage just consumed, so many heads at a time.
+  static constexpr int kJoinFit = kStageBytes / (kKeyWarps * D * 4) / 8 * 8;
+  static constexpr int kJoinHeads = kJoinFit < kHeads ? kJoinFit : kHeads;
   static constexpr int kOffQ = kStages * kStageBytes;
   static constexpr int kOffOffsets = kOffQ + kStages * kQBytes;
   static constexpr int kOffSeen = kOffOffsets + kOffsets * kTile * 8;
   static constexpr int kOffJoin = kOffSeen + kOffsets * (kTile / 32) * 4;
-  static constexpr int kOffScan = kOffJoin + 2 * kWarps * kRows * 4;
+  static constexpr int kOffScan = kOffJoin + 2 * kKeyWarps * kHeads * 4;
   static constexpr int kSmem = kOffScan + kThreads / 32 * 4 + 16;
-  static_assert(kStageBytes >= kWarps * kRows * D * 4, "join buffer");
+  static_assert(kJoinHeads >= 8, "join buffer");
   static_assert(kKeys == 16 || kKeys == 32, "a word of seen keys");
   static_assert(kTile <= kThreads, "a thread per key looks up its page");
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kBlocksPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
 };
 
 // The unit that the end of a block's run cuts, if it starts in that run:
@@ -83,7 +91,7 @@ struct Cut {
 };
 
 struct Launch {
-  int rows;        // query heads per chunk (at most kRows)
+  int rows;        // query heads per chunk (at most 8 NH)
   int chunks;      // chunks of the G query heads of a key/value head
   int blocks;      // blocks per chunk
 };
@@ -112,14 +120,17 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
                : "r"(a)
                : "memory");
 }
-__device__ __forceinline__ void ldsm2(uint32_t& r0, uint32_t& r1, uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(a) : "memory");
-}
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a)
                : "memory");
+}
+// Transposes an 8 x 8 matrix of 16-bit elements held two per lane.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 // c += a b, 16 x 8 x 16, fp32 accumulate; operands bf16 or fp16.
 template <bool F16>
@@ -265,25 +276,25 @@ struct Place {
 };
 
 // ------------------------------------------------------------------ main kernel
-template <int D, bool E4M3, bool HALF>
-__global__ void __launch_bounds__(Shape<D, E4M3, HALF>::kThreads, Shape<D, E4M3, HALF>::kBlocksPerSm)
+template <int D, bool E4M3, int NH>
+__global__ void __launch_bounds__(Shape<D, E4M3, NH>::kThreads, Shape<D, E4M3, NH>::kBlocksPerSm)
     decode_kernel(const DecodeParams p, const Launch lc) {
-  using S = Shape<D, E4M3, HALF>;
+  using S = Shape<D, E4M3, NH>;
   constexpr int TILE = S::kTile, RB = S::kRowBytes, ST = S::kStages, kThreads = S::kThreads;
-  constexpr int NT = S::kKeys / 8;   // a warp's score columns, in groups of 8 keys
+  constexpr int KW = S::kKeyWarps, HEADS = S::kHeads;
+  constexpr int KT = S::kKeys / 16;  // a warp's keys, in rows of the products
   constexpr int DO = D / S::kSplit;  // columns of O of a warp
-  constexpr int NR = HALF ? 1 : 2;   // groups of 8 rows with data
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t sbase = smem_u32(smem);
   long long* const offsets = reinterpret_cast<long long*>(smem + S::kOffOffsets);
   uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + S::kOffSeen);
   float* const join_m = reinterpret_cast<float*>(smem + S::kOffJoin);
-  float* const join_l = join_m + kWarps * kRows;
+  float* const join_l = join_m + KW * HEADS;
   int* const scan = reinterpret_cast<int*>(smem + S::kOffScan);   // [warps]
   int* const found = scan + kThreads / 32;                        // b, hk, t, length
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kwarp = warp % kWarps, c0 = warp / kWarps * DO;   // its part of a tile's keys, its first column of O
+  const int kwarp = warp % KW, c0 = warp / KW * DO;   // its part of a tile's keys, its first column of O
   const int G = p.heads / p.kv.heads_kv;
   const int row0 = blockIdx.y * lc.rows;                 // first query head of this chunk within its group
   const int rows = min(lc.rows, G - row0);
@@ -397,9 +408,11 @@ __global__ void __launch_bounds__(Shape<D, E4M3, HALF>::kThreads, Shape<D, E4M3,
   }
   int page_ahead = ST - 1 < n ? look_up(ahead) : -1;
 
-  uint32_t qa[D / 16][4];                   // query fragments (e4m3: fp16, rescaled per row)
-  float o[DO / 8][4];
-  float m[NR], l[NR], row_scale[NR];
+  // Per lane (g, quad): keys or dimensions g and g + 8 of 16, heads 2 quad and
+  // 2 quad + 1 of 8.
+  uint32_t qf[NH][D / 16][2];               // Q^T fragments (e4m3: fp16, rescaled per head)
+  float o[NH][DO / 16][4];
+  float m[NH][2], l[NH][2], factor[NH][2];  // reference, this lane's sum, scores to units of log 2
   int stage = 0, ring = 0, q_slot = 0;
   int load_stage = ST - 1, load_ring = ST - 1;
   bool fresh = true, first_piece = true;
@@ -424,59 +437,56 @@ __global__ void __launch_bounds__(Shape<D, E4M3, HALF>::kThreads, Shape<D, E4M3,
     if (fresh) {
       fresh = false;
       const uint32_t qb = sbase + S::kOffQ + q_slot * S::kQBytes;
-      const float ks = p.kv.k_scale ? __ldg(p.kv.k_scale + here.hk) : 1.f;
+      const float scale = p.scale * kLog2e * (p.kv.k_scale ? __ldg(p.kv.k_scale + here.hk) : 1.f);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-        row_scale[r] = p.scale * kLog2e * ks;
-      }
+      for (int i = 0; i < NH; ++i) {
 #pragma unroll
-      for (int i = 0; i < DO / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-      if constexpr (!E4M3) {
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          if constexpr (HALF) {
-            ldsm2(qa[j][0], qa[j][2], qb + swizzled<D * 2>(lane & 7, 2 * j + ((lane >> 3) & 1)));
-            qa[j][1] = qa[j][3] = 0u;
-          } else {
-            ldsm4(qa[j], qb + swizzled<D * 2>(lane & 15, 2 * j + (lane >> 4)));
-          }
+        for (int c = 0; c < 2; ++c) {
+          m[i][c] = -INFINITY;
+          l[i][c] = 0.f;
+          factor[i][c] = scale;
         }
-      } else {
-        // A thread's four bytes of a K row are four consecutive dimensions;
-        // they serve as the products' k = 2 quad, + 1, + 8, + 9, and the query
-        // is laid out alike.  It is held in fp16, which its bf16 values fit once
-        // each row is scaled by a power of two that brings its largest element
-        // to [2^14, 2^15): exact but for elements 2^-28 below the largest.
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (r < NR) {
-            float top = 0.f;
+        for (int j = 0; j < DO / 16; ++j)
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-              const uint32_t a = qb + swizzled<D * 2>(g + 8 * r, 2 * j + (quad >> 1)) + (quad & 1) * 8;
-              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(qa[j][r]), "=r"(qa[j][2 + r]) : "r"(a) : "memory");
-              top = fmaxf(top, fmaxf(fmaxf(fabsf(bf_lo(qa[j][r])), fabsf(bf_hi(qa[j][r]))),
-                                     fmaxf(fabsf(bf_lo(qa[j][2 + r])), fabsf(bf_hi(qa[j][2 + r])))));
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = static_cast<int>(__float_as_uint(top) >> 23);
-            const int up = e == 255 ? 127 : min(268 - max(e, 1), 253);   // biased exponent of the factor
-            const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
-            row_scale[r < NR ? r : 0] *= __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+          for (int c = 0; c < 4; ++c) o[i][j][c] = 0.f;
+        if constexpr (!E4M3) {
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-              qa[j][r] = pack_f16x2(bf_lo(qa[j][r]) * f, bf_hi(qa[j][r]) * f);
-              qa[j][2 + r] = pack_f16x2(bf_lo(qa[j][2 + r]) * f, bf_hi(qa[j][2 + r]) * f);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) qa[j][r] = qa[j][2 + r] = 0u;
+          for (int j = 0; j < D / 16; j += 2) {
+            uint32_t b[4];
+            ldsm4(b, qb + swizzled<D * 2>(8 * i + (lane & 7), 2 * j + (lane >> 3)));
+            qf[i][j][0] = b[0];
+            qf[i][j][1] = b[1];
+            qf[i][j + 1][0] = b[2];
+            qf[i][j + 1][1] = b[3];
           }
+        } else {
+          // A lane's four bytes of a K row are four consecutive dimensions;
+          // they serve as the products' k = 2 quad, + 1, + 8, + 9, and the query
+          // is laid out alike.  It is held in fp16, which its bf16 values fit
+          // once each row is scaled by a power of two that brings its largest
+          // element to [2^14, 2^15): exact but for elements 2^-28 below it.
+          float top = 0.f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const uint32_t a = qb + swizzled<D * 2>(8 * i + g, 2 * j + (quad >> 1)) + (quad & 1) * 8;
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(qf[i][j][0]), "=r"(qf[i][j][1]) : "r"(a) : "memory");
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              top = fmaxf(top, fmaxf(fabsf(bf_lo(qf[i][j][c])), fabsf(bf_hi(qf[i][j][c]))));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = static_cast<int>(__float_as_uint(top) >> 23);
+          const int up = e == 255 ? 127 : min(268 - max(e, 1), 253);   // biased exponent of the power
+          const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+          const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) qf[i][j][c] = pack_f16x2(bf_lo(qf[i][j][c]) * f, bf_hi(qf[i][j][c]) * f);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) factor[i][c] *= __shfl_sync(0xffffffffu, back, (2 * quad + c) * 4);
         }
       }
     }
@@ -486,121 +496,139 @@ __global__ void __launch_bounds__(Shape<D, E4M3, HALF>::kThreads, Shape<D, E4M3,
     uint32_t bits = seen[ring * (TILE / 32) + (key0 >> 5)] >> (key0 & 31);
     if constexpr (S::kKeys == 16) bits &= 0xffffu;
     if (bits != 0u) {
-      // S = Q K^T for the warp's keys
-      float x[NT][4];
+      // S^T = K Q^T for the warp's keys; with few products at a time, in two
+      // chains of half the dimensions each.
+      constexpr int CH = NH * KT == 1 ? 2 : 1;
+      float x[KT][NH][4], x2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int k = 0; k < KT; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
-      const int kr = key0 + (lane & 7) + ((lane >> 4) << 3);
-      if constexpr (!E4M3) {
+        for (int i = 0; i < NH; ++i)
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j)
+          for (int c = 0; c < 4; ++c) x[k][i][c] = 0.f;
 #pragma unroll
-          for (int i = 0; i < NT; i += 2) {
+      for (int j = 0; j < D / 16; j += 2) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          const int r = key0 + 16 * k + (lane & 15);
+          uint32_t a0[4], a1[4];   // dimensions 16 j + [0, 16) and + [16, 32)
+          if constexpr (!E4M3) {
+            ldsm4(a0, kt + swizzled<RB>(r, 2 * j + (lane >> 4)));
+            ldsm4(a1, kt + swizzled<RB>(r, 2 * j + 2 + (lane >> 4)));
+          } else {
             uint32_t b[4];
-            ldsm4(b, kt + swizzled<RB>(kr + 8 * i, 2 * j + ((lane >> 3) & 1)));
-            mma<false>(x[i], qa[j], b[0], b[1]);
-            mma<false>(x[i + 1], qa[j], b[2], b[3]);
+            ldsm4(b, kt + swizzled<RB>(r, j + (lane >> 4)));
+            a0[0] = e4m3_lo(b[0]);
+            a0[1] = e4m3_lo(b[1]);
+            a0[2] = e4m3_hi(b[0]);
+            a0[3] = e4m3_hi(b[1]);
+            a1[0] = e4m3_lo(b[2]);
+            a1[1] = e4m3_lo(b[3]);
+            a1[2] = e4m3_hi(b[2]);
+            a1[3] = e4m3_hi(b[3]);
           }
-      } else {
 #pragma unroll
-        for (int j = 0; j < D / 16; j += 2)
-#pragma unroll
-          for (int i = 0; i < NT; i += 2) {
-            uint32_t b[4];
-            ldsm4(b, kt + swizzled<RB>(kr + 8 * i, j + ((lane >> 3) & 1)));
-            mma<true>(x[i], qa[j], e4m3_lo(b[0]), e4m3_hi(b[0]));
-            mma<true>(x[i + 1], qa[j], e4m3_lo(b[2]), e4m3_hi(b[2]));
-            mma<true>(x[i], qa[j + 1], e4m3_lo(b[1]), e4m3_hi(b[1]));
-            mma<true>(x[i + 1], qa[j + 1], e4m3_lo(b[3]), e4m3_hi(b[3]));
+          for (int i = 0; i < NH; ++i) {
+            mma<E4M3>(x[k][i], a0, qf[i][j][0], qf[i][j][1]);
+            mma<E4M3>(CH == 2 ? x2 : x[k][i], a1, qf[i][j + 1][0], qf[i][j + 1][1]);
           }
+        }
       }
-      // scores in units of log 2, unseen keys at -inf
-      if constexpr (S::kKeys == 16) bits |= 0xffff0000u;
-      float top[NR];
-      bool rise = false;
+      if constexpr (CH == 2) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        top[r] = -INFINITY;
+        for (int c = 0; c < 4; ++c) x[0][0][c] += x2[c];
+      }
+      // Weights 2^(x factor - m + kShift), unseen keys 0.  In fp16 (e4m3 caches)
+      // they carry 2^kShift so that none above 2^-18 of the reference is subnormal.
+      constexpr float kShift = E4M3 ? 4.f : 0.f;
+      bool keep = true;
+      float y[KT][NH][4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int i = 0; i < NH; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            y[k][i][c] = fmaf(x[k][i][c], factor[i][c & 1], kShift - m[i][c & 1]);
+            if (bits != (S::kKeys == 16 ? 0xffffu : 0xffffffffu) && !((bits >> (16 * k + 8 * (c >> 1) + g)) & 1u))
+              y[k][i][c] = -INFINITY;
+            keep = keep && y[k][i][c] <= kSlack + kShift;
+          }
+      if (!__all_sync(0xffffffffu, keep)) {
+        // Some score is past the slack (the first tile always): new reference.
+#pragma unroll
+        for (int i = 0; i < NH; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float& v = x[i][2 * r + c];
-            v *= row_scale[r];
-            if (bits != 0xffffffffu && !((bits >> (i * 8 + 2 * quad + c)) & 1u)) v = -INFINITY;
-            top[r] = fmaxf(top[r], v);
+            float top = m[i][c];
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                if ((bits >> (16 * k + 8 * u + g)) & 1u) top = fmaxf(top, x[k][i][2 * u + c] * factor[i][c]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float f = top == m[i][c] ? 1.f : ex2_approx(m[i][c] - top);
+            m[i][c] = top;
+            l[i][c] *= f;
+#pragma unroll
+            for (int j = 0; j < DO / 16; ++j) {
+              o[i][j][c] *= f;
+              o[i][j][2 + c] *= f;
+            }
+            const float ref = kShift - (top == -INFINITY ? 0.f : top);
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                y[k][i][2 * u + c] = (bits >> (16 * k + 8 * u + g)) & 1u
+                                         ? fmaf(x[k][i][2 * u + c], factor[i][c], ref) : -INFINITY;
           }
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-        rise |= top[r] > m[r];
       }
-      if (__any_sync(0xffffffffu, rise)) {
+      // P^T, rounded to 16 bits for the second product, summed in 32.
+      uint32_t pf[KT][NH][2];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float up = fmaxf(m[r], top[r]);
-          const float keep = up == m[r] ? 1.f : ex2_approx(m[r] - up);
-          m[r] = up;
-          l[r] *= keep;
+      for (int k = 0; k < KT; ++k)
 #pragma unroll
-          for (int i = 0; i < DO / 8; ++i) {
-            o[i][2 * r] *= keep;
-            o[i][2 * r + 1] *= keep;
-          }
+        for (int i = 0; i < NH; ++i) {
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) e[c] = ex2_approx(y[k][i][c]);
+          l[i][0] += e[0] + e[2];
+          l[i][1] += e[1] + e[3];
+          pf[k][i][0] = transposed(E4M3 ? pack_f16x2(e[0], e[1]) : pack_bf16x2(e[0], e[1]));
+          pf[k][i][1] = transposed(E4M3 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]));
         }
-      }
-      // P: rounded to 16 bits for the second product, summed in 32.  In fp16
-      // (e4m3 caches) the weights carry a factor 2^8 so that none above 2^-22
-      // of the largest is subnormal.
-      uint32_t pa[NT / 2][4];
+      // O^T += V^T P^T
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (r < NR) {
-          const float ref = (m[r] == -INFINITY ? 0.f : m[r]) - (E4M3 ? 8.f : 0.f);
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const float e0 = ex2_approx(x[i][2 * r] - ref), e1 = ex2_approx(x[i][2 * r + 1] - ref);
-            sum += e0 + e1;
-            pa[i / 2][2 * (i & 1) + r] = E4M3 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
-          }
-          l[r < NR ? r : 0] += sum;
-        } else {
-#pragma unroll
-          for (int i = 0; i < NT; ++i) pa[i / 2][2 * (i & 1) + r] = 0u;
-        }
-      }
-      // O += P V
-      const int vr = key0 + (lane & 15);
-      if constexpr (!E4M3) {
-#pragma unroll
-        for (int i = 0; i < NT / 2; ++i)
+      for (int k = 0; k < KT; ++k) {
+        const int r = key0 + 16 * k;
+        if constexpr (!E4M3) {
 #pragma unroll
           for (int j = 0; j < DO / 16; ++j) {
-            uint32_t b[4];
-            ldsm4t(b, vt + swizzled<RB>(vr + 16 * i, c0 / 8 + 2 * j + (lane >> 4)));
-            mma<false>(o[2 * j], pa[i], b[0], b[1]);
-            mma<false>(o[2 * j + 1], pa[i], b[2], b[3]);
-          }
-      } else {
-        // Transposed as 16-bit units, a register holds two keys' bytes of two
-        // neighbouring dimensions: even and odd dimensions become the two
-        // products' columns.
+            uint32_t a[4];
+            ldsm4t(a, vt + swizzled<RB>(r + (lane & 7) + ((lane >> 4) << 3), c0 / 8 + 2 * j + ((lane >> 3) & 1)));
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i)
+            for (int i = 0; i < NH; ++i) mma<false>(o[i][j], a, pf[k][i][0], pf[k][i][1]);
+          }
+        } else {
+          // Transposed as 16-bit units, a register holds two keys' bytes of two
+          // neighbouring dimensions: rows g and g + 8 of the product are
+          // dimensions 2 g and 2 g + 1.
 #pragma unroll
           for (int j = 0; j < DO / 16; j += 2) {
             uint32_t b[4];
-            ldsm4t(b, vt + swizzled<RB>(vr + 16 * i, c0 / 16 + j + (lane >> 4)));
+            ldsm4t(b, vt + swizzled<RB>(r + (lane & 15), c0 / 16 + j + (lane >> 4)));
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const uint32_t even = __byte_perm(b[2 * u], b[2 * u + 1], 0x6420);
               const uint32_t odd = __byte_perm(b[2 * u], b[2 * u + 1], 0x7531);
-              mma<true>(o[2 * (j + u)], pa[i], e4m3_lo(even), e4m3_hi(even));
-              mma<true>(o[2 * (j + u) + 1], pa[i], e4m3_lo(odd), e4m3_hi(odd));
+              const uint32_t a[4] = {e4m3_lo(even), e4m3_lo(odd), e4m3_hi(even), e4m3_hi(odd)};
+#pragma unroll
+              for (int i = 0; i < NH; ++i) mma<true>(o[i][j + u], a, pf[k][i][0], pf[k][i][1]);
             }
           }
+        }
       }
     }
 
@@ -608,72 +636,85 @@ __global__ void __launch_bounds__(Shape<D, E4M3, HALF>::kThreads, Shape<D, E4M3,
     if (unit_done || s + 1 == n) {
       // Join the warps' states in the stage just consumed.
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (quad == 0) {
-          join_m[kwarp * kRows + g + 8 * r] = m[r];
-          join_l[kwarp * kRows + g + 8 * r] = l[r];
-        }
-      }
-      __syncthreads();   // every warp has read the stage
-      float* const buf = reinterpret_cast<float*>(smem + stage * S::kStageBytes);
+      for (int i = 0; i < NH; ++i)
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int row = g + 8 * r;
-        float* const to = buf + (kwarp * kRows + row) * D + c0;   // groups of 8 columns, swizzled by row
-        if (row < rows) {
-          if constexpr (!E4M3) {
+        for (int c = 0; c < 2; ++c) {
+          float sum = l[i][c];
 #pragma unroll
-            for (int i = 0; i < DO / 8; ++i)
-              *reinterpret_cast<float2*>(to + ((i ^ g) * 8 + 2 * quad)) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < DO / 16; ++j)
-              *reinterpret_cast<float4*>(to + (((2 * j + (quad >> 1)) ^ g) * 8 + 4 * (quad & 1))) =
-                  make_float4(o[2 * j][2 * r], o[2 * j + 1][2 * r], o[2 * j][2 * r + 1], o[2 * j + 1][2 * r + 1]);
+          for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+          if (g == 0) {
+            join_m[kwarp * HEADS + 8 * i + 2 * quad + c] = m[i][c];
+            join_l[kwarp * HEADS + 8 * i + 2 * quad + c] = sum;
           }
         }
-      }
-      __syncthreads();
+      constexpr int JH = S::kJoinHeads;
+      constexpr float kShift = E4M3 ? 4.f : 0.f;
+      float* const buf = reinterpret_cast<float*>(smem + stage * S::kStageBytes);   // [KW][JH][D]
       const bool starts_here = here.t <= s;   // the unit's first tile is in this run
       const bool whole = unit_done && starts_here;
       const int slot = first_piece ? 0 : 1;
-      float* const part = parts_of(p.work, gridDim.x * gridDim.y) + (static_cast<size_t>(block) * 2 + slot) * part_floats(lc.rows, D);
-      for (int i = tid; i < rows * (D / 4); i += kThreads) {
-        const int row = i / (D / 4), c4 = i % (D / 4);
-        float top = -INFINITY;
+      float* const part =
+          parts_of(p.work, gridDim.x * gridDim.y) + (static_cast<size_t>(block) * 2 + slot) * part_floats(lc.rows, D);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, join_m[w * kRows + row]);
-        float sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int h0 = 0; h0 < HEADS; h0 += JH) {
+        if (h0 >= rows) break;
+        __syncthreads();   // every warp has read the stage, or the heads joined before
+        // groups of 8 columns of a head are swizzled by the head
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float lw = join_l[w * kRows + row];
-          const float f = lw == 0.f ? 0.f : ex2_approx(join_m[w * kRows + row] - top);
-          const float4 v = *reinterpret_cast<const float4*>(
-              buf + (w * kRows + row) * D + (((c4 >> 1) ^ (row & 7)) * 8 + (c4 & 1) * 4));
-          sum = fmaf(f, lw, sum);
-          acc.x = fmaf(f, v.x, acc.x);
-          acc.y = fmaf(f, v.y, acc.y);
-          acc.z = fmaf(f, v.z, acc.z);
-          acc.w = fmaf(f, v.w, acc.w);
-        }
-        if (whole) {
-          const float vs = p.kv.v_scale ? __ldg(p.kv.v_scale + here.hk) : 1.f;
-          const float inv = sum == 0.f ? 0.f : vs / sum;
-          const long long at = static_cast<long long>(here.b) * p.heads + here.hk * G + row0 + row;
-          uint2 out;
-          out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-          out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-          *reinterpret_cast<uint2*>(p.o + at * D + c4 * 4) = out;
-          if (p.lse && c4 == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top - (E4M3 ? 8.f : 0.f) + __log2f(sum)) * kLn2;
-        } else {
-          *reinterpret_cast<float2*>(part + row * D + c4 * 4) = make_float2(acc.x, acc.y);
-          *reinterpret_cast<float2*>(part + row * D + c4 * 4 + 2) = make_float2(acc.z, acc.w);
-          if (c4 == 0) {
-            part[lc.rows * D + row] = top;
-            part[lc.rows * D + lc.rows + row] = sum;
+        for (int i = h0 / 8; i < (h0 + JH < HEADS ? h0 + JH : HEADS) / 8; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float* const to = buf + (kwarp * JH + 8 * i - h0 + 2 * quad + c) * D;
+#pragma unroll
+            for (int j = 0; j < DO / 16; ++j) {
+              const int col = c0 + 16 * j;
+              if constexpr (!E4M3) {
+                to[((((col >> 3) ^ quad) << 3) | g)] = o[i][j][c];
+                to[(((((col >> 3) + 1) ^ quad) << 3) | g)] = o[i][j][2 + c];
+              } else {
+                *reinterpret_cast<float2*>(to + (((((col >> 3) + (g >> 2)) ^ quad) << 3) | ((g & 3) * 2))) =
+                    make_float2(o[i][j][c], o[i][j][2 + c]);
+              }
+            }
+          }
+        __syncthreads();
+        const int heads = min(rows - h0, JH);
+        for (int i = tid; i < heads * (D / 4); i += kThreads) {
+          const int local = i / (D / 4), row = h0 + local, c4 = i % (D / 4);
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < KW; ++w) top = fmaxf(top, join_m[w * HEADS + row]);
+          float sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < KW; ++w) {
+            const float lw = join_l[w * HEADS + row];
+            const float f = lw == 0.f ? 0.f : ex2_approx(join_m[w * HEADS + row] - top);
+            const float4 v = *reinterpret_cast<const float4*>(
+                buf + (w * JH + local) * D + ((((c4 >> 1) ^ ((row >> 1) & 3)) << 3) | ((c4 & 1) << 2)));
+            sum = fmaf(f, lw, sum);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+          }
+          top -= kShift;
+          if (whole) {
+            const float vs = p.kv.v_scale ? __ldg(p.kv.v_scale + here.hk) : 1.f;
+            const float inv = sum == 0.f ? 0.f : vs / sum;
+            const long long at = static_cast<long long>(here.b) * p.heads + here.hk * G + row0 + row;
+            uint2 out;
+            out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+            out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(p.o + at * D + c4 * 4) = out;
+            if (p.lse && c4 == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+          } else {
+            *reinterpret_cast<float2*>(part + row * D + c4 * 4) = make_float2(acc.x, acc.y);
+            *reinterpret_cast<float2*>(part + row * D + c4 * 4 + 2) = make_float2(acc.z, acc.w);
+            if (c4 == 0) {
+              part[lc.rows * D + row] = top;
+              part[lc.rows * D + lc.rows + row] = sum;
+            }
           }
         }
       }
@@ -696,13 +737,14 @@ __global__ void __launch_bounds__(Shape<D, E4M3, HALF>::kThreads, Shape<D, E4M3,
 // it starts in that run: joins the partial results of the runs the unit lies
 // in, group g of its threads those of runs g, g + GROUPS, ... in one pass
 // with a running maximum, then the groups in order.
-constexpr int kJoinThreads = 256;
+template <int D>
+constexpr int kJoinThreads = D == 256 ? 256 : 128;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParams p, const Launch lc) {
-  constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
+__global__ void __launch_bounds__(kJoinThreads<D>) combine_kernel(const DecodeParams p, const Launch lc) {
+  constexpr int COLS = D / 4, GROUPS = kJoinThreads<D> / COLS;
   __shared__ float s_top[GROUPS], s_sum[GROUPS];
-  __shared__ float4 s_acc[kJoinThreads];
+  __shared__ float4 s_acc[kJoinThreads<D>];
   const int tid = threadIdx.x, run = blockIdx.x;
   const int chunk = blockIdx.y / lc.rows, row = blockIdx.y % lc.rows;
   const int G = p.heads / p.kv.heads_kv;
@@ -717,7 +759,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
   const int col = tid % COLS, group = tid / COLS;
   float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = group; i < n; i += GROUPS) {
     const float* const part =
         parts + (static_cast<size_t>(chunk * lc.blocks + run + i) * 2 + (i == 0 ? first_slot : 0)) * pf;
@@ -761,14 +803,16 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
   out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(p.o + at * D + tid * 4) = out;
-  if (p.lse && tid == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top - (p.kv.e4m3 ? 8.f : 0.f) + __log2f(sum)) * kLn2;
+  if (p.lse && tid == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ launch
-Launch split_heads(int heads, int heads_kv) {
-  const int G = heads / heads_kv;
+// The G query heads of a key/value head in chunks of at most 8 * max NH heads
+// (the registers allow 32, at head_dim 256 16), as equal as can be.
+Launch split_heads(int heads, int heads_kv, int head_dim) {
+  const int G = heads / heads_kv, most = head_dim == 256 ? 16 : 32;
   Launch lc;
-  lc.chunks = (G + kRows - 1) / kRows;
+  lc.chunks = (G + most - 1) / most;
   lc.rows = (G + lc.chunks - 1) / lc.chunks;
   lc.chunks = (G + lc.rows - 1) / lc.rows;
   lc.blocks = 0;
@@ -783,11 +827,11 @@ int sm_count() {
   return n;
 }
 
-template <int D, bool E4M3, bool HALF>
+template <int D, bool E4M3, int NH>
 cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
-  using Sh = Shape<D, E4M3, HALF>;
+  using Sh = Shape<D, E4M3, NH>;
   static std::atomic<unsigned long long> smem_done{0};
-  auto* const kernel = decode_kernel<D, E4M3, HALF>;
+  auto* const kernel = decode_kernel<D, E4M3, NH>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), Sh::kSmem, smem_done);
   if (e != cudaSuccess) return e;
   // At most one block per tile, at most the blocks that are resident at once.
@@ -804,7 +848,7 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(lc.blocks, lc.chunks * lc.rows);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.blockDim = dim3(kJoinThreads<D>);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -816,15 +860,20 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
 
 template <int D, bool E4M3>
 cudaError_t launch_rows(const DecodeParams& p, cudaStream_t s) {
-  const Launch lc = split_heads(p.heads, p.kv.heads_kv);
-  return lc.rows <= 8 ? launch_shape<D, E4M3, true>(p, lc, s) : launch_shape<D, E4M3, false>(p, lc, s);
+  const Launch lc = split_heads(p.heads, p.kv.heads_kv, D);
+  if (lc.rows <= 8) return launch_shape<D, E4M3, 1>(p, lc, s);
+  if constexpr (D < 256) {
+    if (lc.rows > 24) return launch_shape<D, E4M3, 4>(p, lc, s);
+    if (lc.rows > 16) return launch_shape<D, E4M3, 3>(p, lc, s);
+  }
+  return launch_shape<D, E4M3, 2>(p, lc, s);
 }
 
 }  // namespace
 
 size_t decode_workspace_bytes(int batch, int heads, int heads_kv, int head_dim) {
   if (batch == 0) return 0;
-  const Launch lc = split_heads(heads, heads_kv);
+  const Launch lc = split_heads(heads, heads_kv, head_dim);
   const size_t blocks = lc.chunks > kMaxBlocks ? lc.chunks : kMaxBlocks;
   const size_t bytes = blocks * (sizeof(Cut) + 2 * part_floats(lc.rows, head_dim) * sizeof(float));
   return (bytes + 255) / 256 * 256;
