@@ -36,7 +36,7 @@
 namespace fa {
 namespace {
 
-constexpr int kMaxBlocks = 304;   // upper bound of a launch's blocks: 2 on each of 152 SMs
+constexpr int kMaxBlocks = 608;   // upper bound of a launch's blocks: 4 on each of 152 SMs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A warp's reference for the exponents moves only when a score exceeds it by
@@ -49,15 +49,18 @@ template <int D, bool E4M3, int NH>
 struct Shape {
   static constexpr int kElem = E4M3 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
-  static constexpr int kTile = E4M3 || D == 64 ? 128 : 64;   // keys
+  static constexpr int kTile = E4M3 ? 128 : 64;              // keys
   static constexpr int kTileBytes = kTile * kRowBytes;       // of K, and of V
   static constexpr int kStageBytes = 2 * kTileBytes;
-  // Two blocks per SM where two rings of stages and queries fit; with 8 warps
-  // each where the fragments of O and Q fit 128 registers.
+  // Blocks per SM: what shared memory (rings of stages, offsets and queries)
+  // and registers (fragments of O and Q) leave room for.
   static constexpr int kBlocksPerSm =
-      kStageBytes >= 65536 || (kStageBytes >= 32768 && NH > (E4M3 ? 1 : 2)) ? 1 : 2;
-  static constexpr int kStages = kStageBytes >= 65536 || (kStageBytes >= 32768 && kBlocksPerSm == 2) ? 3 : 5;
-  static constexpr int kKeyWarps = kTile == 64 || (kBlocksPerSm == 2 && NH > 2) ? 4 : 8;
+      kStageBytes >= 65536 || (kStageBytes >= 32768 && NH > (E4M3 ? 1 : 2)) ? 1
+      : kStageBytes >= 32768 || NH > 2                                      ? 2
+      : NH > 1 || E4M3                                                      ? 3
+                                                                            : 4;
+  static constexpr int kStages = kStageBytes < 65536 && kBlocksPerSm == 1 ? 5 : 3;
+  static constexpr int kKeyWarps = kTile == 64 || kStageBytes < 32768 ? 4 : 8;
   // Warps over the same keys, each with a part of O's columns (and all of the
   // scores), where 4 warps would be all that an SM runs.
   static constexpr int kSplit = kTile == 64 && kBlocksPerSm == 1 ? 2 : 1;
@@ -326,18 +329,19 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH>::kThreads, Shape<D, E4M3, N
   pdl_launch();
 
   // Page of this thread's key of a tile, and from it the row's offset (bytes,
-  // without the head's; -1: not seen) and the tile's bits of seen keys.
+  // without the head's; top bit: not seen) and the tile's bits of seen keys.
   auto look_up = [&](const Place<TILE>& at) -> int {
     const int key = at.first + at.t * TILE + tid;
     if (tid >= TILE || key >= at.len) return -1;
-    return __ldg(p.table + at.b * p.table_stride + static_cast<unsigned>(key) / static_cast<unsigned>(p.kv.page_size));
+    return __ldg(p.table + at.b * p.table_stride + p.page_div.quotient(key));
   };
   auto store_offset = [&](const Place<TILE>& at, int page, int ring) {
     if (tid >= TILE) return;
     const int key = at.first + at.t * TILE + tid;
     const bool ok = key < at.len && page >= 0 && page < p.kv.num_pages;
+    const int slot = key - p.page_div.quotient(key) * p.kv.page_size;
     offsets[ring * TILE + tid] =
-        ok ? (page * p.kv.page_stride + (static_cast<unsigned>(key) % static_cast<unsigned>(p.kv.page_size)) * p.kv.slot_stride) * S::kElem : -1;
+        ok ? (page * p.kv.page_stride + slot * p.kv.slot_stride) * S::kElem : static_cast<long long>(1ull << 63);
     const uint32_t bits = __ballot_sync(0xffffffffu, ok);
     if (lane == 0) seen[ring * (TILE / 32) + warp] = bits;
   };
@@ -352,8 +356,9 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH>::kThreads, Shape<D, E4M3, N
       const long long off = offsets[ring * TILE + r];
       const uint32_t to = dst + swizzled<RB>(r, piece);
       const bool ok = off >= 0;   // unseen rows are zero-filled: nothing is read
-      cp_async16(to, ok ? static_cast<const void*>(kb + off) : p.q, ok);
-      cp_async16(to + S::kTileBytes, ok ? static_cast<const void*>(vb + off) : p.q, ok);
+      const long long from = off & 0x7fffffffffffffffll;
+      cp_async16(to, kb + from, ok);
+      cp_async16(to + S::kTileBytes, vb + from, ok);
     };
     // Of a tile that is not full, rows are filled up to the end of the last
     // warp's share that has a key; warps without one skip the tile.

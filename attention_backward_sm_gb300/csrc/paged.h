@@ -25,6 +25,21 @@ struct PagedCache {
   int head_dim;
 };
 
+// n / d for 0 <= n < 2^31 by a product: with 2^shift the power of two at or
+// above d and mul = ceil(2^32 (2^shift - d) / d) (+ 1 where exact), the sum
+// n + floor(n mul / 2^32) over 2^shift is exact for all 32-bit n.
+struct FastDiv {
+  uint32_t mul;
+  uint32_t shift;
+  explicit FastDiv(uint32_t d = 1) : shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int quotient(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
+
 struct DecodeParams {
   PagedCache kv;
   const uint16_t* q;      // [batch, heads, d], rows q_row_stride elements apart
@@ -35,6 +50,7 @@ struct DecodeParams {
   uint16_t* o;            // [batch, heads, d]
   float* lse;             // [batch, heads] or nullptr
   float* work;
+  FastDiv page_div;       // by kv.page_size
   int max_pages;
   int batch;
   int heads;
