@@ -1,0 +1,971 @@
+// Attention of one new token per request over a paged key/value cache.
+//
+// For request b, query head h (key/value head h / G, G = heads / heads_kv)
+// and the visible cached keys j in [max(0, len - window), len):
+//     x_j = scale * q . k_j,  o = sum_j exp(x_j) v_j / sum_j exp(x_j),
+//     lse = ln sum_j exp(x_j)
+// Keys whose block-table entry is not a page of the cache are not seen; a
+// row that sees no key gets o = 0, lse = -inf.
+//
+// The call has to read every visible key and value once and does 2 G
+// operations per cached bf16 byte: it is bound by HBM.  So
+//   * the G query heads of a key/value head share one pass over its keys.  They
+//     are the columns of 16 x 8 tensor-core products S^T = K Q^T, O^T += V^T P^T
+//     (keys and dimensions in the rows, so that few heads waste little), which
+//     keeps the arithmetic far below the time of the loads;
+//   * a tile is some keys of HW neighbouring key/value heads, a warp per head
+//     (HW = 4, 2 or 1: the largest that divides heads_kv).  In the packed
+//     layout a slot's heads lie side by side, and read together they are long
+//     pieces of DRAM rows (e4m3, d = 64: 256 bytes instead of 64); the heads
+//     also share the work of finding the rows.  With fewer heads than warps
+//     the warps share the keys and are joined where a unit ends;
+//   * the tiles of all (request, head group) units, in order, are cut into
+//     equal runs, one per resident block.  Ragged lengths, one long request
+//     and many short ones all load every SM alike, and a unit that lies in
+//     several runs leaves at most one partial result per run, which
+//     combine_kernel joins (fixed order: same bits on every call).  The host
+//     needs no lengths.
+//   * K and V rows come through cp.async into a ring of kStages tiles (any
+//     page size and strides; a TMA box would tie the tile to the page), the
+//     block-table entries one tile further ahead.
+// Each warp keeps a running reference and sum for its keys.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "internal.h"
+#include "paged.h"
+#include "sm103.cuh"
+
+namespace fa {
+namespace decode {
+
+constexpr int kMaxBlocks = 608;   // upper bound of a launch's blocks: 4 on each of 152 SMs
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// A warp's reference for the exponents moves only when a score exceeds it by
+// more than kSlack (units of log 2): weights are at most 2^kSlack, and the
+// maximum over the warp is taken a few times per unit instead of every tile.
+constexpr float kSlack = 8.f;
+
+// NH: groups of 8 query heads per key/value head; HW: key/value heads per tile.
+template <int D, bool E4M3, int NH, int HW>
+struct Shape {
+  static constexpr int kElem = E4M3 ? 1 : 2;
+  static constexpr int kRowBytes = D * kElem;
+  static constexpr int kRowsPerTile = E4M3 && D != 128 ? 128 : 64;   // heads x keys
+  static constexpr int kTile = kRowsPerTile / HW;                    // keys
+  static constexpr int kHeadBytes = kTile * kRowBytes;
+  static constexpr int kTileBytes = kRowsPerTile * kRowBytes;        // of K, and of V
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  // Blocks per SM: what shared memory (the ring of stages) and registers
+  // (fragments of O and Q) leave room for.
+  static constexpr int kBlocksPerSm = kStageBytes >= 65536 || (kStageBytes >= 32768 && NH > 2) ? 1
+                                      : kStageBytes >= 32768 || NH > 2                         ? 2
+                                      : NH > 1 || E4M3                                         ? 3
+                                                                                               : 4;
+  static constexpr int kStages = kStageBytes < 65536 && kBlocksPerSm == 1 ? 6 : 3;
+  static constexpr int kRowWarps = kStageBytes >= 65536 && E4M3 ? 8 : 4;   // warps over a tile's rows
+  static constexpr int kKeyWarps = kRowWarps / HW;
+  static constexpr int kKeys = kTile / kKeyWarps;                          // of a warp
+  // Warps over the same rows, each with a part of O's columns (and all of the
+  // scores), where 4 warps would be all that an SM runs.
+  static constexpr int kSplit = kRowWarps == 4 && kBlocksPerSm == 1 ? 2 : 1;
+  static constexpr int kThreads = kRowWarps * kSplit * 32;
+  static constexpr int kHeads = 8 * NH;
+  static constexpr int kOffsets = kStages + 1;               // tiles whose row offsets are kept
+  // Key warps' O are joined in the stage just consumed, so many heads at a time.
+  static constexpr int kJoinFit = kStageBytes / (kRowWarps * D * 4) / 8 * 8;
+  static constexpr int kJoinHeads = kJoinFit < kHeads ? kJoinFit : kHeads;
+  static constexpr int kSeenWords = (kTile + 31) / 32;
+  static constexpr int kOffOffsets = kStages * kStageBytes;
+  static constexpr int kOffSeen = kOffOffsets + kOffsets * kTile * 8;
+  static constexpr int kOffJoin = kOffSeen + kOffsets * kSeenWords * 4;
+  static constexpr int kOffScan = kOffJoin + (kKeyWarps > 1 ? 2 * kRowWarps * kHeads * 4 : 0);
+  static constexpr int kSmem = kOffScan + kThreads / 32 * 4 + 16;
+  static_assert(kJoinHeads >= 8, "join buffer");
+  static_assert(kKeys == 16 || kKeys == 32, "a word of seen keys");
+  static_assert(kTile <= kThreads && kTile % 16 == 0, "a thread per key looks up its page");
+  static_assert(kBlocksPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
+};
+
+// A unit that the end of the run it starts in cuts, if any: runs [run, last]
+// hold its partial results, in run's slot `slot` and the others' slot 0.  One
+// entry per unit, or where there are more units than runs, one per run.
+struct Cut {
+  int unit;    // b * (heads_kv / HW) + head group, or -1: none
+  int run;
+  int last;
+  int slot;
+};
+
+struct Launch {
+  int rows;        // query heads of a key/value head per chunk (at most 8 NH)
+  int chunks;      // chunks of the G query heads of a key/value head
+  int group;       // key/value heads per tile
+  int blocks;      // blocks per chunk
+  int by_unit;     // cuts are entered by unit
+};
+
+// Workspace: [blocks] cuts, then partial results [blocks][2 slots]: [HW][rows]
+// of D sums of p v, then [HW][rows] references and [HW][rows] sums of p.
+__host__ __device__ inline float* parts_of(float* work, size_t blocks) {
+  return reinterpret_cast<float*>(reinterpret_cast<Cut*>(work) + blocks);
+}
+
+__host__ __device__ inline size_t part_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;   // fewer source bytes than 16: the rest is zero-filled
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// Transposes an 8 x 8 matrix of 16-bit elements held two per lane.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// Word w of lane q of a quad becomes word q of lane w.
+__device__ __forceinline__ void transpose_quad(int q, uint32_t& v0, uint32_t& v1, uint32_t& v2, uint32_t& v3) {
+  const bool odd = q & 1, high = q & 2;
+  const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1), b = __shfl_xor_sync(0xffffffffu, odd ? v2 : v3, 1);
+  (odd ? v0 : v1) = a;
+  (odd ? v2 : v3) = b;
+  const uint32_t c = __shfl_xor_sync(0xffffffffu, high ? v0 : v2, 2), d = __shfl_xor_sync(0xffffffffu, high ? v1 : v3, 2);
+  (high ? v0 : v2) = c;
+  (high ? v1 : v3) = d;
+}
+// c += a b, 16 x 8 x 16, fp32 accumulate; operands bf16 or fp16.
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two 8-bit values to two halves (exact), from bits 0-15 or 16-31.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+// Programmatic dependent launch: the next kernel of the stream may be set up
+// from here on; it waits for this one's end (and its writes) in pdl_wait.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Byte offset of 16-byte piece c of row r in a tile whose rows are RB bytes,
+// so that eight consecutive rows' pieces c lie in different banks.
+template <int RB>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  if constexpr (RB >= 128) return r * RB + ((c ^ (r & 7)) << 4);
+  else return r * RB + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// ------------------------------------------------------------------ partition
+struct Lens {
+  const int32_t* seq;
+  int most;      // max_pages * page_size
+  int window;
+  __device__ __forceinline__ int len(int b) const { return min(max(__ldg(seq + b), 0), most); }
+  __device__ __forceinline__ int first(int len) const { return window > 0 ? max(0, len - window) : 0; }
+  // A request without keys has one (empty) tile: its row is written too.
+  template <int TILE>
+  __device__ __forceinline__ int tiles(int len) const {
+    return max(1, (len - first(len) + TILE - 1) / TILE);
+  }
+};
+
+// The list of all tiles (requests in order, the head groups of each, the
+// tiles of each) cut into `runs` runs, none empty, that differ by one at most.
+struct Runs {
+  int total, runs, base, rem;
+  __device__ __forceinline__ Runs(int total_, int blocks) : total(total_), runs(min(total_, blocks)) {
+    base = static_cast<unsigned>(total) / static_cast<unsigned>(runs);
+    rem = total - base * runs;
+  }
+  __device__ __forceinline__ int start(int c) const { return c * base + min(c, rem); }
+  // The run that holds tile x.
+  __device__ __forceinline__ int of(int x) const {
+    const int y = x - rem * (base + 1);
+    return y < 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(base + 1)
+                 : rem + static_cast<unsigned>(y) / static_cast<unsigned>(base);
+  }
+};
+
+// Tiles of all requests before those of this thread, of its own (requests
+// [b0, b1)) and in all, by a scan over the block.  scan: a word per warp.
+template <int TILE, int THREADS>
+struct Scan {
+  int b0, b1, before, mine, total;
+  __device__ __forceinline__ Scan(const Lens& L, int batch, int groups, int* scan) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (batch + THREADS - 1) / THREADS;
+    b0 = min(tid * per, batch);
+    b1 = min(b0 + per, batch);
+    mine = 0;
+    for (int b = b0; b < b1; ++b) mine += L.tiles<TILE>(L.len(b));
+    mine *= groups;
+    int upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += x;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) upto += scan[w];
+      total += scan[w];
+    }
+    before = upto - mine;
+  }
+  // The thread whose requests hold tile x writes the tile's request, head
+  // group, place and the request's length to found[4].
+  __device__ __forceinline__ void find(const Lens& L, int groups, int x, int* found) const {
+    if (x < before || x >= before + mine) return;
+    int at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int len = L.len(b), nt = L.tiles<TILE>(len);
+      if (x < at + nt * groups) {
+        const unsigned in = x - at;
+        found[0] = b;
+        found[1] = in / static_cast<unsigned>(nt);
+        found[2] = in % static_cast<unsigned>(nt);
+        found[3] = len;
+        return;
+      }
+      at += nt * groups;
+    }
+  }
+};
+
+// A place in the list of tiles: tile t of nt of (request b, head group hk).
+template <int TILE>
+struct Place {
+  int b, hk, t, nt, first, len;
+  __device__ __forceinline__ void request(const Lens& L, int length) {
+    len = length;
+    first = L.first(len);
+    nt = L.tiles<TILE>(len);
+  }
+  __device__ __forceinline__ void next(const Lens& L, int batch, int groups) {
+    if (++t < nt) return;
+    t = 0;
+    if (++hk < groups) return;
+    hk = 0;
+    if (++b < batch) request(L, L.len(b));
+  }
+};
+
+// ------------------------------------------------------------------ main kernel
+template <int D, bool E4M3, int NH, int HW>
+__global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M3, NH, HW>::kBlocksPerSm)
+    decode_kernel(const DecodeParams p, const Launch lc) {
+  using S = Shape<D, E4M3, NH, HW>;
+  constexpr int TILE = S::kTile, RB = S::kRowBytes, ST = S::kStages, kThreads = S::kThreads;
+  constexpr int KW = S::kKeyWarps, HEADS = S::kHeads;
+  constexpr int KT = S::kKeys / 16;  // a warp's keys, in rows of the products
+  constexpr int DO = D / S::kSplit;  // columns of O of a warp
+  constexpr float kShift = E4M3 ? 4.f : 0.f;   // of the weights' exponents
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint32_t sbase = smem_u32(smem);
+  long long* const offsets = reinterpret_cast<long long*>(smem + S::kOffOffsets);
+  uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + S::kOffSeen);
+  int* const scan = reinterpret_cast<int*>(smem + S::kOffScan);   // [warps]
+  int* const found = scan + kThreads / 32;                        // b, hk, t, length
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp's key/value head of a tile, its part of the keys, its first column of O
+  const int hw = warp % HW, kwarp = warp / HW % KW, c0 = warp / S::kRowWarps * DO;
+  const int G = p.heads / p.kv.heads_kv, groups = p.kv.heads_kv / HW;
+  const int row0 = blockIdx.y * lc.rows;                 // first query head of this chunk within its group
+  const int rows = min(lc.rows, G - row0);
+  const int block = blockIdx.y * lc.blocks + blockIdx.x;
+  const Lens L{p.seq_lens, p.max_pages * p.kv.page_size, p.window};
+
+  // The run of this block: every block counts all tiles, then finds where
+  // its share starts.
+  const Scan<TILE, kThreads> tiles(L, p.batch, groups, scan);
+  const Runs runs(tiles.total, lc.blocks);
+  int4* const cuts = reinterpret_cast<int4*>(p.work) + blockIdx.y * lc.blocks;
+  if (static_cast<int>(blockIdx.x) >= runs.runs) {
+    if (!lc.by_unit && tid == 0) cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  const int start = runs.start(blockIdx.x), n = runs.start(blockIdx.x + 1) - start;
+  tiles.find(L, groups, start, found);
+  __syncthreads();
+  Place<TILE> here;   // the tile being computed
+  here.b = found[0];
+  here.hk = found[1];
+  here.t = found[2];
+  here.request(L, found[3]);
+  Place<TILE> ahead = here;   // the next tile to load
+  pdl_launch();
+
+  // Page of this thread's key of a tile, and from it the row's offset (bytes,
+  // without the head's; top bit: not seen) and the tile's bits of seen keys.
+  auto look_up = [&](const Place<TILE>& at) -> int {
+    const int key = at.first + at.t * TILE + tid;
+    if (tid >= TILE || key >= at.len) return -1;
+    return __ldg(p.table + at.b * p.table_stride + p.page_div.quotient(key));
+  };
+  auto store_offset = [&](const Place<TILE>& at, int page, int ring) {
+    if (tid >= TILE) return;
+    const int key = at.first + at.t * TILE + tid;
+    const bool ok = key < at.len && page >= 0 && page < p.kv.num_pages;
+    const int slot = key - p.page_div.quotient(key) * p.kv.page_size;
+    offsets[ring * TILE + tid] =
+        ok ? (page * p.kv.page_stride + slot * p.kv.slot_stride) * S::kElem : static_cast<long long>(1ull << 63);
+    const uint32_t bits = __ballot_sync(TILE < 32 ? (1u << (TILE & 31)) - 1u : 0xffffffffu, ok);
+    if (lane == 0) seen[ring * S::kSeenWords + warp] = bits;
+  };
+  // 16-byte pieces of a key's row of a tile (all heads), keys per pass
+  constexpr int CPR = RB / 16, PIECES = HW * CPR, KPP = kThreads / PIECES;
+  const int piece_head = tid % PIECES / CPR, piece = tid % CPR, key_in_pass = tid / PIECES;
+  auto load_tile = [&](const Place<TILE>& at, int ring, int stage) {
+    const long long head = (at.hk * HW + piece_head) * p.kv.head_stride * S::kElem + piece * 16;
+    const unsigned char* const kb = static_cast<const unsigned char*>(p.kv.k) + head;
+    const unsigned char* const vb = static_cast<const unsigned char*>(p.kv.v) + head;
+    const uint32_t dst = sbase + stage * S::kStageBytes + piece_head * S::kHeadBytes;
+    auto load_row = [&](int r) {
+      const long long off = offsets[ring * TILE + r];
+      const uint32_t to = dst + swizzled<RB>(r, piece);
+      const bool ok = off >= 0;   // unseen rows are zero-filled: nothing is read
+      const long long from = off & 0x7fffffffffffffffll;
+      cp_async16(to, kb + from, ok);
+      cp_async16(to + S::kTileBytes, vb + from, ok);
+    };
+    // Of a tile that is not full, rows are filled up to the end of the last
+    // warp's share that has a key; warps without one skip the tile.
+    const int keys = at.len - at.first - at.t * TILE;
+    if (keys >= TILE) {
+#pragma unroll
+      for (int i = 0; i < (TILE + KPP - 1) / KPP; ++i)
+        if (TILE % KPP == 0 || key_in_pass + i * KPP < TILE) load_row(key_in_pass + i * KPP);
+    } else {
+      const int end = (keys + S::kKeys - 1) / S::kKeys * S::kKeys;
+      for (int r = key_in_pass; r < end; r += KPP) load_row(r);
+    }
+  };
+
+  // Prologue: the first ST - 1 tiles are on their way before the loop.
+  {
+    Place<TILE> load = here;
+    int pages[ST - 1];   // looked up together: one trip to memory
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) {
+      pages[i] = -1;
+      if (i < n) {
+        pages[i] = look_up(ahead);
+        ahead.next(L, p.batch, groups);
+      }
+    }
+    Place<TILE> at = here;
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) {
+      if (i < n) {
+        store_offset(at, pages[i], i);
+        at.next(L, p.batch, groups);
+      }
+    }
+    __syncthreads();
+    for (int i = 0; i < ST - 1; ++i) {
+      if (i < n) {
+        load_tile(load, i, i);
+        load.next(L, p.batch, groups);
+      }
+      cp_commit();
+    }
+  }
+  int page_ahead = ST - 1 < n ? look_up(ahead) : -1;
+
+  // Per lane (g, quad): keys or dimensions g and g + 8 of 16, heads 2 quad and
+  // 2 quad + 1 of 8.
+  uint32_t qf[NH][D / 16][2];               // Q^T fragments (e4m3: fp16, rescaled per head)
+  float o[NH][DO / 16][4];
+  float m[NH][2], l[NH][2], factor[NH][2];  // reference, this lane's sum, scores to units of log 2
+  int stage = 0, ring = 0;
+  int load_stage = ST - 1, load_ring = ST - 1;
+  bool fresh = true, first_piece = true;
+  const int g = lane >> 2, quad = lane & 3;
+
+  for (int s = 0; s < n; ++s) {
+    if (fresh) {   // the unit's queries, on their way while the tile is waited for
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        const uint16_t* const q =
+            p.q + here.b * p.q_row_stride + ((here.hk * HW + hw) * G + row0 + 8 * i + g) * D + quad * (E4M3 ? 4 : 8);
+        const bool have = 8 * i + g < rows;
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const uint2 v = have ? *reinterpret_cast<const uint2*>(q + 16 * j) : make_uint2(0u, 0u);
+            qf[i][j][0] = v.x;
+            qf[i][j][1] = v.y;
+          }
+        } else {
+          // 16 bytes per lane, of which a quad's lanes want each other's words
+          // (transposed where the unit starts)
+#pragma unroll
+          for (int j = 0; j < D / 16; j += 2) {
+            const uint4 v = have ? *reinterpret_cast<const uint4*>(q + 16 * j) : make_uint4(0u, 0u, 0u, 0u);
+            qf[i][j][0] = v.x;
+            qf[i][j][1] = v.y;
+            qf[i][j + 1][0] = v.z;
+            qf[i][j + 1][1] = v.w;
+          }
+        }
+      }
+    }
+    cp_wait<ST - 2>();
+    const bool more = s + ST - 1 < n;
+    if (more) store_offset(ahead, page_ahead, load_ring);
+    __syncthreads();   // tile s has landed for every thread; tile s - 1's stage is free
+    if (more) {
+      load_tile(ahead, load_ring, load_stage);
+      ahead.next(L, p.batch, groups);
+      if (s + ST < n) page_ahead = look_up(ahead);
+      load_stage = load_stage + 1 == ST ? 0 : load_stage + 1;
+      load_ring = load_ring + 1 == S::kOffsets ? 0 : load_ring + 1;
+    }
+    cp_commit();
+
+    if (fresh) {
+      fresh = false;
+      const float scale = p.scale * kLog2e * (p.kv.k_scale ? __ldg(p.kv.k_scale + here.hk * HW + hw) : 1.f);
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          m[i][c] = -INFINITY;
+          l[i][c] = 0.f;
+          factor[i][c] = scale;
+        }
+#pragma unroll
+        for (int j = 0; j < DO / 16; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[i][j][c] = 0.f;
+        if constexpr (!E4M3) {
+#pragma unroll
+          for (int j = 0; j < D / 16; j += 2)
+            transpose_quad(quad, qf[i][j][0], qf[i][j][1], qf[i][j + 1][0], qf[i][j + 1][1]);
+        } else {
+          // A lane's four bytes of a K row are four consecutive dimensions;
+          // they serve as the products' k = 2 quad, + 1, + 8, + 9, and the query
+          // is laid out alike.  It is held in fp16, which its bf16 values fit
+          // once each row is scaled by a power of two that brings its largest
+          // element to [2^14, 2^15): exact but for elements 2^-28 below it.
+          float top = 0.f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              top = fmaxf(top, fmaxf(fabsf(bf_lo(qf[i][j][c])), fabsf(bf_hi(qf[i][j][c]))));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = static_cast<int>(__float_as_uint(top) >> 23);
+          const int up = e == 255 ? 127 : min(268 - max(e, 1), 253);   // biased exponent of the power
+          const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+          const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) qf[i][j][c] = pack_f16x2(bf_lo(qf[i][j][c]) * f, bf_hi(qf[i][j][c]) * f);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) factor[i][c] *= __shfl_sync(0xffffffffu, back, (2 * quad + c) * 4);
+        }
+      }
+    }
+
+    const uint32_t kt = sbase + stage * S::kStageBytes + hw * S::kHeadBytes, vt = kt + S::kTileBytes;
+    const int key0 = kwarp * S::kKeys;
+    uint32_t bits = seen[ring * S::kSeenWords + (key0 >> 5)] >> (key0 & 31);
+    if constexpr (S::kKeys == 16) bits &= 0xffffu;
+    if (bits != 0u) {
+      // S^T = K Q^T for the warp's keys; with few products at a time, in two
+      // chains of half the dimensions each.
+      constexpr int CH = NH * KT == 1 ? 2 : 1;
+      float x[KT][NH][4], x2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int i = 0; i < NH; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[k][i][c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 16; j += 2) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          const int r = key0 + 16 * k + (lane & 15);
+          uint32_t a0[4], a1[4];   // dimensions 16 j + [0, 16) and + [16, 32)
+          if constexpr (!E4M3) {
+            ldsm4(a0, kt + swizzled<RB>(r, 2 * j + (lane >> 4)));
+            ldsm4(a1, kt + swizzled<RB>(r, 2 * j + 2 + (lane >> 4)));
+          } else {
+            uint32_t b[4];
+            ldsm4(b, kt + swizzled<RB>(r, j + (lane >> 4)));
+            a0[0] = e4m3_lo(b[0]);
+            a0[1] = e4m3_lo(b[1]);
+            a0[2] = e4m3_hi(b[0]);
+            a0[3] = e4m3_hi(b[1]);
+            a1[0] = e4m3_lo(b[2]);
+            a1[1] = e4m3_lo(b[3]);
+            a1[2] = e4m3_hi(b[2]);
+            a1[3] = e4m3_hi(b[3]);
+          }
+#pragma unroll
+          for (int i = 0; i < NH; ++i) {
+            mma<E4M3>(x[k][i], a0, qf[i][j][0], qf[i][j][1]);
+            mma<E4M3>(CH == 2 ? x2 : x[k][i], a1, qf[i][j + 1][0], qf[i][j + 1][1]);
+          }
+        }
+      }
+      if constexpr (CH == 2) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[0][0][c] += x2[c];
+      }
+      // Weights 2^(x factor - m + kShift), unseen keys 0.  In fp16 (e4m3 caches)
+      // they carry 2^kShift so that none above 2^-18 of the reference is subnormal.
+      bool keep = true;
+      float y[KT][NH][4];
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int i = 0; i < NH; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            y[k][i][c] = fmaf(x[k][i][c], factor[i][c & 1], kShift - m[i][c & 1]);
+            if (bits != (S::kKeys == 16 ? 0xffffu : 0xffffffffu) && !((bits >> (16 * k + 8 * (c >> 1) + g)) & 1u))
+              y[k][i][c] = -INFINITY;
+            keep = keep && y[k][i][c] <= kSlack + kShift;
+          }
+      if (!__all_sync(0xffffffffu, keep)) {
+        // Some score is past the slack (the first tile always): new reference.
+#pragma unroll
+        for (int i = 0; i < NH; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = m[i][c];
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                if ((bits >> (16 * k + 8 * u + g)) & 1u) top = fmaxf(top, x[k][i][2 * u + c] * factor[i][c]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float f = top == m[i][c] ? 1.f : ex2_approx(m[i][c] - top);
+            m[i][c] = top;
+            l[i][c] *= f;
+#pragma unroll
+            for (int j = 0; j < DO / 16; ++j) {
+              o[i][j][c] *= f;
+              o[i][j][2 + c] *= f;
+            }
+            const float ref = kShift - (top == -INFINITY ? 0.f : top);
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                y[k][i][2 * u + c] = (bits >> (16 * k + 8 * u + g)) & 1u
+                                         ? fmaf(x[k][i][2 * u + c], factor[i][c], ref) : -INFINITY;
+          }
+      }
+      // P^T, rounded to 16 bits for the second product, summed in 32.
+      uint32_t pf[KT][NH][2];
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) e[c] = ex2_approx(y[k][i][c]);
+          l[i][0] += e[0] + e[2];
+          l[i][1] += e[1] + e[3];
+          pf[k][i][0] = transposed(E4M3 ? pack_f16x2(e[0], e[1]) : pack_bf16x2(e[0], e[1]));
+          pf[k][i][1] = transposed(E4M3 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]));
+        }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const int r = key0 + 16 * k;
+        if constexpr (!E4M3) {
+#pragma unroll
+          for (int j = 0; j < DO / 16; ++j) {
+            uint32_t a[4];
+            ldsm4t(a, vt + swizzled<RB>(r + (lane & 7) + ((lane >> 4) << 3), c0 / 8 + 2 * j + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int i = 0; i < NH; ++i) mma<false>(o[i][j], a, pf[k][i][0], pf[k][i][1]);
+          }
+        } else {
+          // Transposed as 16-bit units, a register holds two keys' bytes of two
+          // neighbouring dimensions: rows g and g + 8 of the product are
+          // dimensions 2 g and 2 g + 1.
+#pragma unroll
+          for (int j = 0; j < DO / 16; j += 2) {
+            uint32_t b[4];
+            ldsm4t(b, vt + swizzled<RB>(r + (lane & 15), c0 / 16 + j + (lane >> 4)));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t even = __byte_perm(b[2 * u], b[2 * u + 1], 0x6420);
+              const uint32_t odd = __byte_perm(b[2 * u], b[2 * u + 1], 0x7531);
+              const uint32_t a[4] = {e4m3_lo(even), e4m3_lo(odd), e4m3_hi(even), e4m3_hi(odd)};
+#pragma unroll
+              for (int i = 0; i < NH; ++i) mma<true>(o[i][j + u], a, pf[k][i][0], pf[k][i][1]);
+            }
+          }
+        }
+      }
+    }
+
+    const bool unit_done = here.t + 1 == here.nt;
+    if (unit_done || s + 1 == n) {
+      // This warp's sums; with several key warps, joined in the stage just
+      // consumed, else written from the registers.
+      const bool starts_here = here.t <= s;   // the unit's first tile is in this run
+      const bool whole = unit_done && starts_here;
+      const int slot = first_piece ? 0 : 1;
+      const long long out_row = static_cast<long long>(here.b) * p.heads + here.hk * HW * G + row0;   // of the first head
+      float* const part = parts_of(p.work, gridDim.x * gridDim.y) +
+                          (static_cast<size_t>(block) * 2 + slot) * part_floats(HW * lc.rows, D);
+#pragma unroll
+      for (int i = 0; i < NH; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) l[i][c] += __shfl_xor_sync(0xffffffffu, l[i][c], off);
+      if constexpr (KW == 1) {
+        const float vs = p.kv.v_scale ? __ldg(p.kv.v_scale + here.hk * HW + hw) : 1.f;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          float inv[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            inv[c] = l[i][c] == 0.f ? 0.f : __fdividef(vs, l[i][c]);
+            const int row = 8 * i + 2 * quad + c;
+            if (g == 0 && c0 == 0 && row < rows) {
+              if (!whole) {
+                part[HW * lc.rows * D + hw * lc.rows + row] = m[i][c] - kShift;
+                part[HW * lc.rows * D + (HW + hw) * lc.rows + row] = l[i][c];
+              } else if (p.lse) {
+                p.lse[out_row + hw * G + row] =
+                    l[i][c] == 0.f ? -INFINITY : (m[i][c] - kShift + __log2f(l[i][c])) * kLn2;
+              }
+            }
+          }
+          if (whole) {
+            // transposed to heads in the lanes' rows
+            const bool have = 8 * i + g < rows;
+            uint16_t* const to = p.o + (out_row + hw * G + 8 * i + g) * D + c0;
+#pragma unroll
+            for (int j = 0; j < DO / 16; ++j) {
+              const uint32_t t0 = transposed(pack_bf16x2(o[i][j][0] * inv[0], o[i][j][1] * inv[1]));
+              const uint32_t t1 = transposed(pack_bf16x2(o[i][j][2] * inv[0], o[i][j][3] * inv[1]));
+              if (have) {
+                if constexpr (E4M3) {
+                  *reinterpret_cast<uint2*>(to + 16 * j + 4 * quad) =
+                      make_uint2(__byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632));
+                } else {
+                  *reinterpret_cast<uint32_t*>(to + 16 * j + 2 * quad) = t0;
+                  *reinterpret_cast<uint32_t*>(to + 16 * j + 8 + 2 * quad) = t1;
+                }
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int row = 8 * i + 2 * quad + c;
+              float* const to = part + (hw * lc.rows + row) * D + c0;
+              if (row < rows) {
+#pragma unroll
+                for (int j = 0; j < DO / 16; ++j) {
+                  if constexpr (E4M3) {
+                    *reinterpret_cast<float2*>(to + 16 * j + 2 * g) = make_float2(o[i][j][c], o[i][j][2 + c]);
+                  } else {
+                    to[16 * j + g] = o[i][j][c];
+                    to[16 * j + 8 + g] = o[i][j][2 + c];
+                  }
+                }
+              }
+            }
+          }
+        }
+      } else {
+        constexpr int JH = S::kJoinHeads;
+        float* const join_m = reinterpret_cast<float*>(smem + S::kOffJoin);   // [HW][KW][HEADS]
+        float* const join_l = join_m + S::kRowWarps * HEADS;
+        float* const buf = reinterpret_cast<float*>(smem + stage * S::kStageBytes);   // [HW][KW][JH][D]
+        const int at = hw * KW + kwarp;
+#pragma unroll
+        for (int i = 0; i < NH; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (g == 0) {
+              join_m[at * HEADS + 8 * i + 2 * quad + c] = m[i][c];
+              join_l[at * HEADS + 8 * i + 2 * quad + c] = l[i][c];
+            }
+#pragma unroll
+        for (int h0 = 0; h0 < HEADS; h0 += JH) {
+          if (h0 >= rows) break;
+          __syncthreads();   // every warp has read the stage, or the heads joined before
+          // groups of 8 columns of a head are swizzled by the head
+#pragma unroll
+          for (int i = h0 / 8; i < (h0 + JH < HEADS ? h0 + JH : HEADS) / 8; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float* const to = buf + (at * JH + 8 * i - h0 + 2 * quad + c) * D;
+#pragma unroll
+              for (int j = 0; j < DO / 16; ++j) {
+                const int col = c0 + 16 * j;
+                if constexpr (!E4M3) {
+                  to[((((col >> 3) ^ quad) << 3) | g)] = o[i][j][c];
+                  to[(((((col >> 3) + 1) ^ quad) << 3) | g)] = o[i][j][2 + c];
+                } else {
+                  *reinterpret_cast<float2*>(to + (((((col >> 3) + (g >> 2)) ^ quad) << 3) | ((g & 3) * 2))) =
+                      make_float2(o[i][j][c], o[i][j][2 + c]);
+                }
+              }
+            }
+          __syncthreads();
+          const int heads = min(rows - h0, JH);
+          for (int i = tid; i < HW * heads * (D / 4); i += kThreads) {
+            const int c4 = i % (D / 4), local = i / (D / 4) % heads, h = i / (D / 4) / heads, row = h0 + local;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < KW; ++w) top = fmaxf(top, join_m[(h * KW + w) * HEADS + row]);
+            float sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+              const float lw = join_l[(h * KW + w) * HEADS + row];
+              const float f = lw == 0.f ? 0.f : ex2_approx(join_m[(h * KW + w) * HEADS + row] - top);
+              const float4 v = *reinterpret_cast<const float4*>(
+                  buf + ((h * KW + w) * JH + local) * D + ((((c4 >> 1) ^ ((row >> 1) & 3)) << 3) | ((c4 & 1) << 2)));
+              sum = fmaf(f, lw, sum);
+              acc.x = fmaf(f, v.x, acc.x);
+              acc.y = fmaf(f, v.y, acc.y);
+              acc.z = fmaf(f, v.z, acc.z);
+              acc.w = fmaf(f, v.w, acc.w);
+            }
+            top -= kShift;
+            if (whole) {
+              const float vs = p.kv.v_scale ? __ldg(p.kv.v_scale + here.hk * HW + h) : 1.f;
+              const float inv = sum == 0.f ? 0.f : __fdividef(vs, sum);
+              const long long to = out_row + h * G + row;
+              uint2 out;
+              out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+              out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+              *reinterpret_cast<uint2*>(p.o + to * D + c4 * 4) = out;
+              if (p.lse && c4 == 0) p.lse[to] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+            } else {
+              float2* const to = reinterpret_cast<float2*>(part + (h * lc.rows + row) * D + c4 * 4);
+              to[0] = make_float2(acc.x, acc.y);
+              to[1] = make_float2(acc.z, acc.w);
+              if (c4 == 0) {
+                part[HW * lc.rows * D + h * lc.rows + row] = top;
+                part[HW * lc.rows * D + (HW + h) * lc.rows + row] = sum;
+              }
+            }
+          }
+        }
+      }
+      if (tid == 0 && (lc.by_unit ? starts_here : s + 1 == n)) {
+        const int unit = here.b * groups + here.hk;
+        cuts[lc.by_unit ? unit : blockIdx.x] =
+            make_int4(starts_here && !unit_done ? unit : -1, blockIdx.x, runs.of(start + s - here.t + here.nt - 1), slot);
+      }
+      fresh = true;
+      first_piece = false;
+    }
+    here.next(L, p.batch, groups);
+    stage = stage + 1 == ST ? 0 : stage + 1;
+    ring = ring + 1 == S::kOffsets ? 0 : ring + 1;
+  }
+}
+
+// ------------------------------------------------------------------ combine
+// One block per (cut, query head of a head group): joins the partial results
+// of the runs the unit lies in, group g of its threads those of runs g,
+// g + groups, ... in one pass with a running maximum, then the groups in order.
+constexpr int kMostGroups = 16;
+
+template <int D>
+__global__ void __launch_bounds__(D / 4 * kMostGroups) combine_kernel(const DecodeParams p, const Launch lc) {
+  constexpr int COLS = D / 4;
+  __shared__ float s_top[kMostGroups], s_sum[kMostGroups];
+  extern __shared__ float4 s_acc[];   // [threads]
+  const int tid = threadIdx.x, join_groups = blockDim.x / COLS;
+  const int local = blockIdx.y % (lc.group * lc.rows), chunk = blockIdx.y / (lc.group * lc.rows);
+  const int head = local / lc.rows, row = local % lc.rows;   // of the group; of the head's chunk
+  const int G = p.heads / p.kv.heads_kv;
+  pdl_wait();
+  if (chunk * lc.rows + row >= G) return;
+  const int4 cut = *(reinterpret_cast<const int4*>(p.work) + chunk * lc.blocks + blockIdx.x);
+  if (cut.x < 0) return;
+  const int groups = p.kv.heads_kv / lc.group;
+  const int b = cut.x / groups, hk = cut.x % groups * lc.group + head;
+  const int run = cut.y, n = cut.z - run + 1, first_slot = cut.w;
+  const float* const parts = parts_of(p.work, static_cast<size_t>(lc.blocks) * lc.chunks);
+  const int part_rows = lc.group * lc.rows;
+  const size_t pf = part_floats(part_rows, D);
+  const int col = tid % COLS, group = tid / COLS;
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = group; i < n; i += join_groups) {
+    const float* const part =
+        parts + (static_cast<size_t>(chunk * lc.blocks + run + i) * 2 + (i == 0 ? first_slot : 0)) * pf;
+    const float2* const from = reinterpret_cast<const float2*>(part + local * D + col * 4);
+    const float2 a = from[0], b = from[1];
+    const float mi = part[part_rows * D + local], li = part[part_rows * D + part_rows + local];
+    const float up = fmaxf(top, mi);
+    const float keep = up == top ? 1.f : ex2_approx(top - up);
+    const float f = li == 0.f ? 0.f : ex2_approx(mi - up);
+    top = up;
+    sum = fmaf(sum, keep, f * li);
+    acc.x = fmaf(acc.x, keep, f * a.x);
+    acc.y = fmaf(acc.y, keep, f * a.y);
+    acc.z = fmaf(acc.z, keep, f * b.x);
+    acc.w = fmaf(acc.w, keep, f * b.y);
+  }
+  s_acc[tid] = acc;
+  if (col == 0) {
+    s_top[group] = top;
+    s_sum[group] = sum;
+  }
+  __syncthreads();
+  if (tid >= COLS) return;
+  for (int i = 1; i < join_groups; ++i) top = fmaxf(top, s_top[i]);
+  sum = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < join_groups; ++i) {
+    const float f = s_sum[i] == 0.f ? 0.f : ex2_approx(s_top[i] - top);
+    const float4 a = s_acc[i * COLS + tid];
+    sum = fmaf(f, s_sum[i], sum);
+    acc.x = fmaf(f, a.x, acc.x);
+    acc.y = fmaf(f, a.y, acc.y);
+    acc.z = fmaf(f, a.z, acc.z);
+    acc.w = fmaf(f, a.w, acc.w);
+  }
+  const float inv = sum == 0.f ? 0.f : (p.kv.v_scale ? __ldg(p.kv.v_scale + hk) : 1.f) / sum;
+  const long long at = static_cast<long long>(b) * p.heads + hk * G + chunk * lc.rows + row;
+  uint2 out;
+  out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.o + at * D + tid * 4) = out;
+  if (p.lse && tid == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------------ launch
+inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    n = 152;
+  return n;
+}
+
+template <int D, bool E4M3, int NH, int HW>
+cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
+  using Sh = Shape<D, E4M3, NH, HW>;
+  static std::atomic<unsigned long long> smem_done{0};
+  auto* const kernel = decode_kernel<D, E4M3, NH, HW>;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), Sh::kSmem, smem_done);
+  if (e != cudaSuccess) return e;
+  lc.group = HW;
+  // At most one block per tile, at most the blocks that are resident at once.
+  int longest = p.max_pages * p.kv.page_size;
+  if (p.window > 0 && p.window < longest) longest = p.window;
+  const long long unit_tiles = longest > Sh::kTile ? (longest + static_cast<long long>(Sh::kTile) - 1) / Sh::kTile : 1;
+  const long long tiles = unit_tiles * p.batch * (p.kv.heads_kv / HW);
+  long long blocks = Sh::kBlocksPerSm * sm_count();
+  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
+  blocks = blocks / lc.chunks > 1 ? blocks / lc.chunks : 1;
+  lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
+  const long long units = static_cast<long long>(p.batch) * (p.kv.heads_kv / HW);
+  lc.by_unit = units <= lc.blocks;
+  kernel<<<dim3(lc.blocks, lc.chunks), Sh::kThreads, Sh::kSmem, s>>>(p, lc);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
+  cudaLaunchConfig_t cfg = {};
+  // A unit lies in about blocks / units runs (ragged lengths: some in more); a
+  // group of threads for every four of them.
+  int groups = 2;
+  while (groups < kMostGroups && groups * 4 * units < lc.blocks) groups *= 2;
+  cfg.gridDim = dim3(lc.by_unit ? static_cast<unsigned>(units) : lc.blocks, lc.chunks * HW * lc.rows);
+  cfg.blockDim = dim3(D / 4 * groups);
+  cfg.dynamicSmemBytes = cfg.blockDim.x * sizeof(float4);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p, lc);
+}
+
+// Key/value heads per tile: the largest of 4, 2, 1 that divides heads_kv.
+template <int D, bool E4M3, int NH>
+cudaError_t launch_group(const DecodeParams& p, const Launch& lc, cudaStream_t s) {
+  if (p.kv.heads_kv % 4 == 0) return launch_shape<D, E4M3, NH, 4>(p, lc, s);
+  if (p.kv.heads_kv % 2 == 0) return launch_shape<D, E4M3, NH, 2>(p, lc, s);
+  return launch_shape<D, E4M3, NH, 1>(p, lc, s);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_rows(const DecodeParams& p, const Launch& lc, cudaStream_t s) {
+  if (lc.rows <= 8) return launch_group<D, E4M3, 1>(p, lc, s);
+  if constexpr (D < 256) {
+    // more than 16 query heads on a key/value head: one of those at a time
+    if (lc.rows > 24) return launch_shape<D, E4M3, 4, 1>(p, lc, s);
+    if (lc.rows > 16) return launch_shape<D, E4M3, 3, 1>(p, lc, s);
+  }
+  return launch_group<D, E4M3, 2>(p, lc, s);
+}
+
+}  // namespace decode
+}  // namespace fa

@@ -1,0 +1,8 @@
+// Single-token attention over the paged cache at head_dim 256.
+#include "decode.cuh"
+
+namespace fa {
+cudaError_t launch_decode_d256(const DecodeParams& p, const decode::Launch& lc, cudaStream_t s) {
+  return p.kv.e4m3 ? decode::launch_rows<256, true>(p, lc, s) : decode::launch_rows<256, false>(p, lc, s);
+}
+}  // namespace fa
