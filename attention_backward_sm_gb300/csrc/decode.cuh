@@ -14,7 +14,7 @@
 //     (keys and dimensions in the rows, so that few heads waste little), which
 //     keeps the arithmetic far below the time of the loads;
 //   * a tile is some keys of HW neighbouring key/value heads, a warp per head
-//     (HW = 4, 2 or 1: the largest that divides heads_kv).  In the packed
+//     (HW = 4, 2 or 1).  In the packed
 //     layout a slot's heads lie side by side, and read together they are long
 //     pieces of DRAM rows (e4m3, d = 64: 256 bytes instead of 64); the heads
 //     also share the work of finding the rows.  With fewer heads than warps
@@ -67,7 +67,7 @@ struct Shape {
                                       : kStageBytes >= 32768 || NH > 2                         ? 2
                                       : NH > 1 || E4M3                                         ? 3
                                                                                                : 4;
-  static constexpr int kStages = kStageBytes < 65536 && kBlocksPerSm == 1 ? 6 : 3;
+  static constexpr int kStages = kStageBytes < 65536 && kBlocksPerSm == 1 ? 5 : 3;
   static constexpr int kRowWarps = kStageBytes >= 65536 && E4M3 ? 8 : 4;   // warps over a tile's rows
   static constexpr int kKeyWarps = kRowWarps / HW;
   static constexpr int kKeys = kTile / kKeyWarps;                          // of a warp
@@ -85,11 +85,16 @@ struct Shape {
   static constexpr int kOffSeen = kOffOffsets + kOffsets * kTile * 8;
   static constexpr int kOffJoin = kOffSeen + kOffsets * kSeenWords * 4;
   static constexpr int kOffScan = kOffJoin + (kKeyWarps > 1 ? 2 * kRowWarps * kHeads * 4 : 0);
-  static constexpr int kSmem = kOffScan + kThreads / 32 * 4 + 16;
+  static constexpr int kOffZero = (kOffScan + kThreads / 32 * 4 + 16 + 15) / 16 * 16;   // 16 zero bytes
+  static constexpr int kOffQ = kOffZero + 16;   // query rows of kStages units
   static_assert(kJoinHeads >= 8, "join buffer");
   static_assert(kKeys == 16 || kKeys == 32, "a word of seen keys");
   static_assert(kTile <= kThreads && kTile % 16 == 0, "a thread per key looks up its page");
-  static_assert(kBlocksPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
+  static constexpr int smem(int rows) { return kOffQ + kStages * HW * rows * D * 2; }
+  static constexpr bool fits(int rows) {
+    return smem(rows) <= 227 * 1024 && kBlocksPerSm * (smem(rows) + 1024) <= 228 * 1024;
+  }
+  static_assert(HW > 1 || fits(kHeads), "shared memory");
 };
 
 // A unit that the end of the run it starts in cuts, if any: runs [run, last]
@@ -145,16 +150,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-// Word w of lane q of a quad becomes word q of lane w.
-__device__ __forceinline__ void transpose_quad(int q, uint32_t& v0, uint32_t& v1, uint32_t& v2, uint32_t& v3) {
-  const bool odd = q & 1, high = q & 2;
-  const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1), b = __shfl_xor_sync(0xffffffffu, odd ? v2 : v3, 1);
-  (odd ? v0 : v1) = a;
-  (odd ? v2 : v3) = b;
-  const uint32_t c = __shfl_xor_sync(0xffffffffu, high ? v0 : v2, 2), d = __shfl_xor_sync(0xffffffffu, high ? v1 : v3, 2);
-  (high ? v0 : v2) = c;
-  (high ? v1 : v3) = d;
 }
 // c += a b, 16 x 8 x 16, fp32 accumulate; operands bf16 or fp16.
 template <bool F16>
@@ -325,6 +320,9 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   const int block = blockIdx.y * lc.blocks + blockIdx.x;
   const Lens L{p.seq_lens, p.max_pages * p.kv.page_size, p.window};
 
+  if (tid == 0) *reinterpret_cast<uint4*>(smem + S::kOffZero) = make_uint4(0, 0, 0, 0);
+  const int q_bytes = HW * lc.rows * D * 2;   // of one unit's queries
+
   // The run of this block: every block counts all tiles, then finds where
   // its share starts.
   const Scan<TILE, kThreads> tiles(L, p.batch, groups, scan);
@@ -365,7 +363,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   // 16-byte pieces of a key's row of a tile (all heads), keys per pass
   constexpr int CPR = RB / 16, PIECES = HW * CPR, KPP = kThreads / PIECES;
   const int piece_head = tid % PIECES / CPR, piece = tid % CPR, key_in_pass = tid / PIECES;
-  auto load_tile = [&](const Place<TILE>& at, int ring, int stage) {
+  auto load_tile = [&](const Place<TILE>& at, int ring, int stage, int q_slot, bool with_q) {
     const long long head = (at.hk * HW + piece_head) * p.kv.head_stride * S::kElem + piece * 16;
     const unsigned char* const kb = static_cast<const unsigned char*>(p.kv.k) + head;
     const unsigned char* const vb = static_cast<const unsigned char*>(p.kv.v) + head;
@@ -389,9 +387,18 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
       const int end = (keys + S::kKeys - 1) / S::kKeys * S::kKeys;
       for (int r = key_in_pass; r < end; r += KPP) load_row(r);
     }
+    if (with_q) {
+      const uint16_t* const q = p.q + at.b * p.q_row_stride + (at.hk * HW * G + row0) * D;
+      const uint32_t to = sbase + S::kOffQ + q_slot * q_bytes;
+      for (int i = tid; i < HW * rows * (D / 8); i += kThreads) {
+        const int c = i % (D / 8), h = HW == 1 ? 0 : i / (D / 8) / rows, r = i / (D / 8) - h * rows;
+        cp_async16(to + h * lc.rows * D * 2 + swizzled<D * 2>(r, c), q + (h * G + r) * D + c * 8, true);
+      }
+    }
   };
 
   // Prologue: the first ST - 1 tiles are on their way before the loop.
+  int q_load = 0;                 // query slot of the unit being loaded
   {
     Place<TILE> load = here;
     int pages[ST - 1];   // looked up together: one trip to memory
@@ -414,7 +421,9 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
     __syncthreads();
     for (int i = 0; i < ST - 1; ++i) {
       if (i < n) {
-        load_tile(load, i, i);
+        const bool with_q = i == 0 || load.t == 0;
+        if (i > 0 && with_q) q_load = q_load + 1 == ST ? 0 : q_load + 1;
+        load_tile(load, i, i, q_load, with_q);
         load.next(L, p.batch, groups);
       }
       cp_commit();
@@ -427,45 +436,20 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   uint32_t qf[NH][D / 16][2];               // Q^T fragments (e4m3: fp16, rescaled per head)
   float o[NH][DO / 16][4];
   float m[NH][2], l[NH][2], factor[NH][2];  // reference, this lane's sum, scores to units of log 2
-  int stage = 0, ring = 0;
+  int stage = 0, ring = 0, q_slot = 0;
   int load_stage = ST - 1, load_ring = ST - 1;
   bool fresh = true, first_piece = true;
   const int g = lane >> 2, quad = lane & 3;
 
   for (int s = 0; s < n; ++s) {
-    if (fresh) {   // the unit's queries, on their way while the tile is waited for
-#pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        const uint16_t* const q =
-            p.q + here.b * p.q_row_stride + ((here.hk * HW + hw) * G + row0 + 8 * i + g) * D + quad * (E4M3 ? 4 : 8);
-        const bool have = 8 * i + g < rows;
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            const uint2 v = have ? *reinterpret_cast<const uint2*>(q + 16 * j) : make_uint2(0u, 0u);
-            qf[i][j][0] = v.x;
-            qf[i][j][1] = v.y;
-          }
-        } else {
-          // 16 bytes per lane, of which a quad's lanes want each other's words
-          // (transposed where the unit starts)
-#pragma unroll
-          for (int j = 0; j < D / 16; j += 2) {
-            const uint4 v = have ? *reinterpret_cast<const uint4*>(q + 16 * j) : make_uint4(0u, 0u, 0u, 0u);
-            qf[i][j][0] = v.x;
-            qf[i][j][1] = v.y;
-            qf[i][j + 1][0] = v.z;
-            qf[i][j + 1][1] = v.w;
-          }
-        }
-      }
-    }
     cp_wait<ST - 2>();
     const bool more = s + ST - 1 < n;
     if (more) store_offset(ahead, page_ahead, load_ring);
     __syncthreads();   // tile s has landed for every thread; tile s - 1's stage is free
     if (more) {
-      load_tile(ahead, load_ring, load_stage);
+      const bool with_q = ahead.t == 0;
+      if (with_q) q_load = q_load + 1 == ST ? 0 : q_load + 1;
+      load_tile(ahead, load_ring, load_stage, q_load, with_q);
       ahead.next(L, p.batch, groups);
       if (s + ST < n) page_ahead = look_up(ahead);
       load_stage = load_stage + 1 == ST ? 0 : load_stage + 1;
@@ -475,6 +459,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
 
     if (fresh) {
       fresh = false;
+      const uint32_t qb = sbase + S::kOffQ + q_slot * q_bytes + hw * lc.rows * D * 2;
       const float scale = p.scale * kLog2e * (p.kv.k_scale ? __ldg(p.kv.k_scale + here.hk * HW + hw) : 1.f);
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
@@ -489,9 +474,16 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
 #pragma unroll
           for (int c = 0; c < 4; ++c) o[i][j][c] = 0.f;
         if constexpr (!E4M3) {
+          const int r = 8 * i + (lane & 7);
 #pragma unroll
-          for (int j = 0; j < D / 16; j += 2)
-            transpose_quad(quad, qf[i][j][0], qf[i][j][1], qf[i][j + 1][0], qf[i][j + 1][1]);
+          for (int j = 0; j < D / 16; j += 2) {
+            uint32_t b[4];
+            ldsm4(b, r < rows ? qb + swizzled<D * 2>(r, 2 * j + (lane >> 3)) : sbase + S::kOffZero);
+            qf[i][j][0] = b[0];
+            qf[i][j][1] = b[1];
+            qf[i][j + 1][0] = b[2];
+            qf[i][j + 1][1] = b[3];
+          }
         } else {
           // A lane's four bytes of a K row are four consecutive dimensions;
           // they serve as the products' k = 2 quad, + 1, + 8, + 9, and the query
@@ -501,6 +493,11 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
           float top = 0.f;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
+            const uint32_t a = qb + swizzled<D * 2>(8 * i + g, 2 * j + (quad >> 1)) + (quad & 1) * 8;
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(qf[i][j][0]), "=r"(qf[i][j][1])
+                         : "r"(8 * i + g < rows ? a : sbase + S::kOffZero)
+                         : "memory");
 #pragma unroll
             for (int c = 0; c < 2; ++c)
               top = fmaxf(top, fmaxf(fabsf(bf_lo(qf[i][j][c])), fabsf(bf_hi(qf[i][j][c]))));
@@ -772,7 +769,8 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
           __syncthreads();
           const int heads = min(rows - h0, JH);
           for (int i = tid; i < HW * heads * (D / 4); i += kThreads) {
-            const int c4 = i % (D / 4), local = i / (D / 4) % heads, h = i / (D / 4) / heads, row = h0 + local;
+            const int c4 = i % (D / 4), h = HW == 1 ? 0 : i / (D / 4) / heads;
+            const int local = i / (D / 4) - h * heads, row = h0 + local;
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < KW; ++w) top = fmaxf(top, join_m[(h * KW + w) * HEADS + row]);
@@ -819,6 +817,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
       }
       fresh = true;
       first_piece = false;
+      q_slot = q_slot + 1 == ST ? 0 : q_slot + 1;
     }
     here.next(L, p.batch, groups);
     stage = stage + 1 == ST ? 0 : stage + 1;
@@ -827,17 +826,19 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
 }
 
 // ------------------------------------------------------------------ combine
-// One block per (cut, query head of a head group): joins the partial results
-// of the runs the unit lies in, group g of its threads those of runs g,
-// g + groups, ... in one pass with a running maximum, then the groups in order.
-constexpr int kMostGroups = 16;
+// One block per (cut, query head of a head group, 4 COLS columns): joins the
+// partial results of the runs the unit lies in, group g of its threads those
+// of runs g, g + GROUPS, ... in one pass with a running maximum, then the
+// groups in order.  Few runs: 128 columns (or all); many: 32 columns by 16 groups.
+// Blocks are small so that they can wait beside the main kernel's.
+constexpr int kJoinThreads = 128;
 
-template <int D>
-__global__ void __launch_bounds__(D / 4 * kMostGroups) combine_kernel(const DecodeParams p, const Launch lc) {
-  constexpr int COLS = D / 4;
-  __shared__ float s_top[kMostGroups], s_sum[kMostGroups];
-  extern __shared__ float4 s_acc[];   // [threads]
-  const int tid = threadIdx.x, join_groups = blockDim.x / COLS;
+template <int D, int COLS>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParams p, const Launch lc) {
+  constexpr int GROUPS = kJoinThreads / COLS;
+  __shared__ float s_top[GROUPS], s_sum[GROUPS];
+  __shared__ float4 s_acc[kJoinThreads];
+  const int tid = threadIdx.x;
   const int local = blockIdx.y % (lc.group * lc.rows), chunk = blockIdx.y / (lc.group * lc.rows);
   const int head = local / lc.rows, row = local % lc.rows;   // of the group; of the head's chunk
   const int G = p.heads / p.kv.heads_kv;
@@ -851,11 +852,11 @@ __global__ void __launch_bounds__(D / 4 * kMostGroups) combine_kernel(const Deco
   const float* const parts = parts_of(p.work, static_cast<size_t>(lc.blocks) * lc.chunks);
   const int part_rows = lc.group * lc.rows;
   const size_t pf = part_floats(part_rows, D);
-  const int col = tid % COLS, group = tid / COLS;
+  const int col = blockIdx.z * COLS + tid % COLS, group = tid / COLS;
   float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int i = group; i < n; i += join_groups) {
+  for (int i = group; i < n; i += GROUPS) {
     const float* const part =
         parts + (static_cast<size_t>(chunk * lc.blocks + run + i) * 2 + (i == 0 ? first_slot : 0)) * pf;
     const float2* const from = reinterpret_cast<const float2*>(part + local * D + col * 4);
@@ -872,17 +873,18 @@ __global__ void __launch_bounds__(D / 4 * kMostGroups) combine_kernel(const Deco
     acc.w = fmaf(acc.w, keep, f * b.y);
   }
   s_acc[tid] = acc;
-  if (col == 0) {
+  if (tid % COLS == 0) {
     s_top[group] = top;
     s_sum[group] = sum;
   }
   __syncthreads();
   if (tid >= COLS) return;
-  for (int i = 1; i < join_groups; ++i) top = fmaxf(top, s_top[i]);
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) top = fmaxf(top, s_top[i]);
   sum = 0.f;
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < join_groups; ++i) {
+#pragma unroll
+  for (int i = 0; i < GROUPS; ++i) {
     const float f = s_sum[i] == 0.f ? 0.f : ex2_approx(s_top[i] - top);
     const float4 a = s_acc[i * COLS + tid];
     sum = fmaf(f, s_sum[i], sum);
@@ -896,8 +898,8 @@ __global__ void __launch_bounds__(D / 4 * kMostGroups) combine_kernel(const Deco
   uint2 out;
   out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(p.o + at * D + tid * 4) = out;
-  if (p.lse && tid == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+  *reinterpret_cast<uint2*>(p.o + at * D + col * 4) = out;
+  if (p.lse && col == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ launch
@@ -909,18 +911,26 @@ inline int sm_count() {
   return n;
 }
 
+// The longest stretch of keys that a request can see, and what it comes to in tiles.
+inline int longest(const DecodeParams& p) {
+  const int n = p.max_pages * p.kv.page_size;
+  return p.window > 0 && p.window < n ? p.window : n;
+}
+inline long long tiles_of(const DecodeParams& p, int tile) {
+  const int n = longest(p);
+  return n > tile ? (n + static_cast<long long>(tile) - 1) / tile : 1;
+}
+
 template <int D, bool E4M3, int NH, int HW>
 cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   using Sh = Shape<D, E4M3, NH, HW>;
   static std::atomic<unsigned long long> smem_done{0};
   auto* const kernel = decode_kernel<D, E4M3, NH, HW>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), Sh::kSmem, smem_done);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), 227 * 1024, smem_done);
   if (e != cudaSuccess) return e;
   lc.group = HW;
   // At most one block per tile, at most the blocks that are resident at once.
-  int longest = p.max_pages * p.kv.page_size;
-  if (p.window > 0 && p.window < longest) longest = p.window;
-  const long long unit_tiles = longest > Sh::kTile ? (longest + static_cast<long long>(Sh::kTile) - 1) / Sh::kTile : 1;
+  const long long unit_tiles = tiles_of(p, Sh::kTile);
   const long long tiles = unit_tiles * p.batch * (p.kv.heads_kv / HW);
   long long blocks = Sh::kBlocksPerSm * sm_count();
   if (blocks > kMaxBlocks) blocks = kMaxBlocks;
@@ -928,31 +938,43 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
   const long long units = static_cast<long long>(p.batch) * (p.kv.heads_kv / HW);
   lc.by_unit = units <= lc.blocks;
-  kernel<<<dim3(lc.blocks, lc.chunks), Sh::kThreads, Sh::kSmem, s>>>(p, lc);
+  kernel<<<dim3(lc.blocks, lc.chunks), Sh::kThreads, Sh::smem(lc.rows), s>>>(p, lc);
   e = cudaGetLastError();
   if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
   cudaLaunchConfig_t cfg = {};
-  // A unit lies in about blocks / units runs (ragged lengths: some in more); a
-  // group of threads for every four of them.
-  int groups = 2;
-  while (groups < kMostGroups && groups * 4 * units < lc.blocks) groups *= 2;
   cfg.gridDim = dim3(lc.by_unit ? static_cast<unsigned>(units) : lc.blocks, lc.chunks * HW * lc.rows);
-  cfg.blockDim = dim3(D / 4 * groups);
-  cfg.dynamicSmemBytes = cfg.blockDim.x * sizeof(float4);
+  cfg.gridDim.z = D == 256 ? 2 : 1;
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p, lc);
+  // A unit lies in about blocks / units runs (ragged lengths: some in several
+  // times as many).
+  if (8 * units > lc.blocks) return cudaLaunchKernelEx(&cfg, combine_kernel<D, (D < 128 ? D : 128) / 4>, p, lc);
+  cfg.gridDim.z = D / 32;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D, 8>, p, lc);
 }
 
-// Key/value heads per tile: the largest of 4, 2, 1 that divides heads_kv.
+// Whether tiles of HW key/value heads are taken: where their queries fit
+// beside the ring of stages, and blocks have enough tiles (16 at least, were
+// every request as long as can be) for the longer DRAM pieces to matter more
+// than the more numerous partial results per unit.  4 heads against 1, on one
+// GPU: 128 requests of 1k to 16k keys, 32 / 8 heads, d = 128, e4m3: 221 and
+// 254 us; one request of 1k keys, bf16: 8.1 and 6.9 us.
+template <int D, bool E4M3, int NH, int HW>
+bool take_group(const DecodeParams& p, const Launch& lc) {
+  using Sh = Shape<D, E4M3, NH, HW>;
+  return p.kv.heads_kv % HW == 0 && Sh::fits(lc.rows) &&
+         tiles_of(p, Sh::kTile) * p.batch * (p.kv.heads_kv / HW) >= 16ll * Sh::kBlocksPerSm * 152;
+}
+
 template <int D, bool E4M3, int NH>
 cudaError_t launch_group(const DecodeParams& p, const Launch& lc, cudaStream_t s) {
-  if (p.kv.heads_kv % 4 == 0) return launch_shape<D, E4M3, NH, 4>(p, lc, s);
-  if (p.kv.heads_kv % 2 == 0) return launch_shape<D, E4M3, NH, 2>(p, lc, s);
+  if (take_group<D, E4M3, NH, 4>(p, lc)) return launch_shape<D, E4M3, NH, 4>(p, lc, s);
+  if (take_group<D, E4M3, NH, 2>(p, lc)) return launch_shape<D, E4M3, NH, 2>(p, lc, s);
   return launch_shape<D, E4M3, NH, 1>(p, lc, s);
 }
 
