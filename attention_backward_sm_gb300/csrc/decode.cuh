@@ -937,7 +937,7 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   blocks = blocks / lc.chunks > 1 ? blocks / lc.chunks : 1;
   lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
   const long long units = static_cast<long long>(p.batch) * (p.kv.heads_kv / HW);
-  lc.by_unit = units <= lc.blocks;
+  lc.by_unit = 2 * units <= lc.blocks;
   kernel<<<dim3(lc.blocks, lc.chunks), Sh::kThreads, Sh::smem(lc.rows), s>>>(p, lc);
   e = cudaGetLastError();
   if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
@@ -959,7 +959,7 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
 }
 
 // Whether tiles of HW key/value heads are taken: where their queries fit
-// beside the ring of stages, and blocks have enough tiles (16 at least, were
+// beside the ring of stages, and blocks have enough tiles (12 at least, were
 // every request as long as can be) for the longer DRAM pieces to matter more
 // than the more numerous partial results per unit.  4 heads against 1, on one
 // GPU: 128 requests of 1k to 16k keys, 32 / 8 heads, d = 128, e4m3: 221 and
@@ -968,7 +968,7 @@ template <int D, bool E4M3, int NH, int HW>
 bool take_group(const DecodeParams& p, const Launch& lc) {
   using Sh = Shape<D, E4M3, NH, HW>;
   return p.kv.heads_kv % HW == 0 && Sh::fits(lc.rows) &&
-         tiles_of(p, Sh::kTile) * p.batch * (p.kv.heads_kv / HW) >= 16ll * Sh::kBlocksPerSm * 152;
+         tiles_of(p, Sh::kTile) * p.batch * (p.kv.heads_kv / HW) >= 12ll * Sh::kBlocksPerSm * 152;
 }
 
 template <int D, bool E4M3, int NH>

@@ -100,7 +100,7 @@ fa::PagedCache make_cache(const void* k, const void* v, int kv_type, const float
 }
 
 // ---------------------------------------------------------------- plan
-constexpr int kPlanThreads = 256;
+constexpr int kPlanMaxThreads = 1024;
 
 struct PlanParams {
   int32_t* table;
@@ -112,6 +112,7 @@ struct PlanParams {
   int num_free;
   const int32_t* free_start;
   int page_size;
+  fa::FastDiv page_div;
   int batch;
   int num_tokens;
   int64_t* slots;
@@ -132,68 +133,78 @@ struct Request {
 
 __device__ __forceinline__ Request load_request(const PlanParams& p, int b) {
   Request r;
-  r.seq = max(p.seq_lens[b], 0);
-  r.fresh = max(p.new_lens[b], 0);
-  const long long after = static_cast<long long>(r.seq) + r.fresh;
-  const long long have = (static_cast<long long>(r.seq) + p.page_size - 1) / p.page_size;
-  const long long need = (after + p.page_size - 1) / p.page_size;
-  r.have = static_cast<int>(have < p.max_pages ? have : p.max_pages);
-  r.take = static_cast<int>(need < p.max_pages ? need : p.max_pages) - r.have;
+  r.seq = max(__ldg(p.seq_lens + b), 0);
+  r.fresh = max(__ldg(p.new_lens + b), 0);
+  const int after = clamp_int(static_cast<long long>(r.seq) + r.fresh);
+  // ceil(n / page_size) of n >= 0
+  const int have = r.seq ? p.page_div.quotient(r.seq - 1) + 1 : 0;
+  const int need = after ? p.page_div.quotient(after - 1) + 1 : 0;
+  r.have = min(have, p.max_pages);
+  r.take = min(need, p.max_pages) - r.have;
   return r;
 }
 
 // Every block sums the requests' new tokens and pages itself (a block scan
 // over runs of consecutive requests, one run per thread), then places its
 // own tokens; block 0 also writes what there is one of per request.  Nothing
-// is passed between blocks, so one launch is enough.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
-  __shared__ long long run_tok[kPlanThreads + 1];   // new tokens before each thread's run
-  __shared__ long long run_page[kPlanThreads + 1];  // pages taken before it
-  const int t = threadIdx.x;
-  const int per = (p.batch + kPlanThreads - 1) / kPlanThreads;
+// is passed between blocks, so one launch is enough.  Bound by launch and
+// memory latency: 64 requests 3.1 us, 2048 requests 4.5 us, 85k tokens of 32
+// prompts 3.4 us.
+__global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams p) {
+  __shared__ long long run_tok[kPlanMaxThreads + 1];   // new tokens before each thread's run
+  __shared__ long long run_page[kPlanMaxThreads + 1];  // pages taken before it
+  __shared__ long long warp_tok[32], warp_page[32];
+  const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, lane = t & 31;
+  const int per = (p.batch + threads - 1) / threads;
   const int b0 = min(t * per, p.batch), b1 = min(b0 + per, p.batch);
+  const long long start = p.free_start ? max(__ldg(p.free_start), 0) : 0;
   long long tok = 0, page = 0;
   for (int b = b0; b < b1; ++b) {
     const Request r = load_request(p, b);
     tok += r.fresh;
     page += r.take;
   }
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, tok, off), c = __shfl_up_sync(0xffffffffu, page, off);
+    if (lane >= off) {
+      tok += a;
+      page += c;
+    }
+  }
+  if (lane == 31) {
+    warp_tok[warp] = tok;
+    warp_page[warp] = page;
+  }
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) {
+    tok += warp_tok[w];
+    page += warp_page[w];
+  }
   run_tok[t + 1] = tok;
   run_page[t + 1] = page;
   if (t == 0) run_tok[0] = run_page[0] = 0;
   __syncthreads();
-  for (int off = 1; off < kPlanThreads; off <<= 1) {
-    long long a = 0, c = 0;
-    if (t + 1 > off) {
-      a = run_tok[t + 1 - off];
-      c = run_page[t + 1 - off];
-    }
-    __syncthreads();
-    run_tok[t + 1] += a;
-    run_page[t + 1] += c;
-    __syncthreads();
-  }
-  const long long start = p.free_start ? max(*p.free_start, 0) : 0;
   if (blockIdx.x == 0) {
     long long at = run_tok[t];
     for (int b = b0; b < b1; ++b) {
-      const Request r = load_request(p, b);
+      const int seq = max(__ldg(p.seq_lens + b), 0), fresh = max(__ldg(p.new_lens + b), 0);
       p.cu_new[b] = clamp_int(at);
-      p.seq_lens_out[b] = clamp_int(static_cast<long long>(r.seq) + r.fresh);
-      at += r.fresh;
+      p.seq_lens_out[b] = clamp_int(static_cast<long long>(seq) + fresh);
+      at += fresh;
     }
     if (t == 0) {
-      p.cu_new[p.batch] = clamp_int(run_tok[kPlanThreads]);
-      *p.free_next = clamp_int(start + run_page[kPlanThreads]);
+      p.cu_new[p.batch] = clamp_int(run_tok[threads]);
+      *p.free_next = clamp_int(start + run_page[threads]);
     }
   }
-  const long long total = run_tok[kPlanThreads];
-  for (long long i = static_cast<long long>(blockIdx.x) * kPlanThreads + t; i < p.num_tokens;
-       i += static_cast<long long>(gridDim.x) * kPlanThreads) {
+  const long long total = run_tok[threads];
+  for (long long i = static_cast<long long>(blockIdx.x) * threads + t; i < p.num_tokens;
+       i += static_cast<long long>(gridDim.x) * threads) {
     long long slot = -1;
     int pos = 0;
     if (i < total) {
-      int lo = 0, hi = kPlanThreads;   // run_tok[lo] <= i < run_tok[hi]
+      int lo = 0, hi = threads;   // run_tok[lo] <= i < run_tok[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (run_tok[mid] <= i) lo = mid;
@@ -209,15 +220,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       }
       const long long place = static_cast<long long>(r.seq) + (i - at);
       pos = clamp_int(place);
-      const long long pi = place / p.page_size;
-      const int in_page = static_cast<int>(place - pi * p.page_size);
-      if (pi < p.max_pages) {
+      const int pi = p.page_div.quotient(pos), in_page = pos - pi * p.page_size;
+      if (pi < p.max_pages && place == pos) {
         int id;
         if (pi < r.have) {
           id = p.table[b * p.table_stride + pi];
         } else {
           const long long f = taken + (pi - r.have);
-          id = f < p.num_free ? p.free_pages[f] : -1;
+          id = f < p.num_free ? __ldg(p.free_pages + f) : -1;
           if (in_page == 0) p.table[b * p.table_stride + pi] = id;
         }
         if (id >= 0) slot = static_cast<long long>(id) * p.page_size + in_page;
@@ -238,6 +248,7 @@ struct AppendParams {
   long long k_row_stride;
   long long v_row_stride;
   const int64_t* slots;
+  fa::FastDiv page_div;
   int num_tokens;
 };
 
@@ -251,43 +262,93 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Eight bf16 values divided by `scale` (the correctly rounded quotient: a
-// product with a rounded reciprocal would put values next to a border of two
-// 8-bit numbers on the wrong side) and rounded to eight bytes.
-__device__ __forceinline__ uint2 quantise8(uint4 x, float scale) {
-  uint2 r;
-  r.x = e4m3x2(__fdiv_rn(bf_lo(x.x), scale), __fdiv_rn(bf_hi(x.x), scale)) |
-        e4m3x2(__fdiv_rn(bf_lo(x.y), scale), __fdiv_rn(bf_hi(x.y), scale)) << 16;
-  r.y = e4m3x2(__fdiv_rn(bf_lo(x.z), scale), __fdiv_rn(bf_hi(x.z), scale)) |
-        e4m3x2(__fdiv_rn(bf_lo(x.w), scale), __fdiv_rn(bf_hi(x.w), scale)) << 16;
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
   return r;
 }
 
-// One thread per eight elements of a row of K and of V.
+// A scale and its reciprocal, where that can be used (0: divide).
+struct Scale {
+  float s, inv;
+  __device__ __forceinline__ explicit Scale(const float* p, int h) : s(p ? __ldg(p + h) : 1.f) {
+    inv = s >= 0x1p-100f && s <= 0x1p100f ? 1.f / s : 0.f;
+  }
+};
+
+// Two bf16 values divided by the scale, the quotients rounded to fp32, then
+// to e4m3.  A product with the rounded reciprocal is within 3 units in the
+// last place of the quotient.  Rounding it instead makes no difference unless
+// a border between two 8-bit values (a fraction of 3 bits and a half: the low
+// 20 bits 0x80000) is that near, or the spacing of the 8-bit values differs
+// (below 2^-6); only then is the division carried out.
+__device__ __forceinline__ uint32_t quantise2(uint32_t two, const Scale& sc) {
+  const float x0 = bf_lo(two), x1 = bf_hi(two);
+  float q0 = x0 * sc.inv, q1 = x1 * sc.inv;
+  const uint32_t u0 = __float_as_uint(q0), u1 = __float_as_uint(q1);
+  const bool near = ((u0 & 0xFFFFFu) - 0x7FFFCu) <= 8u || ((u1 & 0xFFFFFu) - 0x7FFFCu) <= 8u;
+  const bool small = !(fminf(fabsf(q0), fabsf(q1)) >= 0x1p-6f);
+  if (near || small) {
+    q0 = __fdiv_rn(x0, sc.s);
+    q1 = __fdiv_rn(x1, sc.s);
+  }
+  return e4m3x2(q0, q1);
+}
+
+__device__ __forceinline__ uint2 quantise8(uint4 x, const Scale& sc) {
+  return make_uint2(quantise2(x.x, sc) | quantise2(x.y, sc) << 16, quantise2(x.z, sc) | quantise2(x.w, sc) << 16);
+}
+
+// Each thread keeps one place in the row (16 bytes of input, so one head and
+// one scale) and takes kRows rows at a time: their slots, then all their
+// loads, then the stores, so that enough loads are in flight.  Bound by HBM.
+// 32768 rows of 8 heads of 128 (269 MB, bf16) AAAA us; 8191 rows of 16 heads
+// of 64 to e4m3 (50 MB) BBBB us.
+constexpr int kAppendRows = 4;
+
 template <bool E4M3>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-  const int per_head = p.kv.head_dim / 8;
-  const int per_row = p.kv.heads_kv * per_head;
-  const long long n = static_cast<long long>(p.num_tokens) * per_row;
+  const int per_head = p.kv.head_dim / 8, per_row = p.kv.heads_kv * per_head;
+  const int wide = min(per_row, kAppendThreads), rows_per_pass = kAppendThreads / wide;
+  const int r0 = threadIdx.x / wide, c = blockIdx.y * kAppendThreads + threadIdx.x - r0 * wide;
+  if (r0 >= rows_per_pass || c >= per_row) return;
+  const int h = c / per_head;
+  const long long column = h * p.kv.head_stride + (c - h * per_head) * 8;
   const long long num_slots = static_cast<long long>(p.kv.num_pages) * p.kv.page_size;
-  for (long long i = static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x; i < n;
-       i += static_cast<long long>(gridDim.x) * kAppendThreads) {
-    const long long row = i / per_row;
-    const int c = static_cast<int>(i - row * per_row);
-    const int h = c / per_head;
-    const long long slot = p.slots[row];
-    if (slot < 0 || slot >= num_slots) continue;
-    const long long page = slot / p.kv.page_size;
-    const long long at = page * p.kv.page_stride + (slot - page * p.kv.page_size) * p.kv.slot_stride +
-                         h * p.kv.head_stride + (c - h * per_head) * 8;
-    const uint4 k = *reinterpret_cast<const uint4*>(p.k + row * p.k_row_stride + c * 8);
-    const uint4 v = *reinterpret_cast<const uint4*>(p.v + row * p.v_row_stride + c * 8);
-    if constexpr (E4M3) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kv.k) + at) = quantise8(k, p.kv.k_scale ? p.kv.k_scale[h] : 1.f);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kv.v) + at) = quantise8(v, p.kv.v_scale ? p.kv.v_scale[h] : 1.f);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.k) + at) = k;
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.v) + at) = v;
+  const Scale ks(E4M3 ? p.kv.k_scale : nullptr, h), vs(E4M3 ? p.kv.v_scale : nullptr, h);
+  const uint16_t* const kc = p.k + c * 8;
+  const uint16_t* const vc = p.v + c * 8;
+  for (long long row = static_cast<long long>(blockIdx.x) * rows_per_pass * kAppendRows + r0; row < p.num_tokens;
+       row += static_cast<long long>(gridDim.x) * rows_per_pass * kAppendRows) {
+    long long at[kAppendRows];   // element of the cache, -1: skipped
+    uint4 k[kAppendRows], v[kAppendRows];
+#pragma unroll
+    for (int i = 0; i < kAppendRows; ++i) {
+      const long long r = row + i * rows_per_pass;
+      at[i] = r < p.num_tokens ? __ldg(reinterpret_cast<const long long*>(p.slots) + r) : -1;
+      if (at[i] >= num_slots) at[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kAppendRows; ++i) {
+      if (at[i] < 0) continue;
+      const long long r = row + i * rows_per_pass;
+      k[i] = ldg_stream(kc + r * p.k_row_stride);
+      v[i] = ldg_stream(vc + r * p.v_row_stride);
+      const long long page = at[i] <= 0x7fffffffll ? p.page_div.quotient(static_cast<int>(at[i])) : at[i] / p.kv.page_size;
+      at[i] = page * p.kv.page_stride + (at[i] - page * p.kv.page_size) * p.kv.slot_stride + column;
+    }
+#pragma unroll
+    for (int i = 0; i < kAppendRows; ++i) {
+      if (at[i] < 0) continue;
+      if constexpr (E4M3) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kv.k) + at[i]) = quantise8(k[i], ks);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kv.v) + at[i]) = quantise8(v[i], vs);
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.k) + at[i]) = k[i];
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.v) + at[i]) = v[i];
+      }
     }
   }
 }
@@ -327,9 +388,14 @@ int fa_kv_plan(int32_t* block_table, long long table_stride, int max_pages, cons
     return set_last_error(FA_ERR_INVALID_ARG, "slots must be 8-byte aligned");
   int rc = check_device();
   if (rc) return rc;
-  const PlanParams p{block_table, table_stride, max_pages,  seq_lens, new_lens,  free_pages, num_free,     free_start,
-                     page_size,   batch,        num_tokens, slots,    positions, cu_new,     seq_lens_out, free_next};
-  plan_kernel<<<blocks_for(num_tokens, kPlanThreads, 2), kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  const PlanParams p{block_table,  table_stride, max_pages, seq_lens,
+                     new_lens,     free_pages,   num_free,  free_start,
+                     page_size,    fa::FastDiv(static_cast<uint32_t>(page_size)),
+                     batch,        num_tokens,   slots,     positions,
+                     cu_new,       seq_lens_out, free_next};
+  // a thread per request, up to a block's most
+  const int threads = batch <= 256 ? 256 : batch <= 512 ? 512 : kPlanMaxThreads;
+  plan_kernel<<<blocks_for(num_tokens, threads, 2), threads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
   return ok();
@@ -347,6 +413,8 @@ int fa_kv_append(const fa_bf16* k, const fa_bf16* v, long long k_row_stride, lon
   if (rc) return rc;
   if (num_tokens < 0) return set_last_error(FA_ERR_INVALID_ARG, "num_tokens must be >= 0, got %d", num_tokens);
   const long long row = static_cast<long long>(heads_kv) * head_dim;
+  if (row > 65535ll * 64)
+    return set_last_error(FA_ERR_UNSUPPORTED, "heads_kv * head_dim too large (%d * %d)", heads_kv, head_dim);
   if ((rc = check_row_stride("k_row_stride", k_row_stride, row, num_tokens))) return rc;
   if ((rc = check_row_stride("v_row_stride", v_row_stride, row, num_tokens))) return rc;
   if (num_tokens == 0 || num_pages == 0) return ok();
@@ -363,7 +431,10 @@ int fa_kv_append(const fa_bf16* k, const fa_bf16* v, long long k_row_stride, lon
   p.v_row_stride = v_row_stride;
   p.slots = slots;
   p.num_tokens = num_tokens;
-  const int grid = blocks_for(num_tokens * (row / 8), kAppendThreads, 8);
+  p.page_div = fa::FastDiv(static_cast<uint32_t>(page_size));
+  const int per_row = static_cast<int>(row / 8);
+  const int rows_per_block = (per_row < kAppendThreads ? kAppendThreads / per_row : 1) * kAppendRows;
+  const dim3 grid(blocks_for(num_tokens, rows_per_block, 64), (per_row + kAppendThreads - 1) / kAppendThreads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (p.kv.e4m3) append_kernel<true><<<grid, kAppendThreads, 0, s>>>(p);
   else append_kernel<false><<<grid, kAppendThreads, 0, s>>>(p);

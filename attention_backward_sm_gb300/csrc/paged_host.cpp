@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -179,9 +180,7 @@ class Place {
   fa_stream_t stream() const {
     return reinterpret_cast<fa_stream_t>(c10::cuda::getCurrentCUDAStream(device_.index()).stream());
   }
-  Tensor empty(at::IntArrayRef size, at::ScalarType type) const {
-    return at::detail::empty_cuda(size, type, device_, std::nullopt);
-  }
+  Tensor bytes(int64_t n) const { return at::detail::empty_cuda({n}, at::kByte, device_, std::nullopt); }
 
  private:
   static int64_t attr(PyObject* o, const char* name) {
@@ -195,6 +194,28 @@ class Place {
   c10::Device device_;
   c10::cuda::OptionalCUDAGuard device_guard_;
   std::optional<c10::cuda::CUDAStreamGuard> stream_guard_;
+};
+
+// Contiguous tensors cut one after the other out of one allocation of bytes
+// (an allocation is the dearest step of a small call).
+class Cutter {
+ public:
+  static int64_t size(int64_t n, int64_t element) { return (n * element + 255) / 256 * 256; }
+  explicit Cutter(Tensor base) : base_(std::move(base)) {}
+  Tensor next(at::IntArrayRef shape, at::ScalarType type) {
+    const int64_t element = static_cast<int64_t>(c10::elementSize(type));
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base_.storage()),
+                                                        c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                        c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    t.unsafeGetTensorImpl()->set_storage_offset(at_ / element);
+    at_ += size(t.numel(), element);
+    return t;
+  }
+
+ private:
+  Tensor base_;
+  int64_t at_ = 0;
 };
 
 template <class T>
@@ -274,11 +295,13 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     place.with(next, "free_next").enter(a[8]);
   } else {
     place.enter(a[8]);
-    slots = place.empty({tokens}, at::kLong);
-    positions = place.empty({tokens}, at::kInt);
-    cu = place.empty({table.batch + 1}, at::kInt);
-    after = place.empty({table.batch}, at::kInt);
-    next = place.empty({1}, at::kInt);
+    Cutter out(place.bytes(Cutter::size(tokens, 8) + Cutter::size(tokens, 4) + Cutter::size(table.batch + 1, 4) +
+                           Cutter::size(table.batch, 4) + Cutter::size(1, 4)));
+    slots = out.next({tokens}, at::kLong);
+    positions = out.next({tokens}, at::kInt);
+    cu = out.next({table.batch + 1}, at::kInt);
+    after = out.next({table.batch}, at::kInt);
+    next = out.next({1}, at::kInt);
   }
   const int num_free = size32(list.numel(), "free_pages");
   check(unlocked([&] {
@@ -348,10 +371,11 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     place.with(o, "o").with(lse, "lse").enter(a[11]);
   } else {
     place.enter(a[11]);
-    o = place.empty({batch, heads, dim}, at::kBFloat16);
-    lse = place.empty({batch, heads}, at::kFloat);
+    Cutter out(place.bytes(Cutter::size(batch * heads * dim, 2) + Cutter::size(batch * heads, 4)));
+    o = out.next({batch, heads, dim}, at::kBFloat16);
+    lse = out.next({batch, heads}, at::kFloat);
   }
-  if (!work && need > 0) work = place.empty({static_cast<int64_t>(need)}, at::kByte);
+  if (!work && need > 0) work = place.bytes(static_cast<int64_t>(need));
   const size_t work_bytes = work ? work->nbytes() : 0;
   check(unlocked([&] {
     return fa_decode(ptr<fa_bf16>(q), q_stride, ptr<void>(c.k), ptr<void>(c.v), c.type, c.ks(), c.vs(),

@@ -182,6 +182,38 @@ def test_append_writes_named_slots_only(tokens, heads_kv, dim, page, kv, layout)
         assert torch.equal(got.view(bits)[~nan], want.view(bits)[~nan])
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.05, 3.0, 1 / 3, 0.0123456, 2.0 ** -7, 448.0, 1e-30, 1e30, 1e-40, 3e38])
+def test_append_rounds_every_bf16_value_as_the_quotient(scale):
+    """All 65536 bf16 bit patterns: the 8-bit value of the fp32 quotient, bit
+    for bit (values next to a border of two 8-bit numbers among them)."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(-1, 1, 64)
+    s = torch.tensor([scale])
+    want = (x.float() / s).clamp(-448, 448).to(torch.float8_e4m3fn)
+    kc = torch.zeros(len(x) // 16, 16, 1, 64, dtype=torch.float8_e4m3fn, device=DEV)
+    vc = torch.zeros_like(kc)
+    fab().kv_append(x.to(DEV), x.to(DEV), kc, vc, torch.arange(len(x), device=DEV), s.to(DEV), s.to(DEV))
+    for got in (kc, vc):
+        got = got.cpu().view(want.shape)
+        nan = torch.isnan(want.float())
+        assert torch.equal(torch.isnan(got.float()), nan)
+        assert torch.equal(got.view(torch.uint8)[~nan], want.view(torch.uint8)[~nan])
+
+
+@pytest.mark.parametrize("tokens,heads_kv,dim", [(3000, 40, 64), (257, 9, 256), (5000, 1, 64)])
+def test_append_many_rows_and_wide_rows(tokens, heads_kv, dim):
+    """Rows of more and of fewer pieces than a block has threads."""
+    g = torch.Generator(device=DEV).manual_seed(tokens)
+    k, v = (torch.randn(tokens, heads_kv, dim, device=DEV, generator=g).bfloat16() for _ in range(2))
+    kc = torch.zeros(-(-tokens // 7), 7, heads_kv, dim, dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    slots = torch.randperm(kc.shape[0] * 7, device=DEV, generator=g)[:tokens]
+    fab().kv_append(k, v, kc, vc, slots)
+    for got, new in ((kc, k), (vc, v)):
+        want = torch.zeros_like(got).view(-1, heads_kv, dim)
+        want[slots] = new
+        assert torch.equal(got.view_as(want), want)
+
+
 # ------------------------------------------------------------------ decode
 GROUPS = [(1, 1), (4, 4), (8, 2), (6, 2), (14, 2), (9, 1), (16, 1), (20, 1), (40, 1)]
 
