@@ -270,84 +270,95 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return r;
 }
 
-// A scale and its reciprocal, where that can be used (0: divide).
+// A scale and two factors, one below and one above its reciprocal: for any x,
+// the fp32 quotient x / s lies between the rounded products x lo and x hi
+// (each is off by less than 2^-22 of itself, the factors are 2^-21 apart from
+// the reciprocal).  Scales whose reciprocal is out of range get 0 and
+// infinity, between which everything lies.
 struct Scale {
-  float s, inv;
+  float s, lo, hi;
   __device__ __forceinline__ explicit Scale(const float* p, int h) : s(p ? __ldg(p + h) : 1.f) {
-    inv = s >= 0x1p-100f && s <= 0x1p100f ? 1.f / s : 0.f;
+    const bool plain = s >= 0x1p-100f && s <= 0x1p100f;
+    const float inv = 1.f / s;
+    lo = plain ? inv * (1.f - 0x1p-21f) : 0.f;
+    hi = plain ? inv * (1.f + 0x1p-21f) : INFINITY;
   }
 };
 
-// Two bf16 values divided by the scale, the quotients rounded to fp32, then
-// to e4m3.  A product with the rounded reciprocal is within 3 units in the
-// last place of the quotient.  Rounding it instead makes no difference unless
-// a border between two 8-bit values (a fraction of 3 bits and a half: the low
-// 20 bits 0x80000) is that near, or the spacing of the 8-bit values differs
-// (below 2^-6); only then is the division carried out.
-__device__ __forceinline__ uint32_t quantise2(uint32_t two, const Scale& sc) {
-  const float x0 = bf_lo(two), x1 = bf_hi(two);
-  float q0 = x0 * sc.inv, q1 = x1 * sc.inv;
-  const uint32_t u0 = __float_as_uint(q0), u1 = __float_as_uint(q1);
-  const bool near = ((u0 & 0xFFFFFu) - 0x7FFFCu) <= 8u || ((u1 & 0xFFFFFu) - 0x7FFFCu) <= 8u;
-  const bool small = !(fminf(fabsf(q0), fabsf(q1)) >= 0x1p-6f);
-  if (near || small) {
-    q0 = __fdiv_rn(x0, sc.s);
-    q1 = __fdiv_rn(x1, sc.s);
-  }
-  return e4m3x2(q0, q1);
-}
-
+// Eight bf16 values divided by the scale, the quotients rounded to fp32, then
+// to e4m3.  Where both products round to the same 8-bit value, so does the
+// quotient between them; only where they do not (one group in 2^13) are the
+// divisions carried out, 5 instructions per value instead of 20.
 __device__ __forceinline__ uint2 quantise8(uint4 x, const Scale& sc) {
-  return make_uint2(quantise2(x.x, sc) | quantise2(x.y, sc) << 16, quantise2(x.z, sc) | quantise2(x.w, sc) << 16);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t lo[4], hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = bf_lo(w[i]), b = bf_hi(w[i]);
+    lo[i] = e4m3x2(a * sc.lo, b * sc.lo);
+    hi[i] = e4m3x2(a * sc.hi, b * sc.hi);
+  }
+  uint2 r = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  if (r.x != (hi[0] | hi[1] << 16) || r.y != (hi[2] | hi[3] << 16)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lo[i] = e4m3x2(__fdiv_rn(bf_lo(w[i]), sc.s), __fdiv_rn(bf_hi(w[i]), sc.s));
+    r = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  }
+  return r;
 }
 
-// Each thread keeps one place in the row (16 bytes of input, so one head and
-// one scale) and takes kRows rows at a time: their slots, then all their
-// loads, then the stores, so that enough loads are in flight.  Bound by HBM.
+// Each thread keeps one place in the row (16 bytes of the cache, so one head and
+// one scale) and takes ROWS rows at a time: their slots, then all their
+// loads, then the stores, so that enough loads are in flight.  Bound by HBM;
+// few tokens by latency, so they take one row per thread.
 // 32768 rows of 8 heads of 128 (269 MB, bf16) AAAA us; 8191 rows of 16 heads
 // of 64 to e4m3 (50 MB) BBBB us.
-constexpr int kAppendRows = 4;
-
-template <bool E4M3>
+template <bool E4M3, int ROWS>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-  const int per_head = p.kv.head_dim / 8, per_row = p.kv.heads_kv * per_head;
+  constexpr int N = E4M3 ? 2 : 1;   // 16-byte pieces of input per thread and row: one piece of the cache
+  const int per_head = p.kv.head_dim / (8 * N), per_row = p.kv.heads_kv * per_head;
   const int wide = min(per_row, kAppendThreads), rows_per_pass = kAppendThreads / wide;
   const int r0 = threadIdx.x / wide, c = blockIdx.y * kAppendThreads + threadIdx.x - r0 * wide;
   if (r0 >= rows_per_pass || c >= per_row) return;
   const int h = c / per_head;
-  const long long column = h * p.kv.head_stride + (c - h * per_head) * 8;
+  const long long column = h * p.kv.head_stride + (c - h * per_head) * (8 * N);
   const long long num_slots = static_cast<long long>(p.kv.num_pages) * p.kv.page_size;
   const Scale ks(E4M3 ? p.kv.k_scale : nullptr, h), vs(E4M3 ? p.kv.v_scale : nullptr, h);
-  const uint16_t* const kc = p.k + c * 8;
-  const uint16_t* const vc = p.v + c * 8;
-  for (long long row = static_cast<long long>(blockIdx.x) * rows_per_pass * kAppendRows + r0; row < p.num_tokens;
-       row += static_cast<long long>(gridDim.x) * rows_per_pass * kAppendRows) {
-    long long at[kAppendRows];   // element of the cache, -1: skipped
-    uint4 k[kAppendRows], v[kAppendRows];
+  const uint16_t* const kc = p.k + c * (8 * N);
+  const uint16_t* const vc = p.v + c * (8 * N);
+  for (long long row = static_cast<long long>(blockIdx.x) * rows_per_pass * ROWS + r0; row < p.num_tokens;
+       row += static_cast<long long>(gridDim.x) * rows_per_pass * ROWS) {
+    long long at[ROWS];   // element of the cache, -1: skipped
+    uint4 k[ROWS][N], v[ROWS][N];
 #pragma unroll
-    for (int i = 0; i < kAppendRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       const long long r = row + i * rows_per_pass;
       at[i] = r < p.num_tokens ? __ldg(reinterpret_cast<const long long*>(p.slots) + r) : -1;
       if (at[i] >= num_slots) at[i] = -1;
     }
 #pragma unroll
-    for (int i = 0; i < kAppendRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       if (at[i] < 0) continue;
       const long long r = row + i * rows_per_pass;
-      k[i] = ldg_stream(kc + r * p.k_row_stride);
-      v[i] = ldg_stream(vc + r * p.v_row_stride);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        k[i][n] = ldg_stream(kc + r * p.k_row_stride + 8 * n);
+        v[i][n] = ldg_stream(vc + r * p.v_row_stride + 8 * n);
+      }
       const long long page = at[i] <= 0x7fffffffll ? p.page_div.quotient(static_cast<int>(at[i])) : at[i] / p.kv.page_size;
       at[i] = page * p.kv.page_stride + (at[i] - page * p.kv.page_size) * p.kv.slot_stride + column;
     }
 #pragma unroll
-    for (int i = 0; i < kAppendRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       if (at[i] < 0) continue;
       if constexpr (E4M3) {
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kv.k) + at[i]) = quantise8(k[i], ks);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kv.v) + at[i]) = quantise8(v[i], vs);
+        const uint2 k0 = quantise8(k[i][0], ks), k1 = quantise8(k[i][1], ks);
+        const uint2 v0 = quantise8(v[i][0], vs), v1 = quantise8(v[i][1], vs);
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.kv.k) + at[i]) = make_uint4(k0.x, k0.y, k1.x, k1.y);
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.kv.v) + at[i]) = make_uint4(v0.x, v0.y, v1.x, v1.y);
       } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.k) + at[i]) = k[i];
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.v) + at[i]) = v[i];
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.k) + at[i]) = k[i][0];
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kv.v) + at[i]) = v[i][0];
       }
     }
   }
@@ -432,12 +443,17 @@ int fa_kv_append(const fa_bf16* k, const fa_bf16* v, long long k_row_stride, lon
   p.slots = slots;
   p.num_tokens = num_tokens;
   p.page_div = fa::FastDiv(static_cast<uint32_t>(page_size));
-  const int per_row = static_cast<int>(row / 8);
-  const int rows_per_block = (per_row < kAppendThreads ? kAppendThreads / per_row : 1) * kAppendRows;
-  const dim3 grid(blocks_for(num_tokens, rows_per_block, 64), (per_row + kAppendThreads - 1) / kAppendThreads);
+  const int per_row = static_cast<int>(row / (p.kv.e4m3 ? 16 : 8));   // threads
+  const int rows_per_pass = per_row < kAppendThreads ? kAppendThreads / per_row : 1;
+  // several rows per thread where that still gives every SM two blocks
+  const int most = p.kv.e4m3 ? 2 : 4;
+  const int rows = static_cast<long long>(num_tokens) * per_row >= 2ll * kAppendThreads * 152 * most ? most : 1;
+  const dim3 grid(blocks_for(num_tokens, rows_per_pass * rows, 64), (per_row + kAppendThreads - 1) / kAppendThreads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (p.kv.e4m3) append_kernel<true><<<grid, kAppendThreads, 0, s>>>(p);
-  else append_kernel<false><<<grid, kAppendThreads, 0, s>>>(p);
+  if (p.kv.e4m3 && rows > 1) append_kernel<true, 2><<<grid, kAppendThreads, 0, s>>>(p);
+  else if (p.kv.e4m3) append_kernel<true, 1><<<grid, kAppendThreads, 0, s>>>(p);
+  else if (rows > 1) append_kernel<false, 4><<<grid, kAppendThreads, 0, s>>>(p);
+  else append_kernel<false, 1><<<grid, kAppendThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "append launch");
   return ok();
