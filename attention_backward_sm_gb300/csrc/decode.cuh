@@ -183,11 +183,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-// Programmatic dependent launch: the next kernel of the stream may be set up
-// from here on; it waits for this one's end (and its writes) in pdl_wait.
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Byte offset of 16-byte piece c of row r in a tile whose rows are RB bytes,
 // so that eight consecutive rows' pieces c lie in different banks.
 template <int RB>
@@ -320,6 +315,8 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   const int block = blockIdx.y * lc.blocks + blockIdx.x;
   const Lens L{p.seq_lens, p.max_pages * p.kv.page_size, p.window};
 
+  pdl_wait();
+  pdl_launch();
   if (tid == 0) *reinterpret_cast<uint4*>(smem + S::kOffZero) = make_uint4(0, 0, 0, 0);
   const int q_bytes = HW * lc.rows * D * 2;   // of one unit's queries
 
@@ -341,7 +338,6 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   here.t = found[2];
   here.request(L, found[3]);
   Place<TILE> ahead = here;   // the next tile to load
-  pdl_launch();
 
   // Page of this thread's key of a tile, and from it the row's offset (bytes,
   // without the head's; top bit: not seen) and the tile's bits of seen keys.
@@ -924,9 +920,9 @@ inline long long tiles_of(const DecodeParams& p, int tile) {
 template <int D, bool E4M3, int NH, int HW>
 cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   using Sh = Shape<D, E4M3, NH, HW>;
-  static std::atomic<unsigned long long> smem_done{0};
+  static std::atomic<unsigned long long> done{0}, few_done{0}, many_done{0};
   auto* const kernel = decode_kernel<D, E4M3, NH, HW>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), 227 * 1024, smem_done);
+  cudaError_t e = prepare_once(reinterpret_cast<const void*>(kernel), 227 * 1024, done);
   if (e != cudaSuccess) return e;
   lc.group = HW;
   // At most one block per tile, at most the blocks that are resident at once.
@@ -938,24 +934,17 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
   const long long units = static_cast<long long>(p.batch) * (p.kv.heads_kv / HW);
   lc.by_unit = 2 * units <= lc.blocks;
-  kernel<<<dim3(lc.blocks, lc.chunks), Sh::kThreads, Sh::smem(lc.rows), s>>>(p, lc);
-  e = cudaGetLastError();
+  e = launch_pdl(kernel, dim3(lc.blocks, lc.chunks), dim3(Sh::kThreads), Sh::smem(lc.rows), s, p, lc);
   if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(lc.by_unit ? static_cast<unsigned>(units) : lc.blocks, lc.chunks * HW * lc.rows);
-  cfg.gridDim.z = D == 256 ? 2 : 1;
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  dim3 grid(lc.by_unit ? static_cast<unsigned>(units) : lc.blocks, lc.chunks * HW * lc.rows, D == 256 ? 2 : 1);
   // A unit lies in about blocks / units runs (ragged lengths: some in several
   // times as many).
-  if (8 * units > lc.blocks) return cudaLaunchKernelEx(&cfg, combine_kernel<D, (D < 128 ? D : 128) / 4>, p, lc);
-  cfg.gridDim.z = D / 32;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D, 8>, p, lc);
+  const bool few = 8 * units > lc.blocks;
+  auto* const combine = few ? combine_kernel<D, (D < 128 ? D : 128) / 4> : combine_kernel<D, 8>;
+  if (!few) grid.z = D / 32;
+  e = prepare_once(reinterpret_cast<const void*>(combine), 0, few ? few_done : many_done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(combine, grid, dim3(kJoinThreads), 0, s, p, lc);
 }
 
 // Whether tiles of HW key/value heads are taken: where their queries fit

@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams 
   __shared__ long long run_page[kPlanMaxThreads + 1];  // pages taken before it
   __shared__ long long warp_tok[32], warp_page[32];
   const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, lane = t & 31;
+  fa::pdl_wait();
   const int per = (p.batch + threads - 1) / threads;
   const int b0 = min(t * per, p.batch), b1 = min(b0 + per, p.batch);
   const long long start = p.free_start ? max(__ldg(p.free_start), 0) : 0;
@@ -315,6 +316,7 @@ __device__ __forceinline__ uint2 quantise8(uint4 x, const Scale& sc) {
 // of 64 to e4m3 (50 MB) BBBB us.
 template <bool E4M3, int ROWS>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+  fa::pdl_wait();
   constexpr int N = E4M3 ? 2 : 1;   // 16-byte pieces of input per thread and row: one piece of the cache
   const int per_head = p.kv.head_dim / (8 * N), per_row = p.kv.heads_kv * per_head;
   const int wide = min(per_row, kAppendThreads), rows_per_pass = kAppendThreads / wide;
@@ -406,8 +408,8 @@ int fa_kv_plan(int32_t* block_table, long long table_stride, int max_pages, cons
                      cu_new,       seq_lens_out, free_next};
   // a thread per request, up to a block's most
   const int threads = batch <= 256 ? 256 : batch <= 512 ? 512 : kPlanMaxThreads;
-  plan_kernel<<<blocks_for(num_tokens, threads, 2), threads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = fa::launch_pdl(plan_kernel, dim3(blocks_for(num_tokens, threads, 2)), dim3(threads), 0,
+                                 reinterpret_cast<cudaStream_t>(stream), p);
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
   return ok();
 }
@@ -450,11 +452,9 @@ int fa_kv_append(const fa_bf16* k, const fa_bf16* v, long long k_row_stride, lon
   const int rows = static_cast<long long>(num_tokens) * per_row >= 2ll * kAppendThreads * 152 * most ? most : 1;
   const dim3 grid(blocks_for(num_tokens, rows_per_pass * rows, 64), (per_row + kAppendThreads - 1) / kAppendThreads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (p.kv.e4m3 && rows > 1) append_kernel<true, 2><<<grid, kAppendThreads, 0, s>>>(p);
-  else if (p.kv.e4m3) append_kernel<true, 1><<<grid, kAppendThreads, 0, s>>>(p);
-  else if (rows > 1) append_kernel<false, 4><<<grid, kAppendThreads, 0, s>>>(p);
-  else append_kernel<false, 1><<<grid, kAppendThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  void (*const kernel)(AppendParams) = p.kv.e4m3 ? (rows > 1 ? append_kernel<true, 2> : append_kernel<true, 1>)
+                                                  : (rows > 1 ? append_kernel<false, 4> : append_kernel<false, 1>);
+  cudaError_t e = fa::launch_pdl(kernel, grid, dim3(kAppendThreads), 0, s, p);
   if (e != cudaSuccess) return cuda_fail(e, "append launch");
   return ok();
 }
