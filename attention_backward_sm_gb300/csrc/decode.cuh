@@ -970,7 +970,7 @@ cudaError_t launch_group(const DecodeParams& p, const Launch& lc, cudaStream_t s
 template <int D, bool E4M3>
 cudaError_t launch_rows(const DecodeParams& p, const Launch& lc, cudaStream_t s) {
   if (lc.rows <= 8) return launch_group<D, E4M3, 1>(p, lc, s);
-  if constexpr (D < 256) {
+  if constexpr (E4M3 && D < 256) {
     // more than 16 query heads on a key/value head: one of those at a time
     if (lc.rows > 24) return launch_shape<D, E4M3, 4, 1>(p, lc, s);
     if (lc.rows > 16) return launch_shape<D, E4M3, 3, 1>(p, lc, s);

@@ -42,19 +42,22 @@ struct FastDiv {
   }
 };
 
-// Programmatic dependent launch.  These kernels are set up while the kernel
-// before them in the stream still runs (2 to 4 us less between two small
-// calls): pdl_wait, before anything is read or written, waits until that one
-// has ended and its writes are visible; pdl_launch lets the next one be set
-// up once all blocks of this one have begun.
+// Programmatic dependent launch.  These kernels' launches need not wait for
+// the kernel before them in the stream to be flushed; pdl_wait, before
+// anything is read or written, waits until it has ended and its writes are
+// visible (calls one after the other: append of 64 rows 4.1 -> 2.8 us each).
+// pdl_launch lets the next kernel be set up while this one still runs.  Only
+// decode does that, for its combine: a decode block that was set up beside
+// others found its SM's shared memory in pieces, and fewer of its neighbours
+// fitted for as long as it ran (64 requests, 16 heads of 64: 97 -> 115 us
+// with combine kernels that let the next decode start).
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Once per kernel and device: its dynamic shared memory, and the largest
-// split of an SM's memory for shared memory even where the kernel needs
-// little.  A decode block that is set up beside blocks with a smaller split
-// would run with fewer neighbours for as long as it lives, since the split
-// only changes on an idle SM (64 requests, 16 heads of 64: 97 and 115 us).
+// split of an SM's memory for shared memory, also for the combine kernel,
+// which needs little: the split only changes on an idle SM, and that kernel's
+// blocks may be the first on theirs.
 inline cudaError_t prepare_once(const void* kernel, int smem, std::atomic<unsigned long long>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

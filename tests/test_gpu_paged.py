@@ -215,48 +215,62 @@ def test_append_many_rows_and_wide_rows(tokens, heads_kv, dim):
 
 
 # ------------------------------------------------------------------ decode
-GROUPS = [(1, 1), (4, 4), (8, 2), (6, 2), (14, 2), (9, 1), (16, 1), (20, 1), (40, 1)]
+# query and key/value heads: 1 to 16 to a key/value head and more (in chunks),
+# key/value heads that go by 4, by 2 or one at a time
+GROUPS = [(1, 1), (4, 4), (8, 2), (6, 2), (14, 2), (9, 1), (16, 1), (20, 1), (40, 1), (12, 12), (20, 4), (32, 4),
+          (44, 4), (64, 4), (32, 2), (18, 6), (27, 1), (33, 1), (48, 2)]
 
 
+# wide: a block table long enough for tiles of several key/value heads, which
+# calls with few keys at most do not take
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("heads,heads_kv", GROUPS)
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-def test_decode_head_layouts(heads, heads_kv, dim, kv):
-    p = Problem([1, 0, 63, 64, 65, 130, 300], heads, heads_kv, dim, 16, kv, seed=heads * dim)
+def test_decode_head_layouts(heads, heads_kv, dim, kv, wide):
+    p = Problem([1, 0, 63, 64, 65, 130, 300], heads, heads_kv, dim, 16, kv, seed=heads * dim,
+                extra_width=8000 if wide else 1)
     p.check(*p.run())
 
 
 @pytest.mark.parametrize("page", [1, 3, 8, 24, 64, 100, 256])
 @pytest.mark.parametrize("window", [0, 1, 17, 64, 1000])
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-def test_decode_pages_and_windows(page, window, kv):
-    p = Problem([1, page, page + 1, 127, 128, 129, 517, 0, 16], 4, 2, 128, page, kv, window, seed=page + window)
+@pytest.mark.parametrize("heads_kv,wide", [(2, False), (4, True)])
+def test_decode_pages_and_windows(page, window, kv, heads_kv, wide):
+    p = Problem([1, page, page + 1, 127, 128, 129, 517, 0, 16], 4, heads_kv, 128, page, kv, window, seed=page + window,
+                extra_width=1 + (100_000 // page if wide else 0))
     p.check(*p.run())
 
 
 @pytest.mark.parametrize("layout", ["plain", "heads_first", "gaps"])
 @pytest.mark.parametrize("dim,kv", [(64, "bf16"), (128, "e4m3"), (256, "bf16")])
-def test_decode_layouts_and_strided_queries(layout, dim, kv):
-    p = Problem([200, 33, 1, 90], 6, 3, dim, 16, kv, layout=layout, seed=dim)
+@pytest.mark.parametrize("heads,heads_kv,width", [(6, 3, 1), (8, 4, 8000)])
+def test_decode_layouts_and_strided_queries(layout, dim, kv, heads, heads_kv, width):
+    p = Problem([200, 33, 1, 90], heads, heads_kv, dim, 16, kv, layout=layout, seed=dim, extra_width=width)
     fused = torch.full((4, 12, dim), float("nan"), dtype=torch.bfloat16)
-    fused[:, :6] = p.q
-    p.check(*p.run(q=fused.to(DEV)[:, :6]))
+    fused[:, :heads] = p.q
+    p.check(*p.run(q=fused.to(DEV)[:, :heads]))
 
 
 @pytest.mark.parametrize("batch,hi,heads,heads_kv,dim,kv", [
     (1, 20000, 8, 2, 128, "bf16"),        # one request over every SM
     (1, 9000, 1, 1, 64, "e4m3"),
+    (1, 30000, 4, 4, 64, "bf16"),         # one head group over every SM
+    (2, 12000, 8, 8, 128, "e4m3"),
     (300, 90, 4, 4, 64, "bf16"),          # many more requests than SMs
+    (700, 40, 4, 1, 64, "e4m3"),
     (33, 3000, 4, 1, 256, "bf16"),        # ragged
     (40, 2500, 24, 1, 128, "e4m3")])
 def test_decode_splits(batch, hi, heads, heads_kv, dim, kv):
     lens = [int(x) for x in np.random.default_rng(batch).integers(0, hi + 1, batch)]
     lens[0] = hi
-    p = Problem(lens, heads, heads_kv, dim, 16, kv, seed=batch)
-    o, lse = p.run()
-    p.check(o, lse)
-    again = p.run()
-    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    for width in (1, 20000):
+        p = Problem(lens, heads, heads_kv, dim, 16, kv, seed=batch, extra_width=width)
+        o, lse = p.run()
+        p.check(o, lse)
+        again = p.run()
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
@@ -276,11 +290,12 @@ def test_decode_peaked_growing_and_shrinking_scores(kv):
 
 
 def test_decode_bad_pages_are_not_seen():
-    p = Problem([70, 200, 40, 10], 4, 2, 128, 16, seed=12,
-                bad=[(0, 1, -1), (0, 4, 10 ** 9), (1, 0, -7), (1, 12, 2 ** 31 - 1), (3, 0, -1)])
-    o, lse = p.run()
-    p.check(o, lse)
-    assert torch.all(o[3] == 0) and torch.all(lse[3] == -float("inf"))
+    for heads_kv, width in ((2, 1), (4, 8000)):
+        p = Problem([70, 200, 40, 10], 4, heads_kv, 128, 16, seed=12, extra_width=width,
+                    bad=[(0, 1, -1), (0, 4, 10 ** 9), (1, 0, -7), (1, 12, 2 ** 31 - 1), (3, 0, -1)])
+        o, lse = p.run()
+        p.check(o, lse)
+        assert torch.all(o[3] == 0) and torch.all(lse[3] == -float("inf"))
 
 
 def test_decode_lengths_are_clamped_to_the_table():
@@ -293,14 +308,26 @@ def test_decode_lengths_are_clamped_to_the_table():
 
 def test_decode_visible_nan_and_inf_reach_the_output():
     """A NaN key or value that is seen shows, in its request and head only."""
-    p = Problem([50, 50], 4, 2, 64, 16, seed=14)
-    clean = p.run()
-    p.v[p.table[0, 1].long(), 3, 0, 5] = float("nan")
-    p.k[p.table[1, 0].long(), 2, 1, 7] = float("nan")
-    o, lse = p.run()
-    assert torch.isnan(o[0, :2, 5]).all() and torch.isnan(o[1, 2:]).all() and torch.isnan(lse[1, 2:]).all()
-    assert torch.equal(o[0, 2:], clean[0][0, 2:]) and torch.equal(o[1, :2], clean[0][1, :2])
-    assert torch.equal(lse[0], clean[1][0])
+    for kv in ("bf16", "e4m3"):
+        p = Problem([50, 50], 4, 2, 64, 16, kv, seed=14)
+        clean = p.run()
+        nan = torch.tensor(float("nan")).to(p.k.dtype)
+        p.v[p.table[0, 1].long(), 3, 0, 5] = nan
+        p.k[p.table[1, 0].long(), 2, 1, 7] = nan
+        o, lse = p.run()
+        assert torch.isnan(o[0, :2, 5]).all() and torch.isnan(o[1, 2:]).all() and torch.isnan(lse[1, 2:]).all()
+        assert torch.equal(o[0, 2:], clean[0][0, 2:]) and torch.equal(o[1, :2], clean[0][1, :2])
+        assert torch.equal(lse[0], clean[1][0])
+    # -inf scores beside finite ones weigh nothing, wherever they come first
+    for at in (0, 49):
+        p = Problem([50], 1, 1, 64, 16, seed=15)
+        p.q[..., 0] = 1.0
+        p.k[p.table[0, at // 16].long(), at % 16, 0, 0] = -float("inf")
+        o, lse = p.run()
+        keep = [j for j in range(50) if j != at]
+        k = torch.stack([p.k[p.table[0, j // 16].long(), j % 16, 0] for j in keep]).double()
+        want = torch.logsumexp(p.scale * (k @ p.q[0, 0].double()), 0)
+        assert abs(lse.item() - want.item()) < 1e-4 and torch.isfinite(o).all()
 
 
 def test_decode_empty_table_and_no_lse():
