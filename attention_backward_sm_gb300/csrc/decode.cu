@@ -24,6 +24,7 @@ decode::Launch split_heads(int heads, int heads_kv, int head_dim, bool e4m3) {
   lc.chunks = (G + lc.rows - 1) / lc.rows;
   lc.group = 1;
   lc.blocks = 0;
+  lc.tile_shift = 0;
   lc.by_unit = 0;
   return lc;
 }

@@ -88,6 +88,7 @@ struct Shape {
   static constexpr int kOffZero = (kOffScan + kThreads / 32 * 4 + 16 + 15) / 16 * 16;   // 16 zero bytes
   static constexpr int kOffQ = kOffZero + 16;   // query rows of kStages units
   static_assert(kJoinHeads >= 8, "join buffer");
+  static_assert(kTile == 16 || kTile == 32 || kTile == 64 || kTile == 128, "tile_shift");
   static_assert(kKeys == 16 || kKeys == 32, "a word of seen keys");
   static_assert(kTile <= kThreads && kTile % 16 == 0, "a thread per key looks up its page");
   static constexpr int smem(int rows) { return kOffQ + kStages * HW * rows * D * 2; }
@@ -97,14 +98,15 @@ struct Shape {
   static_assert(HW > 1 || fits(kHeads), "shared memory");
 };
 
-// A unit that the end of the run it starts in cuts, if any: runs [run, last]
-// hold its partial results, in run's slot `slot` and the others' slot 0.  One
-// entry per unit, or where there are more units than runs, one per run.
+// A unit that the end of a run cuts, entered by the run it starts in: runs
+// [this one, last] hold its partial results, this one's in slot `slot`, the
+// others' in slot 0.  (With fewer units than runs the combine kernel has a
+// block per unit, which works this out from the lengths instead.)
 struct Cut {
   int unit;    // b * (heads_kv / HW) + head group, or -1: none
-  int run;
   int last;
   int slot;
+  int pad;
 };
 
 struct Launch {
@@ -112,7 +114,8 @@ struct Launch {
   int chunks;      // chunks of the G query heads of a key/value head
   int group;       // key/value heads per tile
   int blocks;      // blocks per chunk
-  int by_unit;     // cuts are entered by unit
+  int tile_shift;  // log2 of the keys per tile
+  int by_unit;     // combine goes by units, not by cuts
 };
 
 // Workspace: [blocks] cuts, then partial results [blocks][2 slots]: [HW][rows]
@@ -196,12 +199,15 @@ struct Lens {
   const int32_t* seq;
   int most;      // max_pages * page_size
   int window;
-  __device__ __forceinline__ int len(int b) const { return min(max(__ldg(seq + b), 0), most); }
+  __device__ __forceinline__ int len(int b) const { return min(max(*(seq + b), 0), most); }
   __device__ __forceinline__ int first(int len) const { return window > 0 ? max(0, len - window) : 0; }
   // A request without keys has one (empty) tile: its row is written too.
   template <int TILE>
   __device__ __forceinline__ int tiles(int len) const {
     return max(1, (len - first(len) + TILE - 1) / TILE);
+  }
+  __device__ __forceinline__ int tiles(int len, int tile_shift) const {
+    return max(1, (len - first(len) + (1 << tile_shift) - 1) >> tile_shift);
   }
 };
 
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   const Runs runs(tiles.total, lc.blocks);
   int4* const cuts = reinterpret_cast<int4*>(p.work) + blockIdx.y * lc.blocks;
   if (static_cast<int>(blockIdx.x) >= runs.runs) {
-    if (!lc.by_unit && tid == 0) cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (tid == 0) cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
   const int start = runs.start(blockIdx.x), n = runs.start(blockIdx.x + 1) - start;
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   auto look_up = [&](const Place<TILE>& at) -> int {
     const int key = at.first + at.t * TILE + tid;
     if (tid >= TILE || key >= at.len) return -1;
-    return __ldg(p.table + at.b * p.table_stride + p.page_div.quotient(key));
+    return *(p.table + at.b * p.table_stride + p.page_div.quotient(key));
   };
   auto store_offset = [&](const Place<TILE>& at, int page, int ring) {
     if (tid >= TILE) return;
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
     if (fresh) {
       fresh = false;
       const uint32_t qb = sbase + S::kOffQ + q_slot * q_bytes + hw * lc.rows * D * 2;
-      const float scale = p.scale * kLog2e * (p.kv.k_scale ? __ldg(p.kv.k_scale + here.hk * HW + hw) : 1.f);
+      const float scale = p.scale * kLog2e * (p.kv.k_scale ? *(p.kv.k_scale + here.hk * HW + hw) : 1.f);
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
 #pragma unroll
@@ -671,7 +677,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) l[i][c] += __shfl_xor_sync(0xffffffffu, l[i][c], off);
       if constexpr (KW == 1) {
-        const float vs = p.kv.v_scale ? __ldg(p.kv.v_scale + here.hk * HW + hw) : 1.f;
+        const float vs = p.kv.v_scale ? *(p.kv.v_scale + here.hk * HW + hw) : 1.f;
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
           float inv[2];
@@ -786,7 +792,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
             }
             top -= kShift;
             if (whole) {
-              const float vs = p.kv.v_scale ? __ldg(p.kv.v_scale + here.hk * HW + h) : 1.f;
+              const float vs = p.kv.v_scale ? *(p.kv.v_scale + here.hk * HW + h) : 1.f;
               const float inv = sum == 0.f ? 0.f : __fdividef(vs, sum);
               const long long to = out_row + h * G + row;
               uint2 out;
@@ -806,11 +812,9 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
           }
         }
       }
-      if (tid == 0 && (lc.by_unit ? starts_here : s + 1 == n)) {
-        const int unit = here.b * groups + here.hk;
-        cuts[lc.by_unit ? unit : blockIdx.x] =
-            make_int4(starts_here && !unit_done ? unit : -1, blockIdx.x, runs.of(start + s - here.t + here.nt - 1), slot);
-      }
+      if (tid == 0 && s + 1 == n && !lc.by_unit)
+        cuts[blockIdx.x] = make_int4(starts_here && !unit_done ? here.b * groups + here.hk : -1,
+                                     runs.of(start + s - here.t + here.nt - 1), slot, 0);
       fresh = true;
       first_piece = false;
       q_slot = q_slot + 1 == ST ? 0 : q_slot + 1;
@@ -825,8 +829,10 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
 // One block per (cut, query head of a head group, 4 COLS columns): joins the
 // partial results of the runs the unit lies in, group g of its threads those
 // of runs g, g + GROUPS, ... in one pass with a running maximum, then the
-// groups in order.  Few runs: 128 columns (or all); many: 32 columns by 16 groups.
-// Blocks are small so that they can wait beside the main kernel's.
+// groups in order.  Few runs: 128 columns (or all); many: 32 columns by 16
+// groups.  Blocks are small so that they can wait beside the main kernel's;
+// the lengths, which say what runs a unit lies in, were complete before that
+// kernel let this one be set up, and are read meanwhile.
 constexpr int kJoinThreads = 128;
 
 template <int D, int COLS>
@@ -837,14 +843,54 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
   const int tid = threadIdx.x;
   const int local = blockIdx.y % (lc.group * lc.rows), chunk = blockIdx.y / (lc.group * lc.rows);
   const int head = local / lc.rows, row = local % lc.rows;   // of the group; of the head's chunk
-  const int G = p.heads / p.kv.heads_kv;
-  pdl_wait();
-  if (chunk * lc.rows + row >= G) return;
-  const int4 cut = *(reinterpret_cast<const int4*>(p.work) + chunk * lc.blocks + blockIdx.x);
-  if (cut.x < 0) return;
-  const int groups = p.kv.heads_kv / lc.group;
-  const int b = cut.x / groups, hk = cut.x % groups * lc.group + head;
-  const int run = cut.y, n = cut.z - run + 1, first_slot = cut.w;
+  const int G = p.heads / p.kv.heads_kv, groups = p.kv.heads_kv / lc.group;
+  int unit, run, last, first_slot;
+  if (lc.by_unit) {
+    // the tiles before this unit and in all
+    __shared__ int s_before[kJoinThreads / 32], s_total[kJoinThreads / 32];
+    unit = blockIdx.x;
+    const Lens L{p.seq_lens, p.max_pages * p.kv.page_size, p.window};
+    const int b = unit / groups;
+    int before = 0, total = 0;
+    for (int i = tid; i < p.batch; i += kJoinThreads) {
+      const int nt = L.tiles(L.len(i), lc.tile_shift);
+      total += nt;
+      if (i < b) before += nt;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, off);
+      total += __shfl_xor_sync(0xffffffffu, total, off);
+    }
+    if (tid % 32 == 0) {
+      s_before[tid / 32] = before;
+      s_total[tid / 32] = total;
+    }
+    __syncthreads();
+    before = total = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      before += s_before[w];
+      total += s_total[w];
+    }
+    const Runs runs(total * groups, lc.blocks);
+    const int nt = L.tiles(L.len(b), lc.tile_shift), first = before * groups + (unit - b * groups) * nt;
+    run = runs.of(first);
+    last = runs.of(first + nt - 1);
+    first_slot = first == runs.start(run) ? 0 : 1;
+    pdl_wait();
+  } else {
+    pdl_wait();
+    const int4 cut = *(reinterpret_cast<const int4*>(p.work) + chunk * lc.blocks + blockIdx.x);
+    if (cut.x < 0) return;
+    unit = cut.x;
+    run = blockIdx.x;
+    last = cut.y;
+    first_slot = cut.z;
+  }
+  if (last == run || chunk * lc.rows + row >= G) return;   // not cut; no such head
+  const int b = unit / groups, hk = unit % groups * lc.group + head;
+  const int n = last - run + 1;
   const float* const parts = parts_of(p.work, static_cast<size_t>(lc.blocks) * lc.chunks);
   const int part_rows = lc.group * lc.rows;
   const size_t pf = part_floats(part_rows, D);
@@ -889,7 +935,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
     acc.z = fmaf(f, a.z, acc.z);
     acc.w = fmaf(f, a.w, acc.w);
   }
-  const float inv = sum == 0.f ? 0.f : (p.kv.v_scale ? __ldg(p.kv.v_scale + hk) : 1.f) / sum;
+  const float inv = sum == 0.f ? 0.f : (p.kv.v_scale ? *(p.kv.v_scale + hk) : 1.f) / sum;
   const long long at = static_cast<long long>(b) * p.heads + hk * G + chunk * lc.rows + row;
   uint2 out;
   out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
@@ -934,6 +980,7 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
   const long long units = static_cast<long long>(p.batch) * (p.kv.heads_kv / HW);
   lc.by_unit = 2 * units <= lc.blocks;
+  lc.tile_shift = Sh::kTile == 16 ? 4 : Sh::kTile == 32 ? 5 : Sh::kTile == 64 ? 6 : 7;
   e = launch_pdl(kernel, dim3(lc.blocks, lc.chunks), dim3(Sh::kThreads), Sh::smem(lc.rows), s, p, lc);
   if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
   dim3 grid(lc.by_unit ? static_cast<unsigned>(units) : lc.blocks, lc.chunks * HW * lc.rows, D == 256 ? 2 : 1);

@@ -133,8 +133,8 @@ struct Request {
 
 __device__ __forceinline__ Request load_request(const PlanParams& p, int b) {
   Request r;
-  r.seq = max(__ldg(p.seq_lens + b), 0);
-  r.fresh = max(__ldg(p.new_lens + b), 0);
+  r.seq = max(*(p.seq_lens + b), 0);
+  r.fresh = max(*(p.new_lens + b), 0);
   const int after = clamp_int(static_cast<long long>(r.seq) + r.fresh);
   // ceil(n / page_size) of n >= 0
   const int have = r.seq ? p.page_div.quotient(r.seq - 1) + 1 : 0;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams 
   fa::pdl_wait();
   const int per = (p.batch + threads - 1) / threads;
   const int b0 = min(t * per, p.batch), b1 = min(b0 + per, p.batch);
-  const long long start = p.free_start ? max(__ldg(p.free_start), 0) : 0;
+  const long long start = p.free_start ? max(*(p.free_start), 0) : 0;
   long long tok = 0, page = 0;
   for (int b = b0; b < b1; ++b) {
     const Request r = load_request(p, b);
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams 
   if (blockIdx.x == 0) {
     long long at = run_tok[t];
     for (int b = b0; b < b1; ++b) {
-      const int seq = max(__ldg(p.seq_lens + b), 0), fresh = max(__ldg(p.new_lens + b), 0);
+      const int seq = max(*(p.seq_lens + b), 0), fresh = max(*(p.new_lens + b), 0);
       p.cu_new[b] = clamp_int(at);
       p.seq_lens_out[b] = clamp_int(static_cast<long long>(seq) + fresh);
       at += fresh;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams 
           id = p.table[b * p.table_stride + pi];
         } else {
           const long long f = taken + (pi - r.have);
-          id = f < p.num_free ? __ldg(p.free_pages + f) : -1;
+          id = f < p.num_free ? *(p.free_pages + f) : -1;
           if (in_page == 0) p.table[b * p.table_stride + pi] = id;
         }
         if (id >= 0) slot = static_cast<long long>(id) * p.page_size + in_page;
@@ -265,7 +265,7 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
   return r;
@@ -278,7 +278,7 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
 // infinity, between which everything lies.
 struct Scale {
   float s, lo, hi;
-  __device__ __forceinline__ explicit Scale(const float* p, int h) : s(p ? __ldg(p + h) : 1.f) {
+  __device__ __forceinline__ explicit Scale(const float* p, int h) : s(p ? *(p + h) : 1.f) {
     const bool plain = s >= 0x1p-100f && s <= 0x1p100f;
     const float inv = 1.f / s;
     lo = plain ? inv * (1.f - 0x1p-21f) : 0.f;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const long long r = row + i * rows_per_pass;
-      at[i] = r < p.num_tokens ? __ldg(reinterpret_cast<const long long*>(p.slots) + r) : -1;
+      at[i] = r < p.num_tokens ? *(reinterpret_cast<const long long*>(p.slots) + r) : -1;
       if (at[i] >= num_slots) at[i] = -1;
     }
 #pragma unroll

@@ -46,6 +46,8 @@ struct FastDiv {
 // the kernel before them in the stream to be flushed; pdl_wait, before
 // anything is read or written, waits until it has ended and its writes are
 // visible (calls one after the other: append of 64 rows 4.1 -> 2.8 us each).
+// What an earlier kernel may have written is read with plain loads: it can
+// change while these kernels are already there, which ld.global.nc excludes.
 // pdl_launch lets the next kernel be set up while this one still runs.  Only
 // decode does that, for its combine: a decode block that was set up beside
 // others found its SM's shared memory in pieces, and fewer of its neighbours

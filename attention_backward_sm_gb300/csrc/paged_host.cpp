@@ -10,6 +10,7 @@
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/TensorImpl.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -375,14 +376,18 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     o = out.next({batch, heads, dim}, at::kBFloat16);
     lse = out.next({batch, heads}, at::kFloat);
   }
-  if (!work && need > 0) work = place.bytes(static_cast<int64_t>(need));
-  const size_t work_bytes = work ? work->nbytes() : 0;
+  // A workspace of this call alone goes back to the allocator with the return,
+  // for later work on the same stream.
+  c10::DataPtr own_work;
+  if (!work && need > 0) own_work = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+  void* const work_ptr = work ? ptr<void>(*work) : own_work.get();
+  const size_t work_bytes = work ? work->nbytes() : need;
   check(unlocked([&] {
     return fa_decode(ptr<fa_bf16>(q), q_stride, ptr<void>(c.k), ptr<void>(c.v), c.type, c.ks(), c.vs(),
                      c.k.stride(0), c.k.stride(1), c.k.stride(2), c.pages, c.page_size, ptr<int32_t>(table.t),
                      table.stride, table.width, ptr<int32_t>(seq), table.batch, h32, c.heads_kv, c.dim, window,
                      static_cast<float>(scale), ptr<fa_bf16>(o), lse ? ptr<float>(*lse) : nullptr,
-                     work ? ptr<void>(*work) : nullptr, work_bytes, place.stream());
+                     work_ptr, work_bytes, place.stream());
   }));
   if (!lse) {
     PyObject* w = THPVariable_Wrap(o);
