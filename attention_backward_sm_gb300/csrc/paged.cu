@@ -490,6 +490,8 @@ int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
                           heads, heads_kv);
   if (static_cast<long long>(heads) * head_dim > 65535 * 64)
     return set_last_error(FA_ERR_UNSUPPORTED, "heads * head_dim too large (%d * %d)", heads, head_dim);
+  if (heads / heads_kv > 1024)
+    return set_last_error(FA_ERR_UNSUPPORTED, "at most 1024 query heads per key/value head, got %d", heads / heads_kv);
   if (window < 0) return set_last_error(FA_ERR_INVALID_ARG, "window must be >= 0, got %d", window);
   if (!isfinite(scale)) return set_last_error(FA_ERR_INVALID_ARG, "scale must be finite");
   if (max_pages < 0) return set_last_error(FA_ERR_INVALID_ARG, "max_pages must be >= 0, got %d", max_pages);

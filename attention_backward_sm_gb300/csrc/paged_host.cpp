@@ -158,10 +158,12 @@ class Place {
  public:
   explicit Place(const Tensor& t) : device_(t.device()) {
     if (!device_.is_cuda()) refuse("the tensors must be on a CUDA device, got " + device_.str());
+    used_[count_++] = &t;
   }
   Place& with(const Tensor& t, const char* name) {
     if (t.device() != device_)
       refuse(std::string(name) + " is on " + t.device().str() + ", the others on " + device_.str());
+    used_[count_++] = &t;
     return *this;
   }
   Place& with(const std::optional<Tensor>& t, const char* name) { return t ? with(*t, name) : *this; }
@@ -174,8 +176,13 @@ class Place {
                   type = attr(stream, "device_type");
     if (index != device_.index())
       refuse("the stream is on device " + std::to_string(index) + ", the tensors on " + device_.str());
-    stream_guard_.emplace(c10::cuda::CUDAStream::unpack3(id, static_cast<c10::DeviceIndex>(index),
-                                                         static_cast<c10::DeviceType>(type)));
+    const auto s = c10::cuda::CUDAStream::unpack3(id, static_cast<c10::DeviceIndex>(index),
+                                                  static_cast<c10::DeviceType>(type));
+    // The tensors belong to other streams perhaps: their memory is not to be
+    // handed out again before this stream is done with it.
+    for (int i = 0; i < count_; ++i)
+      c10::cuda::CUDACachingAllocator::recordStream(used_[i]->storage().data_ptr(), s);
+    stream_guard_.emplace(s);
     return *this;
   }
   fa_stream_t stream() const {
@@ -193,6 +200,8 @@ class Place {
     return n;
   }
   c10::Device device_;
+  const Tensor* used_[16];   // every tensor of the call
+  int count_ = 0;
   c10::cuda::OptionalCUDAGuard device_guard_;
   std::optional<c10::cuda::CUDAStreamGuard> stream_guard_;
 };

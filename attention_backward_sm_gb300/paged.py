@@ -11,7 +11,8 @@ is checked in the host extension (csrc/paged_host.cpp) and raises
 ValueError; FabwdError comes from the C layer.
 
 stream: a torch.cuda.Stream of the tensors' device to run on (and to
-allocate outputs on) instead of the current one.
+allocate outputs on) instead of the current one.  The caller orders it after
+what writes the inputs; their memory is kept until the stream is done.
 """
 from __future__ import annotations
 

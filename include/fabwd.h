@@ -330,8 +330,8 @@ int fa_kv_plan(int32_t* block_table, long long table_stride, int max_pages,
  * of a fused projection need no copy), into the cache: row t goes to
  * slots[t]; rows whose slot is outside the cache (-1) are skipped and slots
  * that no row names are left as they were.  The slots of one call must
- * differ from one another: of rows with the same slot any one may remain,
- * or parts of several.  kv_type FA_KV_E4M3 stores
+ * differ from one another (of rows with the same slot any one may remain, or
+ * parts of several), and k and v must not overlap the cache.  kv_type FA_KV_E4M3 stores
  * e4m3(x / k_scale[head]) (v_scale for v; NULL: 1), round to nearest even,
  * saturating at +-448; NaN stays NaN.  Scales: [Hkv] float32 on the device,
  * positive; NULL with FA_KV_BF16. */
@@ -352,7 +352,7 @@ size_t fa_decode_workspace_size(int batch, int heads, int heads_kv, int head_dim
  * [max(0, seq_lens[b] - window), seq_lens[b]) (window 0: all).  The new
  * token's own key and value are in the cache already (fa_kv_append) and
  * count in seq_lens.  Lengths are clamped to max_pages * page_size.  Query
- * head h reads key/value head h / (H / Hkv).  A row that sees no key gets
+ * head h reads key/value head h / (H / Hkv), at most 1024 of them each.  A row that sees no key gets
  * o = 0, lse = -inf.  Contents of slots that are not seen do not matter
  * (NaN included).  o must not overlap q.  workspace: fa_decode_workspace_size() bytes, 16-byte
  * aligned, contents arbitrary; calls whose work overlaps on the GPU need one

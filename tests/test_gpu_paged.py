@@ -523,3 +523,24 @@ def test_stream_argument():
     o, lse = f.decode(**{**args, "q": late}, stream=stream)
     stream.synchronize()
     assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])
+
+
+def test_stream_argument_keeps_the_inputs():
+    """Inputs dropped right after a call on another stream: their memory is
+    not reused before that stream has read them."""
+    f = fab()
+    p = Problem([300, 40], 4, 2, 64, 16, seed=23)
+    plain = p.run()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    args = p.device()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(50_000_000)
+    o, lse = f.decode(**args, stream=stream)
+    sizes = [(t.shape, t.dtype) for t in args.values() if torch.is_tensor(t)]
+    del args
+    junk = [torch.full(s, 1.0, device=DEV).to(d) for s, d in sizes for _ in range(3)]
+    stream.synchronize()
+    assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])
+    assert len(junk) == 3 * len(sizes)

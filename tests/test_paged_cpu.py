@@ -144,6 +144,7 @@ def _decode_rc(lib, **kw):
     (dict(seq=None), 1, b"NULL"), (dict(table=None), 1, b"NULL"), (dict(kc=None), 1, b"NULL"),
     (dict(o=ctypes.c_void_p(8)), 1, b"aligned"), (dict(seq=ctypes.c_void_p(18)), 1, b"aligned"),
     (dict(o=P), 1, b"overlap"), (dict(o=ctypes.c_void_p(16 + 1024)), 1, b"overlap"),
+    (dict(heads=1025, heads_kv=1, qs=1025 * 128), 2, b"1024"),
     (dict(batch=1 << 20, width=1 << 14), 2, b"too many"),
     (dict(heads=1 << 20, qs=1 << 27), 2, b"too large"),
     (dict(kind=0, v_scale=P), 1, b"e4m3"), (dict(slot_stride=100), 1, b"slot_stride")])
