@@ -10,14 +10,16 @@ cudaError_t launch_decode_d256(const DecodeParams& p, const decode::Launch& lc, 
 
 namespace {
 
-// The G query heads of a key/value head in chunks, as equal as can be: of at
-// most 16, whose keys the other chunks' blocks find in the L2, or, for e4m3 at
-// head_dim 64 and 128, of at most 32.  Chunks of 16 against 32: 64 requests of
-// 256 to 8192 keys, 32 heads on one of 128, bf16: 30.6 and 34.5 us; 48 on two,
-// e4m3: 43 and 37 us (converting the keys twice costs more than the second
-// read).
+// The G query heads of a key/value head in chunks, as equal as can be, each of
+// which reads the keys (the second and later ones mostly from the L2).  A chunk
+// holds at most what the registers hold: 32 heads at head_dim 64, 24 (e4m3)
+// or 16 at 128, 16 at 256.  32 requests of 8192 keys, 8 key/value heads, one
+// chunk against two: d = 64, 256 query heads, bf16 129 and 161 us, e4m3 97 and
+// 110; d = 128, 192 query heads, e4m3 138 and 185, but 256 query heads 310
+// and 189 (spilled registers); bf16, 64 requests, 32 heads on one: 34.5 and
+// 30.6 (half the warps).
 decode::Launch split_heads(int heads, int heads_kv, int head_dim, bool e4m3) {
-  const int G = heads / heads_kv, most = e4m3 && head_dim < 256 ? 32 : 16;
+  const int G = heads / heads_kv, most = head_dim == 64 ? 32 : head_dim == 128 && e4m3 ? 24 : 16;
   decode::Launch lc;
   lc.chunks = (G + most - 1) / most;
   lc.rows = (G + lc.chunks - 1) / lc.chunks;
