@@ -63,7 +63,8 @@ template <int D, bool E4M3, int NH, int HW>
 struct Shape {
   static constexpr int kElem = E4M3 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
-  static constexpr int kRowsPerTile = E4M3 && D != 128 ? 128 : 64;   // heads x keys
+  static constexpr int kRowsPerTile =   // heads x keys
+      E4M3 && (D == 64 || (D == 256 && NH > 1)) ? 128 : 64;
   static constexpr int kTile = kRowsPerTile / HW;                    // keys
   static constexpr int kHeadBytes = kTile * kRowBytes;
   static constexpr int kTileBytes = kRowsPerTile * kRowBytes;        // of K, and of V
