@@ -621,8 +621,10 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
                                          ? fmaf(x[k][i][2 * u + c], factor[i][c], ref) : -INFINITY;
           }
       }
-      // P^T, rounded to 16 bits for the second product, summed in 32.
-      uint32_t pf[KT][NH][2];
+      // P^T for the second product (the sums take it in 32 bits): in fp16 (2^-11
+      // off), or beside bf16 values as the sum of two bf16 numbers (2^-17 off).
+      // One bf16 number alone would be off by as much as the rounding of o.
+      uint32_t pf[KT][NH][2], pr[KT][NH][2];
 #pragma unroll
       for (int k = 0; k < KT; ++k)
 #pragma unroll
@@ -632,8 +634,16 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
           for (int c = 0; c < 4; ++c) e[c] = ex2_approx(y[k][i][c]);
           l[i][0] += e[0] + e[2];
           l[i][1] += e[1] + e[3];
-          pf[k][i][0] = transposed(E4M3 ? pack_f16x2(e[0], e[1]) : pack_bf16x2(e[0], e[1]));
-          pf[k][i][1] = transposed(E4M3 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if constexpr (E4M3) {
+              pf[k][i][u] = transposed(pack_f16x2(e[2 * u], e[2 * u + 1]));
+            } else {
+              const uint32_t high = pack_bf16x2(e[2 * u], e[2 * u + 1]);
+              pf[k][i][u] = transposed(high);
+              pr[k][i][u] = transposed(pack_bf16x2(e[2 * u] - bf_lo(high), e[2 * u + 1] - bf_hi(high)));
+            }
+          }
         }
       // O^T += V^T P^T
 #pragma unroll
@@ -645,7 +655,10 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
             uint32_t a[4];
             ldsm4t(a, vt + swizzled<RB>(r + (lane & 7) + ((lane >> 4) << 3), c0 / 8 + 2 * j + ((lane >> 3) & 1)));
 #pragma unroll
-            for (int i = 0; i < NH; ++i) mma<false>(o[i][j], a, pf[k][i][0], pf[k][i][1]);
+            for (int i = 0; i < NH; ++i) {
+              mma<false>(o[i][j], a, pf[k][i][0], pf[k][i][1]);
+              mma<false>(o[i][j], a, pr[k][i][0], pr[k][i][1]);
+            }
           }
         } else {
           // Transposed as 16-bit units, a register holds two keys' bytes of two

@@ -5,9 +5,9 @@ roundoff of a stored type (bf16: 2^-8) and fp32 sums that may truncate
 (2^-23 per addition),
   * a score of d products is off by at most delta = (d + 4) 2^-23 max|x|,
     |x| the sum of the absolute products, so every weight by 2 delta;
-  * weights are rounded once to 16 bits (u) and summed over n keys
-    (n 2^-23), o is rounded to bf16 (u |o|):
-    |o - ref| <= u |o| + (1 + 2^-6) (u + 2 delta + (n + 32) 2^-23) sum p |v|
+  * weights are rounded to w (fp16 for e4m3 caches: 2^-11; two bf16 numbers:
+    2^-16) and summed over n keys (n 2^-23), o is rounded to bf16 (u |o|):
+    |o - ref| <= u |o| + (1 + 2^-6) (w + 2 delta + (n + 32) 2^-23) sum p |v|
   * |lse - ref| <= 2 delta + (n + 32) 2^-23 + 2^-22 |lse|.
 plan and append move whole numbers and bits: they are compared exactly."""
 import threading
@@ -106,7 +106,8 @@ class Problem:
         rlse, lse = np.where(none, 0, rlse), np.where(none, 0, lse)
         tol = 2 * delta + (n + 32) * 2.0 ** -23 + 2.0 ** -22 * np.abs(rlse)
         assert np.all(np.abs(lse - rlse) <= tol), f"lse off by {np.abs(lse - rlse).max():.3e}"
-        tol = U * np.abs(ref) + (1 + 2.0 ** -6) * (U + 2 * delta + (n + 32) * 2.0 ** -23)[..., None] * pv
+        w = 2.0 ** -16 if self.k_scale is None else 2.0 ** -11
+        tol = U * np.abs(ref) + (1 + 2.0 ** -6) * (w + 2 * delta + (n + 32) * 2.0 ** -23)[..., None] * pv
         bad = np.abs(o - ref) > tol + 1e-30
         assert not bad.any(), f"{bad.sum()} of {bad.size} outputs off, worst {np.abs(o - ref)[bad].max():.3e}"
 
