@@ -28,6 +28,8 @@ decode::Launch split_heads(int heads, int heads_kv, int head_dim, bool e4m3) {
   lc.blocks = 0;
   lc.tile_shift = 0;
   lc.by_unit = 0;
+  lc.sms = 0;
+  lc.device = 0;
   return lc;
 }
 
@@ -47,7 +49,17 @@ size_t decode_workspace_bytes(int batch, int heads, int heads_kv, int head_dim) 
 }
 
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t s) {
-  const decode::Launch lc = split_heads(p.heads, p.kv.heads_kv, p.kv.head_dim, p.kv.e4m3);
+  decode::Launch lc = split_heads(p.heads, p.kv.heads_kv, p.kv.head_dim, p.kv.e4m3);
+  static std::atomic<int> sms[64];   // of each device, once asked
+  cudaError_t e = cudaGetDevice(&lc.device);
+  if (e != cudaSuccess) return e;
+  const bool listed = lc.device >= 0 && lc.device < 64;
+  lc.sms = listed ? sms[lc.device].load(std::memory_order_relaxed) : 0;
+  if (lc.sms == 0) {
+    e = cudaDeviceGetAttribute(&lc.sms, cudaDevAttrMultiProcessorCount, lc.device);
+    if (e != cudaSuccess) return e;
+    if (listed) sms[lc.device].store(lc.sms, std::memory_order_relaxed);
+  }
   if (p.kv.head_dim == 64) return launch_decode_d64(p, lc, s);
   if (p.kv.head_dim == 128) return launch_decode_d128(p, lc, s);
   return launch_decode_d256(p, lc, s);

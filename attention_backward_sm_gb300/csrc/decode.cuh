@@ -124,6 +124,8 @@ struct Launch {
   int blocks;      // blocks per chunk
   int tile_shift;  // log2 of the keys per tile
   int by_unit;     // combine goes by units, not by cuts
+  int sms;         // of the device (host only, like the next)
+  int device;
 };
 
 // Workspace: [blocks] cuts, then partial results [blocks][2 slots]: [HW][rows]
@@ -966,14 +968,6 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
 }
 
 // ------------------------------------------------------------------ launch
-inline int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    n = 152;
-  return n;
-}
-
 // The longest stretch of keys that a request can see, and what it comes to in tiles.
 inline int longest(const DecodeParams& p) {
   const int n = p.max_pages * p.kv.page_size;
@@ -989,13 +983,13 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   using Sh = Shape<D, E4M3, NH, HW>;
   static std::atomic<unsigned long long> done{0}, few_done{0}, many_done{0};
   auto* const kernel = decode_kernel<D, E4M3, NH, HW>;
-  cudaError_t e = prepare_once(reinterpret_cast<const void*>(kernel), 227 * 1024, done);
+  cudaError_t e = prepare_once(reinterpret_cast<const void*>(kernel), 227 * 1024, lc.device, done);
   if (e != cudaSuccess) return e;
   lc.group = HW;
   // At most one block per tile, at most the blocks that are resident at once.
   const long long unit_tiles = tiles_of(p, Sh::kTile);
   const long long tiles = unit_tiles * p.batch * (p.kv.heads_kv / HW);
-  long long blocks = Sh::kBlocksPerSm * sm_count();
+  long long blocks = Sh::kBlocksPerSm * lc.sms;
   if (blocks > kMaxBlocks) blocks = kMaxBlocks;
   blocks = blocks / lc.chunks > 1 ? blocks / lc.chunks : 1;
   lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
@@ -1010,7 +1004,7 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   const bool few = 8 * units > lc.blocks;
   auto* const combine = few ? combine_kernel<D, (D < 128 ? D : 128) / 4> : combine_kernel<D, 8>;
   if (!few) grid.z = D / 32;
-  e = prepare_once(reinterpret_cast<const void*>(combine), 0, few ? few_done : many_done);
+  e = prepare_once(reinterpret_cast<const void*>(combine), 0, lc.device, few ? few_done : many_done);
   if (e != cudaSuccess) return e;
   return launch_pdl(combine, grid, dim3(kJoinThreads), 0, s, p, lc);
 }

@@ -60,10 +60,8 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // split of an SM's memory for shared memory, also for the combine kernel,
 // which needs little: the split only changes on an idle SM, and that kernel's
 // blocks may be the first on theirs.
-inline cudaError_t prepare_once(const void* kernel, int smem, std::atomic<unsigned long long>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
+inline cudaError_t prepare_once(const void* kernel, int smem, int dev, std::atomic<unsigned long long>& done) {
+  cudaError_t e = cudaSuccess;
   const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
   if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
   if (smem > 0) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -8,7 +8,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-#include <ATen/cuda/EmptyTensor.h>
+#include <ATen/core/Tensor.h>
 #include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -188,7 +188,11 @@ class Place {
   fa_stream_t stream() const {
     return reinterpret_cast<fa_stream_t>(c10::cuda::getCurrentCUDAStream(device_.index()).stream());
   }
-  Tensor bytes(int64_t n) const { return at::detail::empty_cuda({n}, at::kByte, device_, std::nullopt); }
+  // Device memory of the current stream.
+  c10::Storage bytes(int64_t n) const {
+    auto* const a = c10::cuda::CUDACachingAllocator::get();
+    return c10::Storage(c10::Storage::use_byte_size_t(), n, a->allocate(n), a, /*resizable=*/false);
+  }
 
  private:
   static int64_t attr(PyObject* o, const char* name) {
@@ -211,10 +215,10 @@ class Place {
 class Cutter {
  public:
   static int64_t size(int64_t n, int64_t element) { return (n * element + 255) / 256 * 256; }
-  explicit Cutter(Tensor base) : base_(std::move(base)) {}
+  explicit Cutter(c10::Storage base) : base_(std::move(base)) {}
   Tensor next(at::IntArrayRef shape, at::ScalarType type) {
     const int64_t element = static_cast<int64_t>(c10::elementSize(type));
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base_.storage()),
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base_),
                                                         c10::DispatchKeySet(c10::DispatchKey::CUDA),
                                                         c10::scalarTypeToTypeMeta(type));
     t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
@@ -224,7 +228,7 @@ class Cutter {
   }
 
  private:
-  Tensor base_;
+  c10::Storage base_;
   int64_t at_ = 0;
 };
 
