@@ -521,7 +521,6 @@ int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
     return set_last_error(FA_ERR_INVALID_ARG, "workspace of %zu bytes needed, got %zu", need, workspace_bytes);
   if (misaligned16(workspace)) return set_last_error(FA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   if ((rc = check_device())) return rc;
-  if (num_pages == 0) p.kv.k = p.kv.v = const_cast<fa_bf16*>(q);   // never read; an address for empty copies
   p.q = q;
   p.q_row_stride = q_row_stride;
   p.table = block_table;
@@ -531,7 +530,7 @@ int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
   p.lse = lse;
   p.work = static_cast<float*>(workspace);
   p.page_div = fa::FastDiv(static_cast<uint32_t>(page_size));
-  p.max_pages = max_pages;
+  p.max_pages = num_pages > 0 ? max_pages : 0;   // without pages no key is seen
   p.batch = batch;
   p.heads = heads;
   p.window = window;
