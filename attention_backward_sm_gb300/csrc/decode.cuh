@@ -134,7 +134,9 @@ __host__ __device__ inline float* parts_of(float* work, size_t blocks) {
   return reinterpret_cast<float*>(reinterpret_cast<Cut*>(work) + blocks);
 }
 
-__host__ __device__ inline size_t part_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
+__host__ __device__ inline size_t part_floats(int rows, int d) {
+  return (static_cast<size_t>(rows) * (d + 2) + 3) / 4 * 4;   // 16-byte aligned
+}
 
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -793,43 +795,48 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
             }
           __syncthreads();
           const int heads = min(rows - h0, JH);
-          for (int i = tid; i < HW * heads * (D / 4); i += kThreads) {
-            const int c4 = i % (D / 4), h = HW == 1 ? 0 : i / (D / 4) / heads;
-            const int local = i / (D / 4) - h * heads, row = h0 + local;
-            float top = -INFINITY;
+          for (int i = tid / 16; i < HW * heads; i += kThreads / 16) {   // 16 threads per row
+            const int h = HW == 1 ? 0 : i / heads, local = i - h * heads, row = h0 + local;
+            float top = -INFINITY, sum = 0.f, f[KW];
 #pragma unroll
             for (int w = 0; w < KW; ++w) top = fmaxf(top, join_m[(h * KW + w) * HEADS + row]);
-            float sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
               const float lw = join_l[(h * KW + w) * HEADS + row];
-              const float f = lw == 0.f ? 0.f : ex2_approx(join_m[(h * KW + w) * HEADS + row] - top);
-              const float4 v = *reinterpret_cast<const float4*>(
-                  buf + ((h * KW + w) * JH + local) * D + ((((c4 >> 1) ^ ((row >> 1) & 3)) << 3) | ((c4 & 1) << 2)));
-              sum = fmaf(f, lw, sum);
-              acc.x = fmaf(f, v.x, acc.x);
-              acc.y = fmaf(f, v.y, acc.y);
-              acc.z = fmaf(f, v.z, acc.z);
-              acc.w = fmaf(f, v.w, acc.w);
+              f[w] = lw == 0.f ? 0.f : ex2_approx(join_m[(h * KW + w) * HEADS + row] - top);
+              sum = fmaf(f[w], lw, sum);
             }
             top -= kShift;
-            if (whole) {
-              const float vs = p.kv.v_scale ? *(p.kv.v_scale + here.hk * HW + h) : 1.f;
-              const float inv = sum == 0.f ? 0.f : __fdividef(vs, sum);
-              const long long to = out_row + h * G + row;
-              uint2 out;
-              out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-              out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-              *reinterpret_cast<uint2*>(p.o + to * D + c4 * 4) = out;
-              if (p.lse && c4 == 0) p.lse[to] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
-            } else {
-              float2* const to = reinterpret_cast<float2*>(part + (h * lc.rows + row) * D + c4 * 4);
-              to[0] = make_float2(acc.x, acc.y);
-              to[1] = make_float2(acc.z, acc.w);
-              if (c4 == 0) {
+            const float vs = p.kv.v_scale ? *(p.kv.v_scale + here.hk * HW + h) : 1.f;
+            const float inv = sum == 0.f ? 0.f : __fdividef(vs, sum);
+            const long long to = out_row + h * G + row;
+#pragma unroll(KW > 4 ? 1 : D / 64)
+            for (int c4 = tid % 16; c4 < D / 4; c4 += 16) {
+              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int w = 0; w < KW; ++w) {
+                const float4 v = *reinterpret_cast<const float4*>(
+                    buf + ((h * KW + w) * JH + local) * D + ((((c4 >> 1) ^ ((row >> 1) & 3)) << 3) | ((c4 & 1) << 2)));
+                acc.x = fmaf(f[w], v.x, acc.x);
+                acc.y = fmaf(f[w], v.y, acc.y);
+                acc.z = fmaf(f[w], v.z, acc.z);
+                acc.w = fmaf(f[w], v.w, acc.w);
+              }
+              if (whole) {
+                uint2 out;
+                out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+                out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+                *reinterpret_cast<uint2*>(p.o + to * D + c4 * 4) = out;
+              } else {
+                *reinterpret_cast<float4*>(part + (h * lc.rows + row) * D + c4 * 4) = acc;
+              }
+            }
+            if (tid % 16 == 0) {
+              if (!whole) {
                 part[HW * lc.rows * D + h * lc.rows + row] = top;
                 part[HW * lc.rows * D + (HW + h) * lc.rows + row] = sum;
+              } else if (p.lse) {
+                p.lse[to] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
               }
             }
           }
@@ -858,11 +865,31 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
 // kernel let this one be set up, and are read meanwhile.
 constexpr int kJoinThreads = 128;
 
+// Sums relative to a reference, moved to a reference `up` that is no lower.
+__device__ __forceinline__ void rescale(float& top, float up, float& sum, float4& acc) {
+  const float keep = up == top ? 1.f : ex2_approx(top - up);
+  top = up;
+  sum *= keep;
+  acc.x *= keep;
+  acc.y *= keep;
+  acc.z *= keep;
+  acc.w *= keep;
+}
+// Adds a partial result whose reference is no higher.
+__device__ __forceinline__ void add_part(float top, float& sum, float4& acc, float m, float l, const float4& v) {
+  const float f = l == 0.f ? 0.f : ex2_approx(m - top);
+  sum = fmaf(f, l, sum);
+  acc.x = fmaf(f, v.x, acc.x);
+  acc.y = fmaf(f, v.y, acc.y);
+  acc.z = fmaf(f, v.z, acc.z);
+  acc.w = fmaf(f, v.w, acc.w);
+}
+
 template <int D, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParams p, const Launch lc) {
-  constexpr int GROUPS = kJoinThreads / COLS;
-  __shared__ float s_top[GROUPS], s_sum[GROUPS];
-  __shared__ float4 s_acc[kJoinThreads];
+  constexpr int GROUPS = kJoinThreads / COLS, WARPS = kJoinThreads / 32;
+  __shared__ float s_top[WARPS], s_sum[WARPS];
+  __shared__ float4 s_acc[WARPS][COLS];
   const int tid = threadIdx.x;
   const int local = blockIdx.y % (lc.group * lc.rows), chunk = blockIdx.y / (lc.group * lc.rows);
   const int head = local / lc.rows, row = local % lc.rows;   // of the group; of the head's chunk
@@ -918,47 +945,57 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
   const int part_rows = lc.group * lc.rows;
   const size_t pf = part_floats(part_rows, D);
   const int col = blockIdx.z * COLS + tid % COLS, group = tid / COLS;
+  const float vs = p.kv.v_scale ? *(p.kv.v_scale + hk) : 1.f;
   float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = group; i < n; i += GROUPS) {
-    const float* const part =
-        parts + (static_cast<size_t>(chunk * lc.blocks + run + i) * 2 + (i == 0 ? first_slot : 0)) * pf;
-    const float2* const from = reinterpret_cast<const float2*>(part + local * D + col * 4);
-    const float2 a = from[0], b = from[1];
-    const float mi = part[part_rows * D + local], li = part[part_rows * D + part_rows + local];
-    const float up = fmaxf(top, mi);
-    const float keep = up == top ? 1.f : ex2_approx(top - up);
-    const float f = li == 0.f ? 0.f : ex2_approx(mi - up);
-    top = up;
-    sum = fmaf(sum, keep, f * li);
-    acc.x = fmaf(acc.x, keep, f * a.x);
-    acc.y = fmaf(acc.y, keep, f * a.y);
-    acc.z = fmaf(acc.z, keep, f * b.x);
-    acc.w = fmaf(acc.w, keep, f * b.y);
+  constexpr int U = COLS == 8 ? 4 : 1;   // partial results in flight per thread
+  for (int i0 = group; i0 < n; i0 += U * GROUPS) {
+    float mi[U], li[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * GROUPS;
+      mi[u] = -INFINITY;
+      li[u] = 0.f;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const float* const part =
+            parts + (static_cast<size_t>(chunk * lc.blocks + run + i) * 2 + (i == 0 ? first_slot : 0)) * pf;
+        v[u] = *reinterpret_cast<const float4*>(part + local * D + col * 4);
+        mi[u] = part[part_rows * D + local];
+        li[u] = part[part_rows * D + part_rows + local];
+      }
+    }
+    float up = top;
+#pragma unroll
+    for (int u = 0; u < U; ++u) up = fmaxf(up, mi[u]);
+    rescale(top, up, sum, acc);
+#pragma unroll
+    for (int u = 0; u < U; ++u) add_part(top, sum, acc, mi[u], li[u], v[u]);
   }
-  s_acc[tid] = acc;
-  if (tid % COLS == 0) {
-    s_top[group] = top;
-    s_sum[group] = sum;
+  // the groups of a warp, then the warps
+#pragma unroll
+  for (int off = COLS; off < 32; off <<= 1) {
+    const float mo = __shfl_xor_sync(0xffffffffu, top, off), lo = __shfl_xor_sync(0xffffffffu, sum, off);
+    const float4 vo = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, off), __shfl_xor_sync(0xffffffffu, acc.y, off),
+                                  __shfl_xor_sync(0xffffffffu, acc.z, off), __shfl_xor_sync(0xffffffffu, acc.w, off));
+    rescale(top, fmaxf(top, mo), sum, acc);
+    add_part(top, sum, acc, mo, lo, vo);
+  }
+  const int warp = tid / 32;
+  if (tid % 32 < COLS) s_acc[warp][tid % 32] = acc;
+  if (tid % 32 == 0) {
+    s_top[warp] = top;
+    s_sum[warp] = sum;
   }
   __syncthreads();
   if (tid >= COLS) return;
 #pragma unroll
-  for (int i = 1; i < GROUPS; ++i) top = fmaxf(top, s_top[i]);
-  sum = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < GROUPS; ++i) {
-    const float f = s_sum[i] == 0.f ? 0.f : ex2_approx(s_top[i] - top);
-    const float4 a = s_acc[i * COLS + tid];
-    sum = fmaf(f, s_sum[i], sum);
-    acc.x = fmaf(f, a.x, acc.x);
-    acc.y = fmaf(f, a.y, acc.y);
-    acc.z = fmaf(f, a.z, acc.z);
-    acc.w = fmaf(f, a.w, acc.w);
+  for (int w = 1; w < WARPS; ++w) {
+    rescale(top, fmaxf(top, s_top[w]), sum, acc);
+    add_part(top, sum, acc, s_top[w], s_sum[w], s_acc[w][tid]);
   }
-  const float inv = sum == 0.f ? 0.f : (p.kv.v_scale ? *(p.kv.v_scale + hk) : 1.f) / sum;
+  const float inv = sum == 0.f ? 0.f : __fdividef(vs, sum);
   const long long at = static_cast<long long>(b) * p.heads + hk * G + chunk * lc.rows + row;
   uint2 out;
   out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
@@ -1010,16 +1047,19 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
 }
 
 // Whether tiles of HW key/value heads are taken: where their queries fit
-// beside the ring of stages, and blocks have enough tiles (12 at least, were
-// every request as long as can be) for the longer DRAM pieces to matter more
-// than the more numerous partial results per unit.  4 heads against 1, on one
+// beside the ring of stages, and either blocks have enough tiles (12 at least,
+// were every request as long as can be) for the longer DRAM pieces to matter
+// more than the more numerous partial results per unit, or units are many and
+// of one or two tiles, so that few are cut and what counts is their number.  4 heads against 1, on one
 // GPU: 128 requests of 1k to 16k keys, 32 / 8 heads, d = 128, e4m3: 221 and
-// 254 us; one request of 1k keys, bf16: 8.1 and 6.9 us.
+// 254 us; one request of 1k keys, bf16: 8.1 and 6.9 us; 189 requests of 2
+// keys, 16 heads of 64, e4m3: 7.4 and 14.6 us.
 template <int D, bool E4M3, int NH, int HW>
 bool take_group(const DecodeParams& p, const Launch& lc) {
   using Sh = Shape<D, E4M3, NH, HW>;
+  const long long units = static_cast<long long>(p.batch) * (p.kv.heads_kv / HW), resident = Sh::kBlocksPerSm * 152;
   return p.kv.heads_kv % HW == 0 && Sh::fits(lc.rows) &&
-         tiles_of(p, Sh::kTile) * p.batch * (p.kv.heads_kv / HW) >= 12ll * Sh::kBlocksPerSm * 152;
+         (tiles_of(p, Sh::kTile) * units >= 12 * resident || (units >= resident && tiles_of(p, Sh::kTile) <= 2));
 }
 
 template <int D, bool E4M3, int NH>
