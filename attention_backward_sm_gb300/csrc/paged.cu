@@ -144,12 +144,24 @@ __device__ __forceinline__ Request load_request(const PlanParams& p, int b) {
   return r;
 }
 
+// Sums over the lanes up to and including this one.
+__device__ __forceinline__ void warp_scan(long long& a, long long& b) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, a, off), y = __shfl_up_sync(0xffffffffu, b, off);
+    if (static_cast<int>(threadIdx.x & 31) >= off) {
+      a += x;
+      b += y;
+    }
+  }
+}
+
 // Every block sums the requests' new tokens and pages itself (a block scan
 // over runs of consecutive requests, one run per thread), then places its
 // own tokens; block 0 also writes what there is one of per request.  Nothing
 // is passed between blocks, so one launch is enough.  Bound by launch and
-// memory latency: 64 requests 2.4 us, 2048 requests 5.2 us, 74k tokens of 32
-// prompts 2.5 us.
+// memory latency: 64 requests 2.3 us, 2048 requests 4.5 us, 74k tokens of 32
+// prompts 2.4 us.
 __global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams p) {
   __shared__ long long run_tok[kPlanMaxThreads + 1];   // new tokens before each thread's run
   __shared__ long long run_page[kPlanMaxThreads + 1];  // pages taken before it
@@ -165,22 +177,22 @@ __global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams 
     tok += r.fresh;
     page += r.take;
   }
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, tok, off), c = __shfl_up_sync(0xffffffffu, page, off);
-    if (lane >= off) {
-      tok += a;
-      page += c;
-    }
-  }
+  warp_scan(tok, page);
   if (lane == 31) {
     warp_tok[warp] = tok;
     warp_page[warp] = page;
   }
   __syncthreads();
-  for (int w = 0; w < warp; ++w) {
-    tok += warp_tok[w];
-    page += warp_page[w];
+  if (warp == 0) {
+    long long a = lane < threads / 32 ? warp_tok[lane] : 0, c = lane < threads / 32 ? warp_page[lane] : 0;
+    warp_scan(a, c);
+    warp_tok[lane] = a;
+    warp_page[lane] = c;
+  }
+  __syncthreads();
+  if (warp > 0) {
+    tok += warp_tok[warp - 1];
+    page += warp_page[warp - 1];
   }
   run_tok[t + 1] = tok;
   run_page[t + 1] = page;
