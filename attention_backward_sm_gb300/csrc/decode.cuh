@@ -404,9 +404,10 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
     if (with_q) {
       const uint16_t* const q = p.q + at.b * p.q_row_stride + (at.hk * HW * G + row0) * D;
       const uint32_t to = sbase + S::kOffQ + q_slot * q_bytes;
-      for (int i = tid; i < HW * rows * (D / 8); i += kThreads) {
-        const int c = i % (D / 8), h = HW == 1 ? 0 : i / (D / 8) / rows, r = i / (D / 8) - h * rows;
-        cp_async16(to + h * lc.rows * D * 2 + swizzled<D * 2>(r, c), q + (h * G + r) * D + c * 8, true);
+      // the warps of a head (warp % HW) load its rows
+      for (int i = warp / HW * 32 + lane; i < rows * (D / 8); i += kThreads / HW) {
+        const int c = i % (D / 8), r = i / (D / 8);
+        cp_async16(to + hw * lc.rows * D * 2 + swizzled<D * 2>(r, c), q + (hw * G + r) * D + c * 8, true);
       }
     }
   };
