@@ -2,8 +2,8 @@
 // allocates outputs and workspace and calls the C entry points.
 //
 // One call here costs a few microseconds less than the same steps in Python
-// and ctypes (decode: 25 -> 8 us of host time on a Grace core, with a kernel
-// of 7 us for a single short request), which is what bounds small batches.
+// and ctypes (decode: 25 -> 6.5 us of host time on a Grace core, with kernels
+// of 5.7 us for a single short request), which is what bounds small batches.
 // The arguments are positional; paged.py has the documented signatures.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
