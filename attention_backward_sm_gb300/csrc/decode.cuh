@@ -20,7 +20,7 @@
 //     fewer heads than warps the warps share the keys and are joined where a
 //     unit ends;
 //   * the tiles of all (request, head group) units, in order, are cut into
-//     equal runs, one per resident block.  Ragged lengths, one long request
+//     runs of equal cost, one per resident block.  Ragged lengths, one long request
 //     and many short ones all load every SM alike, and a unit that lies in
 //     several runs leaves at most one partial result per run, which
 //     combine_kernel joins (fixed order: same bits on every call).  The host
@@ -93,7 +93,7 @@ struct Shape {
   static constexpr int kOffSeen = kOffOffsets + kOffsets * kTile * 8;
   static constexpr int kOffJoin = kOffSeen + kOffsets * kSeenWords * 4;
   static constexpr int kOffScan = kOffJoin + (kKeyWarps > 1 ? 2 * kRowWarps * kHeads * 4 : 0);
-  static constexpr int kOffZero = (kOffScan + kThreads / 32 * 4 + 16 + 15) / 16 * 16;   // 16 zero bytes
+  static constexpr int kOffZero = (kOffScan + kThreads / 32 * 4 + 44 + 15) / 16 * 16;   // 16 zero bytes
   static constexpr int kOffQ = kOffZero + 16;   // query rows of kStages units
   static_assert(kJoinHeads >= 8, "join buffer");
   static_assert(kTile == 16 || kTile == 32 || kTile == 64 || kTile == 128, "tile_shift");
@@ -224,15 +224,33 @@ struct Lens {
 };
 
 // The list of all tiles (requests in order, the head groups of each, the
-// tiles of each) cut into `runs` runs, none empty, that differ by one at most.
+// tiles of each) cut into `runs` runs of equal cost, one per block, none with
+// fewer blocks than tiles.  From 4 tiles per block on, a tile costs 2 and the
+// end of a unit (warps joined, rows written: 0.5 to 0.7 us beside 1 to 1.3 for
+// a tile) 1, and a tile belongs to the run its start lies in; against equal
+// numbers of tiles: 37 requests of 1 to 5000 keys, window 1024, 16 heads of
+// 64, 14.3 and 15.9 us; 21 of 19 to 674, 128 / 16 heads of 256, 23.1 and 27.1.
+// With fewer tiles they count alike: whole tiles are all there is to share out
+// (64 of 1 to 120, 32 / 8 heads of 128: 7.8 us, by cost 9.2).
 struct Runs {
-  int total, runs, base, rem;
-  __device__ __forceinline__ Runs(int total_, int blocks) : total(total_), runs(min(total_, blocks)) {
+  static constexpr int kManyTiles = 4;   // per block
+  int tile, end;   // costs
+  int runs, base, rem;
+  __device__ __forceinline__ Runs(int tiles, int units, int blocks) {
+    const bool more = tiles >= kManyTiles * blocks;
+    tile = more ? 2 : 1;
+    end = more ? 1 : 0;
+    const int total = at(tiles, units);
+    runs = min(total, blocks);
     base = static_cast<unsigned>(total) / static_cast<unsigned>(runs);
     rem = total - base * runs;
   }
+  // Where a tile with so many tiles and units (ended ones) before it starts.
+  __device__ __forceinline__ int at(int tiles, int units) const { return tile * tiles + end * units; }
+  // The tiles of a unit that start before place x of it.
+  __device__ __forceinline__ int tiles_before(int x) const { return (x + end) >> end; }
   __device__ __forceinline__ int start(int c) const { return c * base + min(c, rem); }
-  // The run that holds tile x.
+  // The run that holds place x.
   __device__ __forceinline__ int of(int x) const {
     const int y = x - rem * (base + 1);
     return y < 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(base + 1)
@@ -245,13 +263,20 @@ struct Runs {
 template <int TILE, int THREADS>
 struct Scan {
   int b0, b1, before, mine, total;
+  int len0;   // of request b0
   __device__ __forceinline__ Scan(const Lens& L, int batch, int groups, int* scan) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = (batch + THREADS - 1) / THREADS;
     b0 = min(tid * per, batch);
     b1 = min(b0 + per, batch);
     mine = 0;
-    for (int b = b0; b < b1; ++b) mine += L.tiles<TILE>(L.len(b));
+    len0 = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const int len = L.len(b);
+      if (b == b0) len0 = len;
+      mine += L.tiles<TILE>(len);
+    }
     mine *= groups;
     int upto = mine;
 #pragma unroll
@@ -269,22 +294,37 @@ struct Scan {
     }
     before = upto - mine;
   }
-  // The thread whose requests hold tile x writes the tile's request, head
-  // group, place and the request's length to found[4].
-  __device__ __forceinline__ void find(const Lens& L, int groups, int x, int* found) const {
-    if (x < before || x >= before + mine) return;
-    int at = before;
+  // The threads whose requests hold places x and y write to found[6] the first
+  // tile that starts at x or later (request, head group, tile, the request's
+  // length, the number of tiles before it) and the number of tiles before y.
+  __device__ __forceinline__ void find(const Lens& L, const Runs& runs, int batch, int groups, int x, int y,
+                                       int* found) const {
+    int at = runs.at(before, b0 * groups), tiles_before = before;
+    const int end = runs.at(before + mine, b1 * groups);
+    if (x >= end || y < at) return;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const int len = L.len(b), nt = L.tiles<TILE>(len);
-      if (x < at + nt * groups) {
-        const unsigned in = x - at;
-        found[0] = b;
-        found[1] = in / static_cast<unsigned>(nt);
-        found[2] = in % static_cast<unsigned>(nt);
-        found[3] = len;
-        return;
+      const int len = b == b0 ? len0 : L.len(b), nt = L.tiles<TILE>(len);
+      const unsigned unit = runs.at(nt, 1), span = unit * groups;
+      if (static_cast<unsigned>(x - at) < span) {
+        int hk = static_cast<unsigned>(x - at) / unit, t = runs.tiles_before(x - at - hk * unit);
+        found[4] = tiles_before + hk * nt + t;
+        if (t == nt) {   // in the cost of the unit's end
+          t = 0;
+          ++hk;
+        }
+        const bool next = hk == groups;
+        found[0] = next ? b + 1 : b;
+        found[1] = next ? 0 : hk;
+        found[2] = t;
+        found[3] = next && b + 1 < batch ? L.len(b + 1) : len;
       }
-      at += nt * groups;
+      if (static_cast<unsigned>(y - at) < span) {
+        const int hk = static_cast<unsigned>(y - at) / unit;
+        found[5] = tiles_before + hk * nt + runs.tiles_before(y - at - hk * unit);
+      }
+      at += span;
+      tiles_before += nt * groups;
     }
   }
 };
@@ -322,7 +362,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   long long* const offsets = reinterpret_cast<long long*>(smem + S::kOffOffsets);
   uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + S::kOffSeen);
   int* const scan = reinterpret_cast<int*>(smem + S::kOffScan);   // [warps]
-  int* const found = scan + kThreads / 32;                        // b, hk, t, length
+  int* const found = scan + kThreads / 32;                        // of the run: Scan::find's, and the end
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the warp's key/value head of a tile, its part of the keys, its first column of O
@@ -341,15 +381,26 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   // The run of this block: every block counts all tiles, then finds where
   // its share starts.
   const Scan<TILE, kThreads> tiles(L, p.batch, groups, scan);
-  const Runs runs(tiles.total, lc.blocks);
+  const Runs runs(tiles.total, p.batch * groups, lc.blocks);
   int4* const cuts = reinterpret_cast<int4*>(p.work) + blockIdx.y * lc.blocks;
   if (static_cast<int>(blockIdx.x) >= runs.runs) {
     if (tid == 0) cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  const int start = runs.start(blockIdx.x), n = runs.start(blockIdx.x + 1) - start;
-  tiles.find(L, groups, start, found);
+  // For the end: in registers meanwhile it would take what a combine block
+  // needs to be set up beside this one (16 requests of 128 keys: 6.4 -> 8.2 us).
+  Runs* const runs_kept = reinterpret_cast<Runs*>(found + 6);
+  if (tid == 0) {
+    *runs_kept = runs;
+    if (static_cast<int>(blockIdx.x) + 1 == runs.runs) found[5] = tiles.total;
+  }
+  tiles.find(L, runs, p.batch, groups, runs.start(blockIdx.x), runs.start(blockIdx.x + 1), found);
   __syncthreads();
+  const int start = found[4], n = found[5] - start;   // tiles before this run's, and its own
+  if (n <= 0) {
+    if (tid == 0) cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
   Place<TILE> here;   // the tile being computed
   here.b = found[0];
   here.hk = found[1];
@@ -399,12 +450,17 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
         if (TILE % KPP == 0 || key_in_pass + i * KPP < TILE) load_row(key_in_pass + i * KPP);
     } else {
       const int end = (keys + S::kKeys - 1) / S::kKeys * S::kKeys;
+#pragma unroll 1
       for (int r = key_in_pass; r < end; r += KPP) load_row(r);
     }
     if (with_q) {
       const uint16_t* const q = p.q + at.b * p.q_row_stride + (at.hk * HW * G + row0) * D;
       const uint32_t to = sbase + S::kOffQ + q_slot * q_bytes;
       // the warps of a head (warp % HW) load its rows
+      // (Code that a short call runs once is kept short, here and below: the
+      // call waits for its instructions, too.  Loops left to the compiler's
+      // unrolling: +2 to 5 % for calls under 10 us.)
+#pragma unroll 1
       for (int i = warp / HW * 32 + lane; i < rows * (D / 8); i += kThreads / HW) {
         const int c = i % (D / 8), r = i / (D / 8);
         cp_async16(to + hw * lc.rows * D * 2 + swizzled<D * 2>(r, c), q + (hw * G + r) * D + c * 8, true);
@@ -843,9 +899,11 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
           }
         }
       }
-      if (tid == 0 && s + 1 == n && !lc.by_unit)
-        cuts[blockIdx.x] = make_int4(starts_here && !unit_done ? here.b * groups + here.hk : -1,
-                                     runs.of(start + s - here.t + here.nt - 1), slot, 0);
+      if (tid == 0 && s + 1 == n && !lc.by_unit) {
+        const int unit = here.b * groups + here.hk, last_tile = start + s - here.t + here.nt - 1;
+        reinterpret_cast<int4*>(p.work)[blockIdx.y * lc.blocks + blockIdx.x] = make_int4(
+            starts_here && !unit_done ? unit : -1, runs_kept->of(runs_kept->at(last_tile, unit)), slot, 0);
+      }
       fresh = true;
       first_piece = false;
       q_slot = q_slot + 1 == ST ? 0 : q_slot + 1;
@@ -924,11 +982,13 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
       before += s_before[w];
       total += s_total[w];
     }
-    const Runs runs(total * groups, lc.blocks);
-    const int nt = L.tiles(L.len(b), lc.tile_shift), first = before * groups + (unit - b * groups) * nt;
+    const Runs runs(total * groups, p.batch * groups, lc.blocks);
+    const int nt = L.tiles(L.len(b), lc.tile_shift), tiles_before = before * groups + (unit - b * groups) * nt;
+    const int first = runs.at(tiles_before, unit);
     run = runs.of(first);
-    last = runs.of(first + nt - 1);
-    first_slot = first == runs.start(run) ? 0 : 1;
+    last = runs.of(runs.at(tiles_before + nt - 1, unit));
+    // slot 0 where the tile before, of another unit, is not in that run
+    first_slot = first - runs.at(1, 1) < runs.start(run) ? 0 : 1;
     pdl_wait();
   } else {
     pdl_wait();

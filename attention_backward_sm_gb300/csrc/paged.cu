@@ -509,8 +509,9 @@ int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
   if (max_pages < 0) return set_last_error(FA_ERR_INVALID_ARG, "max_pages must be >= 0, got %d", max_pages);
   if (static_cast<long long>(max_pages) * page_size > 0x7fff0000ll)
     return set_last_error(FA_ERR_UNSUPPORTED, "a block table of %d pages of %d slots is too long", max_pages, page_size);
-  // The kernels number tiles of at least 64 keys with 32 bits.
-  if ((static_cast<long long>(max_pages) * page_size / 64 + 1) * heads_kv > 0x7fffffffll / (batch > 0 ? batch : 1))
+  // The kernels count with 32 bits the costs of tiles (64 keys of a head at
+  // least, 2) and units (1).
+  if ((static_cast<long long>(max_pages) * page_size / 64 + 1) * heads_kv > 0x7fffffffll / 3 / (batch > 0 ? batch : 1))
     return set_last_error(FA_ERR_UNSUPPORTED, "%d requests of %d pages of %d slots and %d heads are too many", batch,
                           max_pages, page_size, heads_kv);
   if (batch > 1 && table_stride < 0)
