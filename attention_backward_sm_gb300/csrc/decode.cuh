@@ -961,6 +961,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
     const Lens L{p.seq_lens, p.max_pages * p.kv.page_size, p.window};
     const int b = unit / groups;
     int before = 0, total = 0;
+#pragma unroll 1
     for (int i = tid; i < p.batch; i += kJoinThreads) {
       const int nt = L.tiles(L.len(i), lc.tile_shift);
       total += nt;
@@ -989,7 +990,6 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
     last = runs.of(runs.at(tiles_before + nt - 1, unit));
     // slot 0 where the tile before, of another unit, is not in that run
     first_slot = first - runs.at(1, 1) < runs.start(run) ? 0 : 1;
-    pdl_wait();
   } else {
     pdl_wait();
     const int4 cut = *(reinterpret_cast<const int4*>(p.work) + chunk * lc.blocks + blockIdx.x);
@@ -999,7 +999,6 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
     last = cut.y;
     first_slot = cut.z;
   }
-  if (last == run || chunk * lc.rows + row >= G) return;   // not cut; no such head
   const int b = unit / groups, hk = unit % groups * lc.group + head;
   const int n = last - run + 1;
   const float* const parts = parts_of(p.work, static_cast<size_t>(lc.blocks) * lc.chunks);
@@ -1007,6 +1006,9 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
   const size_t pf = part_floats(part_rows, D);
   const int col = blockIdx.z * COLS + tid % COLS, group = tid / COLS;
   const float vs = p.kv.v_scale ? *(p.kv.v_scale + hk) : 1.f;
+  // Before any block ends: the next kernel waits for this one only.
+  pdl_wait();
+  if (last == run || chunk * lc.rows + row >= G) return;   // not cut; no such head
   float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int U = COLS == 8 ? 4 : 1;   // partial results in flight per thread
