@@ -161,8 +161,8 @@ __device__ __forceinline__ void warp_scan(long long& a, long long& b) {
 // own tokens; block 0 also writes what there is one of per request.  Nothing
 // is passed between blocks, so one launch is enough.  Bound by launch and
 // memory latency, that of the kernel's own instructions included, so its loops
-// are not unrolled (3 to 5 % of the call): 64 requests 2.2 us, 2048 requests
-// 4.5 us, 74k tokens of 32 prompts 2.4 us.
+// are not unrolled (3 to 5 % of the call): 64 requests 2.1 us, 2048 requests
+// 4.4 us, 74k tokens of 32 prompts 2.4 us.
 __global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams p) {
   __shared__ long long run_tok[kPlanMaxThreads + 1];   // new tokens before each thread's run
   __shared__ long long run_page[kPlanMaxThreads + 1];  // pages taken before it

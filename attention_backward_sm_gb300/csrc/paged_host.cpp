@@ -3,7 +3,7 @@
 //
 // One call here costs a few microseconds less than the same steps in Python
 // and ctypes (decode: 25 -> 6.5 us of host time on a Grace core, with kernels
-// of 5.7 us for a single short request), which is what bounds small batches.
+// of 5.4 us for a single short request), which is what bounds small batches.
 // The arguments are positional; paged.py has the documented signatures.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
