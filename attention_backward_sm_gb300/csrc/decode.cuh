@@ -229,8 +229,9 @@ struct Lens {
 // end of a unit (warps joined, rows written: 0.5 to 0.7 us beside 1 to 1.3 for
 // a tile) 1, and a tile belongs to the run its start lies in; against equal
 // numbers of tiles: 37 requests of 1 to 5000 keys, window 1024, 16 heads of
-// 64, 14.3 and 15.9 us; 21 of 19 to 674, 128 / 16 heads of 256, 23.1 and 27.1.
-// With fewer tiles they count alike: whole tiles are all there is to share out
+// 64, 14.9 and 15.9 us; 21 of 19 to 674, 128 / 16 heads of 256, 23.3 and 27.4.
+// (Such runs are at least 8 long, so none is empty.)  With fewer tiles they
+// count alike: whole tiles are all there is to share out
 // (64 of 1 to 120, 32 / 8 heads of 128: 7.8 us, by cost 9.2).
 struct Runs {
   static constexpr int kManyTiles = 4;   // per block
@@ -397,10 +398,6 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
   tiles.find(L, runs, p.batch, groups, runs.start(blockIdx.x), runs.start(blockIdx.x + 1), found);
   __syncthreads();
   const int start = found[4], n = found[5] - start;   // tiles before this run's, and its own
-  if (n <= 0) {
-    if (tid == 0) cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
-  }
   Place<TILE> here;   // the tile being computed
   here.b = found[0];
   here.hk = found[1];
