@@ -161,8 +161,8 @@ __device__ __forceinline__ void warp_scan(long long& a, long long& b) {
 // own tokens; block 0 also writes what there is one of per request.  Nothing
 // is passed between blocks, so one launch is enough.  Bound by launch and
 // memory latency, that of the kernel's own instructions included, so its loops
-// are not unrolled (3 to 5 % of the call): 64 requests 2.1 us, 2048 requests
-// 4.4 us, 74k tokens of 32 prompts 2.4 us.
+// are not unrolled (3 to 5 % of the call): 64 requests 2.2 us, 2048 requests
+// 4.5 us, 74k tokens of 32 prompts 2.4 us.
 __global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams p) {
   __shared__ long long run_tok[kPlanMaxThreads + 1];   // new tokens before each thread's run
   __shared__ long long run_page[kPlanMaxThreads + 1];  // pages taken before it
@@ -254,6 +254,35 @@ __global__ void __launch_bounds__(kPlanMaxThreads) plan_kernel(const PlanParams 
     }
     p.slots[i] = slot;
     p.positions[i] = pos;
+  }
+  if (total <= p.num_tokens) return;
+  // Pages whose first token is past num_tokens are taken, too: the entries
+  // that no token above has written, page by page (batch * max_pages at most,
+  // whatever the lengths).  Calls with slots for all tokens pay 0.06 us for it
+  // (as a function of its own, 0.3 to 1.5 us).
+  const long long pages = run_page[threads];
+#pragma unroll 1
+  for (long long i = static_cast<long long>(blockIdx.x) * threads + t; i < pages;
+       i += static_cast<long long>(gridDim.x) * threads) {
+    int lo = 0, hi = threads;   // run_page[lo] <= i < run_page[hi]
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (run_page[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    long long at = run_tok[lo], taken = run_page[lo];
+    int b = min(lo * per, p.batch);
+    Request r = load_request(p, b);
+#pragma unroll 1
+    while (taken + r.take <= i) {
+      at += r.fresh;
+      taken += r.take;
+      r = load_request(p, ++b);
+    }
+    const long long pi = r.have + (i - taken), f = start + i;
+    if (at + pi * p.page_size - r.seq >= p.num_tokens)
+      p.table[b * p.table_stride + pi] = f < p.num_free ? *(p.free_pages + f) : -1;
   }
 }
 

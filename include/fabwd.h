@@ -316,7 +316,8 @@ enum fa_kv_type {
  * A token for which the table row or the free list has no page gets slot -1
  * (and the table entry -1); *free_next > num_free tells that the list ran
  * out, cu_new[batch] > num_tokens that slots was too short (tokens past it
- * get no place).  seq_lens_out must not overlap seq_lens or new_lens, and
+ * get no slot and position here; their pages are taken and entered like the
+ * others').  seq_lens_out must not overlap seq_lens or new_lens, and
  * free_next not free_start; no other output may overlap an input. */
 int fa_kv_plan(int32_t* block_table, long long table_stride, int max_pages,
                const int32_t* seq_lens, const int32_t* new_lens,

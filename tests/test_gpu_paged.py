@@ -156,6 +156,58 @@ def test_plan_too_few_slots_keeps_the_count():
     assert p.slots.tolist() == [0, 1, 2, 3, 4, 8] and p.cu_new.tolist() == [0, 5, 8] and p.free_next.tolist() == [3]
 
 
+@pytest.mark.parametrize("tokens", [0, 1, 4, 5, 7, 8, 16, 17, 18, 29, 30, 31, 40, 41, 200])
+@pytest.mark.parametrize("start,free", [(0, 30), (3, 30), (0, 6), (2, 0)])
+def test_plan_too_few_slots_enters_every_page(tokens, start, free):
+    """Cuts at num_tokens before, inside and after requests with several new
+    pages (held pages, rows too short and an empty list among them): the table
+    and the tokens' places are those of the definition, and a second call with
+    slots for all tokens finds its pages in the table."""
+    page, seq, new = 4, [0, 3, 8, 0, 5, 0, 1], [5, 12, 0, 1, 11, 40, 2]
+    width = 6
+    table = np.full((len(seq), width), -1)
+    at = 50
+    for b, n in enumerate(seq):
+        for i in range(-(-n // page)):
+            table[b, i], at = at, at + 1
+    free_pages = np.random.default_rng(7).permutation(free)
+    want = paged.plan(table, seq, new, free_pages, page, tokens, start)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).to(DEV)  # noqa: E731
+    wide = i32(np.concatenate([table, np.full((len(seq), 2), 77)], 1))
+    for call in range(2):
+        got = fab().kv_plan(wide[:, :width], i32(seq), i32(new), i32(free_pages), page, tokens, free_start=i32([start]))
+        for name, g, w in zip(("table", "slots", "positions", "cu_new", "seq_lens", "free_next"),
+                              (wide[:, :width], *got), (*want[:5], np.array([want[5]]))):
+            assert np.array_equal(g.cpu().numpy(), w), (name, call)
+        assert torch.all(wide[:, width:] == 77)
+
+
+def test_plan_too_few_slots_for_many_requests():
+    """More requests than threads and pages than a block takes at once, lengths
+    past the table's rows (a thousand million tokens) among them."""
+    rng = np.random.default_rng(8)
+    batch, page, width = 3000, 16, 40
+    seq, new = rng.integers(0, 300, batch), rng.integers(0, 300, batch)
+    table = np.full((batch, width), -1)
+    for b, n in enumerate(seq):
+        table[b, :-(-n // page)] = 10 ** 6 + b
+    free_pages = rng.permutation(batch * width)
+    want = paged.plan(table, seq, new, free_pages, page, 1000)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).to(DEV)  # noqa: E731
+    got_table = i32(table)
+    got = fab().kv_plan(got_table, i32(seq), i32(new), i32(free_pages), page, 1000)
+    for g, w in zip((got_table, *got), (*want[:5], np.array([want[5]]))):
+        assert np.array_equal(g.cpu().numpy(), w)
+    new[:] = 10 ** 9
+    got_table = i32(table)
+    fab().kv_plan(got_table, i32(seq), i32(new), i32(free_pages), page, 10)
+    held = -(-seq // page)
+    first = np.cumsum(width - held) - (width - held)
+    got_table = got_table.cpu().numpy()
+    for b in range(batch):
+        assert np.array_equal(got_table[b, held[b]:], free_pages[first[b]:first[b] + width - held[b]])
+
+
 # ------------------------------------------------------------------ append
 @pytest.mark.parametrize("tokens,heads_kv,dim,page", [(1, 1, 64, 16), (7, 8, 128, 16), (333, 3, 64, 5), (129, 2, 256, 64)])
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
