@@ -680,8 +680,12 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
           }
       }
       // P^T for the second product (the sums take it in 32 bits): in fp16 (2^-11
-      // off), or beside bf16 values as the sum of two bf16 numbers (2^-17 off).
-      // One bf16 number alone would be off by as much as the rounding of o.
+      // off), or beside bf16 values as the sum of two bf16 numbers: its upper
+      // half and the rest, rounded (2^-16 off).  One bf16 number alone would be
+      // off by as much as the rounding of o.  Neither part of a weight is
+      // negative, and with the lowest bit set (2^-23) the rest is not zero, so
+      // that an infinite value stays infinite (inf (p - q) + inf q and
+      // inf 0 would not).
       uint32_t pf[KT][NH][2], pr[KT][NH][2];
 #pragma unroll
       for (int k = 0; k < KT; ++k)
@@ -697,9 +701,10 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
             if constexpr (E4M3) {
               pf[k][i][u] = transposed(pack_f16x2(e[2 * u], e[2 * u + 1]));
             } else {
-              const uint32_t high = pack_bf16x2(e[2 * u], e[2 * u + 1]);
-              pf[k][i][u] = transposed(high);
-              pr[k][i][u] = transposed(pack_bf16x2(e[2 * u] - bf_lo(high), e[2 * u + 1] - bf_hi(high)));
+              const uint32_t b0 = __float_as_uint(e[2 * u]), b1 = __float_as_uint(e[2 * u + 1]);
+              pf[k][i][u] = transposed(__byte_perm(b0, b1, 0x7632));
+              pr[k][i][u] = transposed(pack_bf16x2(__uint_as_float(b0 | 1u) - __uint_as_float(b0 & 0xFFFF0000u),
+                                                   __uint_as_float(b1 | 1u) - __uint_as_float(b1 & 0xFFFF0000u)));
             }
           }
         }

@@ -389,6 +389,34 @@ def test_decode_visible_nan_and_inf_reach_the_output():
         assert abs(lse.item() - want.item()) < 1e-4 and torch.isfinite(o).all()
 
 
+@pytest.mark.parametrize("heads,heads_kv,dim,width", [(4, 2, 64, 1), (4, 4, 128, 8000), (16, 1, 128, 1), (8, 1, 256, 1),
+                                                      (24, 1, 64, 1), (16, 8, 128, 8000)])
+def test_decode_visible_infinite_values(heads, heads_kv, dim, width):
+    """An infinite value among those a row sees makes its element infinite, as
+    any weight above zero times it is; two of both signs make it NaN; the
+    others are the definition's.  Requests of one key (a weight of exactly 1),
+    of part of a tile, of several tiles and of several blocks' runs."""
+    lens = [1, 20, 200, 6000]
+    p = Problem(lens, heads, heads_kv, dim, 16, seed=dim + heads, extra_width=width)
+    want = torch.zeros(len(lens), heads_kv, dim)
+    for b, n in enumerate(lens):
+        for i, j in enumerate({0, n // 3, n - 1}):
+            for h in range(heads_kv):
+                for col, value in ((3 * i, float("inf")), (3 * i + 1, -float("inf")), (dim - 1, (-1) ** i * float("inf"))):
+                    p.v[p.table[b, j // 16].long(), j % 16, h, col] = value
+                    want[b, h, col] = want[b, h, col] + value
+    o, lse = p.run()
+    got = o.float().cpu().view(len(lens), heads_kv, -1, dim)
+    want = want[:, :, None].expand(got.shape)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    infinite = torch.isinf(want)
+    assert torch.equal(got[infinite], want[infinite])
+    p.v = torch.nan_to_num(p.v, nan=float("nan"), posinf=0.0, neginf=0.0)
+    ref = paged.decode(p.q.float(), p.k.float(), p.v.float(), p.table.numpy(), p.lens.numpy(), p.scale)[0]
+    special = infinite.view(o.shape) | torch.isnan(want).reshape(o.shape)
+    p.check(torch.where(special.to(DEV), torch.from_numpy(ref).to(DEV).bfloat16(), o), lse)
+
+
 def test_decode_empty_table_and_no_lse():
     f = fab()
     p = Problem([3, 0], 4, 2, 64, 16, seed=15)
