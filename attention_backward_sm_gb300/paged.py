@@ -21,7 +21,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import FA_ERR_INVALID_ARG, FabwdError, fa_last_error, lib
+from . import FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FabwdError, fa_last_error, lib
 
 FA_KV_BF16 = 0
 FA_KV_E4M3 = 1
@@ -83,8 +83,8 @@ def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=
 def fa_decode_workspace_size(batch: int, heads: int, heads_kv: int, head_dim: int) -> int:
     n = lib().fa_decode_workspace_size(batch, heads, heads_kv, head_dim)
     err = fa_last_error()
-    if err:
-        raise FabwdError(FA_ERR_INVALID_ARG, err)
+    if err:   # the size function gives no code
+        raise FabwdError(FA_ERR_UNSUPPORTED if err.startswith("head_dim") else FA_ERR_INVALID_ARG, err)
     return int(n)
 
 

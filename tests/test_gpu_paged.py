@@ -459,6 +459,22 @@ def test_offsets_past_32_bits(kv):
     assert torch.equal(kc[pool - 1, 5].float(), row[0].to(dtype).float())
 
 
+@pytest.mark.parametrize("heads,dim,code,word", [(4, 96, 2, "head_dim"), (3, 64, 1, "multiple"), (0, 64, 1, "multiple"),
+                                                 (2050, 64, 2, "1024")])
+def test_decode_raises_the_code_of_the_c_entry(heads, dim, code, word):
+    f = fab()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    cache = torch.zeros(4, 16, 2, dim, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(1, heads, dim, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(f.FabwdError, match=word) as e:
+        f.decode(q, cache, cache, torch.zeros(1, 1, **i32), torch.ones(1, **i32), 0.1)
+    assert e.value.code == code
+    if dim == 96:
+        with pytest.raises(f.FabwdError, match=word) as e:
+            f.kv_append(cache[0, :1], cache[0, :1], cache, cache.clone(), torch.zeros(1, dtype=torch.int64, device=DEV))
+        assert e.value.code == code
+
+
 # ------------------------------------------------------------------ as a program uses them
 def test_prefill_then_decode_steps_match_the_forward():
     """plan -> append -> forward over the prompts, then plan -> append ->

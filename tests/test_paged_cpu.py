@@ -217,3 +217,13 @@ def test_append_and_plan_binding_refusals(lib):
         fab.kv_plan(*args[:2], torch.ones(3, **i32), args[3], 8, 2)
     with pytest.raises(ValueError, match="free_start"):
         fab.kv_plan(*args, 8, 2, free_start=torch.zeros(2, **i32))
+
+
+@pytest.mark.parametrize("args,code", [((4, 8, 4, 96), 2), ((4, 6, 4, 128), 1), ((-1, 8, 4, 128), 1), ((4, 0, 1, 96), 1)])
+def test_workspace_size_binding_raises_the_code_of_fa_decode(lib, args, code):
+    import attention_backward_sm_gb300 as fab
+    with pytest.raises(fab.FabwdError) as e:
+        fab.fa_decode_workspace_size(*args)
+    assert e.value.code == code
+    batch, heads, heads_kv, dim = args
+    assert _decode_rc(lib, batch=batch, heads=heads, heads_kv=heads_kv, dim=dim) == (2 if dim == 96 else code)
