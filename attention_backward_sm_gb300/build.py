@@ -3,7 +3,9 @@ extension _paged_host.so beside it with g++ against the installed PyTorch.
 
 Each translation unit compiles to an object in parallel, then nvcc links
 the shared library next to this file.  A rebuild happens only when a
-source or header is newer than the library, or when PyTorch changed.
+source or header is newer than the library (the extension: also when PyTorch
+or Python changed).  The library needs neither; without a PyTorch that has
+CUDA it is all that is built.
 """
 from __future__ import annotations
 
@@ -35,13 +37,19 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _torch_dir() -> str:
-    return importlib.util.find_spec("torch").submodule_search_locations[0]
+def _torch_dir() -> str | None:
+    """The folder of the installed PyTorch, None without one that has CUDA."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    path = spec.submodule_search_locations[0]
+    return path if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
 
 
-def _torch_version() -> str:
+def _host_needs() -> str:
+    """What HOST is built against: this PyTorch and this Python."""
     with open(os.path.join(_torch_dir(), "version.py")) as f:
-        return f.read()
+        return f.read() + str(sysconfig.get_config_var("EXT_SUFFIX"))
 
 
 def _host_tag() -> str:
@@ -52,18 +60,46 @@ def _host_tag() -> str:
         return ""
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(HOST) or _host_tag() != _torch_version():
+def _older(path: str, sources) -> bool:
+    if not os.path.exists(path):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [HOST_SOURCE]]
-    deps.append(os.path.join(ROOT, "include", "fabwd.h"))
-    deps.append(os.path.abspath(__file__))
+    t = os.path.getmtime(path)
+    deps = [os.path.join(CSRC, f) for f in sources]
+    deps += [os.path.join(ROOT, "include", "fabwd.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _run(cmd, what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
+def _compile_host() -> str:
+    obj = os.path.join(BUILD, HOST_SOURCE.replace(".cpp", ".o"))
+    inc = [os.path.join(_torch_dir(), "include"), os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           sysconfig.get_paths()["include"]]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", *[a for i in inc for a in ("-isystem", i)], "-c",
+          os.path.join(CSRC, HOST_SOURCE), "-o", obj], f"g++ for {HOST_SOURCE}")
+    return obj
+
+
+def _link_host(obj: str) -> None:
+    tmp = HOST + ".tmp"
+    libs = os.path.join(_torch_dir(), "lib")
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + os.path.dirname(LIB), "-l:" + os.path.basename(LIB), "-L" + libs,
+          "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN",
+          "-Wl,-rpath," + libs], "g++ link")
+    os.replace(tmp, HOST)
+    with open(HOST_TAG, "w") as f:
+        f.write(_host_needs())
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    make_lib = force or _older(LIB, SOURCES + HEADERS)
+    make_host = _torch_dir() is not None and (force or _host_tag() != _host_needs() or _older(HOST, [HOST_SOURCE]))
+    if not make_lib and not make_host:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
 
@@ -72,44 +108,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc(), *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            sys.stderr.write(r.stdout + r.stderr)
-        return obj
-
-    def compile_host():
-        obj = os.path.join(BUILD, HOST_SOURCE.replace(".cpp", ".o"))
-        inc = [os.path.join(_torch_dir(), "include"), os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
-               sysconfig.get_paths()["include"]]
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", *[a for i in inc for a in ("-isystem", i)], "-c",
-               os.path.join(CSRC, HOST_SOURCE), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for {HOST_SOURCE}:\n{r.stdout}\n{r.stderr}")
+        out = _run(cmd, f"nvcc for {src}")
+        if verbose and out:
+            sys.stderr.write(out)
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        host_obj = ex.submit(compile_host)
-        objs = list(ex.map(compile_one, SOURCES))
-        host_obj = host_obj.result()
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = HOST + ".tmp"
-    libs = os.path.join(_torch_dir(), "lib")
-    cmd = ["g++", "-shared", "-o", tmp, host_obj, "-L" + HERE, "-l:" + os.path.basename(LIB), "-L" + libs, "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, HOST)
-    with open(HOST_TAG, "w") as f:
-        f.write(_torch_version())
+        host_obj = ex.submit(_compile_host) if make_host else None
+        if make_lib:
+            objs = list(ex.map(compile_one, SOURCES))
+            tmp = LIB + ".tmp"
+            _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], "nvcc link")
+            os.replace(tmp, LIB)
+        if make_host:   # a failure here leaves the library in place
+            _link_host(host_obj.result())
     return LIB
 
 
