@@ -81,3 +81,15 @@ def test_extension_is_remade_for_another_pytorch_or_python(compilers, monkeypatc
             monkeypatch.setattr(b.sysconfig, "get_config_var", lambda name: ".cpython-399.so")
         b.build()
         assert compilers.calls == ([] if change == "nothing" else ["g++", "g++"]), change
+
+
+def test_entry_build_imports_the_extension(monkeypatch):
+    """An extension that cannot be imported shows at the build."""
+    import __graft_entry__ as entry
+    from attention_backward_sm_gb300 import paged
+    entry.build()
+    monkeypatch.setattr(paged, "_native", None)
+    monkeypatch.setitem(__import__("sys").modules, "attention_backward_sm_gb300._paged_host", None)
+    monkeypatch.delattr("attention_backward_sm_gb300._paged_host", raising=False)
+    with pytest.raises(ImportError):
+        entry.build()
