@@ -82,6 +82,12 @@ struct Shape {
   // Warps over the same rows, each with a part of O's columns (and all of the
   // scores), where 4 warps would be all that an SM runs.
   static constexpr int kSplit = kRowWarps == 4 && kBlocksPerSm == 1 ? 2 : 1;
+  // Weights of the second product as two 16-bit numbers.  Beside e4m3 values
+  // only for up to 8 heads of up to 128: 128 requests of 1k to 16k keys, 32 / 8
+  // heads of 128, 229 -> 231 us and the error of o 1.681e-3 -> 1.669e-3 (that of
+  // its rounding); but 32 requests of 8192 keys, 8 key/value heads: 16 query heads
+  // each of 128, 105 -> 118; 32 of 64, 98 -> 132; 8 of 256, 92 -> 101.
+  static constexpr bool kTwoParts = !E4M3 || (NH == 1 && D <= 128);
   static constexpr int kThreads = kRowWarps * kSplit * 32;
   static constexpr int kHeads = 8 * NH;
   static constexpr int kOffsets = kStages + 1;               // tiles whose row offsets are kept
@@ -679,10 +685,12 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
                                          ? fmaf(x[k][i][2 * u + c], factor[i][c], ref) : -INFINITY;
           }
       }
-      // P^T for the second product (the sums take it in 32 bits): in fp16 (2^-11
-      // off), or beside bf16 values as the sum of two bf16 numbers: its upper
-      // half and the rest, rounded (2^-16 off).  One bf16 number alone would be
-      // off by as much as the rounding of o.  Neither part of a weight is
+      // P^T for the second product (the sums take it in 32 bits).  One 16-bit
+      // number would put o further from the exact row than its own rounding
+      // does (bf16: 1.4 times), so it is the sum of two: beside bf16 values its
+      // upper half and the rest, rounded (2^-16 off); beside e4m3 values its
+      // upper 11 bits and the rest in fp16 (2^-21 off), or one fp16 number
+      // (2^-11 off) where kTwoParts says so.  Neither part of a bf16 weight is
       // negative, and with the lowest bit set (2^-23) the rest is not zero, so
       // that an infinite value stays infinite (inf (p - q) + inf q and
       // inf 0 would not).
@@ -699,7 +707,14 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             if constexpr (E4M3) {
-              pf[k][i][u] = transposed(pack_f16x2(e[2 * u], e[2 * u + 1]));
+              if constexpr (S::kTwoParts) {
+                const float t0 = __uint_as_float(__float_as_uint(e[2 * u]) & 0xFFFFE000u);
+                const float t1 = __uint_as_float(__float_as_uint(e[2 * u + 1]) & 0xFFFFE000u);
+                pf[k][i][u] = transposed(pack_f16x2(t0, t1));
+                pr[k][i][u] = transposed(pack_f16x2(e[2 * u] - t0, e[2 * u + 1] - t1));
+              } else {
+                pf[k][i][u] = transposed(pack_f16x2(e[2 * u], e[2 * u + 1]));
+              }
             } else {
               const uint32_t b0 = __float_as_uint(e[2 * u]), b1 = __float_as_uint(e[2 * u + 1]);
               pf[k][i][u] = transposed(__byte_perm(b0, b1, 0x7632));
@@ -737,7 +752,10 @@ __global__ void __launch_bounds__(Shape<D, E4M3, NH, HW>::kThreads, Shape<D, E4M
               const uint32_t odd = __byte_perm(b[2 * u], b[2 * u + 1], 0x7531);
               const uint32_t a[4] = {e4m3_lo(even), e4m3_lo(odd), e4m3_hi(even), e4m3_hi(odd)};
 #pragma unroll
-              for (int i = 0; i < NH; ++i) mma<true>(o[i][j + u], a, pf[k][i][0], pf[k][i][1]);
+              for (int i = 0; i < NH; ++i) {
+                mma<true>(o[i][j + u], a, pf[k][i][0], pf[k][i][1]);
+                if constexpr (S::kTwoParts) mma<true>(o[i][j + u], a, pr[k][i][0], pr[k][i][1]);
+              }
             }
           }
         }

@@ -429,6 +429,35 @@ def test_decode_visible_nan_and_inf_reach_the_output():
         assert abs(lse.item() - want.item()) < 1e-4 and torch.isfinite(o).all()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,heads_kv,dim,width", [(4, 2, 64, 1), (8, 1, 128, 1), (4, 4, 128, 8000), (4, 4, 64, 8000),
+                                                      (12, 6, 128, 4000)])
+def test_decode_weights_are_not_rounded_to_16_bits(heads, heads_kv, dim, width, kv):
+    """Up to 8 query heads to a key/value head (of at most 128 at e4m3): values
+    that cancel, so that o is small beside sum p |v| and its own rounding does not
+    hide that of the weights.  A weight is two 16-bit numbers; fp16: the upper
+    11 bits, exact, and a rest below 2^-10 of it, rounded to 2^-11 of itself
+    (2^-21), or to steps of 2^-24 where it is subnormal (2^-25 over the 2^4 that
+    weights carry)."""
+    lens = [2, 4, 6, 9, 40]
+    p = Problem(lens, heads, heads_kv, dim, 16, kv, seed=dim, q_scale=0.02, extra_width=width)
+    for b, n in enumerate(lens):
+        for j in range(n):
+            p.v[p.table[b, j // 16].long(), j % 16] = torch.tensor((-1.0) ** j * 384).to(p.v.dtype)
+    o, lse = p.run()
+    ref, _, pv, xa = paged.decode(p.q.float(), p.k.float(), p.v.float(), p.table.numpy(), p.lens.numpy(), p.scale, 0,
+                                  p.k_scale, p.v_scale)
+    n = p.lens.numpy()[:, None]
+    delta = (dim + 4) * 2.0 ** -23 * xa
+    w = 2.0 ** -16 if kv == "bf16" else 2.0 ** -21
+    tol = U * np.abs(ref) + (1 + 2.0 ** -6) * (w + 2 * delta + (n + 32) * 2.0 ** -23)[..., None] * pv
+    if kv == "e4m3":
+        tol = tol + (n * 2.0 ** -29)[..., None] * 384 * p.v_scale.max().item()
+    off = np.abs(o.float().cpu().double().numpy() - ref)
+    assert np.all(off <= tol), (off / tol).max()
+    p.check(o, lse)
+
+
 @pytest.mark.parametrize("heads,heads_kv,dim,width", [(4, 2, 64, 1), (4, 4, 128, 8000), (16, 1, 128, 1), (8, 1, 256, 1),
                                                       (24, 1, 64, 1), (16, 8, 128, 8000)])
 def test_decode_visible_infinite_values(heads, heads_kv, dim, width):
