@@ -43,6 +43,7 @@
 
 #include <atomic>
 
+#include "decode_shape.h"
 #include "internal.h"
 #include "paged.h"
 #include "sm103.cuh"
@@ -50,7 +51,6 @@
 namespace fa {
 namespace decode {
 
-constexpr int kMaxBlocks = 608;   // upper bound of a launch's blocks: 4 on each of 152 SMs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A warp's reference for the exponents moves only when a score exceeds it by
@@ -58,90 +58,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // maximum over the warp is taken a few times per unit instead of every tile.
 constexpr float kSlack = 8.f;
 
-// NH: groups of 8 query heads per key/value head; HW: key/value heads per tile.
-template <int D, bool E4M3, int NH, int HW>
-struct Shape {
-  static constexpr int kElem = E4M3 ? 1 : 2;
-  static constexpr int kRowBytes = D * kElem;
-  static constexpr int kRowsPerTile =   // heads x keys
-      E4M3 && (D == 64 || (D == 256 && NH > 1)) ? 128 : 64;
-  static constexpr int kTile = kRowsPerTile / HW;                    // keys
-  static constexpr int kHeadBytes = kTile * kRowBytes;
-  static constexpr int kTileBytes = kRowsPerTile * kRowBytes;        // of K, and of V
-  static constexpr int kStageBytes = 2 * kTileBytes;
-  // Blocks per SM: what shared memory (the ring of stages) and registers
-  // (fragments of O and Q) leave room for.
-  static constexpr int kBlocksPerSm = kStageBytes >= 65536 || (kStageBytes >= 32768 && NH > 2) ? 1
-                                      : kStageBytes >= 32768 || NH > 2                         ? 2
-                                      : NH > 1 || E4M3                                         ? 3
-                                                                                               : 4;
-  static constexpr int kStages = kStageBytes < 65536 && kBlocksPerSm == 1 ? 5 : 3;
-  static constexpr int kRowWarps = kStageBytes >= 65536 && E4M3 ? 8 : 4;   // warps over a tile's rows
-  static constexpr int kKeyWarps = kRowWarps / HW;
-  static constexpr int kKeys = kTile / kKeyWarps;                          // of a warp
-  // Warps over the same rows, each with a part of O's columns (and all of the
-  // scores), where 4 warps would be all that an SM runs.
-  static constexpr int kSplit = kRowWarps == 4 && kBlocksPerSm == 1 ? 2 : 1;
-  // Weights of the second product as two 16-bit numbers.  Beside e4m3 values
-  // only for up to 8 heads of up to 128: 128 requests of 1k to 16k keys, 32 / 8
-  // heads of 128, 229 -> 231 us and the error of o 1.681e-3 -> 1.669e-3 (that of
-  // its rounding); but 32 requests of 8192 keys, 8 key/value heads: 16 query heads
-  // each of 128, 105 -> 118; 32 of 64, 98 -> 132; 8 of 256, 92 -> 101.
-  static constexpr bool kTwoParts = !E4M3 || (NH == 1 && D <= 128);
-  static constexpr int kThreads = kRowWarps * kSplit * 32;
-  static constexpr int kHeads = 8 * NH;
-  static constexpr int kOffsets = kStages + 1;               // tiles whose row offsets are kept
-  // Key warps' O are joined in the stage just consumed, so many heads at a time.
-  static constexpr int kJoinFit = kStageBytes / (kRowWarps * D * 4) / 8 * 8;
-  static constexpr int kJoinHeads = kJoinFit < kHeads ? kJoinFit : kHeads;
-  static constexpr int kSeenWords = (kTile + 31) / 32;
-  static constexpr int kOffOffsets = kStages * kStageBytes;
-  static constexpr int kOffSeen = kOffOffsets + kOffsets * kTile * 8;
-  static constexpr int kOffJoin = kOffSeen + kOffsets * kSeenWords * 4;
-  static constexpr int kOffScan = kOffJoin + (kKeyWarps > 1 ? 2 * kRowWarps * kHeads * 4 : 0);
-  static constexpr int kOffZero = (kOffScan + kThreads / 32 * 4 + 44 + 15) / 16 * 16;   // 16 zero bytes
-  static constexpr int kOffQ = kOffZero + 16;   // query rows of kStages units
-  static_assert(kJoinHeads >= 8, "join buffer");
-  static_assert(kTile == 16 || kTile == 32 || kTile == 64 || kTile == 128, "tile_shift");
-  static_assert(kKeys == 16 || kKeys == 32, "a word of seen keys");
-  static_assert(kTile <= kThreads && kTile % 16 == 0, "a thread per key looks up its page");
-  static constexpr int smem(int rows) { return kOffQ + kStages * HW * rows * D * 2; }
-  static constexpr bool fits(int rows) {
-    return smem(rows) <= 227 * 1024 && kBlocksPerSm * (smem(rows) + 1024) <= 228 * 1024;
-  }
-  static_assert(HW > 1 || fits(kHeads), "shared memory");
-};
-
-// A unit that the end of a run cuts, entered by the run it starts in: runs
-// [this one, last] hold its partial results, this one's in slot `slot`, the
-// others' in slot 0.  (With fewer units than runs the combine kernel has a
-// block per unit, which works this out from the lengths instead.)
-struct Cut {
-  int unit;    // b * (heads_kv / HW) + head group, or -1: none
-  int last;
-  int slot;
-  int pad;
-};
-
-struct Launch {
-  int rows;        // query heads of a key/value head per chunk (at most 8 NH)
-  int chunks;      // chunks of the G query heads of a key/value head
-  int group;       // key/value heads per tile
-  int blocks;      // blocks per chunk
-  int tile_shift;  // log2 of the keys per tile
-  int by_unit;     // combine goes by units, not by cuts
-  int sms;         // of the device (host only, like the next)
-  int device;
-};
-
 // Workspace: [blocks] cuts, then partial results [blocks][2 slots]: [HW][rows]
 // of D sums of p v, then [HW][rows] references and [HW][rows] sums of p.
-__host__ __device__ inline float* parts_of(float* work, size_t blocks) {
+__device__ __forceinline__ float* parts_of(float* work, size_t blocks) {
   return reinterpret_cast<float*>(reinterpret_cast<Cut*>(work) + blocks);
-}
-
-__host__ __device__ inline size_t part_floats(int rows, int d) {
-  return (static_cast<size_t>(rows) * (d + 2) + 3) / 4 * 4;   // 16-byte aligned
 }
 
 // ------------------------------------------------------------------ PTX
@@ -230,8 +150,8 @@ struct Lens {
 };
 
 // The list of all tiles (requests in order, the head groups of each, the
-// tiles of each) cut into `runs` runs of equal cost, one per block, none with
-// fewer blocks than tiles.  From 4 tiles per block on, a tile costs 2 and the
+// tiles of each) cut into `runs` runs of equal cost, one per block; with fewer
+// tiles than blocks, as many runs as tiles.  From 4 tiles per block on, a tile costs 2 and the
 // end of a unit (warps joined, rows written: 0.5 to 0.7 us beside 1 to 1.3 for
 // a tile) 1, and a tile belongs to the run its start lies in; against equal
 // numbers of tiles: 37 requests of 1 to 5000 keys, window 1024, 16 heads of
@@ -240,7 +160,6 @@ struct Lens {
 // count alike: whole tiles are all there is to share out
 // (64 of 1 to 120, 32 / 8 heads of 128: 7.8 us, by cost 9.2).
 struct Runs {
-  static constexpr int kManyTiles = 4;   // per block
   int tile, end;   // costs
   int runs, base, rem;
   __device__ __forceinline__ Runs(int tiles, int units, int blocks) {
@@ -1088,40 +1007,21 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const DecodeParam
 }
 
 // ------------------------------------------------------------------ launch
-// The longest stretch of keys that a request can see, and what it comes to in tiles.
-inline int longest(const DecodeParams& p) {
-  const int n = p.max_pages * p.kv.page_size;
-  return p.window > 0 && p.window < n ? p.window : n;
-}
-inline long long tiles_of(const DecodeParams& p, int tile) {
-  const int n = longest(p);
-  return n > tile ? (n + static_cast<long long>(tile) - 1) / tile : 1;
-}
-
 template <int D, bool E4M3, int NH, int HW>
-cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
+cudaError_t launch_shape(const DecodeParams& p, const Call& c, Launch lc, cudaStream_t s) {
   using Sh = Shape<D, E4M3, NH, HW>;
   static std::atomic<unsigned long long> done{0}, few_done{0}, many_done{0};
   auto* const kernel = decode_kernel<D, E4M3, NH, HW>;
   cudaError_t e = prepare_once(reinterpret_cast<const void*>(kernel), 227 * 1024, lc.device, done);
   if (e != cudaSuccess) return e;
-  lc.group = HW;
-  // At most one block per tile, at most the blocks that are resident at once.
-  const long long unit_tiles = tiles_of(p, Sh::kTile);
-  const long long tiles = unit_tiles * p.batch * (p.kv.heads_kv / HW);
-  long long blocks = Sh::kBlocksPerSm * lc.sms;
-  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
-  blocks = blocks / lc.chunks > 1 ? blocks / lc.chunks : 1;
-  lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
-  const long long units = static_cast<long long>(p.batch) * (p.kv.heads_kv / HW);
-  lc.by_unit = 2 * units <= lc.blocks;
-  lc.tile_shift = Sh::kTile == 16 ? 4 : Sh::kTile == 32 ? 5 : Sh::kTile == 64 ? 6 : 7;
+  set_blocks<Sh, HW>(c, lc);
   e = launch_pdl(kernel, dim3(lc.blocks, lc.chunks), dim3(Sh::kThreads), Sh::smem(lc.rows), s, p, lc);
-  if (e != cudaSuccess || unit_tiles == 1) return e;   // units of one tile are never cut
-  dim3 grid(lc.by_unit ? static_cast<unsigned>(units) : lc.blocks, lc.chunks * HW * lc.rows, D == 256 ? 2 : 1);
+  if (e != cudaSuccess || !lc.joined) return e;
+  const int units = p.batch * (p.kv.heads_kv / HW);
+  dim3 grid(lc.by_unit ? units : lc.blocks, lc.chunks * HW * lc.rows, D == 256 ? 2 : 1);
   // A unit lies in about blocks / units runs (ragged lengths: some in several
   // times as many).
-  const bool few = 8 * units > lc.blocks;
+  const bool few = 8ll * units > lc.blocks;
   auto* const combine = few ? combine_kernel<D, (D < 128 ? D : 128) / 4> : combine_kernel<D, 8>;
   if (!few) grid.z = D / 32;
   e = prepare_once(reinterpret_cast<const void*>(combine), 0, lc.device, few ? few_done : many_done);
@@ -1129,39 +1029,11 @@ cudaError_t launch_shape(const DecodeParams& p, Launch lc, cudaStream_t s) {
   return launch_pdl(combine, grid, dim3(kJoinThreads), 0, s, p, lc);
 }
 
-// Whether tiles of HW key/value heads are taken: where their queries fit
-// beside the ring of stages, and either blocks have enough tiles (12 at least,
-// were every request as long as can be) for the longer DRAM pieces to matter
-// more than the more numerous partial results per unit, or units are many and
-// of one or two tiles, so that few are cut and what counts is their number.  4 heads against 1, on one
-// GPU: 128 requests of 1k to 16k keys, 32 / 8 heads, d = 128, e4m3: 221 and
-// 254 us; one request of 1k keys, bf16: 8.1 and 6.9 us; 189 requests of 2
-// keys, 16 heads of 64, e4m3: 7.4 and 14.6 us.
-template <int D, bool E4M3, int NH, int HW>
-bool take_group(const DecodeParams& p, const Launch& lc) {
-  using Sh = Shape<D, E4M3, NH, HW>;
-  const long long units = static_cast<long long>(p.batch) * (p.kv.heads_kv / HW), resident = Sh::kBlocksPerSm * 152;
-  return p.kv.heads_kv % HW == 0 && Sh::fits(lc.rows) &&
-         (tiles_of(p, Sh::kTile) * units >= 12 * resident || (units >= resident && tiles_of(p, Sh::kTile) <= 2));
-}
-
-template <int D, bool E4M3, int NH>
-cudaError_t launch_group(const DecodeParams& p, const Launch& lc, cudaStream_t s) {
-  if (take_group<D, E4M3, NH, 4>(p, lc)) return launch_shape<D, E4M3, NH, 4>(p, lc, s);
-  if (take_group<D, E4M3, NH, 2>(p, lc)) return launch_shape<D, E4M3, NH, 2>(p, lc, s);
-  return launch_shape<D, E4M3, NH, 1>(p, lc, s);
-}
-
 template <int D, bool E4M3>
-cudaError_t launch_rows(const DecodeParams& p, const Launch& lc, cudaStream_t s) {
-  if (lc.rows <= 8) return launch_group<D, E4M3, 1>(p, lc, s);
-  if constexpr (D == 64 || (D == 128 && E4M3)) {
-    // more than 16 query heads on a key/value head: one of those at a time
-    if constexpr (D == 64)
-      if (lc.rows > 24) return launch_shape<D, E4M3, 4, 1>(p, lc, s);
-    if (lc.rows > 16) return launch_shape<D, E4M3, 3, 1>(p, lc, s);
-  }
-  return launch_group<D, E4M3, 2>(p, lc, s);
+cudaError_t launch_dim(const DecodeParams& p, const Call& c, const Launch& lc, cudaStream_t s) {
+  return with_shape<D, E4M3>(c, lc, [&](auto nh, auto hw) {
+    return launch_shape<D, E4M3, decltype(nh)::value, decltype(hw)::value>(p, c, lc, s);
+  });
 }
 
 }  // namespace decode

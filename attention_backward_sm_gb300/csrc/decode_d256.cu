@@ -2,7 +2,7 @@
 #include "decode.cuh"
 
 namespace fa {
-cudaError_t launch_decode_d256(const DecodeParams& p, const decode::Launch& lc, cudaStream_t s) {
-  return p.kv.e4m3 ? decode::launch_rows<256, true>(p, lc, s) : decode::launch_rows<256, false>(p, lc, s);
+cudaError_t launch_decode_d256(const DecodeParams& p, const decode::Call& c, const decode::Launch& lc, cudaStream_t s) {
+  return p.kv.e4m3 ? decode::launch_dim<256, true>(p, c, lc, s) : decode::launch_dim<256, false>(p, c, lc, s);
 }
 }  // namespace fa

@@ -22,6 +22,7 @@ import torch
 import oracle
 import seeded_inputs as si
 from oracle import paged
+from paged_paths import PATHS
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -370,6 +371,25 @@ def test_decode_splits(batch, hi, heads, heads_kv, dim, kv):
         p.check(o, lse)
         again = p.run()
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("path", PATHS, ids=str)
+def test_decode_paths(path):
+    """Every way of cutting and joining runs, with each shape of tiles (what a
+    case takes is pinned in test_paged_cpu.py).  The workspace holds NaN before
+    the call, and what lies behind it is left alone."""
+    f = fab()
+    have = -(-max(path.lens) // path.page)
+    p = Problem(path.lens, path.heads, path.heads_kv, path.dim, path.page, path.kv, seed=path.heads,
+                extra_width=path.width - have)
+    size = f.fa_decode_workspace_size(path.batch, path.heads, path.heads_kv, path.dim)
+    work = torch.full((size + 4096,), 255, dtype=torch.uint8, device=DEV)
+    args = p.device()
+    o, lse = f.decode(**args, workspace=work[:size])
+    assert torch.all(work[size:] == 255)
+    p.check(o, lse)
+    again = f.decode(**args)
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])

@@ -2,6 +2,8 @@
 of the C entry points and of the binding (all before anything touches the
 device)."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -9,6 +11,7 @@ import torch
 
 import oracle
 from oracle import paged
+from paged_paths import PATHS
 
 
 @pytest.fixture(scope="module")
@@ -227,3 +230,73 @@ def test_workspace_size_binding_raises_the_code_of_fa_decode(lib, args, code):
     assert e.value.code == code
     batch, heads, heads_kv, dim = args
     assert _decode_rc(lib, batch=batch, heads=heads, heads_kv=heads_kv, dim=dim) == (2 if dim == 96 else code)
+
+
+# ------------------------------------------------------------------ what a call launches
+SHAPES = r"""
+#include <cstdio>
+#include "decode_shape.h"
+using namespace fa::decode;
+
+template <int D, bool E>
+void show(const Call& c) {
+  Launch lc = split_heads(c.heads, c.heads_kv, c.head_dim, c.e4m3);
+  with_shape<D, E>(c, lc, [&](auto nh, auto hw) {
+    using Sh = Shape<D, E, decltype(nh)::value, decltype(hw)::value>;
+    set_blocks<Sh, decltype(hw)::value>(c, lc);
+    // what the launch writes: cuts, and two partial results per block
+    const size_t used = static_cast<size_t>(lc.blocks) * lc.chunks *
+                        (sizeof(Cut) + 2 * part_floats(lc.group * lc.rows, D) * sizeof(float));
+    std::printf("%d %d %d %d %d %d %d %d %d %zu %zu\n", decltype(nh)::value, decltype(hw)::value, lc.rows, lc.chunks,
+                lc.blocks, 1 << lc.tile_shift, lc.by_unit, lc.joined, Sh::kTile, used,
+                workspace_bytes(c.batch, c.heads, c.heads_kv, c.head_dim));
+    return 0;
+  });
+}
+
+int main() {
+  Call c;
+  int e4m3;
+  while (std::scanf("%d %d %d %d %d %d %d %d", &c.batch, &c.heads, &c.heads_kv, &c.head_dim, &e4m3, &c.keys, &c.window,
+                    &c.sms) == 8) {
+    c.e4m3 = e4m3 != 0;
+    if (c.head_dim == 64) c.e4m3 ? show<64, true>(c) : show<64, false>(c);
+    if (c.head_dim == 128) c.e4m3 ? show<128, true>(c) : show<128, false>(c);
+    if (c.head_dim == 256) c.e4m3 ? show<256, true>(c) : show<256, false>(c);
+  }
+}
+"""
+
+
+class Shape:
+    def __init__(self, line):
+        (self.nh, self.hw, self.rows, self.chunks, self.blocks, self.tile, self.by_unit, self.joined, self.kernel_tile,
+         self.used, self.workspace) = map(int, line.split())
+
+
+@pytest.fixture(scope="module")
+def shapes(tmp_path_factory):
+    """shapes(calls): what each of (batch, heads, heads_kv, head_dim, e4m3,
+    keys, window, SMs) launches, from the library's own header."""
+    at = tmp_path_factory.mktemp("shapes")
+    (at / "main.cpp").write_text(SHAPES)
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "attention_backward_sm_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I" + csrc, str(at / "main.cpp"), "-o", str(at / "main")],
+                   check=True)
+
+    def ask(calls):
+        text = "".join(" ".join(map(str, c)) + "\n" for c in calls)
+        out = subprocess.run([str(at / "main")], input=text, capture_output=True, text=True, check=True).stdout
+        return [Shape(line) for line in out.splitlines()]
+    return ask
+
+
+@pytest.mark.parametrize("path", PATHS, ids=str)
+def test_decode_takes_the_path_that_its_case_is_there_for(shapes, path):
+    assert max(path.lens) <= path.width * path.page
+    s, = shapes([(path.batch, path.heads, path.heads_kv, path.dim, int(path.kv == "e4m3"), path.width * path.page, 0, 152)])
+    tiles = sum(max(1, -(-n // s.tile)) for n in path.lens) * (path.heads_kv // s.hw)
+    assert (s.nh, s.hw, s.chunks) == (path.nh, path.hw, path.chunks)
+    assert ("none" if not s.joined else "unit" if s.by_unit else "cut") == path.join
+    assert (tiles >= 4 * s.blocks) == path.cost
+    assert s.tile == s.kernel_tile
