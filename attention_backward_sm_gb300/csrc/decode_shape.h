@@ -11,7 +11,7 @@
 namespace fa {
 namespace decode {
 
-constexpr int kMaxBlocks = 608;   // upper bound of a launch's blocks: 4 on each of 152 SMs
+constexpr int kMaxSms = 152;   // of a GB300; a launch's blocks are at most what it holds
 // Tiles per block from which on runs are cut by cost (Runs in decode.cuh).
 constexpr int kManyTiles = 4;
 
@@ -152,25 +152,37 @@ bool take_group(const Call& c, const Launch& lc) {
          (tiles_of(c, Sh::kTile) * units >= 12 * resident || (units >= resident && tiles_of(c, Sh::kTile) <= 2));
 }
 
-// f(NH, HW), as integral constants, with the shape that a call takes.
-template <int D, bool E4M3, int NH, class F>
-auto with_group(const Call& c, const Launch& lc, F f) {
+// f(NH), as an integral constant, for so many query heads per chunk.
+template <int D, bool E4M3, class F>
+auto with_rows(int rows, F f) {
   using std::integral_constant;
-  if (take_group<D, E4M3, NH, 4>(c, lc)) return f(integral_constant<int, NH>(), integral_constant<int, 4>());
-  if (take_group<D, E4M3, NH, 2>(c, lc)) return f(integral_constant<int, NH>(), integral_constant<int, 2>());
-  return f(integral_constant<int, NH>(), integral_constant<int, 1>());
+  if (rows <= 8) return f(integral_constant<int, 1>());
+  if constexpr (D == 64)
+    if (rows > 24) return f(integral_constant<int, 4>());
+  if constexpr (D == 64 || (D == 128 && E4M3))
+    if (rows > 16) return f(integral_constant<int, 3>());
+  return f(integral_constant<int, 2>());
 }
+
+// f(NH, HW), as integral constants, with the shape that a call takes.
 template <int D, bool E4M3, class F>
 auto with_shape(const Call& c, const Launch& lc, F f) {
   using std::integral_constant;
-  if (lc.rows <= 8) return with_group<D, E4M3, 1>(c, lc, f);
-  if constexpr (D == 64 || (D == 128 && E4M3)) {
-    // more than 16 query heads on a key/value head: one of those at a time
-    if constexpr (D == 64)
-      if (lc.rows > 24) return f(integral_constant<int, 4>(), integral_constant<int, 1>());
-    if (lc.rows > 16) return f(integral_constant<int, 3>(), integral_constant<int, 1>());
-  }
-  return with_group<D, E4M3, 2>(c, lc, f);
+  return with_rows<D, E4M3>(lc.rows, [&](auto nh) {
+    constexpr int NH = decltype(nh)::value;
+    if constexpr (NH <= 2) {   // more than 16 query heads on a key/value head: one of those at a time
+      if (take_group<D, E4M3, NH, 4>(c, lc)) return f(nh, integral_constant<int, 4>());
+      if (take_group<D, E4M3, NH, 2>(c, lc)) return f(nh, integral_constant<int, 2>());
+    }
+    return f(nh, integral_constant<int, 1>());
+  });
+}
+
+// The blocks of a chunk that are resident at once, of all chunks together.
+template <class Sh>
+int resident_blocks(const Launch& lc, int sms) {
+  const int blocks = Sh::kBlocksPerSm * (sms < kMaxSms ? sms : kMaxSms) / lc.chunks;
+  return blocks > 1 ? blocks : 1;
 }
 
 // At most one block per tile, at most the blocks that are resident at once.
@@ -179,25 +191,45 @@ void set_blocks(const Call& c, Launch& lc) {
   lc.group = HW;
   const long long unit_tiles = tiles_of(c, Sh::kTile);
   const long long units = static_cast<long long>(c.batch) * (c.heads_kv / HW), tiles = unit_tiles * units;
-  long long blocks = Sh::kBlocksPerSm * c.sms;
-  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
-  blocks = blocks / lc.chunks > 1 ? blocks / lc.chunks : 1;
-  lc.blocks = static_cast<int>(tiles < blocks ? tiles : blocks);
+  const int blocks = resident_blocks<Sh>(lc, c.sms);
+  lc.blocks = tiles < blocks ? static_cast<int>(tiles) : blocks;
   lc.by_unit = 2 * units <= lc.blocks;
   lc.tile_shift = Sh::kTile == 16 ? 4 : Sh::kTile == 32 ? 5 : Sh::kTile == 64 ? 6 : 7;
   lc.joined = unit_tiles > 1;   // units of one tile are never cut
 }
 
-// Bytes for any lengths, in a cache of either type.
-inline size_t workspace_bytes(const Launch& lc, int heads_kv, int head_dim) {
-  const int group = lc.rows > 16 ? 1 : heads_kv % 4 == 0 ? 4 : heads_kv % 2 == 0 ? 2 : 1;
-  const size_t blocks = lc.chunks > kMaxBlocks ? lc.chunks : kMaxBlocks;
-  return blocks * (sizeof(Cut) + 2 * part_floats(group * lc.rows, head_dim) * sizeof(float));
+// Bytes of the workspace of a shape, if calls of these heads can take it.
+template <int D, bool E4M3, int NH, int HW>
+size_t shape_bytes(const Launch& lc, int heads_kv) {
+  using Sh = Shape<D, E4M3, NH, HW>;
+  if (heads_kv % HW != 0 || (HW > 1 && !Sh::fits(lc.rows))) return 0;
+  const size_t blocks = static_cast<size_t>(resident_blocks<Sh>(lc, kMaxSms)) * lc.chunks;
+  return blocks * (sizeof(Cut) + 2 * part_floats(HW * lc.rows, D) * sizeof(float));
 }
+template <int D, bool E4M3>
+size_t cache_bytes(int heads, int heads_kv) {
+  const Launch lc = split_heads(heads, heads_kv, D, E4M3);
+  return with_rows<D, E4M3>(lc.rows, [&](auto nh) {
+    constexpr int NH = decltype(nh)::value;
+    size_t most = shape_bytes<D, E4M3, NH, 1>(lc, heads_kv);
+    if constexpr (NH <= 2) {
+      const size_t two = shape_bytes<D, E4M3, NH, 2>(lc, heads_kv), four = shape_bytes<D, E4M3, NH, 4>(lc, heads_kv);
+      most = most > two ? most : two;
+      most = most > four ? most : four;
+    }
+    return most;
+  });
+}
+
+// Bytes that are enough for any lengths, table and cache of either type.
 inline size_t workspace_bytes(int batch, int heads, int heads_kv, int head_dim) {
   if (batch == 0) return 0;
-  const size_t a = workspace_bytes(split_heads(heads, heads_kv, head_dim, false), heads_kv, head_dim);
-  const size_t b = workspace_bytes(split_heads(heads, heads_kv, head_dim, true), heads_kv, head_dim);
+  const size_t a = head_dim == 64    ? cache_bytes<64, false>(heads, heads_kv)
+                   : head_dim == 128 ? cache_bytes<128, false>(heads, heads_kv)
+                                     : cache_bytes<256, false>(heads, heads_kv);
+  const size_t b = head_dim == 64    ? cache_bytes<64, true>(heads, heads_kv)
+                   : head_dim == 128 ? cache_bytes<128, true>(heads, heads_kv)
+                                     : cache_bytes<256, true>(heads, heads_kv);
   return ((a > b ? a : b) + 255) / 256 * 256;
 }
 

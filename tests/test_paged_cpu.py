@@ -300,3 +300,31 @@ def test_decode_takes_the_path_that_its_case_is_there_for(shapes, path):
     assert ("none" if not s.joined else "unit" if s.by_unit else "cut") == path.join
     assert (tiles >= 4 * s.blocks) == path.cost
     assert s.tile == s.kernel_tile
+
+
+def test_decode_workspace_holds_what_any_launch_writes(lib, shapes):
+    """For every shape of heads, either cache, tables and windows of one key to
+    a million, few and many requests, fewer and more SMs than a GB300's: cuts
+    and partial results of all blocks fit, and the size is the C entry's."""
+    calls = []
+    for dim in (64, 128, 256):
+        for heads_kv in (1, 2, 3, 4, 6, 8, 16, 40):
+            for group in [*range(1, 35), 47, 48, 49, 63, 64, 65, 127, 128, 255, 300, 512, 1000, 1024]:
+                for e4m3 in (0, 1):
+                    for batch, keys, window, sms in ((1, 1, 0, 152), (1, 1 << 20, 0, 152), (3, 4096, 0, 148),
+                                                     (64, 8192, 0, 152), (64, 131072, 100, 152), (300, 64, 0, 152),
+                                                     (4000, 131072, 0, 152), (64, 8192, 0, 160), (64, 1 << 18, 0, 2),
+                                                     (700, 30, 0, 152), (700, 17, 0, 400)):
+                        calls.append((batch, heads_kv * group, heads_kv, dim, e4m3, keys, window, sms))
+    for c, s in zip(calls, shapes(calls)):
+        assert s.used <= s.workspace == lib.fa_decode_workspace_size(c[0], c[1], c[2], c[3]), c
+        assert s.blocks >= 1 and s.rows * s.chunks >= c[1] // c[2] > s.rows * (s.chunks - 1), c
+        assert s.tile == s.kernel_tile
+
+
+@pytest.mark.parametrize("heads,heads_kv,dim", [(64, 4, 256), (32, 8, 128), (16, 16, 64), (8, 1, 256), (300, 1, 128)])
+def test_decode_workspace_is_what_some_launch_needs(shapes, lib, heads, heads_kv, dim):
+    """No shape's blocks and heads per tile are multiplied with another's."""
+    calls = [(batch, heads, heads_kv, dim, e4m3, keys, 0, 152) for e4m3 in (0, 1)
+             for batch, keys in ((1, 1 << 20), (1, 4096), (64, 1 << 17), (700, 30))]
+    assert lib.fa_decode_workspace_size(1, heads, heads_kv, dim) <= max(s.used for s in shapes(calls)) + 255
