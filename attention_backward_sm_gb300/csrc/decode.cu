@@ -13,20 +13,11 @@ size_t decode_workspace_bytes(int batch, int heads, int heads_kv, int head_dim) 
   return decode::workspace_bytes(batch, heads, heads_kv, head_dim);
 }
 
-cudaError_t launch_decode(const DecodeParams& p, cudaStream_t s) {
+cudaError_t launch_decode(const DecodeParams& p, const Device& dev, cudaStream_t s) {
   decode::Launch lc = decode::split_heads(p.heads, p.kv.heads_kv, p.kv.head_dim, p.kv.e4m3);
-  decode::Call c{p.batch, p.heads, p.kv.heads_kv, p.kv.head_dim, p.kv.e4m3 != 0, p.max_pages * p.kv.page_size,
-                 p.window, 0};
-  static std::atomic<int> sms[64];   // of each device, once asked
-  cudaError_t e = cudaGetDevice(&lc.device);
-  if (e != cudaSuccess) return e;
-  const bool listed = lc.device >= 0 && lc.device < 64;
-  c.sms = listed ? sms[lc.device].load(std::memory_order_relaxed) : 0;
-  if (c.sms == 0) {
-    e = cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, lc.device);
-    if (e != cudaSuccess) return e;
-    if (listed) sms[lc.device].store(c.sms, std::memory_order_relaxed);
-  }
+  lc.device = dev.id;
+  const decode::Call c{p.batch, p.heads, p.kv.heads_kv, p.kv.head_dim, p.kv.e4m3 != 0, p.max_pages * p.kv.page_size,
+                       p.window, dev.sms};
   if (p.kv.head_dim == 64) return launch_decode_d64(p, c, lc, s);
   if (p.kv.head_dim == 128) return launch_decode_d128(p, c, lc, s);
   return launch_decode_d256(p, c, lc, s);

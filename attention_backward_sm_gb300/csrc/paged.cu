@@ -23,20 +23,23 @@ int cuda_fail(cudaError_t e, const char* where) {
 bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
-int check_device() {
-  static std::atomic<unsigned long long> ok_mask{0};   // devices already found to be sm_103
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+// The current device, which has to be what the library is built for.
+int check_device(fa::Device& d) {
+  static std::atomic<int> known[64];   // SMs of the devices already found to be sm_103
+  cudaError_t e = cudaGetDevice(&d.id);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
-  if (bit && (ok_mask.load(std::memory_order_acquire) & bit)) return FA_OK;
+  const bool listed = d.id >= 0 && d.id < 64;
+  d.sms = listed ? known[d.id].load(std::memory_order_acquire) : 0;
+  if (d.sms > 0) return FA_OK;
   int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d.id);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, d.id);
   if (major != 10 || minor != 3)
-    return set_last_error(FA_ERR_UNSUPPORTED, "this library is built for sm_103a; device %d is sm_%d%d", dev, major,
+    return set_last_error(FA_ERR_UNSUPPORTED, "this library is built for sm_103a; device %d is sm_%d%d", d.id, major,
                           minor);
-  if (bit) ok_mask.fetch_or(bit, std::memory_order_release);
+  e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, d.id);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  if (listed) known[d.id].store(d.sms, std::memory_order_release);
   return FA_OK;
 }
 
@@ -419,9 +422,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   }
 }
 
-int blocks_for(long long items, int threads, int per_sm) {
-  const long long want = (items + threads - 1) / threads;
-  const long long cap = 152ll * per_sm;   // SMs of a GB300
+int blocks_for(long long items, int threads, int most) {
+  const long long want = (items + threads - 1) / threads, cap = most;
   return static_cast<int>(want < 1 ? 1 : (want > cap ? cap : want));
 }
 
@@ -452,7 +454,8 @@ int fa_kv_plan(int32_t* block_table, long long table_stride, int max_pages, cons
     if (misaligned4(ptr)) return set_last_error(FA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(slots) & 7u)
     return set_last_error(FA_ERR_INVALID_ARG, "slots must be 8-byte aligned");
-  int rc = check_device();
+  fa::Device dev;
+  int rc = check_device(dev);
   if (rc) return rc;
   const PlanParams p{block_table,  table_stride, max_pages, seq_lens,
                      new_lens,     free_pages,   num_free,  free_start,
@@ -461,7 +464,7 @@ int fa_kv_plan(int32_t* block_table, long long table_stride, int max_pages, cons
                      cu_new,       seq_lens_out, free_next};
   // a thread per request, up to a block's most
   const int threads = batch <= 256 ? 256 : batch <= 512 ? 512 : kPlanMaxThreads;
-  cudaError_t e = fa::launch_pdl(plan_kernel, dim3(blocks_for(num_tokens, threads, 2)), dim3(threads), 0,
+  cudaError_t e = fa::launch_pdl(plan_kernel, dim3(blocks_for(num_tokens, threads, 2 * dev.sms)), dim3(threads), 0,
                                  reinterpret_cast<cudaStream_t>(stream), p);
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
   return ok();
@@ -490,7 +493,8 @@ int fa_kv_append(const fa_bf16* k, const fa_bf16* v, long long k_row_stride, lon
     return set_last_error(FA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(slots) & 7u)
     return set_last_error(FA_ERR_INVALID_ARG, "slots must be 8-byte aligned");
-  if ((rc = check_device())) return rc;
+  fa::Device dev;
+  if ((rc = check_device(dev))) return rc;
   p.k = k;
   p.v = v;
   p.k_row_stride = k_row_stride;
@@ -502,8 +506,8 @@ int fa_kv_append(const fa_bf16* k, const fa_bf16* v, long long k_row_stride, lon
   const int rows_per_pass = per_row < kAppendThreads ? kAppendThreads / per_row : 1;
   // several rows per thread where that still gives every SM two blocks
   const int most = p.kv.e4m3 ? 2 : 4;
-  const int rows = static_cast<long long>(num_tokens) * per_row >= 2ll * kAppendThreads * 152 * most ? most : 1;
-  const dim3 grid(blocks_for(num_tokens, rows_per_pass * rows, 64), (per_row + kAppendThreads - 1) / kAppendThreads);
+  const int rows = static_cast<long long>(num_tokens) * per_row >= 2ll * kAppendThreads * dev.sms * most ? most : 1;
+  const dim3 grid(blocks_for(num_tokens, rows_per_pass * rows, 64 * dev.sms), (per_row + kAppendThreads - 1) / kAppendThreads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void (*const kernel)(AppendParams) = p.kv.e4m3 ? (rows > 1 ? append_kernel<true, 2> : append_kernel<true, 1>)
                                                   : (rows > 1 ? append_kernel<false, 4> : append_kernel<false, 1>);
@@ -574,7 +578,8 @@ int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
   if (need > 0 && (!workspace || workspace_bytes < need))
     return set_last_error(FA_ERR_INVALID_ARG, "workspace of %zu bytes needed, got %zu", need, workspace_bytes);
   if (misaligned16(workspace)) return set_last_error(FA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-  if ((rc = check_device())) return rc;
+  fa::Device dev;
+  if ((rc = check_device(dev))) return rc;
   p.q = q;
   p.q_row_stride = q_row_stride;
   p.table = block_table;
@@ -589,7 +594,7 @@ int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
   p.heads = heads;
   p.window = window;
   p.scale = scale;
-  cudaError_t e = fa::launch_decode(p, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = fa::launch_decode(p, dev, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   return ok();
 }

@@ -105,7 +105,12 @@ struct DecodeParams {
   float scale;
 };
 
+struct Device {
+  int id;
+  int sms;
+};
+
 size_t decode_workspace_bytes(int batch, int heads, int heads_kv, int head_dim);
-cudaError_t launch_decode(const DecodeParams& p, cudaStream_t s);
+cudaError_t launch_decode(const DecodeParams& p, const Device& dev, cudaStream_t s);
 
 }  // namespace fa
