@@ -738,3 +738,95 @@ def test_stream_argument_keeps_the_inputs():
     stream.synchronize()
     assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])
     assert len(junk) == 3 * len(sizes)
+
+
+def test_refusals_beside_a_device():
+    """Malformed outputs and workspaces, tensors and streams of other devices:
+    refused before anything is launched."""
+    f = fab()
+    p = Problem([40, 3], 4, 2, 64, 16, seed=31)
+    a = p.device()
+    o, lse = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 4, device=DEV)
+    wide = torch.zeros(2, 8, 64, dtype=torch.bfloat16, device=DEV)
+
+    class Elsewhere:
+        stream_id, device_index, device_type = 0, torch.cuda.current_device() + 1, 1
+
+    for kw, word in ((dict(out=o), "tuple"), (dict(out=(o,)), "tuple"), (dict(out=[o, lse]), "tuple"),
+                     (dict(out=(o.float(), lse)), "o must"), (dict(out=(o[:1], lse)), "o must"),
+                     (dict(out=(wide[:, :4], lse)), "contiguous"), (dict(out=(o, lse.double())), "lse"),
+                     (dict(out=(o, lse[:, :3])), "lse"), (dict(out=(o, wide)), "lse"), (dict(out=(None, lse)), "o must"),
+                     (dict(out=(o.cpu(), lse)), "o is on"), (dict(out=(o, lse.cpu())), "lse is on"),
+                     (dict(workspace=torch.zeros(2, 1 << 20, device=DEV).t()), "workspace"),
+                     (dict(workspace=torch.zeros(1 << 20)), "workspace is on"),
+                     (dict(seq_lens=a["seq_lens"].cpu()), "seq_lens is on"), (dict(v_cache=a["v_cache"].cpu()), "v_cache is on"),
+                     (dict(stream=Elsewhere()), "stream is on device")):
+        with pytest.raises(ValueError, match=word):
+            f.decode(**{**a, **kw})
+    with pytest.raises(f.FabwdError, match="workspace"):
+        f.decode(**a, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(f.FabwdError, match="overlap"):
+        f.decode(**a, out=(a["q"], lse))
+    with pytest.raises(AttributeError):
+        f.decode(**a, stream="a stream")
+    i32 = dict(dtype=torch.int32, device=DEV)
+    args = (a["block_table"], a["seq_lens"], torch.ones(2, **i32), torch.arange(4, **i32), 16)
+    out = [torch.zeros(2, dtype=torch.int64, device=DEV), torch.zeros(2, **i32), torch.zeros(3, **i32), torch.zeros(2, **i32),
+           torch.zeros(1, **i32)]
+    for i, word in enumerate(("slots", "positions", "cu_new", "seq_lens_out", "free_next")):
+        with pytest.raises(ValueError, match=word):   # another type
+            f.fa_kv_plan(*args, *(out[:i] + [out[i].float()] + out[i + 1:]))
+        with pytest.raises(ValueError, match=word):   # another device
+            f.fa_kv_plan(*args, *(out[:i] + [out[i].cpu()] + out[i + 1:]))
+    with pytest.raises(ValueError, match="positions"):
+        f.fa_kv_plan(*args, *(out[:1] + [out[2]] + out[2:]))
+    with pytest.raises(f.FabwdError, match="seq_lens_out"):
+        f.fa_kv_plan(*args, *(out[:3] + [a["seq_lens"]] + out[4:]))
+    slots = torch.zeros(2, dtype=torch.int64, device=DEV)
+    rows = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    for kw, word in ((dict(k=rows.cpu()), "k is on"), (dict(slots=slots.cpu()), "slots is on"),
+                     (dict(stream=Elsewhere()), "stream is on device"), (dict(k_scale=torch.ones(2)), "k_scale is on")):
+        with pytest.raises(ValueError, match=word):
+            f.kv_append(**{**dict(k=rows, v=rows, k_cache=a["k_cache"], v_cache=a["v_cache"], slots=slots), **kw})
+    got, want = f.decode(**a), p.run()   # the device is as it was
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_serving_steps_match_the_definition(kv):
+    """plan -> append -> decode, prompts and then token by token, one request
+    getting none for some steps: tables, slots, caches and rows are the
+    definition's over the same history (rows within their bounds)."""
+    f = fab()
+    H, Hkv, d, page, pool, width = 8, 2, 128, 16, 40, 8
+    g = torch.Generator().manual_seed(41)
+    p = Problem([1] * 4, H, Hkv, d, page, kv, seed=41)
+    on = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    dtype = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    bits = torch.int16 if kv == "bf16" else torch.uint8
+    p.k = torch.full((pool, page, Hkv, d), float("nan")).to(dtype)
+    p.v = p.k.clone()
+    kc, vc = p.k.to(DEV), p.v.to(DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    free = torch.randperm(pool, generator=g).int()
+    table, seq, start = torch.full((4, width), -1, **i32), torch.zeros(4, **i32), torch.zeros(1, **i32)
+    want_table, want_seq, nxt = np.full((4, width), -1), [0] * 4, 0
+    for step in range(14):
+        new = [37, 0, 64, 15] if step == 0 else [1, 1, 1, 1 if step % 3 else 0]
+        n = sum(new) + 2                       # two rows of padding
+        want_table, slots, _, _, after, nxt = paged.plan(want_table, want_seq, new, free.numpy(), page, n, nxt)
+        want_seq = after.tolist()
+        rows = [torch.randn(n, Hkv, d, generator=g).bfloat16() for _ in range(2)]
+        plan = f.kv_plan(table, seq, torch.tensor(new, **i32), free.to(DEV), page, n, free_start=start)
+        f.kv_append(rows[0].to(DEV), rows[1].to(DEV), kc, vc, plan.slots, on(p.k_scale), on(p.v_scale))
+        seq, start = plan.seq_lens, plan.free_next
+        assert np.array_equal(table.cpu().numpy(), want_table) and np.array_equal(plan.slots.cpu().numpy(), slots)
+        ok = torch.from_numpy(slots >= 0)
+        for cache, row, scale, got in ((p.k, rows[0], p.k_scale, kc), (p.v, rows[1], p.v_scale, vc)):
+            if scale is not None:
+                row = (row.float() / scale[:, None]).clamp(-448, 448).to(dtype)
+            cache.view(bits).view(-1, Hkv, d)[torch.from_numpy(slots)[ok]] = row.view(bits)[ok]
+            assert torch.equal(got.cpu().view(bits), cache.view(bits))
+        p.q = torch.randn(4, H, d, generator=g).bfloat16()
+        p.table, p.lens = torch.from_numpy(want_table), torch.tensor(want_seq, dtype=torch.int32)
+        p.check(*f.decode(p.q.to(DEV), kc, vc, table, seq, p.scale, k_scale=on(p.k_scale), v_scale=on(p.v_scale)))

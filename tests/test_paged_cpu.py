@@ -328,3 +328,50 @@ def test_decode_workspace_is_what_some_launch_needs(shapes, lib, heads, heads_kv
     calls = [(batch, heads, heads_kv, dim, e4m3, keys, 0, 152) for e4m3 in (0, 1)
              for batch, keys in ((1, 1 << 20), (1, 4096), (64, 1 << 17), (700, 30))]
     assert lib.fa_decode_workspace_size(1, heads, heads_kv, dim) <= max(s.used for s in shapes(calls)) + 255
+
+
+# ------------------------------------------------------------------ more refusals
+@pytest.mark.parametrize("call,kw,code,word", [
+    ("plan", dict(out=ctypes.c_void_p(32)), 1, b"seq_lens_out"), ("plan", dict(new=None), 1, b"NULL"),
+    ("plan", dict(out=None), 1, b"NULL"), ("plan", dict(pos=None), 1, b"NULL"),
+    ("plan", dict(table=ctypes.c_void_p(18)), 1, b"aligned"), ("plan", dict(next=ctypes.c_void_p(98)), 1, b"aligned"),
+    ("append", dict(heads_kv=40000, ks=40000 * 128, vs=40000 * 128), 2, b"too large"),
+    ("append", dict(kind=1, k_scale=ctypes.c_void_p(18)), 1, b"aligned"),
+    ("append", dict(kind=1, v_scale=ctypes.c_void_p(18)), 1, b"aligned"),
+    ("append", dict(v_scale=P), 1, b"e4m3"), ("append", dict(vc=ctypes.c_void_p(24)), 1, b"aligned"),
+    ("append", dict(v=None), 1, b"NULL"), ("append", dict(vc=None), 1, b"NULL"),
+    ("decode", dict(lse=ctypes.c_void_p(18)), 1, b"aligned"), ("decode", dict(table=ctypes.c_void_p(18)), 1, b"aligned"),
+    ("decode", dict(q=ctypes.c_void_p(24)), 1, b"aligned"), ("decode", dict(o=None), 1, b"NULL"),
+    ("decode", dict(vc=None), 1, b"NULL"), ("decode", dict(kind=1, k_scale=ctypes.c_void_p(18)), 1, b"aligned"),
+    ("decode", dict(kind=-1), 1, b"kv_type"), ("decode", dict(pages=-1), 1, b"num_pages"),
+    ("decode", dict(page=0), 1, b"page_size"), ("decode", dict(heads_kv=0), 1, b"heads_kv")])
+def test_refusals_of_the_other_arguments(lib, call, kw, code, word):
+    assert {"plan": _plan_rc, "append": _append_rc, "decode": _decode_rc}[call](lib, **kw) == code
+    assert word in lib.fa_last_error()
+
+
+def test_decode_refuses_a_workspace_that_is_too_small(lib):
+    n = lib.fa_decode_workspace_size(64, 32, 8, 128)
+    assert n >= 2 * 152 * (16 + 2 * 4 * 4 * 130)   # two partial results of a head group for a block on every SM, at least
+    kw = dict(batch=64, heads=32, heads_kv=8, page_stride=16384, slot_stride=1024, qs=4096)
+    for bad in (dict(ws_bytes=n - 1), dict(ws_bytes=0), dict(ws=None), dict(ws=ctypes.c_void_p(8))):
+        assert _decode_rc(lib, **kw, **bad) == 1 and b"workspace" in lib.fa_last_error()
+
+
+def test_binding_refuses_what_is_no_tensor_or_number(lib):
+    import attention_backward_sm_gb300 as fab
+    t = _tensors()
+    with pytest.raises(ValueError, match="q must be a tensor"):
+        fab.decode(**{**t, "q": [1.0]}, scale=0.1)
+    with pytest.raises(TypeError):
+        fab.decode(**t, scale="large")
+    with pytest.raises(TypeError):
+        fab.decode(**t, scale=0.1, window=1.5)
+    with pytest.raises(ValueError, match="window does not fit"):
+        fab.decode(**t, scale=0.1, window=1 << 40)
+    i32 = dict(dtype=torch.int32)
+    args = [t["block_table"], t["seq_lens"], torch.ones(2, **i32), torch.zeros(4, **i32)]
+    with pytest.raises(ValueError, match="num_tokens"):
+        fab.kv_plan(*args, 8, -1)
+    with pytest.raises(ValueError, match="page_size does not fit"):
+        fab.kv_plan(*args, 1 << 40, 2)
