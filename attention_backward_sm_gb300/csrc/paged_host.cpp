@@ -103,7 +103,7 @@ int64_t row_stride(const Tensor& t, const char* name, int64_t n, int64_t heads, 
   if (t.scalar_type() != at::kBFloat16 || t.dim() != 3 || t.size(0) != n || t.size(1) != heads || t.size(2) != dim)
     refuse(std::string(name) + " must be bfloat16 (" + std::to_string(n) + ", " + std::to_string(heads) + ", " +
            std::to_string(dim) + "), the last being the cache's head_dim, got " + kind(t));
-  if (t.stride(2) != 1 || (heads > 1 && t.stride(1) != dim))
+  if (t.numel() && (t.stride(2) != 1 || (heads > 1 && t.stride(1) != dim)))
     refuse(std::string(name) + " must have its heads packed in each row, got strides " + dims(t.strides()));
   return n > 1 ? t.stride(0) : heads * dim;
 }
@@ -122,7 +122,9 @@ struct Cache {
     const auto st = k.scalar_type();
     if ((st != at::kBFloat16 && st != at::kFloat8_e4m3fn) || v.scalar_type() != st)
       refuse("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn, got " + kind(k) + " and " + kind(v));
-    if (k.stride(3) != 1 || k.strides() != v.strides())
+    bool alike = true;   // where there is more than one of something
+    for (int i = 0; i < 4; ++i) alike = alike && (k.size(i) <= 1 || k.stride(i) == v.stride(i));
+    if (k.numel() && (k.stride(3) != 1 || v.stride(3) != 1 || !alike))
       refuse("k_cache and v_cache must have the same strides, the last 1, got " + dims(k.strides()) + " and " +
              dims(v.strides()));
     type = st == at::kBFloat16 ? FA_KV_BF16 : FA_KV_E4M3;
@@ -146,7 +148,7 @@ struct Table {
       refuse("block_table must be int32 [batch, max_pages], got " + kind(t));
     batch = size32(t.size(0), "batch");
     width = size32(t.size(1), "max_pages");
-    if (width > 1 && t.stride(1) != 1)
+    if (batch > 0 && width > 1 && t.stride(1) != 1)
       refuse("block_table must have contiguous rows, got strides " + dims(t.strides()));
     stride = batch > 1 ? t.stride(0) : width;
   }

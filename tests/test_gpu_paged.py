@@ -830,3 +830,26 @@ def test_serving_steps_match_the_definition(kv):
         p.q = torch.randn(4, H, d, generator=g).bfloat16()
         p.table, p.lens = torch.from_numpy(want_table), torch.tensor(want_seq, dtype=torch.int32)
         p.check(*f.decode(p.q.to(DEV), kc, vc, table, seq, p.scale, k_scale=on(p.k_scale), v_scale=on(p.v_scale)))
+
+
+def test_strides_that_are_never_used_do_not_matter():
+    """Of a dimension of one, and of tensors without elements."""
+    f = fab()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    p = Problem([40, 3], 4, 1, 64, 16, seed=51)          # one key/value head: laid out alike, whatever its stride
+    a = p.device()
+    v = a["v_cache"].as_strided(a["v_cache"].shape, (16 * 64, 64, 1 << 20, 1))
+    got = f.decode(**{**a, "v_cache": v})
+    p.check(*got)
+    rows = torch.randn(5, 1, 64, device=DEV).bfloat16()
+    caches = [torch.zeros_like(v), torch.zeros(v.shape, dtype=v.dtype, device=DEV).as_strided(v.shape, v.stride())]
+    f.kv_append(rows, rows, *caches, torch.arange(5, device=DEV))
+    assert torch.equal(caches[0], caches[1]) and torch.equal(caches[0].view(-1, 64)[:5], rows[:, 0])
+    empty = torch.zeros(0, 6, **i32).as_strided((0, 6), (0, 0))
+    plan = f.kv_plan(empty, torch.zeros(0, **i32), torch.zeros(0, **i32), torch.arange(4, **i32), 16, 3,
+                     free_start=torch.tensor([2], **i32))
+    assert plan.slots.tolist() == [-1] * 3 and plan.positions.tolist() == [0] * 3
+    assert plan.cu_new.tolist() == [0] and plan.seq_lens.numel() == 0 and plan.free_next.tolist() == [2]
+    o, lse = f.decode(a["q"][:0].as_strided((0, 4, 64), (0, 0, 0)), a["k_cache"], v, empty, a["seq_lens"][:0], p.scale)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    f.kv_append(rows[:0].as_strided((0, 1, 64), (0, 0, 0)), rows[:0], *caches, torch.zeros(0, dtype=torch.int64, device=DEV))
