@@ -32,8 +32,8 @@
 //
 // Measured (GPU time, bytes that have to be read over it): 64 requests of 256
 // to 8192 keys, 32 / 8 heads of 128, bf16: 96 us, 6.3 TB/s; 4 of 65536 to
-// 131072: 222 us, 7.0 TB/s (of a copy's 6.8); 128 of 1024 to 16384, e4m3: 229
-// us, 6.4 TB/s; one of 1024: 5.4 us, of which 0.6 are its bytes: two launches,
+// 131072: 222 us, 7.0 TB/s (of a copy's 6.7); 128 of 1024 to 16384, e4m3: 231
+// us, 6.3 TB/s; one of 1024: 5.4 us, of which 0.6 are its bytes: two launches,
 // the lengths, the table, the keys and the partial results are read one after
 // the other.
 #pragma once

@@ -27,9 +27,10 @@ struct PagedCache {
   int head_dim;
 };
 
-// n / d for 0 <= n < 2^31 by a product: with 2^shift the power of two at or
-// above d and mul = ceil(2^32 (2^shift - d) / d) (+ 1 where exact), the sum
-// n + floor(n mul / 2^32) over 2^shift is exact for all 32-bit n.
+// n / d for 0 <= n < 2^31 by a product, after Granlund and Montgomery
+// (Division by Invariant Integers using Multiplication, 1994): with 2^shift
+// the power of two at or above d and mul = floor(2^32 (2^shift - d) / d) + 1,
+// the sum n + floor(n mul / 2^32) over 2^shift is exact for all 32-bit n.
 struct FastDiv {
   uint32_t mul;
   uint32_t shift;

@@ -44,7 +44,9 @@ def _host():
 class KvPlan(NamedTuple):
     """What kv_plan returns: slots int64 and positions int32 per new token,
     cu_new int32 [batch + 1], seq_lens int32 [batch] with the new tokens
-    counted, free_next int32 [1]."""
+    counted, free_next int32 [1].  They are cut from one allocation: keeping
+    one keeps all (as does record_stream), and torch.save of one writes all
+    unless it is cloned.  fa_kv_plan fills tensors of your own."""
     slots: torch.Tensor
     positions: torch.Tensor
     cu_new: torch.Tensor
@@ -98,8 +100,8 @@ def fa_decode(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: float, 
 def decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, window: int = 0, k_scale=None, v_scale=None,
            out=None, workspace=None, stream=None):
     """Attention of one new token per request, q [batch, H, d], over the
-    cache; returns (o, lse).  out: (o, lse) to fill instead of new tensors
-    (lse may be None).  workspace: fa_decode_workspace_size() bytes to use
+    cache; returns (o, lse), cut from one allocation like kv_plan's.  out:
+    (o, lse) to fill instead of new tensors (lse may be None).  workspace: fa_decode_workspace_size() bytes to use
     instead of fresh ones (calls that may overlap need one each)."""
     return (_native or _host()).decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, k_scale, v_scale, out,
                                        workspace, stream)

@@ -311,7 +311,7 @@ enum fa_kv_type {
  *     request of every new token, requests in order.  Rows past the last new
  *     token (a padded batch) get slot -1, position 0.
  *   cu_new[batch+1]: offsets of the requests' new tokens (the cu_q of a
- *     following fa_fwd_* call);  seq_lens_out[batch] = seq_lens + new_lens;
+ *     following fa_fwd_* call, which takes the same offsets on the host, too);  seq_lens_out[batch] = seq_lens + new_lens;
  *   free_next[1]: the first entry of free_pages not taken.
  * A token for which the table row or the free list has no page gets slot -1
  * (and the table entry -1); *free_next > num_free tells that the list ran
@@ -355,7 +355,8 @@ size_t fa_decode_workspace_size(int batch, int heads, int heads_kv, int head_dim
  * count in seq_lens.  Lengths are clamped to max_pages * page_size.  Query
  * head h reads key/value head h / (H / Hkv), at most 1024 of them each.  A row that sees no key gets
  * o = 0, lse = -inf.  Contents of slots that are not seen do not matter
- * (NaN included).  o must not overlap q.  workspace: fa_decode_workspace_size() bytes, 16-byte
+ * (NaN included); an infinite value that is seen gives an infinite element.
+ * o must not overlap q.  workspace: fa_decode_workspace_size() bytes, 16-byte
  * aligned, contents arbitrary; calls whose work overlaps on the GPU need one
  * each.  Results do not depend on timing: the same call gives the same bits. */
 int fa_decode(const fa_bf16* q, long long q_row_stride,
