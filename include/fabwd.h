@@ -355,7 +355,8 @@ size_t fa_decode_workspace_size(int batch, int heads, int heads_kv, int head_dim
  * count in seq_lens.  Lengths are clamped to max_pages * page_size.  Query
  * head h reads key/value head h / (H / Hkv), at most 1024 of them each.  A row that sees no key gets
  * o = 0, lse = -inf.  Contents of slots that are not seen do not matter
- * (NaN included); an infinite value that is seen gives an infinite element.
+ * (NaN included); an infinite value that is seen gives an infinite element
+ * (NaN beside one of the other sign, or where its weight underflows to 0).
  * o must not overlap q.  workspace: fa_decode_workspace_size() bytes, 16-byte
  * aligned, contents arbitrary; calls whose work overlaps on the GPU need one
  * each.  Results do not depend on timing: the same call gives the same bits. */

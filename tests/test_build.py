@@ -93,3 +93,15 @@ def test_entry_build_imports_the_extension(monkeypatch):
     monkeypatch.delattr("attention_backward_sm_gb300._paged_host", raising=False)
     with pytest.raises(ImportError):
         entry.build()
+
+
+def test_entry_build_without_the_extension(compilers, monkeypatch, tmp_path):
+    """Beside a PyTorch without CUDA the entry builds and loads the library."""
+    import __graft_entry__ as entry
+    import attention_backward_sm_gb300 as fab
+    torch_at(monkeypatch, fake_torch(tmp_path / "torch", "1", cuda=False))
+    loaded = []
+    monkeypatch.setattr(fab, "lib", lambda: loaded.append(1))
+    monkeypatch.setattr(fab.paged, "_host", lambda: pytest.fail("there is none"))
+    entry.build()
+    assert loaded and not os.path.exists(b.HOST)
