@@ -7,100 +7,14 @@
 #include <atomic>
 
 #include "../../include/fabwd.h"
+#include "checks.h"
 #include "internal.h"
 #include "paged.h"
+#include "quantise.cuh"
 
 namespace {
 
-using fa::set_last_error;
-
-int ok() { return set_last_error(FA_OK, "%s", ""); }
-
-int cuda_fail(cudaError_t e, const char* where) {
-  return set_last_error(FA_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
-
-// The current device, which has to be what the library is built for.
-int check_device(fa::Device& d) {
-  static std::atomic<int> known[64];   // SMs of the devices already found to be sm_103
-  cudaError_t e = cudaGetDevice(&d.id);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  const bool listed = d.id >= 0 && d.id < 64;
-  d.sms = listed ? known[d.id].load(std::memory_order_acquire) : 0;
-  if (d.sms > 0) return FA_OK;
-  int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d.id);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, d.id);
-  if (major != 10 || minor != 3)
-    return set_last_error(FA_ERR_UNSUPPORTED, "this library is built for sm_103a; device %d is sm_%d%d", d.id, major,
-                          minor);
-  e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, d.id);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-  if (listed) known[d.id].store(d.sms, std::memory_order_release);
-  return FA_OK;
-}
-
-// The cache's sizes, strides and types; pointers only where they are set.
-int check_cache(const fa::PagedCache& c, int kv_type) {
-  if (kv_type != FA_KV_BF16 && kv_type != FA_KV_E4M3)
-    return set_last_error(FA_ERR_INVALID_ARG, "kv_type must be 0 (bf16) or 1 (e4m3), got %d", kv_type);
-  if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
-    return set_last_error(FA_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256, got %d", c.head_dim);
-  if (c.heads_kv < 1) return set_last_error(FA_ERR_INVALID_ARG, "heads_kv must be >= 1, got %d", c.heads_kv);
-  if (c.num_pages < 0) return set_last_error(FA_ERR_INVALID_ARG, "num_pages must be >= 0, got %d", c.num_pages);
-  if (c.page_size < 1) return set_last_error(FA_ERR_INVALID_ARG, "page_size must be >= 1, got %d", c.page_size);
-  if (kv_type == FA_KV_BF16 && (c.k_scale || c.v_scale))
-    return set_last_error(FA_ERR_INVALID_ARG, "k_scale and v_scale belong to an e4m3 cache");
-  const long long unit = kv_type == FA_KV_E4M3 ? 16 : 8;   // elements in 16 bytes
-  const struct { const char* name; long long v; int n; } st[] = {
-      {"page_stride", c.page_stride, c.num_pages}, {"slot_stride", c.slot_stride, c.page_size},
-      {"head_stride", c.head_stride, c.heads_kv}};
-  for (const auto& s : st) {
-    if (s.n <= 1) continue;   // never multiplied by anything but 0
-    if (s.v < c.head_dim)
-      return set_last_error(FA_ERR_INVALID_ARG, "%s must be at least head_dim (%d elements), got %lld", s.name,
-                            c.head_dim, s.v);
-    if (s.v % unit)
-      return set_last_error(FA_ERR_INVALID_ARG, "%s must be a multiple of 16 bytes (%lld elements), got %lld", s.name,
-                            unit, s.v);
-  }
-  if (misaligned16(c.k) || misaligned16(c.v))
-    return set_last_error(FA_ERR_INVALID_ARG, "k_cache and v_cache must be 16-byte aligned");
-  if (misaligned4(c.k_scale) || misaligned4(c.v_scale))
-    return set_last_error(FA_ERR_INVALID_ARG, "k_scale and v_scale must be 4-byte aligned");
-  return FA_OK;
-}
-
-int check_row_stride(const char* name, long long stride, long long row, int rows) {
-  if (rows <= 1) return FA_OK;
-  if (stride < row || stride % 8)
-    return set_last_error(FA_ERR_INVALID_ARG,
-                          "%s must be a multiple of 8 elements and hold a whole row (%lld elements), got %lld", name,
-                          row, stride);
-  return FA_OK;
-}
-
-fa::PagedCache make_cache(const void* k, const void* v, int kv_type, const float* k_scale, const float* v_scale,
-                          long long page_stride, long long slot_stride, long long head_stride, int num_pages,
-                          int page_size, int heads_kv, int head_dim) {
-  fa::PagedCache c;
-  c.k = const_cast<void*>(k);
-  c.v = const_cast<void*>(v);
-  c.k_scale = k_scale;
-  c.v_scale = v_scale;
-  c.page_stride = page_stride;
-  c.slot_stride = slot_stride;
-  c.head_stride = head_stride;
-  c.e4m3 = kv_type == FA_KV_E4M3;
-  c.num_pages = num_pages;
-  c.page_size = page_size;
-  c.heads_kv = heads_kv;
-  c.head_dim = head_dim;
-  return c;
-}
+using namespace fa;
 
 // ---------------------------------------------------------------- plan
 constexpr int kPlanMaxThreads = 1024;
@@ -302,67 +216,6 @@ struct AppendParams {
   fa::FastDiv page_div;
   int num_tokens;
 };
-
-__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-
-// Two values to e4m3 (round to nearest even, saturating to +-448, NaN stays).
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
-
-// A scale and two factors, one below and one above its reciprocal: for any x,
-// the fp32 quotient x / s lies between the rounded products x lo and x hi
-// (each is off by less than 2^-22 of itself, the factors are 2^-21 apart from
-// the reciprocal).  Scales whose reciprocal is out of range get 0 and
-// infinity, between which everything lies.  The reciprocal of a power of two
-// (of the scale 1 of a cache without scales) is exact and the product with it
-// is the quotient, so it is both factors.
-struct Scale {
-  float s, lo, hi;
-  __device__ __forceinline__ explicit Scale(const float* p, int h) : s(p ? *(p + h) : 1.f) {
-    const bool plain = s >= 0x1p-100f && s <= 0x1p100f;
-    const float inv = 1.f / s, apart = (__float_as_uint(s) & 0x7FFFFFu) == 0 ? 0.f : 0x1p-21f;
-    lo = plain ? inv * (1.f - apart) : 0.f;
-    hi = plain ? inv * (1.f + apart) : INFINITY;
-  }
-};
-
-// Eight bf16 values divided by the scale, the quotients rounded to fp32, then
-// to e4m3.  Where both products round to the same 8-bit value, so does the
-// quotient between them; only where they do not are the divisions carried out
-// (5 instructions per value instead of 20).  That is one group of eight in
-// 2^13 for a scale with many significant bits, as a largest value over 448
-// has.  A scale of few, but no power of two (1.5, 3), puts every 16th value on
-// the border of two 8-bit values, and nearly every warp divides: 8191 rows of 16
-// heads of 64 10.2 us with 0.0123 or powers of two, 17.6 with 1.5.
-__device__ __forceinline__ uint2 quantise8(uint4 x, const Scale& sc) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t lo[4], hi[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = bf_lo(w[i]), b = bf_hi(w[i]);
-    lo[i] = e4m3x2(a * sc.lo, b * sc.lo);
-    hi[i] = e4m3x2(a * sc.hi, b * sc.hi);
-  }
-  uint2 r = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-  if (r.x != (hi[0] | hi[1] << 16) || r.y != (hi[2] | hi[3] << 16)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lo[i] = e4m3x2(__fdiv_rn(bf_lo(w[i]), sc.s), __fdiv_rn(bf_hi(w[i]), sc.s));
-    r = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-  }
-  return r;
-}
 
 // Each thread keeps one place in the row (16 bytes of the cache, so one head and
 // one scale) and takes ROWS rows at a time: their slots, then all their

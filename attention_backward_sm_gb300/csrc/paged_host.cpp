@@ -1,10 +1,12 @@
-// Host side of the paged-cache operators for Python: checks tensors,
-// allocates outputs and workspace and calls the C entry points.
+// Host side of the paged-cache operators and of the rotation by positions for
+// Python: checks tensors, allocates outputs and workspace and calls the C entry
+// points.
 //
 // One call here costs a few microseconds less than the same steps in Python
 // and ctypes (decode: 25 -> 6.5 us of host time on a Grace core, with kernels
 // of 5.4 us for a single short request), which is what bounds small batches.
-// The arguments are positional; paged.py has the documented signatures.
+// The arguments are positional; paged.py and rope.py have the documented
+// signatures.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -99,10 +101,11 @@ void vector(const std::optional<Tensor>& t, const char* name, at::ScalarType typ
 }
 
 // Elements from one row of a [n, heads, dim] bf16 tensor to the next.
-int64_t row_stride(const Tensor& t, const char* name, int64_t n, int64_t heads, int64_t dim) {
+int64_t row_stride(const Tensor& t, const char* name, int64_t n, int64_t heads, int64_t dim,
+                   const char* dim_is = ", the last being the cache's head_dim") {
   if (t.scalar_type() != at::kBFloat16 || t.dim() != 3 || t.size(0) != n || t.size(1) != heads || t.size(2) != dim)
     refuse(std::string(name) + " must be bfloat16 (" + std::to_string(n) + ", " + std::to_string(heads) + ", " +
-           std::to_string(dim) + "), the last being the cache's head_dim, got " + kind(t));
+           std::to_string(dim) + ")" + dim_is + ", got " + kind(t));
   if (t.numel() && (t.stride(2) != 1 || (heads > 1 && t.stride(1) != dim)))
     refuse(std::string(name) + " must have its heads packed in each row, got strides " + dims(t.strides()));
   return n > 1 ? t.stride(0) : heads * dim;
@@ -249,12 +252,13 @@ int unlocked(F f) {
   return f();
 }
 
+// An undefined tensor becomes None.
 PyObject* pack(std::initializer_list<Tensor> ts) {
   PyObject* out = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
   if (!out) return nullptr;
   Py_ssize_t i = 0;
   for (const Tensor& t : ts) {
-    PyObject* o = THPVariable_Wrap(t);
+    PyObject* o = t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
     if (!o) {
       Py_DECREF(out);
       return nullptr;
@@ -412,10 +416,208 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FAB_END
 }
 
+double real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+
+// Rows [n, heads, dim] of bf16 values that may be absent (heads 0).
+struct Rows {
+  std::optional<Tensor> t;
+  int heads = 0;
+  int64_t stride = 0;
+  Rows() = default;
+  // n, dim, heads < 0: whatever the tensor has
+  Rows(PyObject* o, const char* name, int64_t& n, int64_t& dim, int64_t want_heads = -1) : t(tensor_or_none(o, name)) {
+    if (!t) return;
+    if (t->dim() != 3) refuse(std::string(name) + " must be [num_tokens, heads, d], got " + kind(*t));
+    if (n < 0) n = t->size(0);
+    if (dim < 0) dim = t->size(2);
+    stride = row_stride(*t, name, n, want_heads < 0 ? t->size(1) : want_heads, dim, "");
+    heads = size32(t->size(1), "heads");
+  }
+  fa_bf16* p() const { return t ? ptr<fa_bf16>(*t) : nullptr; }
+};
+
+// What the three rotation calls share.
+struct Turns {
+  Tensor positions, freqs;
+  std::optional<Tensor> q_weight, k_weight;
+  int rotary, layout, weight_type = FA_WEIGHT_BF16;
+  float mscale, eps;
+  // positions, freqs, layout, mscale, q_weight, k_weight, eps
+  Turns(PyObject* const* a, int64_t tokens, int64_t dim)
+      : positions(tensor(a[0], "positions")), freqs(tensor(a[1], "freqs")), q_weight(tensor_or_none(a[4], "q_weight")),
+        k_weight(tensor_or_none(a[5], "k_weight")), layout(integer32(a[2], "layout")),
+        mscale(static_cast<float>(real(a[3]))), eps(static_cast<float>(real(a[6]))) {
+    vector(positions, "positions", at::kInt, tokens);
+    vector(freqs, "freqs", at::kLong);
+    rotary = size32(2 * freqs.numel(), "rotary_dim");
+    for (const auto* w : {&q_weight, &k_weight}) {
+      const char* const name = w == &q_weight ? "q_weight" : "k_weight";
+      if (!*w) continue;
+      const auto st = (*w)->scalar_type();
+      if (st != at::kBFloat16 && st != at::kFloat) refuse(std::string(name) + " must be bfloat16 or float32, got " + kind(**w));
+      vector(**w, name, st, dim);
+      weight_type = st == at::kFloat ? FA_WEIGHT_F32 : FA_WEIGHT_BF16;
+    }
+    if (q_weight && k_weight && q_weight->scalar_type() != k_weight->scalar_type())
+      refuse("q_weight and k_weight must have one type, got " + kind(*q_weight) + " and " + kind(*k_weight));
+  }
+  void place(Place& pl) const {
+    pl.with(positions, "positions").with(freqs, "freqs").with(q_weight, "q_weight").with(k_weight, "k_weight");
+  }
+  const uint64_t* f() const { return reinterpret_cast<const uint64_t*>(ptr<int64_t>(freqs)); }
+  static void* w(const std::optional<Tensor>& t) { return t ? t->data_ptr() : nullptr; }
+};
+
+const Tensor& first_of(const Rows& a, const Rows& b, const char* what) {
+  if (!a.t && !b.t) refuse(std::string("one at least of ") + what + " must be given");
+  return a.t ? *a.t : *b.t;
+}
+
+// q, k, [positions, freqs, layout, mscale, q_weight, k_weight, eps], out, stream
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  FAB_BEGIN
+  if (!arity(n, 11)) return nullptr;
+  int64_t tokens = -1, dim = -1;
+  const Rows q(a[0], "q", tokens, dim), k(a[1], "k", tokens, dim);
+  const Tensor& lead = first_of(q, k, "q and k");
+  const Turns r(a + 2, tokens, dim);
+  Place place(lead);
+  place.with(k.t, "k");
+  r.place(place);
+  Rows qo, ko;
+  if (a[9] != Py_None) {
+    if (!PyTuple_Check(a[9]) || PyTuple_GET_SIZE(a[9]) != 2) refuse("out must be a tuple (q_out, k_out)");
+    qo = Rows(PyTuple_GET_ITEM(a[9], 0), "q_out", tokens, dim, q.heads);
+    ko = Rows(PyTuple_GET_ITEM(a[9], 1), "k_out", tokens, dim, k.heads);
+    if (!qo.t != !q.t || !ko.t != !k.t) refuse("out must have a tensor for q and for k where they are given");
+    place.with(qo.t, "q_out").with(ko.t, "k_out").enter(a[10]);
+  } else {
+    place.enter(a[10]);
+    Cutter out(place.bytes(Cutter::size(tokens * q.heads * dim, 2) + Cutter::size(tokens * k.heads * dim, 2)));
+    if (q.t) qo.t = out.next({tokens, q.heads, dim}, at::kBFloat16);
+    if (k.t) ko.t = out.next({tokens, k.heads, dim}, at::kBFloat16);
+    qo.stride = q.heads * dim;
+    ko.stride = k.heads * dim;
+  }
+  const int t32 = size32(tokens, "num_tokens"), d32 = size32(dim, "head_dim");
+  check(unlocked([&] {
+    return fa_qk_rope(q.p(), k.p(), q.stride, k.stride, ptr<int32_t>(r.positions), r.f(), r.rotary, r.layout, r.mscale,
+                      r.w(r.q_weight), r.w(r.k_weight), r.weight_type, r.eps, t32, q.heads, k.heads, d32, qo.p(),
+                      ko.p(), qo.stride, ko.stride, place.stream());
+  }));
+  return pack({qo.t ? *qo.t : Tensor(), ko.t ? *ko.t : Tensor()});
+  FAB_END
+}
+
+// dq_out, dk_out, [as above], q, k, out (None or 4 tensors), workspace, stream
+PyObject* rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  FAB_BEGIN
+  if (!arity(n, 14)) return nullptr;
+  int64_t tokens = -1, dim = -1;
+  const Rows gq(a[0], "dq_out", tokens, dim), gk(a[1], "dk_out", tokens, dim);
+  const Tensor& lead = first_of(gq, gk, "dq_out and dk_out");
+  const Turns r(a + 2, tokens, dim);
+  const Rows q(a[9], "q", tokens, dim, gq.heads), k(a[10], "k", tokens, dim, gk.heads);
+  if ((r.q_weight && gq.t && !q.t) || (r.k_weight && gk.t && !k.t))
+    refuse("the gradient of a norm needs its input (q for q_weight, k for k_weight)");
+  auto work = tensor_or_none(a[12], "workspace");
+  if (work && !work->is_contiguous()) refuse("workspace must be contiguous");
+  Place place(lead);
+  place.with(gk.t, "dk_out").with(q.t, "q").with(k.t, "k").with(work, "workspace");
+  r.place(place);
+  Rows dq, dk;
+  Tensor dqw, dkw;
+  if (a[11] != Py_None) {
+    if (!PyTuple_Check(a[11]) || PyTuple_GET_SIZE(a[11]) != 4) refuse("out must be a tuple (dq, dk, dq_weight, dk_weight)");
+    dq = Rows(PyTuple_GET_ITEM(a[11], 0), "dq", tokens, dim, gq.heads);
+    dk = Rows(PyTuple_GET_ITEM(a[11], 1), "dk", tokens, dim, gk.heads);
+    const auto wq = tensor_or_none(PyTuple_GET_ITEM(a[11], 2), "dq_weight"),
+               wk = tensor_or_none(PyTuple_GET_ITEM(a[11], 3), "dk_weight");
+    if (!dq.t != !gq.t || !dk.t != !gk.t || !wq != !r.q_weight || !wk != !r.k_weight)
+      refuse("out must have a tensor for each of dq, dk and the weights' gradients that the call computes, else None");
+    vector(wq, "dq_weight", at::kFloat, dim);
+    vector(wk, "dk_weight", at::kFloat, dim);
+    if (wq) dqw = *wq;
+    if (wk) dkw = *wk;
+    place.with(dq.t, "dq").with(dk.t, "dk").with(wq, "dq_weight").with(wk, "dk_weight").enter(a[13]);
+  } else {
+    place.enter(a[13]);
+    Cutter out(place.bytes(Cutter::size(tokens * gq.heads * dim, 2) + Cutter::size(tokens * gk.heads * dim, 2) +
+                           2 * Cutter::size(dim, 4)));
+    if (gq.t) dq.t = out.next({tokens, gq.heads, dim}, at::kBFloat16);
+    if (gk.t) dk.t = out.next({tokens, gk.heads, dim}, at::kBFloat16);
+    if (r.q_weight) dqw = out.next({dim}, at::kFloat);
+    if (r.k_weight) dkw = out.next({dim}, at::kFloat);
+    dq.stride = gq.heads * dim;
+    dk.stride = gk.heads * dim;
+  }
+  const int t32 = size32(tokens, "num_tokens"), d32 = size32(dim, "head_dim");
+  // 0 for a head_dim that fa_qk_rope_bwd refuses, below, with its code.
+  const size_t need = r.q_weight || r.k_weight ? fa_qk_rope_bwd_workspace_size(d32) : 0;
+  c10::DataPtr own_work;
+  if (!work && need > 0) own_work = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+  void* const work_ptr = work ? ptr<void>(*work) : own_work.get();
+  const size_t work_bytes = work ? work->nbytes() : need;
+  check(unlocked([&] {
+    return fa_qk_rope_bwd(gq.p(), gk.p(), gq.stride, gk.stride, q.p(), k.p(), q.stride, k.stride,
+                          ptr<int32_t>(r.positions), r.f(), r.rotary, r.layout, r.mscale, r.w(r.q_weight),
+                          r.w(r.k_weight), r.weight_type, r.eps, t32, gq.heads, gk.heads, d32, dq.p(), dk.p(),
+                          dq.stride, dk.stride, dqw.defined() ? ptr<float>(dqw) : nullptr,
+                          dkw.defined() ? ptr<float>(dkw) : nullptr, work_ptr, work_bytes, place.stream());
+  }));
+  return pack({dq.t ? *dq.t : Tensor(), dk.t ? *dk.t : Tensor(), dqw, dkw});
+  FAB_END
+}
+
+// q, k, v, [as above], k_cache, v_cache, slots, k_scale, v_scale, out (None or
+// q_out), stream
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  FAB_BEGIN
+  if (!arity(n, 17)) return nullptr;
+  const Cache c(a[10], a[11], a[13], a[14]);
+  const Tensor& slots = tensor(a[12], "slots");
+  vector(slots, "slots", at::kLong);
+  int64_t tokens = slots.numel(), dim = c.dim;
+  const Rows q(a[0], "q", tokens, dim), k(a[1], "k", tokens, dim, c.heads_kv), v(a[2], "v", tokens, dim, c.heads_kv);
+  if (!q.t || !k.t || !v.t) refuse("q, k and v must be tensors");
+  const Turns r(a + 3, tokens, dim);
+  Place place(c.k);
+  place.with(c.v, "v_cache").with(*q.t, "q").with(*k.t, "k").with(*v.t, "v").with(slots, "slots");
+  place.with(c.k_scale, "k_scale").with(c.v_scale, "v_scale");
+  r.place(place);
+  Rows qo;
+  if (a[15] != Py_None) {
+    qo = Rows(a[15], "out", tokens, dim, q.heads);
+    place.with(qo.t, "out").enter(a[16]);
+  } else {
+    place.enter(a[16]);
+    Cutter out(place.bytes(Cutter::size(tokens * q.heads * dim, 2)));
+    qo.t = out.next({tokens, q.heads, dim}, at::kBFloat16);
+    qo.stride = q.heads * dim;
+  }
+  const int t32 = size32(tokens, "num_tokens");
+  check(unlocked([&] {
+    return fa_qk_rope_append(q.p(), k.p(), v.p(), q.stride, k.stride, v.stride, ptr<int32_t>(r.positions), r.f(),
+                             r.rotary, r.layout, r.mscale, r.w(r.q_weight), r.w(r.k_weight), r.weight_type, r.eps, t32,
+                             q.heads, qo.p(), qo.stride, ptr<int64_t>(slots), ptr<void>(c.k), ptr<void>(c.v), c.type,
+                             c.ks(), c.vs(), c.k.stride(0), c.k.stride(1), c.k.stride(2), c.pages, c.page_size,
+                             c.heads_kv, c.dim, place.stream());
+  }));
+  return THPVariable_Wrap(*qo.t);
+  FAB_END
+}
+
 PyMethodDef methods[] = {
     {"plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(plan)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode)), METH_FASTCALL, nullptr},
+    {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, nullptr},
+    {"rope_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_bwd)), METH_FASTCALL, nullptr},
+    {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_append)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_host", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

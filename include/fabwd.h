@@ -368,6 +368,82 @@ int fa_decode(const fa_bf16* q, long long q_row_stride,
               int window, float scale, fa_bf16* o, float* lse,
               void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rotation of queries and keys by their positions, with an optional norm per
+ * head: what stands between a projection and fa_fwd_* or the cache.
+ *
+ * A head x of d values at position p becomes
+ *   n = x / sqrt(mean(x^2) + eps) * weight     (n = x where the weight is NULL)
+ *   y_a = mscale (n_a cos t_i - n_b sin t_i),  y_b = mscale (n_b cos t_i + n_a sin t_i)
+ * for the pairs i of its first rotary_dim values, t_i = p * theta_i; the others
+ * are n.  Computed in fp32, rounded once.
+ *   rotary_dim  a multiple of 16 from 0 (the norm alone) to d
+ *   positions   [num_tokens] int32 on the device (fa_kv_plan's), any value
+ *   freqs       [rotary_dim / 2] on the device: theta_i / (2 pi) mod 1 as a
+ *               64-bit fixed-point fraction of a turn (rounded times 2^64), which
+ *               keeps the angle of any position exact to 2^-32 turns.  Stretched
+ *               positions are other frequencies; mscale carries a factor of the
+ *               outputs that goes with them (1 otherwise).
+ *   weights     [d] of weight_type on the device, or NULL: no norm of this tensor
+ * q [num_tokens, H, d], k [num_tokens, Hkv, d] bf16, rows row_stride elements
+ * apart (multiples of 8: slices of a fused projection need no copy), 16-byte
+ * aligned; H or Hkv may be 0 (the tensor may then be NULL).  d 64, 128 or 256.
+ * ------------------------------------------------------------------------ */
+enum fa_rope_layout {
+    FA_ROPE_HALF = 0,         /* pairs (i, i + rotary_dim / 2) */
+    FA_ROPE_INTERLEAVED = 1   /* pairs (2i, 2i + 1) */
+};
+enum fa_weight_type {
+    FA_WEIGHT_BF16 = 0,
+    FA_WEIGHT_F32 = 1
+};
+
+/* q_out and k_out, shaped like q and k with row strides of their own.  q_out
+ * may be q (same stride), k_out k; otherwise no output may overlap an input or
+ * the other output. */
+int fa_qk_rope(const fa_bf16* q, const fa_bf16* k, long long q_row_stride, long long k_row_stride,
+               const int32_t* positions, const uint64_t* freqs, int rotary_dim, int layout, float mscale,
+               const void* q_weight, const void* k_weight, int weight_type, float eps,
+               int num_tokens, int heads, int heads_kv, int head_dim,
+               fa_bf16* q_out, fa_bf16* k_out, long long q_out_row_stride, long long k_out_row_stride,
+               fa_stream_t stream);
+
+/* Bytes of device workspace fa_qk_rope_bwd needs where a weight is given.
+ * Returns 0 and sets fa_last_error() on bad arguments. */
+size_t fa_qk_rope_bwd_workspace_size(int head_dim);
+
+/* Gradient of fa_qk_rope.  dq_out, dk_out: gradients of its outputs.  q, k: its
+ * inputs, read only where the tensor has a weight (may be NULL otherwise).
+ * Outputs: dq, dk (dq may be dq_out with the same stride, dk dk_out), and where
+ * a weight is given its gradient dq_weight, dk_weight [d] float32 (whatever the
+ * weight's type), overwritten.  The norm's factor is worked out again from q
+ * and k.  Sums over rows go in a fixed order: same bits on every call.
+ * workspace: needed with a weight, 16-byte aligned, contents arbitrary; calls
+ * whose work overlaps on the GPU need one each. */
+int fa_qk_rope_bwd(const fa_bf16* dq_out, const fa_bf16* dk_out, long long dq_out_row_stride,
+                   long long dk_out_row_stride, const fa_bf16* q, const fa_bf16* k, long long q_row_stride,
+                   long long k_row_stride, const int32_t* positions, const uint64_t* freqs, int rotary_dim,
+                   int layout, float mscale, const void* q_weight, const void* k_weight, int weight_type, float eps,
+                   int num_tokens, int heads, int heads_kv, int head_dim, fa_bf16* dq, fa_bf16* dk,
+                   long long dq_row_stride, long long dk_row_stride, float* dq_weight, float* dk_weight,
+                   void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* fa_qk_rope and fa_kv_append in one pass: q is rotated (and normed) into
+ * q_out, k likewise into the cache, v goes into the cache as it is.  Cache,
+ * slots (rows whose slot is outside the cache are skipped in the cache, their
+ * q_out row is written) and scales as in fa_kv_append.  To an e4m3 cache a
+ * rotated key is rounded once, as e4m3(y / k_scale[head]); values are stored as
+ * fa_kv_append stores them.  q, k, v must not overlap the cache or q_out
+ * (which may be q with the same stride). */
+int fa_qk_rope_append(const fa_bf16* q, const fa_bf16* k, const fa_bf16* v, long long q_row_stride,
+                      long long k_row_stride, long long v_row_stride, const int32_t* positions,
+                      const uint64_t* freqs, int rotary_dim, int layout, float mscale, const void* q_weight,
+                      const void* k_weight, int weight_type, float eps, int num_tokens, int heads,
+                      fa_bf16* q_out, long long q_out_row_stride, const int64_t* slots,
+                      void* k_cache, void* v_cache, int kv_type, const float* k_scale, const float* v_scale,
+                      long long page_stride, long long slot_stride, long long head_stride,
+                      int num_pages, int page_size, int heads_kv, int head_dim, fa_stream_t stream);
+
 /* Diagnostic (the pages have no counterpart): launches one block that
  * waits, through the same bounded mbarrier wait the kernels use, on a
  * barrier nothing arrives on.  After its own short limit (1 s; the
