@@ -320,8 +320,9 @@ def backward_lse(q, k, v, o, do, lse, cu_q_dev, cu_kv_dev, cu_q_host, cu_kv_host
     return dq, dk, dv
 
 
-from .paged import (FA_KV_BF16, FA_KV_E4M3, KvPlan, decode, fa_decode, fa_decode_workspace_size,  # noqa: E402,F401
-                    fa_kv_append, fa_kv_plan, kv_append, kv_plan)
+from .paged import (FA_KV_BF16, FA_KV_E4M3, KvPlan, decode, extend, fa_decode,  # noqa: E402,F401
+                    fa_decode_workspace_size, fa_extend, fa_extend_workspace_size, fa_kv_append, fa_kv_plan, kv_append,
+                    kv_plan)
 from .rope import (FA_ROPE_HALF, FA_ROPE_INTERLEAVED, FA_WEIGHT_BF16, FA_WEIGHT_F32, fa_qk_rope,  # noqa: E402,F401
                    fa_qk_rope_append, fa_qk_rope_bwd, fa_qk_rope_bwd_workspace_size, qk_rope, qk_rope_append,
                    qk_rope_backward, rope_freqs)

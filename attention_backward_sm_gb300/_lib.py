@@ -40,6 +40,9 @@ SIGNATURES = {
     "fa_decode_workspace_size": (_sz, [_i, _i, _i, _i]),
     "fa_decode": (_i, [_p, _ll, _p, _p, _i, _p, _p, _ll, _ll, _ll, _i, _i, _p, _ll, _i, _p, _i, _i, _i, _i, _i, _f,
                        _p, _p, _p, _sz, _p]),
+    "fa_extend_workspace_size": (_sz, [_i]),
+    "fa_extend": (_i, [_p, _ll, _p, _p, _i, _p, _p, _ll, _ll, _ll, _i, _i, _p, _ll, _i, _p, _p, _i, _i, _i, _i, _i, _i,
+                       _f, _p, _p, _p, _sz, _p]),
     "fa_qk_rope": (_i, [_p, _p, _ll, _ll, _p, _p, _i, _i, _f, _p, _p, _i, _f, _i, _i, _i, _i, _p, _p, _ll, _ll, _p]),
     "fa_qk_rope_bwd_workspace_size": (_sz, [_i]),
     "fa_qk_rope_bwd": (_i, [_p, _p, _ll, _ll, _p, _p, _ll, _ll, _p, _p, _i, _i, _f, _p, _p, _i, _f, _i, _i, _i, _i,

@@ -1,0 +1,1058 @@
+// Attention of several new tokens per request over a paged key/value cache.
+//
+// Request b has n new tokens (rows cu[b] to cu[b + 1] of q) whose keys and
+// values are in the cache already, s keys in all.  New token i is at position
+// p = s - n + i and sees the keys j in [max(0, p - window + 1), p]:
+//     x_j = scale * q . k_j,  o = sum_j exp(x_j) v_j / sum_j exp(x_j),
+//     lse = ln sum_j exp(x_j)
+// Keys whose block-table entry is not a page of the cache are not seen; a row
+// that sees no key gets o = 0, lse = -inf.
+//
+// Products.  The rows of a unit are the query heads of one key/value head for
+// some consecutive tokens (row r is token r / G, head r % G, G = heads /
+// heads_kv), 256 of them as two tiles of 128 (one tile at head_dim 256).  So a
+// key is read once for all heads that share it, and a call of a few tokens per
+// request (2 G rows) has the tensor work of one that has none to share.  Per
+// block of 128 keys (64 at head_dim 256): S = Q K^T into tensor memory, softmax
+// with a thread per row, P as 16-bit values over S, O += P V with P from tensor
+// memory; tcgen05 throughout.  Chunks of hundreds of tokens are bound by these
+// products and the exponentials, short ones by HBM.
+//
+// Work.  The units of all requests (requests in order, key/value heads, tiles
+// of rows) and their blocks of keys are laid out on a line by what they cost
+// (keys seen, and as much as a block for a unit's start and end), and the line
+// is cut into runs of equal length, one per SM: ragged lengths, one long
+// document and a causal mask's short first rows all load every SM alike, and
+// the host needs no lengths.  A unit that lies in several runs leaves partial
+// results (at most two per run), which a second kernel joins in a fixed order.
+// The costs are closed forms of a request's numbers, so that every block finds
+// its run with one scan over the requests.
+//
+// Warps: per tile of 128 rows four for the softmax and the output, then four
+// that load (cp.async, so any page size, strides and missing pages; 8-bit
+// caches are converted to fp16 on the way), one that issues the products, one
+// that walks along the run and tells the others what is next.
+//   Two tiles: the products of one run while the softmax works on the other,
+//   in the order P_A V, S_A (of the next block), P_B V, S_B.
+//   One tile (at most 128 rows): two score buffers, S of the next block is
+//   issued before P V of this one.
+// The tensor core takes a block's products in the order they are issued, which
+// is what lets S overwrite the P before it without waiting.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "../../include/fabwd.h"
+#include "checks.h"
+#include "extend.h"
+#include "internal.h"
+#include "paged.h"
+#include "quantise.cuh"
+#include "sm103.cuh"
+
+namespace fa {
+
+__device__ int g_extend_status = 0;
+
+namespace extend {
+namespace {
+
+constexpr uint32_t TMEM_COLS = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// A row's reference for the exponents moves only when a score exceeds it by
+// more than this (units of log 2), so O is rescaled rarely.
+constexpr float kSlack = 8.f;
+// fp16 weights (8-bit caches) are stored times 2^7: at most 2^15, and the
+// smallest step 2^-24 counts 2^-31 beside the row's largest weight.
+constexpr float kF16Shift = 7.f;
+constexpr int kPieces = 4;     // pieces of the run that the walker is ahead
+constexpr int kMarks = 8;      // blocks whose missing pages are kept
+constexpr int kLag = 2;        // loads in flight behind the newest
+
+struct Piece {
+  int n;            // blocks of keys; 0: the run is over
+  int kb0;          // the first one
+  int b;            // request
+  int head_kv;
+  int key_lo;       // keys that any row of the unit sees: [key_lo, key_hi)
+  int key_hi;
+  int token0;       // row of q of the request's first token
+  int row_first;    // first row of the unit in the request
+  int rows;         // of the unit
+  int pos0;         // position of the request's first token
+  int part;         // 0: the whole unit; 1, 2: partial, to slot part - 1
+  int pad;
+};
+
+// S_FULL and P_READY: of tile 0 (and the first score buffer of a single tile), of
+// tile 1, and of a single tile's second buffer.  Waits are by parity, so whoever
+// waits on a barrier has to see each of its phases: tile 1's warps take no part in
+// units of one tile.
+enum { B_Q_FULL = 0, B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 3, B_O_DONE = B_P_READY + 3, B_O_FREE = B_O_DONE + 2,
+       B_PIECE_FULL = B_O_FREE + 2, B_PIECE_EMPTY = B_PIECE_FULL + kPieces, B_TEARDOWN = B_PIECE_EMPTY + kPieces,
+       B_FULL, NUM_FIXED = B_FULL };
+
+template <int D, bool E4M3>
+struct Layout {
+  using S = Shape<D>;
+  static constexpr int BK = S::kKeys;
+  static constexpr uint32_t TILE_Q = 128 * D * 2;
+  static constexpr uint32_t CHUNK_Q = 128 * 128;
+  static constexpr uint32_t TILE_KV = BK * D * 2;
+  static constexpr uint32_t CHUNK_KV = BK * 128;
+  static constexpr int NS = D == 64 ? 8 : 5;            // ring of key and value tiles
+  static constexpr uint32_t Q = 0;
+  static constexpr uint32_t KV = S::kTiles * TILE_Q;
+  static constexpr uint32_t BARS = KV + NS * TILE_KV;
+  static constexpr int NUM_BARS = B_FULL + 2 * NS;
+  static constexpr uint32_t MARKS = (BARS + NUM_BARS * 8 + 15) / 16 * 16;    // [kMarks][4] words
+  static constexpr uint32_t PIECES = MARKS + kMarks * 16;
+  static constexpr uint32_t QSCALE = PIECES + kPieces * sizeof(Piece);       // [2 pieces][rows] (8-bit caches)
+  static constexpr uint32_t SCAN = QSCALE + (E4M3 ? 2 * S::kRows * 4 : 0);       // [warps] 64-bit sums, then Found
+  static constexpr uint32_t MISC = SCAN + 16 * 8 + 64;
+  static constexpr uint32_t BYTES = MISC + 16;
+  static constexpr uint32_t COL_O = 2 * BK;              // after two score buffers
+  static constexpr int WARPS = 4 * S::kTiles + 8;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int LOAD_WARP = 4 * S::kTiles;
+  static constexpr int MMA_WARP = LOAD_WARP + 4;
+  static constexpr int WALK_WARP = MMA_WARP + 1;
+  // registers: 65536 / THREADS at launch
+  static constexpr uint32_t REG_LAUNCH = 65536 / THREADS / 8 * 8;
+  static constexpr uint32_t REG_SOFTMAX = S::kTiles == 2 ? 184 : 208;
+  static constexpr uint32_t REG_OTHER = S::kTiles == 2 ? 72 : 144;
+  static_assert(S::kTiles * 128 * REG_SOFTMAX + 256 * REG_OTHER <= REG_LAUNCH * THREADS, "register budget");
+  static_assert(COL_O + S::kTiles * D <= TMEM_COLS, "tensor memory budget");
+  static_assert(BYTES <= 232448, "shared memory budget");
+  static_assert(NS > kLag + 1, "loads in flight");
+  static_assert(2 * kMarks - NS >= 2, "marks outlive their block");
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t tile) { return sw128_desc(tile, 16, 1024); }
+__device__ __forceinline__ constexpr uint64_t step_kmajor(int t, uint32_t chunk) {
+  return ((t >> 2) * chunk + (t & 3) * 32) >> 4;
+}
+__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t tile, uint32_t chunk) { return sw128_desc(tile, chunk, 1024); }
+__device__ __forceinline__ constexpr uint64_t step_mnmajor(int t) { return (t * 2048) >> 4; }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;   // fewer source bytes than 16: the rest is zero-filled
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four 8-bit values to four halves (exact).
+__device__ __forceinline__ uint2 e4m3x4_f16(uint32_t x) {
+  uint2 r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(x));
+  return r;
+}
+// (a.x, a.y) * m + c, both halves
+__device__ __forceinline__ float2 fma2(float2 a, float2 m, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, m, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 m, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, m, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(m.x), "f"(m.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// ------------------------------------------------------------------ partition
+// A request's numbers, and the cost of its units: tile x costs the keys that
+// its last row sees (as if none were missing) and kUnitCost more.
+template <int D>
+struct Request {
+  using S = Shape<D>;
+  static constexpr int kUnitCost = S::kKeys;
+  int token0, len, pos0;
+  long long rows;       // tokens * group
+  int tiles;
+  long long base, cap;  // cost of a tile without its tokens' own keys; with a window: of a tile at most
+  int ramp;             // tiles that cost less than cap
+  long long last;       // what the last tile costs
+  long long cost;       // of all tiles, for one key/value head
+  __device__ __forceinline__ Request(const ExtendParams& p, int b, int group) {
+    const int most = p.max_pages * p.kv.page_size;
+    const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1];
+    token0 = min(max(c0, 0), p.num_tokens);
+    const int end = min(max(c1, token0), p.num_tokens);
+    len = min(max(p.seq_lens[b], 0), most);
+    const long long n = max(static_cast<long long>(c1) - c0, 0ll);
+    pos0 = static_cast<int>(max(len - n, -static_cast<long long>(p.num_tokens) - 1));
+    rows = static_cast<long long>(end - token0) * group;
+    tiles = static_cast<int>((rows + S::kRows - 1) / S::kRows);
+    base = max(pos0, 0) + kUnitCost;
+    cap = p.window > 0 ? static_cast<long long>(p.window) + S::kRows / group + 1 + kUnitCost : 0;
+    ramp = tiles;
+    if (p.window > 0) {
+      const long long r = cap > base ? (cap - base) * group / S::kRows : 0;
+      ramp = static_cast<int>(min(r, static_cast<long long>(tiles)));
+    }
+    last = base + end - token0;
+    if (p.window > 0) last = min(last, cap);
+    cost = tiles > 0 ? before(tiles, group) : 0;
+  }
+  // Of the tiles before tile x.
+  __device__ __forceinline__ long long before(int x, int group) const {
+    if (x == tiles) return before_full(tiles - 1, group) + last;
+    return before_full(x, group);
+  }
+  __device__ __forceinline__ long long before_full(int x, int group) const {
+    const long long y = min(x, ramp);
+    return y * base + S::kRows * y * (y + 1) / (2 * group) + (x - y) * cap;
+  }
+};
+
+struct Runs {
+  long long base, rem;
+  int runs;
+  __device__ __forceinline__ Runs(long long total, int blocks, long long least) {
+    const long long most = total / least;
+    runs = most < 1 ? 1 : most < blocks ? static_cast<int>(most) : blocks;
+    base = total / runs;
+    rem = total - base * runs;
+  }
+  __device__ __forceinline__ long long start(int r) const { return r * base + min(static_cast<long long>(r), rem); }
+  // The run that holds place x.
+  __device__ __forceinline__ int of(long long x) const {
+    const long long y = x - rem * (base + 1);
+    return static_cast<int>(y < 0 ? x / (base + 1) : rem + y / base);
+  }
+};
+
+// What a block knows of its run after the scan.
+struct Found {
+  long long at;      // the request's place on the line
+  long long total;
+  int b;
+};
+
+// Workspace: [runs] cuts, then the partial results.
+__device__ __forceinline__ float* parts_of(void* work, int runs) {
+  return reinterpret_cast<float*>(static_cast<Cut*>(work) + runs);
+}
+
+// ------------------------------------------------------------------ main kernel
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(const ExtendParams p) {
+  using L = Layout<D, E4M3>;
+  using S = Shape<D>;
+  constexpr int BK = L::BK, NS = L::NS, TILES = S::kTiles, ROWS = S::kRows;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = p.heads / p.kv.heads_kv;
+  int* const status = &g_extend_status;
+  volatile int* const abort = reinterpret_cast<volatile int*>(smem + L::MISC);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC + 4);
+  Piece* const pieces = reinterpret_cast<Piece*>(smem + L::PIECES);
+  uint32_t* const marks = reinterpret_cast<uint32_t*>(smem + L::MARKS);
+  float* const q_scale = reinterpret_cast<float*>(smem + L::QSCALE);
+  long long* const scan = reinterpret_cast<long long*>(smem + L::SCAN);
+  Found* const found = reinterpret_cast<Found*>(scan + 16);
+  const uint32_t bars = sbase + L::BARS;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  auto full = [&](int s) { return bars + 8u * (B_FULL + s); };
+  auto empty = [&](int s) { return bars + 8u * (B_FULL + NS + s); };
+
+  if (sbase & 1023) {
+    if (threadIdx.x == 0) atomicCAS(status, 0, 99);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    mbar_init(bar(B_Q_FULL), 128);
+    mbar_init(bar(B_Q_EMPTY), 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(bar(B_S_FULL + i), 1);
+      mbar_init(bar(B_P_READY + i), 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_O_DONE + i), 1);
+      mbar_init(bar(B_O_FREE + i), 128);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(bar(B_PIECE_FULL + i), 1);
+      mbar_init(bar(B_PIECE_EMPTY + i), 4 * TILES + 5);   // a lane of every other warp
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full(i), 128);
+      mbar_init(empty(i), 1);
+    }
+    mbar_init(bar(B_TEARDOWN), 1);
+    mbar_init_fence();
+  }
+  if (warp == L::MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch();
+
+  // The line's length, and the request that this block's run starts in.
+  const int per = (p.batch + L::THREADS - 1) / L::THREADS;
+  const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
+  long long mine = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) mine += Request<D>(p, b, group).cost * p.kv.heads_kv;
+  long long upto = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += x;
+  }
+  if (lane == 31) scan[warp] = upto;
+  // Rows that belong to no request.
+  {
+    const int first = min(max(p.cu_new[p.batch], 0), p.num_tokens);
+    const long long pieces16 = static_cast<long long>(p.num_tokens - first) * p.heads * (D / 8);
+    for (long long i = static_cast<long long>(blockIdx.x) * L::THREADS + threadIdx.x; i < pieces16;
+         i += static_cast<long long>(gridDim.x) * L::THREADS) {
+      const long long row = static_cast<long long>(first) * p.heads + i / (D / 8);
+      *reinterpret_cast<uint4*>(p.o + row * D + i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+      if (p.lse && i % (D / 8) == 0) p.lse[row] = -INFINITY;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  long long total = 0;
+#pragma unroll 1
+  for (int w = 0; w < L::WARPS; ++w) {
+    if (w < warp) upto += scan[w];
+    total += scan[w];
+  }
+  const Runs runs(total, gridDim.x, 2 * BK);
+  const long long run_start = total > 0 && static_cast<int>(blockIdx.x) < runs.runs ? runs.start(blockIdx.x) : total;
+  const long long run_end = run_start < total ? runs.start(blockIdx.x + 1) : total;
+  if (run_start < total && run_start >= upto - mine && run_start < upto) {
+    long long at = upto - mine;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const long long cost = Request<D>(p, b, group).cost * p.kv.heads_kv;
+      if (run_start < at + cost) {
+        found->at = at;
+        found->b = b;
+        break;
+      }
+      at += cost;
+    }
+  }
+  __syncthreads();
+
+  if (warp == L::WALK_WARP) {
+    // ------------------------------------------------------------ walker
+    setmaxnreg_to<L::REG_OTHER, L::REG_LAUNCH>();
+    Cut cut = {};
+    int count = 0;   // pieces
+    bool ok = true;
+    auto emit = [&](const Piece& piece) {
+      const int slot = count % kPieces;
+      if (count >= kPieces && !mbar_wait(bar(B_PIECE_EMPTY + slot), (count / kPieces - 1) & 1, abort, status)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      if (lane == 0) {
+        pieces[slot] = piece;
+        mbar_arrive(bar(B_PIECE_FULL + slot));
+      }
+      __syncwarp();
+      ++count;
+    };
+    if (run_start < total) {
+      int b = found->b;
+      long long at = found->at;
+      while (ok && b < p.batch && at < run_end) {
+        const Request<D> r(p, b, group);
+        if (r.cost == 0) {
+          ++b;
+          continue;
+        }
+        int hk = 0, x = 0;
+        if (run_start > at) {
+          const long long in = run_start - at;
+          hk = static_cast<int>(in / r.cost);
+          const long long rem = in - hk * r.cost;
+          int hi = r.tiles;   // before(x) <= rem < before(hi)
+          while (hi - x > 1) {
+            const int mid = (x + hi) >> 1;
+            if (r.before(mid, group) <= rem) x = mid;
+            else hi = mid;
+          }
+        }
+        bool in_run = true;
+        for (; ok && in_run && hk < p.kv.heads_kv; ++hk, x = 0) {
+          for (; ok && x < r.tiles; ++x) {
+            const long long c = at + hk * r.cost + r.before(x, group);
+            if (c >= run_end) {
+              in_run = false;
+              break;
+            }
+            const long long w = r.before(x + 1, group) - r.before(x, group);
+            Piece u;
+            u.b = b;
+            u.head_kv = hk;
+            u.token0 = r.token0;
+            u.row_first = x * ROWS;
+            u.rows = static_cast<int>(min(static_cast<long long>(ROWS), r.rows - u.row_first));
+            u.pos0 = r.pos0;
+            const int first = r.pos0 + p.group_div.quotient(u.row_first);
+            const int last = r.pos0 + p.group_div.quotient(u.row_first + u.rows - 1);
+            u.key_hi = max(last + 1, 0);
+            u.key_lo = p.window > 0 ? min(max(first - p.window + 1, 0), u.key_hi) : 0;
+            const int kb = u.key_lo / BK;
+            const int nblk = max(1, (u.key_hi + BK - 1) / BK - kb);   // a unit that sees nothing has one (masked) block
+            // the blocks that start in the run: c + j w / nblk in [run_start, run_end)
+            const long long lo = run_start > c ? ((run_start - c) * nblk + w - 1) / w : 0;
+            const long long hi = ((run_end - c) * nblk + w - 1) / w;
+            const int j0 = static_cast<int>(min(lo, static_cast<long long>(nblk)));
+            const int j1 = static_cast<int>(min(hi, static_cast<long long>(nblk)));
+            if (j1 <= j0) {
+              // a run inside a unit's one long block: no partial result of this unit
+              if (j0 > 0 && j0 < nblk) {
+                float* const l = parts_of(p.work, gridDim.x) +
+                                 static_cast<size_t>(blockIdx.x) * 2 * part_floats(ROWS, D) + static_cast<size_t>(ROWS) * (D + 1);
+                for (int i = lane; i < ROWS; i += 32) l[i] = 0.f;
+              }
+              continue;
+            }
+            u.kb0 = kb + j0;
+            u.n = j1 - j0;
+            u.part = j0 > 0 ? 1 : j1 < nblk ? 2 : 0;
+            if (u.part == 2) {
+              // the run in which the unit's last block starts
+              cut.row_end = static_cast<int>(r.rows);
+              cut.row_first = u.row_first;
+              cut.token0 = r.token0;
+              cut.head_kv = hk;
+              cut.last = runs.of(c + (nblk - 1) * w / nblk);
+            }
+            emit(u);
+          }
+        }
+        at += r.cost * p.kv.heads_kv;
+        ++b;
+      }
+    }
+    Piece over = {};
+    if (ok) emit(over);
+    if (lane == 0) reinterpret_cast<Cut*>(p.work)[blockIdx.x] = cut;
+  } else if (warp == L::MMA_WARP) {
+    // ------------------------------------------------------------ products
+    setmaxnreg_to<L::REG_OTHER, L::REG_LAUNCH>();
+    constexpr uint32_t ID_S = E4M3 ? idesc_f16(128, BK, 0) : idesc_bf16(128, BK, 0, 0);
+    constexpr uint32_t ID_O = E4M3 ? idesc_f16(128, D, 1) : idesc_bf16(128, D, 0, 1);
+    int slot = 0, phase = 0;                    // of the ring of tiles
+    int used[2] = {0, 0}, used_odd = 0;         // P_READY phases
+    int freed[2] = {0, 0};                      // pieces of a tile
+    auto next_slot = [&] {
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    auto issue_s = [&](int t, int buf, int at) {
+      const uint64_t a0 = desc_kmajor(sbase + L::Q + t * L::TILE_Q), b0 = desc_kmajor(sbase + L::KV + at * L::TILE_KV);
+#pragma unroll 4
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(tmem + buf * BK, a0 + step_kmajor(k, L::CHUNK_Q), b0 + step_kmajor(k, L::CHUNK_KV), ID_S, k > 0);
+    };
+    auto issue_pv = [&](int t, int buf, int at, bool more) {
+      const uint64_t b0 = desc_mnmajor(sbase + L::KV + at * L::TILE_KV, L::CHUNK_KV);
+#pragma unroll 4
+      for (int k = 0; k < BK / 16; ++k)
+        mma_ts(tmem + L::COL_O + t * D, tmem + buf * BK + k * 8, b0 + step_mnmajor(k), ID_O, more | (k > 0));
+    };
+    bool ok = true;
+    auto wait = [&](uint32_t b, int parity) {
+      if (ok && !mbar_wait(b, parity & 1, abort, status)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    for (int count = 0; ok; ++count) {
+      const int ps = count % kPieces;
+      if (!wait(bar(B_PIECE_FULL + ps), count / kPieces)) break;
+      const int n = pieces[ps].n;
+      const bool two = TILES == 2 && pieces[ps].rows > 128;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_PIECE_EMPTY + ps));
+      if (n == 0) break;
+      if (!wait(bar(B_Q_FULL), count) || !wait(full(slot), phase)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_s(0, 0, slot);
+        mma_commit(bar(B_S_FULL));
+        if (two) {
+          issue_s(1, 1, slot);
+          mma_commit(bar(B_S_FULL + 1));
+        }
+        mma_commit(empty(slot));
+        if (n == 1) mma_commit(bar(B_Q_EMPTY));
+      }
+      __syncwarp();
+      next_slot();
+      if (two) {
+        for (int j = 0; ok && j < n; ++j) {
+          if (!wait(full(slot), phase)) break;
+          const int v_slot = slot;
+          next_slot();
+          for (int t = 0; t < 2; ++t) {
+            if (!wait(bar(B_P_READY + t), used[t])) break;
+            if (j == 0 && freed[t] > 0 && !wait(bar(B_O_FREE + t), freed[t] - 1)) break;
+            if (t == 0 && j + 1 < n && !wait(full(slot), phase)) break;
+            ++used[t];
+            tc_fence_after();
+            if (elect_one()) {
+              issue_pv(t, t, v_slot, j > 0);
+              if (t == 1) mma_commit(empty(v_slot));
+              mma_commit(bar(B_O_DONE + t));
+              if (j + 1 < n) {
+                issue_s(t, t, slot);
+                mma_commit(bar(B_S_FULL + t));
+                if (t == 1) {
+                  mma_commit(empty(slot));
+                  if (j + 2 == n) mma_commit(bar(B_Q_EMPTY));
+                }
+              }
+            }
+            __syncwarp();
+          }
+          if (j + 1 < n) next_slot();
+        }
+        ++freed[0];
+        ++freed[1];
+      } else {
+        for (int j = 0; ok && j < n; ++j) {
+          if (j + 1 < n) {
+            if (!wait(full(slot), phase)) break;
+            tc_fence_after();
+            if (elect_one()) {
+              issue_s(0, (j + 1) & 1, slot);
+              mma_commit(bar(B_S_FULL + (j & 1 ? 0 : 2)));
+              mma_commit(empty(slot));
+              if (j + 2 == n) mma_commit(bar(B_Q_EMPTY));
+            }
+            __syncwarp();
+            next_slot();
+          }
+          const int buf = j & 1;
+          if (!wait(full(slot), phase) || !wait(bar(B_P_READY + 2 * buf), buf ? used_odd : used[0])) break;
+          if (j == 0 && freed[0] > 0 && !wait(bar(B_O_FREE), freed[0] - 1)) break;
+          if (buf) ++used_odd;
+          else ++used[0];
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(0, buf, slot, j > 0);
+            mma_commit(empty(slot));
+            mma_commit(bar(B_O_DONE));
+          }
+          __syncwarp();
+          next_slot();
+        }
+        ++freed[0];
+      }
+    }
+    // every product issued has to end before the block does, after an abort, too
+    if (elect_one()) mma_commit(bar(B_TEARDOWN));
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait(bar(B_TEARDOWN), 0, &no_abort, status);
+  } else if (warp >= L::LOAD_WARP && warp < L::MMA_WARP) {
+    // ------------------------------------------------------------ loads
+    setmaxnreg_to<L::REG_OTHER, L::REG_LAUNCH>();
+    constexpr int RPW = BK / 4;              // keys of a block per warp
+    constexpr int CPR = D / 8;               // 16-byte pieces per row of a tile
+    constexpr int RPI = 32 / CPR;            // rows a warp's instruction covers
+    const int w = warp - L::LOAD_WARP;
+    int slot = 0, phase = 1;                 // of the ring: the first pass finds every slot empty
+    uint32_t pending[kLag] = {};             // barriers of the loads in flight, oldest last
+    int block = 0;                           // blocks of keys so far
+    bool ok = true;
+    auto wait = [&](uint32_t b, int parity) {
+      if (ok && !mbar_wait(b, parity & 1, abort, status)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    // a load of this thread has been issued; the one kLag before it has landed
+    auto issued = [&](uint32_t b) {
+      cp_commit();
+      cp_wait<kLag>();
+      if (pending[kLag - 1]) {
+        fence_proxy_async_smem();
+        mbar_arrive(pending[kLag - 1]);
+      }
+#pragma unroll
+      for (int i = kLag - 1; i > 0; --i) pending[i] = pending[i - 1];
+      pending[0] = b;
+    };
+    auto drain = [&] {
+      cp_wait<0>();
+      fence_proxy_async_smem();
+#pragma unroll
+      for (int i = kLag - 1; i >= 0; --i) {
+        if (pending[i]) mbar_arrive(pending[i]);
+        pending[i] = 0;
+      }
+    };
+    for (int count = 0; ok; ++count) {
+      const int ps = count % kPieces;
+      if (!wait(bar(B_PIECE_FULL + ps), count / kPieces)) break;
+      const Piece u = pieces[ps];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_PIECE_EMPTY + ps));
+      if (u.n == 0) break;
+      const int32_t* const table = p.table + u.b * p.table_stride;
+      const int last_page = u.key_hi > 0 ? p.page_div.quotient(u.key_hi - 1) : -1;
+      auto page_of = [&](int kb) {   // of this lane's key
+        const int key = kb * BK + w * RPW + lane;
+        const int pi = p.page_div.quotient(key);
+        return pi <= last_page && lane < RPW ? table[pi] : -1;
+      };
+      int page = page_of(u.kb0);
+      // Q: rows of two tiles, 32 per warp and step
+      if (count > 0 && !wait(bar(B_Q_EMPTY), count - 1)) break;
+      const int q_rows = TILES == 2 && u.rows > 128 ? ROWS : 128;
+#pragma unroll 1
+      for (int r0 = w * 32; r0 < q_rows; r0 += 128) {
+        const int r = r0 + lane, row = u.row_first + r, tok = p.group_div.quotient(row);
+        const long long from = (u.token0 + tok) * p.q_row_stride + (u.head_kv * group + row - tok * group) * D;
+        const unsigned valid = __ballot_sync(0xffffffffu, r < u.rows);
+#pragma unroll 4
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int lr = i * RPI + lane / CPR, c = lane % CPR, rr = r0 + lr;
+          const long long off = __shfl_sync(0xffffffffu, from, lr);
+          const bool have = valid >> lr & 1;
+          const uint32_t dst = sbase + L::Q + (rr >> 7) * L::TILE_Q + (c >> 3) * L::CHUNK_Q + (rr & 127) * 128 +
+                               (((c & 7) ^ (rr & 7)) << 4);
+          if constexpr (!E4M3) {
+            cp_async16(dst, p.q + (have ? off + c * 8 : 0), have);
+          } else {
+            // as fp16, the row times a power of two that puts its largest value just below 2^15
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (have) v = ldg_stream(p.q + off + c * 8);
+            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(words[e] << 16 & 0x7FFF0000u, words[e] & 0x7FFF0000u));
+#pragma unroll
+            for (int o = CPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // exponent field of the factor: 127 + 14 - (top's - 127), kept a normal number
+            const int ex = min(max(268 - static_cast<int>(top >> 23), 1), 254);
+            const float f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+            uint32_t out[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[e] = pack_f16x2(bf_lo(words[e]) * f, bf_hi(words[e]) * f);
+            st_shared_v4(dst, out[0], out[1], out[2], out[3]);
+            if (c == 0) q_scale[(count & 1) * ROWS + rr] = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+          }
+        }
+      }
+      if constexpr (E4M3) {
+        fence_proxy_async_smem();
+        mbar_arrive(bar(B_Q_FULL));
+      } else {
+        issued(bar(B_Q_FULL));
+      }
+      // blocks of keys
+      long long off[2] = {0, 0};     // of this lane's key; of the block before
+      unsigned good[2] = {0, 0};     // keys that are there
+      auto locate = [&](int kb) {
+        off[1] = off[0];
+        good[1] = good[0];
+        const int key = kb * BK + w * RPW + lane;
+        const bool in = lane < RPW && key >= u.key_lo && key < u.key_hi;
+        const bool there = in && page >= 0 && page < p.kv.num_pages;
+        off[0] = there ? page * p.kv.page_stride + (key - p.page_div.quotient(key) * p.kv.page_size) * p.kv.slot_stride +
+                             u.head_kv * p.kv.head_stride
+                       : 0;
+        good[0] = __ballot_sync(0xffffffffu, there);
+        const unsigned missing = __ballot_sync(0xffffffffu, in && !there);
+        if (lane == 0) marks[(block % kMarks) * 4 + w] = missing;
+        ++block;
+        page = page_of(kb + 1);
+      };
+      auto load = [&](const void* cache, int which) {
+        if (!wait(empty(slot), phase)) return;
+        const uint32_t tile = sbase + L::KV + slot * L::TILE_KV;
+        if constexpr (!E4M3) {
+          const uint16_t* const from = static_cast<const uint16_t*>(cache);
+#pragma unroll 4
+          for (int i = 0; i < RPW / RPI; ++i) {
+            const int lr = i * RPI + lane / CPR, c = lane % CPR, rr = w * RPW + lr;
+            const long long o = __shfl_sync(0xffffffffu, off[which], lr);
+            const bool have = good[which] >> lr & 1;
+            cp_async16(tile + (c >> 3) * L::CHUNK_KV + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
+                       have ? from + o + c * 8 : p.q, have);
+          }
+          issued(full(slot));
+        } else {
+          constexpr int CP8 = D / 16, RP8 = 32 / CP8, N8 = RPW / RP8;   // pieces per cached row, rows per step, steps
+          const uint8_t* const from = static_cast<const uint8_t*>(cache);
+          uint4 v[N8];
+#pragma unroll
+          for (int i = 0; i < N8; ++i) {
+            const int lr = i * RP8 + lane / CP8, c = lane % CP8;
+            const long long o = __shfl_sync(0xffffffffu, off[which], lr);
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (good[which] >> lr & 1) v[i] = ldg_stream(reinterpret_cast<const uint16_t*>(from + o + c * 16));
+          }
+#pragma unroll
+          for (int i = 0; i < N8; ++i) {
+            const int lr = i * RP8 + lane / CP8, c = 2 * (lane % CP8), rr = w * RPW + lr;
+            const uint2 a = e4m3x4_f16(v[i].x), b = e4m3x4_f16(v[i].y), e = e4m3x4_f16(v[i].z), f = e4m3x4_f16(v[i].w);
+            const uint32_t row = tile + (c >> 3) * L::CHUNK_KV + rr * 128;
+            st_shared_v4(row + (((c & 7) ^ (rr & 7)) << 4), a.x, a.y, b.x, b.y);
+            st_shared_v4(row + ((((c & 7) + 1) ^ (rr & 7)) << 4), e.x, e.y, f.x, f.y);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(full(slot));
+        }
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      const bool two = TILES == 2 && u.rows > 128;
+      locate(u.kb0);
+      load(p.kv.k, 0);
+      for (int j = 0; ok && j < u.n; ++j) {
+        if (two) {
+          load(p.kv.v, 0);
+          if (ok && j + 1 < u.n) {
+            locate(u.kb0 + j + 1);
+            load(p.kv.k, 0);
+          }
+        } else {
+          if (j + 1 < u.n) {
+            locate(u.kb0 + j + 1);
+            load(p.kv.k, 0);
+            if (ok) load(p.kv.v, 1);
+          } else {
+            load(p.kv.v, 0);
+          }
+        }
+      }
+      if constexpr (!E4M3) drain();   // before the wait for the products that need them
+    }
+    if constexpr (!E4M3) cp_wait<0>();
+  } else if (warp < 4 * TILES) {
+    // ------------------------------------------------------------ softmax and output
+    setmaxnreg_to<L::REG_SOFTMAX, L::REG_LAUNCH>();
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;                 // row of the tile (TMEM lane)
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_o = tmem + lane_addr + L::COL_O + t * D;
+    int s_used = 0, s_odd = 0, o_used = 0, block = 0;   // phases seen of S_FULL, of its third, of O_DONE; blocks
+    bool ok = true;
+    for (int count = 0; ok; ++count) {
+      const int ps = count % kPieces;
+      ok = mbar_wait(bar(B_PIECE_FULL + ps), (count / kPieces) & 1, abort, status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const Piece u = pieces[ps];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_PIECE_EMPTY + ps));
+      if (u.n == 0) break;
+      const bool two = TILES == 2 && u.rows > 128;
+      if (t == 1 && !two) {   // the first tile's warps take both score buffers
+        block += u.n;
+        continue;
+      }
+      const int row = u.row_first + t * 128 + r, tok = p.group_div.quotient(row);
+      const bool valid = t * 128 + r < u.rows;
+      const int pos = u.pos0 + tok;
+      // visible keys [lo, hi); rows past the unit's are computed like any and not written
+      const int hi = valid ? pos + 1 : 0x7fffffff;
+      const int lo = valid && p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+      const float k_scale = E4M3 && p.kv.k_scale ? p.kv.k_scale[u.head_kv] : 1.f;
+      const bool negative = p.scale * k_scale < 0.f;
+      float sl2 = 0.f;   // > 0, set once Q is there
+      float m_used = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < u.n; ++j, ++block) {
+        const bool odd = !two && (j & 1);
+        const int which = odd ? 2 : t;   // barrier
+        const uint32_t t_s = tmem + lane_addr + (odd ? 1 : t) * BK;
+        if (!mbar_wait(bar(B_S_FULL + which), (odd ? s_odd : s_used) & 1, abort, status)) ok = false;
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (odd) ++s_odd;
+        else ++s_used;
+        tc_fence_after();
+        float x[BK];
+#pragma unroll
+        for (int c = 0; c < BK / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_s + c * 32, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(v[e]);
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < BK; ++e) asm volatile("" : "+f"(x[e]));   // no use before the wait
+        if (j == 0) {
+          sl2 = fabsf(p.scale * k_scale) * kLog2e;
+          if constexpr (E4M3) sl2 *= q_scale[(count & 1) * ROWS + t * 128 + r];
+          sl2 = fmaxf(sl2, 0x1p-126f);   // a masked score times it stays -inf
+        }
+        if (negative) {
+#pragma unroll
+          for (int e = 0; e < BK; ++e) x[e] = -x[e];
+        }
+        const int key0 = (u.kb0 + j) * BK;
+        const int c_lo = max(lo - key0, 0), c_hi = hi == 0x7fffffff ? BK : min(max(hi - key0, 0), BK);
+        if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < BK)) {
+          const unsigned span = c_hi > c_lo ? c_hi - c_lo : 0;
+#pragma unroll
+          for (int e = 0; e < BK; ++e) x[e] = static_cast<unsigned>(e - c_lo) < span ? x[e] : -INFINITY;
+        }
+        const uint4 missing = *reinterpret_cast<const uint4*>(marks + (block % kMarks) * 4);
+        if (missing.x | missing.y | missing.z | missing.w) {
+          const uint32_t words[4] = {missing.x, missing.y, missing.z, missing.w};
+#pragma unroll
+          for (int e = 0; e < BK; ++e)
+            if (words[e / (BK / 4)] >> (e % (BK / 4)) & 1) x[e] = -INFINITY;
+        }
+        float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+        for (int e = 4; e < BK; e += 4) {
+          mx0 = fmaxf(mx0, x[e]);
+          mx1 = fmaxf(mx1, x[e + 1]);
+          mx2 = fmaxf(mx2, x[e + 2]);
+          mx3 = fmaxf(mx3, x[e + 3]);
+        }
+        const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2);
+        const bool grow = m_new > m_used + kSlack;   // also for the first visible key
+        float alpha = 1.f;
+        if (grow) {
+          alpha = ex2_approx(m_used - m_new);        // 0 while m_used = -inf
+          l_run *= alpha;
+          m_used = m_new;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, grow)) {
+          if (!mbar_wait(bar(B_O_DONE + t), (o_used + j - 1) & 1, abort, status)) ok = false;
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16(t_o + c * 16, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+            tmem_st16(t_o + c * 16, v);
+          }
+          tmem_st_wait();
+        }
+        // P = 2^(x sl2 - m), masked scores give 0 (any finite reference does until a key is seen)
+        const float ref = (m_used == -INFINITY ? 0.f : m_used) - (E4M3 ? kF16Shift : 0.f);
+        const float2 mul = make_float2(sl2, sl2), sub = make_float2(-ref, -ref);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int c = 0; c < BK / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 a = fma2(make_float2(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), mul, sub);
+            a.x = ex2_approx(a.x);
+            a.y = ex2_approx(a.y);
+            if (e & 1) sum1 = add2(sum1, a);
+            else sum0 = add2(sum0, a);
+            pk[e] = E4M3 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
+          }
+          tmem_st16(t_s + c * 16, pk);
+        }
+        l_run += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(B_P_READY + which));
+      }
+      if (!ok) break;
+      // ------------------------------------------------------------ output
+      // (S of the last block says nothing of the P V before it: two phases to see)
+      if (u.n > 1 && !mbar_wait(bar(B_O_DONE + t), (o_used + u.n - 2) & 1, abort, status)) ok = false;
+      if (ok && !mbar_wait(bar(B_O_DONE + t), (o_used + u.n - 1) & 1, abort, status)) ok = false;
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      o_used += u.n;
+      tc_fence_after();
+      const float top = m_used - (E4M3 ? kF16Shift : 0.f);   // what l_run and O are relative to
+      if (u.part == 0) {
+        const float v_scale = E4M3 && p.kv.v_scale ? p.kv.v_scale[u.head_kv] : 1.f;
+        const float inv = l_run == 0.f ? 0.f : v_scale / l_run;
+        const long long out = static_cast<long long>(u.token0 + tok) * p.heads + u.head_kv * group + (row - tok * group);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_o + c * 32, v);
+          tmem_ld_wait();
+          if (valid) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              pk[e] = l_run == 0.f ? 0u
+                                   : pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+            uint4* const to = reinterpret_cast<uint4*>(p.o + out * D + c * 32);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) to[g] = make_uint4(pk[4 * g], pk[4 * g + 1], pk[4 * g + 2], pk[4 * g + 3]);
+          }
+        }
+        if (valid && p.lse) p.lse[out] = l_run == 0.f ? -INFINITY : (top + log2f(l_run)) * kLn2;
+      } else {
+        float* const part = parts_of(p.work, gridDim.x) +
+                            (static_cast<size_t>(blockIdx.x) * 2 + u.part - 1) * part_floats(ROWS, D);
+        const int at = t * 128 + r;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_o + c * 32, v);
+          tmem_ld_wait();
+          if (valid) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              *reinterpret_cast<uint4*>(part + (static_cast<size_t>(c * 8 + g) * ROWS + at) * 4) =
+                  make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+          }
+        }
+        if (valid) {
+          part[static_cast<size_t>(ROWS) * D + at] = top;
+          part[static_cast<size_t>(ROWS) * (D + 1) + at] = l_run;
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(B_O_FREE + t));
+    }
+  } else {
+    setmaxnreg_to<L::REG_OTHER, L::REG_LAUNCH>();   // two warps of the last four have nothing to do
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == L::MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------ join
+// Block (run, 32 rows): joins the partial results of the unit that run `run`
+// starts and later runs go on with.  A lane per row, a warp for some columns.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const ExtendParams p, int blocks) {
+  constexpr int ROWS = Shape<D>::kRows, WARPS = kJoinThreads / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, at = blockIdx.y * 32 + lane, run = blockIdx.x;
+  pdl_wait();
+  const Cut cut = reinterpret_cast<const Cut*>(p.work)[run];
+  if (cut.row_first + static_cast<int>(blockIdx.y) * 32 >= cut.row_end) return;
+  const bool valid = cut.row_first + at < cut.row_end;
+  const float* const parts = parts_of(p.work, blocks);
+  auto part = [&](int i) {   // of run `run + i`
+    return parts + (static_cast<size_t>(run + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(ROWS, D);
+  };
+  const int n = cut.last - run + 1;
+  float top = -INFINITY;
+  if (valid)
+    for (int i = 0; i < n; ++i) {
+      const float* const q = part(i) + static_cast<size_t>(ROWS) * D + at;
+      if (q[ROWS] != 0.f) top = fmaxf(top, q[0]);
+    }
+  float sum = 0.f;
+  float4 acc[D / 4 / WARPS];
+#pragma unroll
+  for (int c = 0; c < D / 4 / WARPS; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (valid)
+    for (int i = 0; i < n; ++i) {
+      const float* const q = part(i);
+      const float l = q[static_cast<size_t>(ROWS) * (D + 1) + at];
+      if (l == 0.f) continue;
+      const float f = ex2_approx(q[static_cast<size_t>(ROWS) * D + at] - top);
+      sum = fmaf(f, l, sum);
+#pragma unroll
+      for (int c = 0; c < D / 4 / WARPS; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(q + (static_cast<size_t>(c * WARPS + warp) * ROWS + at) * 4);
+        acc[c].x = fmaf(f, v.x, acc[c].x);
+        acc[c].y = fmaf(f, v.y, acc[c].y);
+        acc[c].z = fmaf(f, v.z, acc[c].z);
+        acc[c].w = fmaf(f, v.w, acc[c].w);
+      }
+    }
+  if (!valid) return;
+  const int group = p.heads / p.kv.heads_kv, row = cut.row_first + at, tok = p.group_div.quotient(row);
+  const long long out = static_cast<long long>(cut.token0 + tok) * p.heads + cut.head_kv * group + (row - tok * group);
+  const float v_scale = p.kv.v_scale ? p.kv.v_scale[cut.head_kv] : 1.f;
+  const float inv = sum == 0.f ? 0.f : v_scale / sum;
+#pragma unroll
+  for (int c = 0; c < D / 4 / WARPS; ++c)
+    *reinterpret_cast<uint2*>(p.o + out * D + (c * WARPS + warp) * 4) =
+        make_uint2(pack_bf16x2(acc[c].x * inv, acc[c].y * inv), pack_bf16x2(acc[c].z * inv, acc[c].w * inv));
+  if (p.lse && warp == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_dim(const ExtendParams& p, const Device& dev, cudaStream_t s) {
+  using L = Layout<D, E4M3>;
+  static std::atomic<unsigned long long> done{0}, join_done{0};
+  auto* const kernel = extend_kernel<D, E4M3>;
+  cudaError_t e = prepare_once(reinterpret_cast<const void*>(kernel), L::BYTES, dev.id, done);
+  if (e != cudaSuccess) return e;
+  const int blocks = dev.sms < kMaxSms ? dev.sms : kMaxSms;
+  e = launch_pdl(kernel, dim3(blocks), dim3(L::THREADS), L::BYTES, s, p);
+  if (e != cudaSuccess) return e;
+  // units of one block are never cut
+  if (static_cast<long long>(p.max_pages) * p.kv.page_size <= L::BK) return e;
+  e = prepare_once(reinterpret_cast<const void*>(join_kernel<D>), 0, dev.id, join_done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(join_kernel<D>, dim3(blocks, Shape<D>::kRows / 32), dim3(kJoinThreads), 0, s, p, blocks);
+}
+
+}  // namespace
+}  // namespace extend
+
+cudaError_t launch_extend(const ExtendParams& p, const Device& dev, cudaStream_t s) {
+  using namespace extend;
+  if (p.kv.e4m3)
+    return p.kv.head_dim == 64    ? launch_dim<64, true>(p, dev, s)
+           : p.kv.head_dim == 128 ? launch_dim<128, true>(p, dev, s)
+                                  : launch_dim<256, true>(p, dev, s);
+  return p.kv.head_dim == 64    ? launch_dim<64, false>(p, dev, s)
+         : p.kv.head_dim == 128 ? launch_dim<128, false>(p, dev, s)
+                                : launch_dim<256, false>(p, dev, s);
+}
+
+int extend_read_and_clear_status(cudaStream_t s, int* status) {
+  int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_extend_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_extend_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return static_cast<int>(e);
+}
+
+}  // namespace fa

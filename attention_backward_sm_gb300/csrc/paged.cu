@@ -1,5 +1,6 @@
-// Paged key/value cache: C entry points, and the kernels that give new
-// tokens their places in the cache (plan) and write them there (append).
+// Paged key/value cache: C entry points (those of decode and extend, too), and
+// the kernels that give new tokens their places in the cache (plan) and write
+// them there (append).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -8,6 +9,7 @@
 
 #include "../../include/fabwd.h"
 #include "checks.h"
+#include "extend.h"
 #include "internal.h"
 #include "paged.h"
 #include "quantise.cuh"
@@ -449,6 +451,87 @@ int fa_decode(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
   p.scale = scale;
   cudaError_t e = fa::launch_decode(p, dev, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
+  return ok();
+}
+
+size_t fa_extend_workspace_size(int head_dim) {
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) {
+    set_last_error(FA_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256, got %d", head_dim);
+    return 0;
+  }
+  ok();
+  return fa::extend::workspace_bytes(head_dim);
+}
+
+int fa_extend(const fa_bf16* q, long long q_row_stride, const void* k_cache, const void* v_cache, int kv_type,
+              const float* k_scale, const float* v_scale, long long page_stride, long long slot_stride,
+              long long head_stride, int num_pages, int page_size, const int32_t* block_table,
+              long long table_stride, int max_pages, const int32_t* seq_lens, const int32_t* cu_new, int batch,
+              int num_tokens, int heads, int heads_kv, int head_dim, int window, float scale, fa_bf16* o, float* lse,
+              void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  fa::ExtendParams p;
+  p.kv = make_cache(k_cache, v_cache, kv_type, k_scale, v_scale, page_stride, slot_stride, head_stride, num_pages,
+                    page_size, heads_kv, head_dim);
+  int rc = check_cache(p.kv, kv_type);
+  if (rc) return rc;
+  if (batch < 0 || num_tokens < 0)
+    return set_last_error(FA_ERR_INVALID_ARG, "batch and num_tokens must be >= 0, got %d and %d", batch, num_tokens);
+  if (heads < 1 || heads % heads_kv != 0)
+    return set_last_error(FA_ERR_INVALID_ARG, "query heads (%d) must be a positive multiple of key/value heads (%d)",
+                          heads, heads_kv);
+  if (static_cast<long long>(heads) * head_dim > 65535 * 64)
+    return set_last_error(FA_ERR_UNSUPPORTED, "heads * head_dim too large (%d * %d)", heads, head_dim);
+  // Rows (tokens by heads) and units (of a request and a key/value head) are counted with 32 bits.
+  if (static_cast<long long>(num_tokens) * heads > 0x7ff00000ll || static_cast<long long>(batch) * heads_kv > 0x7fffffffll)
+    return set_last_error(FA_ERR_UNSUPPORTED, "%d tokens of %d requests and %d heads are too many", num_tokens, batch,
+                          heads);
+  if (window < 0) return set_last_error(FA_ERR_INVALID_ARG, "window must be >= 0, got %d", window);
+  if (!isfinite(scale)) return set_last_error(FA_ERR_INVALID_ARG, "scale must be finite");
+  if (max_pages < 0) return set_last_error(FA_ERR_INVALID_ARG, "max_pages must be >= 0, got %d", max_pages);
+  if (static_cast<long long>(max_pages) * page_size > 0x7fff0000ll)
+    return set_last_error(FA_ERR_UNSUPPORTED, "a block table of %d pages of %d slots is too long", max_pages, page_size);
+  if (batch > 1 && table_stride < 0)
+    return set_last_error(FA_ERR_INVALID_ARG, "table_stride must be >= 0, got %lld", table_stride);
+  if ((rc = check_row_stride("q_row_stride", q_row_stride, static_cast<long long>(heads) * head_dim, num_tokens)))
+    return rc;
+  if (num_tokens == 0) return ok();
+  if (!q || !o || !cu_new || (batch > 0 && !seq_lens) || (batch > 0 && max_pages > 0 && !block_table) ||
+      (batch > 0 && max_pages > 0 && num_pages > 0 && (!k_cache || !v_cache)))
+    return set_last_error(FA_ERR_INVALID_ARG, "a device pointer is NULL");
+  if (misaligned16(q) || misaligned16(o)) return set_last_error(FA_ERR_INVALID_ARG, "q and o must be 16-byte aligned");
+  if (misaligned4(block_table) || misaligned4(seq_lens) || misaligned4(cu_new) || misaligned4(lse))
+    return set_last_error(FA_ERR_INVALID_ARG, "block_table, seq_lens, cu_new and lse must be 4-byte aligned");
+  // Blocks write rows of o while others still read q.
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+  const uintptr_t row = 2ull * heads * head_dim;
+  const uintptr_t q_bytes = (num_tokens - 1) * 2ull * (num_tokens > 1 ? q_row_stride : 0) + row;
+  if (q0 < o0 + num_tokens * row && o0 < q0 + q_bytes)
+    return set_last_error(FA_ERR_INVALID_ARG, "o must not overlap q");
+  const size_t need = fa::extend::workspace_bytes(head_dim);
+  if (!workspace || workspace_bytes < need)
+    return set_last_error(FA_ERR_INVALID_ARG, "workspace of %zu bytes needed, got %zu", need, workspace_bytes);
+  if (misaligned16(workspace)) return set_last_error(FA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  fa::Device dev;
+  if ((rc = check_device(dev))) return rc;
+  p.q = q;
+  p.q_row_stride = q_row_stride;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.seq_lens = seq_lens;
+  p.cu_new = cu_new;
+  p.o = o;
+  p.lse = lse;
+  p.work = workspace;
+  p.page_div = fa::FastDiv(static_cast<uint32_t>(page_size));
+  p.group_div = fa::FastDiv(static_cast<uint32_t>(heads / heads_kv));
+  p.max_pages = num_pages > 0 ? max_pages : 0;   // without pages no key is seen
+  p.batch = batch;
+  p.num_tokens = num_tokens;
+  p.heads = heads;
+  p.window = window;
+  p.scale = scale;
+  cudaError_t e = fa::launch_extend(p, dev, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "extend launch");
   return ok();
 }
 

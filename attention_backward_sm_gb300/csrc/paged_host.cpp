@@ -416,6 +416,62 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FAB_END
 }
 
+// q, k_cache, v_cache, block_table, seq_lens, cu_new, scale, window, k_scale,
+// v_scale, out (None or (o, lse or None)), workspace, stream
+PyObject* extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  FAB_BEGIN
+  if (!arity(n, 13)) return nullptr;
+  const Cache c(a[1], a[2], a[8], a[9]);
+  const Table table(a[3]);
+  const Tensor &q = tensor(a[0], "q"), &seq = tensor(a[4], "seq_lens"), &cu = tensor(a[5], "cu_new");
+  if (q.dim() != 3) refuse("q must be [num_tokens, H, d], got " + kind(q));
+  const int64_t tokens = q.size(0), heads = q.size(1), dim = c.dim;
+  const int64_t q_stride = row_stride(q, "q", tokens, heads, dim);
+  vector(seq, "seq_lens", at::kInt, table.batch);
+  vector(cu, "cu_new", at::kInt, table.batch + int64_t{1});
+  const double scale = PyFloat_AsDouble(a[6]);
+  if (scale == -1.0 && PyErr_Occurred()) throw python_error();
+  const int window = integer32(a[7], "window"), h32 = size32(heads, "H"), t32 = size32(tokens, "num_tokens");
+  auto work = tensor_or_none(a[11], "workspace");
+  if (work && !work->is_contiguous()) refuse("workspace must be contiguous");
+  Place place(q);
+  place.with(c.k, "k_cache").with(c.v, "v_cache").with(table.t, "block_table").with(seq, "seq_lens").with(cu, "cu_new");
+  place.with(c.k_scale, "k_scale").with(c.v_scale, "v_scale").with(work, "workspace");
+  // 0 for a head_dim that fa_extend refuses, below, with its code.
+  const size_t need = fa_extend_workspace_size(c.dim);
+  Tensor o;
+  std::optional<Tensor> lse;
+  if (a[10] != Py_None) {
+    if (!PyTuple_Check(a[10]) || PyTuple_GET_SIZE(a[10]) != 2) refuse("out must be a tuple (o, lse)");
+    o = tensor(PyTuple_GET_ITEM(a[10], 0), "o");
+    lse = tensor_or_none(PyTuple_GET_ITEM(a[10], 1), "lse");
+    row_stride(o, "o", tokens, heads, dim);
+    if (!o.is_contiguous()) refuse("o must be contiguous");
+    if (lse && (lse->scalar_type() != at::kFloat || lse->dim() != 2 || lse->size(0) != tokens ||
+                lse->size(1) != heads || !lse->is_contiguous()))
+      refuse("lse must be contiguous float32 [num_tokens, H], got " + kind(*lse));
+    place.with(o, "o").with(lse, "lse").enter(a[12]);
+  } else {
+    place.enter(a[12]);
+    Cutter out(place.bytes(Cutter::size(tokens * heads * dim, 2) + Cutter::size(tokens * heads, 4)));
+    o = out.next({tokens, heads, dim}, at::kBFloat16);
+    lse = out.next({tokens, heads}, at::kFloat);
+  }
+  c10::DataPtr own_work;
+  if (!work && need > 0) own_work = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+  void* const work_ptr = work ? ptr<void>(*work) : own_work.get();
+  const size_t work_bytes = work ? work->nbytes() : need;
+  check(unlocked([&] {
+    return fa_extend(ptr<fa_bf16>(q), q_stride, ptr<void>(c.k), ptr<void>(c.v), c.type, c.ks(), c.vs(), c.k.stride(0),
+                     c.k.stride(1), c.k.stride(2), c.pages, c.page_size, ptr<int32_t>(table.t), table.stride,
+                     table.width, ptr<int32_t>(seq), ptr<int32_t>(cu), table.batch, t32, h32, c.heads_kv, c.dim, window,
+                     static_cast<float>(scale), ptr<fa_bf16>(o), lse ? ptr<float>(*lse) : nullptr, work_ptr, work_bytes,
+                     place.stream());
+  }));
+  return pack({o, lse ? *lse : Tensor()});
+  FAB_END
+}
+
 double real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -615,6 +671,7 @@ PyMethodDef methods[] = {
     {"plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(plan)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode)), METH_FASTCALL, nullptr},
+    {"extend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(extend)), METH_FASTCALL, nullptr},
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, nullptr},
     {"rope_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_bwd)), METH_FASTCALL, nullptr},
     {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_append)), METH_FASTCALL, nullptr},

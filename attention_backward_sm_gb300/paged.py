@@ -1,4 +1,5 @@
-"""Paged key/value cache: fa_kv_plan, fa_kv_append and fa_decode for torch.
+"""Paged key/value cache: fa_kv_plan, fa_kv_append, fa_decode and fa_extend for
+torch.
 
 k_cache and v_cache are [num_pages, page_size, Hkv, d] tensors, bf16 or
 float8_e4m3fn, in any strided layout whose last dimension is contiguous
@@ -105,3 +106,28 @@ def decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, window: int
     instead of fresh ones (calls that may overlap need one each)."""
     return (_native or _host()).decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, k_scale, v_scale, out,
                                        workspace, stream)
+
+
+def fa_extend_workspace_size(head_dim: int) -> int:
+    n = lib().fa_extend_workspace_size(head_dim)
+    if n == 0:
+        raise FabwdError(FA_ERR_UNSUPPORTED, fa_last_error())
+    return int(n)
+
+
+def fa_extend(q, k_cache, v_cache, block_table, seq_lens, cu_new, o, lse, scale: float, window: int = 0, k_scale=None,
+              v_scale=None, workspace=None, stream=None):
+    """Fills o (bf16, contiguous) and lse (fp32, or None) in place."""
+    (_native or _host()).extend(q, k_cache, v_cache, block_table, seq_lens, cu_new, scale, window, k_scale, v_scale,
+                                (o, lse), workspace, stream)
+
+
+def extend(q, k_cache, v_cache, block_table, seq_lens, cu_new, scale: float, window: int = 0, k_scale=None,
+           v_scale=None, out=None, workspace=None, stream=None):
+    """Attention of the new tokens q [num_tokens, H, d] over the cache, causal
+    within each request; seq_lens and cu_new are kv_plan's.  Returns (o, lse),
+    cut from one allocation like kv_plan's.  out: (o, lse) to fill instead of new
+    tensors (lse may be None).  workspace: fa_extend_workspace_size() bytes to use
+    instead of fresh ones (calls that may overlap need one each)."""
+    return (_native or _host()).extend(q, k_cache, v_cache, block_table, seq_lens, cu_new, scale, window, k_scale,
+                                       v_scale, out, workspace, stream)

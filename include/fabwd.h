@@ -368,6 +368,38 @@ int fa_decode(const fa_bf16* q, long long q_row_stride,
               int window, float scale, fa_bf16* o, float* lse,
               void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
+/* Bytes of device workspace fa_extend needs, whatever the sizes.  Returns 0 and
+ * sets fa_last_error() on bad arguments. */
+size_t fa_extend_workspace_size(int head_dim);
+
+/* Attention of several new tokens per request over the cache (a chunk of a
+ * prompt, drafted tokens to be verified, single tokens, or a mixture): q
+ * [num_tokens, H, d] bf16 (rows q_row_stride elements apart, a multiple of 8),
+ * request b's rows are cu_new[b] to cu_new[b+1], cu_new [batch+1] int32 and
+ * seq_lens [batch] int32 on the device as fa_kv_plan writes them: seq_lens[b]
+ * keys with the new tokens' own, which are in the cache already
+ * (fa_kv_append, fa_qk_rope_append).  Token i of n is at position
+ * p = seq_lens[b] - n + i and sees the keys [max(0, p - window + 1), p] (window 0:
+ * [0, p]).  o [num_tokens, H, d] bf16 contiguous, lse [num_tokens, H] float32
+ * (may be NULL): for one new token per request, what fa_decode gives up to
+ * rounding.  Lengths are clamped to max_pages * page_size, offsets to
+ * num_tokens (a request cut off by num_tokens keeps its positions).  A row that
+ * sees no key, and one that belongs to no request (from cu_new[batch] on; a
+ * padded batch), gets o = 0, lse = -inf.  Contents of slots that no row of a
+ * request sees do not matter (NaN included).  The weights exp(x - max) are
+ * rounded to bf16 beside a bf16 cache (as in fa_fwd_*), to fp16 beside an e4m3
+ * one; sums are fp32.  o must not overlap q.  workspace: 16-byte aligned,
+ * contents arbitrary; calls whose work overlaps on the GPU need one each.
+ * Results do not depend on timing: the same call gives the same bits.  Waits
+ * inside are bounded: fa_check_device_status reports one that ran out. */
+int fa_extend(const fa_bf16* q, long long q_row_stride,
+              const void* k_cache, const void* v_cache, int kv_type, const float* k_scale, const float* v_scale,
+              long long page_stride, long long slot_stride, long long head_stride,
+              int num_pages, int page_size, const int32_t* block_table, long long table_stride, int max_pages,
+              const int32_t* seq_lens, const int32_t* cu_new, int batch, int num_tokens,
+              int heads, int heads_kv, int head_dim, int window, float scale, fa_bf16* o, float* lse,
+              void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Rotation of queries and keys by their positions, with an optional norm per
  * head: what stands between a projection and fa_fwd_* or the cache.

@@ -78,3 +78,29 @@ def decode(q, k_cache, v_cache, table, seq_lens, scale: float, window: int = 0, 
             lse[b, h] = x.max() + np.log(e.sum())
             xa[b, h] = abs(scale) * (np.abs(k) @ np.abs(q[b, h])).max()
     return o, lse, pv, xa
+
+
+def extend(q, k_cache, v_cache, table, seq_lens, cu_new, scale: float, window: int = 0, k_scale=None, v_scale=None):
+    """(o, lse, p_abs_v, x_abs, keys) of several new tokens per request, one
+    token at a time: decode() of the request as long as it was when that token
+    was its last; keys [T] is how many positions it sees.  Rows of no request: o =
+    0, lse = -inf."""
+    q = _f64(q)
+    table = np.asarray(table)
+    T, H, d = q.shape
+    most = table.shape[1] * np.shape(k_cache)[1]
+    o, pv = np.zeros((T, H, d)), np.zeros((T, H, d))
+    lse, xa, keys = np.full((T, H), -np.inf), np.zeros((T, H)), np.zeros(T, dtype=np.int64)
+    for b in range(len(seq_lens)):
+        first, new = int(cu_new[b]), int(cu_new[b + 1]) - int(cu_new[b])
+        rows = np.arange(first, min(first + new, T))
+        at = min(max(int(seq_lens[b]), 0), most) - new + (rows - first) + 1
+        if len(rows) == 0:
+            continue
+        n = np.maximum(at, 0)
+        keys[rows] = np.minimum(n, window) if window else n
+        r = decode(q[rows], k_cache, v_cache, np.repeat(table[b][None], len(rows), 0), n, scale, window, k_scale,
+                   v_scale)
+        for out, part in zip((o, lse, pv, xa), r):
+            out[rows] = part
+    return o, lse, pv, xa, keys
