@@ -203,6 +203,8 @@ int check_device() {
 }  // namespace
 
 namespace fa {
+
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
 int set_last_error(int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);

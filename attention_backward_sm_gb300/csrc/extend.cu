@@ -29,8 +29,7 @@
 // its run with one scan over the requests.
 //
 // Warps: per tile of 128 rows four for the softmax and the output, then four
-// that load (cp.async, so any page size, strides and missing pages; 8-bit
-// caches are converted to fp16 on the way), one that issues the products, one
+// that load, one that issues the products, one
 // that walks along the run and tells the others what is next.
 //   Two tiles: the products of one run while the softmax works on the other,
 //   in the order P_A V, S_A (of the next block), P_B V, S_B.
@@ -38,10 +37,13 @@
 //   issued before P V of this one.
 // The tensor core takes a block's products in the order they are issued, which
 // is what lets S overwrite the P before it without waiting.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -70,6 +72,7 @@ constexpr float kSlack = 8.f;
 // smallest step 2^-24 counts 2^-31 beside the row's largest weight.
 constexpr float kF16Shift = 7.f;
 constexpr int kPieces = 4;     // pieces of the run that the walker is ahead
+constexpr int kLeastRun = 2;   // costs
 constexpr int kMarks = 8;      // blocks whose missing pages are kept
 constexpr int kLag = 2;        // loads in flight behind the newest
 
@@ -104,16 +107,21 @@ struct Layout {
   static constexpr uint32_t CHUNK_Q = 128 * 128;
   static constexpr uint32_t TILE_KV = BK * D * 2;
   static constexpr uint32_t CHUNK_KV = BK * 128;
-  static constexpr int NS = D == 64 ? 8 : 5;            // ring of key and value tiles
+  // Ring of key and value tiles; 8-bit caches: and one of rows as they are cached,
+  // on their way.
+  static constexpr int NS = E4M3 ? (D == 64 ? 6 : 3) : D == 64 ? 8 : 5;
+  static constexpr int NR = E4M3 ? (D == 64 ? 6 : 4) : 0;
+  static constexpr uint32_t TILE_RAW = BK * D;
   static constexpr uint32_t Q = 0;
   static constexpr uint32_t KV = S::kTiles * TILE_Q;
-  static constexpr uint32_t BARS = KV + NS * TILE_KV;
+  static constexpr uint32_t RAW = KV + NS * TILE_KV;
+  static constexpr uint32_t BARS = RAW + NR * TILE_RAW;
   static constexpr int NUM_BARS = B_FULL + 2 * NS;
   static constexpr uint32_t MARKS = (BARS + NUM_BARS * 8 + 15) / 16 * 16;    // [kMarks][4] words
   static constexpr uint32_t PIECES = MARKS + kMarks * 16;
   static constexpr uint32_t QSCALE = PIECES + kPieces * sizeof(Piece);       // [2 pieces][rows] (8-bit caches)
-  static constexpr uint32_t SCAN = QSCALE + (E4M3 ? 2 * S::kRows * 4 : 0);       // [warps] 64-bit sums, then Found
-  static constexpr uint32_t MISC = SCAN + 16 * 8 + 64;
+  static constexpr uint32_t SCAN = QSCALE + (E4M3 ? 2 * S::kRows * 4 : 0);       // [warps] sums, then Found
+  static constexpr uint32_t MISC = SCAN + 16 * 4 + 16;
   static constexpr uint32_t BYTES = MISC + 16;
   static constexpr uint32_t COL_O = 2 * BK;              // after two score buffers
   static constexpr int WARPS = 4 * S::kTiles + 8;
@@ -128,7 +136,7 @@ struct Layout {
   static_assert(S::kTiles * 128 * REG_SOFTMAX + 256 * REG_OTHER <= REG_LAUNCH * THREADS, "register budget");
   static_assert(COL_O + S::kTiles * D <= TMEM_COLS, "tensor memory budget");
   static_assert(BYTES <= 232448, "shared memory budget");
-  static_assert(NS > kLag + 1, "loads in flight");
+  static_assert(E4M3 || NS > kLag + 1, "loads in flight");
   static_assert(2 * kMarks - NS >= 2, "marks outlive their block");
 };
 
@@ -187,72 +195,72 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // ------------------------------------------------------------------ partition
-// A request's numbers, and the cost of its units: tile x costs the keys that
-// its last row sees (as if none were missing) and kUnitCost more.
+// A request's numbers, and the cost of its units.  Tile x costs kUnitCost and one
+// for every 2^cost_shift keys that its last row sees (as if none were missing),
+// summed over tiles in closed form: costs only share out the work, so they are
+// rounded as suits, but every block has to come to the same ones.  Plain 32-bit
+// integers, without a division: the walk to a block's run is on the way of short
+// calls.
 template <int D>
 struct Request {
   using S = Shape<D>;
-  static constexpr int kUnitCost = S::kKeys;
-  int token0, len, pos0;
-  long long rows;       // tokens * group
+  static constexpr int kUnitCost = 2;
+  static constexpr int kRowBits = S::kRows == 256 ? 8 : 7;
+  int token0, len, pos0, base, rows;   // rows: tokens * group
   int tiles;
-  long long base, cap;  // cost of a tile without its tokens' own keys; with a window: of a tile at most
-  int ramp;             // tiles that cost less than cap
-  long long last;       // what the last tile costs
-  long long cost;       // of all tiles, for one key/value head
+  int ramp;   // tiles that see less than the window
+  int most;   // with a window: what a tile costs at most
+  int last;   // what the last tile costs
+  int cost;   // of all tiles, for one key/value head
   __device__ __forceinline__ Request(const ExtendParams& p, int b, int group) {
-    const int most = p.max_pages * p.kv.page_size;
     const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1];
+    len = min(max(p.seq_lens[b], 0), p.max_pages * p.kv.page_size);
     token0 = min(max(c0, 0), p.num_tokens);
     const int end = min(max(c1, token0), p.num_tokens);
-    len = min(max(p.seq_lens[b], 0), most);
     const long long n = max(static_cast<long long>(c1) - c0, 0ll);
     pos0 = static_cast<int>(max(len - n, -static_cast<long long>(p.num_tokens) - 1));
-    rows = static_cast<long long>(end - token0) * group;
-    tiles = static_cast<int>((rows + S::kRows - 1) / S::kRows);
-    base = max(pos0, 0) + kUnitCost;
-    cap = p.window > 0 ? static_cast<long long>(p.window) + S::kRows / group + 1 + kUnitCost : 0;
+    rows = (end - token0) * group;
+    tiles = (rows + S::kRows - 1) >> kRowBits;
+    base = max(pos0, 0);
     ramp = tiles;
+    last = kUnitCost + ((base + end - token0) >> p.cost_shift);
+    most = 0x7fffffff;
     if (p.window > 0) {
-      const long long r = cap > base ? (cap - base) * group / S::kRows : 0;
-      ramp = static_cast<int>(min(r, static_cast<long long>(tiles)));
+      const long long seen = static_cast<long long>(p.window) + p.tile_tokens;
+      ramp = seen > base ? static_cast<int>(min(((seen - base) * group) >> kRowBits, static_cast<long long>(tiles))) : 0;
+      most = kUnitCost + 1 + static_cast<int>(min(seen, 0x7fffffffll) >> p.cost_shift);
+      last = min(last, most);
     }
-    last = base + end - token0;
-    if (p.window > 0) last = min(last, cap);
-    cost = tiles > 0 ? before(tiles, group) : 0;
+    cost = tiles > 0 ? full(p, tiles - 1) + last : 0;
   }
   // Of the tiles before tile x.
-  __device__ __forceinline__ long long before(int x, int group) const {
-    if (x == tiles) return before_full(tiles - 1, group) + last;
-    return before_full(x, group);
-  }
-  __device__ __forceinline__ long long before_full(int x, int group) const {
-    const long long y = min(x, ramp);
-    return y * base + S::kRows * y * (y + 1) / (2 * group) + (x - y) * cap;
+  __device__ __forceinline__ int before(const ExtendParams& p, int x) const { return x == tiles ? cost : full(p, x); }
+  __device__ __forceinline__ int full(const ExtendParams& p, int x) const {
+    const long long y = min(x, ramp);   // the sum of base + (i + 1) rows / group over i < y, in 32nds
+    const long long keys = y * base * 32 + y * (y + 1) * p.tile_keys16;
+    return x * kUnitCost + static_cast<int>(keys >> (p.cost_shift + 5)) + (x - static_cast<int>(y)) * (most - kUnitCost);
   }
 };
 
 struct Runs {
-  long long base, rem;
-  int runs;
-  __device__ __forceinline__ Runs(long long total, int blocks, long long least) {
-    const long long most = total / least;
-    runs = most < 1 ? 1 : most < blocks ? static_cast<int>(most) : blocks;
-    base = total / runs;
+  int base, rem, runs;
+  __device__ __forceinline__ Runs(int total, int blocks) {
+    runs = max(1, min(total / kLeastRun, blocks));
+    base = static_cast<unsigned>(total) / static_cast<unsigned>(runs);
     rem = total - base * runs;
   }
-  __device__ __forceinline__ long long start(int r) const { return r * base + min(static_cast<long long>(r), rem); }
+  __device__ __forceinline__ int start(int r) const { return r * base + min(r, rem); }
   // The run that holds place x.
-  __device__ __forceinline__ int of(long long x) const {
-    const long long y = x - rem * (base + 1);
-    return static_cast<int>(y < 0 ? x / (base + 1) : rem + y / base);
+  __device__ __forceinline__ int of(int x) const {
+    const int y = x - rem * (base + 1);
+    return y < 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(base + 1)
+                 : rem + static_cast<unsigned>(y) / static_cast<unsigned>(base);
   }
 };
 
 // What a block knows of its run after the scan.
 struct Found {
-  long long at;      // the request's place on the line
-  long long total;
+  int at;   // the request's place on the line
   int b;
 };
 
@@ -263,7 +271,7 @@ __device__ __forceinline__ float* parts_of(void* work, int runs) {
 
 // ------------------------------------------------------------------ main kernel
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(const ExtendParams p) {
+__global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(const __grid_constant__ ExtendParams p) {
   using L = Layout<D, E4M3>;
   using S = Shape<D>;
   constexpr int BK = L::BK, NS = L::NS, TILES = S::kTiles, ROWS = S::kRows;
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
   Piece* const pieces = reinterpret_cast<Piece*>(smem + L::PIECES);
   uint32_t* const marks = reinterpret_cast<uint32_t*>(smem + L::MARKS);
   float* const q_scale = reinterpret_cast<float*>(smem + L::QSCALE);
-  long long* const scan = reinterpret_cast<long long*>(smem + L::SCAN);
+  int* const scan = reinterpret_cast<int*>(smem + L::SCAN);
   Found* const found = reinterpret_cast<Found*>(scan + 16);
   const uint32_t bars = sbase + L::BARS;
   auto bar = [&](int i) { return bars + 8u * i; };
@@ -290,22 +298,22 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
   }
   if (threadIdx.x == 0) {
     *abort = 0;
-    mbar_init(bar(B_Q_FULL), 128);
+    mbar_init(bar(B_Q_FULL), 4);   // a lane of every warp, here and below
     mbar_init(bar(B_Q_EMPTY), 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(bar(B_S_FULL + i), 1);
-      mbar_init(bar(B_P_READY + i), 128);
+      mbar_init(bar(B_P_READY + i), 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_O_DONE + i), 1);
-      mbar_init(bar(B_O_FREE + i), 128);
+      mbar_init(bar(B_O_FREE + i), 4);
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(bar(B_PIECE_FULL + i), 1);
       mbar_init(bar(B_PIECE_EMPTY + i), 4 * TILES + 5);   // a lane of every other warp
     }
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full(i), 128);
+      mbar_init(full(i), 4);
       mbar_init(empty(i), 1);
     }
     mbar_init(bar(B_TEARDOWN), 1);
@@ -321,13 +329,13 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
   // The line's length, and the request that this block's run starts in.
   const int per = (p.batch + L::THREADS - 1) / L::THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
-  long long mine = 0;
+  int mine = 0;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += Request<D>(p, b, group).cost * p.kv.heads_kv;
-  long long upto = mine;
+  int upto = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+    const int x = __shfl_up_sync(0xffffffffu, upto, off);
     if (lane >= off) upto += x;
   }
   if (lane == 31) scan[warp] = upto;
@@ -346,20 +354,20 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  long long total = 0;
-#pragma unroll 1
+  int total = 0;
+#pragma unroll
   for (int w = 0; w < L::WARPS; ++w) {
     if (w < warp) upto += scan[w];
     total += scan[w];
   }
-  const Runs runs(total, gridDim.x, 2 * BK);
-  const long long run_start = total > 0 && static_cast<int>(blockIdx.x) < runs.runs ? runs.start(blockIdx.x) : total;
-  const long long run_end = run_start < total ? runs.start(blockIdx.x + 1) : total;
+  const Runs runs(total, gridDim.x);
+  const int run_start = static_cast<int>(blockIdx.x) < runs.runs ? runs.start(blockIdx.x) : total;
+  const int run_end = run_start < total ? runs.start(blockIdx.x + 1) : total;
   if (run_start < total && run_start >= upto - mine && run_start < upto) {
-    long long at = upto - mine;
+    int at = upto - mine;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const long long cost = Request<D>(p, b, group).cost * p.kv.heads_kv;
+      const int cost = b1 - b0 == 1 ? mine : Request<D>(p, b, group).cost * p.kv.heads_kv;
       if (run_start < at + cost) {
         found->at = at;
         found->b = b;
@@ -375,6 +383,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     setmaxnreg_to<L::REG_OTHER, L::REG_LAUNCH>();
     Cut cut = {};
     int count = 0;   // pieces
+    const int spare = p.cost_shift - (BK == 128 ? 7 : 6);   // blocks that cost 1 together, log 2
     bool ok = true;
     auto emit = [&](const Piece& piece) {
       const int slot = count % kPieces;
@@ -389,8 +398,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       ++count;
     };
     if (run_start < total) {
-      int b = found->b;
-      long long at = found->at;
+      int b = found->b, at = found->at;
       while (ok && b < p.batch && at < run_end) {
         const Request<D> r(p, b, group);
         if (r.cost == 0) {
@@ -399,31 +407,31 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         }
         int hk = 0, x = 0;
         if (run_start > at) {
-          const long long in = run_start - at;
-          hk = static_cast<int>(in / r.cost);
-          const long long rem = in - hk * r.cost;
+          const int in = run_start - at;
+          hk = static_cast<unsigned>(in) / static_cast<unsigned>(r.cost);
+          const int rem = in - hk * r.cost;
           int hi = r.tiles;   // before(x) <= rem < before(hi)
           while (hi - x > 1) {
             const int mid = (x + hi) >> 1;
-            if (r.before(mid, group) <= rem) x = mid;
+            if (r.before(p, mid) <= rem) x = mid;
             else hi = mid;
           }
         }
         bool in_run = true;
         for (; ok && in_run && hk < p.kv.heads_kv; ++hk, x = 0) {
           for (; ok && x < r.tiles; ++x) {
-            const long long c = at + hk * r.cost + r.before(x, group);
+            const int c = at + hk * r.cost + r.before(p, x);
             if (c >= run_end) {
               in_run = false;
               break;
             }
-            const long long w = r.before(x + 1, group) - r.before(x, group);
+            const int w = r.before(p, x + 1) - r.before(p, x);
             Piece u;
             u.b = b;
             u.head_kv = hk;
             u.token0 = r.token0;
             u.row_first = x * ROWS;
-            u.rows = static_cast<int>(min(static_cast<long long>(ROWS), r.rows - u.row_first));
+            u.rows = min(ROWS, r.rows - u.row_first);
             u.pos0 = r.pos0;
             const int first = r.pos0 + p.group_div.quotient(u.row_first);
             const int last = r.pos0 + p.group_div.quotient(u.row_first + u.rows - 1);
@@ -431,13 +439,11 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             u.key_lo = p.window > 0 ? min(max(first - p.window + 1, 0), u.key_hi) : 0;
             const int kb = u.key_lo / BK;
             const int nblk = max(1, (u.key_hi + BK - 1) / BK - kb);   // a unit that sees nothing has one (masked) block
-            // the blocks that start in the run: c + j w / nblk in [run_start, run_end)
-            const long long lo = run_start > c ? ((run_start - c) * nblk + w - 1) / w : 0;
-            const long long hi = ((run_end - c) * nblk + w - 1) / w;
-            const int j0 = static_cast<int>(min(lo, static_cast<long long>(nblk)));
-            const int j1 = static_cast<int>(min(hi, static_cast<long long>(nblk)));
+            // Block j starts at c + min(j >> spare, w - 1).  Those in [run_start, run_end):
+            const int j0 = run_start <= c ? 0 : min((run_start - c) << spare, nblk);
+            const int j1 = run_end >= c + w ? nblk : min((run_end - c) << spare, nblk);
             if (j1 <= j0) {
-              // a run inside a unit's one long block: no partial result of this unit
+              // inside a unit, but none of its blocks starts here: no partial result
               if (j0 > 0 && j0 < nblk) {
                 float* const l = parts_of(p.work, gridDim.x) +
                                  static_cast<size_t>(blockIdx.x) * 2 * part_floats(ROWS, D) + static_cast<size_t>(ROWS) * (D + 1);
@@ -450,11 +456,11 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             u.part = j0 > 0 ? 1 : j1 < nblk ? 2 : 0;
             if (u.part == 2) {
               // the run in which the unit's last block starts
-              cut.row_end = static_cast<int>(r.rows);
+              cut.row_end = r.rows;
               cut.row_first = u.row_first;
               cut.token0 = r.token0;
               cut.head_kv = hk;
-              cut.last = runs.of(c + (nblk - 1) * w / nblk);
+              cut.last = min(runs.of(c + min((nblk - 1) >> spare, w - 1)), runs.runs - 1);
             }
             emit(u);
           }
@@ -594,35 +600,48 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     constexpr int RPI = 32 / CPR;            // rows a warp's instruction covers
     const int w = warp - L::LOAD_WARP;
     int slot = 0, phase = 1;                 // of the ring: the first pass finds every slot empty
-    uint32_t pending[kLag] = {};             // barriers of the loads in flight, oldest last
-    int block = 0;                           // blocks of keys so far
+    uint32_t pending[kLag] = {};             // barriers of the copies in flight, oldest last (0: none)
+    int block = 0, raw_in = 0, raw_out = 0;  // blocks of keys so far; places in the ring of cached rows
+    int tiles = 0;                           // asked for so far
     bool ok = true;
     auto wait = [&](uint32_t b, int parity) {
       if (ok && !mbar_wait(b, parity & 1, abort, status)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
-    // a load of this thread has been issued; the one kLag before it has landed
+    auto arrive = [&](uint32_t b) {          // this warp's part is there
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b);
+    };
+    // Copies of this warp have been issued (or, with 0, none); those kLag before them have landed.
     auto issued = [&](uint32_t b) {
       cp_commit();
       cp_wait<kLag>();
-      if (pending[kLag - 1]) {
-        fence_proxy_async_smem();
-        mbar_arrive(pending[kLag - 1]);
-      }
+      if (pending[kLag - 1]) arrive(pending[kLag - 1]);
 #pragma unroll
       for (int i = kLag - 1; i > 0; --i) pending[i] = pending[i - 1];
       pending[0] = b;
     };
     auto drain = [&] {
       cp_wait<0>();
-      fence_proxy_async_smem();
 #pragma unroll
       for (int i = kLag - 1; i >= 0; --i) {
-        if (pending[i]) mbar_arrive(pending[i]);
+        if (pending[i]) arrive(pending[i]);
         pending[i] = 0;
       }
     };
+    auto next_slot = [&] {
+      ++tiles;
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    if (!E4M3 && p.box_rows > 0 && lane == 0) {
+      tma_prefetch_desc(&p.tm_k);
+      tma_prefetch_desc(&p.tm_v);
+    }
     for (int count = 0; ok; ++count) {
       const int ps = count % kPieces;
       if (!wait(bar(B_PIECE_FULL + ps), count / kPieces)) break;
@@ -638,132 +657,176 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         return pi <= last_page && lane < RPW ? table[pi] : -1;
       };
       int page = page_of(u.kb0);
-      // Q: rows of two tiles, 32 per warp and step
-      if (count > 0 && !wait(bar(B_Q_EMPTY), count - 1)) break;
-      const int q_rows = TILES == 2 && u.rows > 128 ? ROWS : 128;
-#pragma unroll 1
-      for (int r0 = w * 32; r0 < q_rows; r0 += 128) {
-        const int r = r0 + lane, row = u.row_first + r, tok = p.group_div.quotient(row);
-        const long long from = (u.token0 + tok) * p.q_row_stride + (u.head_kv * group + row - tok * group) * D;
-        const unsigned valid = __ballot_sync(0xffffffffu, r < u.rows);
-#pragma unroll 4
-        for (int i = 0; i < 32 / RPI; ++i) {
-          const int lr = i * RPI + lane / CPR, c = lane % CPR, rr = r0 + lr;
-          const long long off = __shfl_sync(0xffffffffu, from, lr);
-          const bool have = valid >> lr & 1;
-          const uint32_t dst = sbase + L::Q + (rr >> 7) * L::TILE_Q + (c >> 3) * L::CHUNK_Q + (rr & 127) * 128 +
-                               (((c & 7) ^ (rr & 7)) << 4);
-          if constexpr (!E4M3) {
-            cp_async16(dst, p.q + (have ? off + c * 8 : 0), have);
-          } else {
-            // as fp16, the row times a power of two that puts its largest value just below 2^15
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (have) v = ldg_stream(p.q + off + c * 8);
-            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(words[e] << 16 & 0x7FFF0000u, words[e] & 0x7FFF0000u));
-#pragma unroll
-            for (int o = CPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // exponent field of the factor: 127 + 14 - (top's - 127), kept a normal number
-            const int ex = min(max(268 - static_cast<int>(top >> 23), 1), 254);
-            const float f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
-            uint32_t out[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) out[e] = pack_f16x2(bf_lo(words[e]) * f, bf_hi(words[e]) * f);
-            st_shared_v4(dst, out[0], out[1], out[2], out[3]);
-            if (c == 0) q_scale[(count & 1) * ROWS + rr] = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-          }
-        }
-      }
-      if constexpr (E4M3) {
-        fence_proxy_async_smem();
-        mbar_arrive(bar(B_Q_FULL));
-      } else {
-        issued(bar(B_Q_FULL));
-      }
-      // blocks of keys
-      long long off[2] = {0, 0};     // of this lane's key; of the block before
-      unsigned good[2] = {0, 0};     // keys that are there
+      // Where this lane's key is (of the block at hand, and of the one before), and
+      // which keys of the warp are there.
+      long long off[2] = {0, 0};
+      int at_page[2] = {0, 0}, at_slot[2] = {0, 0};
+      unsigned good[2] = {0, 0};
       auto locate = [&](int kb) {
         off[1] = off[0];
         good[1] = good[0];
+        at_page[1] = at_page[0];
+        at_slot[1] = at_slot[0];
         const int key = kb * BK + w * RPW + lane;
         const bool in = lane < RPW && key >= u.key_lo && key < u.key_hi;
         const bool there = in && page >= 0 && page < p.kv.num_pages;
-        off[0] = there ? page * p.kv.page_stride + (key - p.page_div.quotient(key) * p.kv.page_size) * p.kv.slot_stride +
-                             u.head_kv * p.kv.head_stride
-                       : 0;
+        at_page[0] = page;
+        at_slot[0] = key - p.page_div.quotient(key) * p.kv.page_size;
+        off[0] = there ? page * p.kv.page_stride + at_slot[0] * p.kv.slot_stride + u.head_kv * p.kv.head_stride : 0;
         good[0] = __ballot_sync(0xffffffffu, there);
         const unsigned missing = __ballot_sync(0xffffffffu, in && !there);
         if (lane == 0) marks[(block % kMarks) * 4 + w] = missing;
         ++block;
         page = page_of(kb + 1);
       };
-      auto load = [&](const void* cache, int which) {
-        if (!wait(empty(slot), phase)) return;
-        const uint32_t tile = sbase + L::KV + slot * L::TILE_KV;
-        if constexpr (!E4M3) {
-          const uint16_t* const from = static_cast<const uint16_t*>(cache);
+      const bool two = TILES == 2 && u.rows > 128;
+      // Tile e of the piece in the order in which the products take them:
+      // K0 V0 K1 V1 ... for two tiles of rows, K0 K1 V0 K2 V1 ... for one.
+      auto is_key = [&](int e) { return two ? !(e & 1) : e == 0 || ((e & 1) && e + 1 < 2 * u.n); };
+      // of the block before the newest one: values of a single tile but the last
+      auto is_old = [&](int e) { return !two && e + 1 < 2 * u.n; };
+      int located = 0;
+
+      // Rows of Q, 32 per warp and step.
+      auto load_q = [&] {
+        if (count > 0 && !wait(bar(B_Q_EMPTY), count - 1)) return;
+        const int q_rows = two ? ROWS : 128;
+#pragma unroll 1
+        for (int r0 = w * 32; r0 < q_rows; r0 += 128) {
+          const int r = r0 + lane, row = u.row_first + r, tok = p.group_div.quotient(row);
+          const long long from = (u.token0 + tok) * p.q_row_stride + (u.head_kv * group + row - tok * group) * D;
+          const unsigned valid = __ballot_sync(0xffffffffu, r < u.rows);
 #pragma unroll 4
-          for (int i = 0; i < RPW / RPI; ++i) {
-            const int lr = i * RPI + lane / CPR, c = lane % CPR, rr = w * RPW + lr;
-            const long long o = __shfl_sync(0xffffffffu, off[which], lr);
-            const bool have = good[which] >> lr & 1;
-            cp_async16(tile + (c >> 3) * L::CHUNK_KV + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
-                       have ? from + o + c * 8 : p.q, have);
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int lr = i * RPI + lane / CPR, c = lane % CPR, rr = r0 + lr;
+            const long long o = __shfl_sync(0xffffffffu, from, lr);
+            const bool have = valid >> lr & 1;
+            const uint32_t dst = sbase + L::Q + (rr >> 7) * L::TILE_Q + (c >> 3) * L::CHUNK_Q + (rr & 127) * 128 +
+                                 (((c & 7) ^ (rr & 7)) << 4);
+            if constexpr (!E4M3) {
+              cp_async16(dst, p.q + (have ? o + c * 8 : 0), have);
+            } else {
+              // as fp16, the row times a power of two that puts its largest value just below 2^15
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (have) v = ldg_stream(p.q + o + c * 8);
+              const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+              uint32_t top = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = max(top, max(words[e] << 16 & 0x7FFF0000u, words[e] & 0x7FFF0000u));
+#pragma unroll
+              for (int x = CPR / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+              // exponent field of the factor: 127 + 14 - (top's - 127), kept a normal number
+              const int ex = min(max(268 - static_cast<int>(top >> 23), 1), 254);
+              const float f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+              uint32_t out[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) out[e] = pack_f16x2(bf_lo(words[e]) * f, bf_hi(words[e]) * f);
+              st_shared_v4(dst, out[0], out[1], out[2], out[3]);
+              if (c == 0) q_scale[(count & 1) * ROWS + rr] = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+            }
           }
-          issued(full(slot));
-        } else {
-          constexpr int CP8 = D / 16, RP8 = 32 / CP8, N8 = RPW / RP8;   // pieces per cached row, rows per step, steps
-          const uint8_t* const from = static_cast<const uint8_t*>(cache);
-          uint4 v[N8];
+        }
+        if constexpr (E4M3) arrive(bar(B_Q_FULL));
+        else issued(bar(B_Q_FULL));
+      };
+
+      if constexpr (!E4M3) {
+        load_q();
+        for (int e = 0; ok && e < 2 * u.n; ++e) {
+          const bool key = is_key(e);
+          if (key) locate(u.kb0 + located++);
+          const int old = !key && is_old(e);
+          if (!wait(empty(slot), phase)) break;
+          const uint32_t tile = sbase + L::KV + slot * L::TILE_KV;
+          const unsigned have_rows = old ? good[1] : good[0];
+          if (p.box_rows > 0 && have_rows == (RPW == 32 ? 0xffffffffu : (1u << RPW) - 1)) {
+            // boxes of box_rows keys, a lane each
+            if (lane == 0) mbar_arrive_expect_tx(full(slot), RPW * D * 2);
+            __syncwarp();
+            if (lane < RPW && (lane & (p.box_rows - 1)) == 0) {
+              const int pg = old ? at_page[1] : at_page[0], sl = old ? at_slot[1] : at_slot[0];
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(tile + c * L::CHUNK_KV + (w * RPW + lane) * 128, key ? &p.tm_k : &p.tm_v, c * 64, u.head_kv, sl,
+                            pg, full(slot));
+            }
+            __syncwarp();
+            issued(0);
+          } else {
+            const uint16_t* const from = static_cast<const uint16_t*>(key ? p.kv.k : p.kv.v);
+            const long long mine = old ? off[1] : off[0];
+#pragma unroll 4
+            for (int i = 0; i < RPW / RPI; ++i) {
+              const int lr = i * RPI + lane / CPR, c = lane % CPR, rr = w * RPW + lr;
+              const long long o = __shfl_sync(0xffffffffu, mine, lr);
+              const bool have = have_rows >> lr & 1;
+              cp_async16(tile + (c >> 3) * L::CHUNK_KV + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
+                         have ? from + o + c * 8 : p.q, have);
+            }
+            issued(full(slot));
+          }
+          next_slot();
+        }
+        drain();   // before the wait for the products that need them
+      } else {
+        // Every thread copies its own pieces to the ring of cached rows, NR - 1 tiles
+        // ahead, and later converts them.
+        constexpr int CP8 = D / 16, RP8 = 32 / CP8, N8 = RPW / RP8;   // pieces per cached row, rows per step, steps
+        const uint32_t raw = sbase + L::RAW + (w * 32 + lane) * 16;
+        int staged = 0;
+        auto stage = [&] {
+          if (staged < 2 * u.n) {
+            const int e = staged++;
+            const bool key = is_key(e);
+            if (key) locate(u.kb0 + located++);
+            const int old = !key && is_old(e);
+            const uint8_t* const from = static_cast<const uint8_t*>(key ? p.kv.k : p.kv.v);
+            const long long mine = old ? off[1] : off[0];
+            const unsigned have_rows = old ? good[1] : good[0];
+#pragma unroll
+            for (int i = 0; i < N8; ++i) {
+              const int lr = i * RP8 + lane / CP8, c = lane % CP8;
+              const long long o = __shfl_sync(0xffffffffu, mine, lr);
+              const bool have = have_rows >> lr & 1;
+              cp_async16(raw + raw_in * L::TILE_RAW + i * 2048, have ? static_cast<const void*>(from + o + c * 16) : p.q, have);
+            }
+            raw_in = raw_in + 1 == L::NR ? 0 : raw_in + 1;
+          }
+          cp_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < L::NR - 1; ++i) stage();
+        load_q();
+        for (int e = 0; ok && e < 2 * u.n; ++e) {
+          stage();
+          cp_wait<L::NR - 1>();
+          if (!wait(empty(slot), phase)) break;
+          const uint32_t tile = sbase + L::KV + slot * L::TILE_KV;
 #pragma unroll
           for (int i = 0; i < N8; ++i) {
-            const int lr = i * RP8 + lane / CP8, c = lane % CP8;
-            const long long o = __shfl_sync(0xffffffffu, off[which], lr);
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (good[which] >> lr & 1) v[i] = ldg_stream(reinterpret_cast<const uint16_t*>(from + o + c * 16));
-          }
-#pragma unroll
-          for (int i = 0; i < N8; ++i) {
-            const int lr = i * RP8 + lane / CP8, c = 2 * (lane % CP8), rr = w * RPW + lr;
-            const uint2 a = e4m3x4_f16(v[i].x), b = e4m3x4_f16(v[i].y), e = e4m3x4_f16(v[i].z), f = e4m3x4_f16(v[i].w);
+            const int c = 2 * (lane % CP8), rr = w * RPW + i * RP8 + lane / CP8;
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(raw + raw_out * L::TILE_RAW + i * 2048)
+                         : "memory");
+            const uint2 a = e4m3x4_f16(v.x), b = e4m3x4_f16(v.y), f = e4m3x4_f16(v.z), g = e4m3x4_f16(v.w);
             const uint32_t row = tile + (c >> 3) * L::CHUNK_KV + rr * 128;
             st_shared_v4(row + (((c & 7) ^ (rr & 7)) << 4), a.x, a.y, b.x, b.y);
-            st_shared_v4(row + ((((c & 7) + 1) ^ (rr & 7)) << 4), e.x, e.y, f.x, f.y);
+            st_shared_v4(row + ((((c & 7) + 1) ^ (rr & 7)) << 4), f.x, f.y, g.x, g.y);
           }
-          fence_proxy_async_smem();
-          mbar_arrive(full(slot));
-        }
-        if (++slot == NS) {
-          slot = 0;
-          phase ^= 1;
-        }
-      };
-      const bool two = TILES == 2 && u.rows > 128;
-      locate(u.kb0);
-      load(p.kv.k, 0);
-      for (int j = 0; ok && j < u.n; ++j) {
-        if (two) {
-          load(p.kv.v, 0);
-          if (ok && j + 1 < u.n) {
-            locate(u.kb0 + j + 1);
-            load(p.kv.k, 0);
-          }
-        } else {
-          if (j + 1 < u.n) {
-            locate(u.kb0 + j + 1);
-            load(p.kv.k, 0);
-            if (ok) load(p.kv.v, 1);
-          } else {
-            load(p.kv.v, 0);
-          }
+          raw_out = raw_out + 1 == L::NR ? 0 : raw_out + 1;
+          arrive(full(slot));
+          next_slot();
         }
       }
-      if constexpr (!E4M3) drain();   // before the wait for the products that need them
     }
-    if constexpr (!E4M3) cp_wait<0>();
+    cp_wait<0>();
+    if (!ok) {   // after an abort, what has been asked for lands before the block ends
+      volatile int no_abort = 0;
+      for (int i = max(0, tiles - NS); i < tiles; ++i)
+        mbar_wait(full(i % NS), (i / NS) & 1, &no_abort, status, 1000000000ull);
+    }
   } else if (warp < 4 * TILES) {
     // ------------------------------------------------------------ softmax and output
     setmaxnreg_to<L::REG_SOFTMAX, L::REG_LAUNCH>();
@@ -892,7 +955,8 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         l_run += (sum0.x + sum0.y) + (sum1.x + sum1.y);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar(B_P_READY + which));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_P_READY + which));
       }
       if (!ok) break;
       // ------------------------------------------------------------ output
@@ -946,7 +1010,8 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         }
       }
       tc_fence_before();
-      mbar_arrive(bar(B_O_FREE + t));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_O_FREE + t));
     }
   } else {
     setmaxnreg_to<L::REG_OTHER, L::REG_LAUNCH>();   // two warps of the last four have nothing to do
@@ -1016,9 +1081,44 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const ExtendParams p
   if (p.lse && warp == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
+// The cache as [pages, page_size, heads, d], boxes of rows slots by 64 values of a head.
+bool make_page_map(CUtensorMap* m, const PagedCache& c, const void* base, int rows) {
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return false;
+  // strides of dimensions of one are never used, but have to be valid ones
+  auto stride = [](long long elements, int n) { return static_cast<cuuint64_t>(n > 1 ? 2 * elements : 16); };
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.heads_kv),
+                              static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[3] = {stride(c.head_stride, c.heads_kv), stride(c.slot_stride, c.page_size),
+                                 stride(c.page_stride, c.num_pages)};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1}, steps[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool E4M3>
-cudaError_t launch_dim(const ExtendParams& p, const Device& dev, cudaStream_t s) {
+cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
   using L = Layout<D, E4M3>;
+  using S = Shape<D>;
+  const long long group = p.heads / p.kv.heads_kv;
+  const long long keys = static_cast<long long>(p.max_pages) * p.kv.page_size + p.num_tokens;   // as the costs have it
+  p.tile_keys16 = static_cast<int>(S::kRows * 16 / group);
+  p.tile_tokens = static_cast<int>(S::kRows / group + 1);
+  // A cost for a block of keys, or for as many as keep the sum of any lengths below 2^30.
+  const long long units = (p.num_tokens * group / S::kRows + p.batch) * p.kv.heads_kv;
+  p.cost_shift = S::kKeys == 128 ? 7 : 6;
+  while (units >= (1ll << 30) / ((keys >> p.cost_shift) + 8)) ++p.cost_shift;
+  // Boxes of the largest power of two that divides a page, up to a warp's keys.
+  p.box_rows = 0;
+  const long long most = std::max({p.kv.page_stride, p.kv.slot_stride, p.kv.head_stride});
+  if (!E4M3 && p.kv.page_size % 8 == 0 && p.max_pages > 0 && most < (1ll << 39)) {
+    int rows = 8;
+    while (rows < S::kKeys / 4 && p.kv.page_size % (2 * rows) == 0) rows *= 2;
+    if (!make_page_map(&p.tm_k, p.kv, p.kv.k, rows) || !make_page_map(&p.tm_v, p.kv, p.kv.v, rows))
+      return cudaErrorInvalidValue;
+    p.box_rows = rows;
+  }
   static std::atomic<unsigned long long> done{0}, join_done{0};
   auto* const kernel = extend_kernel<D, E4M3>;
   cudaError_t e = prepare_once(reinterpret_cast<const void*>(kernel), L::BYTES, dev.id, done);

@@ -1,6 +1,7 @@
 // What a call of fa_extend launches, from its sizes, and its workspace.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -10,6 +11,8 @@
 namespace fa {
 
 struct ExtendParams {
+  CUtensorMap tm_k;         // with box_rows
+  CUtensorMap tm_v;
   PagedCache kv;
   const uint16_t* q;        // [num_tokens, heads, d], rows q_row_stride elements apart
   long long q_row_stride;
@@ -28,6 +31,11 @@ struct ExtendParams {
   int heads;
   int window;
   float scale;
+  // set by launch_extend, like the tensor maps:
+  int box_rows;             // keys of a TMA box, 0: none
+  int cost_shift;           // keys that cost 1, log 2
+  int tile_keys16;          // rows of a tile / group, in 16ths
+  int tile_tokens;          // tokens that a tile's rows belong to, at most
 };
 
 namespace extend {

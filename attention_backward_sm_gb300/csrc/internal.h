@@ -108,6 +108,10 @@ inline cudaError_t set_smem_once(const void* func, int bytes, std::atomic<unsign
   return e;
 }
 
+// The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or
+// nullptr.
+void* tensor_map_encoder();
+
 // Records a message for fa_last_error() on the calling thread and returns code.
 int set_last_error(int code, const char* fmt, ...);
 

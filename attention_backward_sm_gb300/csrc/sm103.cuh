@@ -138,6 +138,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* desc, int 
       : "memory");
 }
 
+// 4-D tiled load, as tma_load_2d.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* desc, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // 2-D tiled reduce-add (fp32 add in the L2) of one shared-memory box into
 // global memory, tracked by the issuing thread's bulk async-group.
 __device__ __forceinline__ void tma_reduce_add_2d(const void* desc, uint32_t src, int x, int y) {
