@@ -29,8 +29,8 @@
 // its run with one scan over the requests.
 //
 // Warps: per tile of 128 rows four for the softmax and the output, then four
-// that load, one that issues the products, one
-// that walks along the run and tells the others what is next.
+// that load keys and values, one that issues the products, one that walks along
+// the run and tells the others what is next, two that load queries.
 //   Two tiles: the products of one run while the softmax works on the other,
 //   in the order P_A V, S_A (of the next block), P_B V, S_B.
 //   One tile (at most 128 rows): two score buffers, S of the next block is
@@ -92,11 +92,13 @@ struct Piece {
 };
 
 // S_FULL and P_READY: of tile 0 (and the first score buffer of a single tile), of
-// tile 1, and of a single tile's second buffer.  Waits are by parity, so whoever
-// waits on a barrier has to see each of its phases: tile 1's warps take no part in
-// units of one tile.
-enum { B_Q_FULL = 0, B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 3, B_O_DONE = B_P_READY + 3, B_O_FREE = B_O_DONE + 2,
-       B_PIECE_FULL = B_O_FREE + 2, B_PIECE_EMPTY = B_PIECE_FULL + kPieces, B_TEARDOWN = B_PIECE_EMPTY + kPieces,
+// tile 1, and of a single tile's second buffer.  Waits are by parity, so a wait for
+// a phase must neither come before the phase ahead of it has ended nor after the
+// one behind it: tile 1's warps, which take no part in units of one tile, have
+// barriers of their own, and so has the end of a piece (O_LAST; O_DONE is of every
+// block).
+enum { B_Q_FULL = 0, B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 3, B_O_DONE = B_P_READY + 3, B_O_LAST = B_O_DONE + 2,
+       B_O_FREE = B_O_LAST + 2, B_PIECE_FULL = B_O_FREE + 2, B_PIECE_EMPTY = B_PIECE_FULL + kPieces, B_TEARDOWN = B_PIECE_EMPTY + kPieces,
        B_FULL, NUM_FIXED = B_FULL };
 
 template <int D, bool E4M3>
@@ -120,8 +122,7 @@ struct Layout {
   static constexpr uint32_t MARKS = (BARS + NUM_BARS * 8 + 15) / 16 * 16;    // [kMarks][4] words
   static constexpr uint32_t PIECES = MARKS + kMarks * 16;
   static constexpr uint32_t QSCALE = PIECES + kPieces * sizeof(Piece);       // [2 pieces][rows] (8-bit caches)
-  static constexpr uint32_t SCAN = QSCALE + (E4M3 ? 2 * S::kRows * 4 : 0);       // [warps] sums, then Found
-  static constexpr uint32_t MISC = SCAN + 16 * 4 + 16;
+  static constexpr uint32_t MISC = QSCALE + (E4M3 ? 2 * S::kRows * 4 : 0);
   static constexpr uint32_t BYTES = MISC + 16;
   static constexpr uint32_t COL_O = 2 * BK;              // after two score buffers
   static constexpr int WARPS = 4 * S::kTiles + 8;
@@ -129,6 +130,7 @@ struct Layout {
   static constexpr int LOAD_WARP = 4 * S::kTiles;
   static constexpr int MMA_WARP = LOAD_WARP + 4;
   static constexpr int WALK_WARP = MMA_WARP + 1;
+  static constexpr int Q_WARP = WALK_WARP + 1;           // two
   // registers: 65536 / THREADS at launch
   static constexpr uint32_t REG_LAUNCH = 65536 / THREADS / 8 * 8;
   static constexpr uint32_t REG_SOFTMAX = S::kTiles == 2 ? 184 : 208;
@@ -258,12 +260,6 @@ struct Runs {
   }
 };
 
-// What a block knows of its run after the scan.
-struct Found {
-  int at;   // the request's place on the line
-  int b;
-};
-
 // Workspace: [runs] cuts, then the partial results.
 __device__ __forceinline__ float* parts_of(void* work, int runs) {
   return reinterpret_cast<float*>(static_cast<Cut*>(work) + runs);
@@ -285,8 +281,6 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
   Piece* const pieces = reinterpret_cast<Piece*>(smem + L::PIECES);
   uint32_t* const marks = reinterpret_cast<uint32_t*>(smem + L::MARKS);
   float* const q_scale = reinterpret_cast<float*>(smem + L::QSCALE);
-  int* const scan = reinterpret_cast<int*>(smem + L::SCAN);
-  Found* const found = reinterpret_cast<Found*>(scan + 16);
   const uint32_t bars = sbase + L::BARS;
   auto bar = [&](int i) { return bars + 8u * i; };
   auto full = [&](int s) { return bars + 8u * (B_FULL + s); };
@@ -298,7 +292,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
   }
   if (threadIdx.x == 0) {
     *abort = 0;
-    mbar_init(bar(B_Q_FULL), 4);   // a lane of every warp, here and below
+    mbar_init(bar(B_Q_FULL), 2);   // a lane of every warp, here and below
     mbar_init(bar(B_Q_EMPTY), 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(bar(B_S_FULL + i), 1);
@@ -306,11 +300,12 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_O_DONE + i), 1);
+      mbar_init(bar(B_O_LAST + i), 1);
       mbar_init(bar(B_O_FREE + i), 4);
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(bar(B_PIECE_FULL + i), 1);
-      mbar_init(bar(B_PIECE_EMPTY + i), 4 * TILES + 5);   // a lane of every other warp
+      mbar_init(bar(B_PIECE_EMPTY + i), 4 * TILES + 7);   // all warps but the walker
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(full(i), 4);
@@ -323,60 +318,12 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_wait();
-  pdl_launch();
-
-  // The line's length, and the request that this block's run starts in.
-  const int per = (p.batch + L::THREADS - 1) / L::THREADS;
-  const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
-  int mine = 0;
-#pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine += Request<D>(p, b, group).cost * p.kv.heads_kv;
-  int upto = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += x;
-  }
-  if (lane == 31) scan[warp] = upto;
-  // Rows that belong to no request.
-  {
-    const int first = min(max(p.cu_new[p.batch], 0), p.num_tokens);
-    const long long pieces16 = static_cast<long long>(p.num_tokens - first) * p.heads * (D / 8);
-    for (long long i = static_cast<long long>(blockIdx.x) * L::THREADS + threadIdx.x; i < pieces16;
-         i += static_cast<long long>(gridDim.x) * L::THREADS) {
-      const long long row = static_cast<long long>(first) * p.heads + i / (D / 8);
-      *reinterpret_cast<uint4*>(p.o + row * D + i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
-      if (p.lse && i % (D / 8) == 0) p.lse[row] = -INFINITY;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < L::WARPS; ++w) {
-    if (w < warp) upto += scan[w];
-    total += scan[w];
-  }
-  const Runs runs(total, gridDim.x);
-  const int run_start = static_cast<int>(blockIdx.x) < runs.runs ? runs.start(blockIdx.x) : total;
-  const int run_end = run_start < total ? runs.start(blockIdx.x + 1) : total;
-  if (run_start < total && run_start >= upto - mine && run_start < upto) {
-    int at = upto - mine;
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      const int cost = b1 - b0 == 1 ? mine : Request<D>(p, b, group).cost * p.kv.heads_kv;
-      if (run_start < at + cost) {
-        found->at = at;
-        found->b = b;
-        break;
-      }
-      at += cost;
-    }
-  }
-  __syncthreads();
+  pdl_wait();
+  pdl_launch();
 
   if (warp == L::WALK_WARP) {
     // ------------------------------------------------------------ walker
@@ -397,8 +344,37 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       __syncwarp();
       ++count;
     };
+    // The line's length, then the request that this block's run starts in: 32
+    // requests at a time.
+    const int heads_kv = p.kv.heads_kv;
+    int total = 0, mine = 0;   // mine: of this lane's request among the last 32
+#pragma unroll 1
+    for (int b = lane; b < p.batch; b += 32) total += mine = Request<D>(p, b, group).cost * heads_kv;
+    total = __reduce_add_sync(0xffffffffu, total);
+    const Runs runs(total, gridDim.x);
+    const int run_start = static_cast<int>(blockIdx.x) < runs.runs ? runs.start(blockIdx.x) : total;
+    const int run_end = run_start < total ? runs.start(blockIdx.x + 1) : total;
     if (run_start < total) {
-      int b = found->b, at = found->at;
+      int b = 0, at = 0;   // the request and its place on the line
+#pragma unroll 1
+      for (int b32 = 0; b32 < p.batch; b32 += 32) {
+        if (p.batch > 32) mine = b32 + lane < p.batch ? Request<D>(p, b32 + lane, group).cost * heads_kv : 0;
+        else if (lane >= p.batch) mine = 0;
+        int upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, at + upto > run_start);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          b = b32 + l;
+          at += __shfl_sync(0xffffffffu, upto - mine, l);
+          break;
+        }
+        at += __shfl_sync(0xffffffffu, upto, 31);
+      }
       while (ok && b < p.batch && at < run_end) {
         const Request<D> r(p, b, group);
         if (r.cost == 0) {
@@ -418,7 +394,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           }
         }
         bool in_run = true;
-        for (; ok && in_run && hk < p.kv.heads_kv; ++hk, x = 0) {
+        for (; ok && in_run && hk < heads_kv; ++hk, x = 0) {
           for (; ok && x < r.tiles; ++x) {
             const int c = at + hk * r.cost + r.before(p, x);
             if (c >= run_end) {
@@ -465,7 +441,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             emit(u);
           }
         }
-        at += r.cost * p.kv.heads_kv;
+        at += r.cost * heads_kv;
         ++b;
       }
     }
@@ -541,6 +517,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
               issue_pv(t, t, v_slot, j > 0);
               if (t == 1) mma_commit(empty(v_slot));
               mma_commit(bar(B_O_DONE + t));
+              if (j + 1 == n) mma_commit(bar(B_O_LAST + t));
               if (j + 1 < n) {
                 issue_s(t, t, slot);
                 mma_commit(bar(B_S_FULL + t));
@@ -580,6 +557,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             issue_pv(0, buf, slot, j > 0);
             mma_commit(empty(slot));
             mma_commit(bar(B_O_DONE));
+            if (j + 1 == n) mma_commit(bar(B_O_LAST));
           }
           __syncwarp();
           next_slot();
@@ -687,51 +665,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       auto is_old = [&](int e) { return !two && e + 1 < 2 * u.n; };
       int located = 0;
 
-      // Rows of Q, 32 per warp and step.
-      auto load_q = [&] {
-        if (count > 0 && !wait(bar(B_Q_EMPTY), count - 1)) return;
-        const int q_rows = two ? ROWS : 128;
-#pragma unroll 1
-        for (int r0 = w * 32; r0 < q_rows; r0 += 128) {
-          const int r = r0 + lane, row = u.row_first + r, tok = p.group_div.quotient(row);
-          const long long from = (u.token0 + tok) * p.q_row_stride + (u.head_kv * group + row - tok * group) * D;
-          const unsigned valid = __ballot_sync(0xffffffffu, r < u.rows);
-#pragma unroll 4
-          for (int i = 0; i < 32 / RPI; ++i) {
-            const int lr = i * RPI + lane / CPR, c = lane % CPR, rr = r0 + lr;
-            const long long o = __shfl_sync(0xffffffffu, from, lr);
-            const bool have = valid >> lr & 1;
-            const uint32_t dst = sbase + L::Q + (rr >> 7) * L::TILE_Q + (c >> 3) * L::CHUNK_Q + (rr & 127) * 128 +
-                                 (((c & 7) ^ (rr & 7)) << 4);
-            if constexpr (!E4M3) {
-              cp_async16(dst, p.q + (have ? o + c * 8 : 0), have);
-            } else {
-              // as fp16, the row times a power of two that puts its largest value just below 2^15
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (have) v = ldg_stream(p.q + o + c * 8);
-              const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-              uint32_t top = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) top = max(top, max(words[e] << 16 & 0x7FFF0000u, words[e] & 0x7FFF0000u));
-#pragma unroll
-              for (int x = CPR / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-              // exponent field of the factor: 127 + 14 - (top's - 127), kept a normal number
-              const int ex = min(max(268 - static_cast<int>(top >> 23), 1), 254);
-              const float f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
-              uint32_t out[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) out[e] = pack_f16x2(bf_lo(words[e]) * f, bf_hi(words[e]) * f);
-              st_shared_v4(dst, out[0], out[1], out[2], out[3]);
-              if (c == 0) q_scale[(count & 1) * ROWS + rr] = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-            }
-          }
-        }
-        if constexpr (E4M3) arrive(bar(B_Q_FULL));
-        else issued(bar(B_Q_FULL));
-      };
-
       if constexpr (!E4M3) {
-        load_q();
         for (int e = 0; ok && e < 2 * u.n; ++e) {
           const bool key = is_key(e);
           if (key) locate(u.kb0 + located++);
@@ -739,16 +673,19 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           if (!wait(empty(slot), phase)) break;
           const uint32_t tile = sbase + L::KV + slot * L::TILE_KV;
           const unsigned have_rows = old ? good[1] : good[0];
-          if (p.box_rows > 0 && have_rows == (RPW == 32 ? 0xffffffffu : (1u << RPW) - 1)) {
-            // boxes of box_rows keys, a lane each
+          if (p.box_rows > 0 && (key || have_rows == (RPW == 32 ? 0xffffffffu : (1u << RPW) - 1))) {
+            // Boxes of box_rows keys, a lane each.  Scores of keys that a row does not
+            // see are replaced, so it does not matter what is read for them (pages
+            // that are none read as zeros); their values have to be zeros.
             if (lane == 0) mbar_arrive_expect_tx(full(slot), RPW * D * 2);
             __syncwarp();
             if (lane < RPW && (lane & (p.box_rows - 1)) == 0) {
               const int pg = old ? at_page[1] : at_page[0], sl = old ? at_slot[1] : at_slot[0];
+              const int in = pg >= 0 && pg < p.kv.num_pages ? pg : p.kv.num_pages;
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
                 tma_load_4d(tile + c * L::CHUNK_KV + (w * RPW + lane) * 128, key ? &p.tm_k : &p.tm_v, c * 64, u.head_kv, sl,
-                            pg, full(slot));
+                            in, full(slot));
             }
             __syncwarp();
             issued(0);
@@ -767,7 +704,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           }
           next_slot();
         }
-        drain();   // before the wait for the products that need them
+        drain();   // the products to come wait for them, and these loads for the products
       } else {
         // Every thread copies its own pieces to the ring of cached rows, NR - 1 tiles
         // ahead, and later converts them.
@@ -796,7 +733,6 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         };
 #pragma unroll 1
         for (int i = 0; i < L::NR - 1; ++i) stage();
-        load_q();
         for (int e = 0; ok && e < 2 * u.n; ++e) {
           stage();
           cp_wait<L::NR - 1>();
@@ -834,7 +770,21 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     const int r = (warp & 3) * 32 + lane;                 // row of the tile (TMEM lane)
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lane_addr + L::COL_O + t * D;
-    int s_used = 0, s_odd = 0, o_used = 0, block = 0;   // phases seen of S_FULL, of its third, of O_DONE; blocks
+    constexpr float kShift = E4M3 ? kF16Shift : 0.f;
+    // phases seen of S_FULL, of its third, of O_DONE, of O_LAST; blocks
+    int s_used = 0, s_odd = 0, o_used = 0, done = 0, block = 0;
+    // Rows that belong to no request, while there is nothing else to do.
+    {
+      const int first = min(max(p.cu_new[p.batch], 0), p.num_tokens);
+      const long long n16 = static_cast<long long>(p.num_tokens - first) * p.heads * (D / 8);
+#pragma unroll 1
+      for (long long i = static_cast<long long>(blockIdx.x) * (128 * TILES) + threadIdx.x; i < n16;
+           i += static_cast<long long>(gridDim.x) * (128 * TILES)) {
+        const long long row = static_cast<long long>(first) * p.heads + i / (D / 8);
+        *reinterpret_cast<uint4*>(p.o + row * D + i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+        if (p.lse && i % (D / 8) == 0) p.lse[row] = -INFINITY;
+      }
+    }
     bool ok = true;
     for (int count = 0; ok; ++count) {
       const int ps = count % kPieces;
@@ -857,8 +807,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       const int hi = valid ? pos + 1 : 0x7fffffff;
       const int lo = valid && p.window > 0 ? max(pos - p.window + 1, 0) : 0;
       const float k_scale = E4M3 && p.kv.k_scale ? p.kv.k_scale[u.head_kv] : 1.f;
-      const bool negative = p.scale * k_scale < 0.f;
-      float sl2 = 0.f;   // > 0, set once Q is there
+      float sl2 = 0.f;   // set once Q is there
       float m_used = -INFINITY, l_run = 0.f;
       for (int j = 0; j < u.n; ++j, ++block) {
         const bool odd = !two && (j & 1);
@@ -869,56 +818,72 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         if (odd) ++s_odd;
         else ++s_used;
         tc_fence_after();
-        float x[BK];
-#pragma unroll
-        for (int c = 0; c < BK / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(t_s + c * 32, v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(v[e]);
-        }
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < BK; ++e) asm volatile("" : "+f"(x[e]));   // no use before the wait
         if (j == 0) {
-          sl2 = fabsf(p.scale * k_scale) * kLog2e;
+          sl2 = p.scale * k_scale * kLog2e;
           if constexpr (E4M3) sl2 *= q_scale[(count & 1) * ROWS + t * 128 + r];
-          sl2 = fmaxf(sl2, 0x1p-126f);   // a masked score times it stays -inf
-        }
-        if (negative) {
-#pragma unroll
-          for (int e = 0; e < BK; ++e) x[e] = -x[e];
         }
         const int key0 = (u.kb0 + j) * BK;
         const int c_lo = max(lo - key0, 0), c_hi = hi == 0x7fffffff ? BK : min(max(hi - key0, 0), BK);
-        if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < BK)) {
-          const unsigned span = c_hi > c_lo ? c_hi - c_lo : 0;
-#pragma unroll
-          for (int e = 0; e < BK; ++e) x[e] = static_cast<unsigned>(e - c_lo) < span ? x[e] : -INFINITY;
-        }
         const uint4 missing = *reinterpret_cast<const uint4*>(marks + (block % kMarks) * 4);
-        if (missing.x | missing.y | missing.z | missing.w) {
-          const uint32_t words[4] = {missing.x, missing.y, missing.z, missing.w};
+        const bool masked = __any_sync(0xffffffffu, c_lo > 0 || c_hi < BK) || (missing.x | missing.y | missing.z | missing.w);
+        // P = 2^a, a = x sl2 - ref, with the reference of the blocks before: the
+        // largest a says whether that will do.  Where it does not (always in a row's
+        // first block), the reference moves and P is worked out again.  So the
+        // exponentials need not wait for the maximum: 4 chunks of 2048 tokens
+        // @SOFT0@ us with the maximum first, @SOFT1@ so.
+        uint32_t pk[BK / 2];
+        float sum = 0.f;
+        const float m_old = m_used;
+        auto pass = [&](auto mask) -> float {
+          const float ref = (m_used == -INFINITY ? 0.f : m_used) - kShift;
+          const float2 mul = make_float2(sl2, sl2), sub = make_float2(-ref, -ref);
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+          float top0 = -INFINITY, top1 = -INFINITY;
+          uint32_t v[2][32];
+          tmem_ld32(t_s, v[0]);
 #pragma unroll
-          for (int e = 0; e < BK; ++e)
-            if (words[e / (BK / 4)] >> (e % (BK / 4)) & 1) x[e] = -INFINITY;
-        }
-        float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+          for (int c = 0; c < BK / 32; ++c) {
+            tmem_ld_wait();
 #pragma unroll
-        for (int e = 4; e < BK; e += 4) {
-          mx0 = fmaxf(mx0, x[e]);
-          mx1 = fmaxf(mx1, x[e + 1]);
-          mx2 = fmaxf(mx2, x[e + 2]);
-          mx3 = fmaxf(mx3, x[e + 3]);
+            for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(v[c & 1][e]));   // no use before the wait
+            if (c + 1 < BK / 32) tmem_ld32(t_s + (c + 1) * 32, v[(c + 1) & 1]);
+            [[maybe_unused]] uint32_t seen = 0;
+            if constexpr (decltype(mask)::value) {
+              // columns [c_lo, c_hi) but the missing ones, of these 32
+              const int a = min(max(c_lo - 32 * c, 0), 32), b = min(max(c_hi - 32 * c, 0), 32);
+              seen = a < b ? (0xffffffffu >> (32 - (b - a))) << a : 0u;
+              const uint32_t words[4] = {missing.x, missing.y, missing.z, missing.w};
+              seen &= ~(BK == 128 ? words[c] : words[(2 * c) & 3] | words[(2 * c + 1) & 3] << 16);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 a = fma2(make_float2(__uint_as_float(v[c & 1][2 * e]), __uint_as_float(v[c & 1][2 * e + 1])), mul, sub);
+              if constexpr (decltype(mask)::value) {
+                a.x = seen >> (2 * e) & 1 ? a.x : -INFINITY;
+                a.y = seen >> (2 * e + 1) & 1 ? a.y : -INFINITY;
+              }
+              if (e & 1) top1 = fmaxf(fmaxf(a.x, a.y), top1);
+              else top0 = fmaxf(fmaxf(a.x, a.y), top0);
+              a.x = ex2_approx(a.x);
+              a.y = ex2_approx(a.y);
+              if (e & 1) sum1 = add2(sum1, a);
+              else sum0 = add2(sum0, a);
+              pk[c * 16 + e] = E4M3 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
+            }
+          }
+          sum = (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          return fmaxf(top0, top1);
+        };
+        // (a reference in the 2^30s is off by more than the slack: a few rounds)
+        for (int round = 0; round < 4; ++round) {
+          const float top = (masked ? pass(std::true_type()) : pass(std::false_type())) - kShift;
+          const bool move = top > (m_used == -INFINITY ? -INFINITY : kSlack);
+          if (!__any_sync(0xffffffffu, move)) break;
+          if (move) m_used = (m_used == -INFINITY ? 0.f : m_used) + top;
         }
-        const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2);
-        const bool grow = m_new > m_used + kSlack;   // also for the first visible key
-        float alpha = 1.f;
-        if (grow) {
-          alpha = ex2_approx(m_used - m_new);        // 0 while m_used = -inf
-          l_run *= alpha;
-          m_used = m_new;
-        }
+        const bool grow = m_used != m_old;
+        const float alpha = grow ? ex2_approx(m_old - m_used) : 1.f;   // 0 from -inf
+        l_run = fmaf(l_run, alpha, sum);
         if (j > 0 && __any_sync(0xffffffffu, grow)) {
           if (!mbar_wait(bar(B_O_DONE + t), (o_used + j - 1) & 1, abort, status)) ok = false;
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -932,27 +897,14 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
             tmem_st16(t_o + c * 16, v);
           }
-          tmem_st_wait();
         }
-        // P = 2^(x sl2 - m), masked scores give 0 (any finite reference does until a key is seen)
-        const float ref = (m_used == -INFINITY ? 0.f : m_used) - (E4M3 ? kF16Shift : 0.f);
-        const float2 mul = make_float2(sl2, sl2), sub = make_float2(-ref, -ref);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
         for (int c = 0; c < BK / 32; ++c) {
-          uint32_t pk[16];
+          uint32_t part[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 a = fma2(make_float2(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), mul, sub);
-            a.x = ex2_approx(a.x);
-            a.y = ex2_approx(a.y);
-            if (e & 1) sum1 = add2(sum1, a);
-            else sum0 = add2(sum0, a);
-            pk[e] = E4M3 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
-          }
-          tmem_st16(t_s + c * 16, pk);
+          for (int e = 0; e < 16; ++e) part[e] = pk[c * 16 + e];
+          tmem_st16(t_s + c * 16, part);
         }
-        l_run += (sum0.x + sum0.y) + (sum1.x + sum1.y);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -960,13 +912,11 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       }
       if (!ok) break;
       // ------------------------------------------------------------ output
-      // (S of the last block says nothing of the P V before it: two phases to see)
-      if (u.n > 1 && !mbar_wait(bar(B_O_DONE + t), (o_used + u.n - 2) & 1, abort, status)) ok = false;
-      if (ok && !mbar_wait(bar(B_O_DONE + t), (o_used + u.n - 1) & 1, abort, status)) ok = false;
+      if (!mbar_wait(bar(B_O_LAST + t), done++ & 1, abort, status)) ok = false;
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       o_used += u.n;
       tc_fence_after();
-      const float top = m_used - (E4M3 ? kF16Shift : 0.f);   // what l_run and O are relative to
+      const float top = m_used - kShift;   // what l_run and O are relative to
       if (u.part == 0) {
         const float v_scale = E4M3 && p.kv.v_scale ? p.kv.v_scale[u.head_kv] : 1.f;
         const float inv = l_run == 0.f ? 0.f : v_scale / l_run;
@@ -1013,8 +963,90 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_O_FREE + t));
     }
-  } else {
-    setmaxnreg_to<L::REG_OTHER, L::REG_LAUNCH>();   // two warps of the last four have nothing to do
+  } else if (warp >= L::Q_WARP) {
+    // ------------------------------------------------------------ queries
+    setmaxnreg_to<L::REG_OTHER, L::REG_LAUNCH>();
+    constexpr int CPR = D / 8;               // 16-byte pieces per row
+    constexpr int RPI = 32 / CPR;            // rows a warp's instruction covers
+    const int w = warp - L::Q_WARP;
+    bool ok = true;
+    int asked = 0;
+    for (int count = 0; ok; ++count) {
+      const int ps = count % kPieces;
+      ok = mbar_wait(bar(B_PIECE_FULL + ps), (count / kPieces) & 1, abort, status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const Piece u = pieces[ps];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_PIECE_EMPTY + ps));
+      if (u.n == 0) break;
+      const int tiles = TILES == 2 && u.rows > 128 ? 2 : 1;
+      if (count > 0) {
+        ok = mbar_wait(bar(B_Q_EMPTY), (count - 1) & 1, abort, status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      }
+      if (!E4M3 && p.q_boxes) {
+        // 128 rows are whole tokens: a box of the group's heads for 128 / group tokens
+        if (lane == 0) {
+          if (w == 0) {
+            mbar_arrive_expect_tx(bar(B_Q_FULL), tiles * L::TILE_Q);
+            for (int t = 0; t < tiles; ++t)
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(sbase + L::Q + t * L::TILE_Q + c * L::CHUNK_Q, &p.tm_q, c * 64, u.head_kv * group,
+                            u.token0 + p.group_div.quotient(u.row_first + t * 128), bar(B_Q_FULL));
+          } else {
+            mbar_arrive(bar(B_Q_FULL));
+          }
+        }
+        __syncwarp();
+        asked = count + 1;
+        continue;
+      }
+#pragma unroll 1
+      for (int r0 = w * 32; r0 < tiles * 128; r0 += 64) {
+        const int r = r0 + lane, row = u.row_first + r, tok = p.group_div.quotient(row);
+        const long long from = (u.token0 + tok) * p.q_row_stride + (u.head_kv * group + row - tok * group) * D;
+        const unsigned valid = __ballot_sync(0xffffffffu, r < u.rows);
+#pragma unroll 4
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int lr = i * RPI + lane / CPR, c = lane % CPR, rr = r0 + lr;
+          const long long o = __shfl_sync(0xffffffffu, from, lr);
+          const bool have = valid >> lr & 1;
+          const uint32_t dst = sbase + L::Q + (rr >> 7) * L::TILE_Q + (c >> 3) * L::CHUNK_Q + (rr & 127) * 128 +
+                               (((c & 7) ^ (rr & 7)) << 4);
+          if constexpr (!E4M3) {
+            cp_async16(dst, p.q + (have ? o + c * 8 : 0), have);
+          } else {
+            // as fp16, the row times a power of two that puts its largest value just below 2^15
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (have) v = ldg_stream(p.q + o + c * 8);
+            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(words[e] << 16 & 0x7FFF0000u, words[e] & 0x7FFF0000u));
+#pragma unroll
+            for (int x = CPR / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+            // exponent field of the factor: 127 + 14 - (top's - 127), kept a normal number
+            const int ex = min(max(268 - static_cast<int>(top >> 23), 1), 254);
+            const float f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+            uint32_t out[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[e] = pack_f16x2(bf_lo(words[e]) * f, bf_hi(words[e]) * f);
+            st_shared_v4(dst, out[0], out[1], out[2], out[3]);
+            if (c == 0) q_scale[(count & 1) * ROWS + rr] = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+          }
+        }
+      }
+      cp_commit();
+      cp_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_Q_FULL));
+    }
+    if (!ok && asked > 0) {   // after an abort, what has been asked for lands before the block ends
+      volatile int no_abort = 0;
+      mbar_wait(bar(B_Q_FULL), (asked - 1) & 1, &no_abort, status, 1000000000ull);
+    }
   }
 
   tc_fence_before();
@@ -1097,6 +1129,20 @@ bool make_page_map(CUtensorMap* m, const PagedCache& c, const void* base, int ro
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as [tokens, heads, d], boxes of 128 rows by 64 values.
+bool make_query_map(CUtensorMap* m, const ExtendParams& p, int group) {
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.kv.head_dim), static_cast<cuuint64_t>(p.heads),
+                              static_cast<cuuint64_t>(p.num_tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * p.kv.head_dim),
+                                 static_cast<cuuint64_t>(2 * (p.num_tokens > 1 ? p.q_row_stride : p.heads * p.kv.head_dim))};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group)}, steps[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool E4M3>
 cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
   using L = Layout<D, E4M3>;
@@ -1118,6 +1164,12 @@ cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
     if (!make_page_map(&p.tm_k, p.kv, p.kv.k, rows) || !make_page_map(&p.tm_v, p.kv, p.kv.v, rows))
       return cudaErrorInvalidValue;
     p.box_rows = rows;
+  }
+  // Queries in boxes where 128 rows are whole tokens.
+  p.q_boxes = 0;
+  if (!E4M3 && group <= 128 && (group & (group - 1)) == 0 && p.q_row_stride < (1ll << 39)) {
+    if (!make_query_map(&p.tm_q, p, static_cast<int>(group))) return cudaErrorInvalidValue;
+    p.q_boxes = 1;
   }
   static std::atomic<unsigned long long> done{0}, join_done{0};
   auto* const kernel = extend_kernel<D, E4M3>;

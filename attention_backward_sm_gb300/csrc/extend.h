@@ -13,6 +13,7 @@ namespace fa {
 struct ExtendParams {
   CUtensorMap tm_k;         // with box_rows
   CUtensorMap tm_v;
+  CUtensorMap tm_q;         // with q_boxes
   PagedCache kv;
   const uint16_t* q;        // [num_tokens, heads, d], rows q_row_stride elements apart
   long long q_row_stride;
@@ -33,6 +34,7 @@ struct ExtendParams {
   float scale;
   // set by launch_extend, like the tensor maps:
   int box_rows;             // keys of a TMA box, 0: none
+  int q_boxes;
   int cost_shift;           // keys that cost 1, log 2
   int tile_keys16;          // rows of a tile / group, in 16ths
   int tile_tokens;          // tokens that a tile's rows belong to, at most

@@ -138,7 +138,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* desc, int 
       : "memory");
 }
 
-// 4-D tiled load, as tma_load_2d.
+// 3-D and 4-D tiled loads, as tma_load_2d.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* desc, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* desc, int x, int y, int z, int w, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
