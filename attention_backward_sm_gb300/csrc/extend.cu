@@ -65,9 +65,9 @@ namespace {
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// A row's reference for the exponents moves only when a score exceeds it by
-// more than this (units of log 2), so O is rescaled rarely.
-constexpr float kSlack = 8.f;
+// A row's reference for the exponents moves where the weights of half a block add
+// up to more than kMostSum, or one of them exceeds 2^kMostLog.  bf16 weights and
+// the fp32 sums of 2^31 of them times values have room up to 2^127.
 // fp16 weights (8-bit caches) are stored times 2^7: at most 2^15, and the
 // smallest step 2^-24 counts 2^-31 beside the row's largest weight.
 constexpr float kF16Shift = 7.f;
@@ -97,7 +97,7 @@ struct Piece {
 // one behind it: tile 1's warps, which take no part in units of one tile, have
 // barriers of their own, and so has the end of a piece (O_LAST; O_DONE is of every
 // block).
-enum { B_Q_FULL = 0, B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 3, B_O_DONE = B_P_READY + 3, B_O_LAST = B_O_DONE + 2,
+enum { B_Q_FULL = 0, B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 3, B_P_HALF = B_P_READY + 3, B_O_DONE = B_P_HALF + 2, B_O_LAST = B_O_DONE + 2,
        B_O_FREE = B_O_LAST + 2, B_PIECE_FULL = B_O_FREE + 2, B_PIECE_EMPTY = B_PIECE_FULL + kPieces, B_TEARDOWN = B_PIECE_EMPTY + kPieces,
        B_FULL, NUM_FIXED = B_FULL };
 
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       mbar_init(bar(B_P_READY + i), 4);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_P_HALF + i), 4);
       mbar_init(bar(B_O_DONE + i), 1);
       mbar_init(bar(B_O_LAST + i), 1);
       mbar_init(bar(B_O_FREE + i), 4);
@@ -454,7 +455,8 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     constexpr uint32_t ID_S = E4M3 ? idesc_f16(128, BK, 0) : idesc_bf16(128, BK, 0, 0);
     constexpr uint32_t ID_O = E4M3 ? idesc_f16(128, D, 1) : idesc_bf16(128, D, 0, 1);
     int slot = 0, phase = 0;                    // of the ring of tiles
-    int used[2] = {0, 0}, used_odd = 0;         // P_READY phases
+    int used[2] = {0, 0};                       // phases of P_HALF
+    int used_all[2] = {0, 0}, used_odd = 0;     // of P_READY
     int freed[2] = {0, 0};                      // pieces of a tile
     auto next_slot = [&] {
       if (++slot == NS) {
@@ -468,10 +470,10 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       for (int k = 0; k < D / 16; ++k)
         mma_ss(tmem + buf * BK, a0 + step_kmajor(k, L::CHUNK_Q), b0 + step_kmajor(k, L::CHUNK_KV), ID_S, k > 0);
     };
-    auto issue_pv = [&](int t, int buf, int at, bool more) {
+    auto issue_pv = [&](int t, int buf, int at, int k0, int k1, bool more) {   // 16 keys each
       const uint64_t b0 = desc_mnmajor(sbase + L::KV + at * L::TILE_KV, L::CHUNK_KV);
 #pragma unroll 4
-      for (int k = 0; k < BK / 16; ++k)
+      for (int k = k0; k < k1; ++k)
         mma_ts(tmem + L::COL_O + t * D, tmem + buf * BK + k * 8, b0 + step_mnmajor(k), ID_O, more | (k > 0));
     };
     bool ok = true;
@@ -508,13 +510,18 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           const int v_slot = slot;
           next_slot();
           for (int t = 0; t < 2; ++t) {
-            if (!wait(bar(B_P_READY + t), used[t])) break;
+            if (!wait(bar(B_P_HALF + t), used[t])) break;
             if (j == 0 && freed[t] > 0 && !wait(bar(B_O_FREE + t), freed[t] - 1)) break;
+            tc_fence_after();
+            if (elect_one()) issue_pv(t, t, v_slot, 0, BK / 32, j > 0);
+            __syncwarp();
             if (t == 0 && j + 1 < n && !wait(full(slot), phase)) break;
+            if (!wait(bar(B_P_READY + t), used_all[t])) break;
             ++used[t];
+            ++used_all[t];
             tc_fence_after();
             if (elect_one()) {
-              issue_pv(t, t, v_slot, j > 0);
+              issue_pv(t, t, v_slot, BK / 32, BK / 16, true);
               if (t == 1) mma_commit(empty(v_slot));
               mma_commit(bar(B_O_DONE + t));
               if (j + 1 == n) mma_commit(bar(B_O_LAST + t));
@@ -548,13 +555,13 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             next_slot();
           }
           const int buf = j & 1;
-          if (!wait(full(slot), phase) || !wait(bar(B_P_READY + 2 * buf), buf ? used_odd : used[0])) break;
+          if (!wait(full(slot), phase) || !wait(bar(B_P_READY + 2 * buf), buf ? used_odd : used_all[0])) break;
           if (j == 0 && freed[0] > 0 && !wait(bar(B_O_FREE), freed[0] - 1)) break;
           if (buf) ++used_odd;
-          else ++used[0];
+          else ++used_all[0];
           tc_fence_after();
           if (elect_one()) {
-            issue_pv(0, buf, slot, j > 0);
+            issue_pv(0, buf, slot, 0, BK / 16, j > 0);
             mma_commit(empty(slot));
             mma_commit(bar(B_O_DONE));
             if (j + 1 == n) mma_commit(bar(B_O_LAST));
@@ -770,7 +777,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     const int r = (warp & 3) * 32 + lane;                 // row of the tile (TMEM lane)
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lane_addr + L::COL_O + t * D;
-    constexpr float kShift = E4M3 ? kF16Shift : 0.f;
+    constexpr float kShift = E4M3 ? kF16Shift : 0.f, kMostLog = E4M3 ? 14.5f : 60.f, kMostSum = E4M3 ? 0x1p15f : 0x1p60f;
     // phases seen of S_FULL, of its third, of O_DONE, of O_LAST; blocks
     int s_used = 0, s_odd = 0, o_used = 0, done = 0, block = 0;
     // Rows that belong to no request, while there is nothing else to do.
@@ -803,9 +810,11 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       const int row = u.row_first + t * 128 + r, tok = p.group_div.quotient(row);
       const bool valid = t * 128 + r < u.rows;
       const int pos = u.pos0 + tok;
-      // visible keys [lo, hi); rows past the unit's are computed like any and not written
+      // Visible keys [lo, hi), and of the warp's rows the largest lo and the smallest
+      // hi; rows past the unit's are computed like any and not written.
       const int hi = valid ? pos + 1 : 0x7fffffff;
       const int lo = valid && p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+      const int lo_most = __reduce_max_sync(0xffffffffu, lo), hi_least = __reduce_min_sync(0xffffffffu, hi);
       const float k_scale = E4M3 && p.kv.k_scale ? p.kv.k_scale[u.head_kv] : 1.f;
       float sl2 = 0.f;   // set once Q is there
       float m_used = -INFINITY, l_run = 0.f;
@@ -818,72 +827,96 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         if (odd) ++s_odd;
         else ++s_used;
         tc_fence_after();
+        float x[BK];
+#pragma unroll
+        for (int c = 0; c < BK / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_s + c * 32, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(v[e]);
+        }
         if (j == 0) {
           sl2 = p.scale * k_scale * kLog2e;
           if constexpr (E4M3) sl2 *= q_scale[(count & 1) * ROWS + t * 128 + r];
         }
-        const int key0 = (u.kb0 + j) * BK;
-        const int c_lo = max(lo - key0, 0), c_hi = hi == 0x7fffffff ? BK : min(max(hi - key0, 0), BK);
         const uint4 missing = *reinterpret_cast<const uint4*>(marks + (block % kMarks) * 4);
-        const bool masked = __any_sync(0xffffffffu, c_lo > 0 || c_hi < BK) || (missing.x | missing.y | missing.z | missing.w);
-        // P = 2^a, a = x sl2 - ref, with the reference of the blocks before: the
-        // largest a says whether that will do.  Where it does not (always in a row's
-        // first block), the reference moves and P is worked out again.  So the
-        // exponentials need not wait for the maximum: 4 chunks of 2048 tokens
-        // @SOFT0@ us with the maximum first, @SOFT1@ so.
-        uint32_t pk[BK / 2];
-        float sum = 0.f;
-        const float m_old = m_used;
-        auto pass = [&](auto mask) -> float {
+        const int key0 = (u.kb0 + j) * BK;
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < BK; ++e) asm volatile("" : "+f"(x[e]));   // no use before the wait
+        // a = x sl2 - ref; P = 2^a
+        {
           const float ref = (m_used == -INFINITY ? 0.f : m_used) - kShift;
           const float2 mul = make_float2(sl2, sl2), sub = make_float2(-ref, -ref);
-          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-          float top0 = -INFINITY, top1 = -INFINITY;
-          uint32_t v[2][32];
-          tmem_ld32(t_s, v[0]);
+#pragma unroll
+          for (int e = 0; e < BK; e += 2) {
+            const float2 a = fma2(make_float2(x[e], x[e + 1]), mul, sub);
+            x[e] = a.x;
+            x[e + 1] = a.y;
+          }
+        }
+        if (key0 < lo_most || key0 + BK > hi_least || (missing.x | missing.y | missing.z | missing.w)) {
+          const int c_lo = max(lo - key0, 0), c_hi = min(max(hi - key0, 0), BK);
+          const uint32_t words[4] = {missing.x, missing.y, missing.z, missing.w};
 #pragma unroll
           for (int c = 0; c < BK / 32; ++c) {
-            tmem_ld_wait();
+            // columns [c_lo, c_hi) but the missing ones, of these 32
+            const int from = min(max(c_lo - 32 * c, 0), 32), to = min(max(c_hi - 32 * c, 0), 32);
+            uint32_t seen = from < to ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+            seen &= ~(BK == 128 ? words[c] : words[(2 * c) & 3] | words[(2 * c + 1) & 3] << 16);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(v[c & 1][e]));   // no use before the wait
-            if (c + 1 < BK / 32) tmem_ld32(t_s + (c + 1) * 32, v[(c + 1) & 1]);
-            [[maybe_unused]] uint32_t seen = 0;
-            if constexpr (decltype(mask)::value) {
-              // columns [c_lo, c_hi) but the missing ones, of these 32
-              const int a = min(max(c_lo - 32 * c, 0), 32), b = min(max(c_hi - 32 * c, 0), 32);
-              seen = a < b ? (0xffffffffu >> (32 - (b - a))) << a : 0u;
-              const uint32_t words[4] = {missing.x, missing.y, missing.z, missing.w};
-              seen &= ~(BK == 128 ? words[c] : words[(2 * c) & 3] | words[(2 * c + 1) & 3] << 16);
-            }
+            for (int e = 0; e < 32; ++e) x[c * 32 + e] = seen >> e & 1 ? x[c * 32 + e] : -INFINITY;
+          }
+        }
+        // The reference is that of the blocks before: floating-point weights may be
+        // far above 1.  It moves only where a row has none yet and where its weights
+        // would come near the end of their type's range: then, rarely, the largest a
+        // is looked for and the first half is worked out again.  So the exponentials
+        // wait for no maximum.
+        float sum = 0.f;
+        const float m_old = m_used;
+        bool fresh = valid && m_used == -INFINITY;
+        auto half = [&](auto h) {   // weights of half the block, into the place of the scores
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+          for (int c = decltype(h)::value * BK / 64; c < (decltype(h)::value + 1) * BK / 64; ++c) {
+            uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float2 a = fma2(make_float2(__uint_as_float(v[c & 1][2 * e]), __uint_as_float(v[c & 1][2 * e + 1])), mul, sub);
-              if constexpr (decltype(mask)::value) {
-                a.x = seen >> (2 * e) & 1 ? a.x : -INFINITY;
-                a.y = seen >> (2 * e + 1) & 1 ? a.y : -INFINITY;
-              }
-              if (e & 1) top1 = fmaxf(fmaxf(a.x, a.y), top1);
-              else top0 = fmaxf(fmaxf(a.x, a.y), top0);
-              a.x = ex2_approx(a.x);
-              a.y = ex2_approx(a.y);
-              if (e & 1) sum1 = add2(sum1, a);
-              else sum0 = add2(sum0, a);
-              pk[c * 16 + e] = E4M3 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
+              const float2 w = make_float2(ex2_approx(x[c * 32 + 2 * e]), ex2_approx(x[c * 32 + 2 * e + 1]));
+              if (e & 1) sum1 = add2(sum1, w);
+              else sum0 = add2(sum0, w);
+              pk[e] = E4M3 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
             }
+            tmem_st16(t_s + c * 16, pk);
           }
-          sum = (sum0.x + sum0.y) + (sum1.x + sum1.y);
-          return fmaxf(top0, top1);
+          return (sum0.x + sum0.y) + (sum1.x + sum1.y);
         };
-        // (a reference in the 2^30s is off by more than the slack: a few rounds)
-        for (int round = 0; round < 4; ++round) {
-          const float top = (masked ? pass(std::true_type()) : pass(std::false_type())) - kShift;
-          const bool move = top > (m_used == -INFINITY ? -INFINITY : kSlack);
-          if (!__any_sync(0xffffffffu, move)) break;
-          if (move) m_used = (m_used == -INFINITY ? 0.f : m_used) + top;
+        float rest0 = x[BK / 2], rest1 = x[BK / 2 + 1];   // largest a of the second half
+#pragma unroll
+        for (int e = BK / 2 + 2; e < BK; e += 4) {
+          rest0 = fmaxf(fmaxf(x[e], x[e + 1]), rest0);
+          if (e + 2 < BK) rest1 = fmaxf(fmaxf(x[e + 2], x[e + 3]), rest1);
+        }
+        for (int round = 0;; ++round) {
+          sum = half(std::integral_constant<int, 0>());
+          const bool move = valid && (fresh || !(sum <= kMostSum) || fmaxf(rest0, rest1) > kMostLog);
+          // (a reference in the 2^30s is off by more than the range allows for: a few rounds)
+          if (!__any_sync(0xffffffffu, move) || round == 4) break;
+          float top = x[0];
+#pragma unroll
+          for (int e = 1; e < BK - 1; e += 2) top = fmaxf(fmaxf(x[e], x[e + 1]), top);
+          top = fmaxf(top, x[BK - 1]) - kShift;
+          const float by = move && top > -INFINITY ? top : 0.f;
+          if (move && top > -INFINITY) m_used = (m_used == -INFINITY ? 0.f : m_used) + top;
+#pragma unroll
+          for (int e = 0; e < BK; ++e) x[e] -= by;
+          rest0 -= by;
+          rest1 -= by;
+          fresh = false;
         }
         const bool grow = m_used != m_old;
         const float alpha = grow ? ex2_approx(m_old - m_used) : 1.f;   // 0 from -inf
-        l_run = fmaf(l_run, alpha, sum);
         if (j > 0 && __any_sync(0xffffffffu, grow)) {
           if (!mbar_wait(bar(B_O_DONE + t), (o_used + j - 1) & 1, abort, status)) ok = false;
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -898,13 +931,13 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             tmem_st16(t_o + c * 16, v);
           }
         }
-#pragma unroll
-        for (int c = 0; c < BK / 32; ++c) {
-          uint32_t part[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) part[e] = pk[c * 16 + e];
-          tmem_st16(t_s + c * 16, part);
+        if (two) {   // the products of the first half's keys can start
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_P_HALF + t));
         }
+        l_run = fmaf(l_run, alpha, sum + half(std::integral_constant<int, 1>()));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
