@@ -99,7 +99,7 @@ struct Piece {
 // block).
 enum { B_Q_FULL = 0, B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 3, B_P_HALF = B_P_READY + 3, B_O_DONE = B_P_HALF + 2, B_O_LAST = B_O_DONE + 2,
        B_O_FREE = B_O_LAST + 2, B_PIECE_FULL = B_O_FREE + 2, B_PIECE_EMPTY = B_PIECE_FULL + kPieces, B_TEARDOWN = B_PIECE_EMPTY + kPieces,
-       B_FULL, NUM_FIXED = B_FULL };
+       B_FULL };
 
 template <int D, bool E4M3>
 struct Layout {
@@ -118,7 +118,7 @@ struct Layout {
   static constexpr uint32_t KV = S::kTiles * TILE_Q;
   static constexpr uint32_t RAW = KV + NS * TILE_KV;
   static constexpr uint32_t BARS = RAW + NR * TILE_RAW;
-  static constexpr int NUM_BARS = B_FULL + 2 * NS;
+  static constexpr int NUM_BARS = B_FULL + 2 * NS + 4 * NR;
   static constexpr uint32_t MARKS = (BARS + NUM_BARS * 8 + 15) / 16 * 16;    // [kMarks][4] words
   static constexpr uint32_t PIECES = MARKS + kMarks * 16;
   static constexpr uint32_t QSCALE = PIECES + kPieces * sizeof(Piece);       // [2 pieces][rows] (8-bit caches)
@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
   auto bar = [&](int i) { return bars + 8u * i; };
   auto full = [&](int s) { return bars + 8u * (B_FULL + s); };
   auto empty = [&](int s) { return bars + 8u * (B_FULL + NS + s); };
+  [[maybe_unused]] auto landed = [&](int s, int w) { return bars + 8u * (B_FULL + 2 * NS + 4 * s + w); };   // cached rows of a warp
 
   if (sbase & 1023) {
     if (threadIdx.x == 0) atomicCAS(status, 0, 99);
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       mbar_init(full(i), 4);
       mbar_init(empty(i), 1);
     }
+    for (int i = 0; i < 4 * L::NR; ++i) mbar_init(landed(0, i), 1);
     mbar_init(bar(B_TEARDOWN), 1);
     mbar_init_fence();
   }
@@ -588,6 +590,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     uint32_t pending[kLag] = {};             // barriers of the copies in flight, oldest last (0: none)
     int block = 0, raw_in = 0, raw_out = 0;  // blocks of keys so far; places in the ring of cached rows
     int tiles = 0;                           // asked for so far
+    [[maybe_unused]] int raw_turns = 0;      // tiles of cached rows taken so far
     bool ok = true;
     auto wait = [&](uint32_t b, int parity) {
       if (ok && !mbar_wait(b, parity & 1, abort, status)) ok = false;
@@ -623,7 +626,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         phase ^= 1;
       }
     };
-    if (!E4M3 && p.box_rows > 0 && lane == 0) {
+    if (p.box_rows > 0 && lane == 0) {
       tma_prefetch_desc(&p.tm_k);
       tma_prefetch_desc(&p.tm_v);
     }
@@ -713,46 +716,74 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         }
         drain();   // the products to come wait for them, and these loads for the products
       } else {
-        // Every thread copies its own pieces to the ring of cached rows, NR - 1 tiles
-        // ahead, and later converts them.
+        // Every warp brings its own rows to the ring of cached rows, NR - 1 tiles
+        // ahead (in boxes, or each thread the pieces that it later converts), and
+        // converts them.
         constexpr int CP8 = D / 16, RP8 = 32 / CP8, N8 = RPW / RP8;   // pieces per cached row, rows per step, steps
-        const uint32_t raw = sbase + L::RAW + (w * 32 + lane) * 16;
+        const bool boxes = p.box_rows > 0;
+        const uint32_t raw = sbase + L::RAW + w * (RPW * D);
         int staged = 0;
+        unsigned rows_in[L::NR];   // which rows of the tiles on their way are there, newest first
         auto stage = [&] {
+          unsigned have_rows = 0;
           if (staged < 2 * u.n) {
             const int e = staged++;
             const bool key = is_key(e);
             if (key) locate(u.kb0 + located++);
             const int old = !key && is_old(e);
-            const uint8_t* const from = static_cast<const uint8_t*>(key ? p.kv.k : p.kv.v);
-            const long long mine = old ? off[1] : off[0];
-            const unsigned have_rows = old ? good[1] : good[0];
+            have_rows = old ? good[1] : good[0];
+            const uint32_t to = raw + raw_in * L::TILE_RAW;
+            if (boxes) {
+              if (lane == 0) mbar_arrive_expect_tx(landed(raw_in, w), RPW * D);
+              __syncwarp();
+              if (lane < RPW && (lane & (p.box_rows - 1)) == 0) {
+                const int pg = old ? at_page[1] : at_page[0], sl = old ? at_slot[1] : at_slot[0];
+                const int in = pg >= 0 && pg < p.kv.num_pages ? pg : p.kv.num_pages;
+                tma_load_4d(to + lane * D, key ? &p.tm_k : &p.tm_v, 0, u.head_kv, sl, in, landed(raw_in, w));
+              }
+              __syncwarp();
+            } else {
+              const uint8_t* const from = static_cast<const uint8_t*>(key ? p.kv.k : p.kv.v);
+              const long long mine = old ? off[1] : off[0];
 #pragma unroll
-            for (int i = 0; i < N8; ++i) {
-              const int lr = i * RP8 + lane / CP8, c = lane % CP8;
-              const long long o = __shfl_sync(0xffffffffu, mine, lr);
-              const bool have = have_rows >> lr & 1;
-              cp_async16(raw + raw_in * L::TILE_RAW + i * 2048, have ? static_cast<const void*>(from + o + c * 16) : p.q, have);
+              for (int i = 0; i < N8; ++i) {
+                const int lr = i * RP8 + lane / CP8, c = lane % CP8;
+                const long long o = __shfl_sync(0xffffffffu, mine, lr);
+                const bool have = have_rows >> lr & 1;
+                cp_async16(to + (i * 32 + lane) * 16, have ? static_cast<const void*>(from + o + c * 16) : p.q, have);
+              }
             }
             raw_in = raw_in + 1 == L::NR ? 0 : raw_in + 1;
           }
           cp_commit();
+#pragma unroll
+          for (int i = L::NR - 1; i > 0; --i) rows_in[i] = rows_in[i - 1];
+          rows_in[0] = have_rows;
         };
 #pragma unroll 1
         for (int i = 0; i < L::NR - 1; ++i) stage();
         for (int e = 0; ok && e < 2 * u.n; ++e) {
           stage();
-          cp_wait<L::NR - 1>();
+          if (boxes) {
+            if (!wait(landed(raw_out, w), raw_turns / L::NR)) break;
+          } else {
+            cp_wait<L::NR - 1>();
+          }
+          ++raw_turns;
           if (!wait(empty(slot), phase)) break;
           const uint32_t tile = sbase + L::KV + slot * L::TILE_KV;
+          // Values that no row sees have to be zeros (whatever is in their slots).
+          const unsigned have_rows = is_key(e) ? 0xffffffffu : rows_in[L::NR - 1];
+          const bool all = (RPW == 32 ? ~have_rows : ~have_rows & ((1u << RPW) - 1)) == 0;
 #pragma unroll
           for (int i = 0; i < N8; ++i) {
-            const int c = 2 * (lane % CP8), rr = w * RPW + i * RP8 + lane / CP8;
+            const int lr = i * RP8 + lane / CP8, c = 2 * (lane % CP8), rr = w * RPW + lr;
             uint4 v;
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(raw + raw_out * L::TILE_RAW + i * 2048)
+                         : "r"(raw + raw_out * L::TILE_RAW + (i * 32 + lane) * 16)
                          : "memory");
+            if (!all && !(have_rows >> lr & 1)) v = make_uint4(0, 0, 0, 0);
             const uint2 a = e4m3x4_f16(v.x), b = e4m3x4_f16(v.y), f = e4m3x4_f16(v.z), g = e4m3x4_f16(v.w);
             const uint32_t row = tile + (c >> 3) * L::CHUNK_KV + rr * 128;
             st_shared_v4(row + (((c & 7) ^ (rr & 7)) << 4), a.x, a.y, b.x, b.y);
@@ -767,8 +798,14 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     cp_wait<0>();
     if (!ok) {   // after an abort, what has been asked for lands before the block ends
       volatile int no_abort = 0;
-      for (int i = max(0, tiles - NS); i < tiles; ++i)
-        mbar_wait(full(i % NS), (i / NS) & 1, &no_abort, status, 1000000000ull);
+      if constexpr (E4M3) {
+        if (p.box_rows > 0)
+          for (int i = raw_turns; i < raw_turns + L::NR; ++i)
+            mbar_wait(landed(i % L::NR, w), (i / L::NR) & 1, &no_abort, status, 100000000ull);
+      } else {
+        for (int i = max(0, tiles - NS); i < tiles; ++i)
+          mbar_wait(full(i % NS), (i / NS) & 1, &no_abort, status, 100000000ull);
+      }
     }
   } else if (warp < 4 * TILES) {
     // ------------------------------------------------------------ softmax and output
@@ -1078,7 +1115,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     }
     if (!ok && asked > 0) {   // after an abort, what has been asked for lands before the block ends
       volatile int no_abort = 0;
-      mbar_wait(bar(B_Q_FULL), (asked - 1) & 1, &no_abort, status, 1000000000ull);
+      mbar_wait(bar(B_Q_FULL), (asked - 1) & 1, &no_abort, status, 100000000ull);
     }
   }
 
@@ -1108,57 +1145,75 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const ExtendParams p
     return parts + (static_cast<size_t>(run + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(ROWS, D);
   };
   const int n = cut.last - run + 1;
-  float top = -INFINITY;
-  if (valid)
-    for (int i = 0; i < n; ++i) {
-      const float* const q = part(i) + static_cast<size_t>(ROWS) * D + at;
-      if (q[ROWS] != 0.f) top = fmaxf(top, q[0]);
+  // kAhead partial results in flight, relative to a running maximum
+  constexpr int kAhead = D == 256 ? 2 : 4, COLS = D / 4 / WARPS;
+  float top = -INFINITY, sum = 0.f;
+  float4 acc[COLS];
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; valid && i0 < n; i0 += kAhead) {
+    float m[kAhead], l[kAhead];
+    float4 v[kAhead][COLS];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const float* const q = part(min(i0 + a, n - 1));
+      m[a] = q[static_cast<size_t>(ROWS) * D + at];
+      l[a] = i0 + a < n ? q[static_cast<size_t>(ROWS) * (D + 1) + at] : 0.f;
+#pragma unroll
+      for (int c = 0; c < COLS; ++c)
+        v[a][c] = *reinterpret_cast<const float4*>(q + (static_cast<size_t>(c * WARPS + warp) * ROWS + at) * 4);
     }
-  float sum = 0.f;
-  float4 acc[D / 4 / WARPS];
+    float up = top;
 #pragma unroll
-  for (int c = 0; c < D / 4 / WARPS; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (valid)
-    for (int i = 0; i < n; ++i) {
-      const float* const q = part(i);
-      const float l = q[static_cast<size_t>(ROWS) * (D + 1) + at];
-      if (l == 0.f) continue;
-      const float f = ex2_approx(q[static_cast<size_t>(ROWS) * D + at] - top);
-      sum = fmaf(f, l, sum);
+    for (int a = 0; a < kAhead; ++a)
+      if (l[a] != 0.f) up = fmaxf(up, m[a]);
+    const float keep = up == top ? 1.f : ex2_approx(top - up);
+    top = up;
+    sum *= keep;
 #pragma unroll
-      for (int c = 0; c < D / 4 / WARPS; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(q + (static_cast<size_t>(c * WARPS + warp) * ROWS + at) * 4);
-        acc[c].x = fmaf(f, v.x, acc[c].x);
-        acc[c].y = fmaf(f, v.y, acc[c].y);
-        acc[c].z = fmaf(f, v.z, acc[c].z);
-        acc[c].w = fmaf(f, v.w, acc[c].w);
+    for (int c = 0; c < COLS; ++c) acc[c].x *= keep, acc[c].y *= keep, acc[c].z *= keep, acc[c].w *= keep;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (l[a] == 0.f) continue;   // nothing seen: what is there does not count
+      const float f = ex2_approx(m[a] - top);
+      sum = fmaf(f, l[a], sum);
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        acc[c].x = fmaf(f, v[a][c].x, acc[c].x);
+        acc[c].y = fmaf(f, v[a][c].y, acc[c].y);
+        acc[c].z = fmaf(f, v[a][c].z, acc[c].z);
+        acc[c].w = fmaf(f, v[a][c].w, acc[c].w);
       }
     }
+  }
   if (!valid) return;
   const int group = p.heads / p.kv.heads_kv, row = cut.row_first + at, tok = p.group_div.quotient(row);
   const long long out = static_cast<long long>(cut.token0 + tok) * p.heads + cut.head_kv * group + (row - tok * group);
   const float v_scale = p.kv.v_scale ? p.kv.v_scale[cut.head_kv] : 1.f;
   const float inv = sum == 0.f ? 0.f : v_scale / sum;
 #pragma unroll
-  for (int c = 0; c < D / 4 / WARPS; ++c)
+  for (int c = 0; c < COLS; ++c)
     *reinterpret_cast<uint2*>(p.o + out * D + (c * WARPS + warp) * 4) =
         make_uint2(pack_bf16x2(acc[c].x * inv, acc[c].y * inv), pack_bf16x2(acc[c].z * inv, acc[c].w * inv));
   if (p.lse && warp == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-// The cache as [pages, page_size, heads, d], boxes of rows slots by 64 values of a head.
+// The cache as [pages, page_size, heads, d], boxes of rows slots by 64 values of a
+// head, swizzled as the products read them, or (8-bit caches) by the whole head.
 bool make_page_map(CUtensorMap* m, const PagedCache& c, const void* base, int rows) {
   const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
   if (!enc) return false;
   // strides of dimensions of one are never used, but have to be valid ones
-  auto stride = [](long long elements, int n) { return static_cast<cuuint64_t>(n > 1 ? 2 * elements : 16); };
+  auto stride = [&](long long elements, int n) { return static_cast<cuuint64_t>(n > 1 ? (c.e4m3 ? 1 : 2) * elements : 16); };
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.heads_kv),
                               static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.num_pages)};
   const cuuint64_t strides[3] = {stride(c.head_stride, c.heads_kv), stride(c.slot_stride, c.page_size),
                                  stride(c.page_stride, c.num_pages)};
-  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1}, steps[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, steps,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.e4m3 ? c.head_dim : 64), 1, static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return enc(m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+             dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             c.e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1191,7 +1246,7 @@ cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
   // Boxes of the largest power of two that divides a page, up to a warp's keys.
   p.box_rows = 0;
   const long long most = std::max({p.kv.page_stride, p.kv.slot_stride, p.kv.head_stride});
-  if (!E4M3 && p.kv.page_size % 8 == 0 && p.max_pages > 0 && most < (1ll << 39)) {
+  if (p.kv.page_size % 8 == 0 && p.max_pages > 0 && most < (1ll << 39)) {
     int rows = 8;
     while (rows < S::kKeys / 4 && p.kv.page_size % (2 * rows) == 0) rows *= 2;
     if (!make_page_map(&p.tm_k, p.kv, p.kv.k, rows) || !make_page_map(&p.tm_v, p.kv, p.kv.v, rows))
