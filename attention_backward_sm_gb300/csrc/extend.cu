@@ -118,28 +118,30 @@ struct Layout {
   static constexpr uint32_t KV = S::kTiles * TILE_Q;
   static constexpr uint32_t RAW = KV + NS * TILE_KV;
   static constexpr uint32_t BARS = RAW + NR * TILE_RAW;
-  static constexpr int NUM_BARS = B_FULL + 2 * NS + 4 * NR;
-  static constexpr uint32_t MARKS = (BARS + NUM_BARS * 8 + 15) / 16 * 16;    // [kMarks][4] words
+  static constexpr int NUM_BARS = B_FULL + 2 * NS + 2 * NR;
+  static constexpr uint32_t MARKS = (BARS + NUM_BARS * 8 + 15) / 16 * 16;    // [kMarks][4] words, a bit per key
   static constexpr uint32_t PIECES = MARKS + kMarks * 16;
   static constexpr uint32_t QSCALE = PIECES + kPieces * sizeof(Piece);       // [2 pieces][rows] (8-bit caches)
   static constexpr uint32_t MISC = QSCALE + (E4M3 ? 2 * S::kRows * 4 : 0);
   static constexpr uint32_t BYTES = MISC + 16;
   static constexpr uint32_t COL_O = 2 * BK;              // after two score buffers
-  static constexpr int WARPS = 4 * S::kTiles + 8;
+  static constexpr int LOAD_WARPS = E4M3 && S::kTiles == 1 ? 8 : 4;
+  static constexpr int WARPS = 4 * S::kTiles + LOAD_WARPS + 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int LOAD_WARP = 4 * S::kTiles;
-  static constexpr int MMA_WARP = LOAD_WARP + 4;
+  static constexpr int MMA_WARP = LOAD_WARP + LOAD_WARPS;
   static constexpr int WALK_WARP = MMA_WARP + 1;
   static constexpr int Q_WARP = WALK_WARP + 1;           // two
   // registers: 65536 / THREADS at launch
   static constexpr uint32_t REG_LAUNCH = 65536 / THREADS / 8 * 8;
   static constexpr uint32_t REG_SOFTMAX = S::kTiles == 2 ? 184 : 208;
-  static constexpr uint32_t REG_OTHER = S::kTiles == 2 ? 72 : 144;
-  static_assert(S::kTiles * 128 * REG_SOFTMAX + 256 * REG_OTHER <= REG_LAUNCH * THREADS, "register budget");
+  static constexpr uint32_t REG_OTHER = S::kTiles == 2 ? 72 : E4M3 ? 96 : 144;
+  static_assert(S::kTiles * 128 * REG_SOFTMAX + (THREADS - S::kTiles * 128) * REG_OTHER <= REG_LAUNCH * THREADS,
+                "register budget");
   static_assert(COL_O + S::kTiles * D <= TMEM_COLS, "tensor memory budget");
   static_assert(BYTES <= 232448, "shared memory budget");
   static_assert(E4M3 || NS > kLag + 1, "loads in flight");
-  static_assert(2 * kMarks - NS >= 2, "marks outlive their block");
+  static_assert(2 * kMarks - NS - NR >= 2, "marks outlive their block");
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
@@ -265,12 +267,20 @@ __device__ __forceinline__ float* parts_of(void* work, int runs) {
   return reinterpret_cast<float*>(static_cast<Cut*>(work) + runs);
 }
 
+// Tile e of a piece of n blocks, in the order in which the products take them: K0
+// V0 K1 V1 ... for two tiles of rows, K0 K1 V0 K2 V1 ... for one.
+__device__ __forceinline__ bool is_key(int e, int n, bool two) {
+  return two ? !(e & 1) : e == 0 || ((e & 1) && e + 1 < 2 * n);
+}
+// Values of the block before the newest key's.
+__device__ __forceinline__ bool is_old(int e, int n, bool two) { return !two && e + 1 < 2 * n; }
+
 // ------------------------------------------------------------------ main kernel
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(const __grid_constant__ ExtendParams p) {
   using L = Layout<D, E4M3>;
   using S = Shape<D>;
-  constexpr int BK = L::BK, NS = L::NS, TILES = S::kTiles, ROWS = S::kRows;
+  constexpr int BK = L::BK, NS = L::NS, NR = E4M3 ? L::NR : 1, TILES = S::kTiles, ROWS = S::kRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -285,7 +295,9 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
   auto bar = [&](int i) { return bars + 8u * i; };
   auto full = [&](int s) { return bars + 8u * (B_FULL + s); };
   auto empty = [&](int s) { return bars + 8u * (B_FULL + NS + s); };
-  [[maybe_unused]] auto landed = [&](int s, int w) { return bars + 8u * (B_FULL + 2 * NS + 4 * s + w); };   // cached rows of a warp
+  // of the ring of cached rows, where the walker fills it
+  [[maybe_unused]] auto landed = [&](int s) { return bars + 8u * (B_FULL + 2 * NS + s); };
+  [[maybe_unused]] auto taken = [&](int s) { return bars + 8u * (B_FULL + 2 * NS + NR + s); };
 
   if (sbase & 1023) {
     if (threadIdx.x == 0) atomicCAS(status, 0, 99);
@@ -307,13 +319,17 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(bar(B_PIECE_FULL + i), 1);
-      mbar_init(bar(B_PIECE_EMPTY + i), 4 * TILES + 7);   // all warps but the walker
+      mbar_init(bar(B_PIECE_EMPTY + i), 4 * TILES + L::LOAD_WARPS + 3);   // all warps but the walker
     }
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full(i), 4);
+      mbar_init(full(i), L::LOAD_WARPS);
       mbar_init(empty(i), 1);
     }
-    for (int i = 0; i < 4 * L::NR; ++i) mbar_init(landed(0, i), 1);
+    if constexpr (E4M3)
+      for (int i = 0; i < NR; ++i) {
+        mbar_init(landed(i), 1);
+        mbar_init(taken(i), L::LOAD_WARPS);
+      }
     mbar_init(bar(B_TEARDOWN), 1);
     mbar_init_fence();
   }
@@ -335,6 +351,52 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     int count = 0;   // pieces
     const int spare = p.cost_shift - (BK == 128 ? 7 : 6);   // blocks that cost 1 together, log 2
     bool ok = true;
+    // 8-bit caches in boxes: brings a piece's rows to the ring of cached rows, a lane
+    // per box, and marks missing pages.
+    [[maybe_unused]] int asked = 0, block = 0;   // tiles, blocks
+    [[maybe_unused]] auto bring = [&](const Piece& u) {
+      const int32_t* const table = p.table + u.b * p.table_stride;
+      const bool two = TILES == 2 && u.rows > 128;
+      const int boxes = BK / p.box_rows, last_page = u.key_hi > 0 ? p.page_div.quotient(u.key_hi - 1) : -1;
+      int first_key = u.kb0 * BK + lane * p.box_rows;   // of this lane's box in the next block
+      auto page_of = [&](int key) {
+        const int pi = p.page_div.quotient(key);
+        return lane < boxes && key + p.box_rows > u.key_lo && pi <= last_page ? table[pi] : -1;
+      };
+      int page = page_of(first_key), at_page[2] = {0, 0}, at_slot[2] = {0, 0};
+#pragma unroll 1
+      for (int e = 0; ok && e < 2 * u.n; ++e, ++asked) {
+        const bool key = is_key(e, u.n, two);
+        if (key) {
+          at_page[1] = at_page[0];
+          at_slot[1] = at_slot[0];
+          const bool there = page >= 0 && page < p.kv.num_pages;
+          at_page[0] = there ? page : p.kv.num_pages;   // past the last: reads as zeros
+          at_slot[0] = first_key - p.page_div.quotient(first_key) * p.kv.page_size;
+          const unsigned missing = __ballot_sync(0xffffffffu, lane < boxes && !there);
+          if (lane < BK / 32) {   // a bit per key
+            uint32_t word = 0;
+            if (missing)
+              for (int i = 0; i < 32; ++i) word |= (missing >> ((lane * 32 + i) / p.box_rows) & 1) << i;
+            marks[(block % kMarks) * 4 + lane] = word;
+          }
+          __syncwarp();
+          ++block;
+          first_key += BK;
+          page = page_of(first_key);
+        }
+        const int s = asked % NR;
+        if (asked >= NR && !mbar_wait(taken(s), (asked / NR - 1) & 1, abort, status)) ok = false;
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) mbar_arrive_expect_tx(landed(s), BK * D);
+        __syncwarp();
+        const int old = !key && is_old(e, u.n, two);
+        if (lane < boxes)
+          tma_load_4d(sbase + L::RAW + s * L::TILE_RAW + lane * p.box_rows * D, key ? &p.tm_k : &p.tm_v, 0, u.head_kv,
+                      old ? at_slot[1] : at_slot[0], old ? at_page[1] : at_page[0], landed(s));
+        __syncwarp();
+      }
+    };
     auto emit = [&](const Piece& piece) {
       const int slot = count % kPieces;
       if (count >= kPieces && !mbar_wait(bar(B_PIECE_EMPTY + slot), (count / kPieces - 1) & 1, abort, status)) ok = false;
@@ -346,6 +408,8 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       }
       __syncwarp();
       ++count;
+      if constexpr (E4M3)
+        if (p.box_rows > 0 && piece.n > 0) bring(piece);
     };
     // The line's length, then the request that this block's run starts in: 32
     // requests at a time.
@@ -450,6 +514,12 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     }
     Piece over = {};
     if (ok) emit(over);
+    if constexpr (E4M3)
+      if (!ok) {   // after an abort, what has been asked for lands before the block ends
+        volatile int no_abort = 0;
+        for (int i = max(0, asked - NR); i < asked; ++i)
+          mbar_wait(landed(i % NR), (i / NR) & 1, &no_abort, status, 100000000ull);
+      }
     if (lane == 0) reinterpret_cast<Cut*>(p.work)[blockIdx.x] = cut;
   } else if (warp == L::MMA_WARP) {
     // ------------------------------------------------------------ products
@@ -582,7 +652,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
   } else if (warp >= L::LOAD_WARP && warp < L::MMA_WARP) {
     // ------------------------------------------------------------ loads
     setmaxnreg_to<L::REG_OTHER, L::REG_LAUNCH>();
-    constexpr int RPW = BK / 4;              // keys of a block per warp
+    constexpr int RPW = BK / L::LOAD_WARPS;  // keys of a block per warp
     constexpr int CPR = D / 8;               // 16-byte pieces per row of a tile
     constexpr int RPI = 32 / CPR;            // rows a warp's instruction covers
     const int w = warp - L::LOAD_WARP;
@@ -626,7 +696,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         phase ^= 1;
       }
     };
-    if (p.box_rows > 0 && lane == 0) {
+    if (!E4M3 && p.box_rows > 0 && lane == 0) {
       tma_prefetch_desc(&p.tm_k);
       tma_prefetch_desc(&p.tm_v);
     }
@@ -644,14 +714,12 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         const int pi = p.page_div.quotient(key);
         return pi <= last_page && lane < RPW ? table[pi] : -1;
       };
-      int page = page_of(u.kb0);
+      int page = E4M3 && p.box_rows > 0 ? -1 : page_of(u.kb0);
       // Where this lane's key is (of the block at hand, and of the one before), and
       // which keys of the warp are there.
-      long long off[2] = {0, 0};
       int at_page[2] = {0, 0}, at_slot[2] = {0, 0};
       unsigned good[2] = {0, 0};
       auto locate = [&](int kb) {
-        off[1] = off[0];
         good[1] = good[0];
         at_page[1] = at_page[0];
         at_slot[1] = at_slot[0];
@@ -660,26 +728,28 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         const bool there = in && page >= 0 && page < p.kv.num_pages;
         at_page[0] = page;
         at_slot[0] = key - p.page_div.quotient(key) * p.kv.page_size;
-        off[0] = there ? page * p.kv.page_stride + at_slot[0] * p.kv.slot_stride + u.head_kv * p.kv.head_stride : 0;
         good[0] = __ballot_sync(0xffffffffu, there);
         const unsigned missing = __ballot_sync(0xffffffffu, in && !there);
-        if (lane == 0) marks[(block % kMarks) * 4 + w] = missing;
+        if (lane == 0) {   // RPW bits of the block's
+          if constexpr (RPW == 32) marks[(block % kMarks) * 4 + w] = missing;
+          else if constexpr (RPW == 16) reinterpret_cast<uint16_t*>(marks)[(block % kMarks) * 8 + w] = missing;
+          else reinterpret_cast<uint8_t*>(marks)[(block % kMarks) * 16 + w] = missing;
+        }
         ++block;
         page = page_of(kb + 1);
       };
+      auto offset = [&](int old) {   // elements of the cache; of keys that are there
+        return static_cast<long long>(old ? at_page[1] : at_page[0]) * p.kv.page_stride +
+               (old ? at_slot[1] : at_slot[0]) * p.kv.slot_stride + u.head_kv * p.kv.head_stride;
+      };
       const bool two = TILES == 2 && u.rows > 128;
-      // Tile e of the piece in the order in which the products take them:
-      // K0 V0 K1 V1 ... for two tiles of rows, K0 K1 V0 K2 V1 ... for one.
-      auto is_key = [&](int e) { return two ? !(e & 1) : e == 0 || ((e & 1) && e + 1 < 2 * u.n); };
-      // of the block before the newest one: values of a single tile but the last
-      auto is_old = [&](int e) { return !two && e + 1 < 2 * u.n; };
       int located = 0;
 
       if constexpr (!E4M3) {
         for (int e = 0; ok && e < 2 * u.n; ++e) {
-          const bool key = is_key(e);
+          const bool key = is_key(e, u.n, two);
           if (key) locate(u.kb0 + located++);
-          const int old = !key && is_old(e);
+          const int old = !key && is_old(e, u.n, two);
           if (!wait(empty(slot), phase)) break;
           const uint32_t tile = sbase + L::KV + slot * L::TILE_KV;
           const unsigned have_rows = old ? good[1] : good[0];
@@ -701,7 +771,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             issued(0);
           } else {
             const uint16_t* const from = static_cast<const uint16_t*>(key ? p.kv.k : p.kv.v);
-            const long long mine = old ? off[1] : off[0];
+            const long long mine = offset(old);
 #pragma unroll 4
             for (int i = 0; i < RPW / RPI; ++i) {
               const int lr = i * RPI + lane / CPR, c = lane % CPR, rr = w * RPW + lr;
@@ -716,96 +786,105 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         }
         drain();   // the products to come wait for them, and these loads for the products
       } else {
-        // Every warp brings its own rows to the ring of cached rows, NR - 1 tiles
-        // ahead (in boxes, or each thread the pieces that it later converts), and
-        // converts them.
         constexpr int CP8 = D / 16, RP8 = 32 / CP8, N8 = RPW / RP8;   // pieces per cached row, rows per step, steps
-        const bool boxes = p.box_rows > 0;
         const uint32_t raw = sbase + L::RAW + w * (RPW * D);
-        int staged = 0;
-        unsigned rows_in[L::NR];   // which rows of the tiles on their way are there, newest first
-        auto stage = [&] {
-          unsigned have_rows = 0;
-          if (staged < 2 * u.n) {
-            const int e = staged++;
-            const bool key = is_key(e);
-            if (key) locate(u.kb0 + located++);
-            const int old = !key && is_old(e);
-            have_rows = old ? good[1] : good[0];
-            const uint32_t to = raw + raw_in * L::TILE_RAW;
-            if (boxes) {
-              if (lane == 0) mbar_arrive_expect_tx(landed(raw_in, w), RPW * D);
-              __syncwarp();
-              if (lane < RPW && (lane & (p.box_rows - 1)) == 0) {
-                const int pg = old ? at_page[1] : at_page[0], sl = old ? at_slot[1] : at_slot[0];
-                const int in = pg >= 0 && pg < p.kv.num_pages ? pg : p.kv.num_pages;
-                tma_load_4d(to + lane * D, key ? &p.tm_k : &p.tm_v, 0, u.head_kv, sl, in, landed(raw_in, w));
-              }
-              __syncwarp();
-            } else {
+        // This warp's rows of a tile from the ring of cached rows, as fp16; zeros where
+        // have_rows says so (of values that no row sees, whatever is in their slots).
+        auto convert = [&](unsigned have_rows) {
+          const uint32_t from = raw + raw_out * L::TILE_RAW + lane * 16, tile = sbase + L::KV + slot * L::TILE_KV;
+          const bool all = (RPW == 32 ? ~have_rows : ~have_rows & ((1u << (RPW & 31)) - 1)) == 0;
+          constexpr int NB = N8 < 4 ? N8 : 4;   // loads in flight
+          const int c = 2 * (lane % CP8);
+#pragma unroll
+          for (int i0 = 0; i0 < N8; i0 += NB) {
+            uint4 v[NB];
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                           : "r"(from + (i0 + i) * 512)
+                           : "memory");
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              const int lr = (i0 + i) * RP8 + lane / CP8, rr = w * RPW + lr;
+              if (!all && !(have_rows >> lr & 1)) v[i] = make_uint4(0, 0, 0, 0);
+              const uint2 a = e4m3x4_f16(v[i].x), b = e4m3x4_f16(v[i].y), f = e4m3x4_f16(v[i].z), g = e4m3x4_f16(v[i].w);
+              const uint32_t row = tile + (c >> 3) * L::CHUNK_KV + rr * 128;
+              st_shared_v4(row + (((c & 7) ^ (rr & 7)) << 4), a.x, a.y, b.x, b.y);
+              st_shared_v4(row + ((((c & 7) + 1) ^ (rr & 7)) << 4), f.x, f.y, g.x, g.y);
+            }
+          }
+          arrive(full(slot));
+          next_slot();
+        };
+        if (p.box_rows > 0) {   // the walker fills the ring
+          int values = 0;       // blocks whose values have been converted
+#pragma unroll 1
+          for (int e = 0; ok && e < 2 * u.n; ++e) {
+            unsigned have_rows = 0xffffffffu;
+            if (!wait(landed(raw_out), raw_turns / NR) || !wait(empty(slot), phase)) break;
+            ++raw_turns;
+            if (!is_key(e, u.n, two)) {
+              // rows [key_lo, key_hi) of this warp's, without missing pages
+              const int k0 = (u.kb0 + values) * BK + w * RPW;
+              const int a = min(max(u.key_lo - k0, 0), RPW), b = min(max(u.key_hi - k0, 0), RPW);
+              have_rows = a < b ? (0xffffffffu >> (32 - (b - a))) << a : 0u;
+              have_rows &= ~(marks[((block + values) % kMarks) * 4 + w * RPW / 32] >> (w * RPW % 32));
+              ++values;
+            }
+            convert(have_rows);
+            if (lane == 0) mbar_arrive(taken(raw_out));
+            raw_out = raw_out + 1 == NR ? 0 : raw_out + 1;
+          }
+          block += u.n;
+        } else {
+          // Every thread copies the pieces that it later converts, NR tiles ahead.
+          int staged = 0;
+          unsigned rows_in[NR];   // which rows of the tiles on their way are there, newest first
+          auto stage = [&] {
+            unsigned have_rows = 0;
+            if (staged < 2 * u.n) {
+              const int e = staged++;
+              const bool key = is_key(e, u.n, two);
+              if (key) locate(u.kb0 + located++);
+              const int old = !key && is_old(e, u.n, two);
+              have_rows = old ? good[1] : good[0];
+              const uint32_t to = raw + raw_in * L::TILE_RAW + lane * 16;
               const uint8_t* const from = static_cast<const uint8_t*>(key ? p.kv.k : p.kv.v);
-              const long long mine = old ? off[1] : off[0];
+              const long long mine = offset(old);
 #pragma unroll
               for (int i = 0; i < N8; ++i) {
                 const int lr = i * RP8 + lane / CP8, c = lane % CP8;
                 const long long o = __shfl_sync(0xffffffffu, mine, lr);
                 const bool have = have_rows >> lr & 1;
-                cp_async16(to + (i * 32 + lane) * 16, have ? static_cast<const void*>(from + o + c * 16) : p.q, have);
+                cp_async16(to + i * 512, have ? static_cast<const void*>(from + o + c * 16) : p.q, have);
               }
+              raw_in = raw_in + 1 == NR ? 0 : raw_in + 1;
             }
-            raw_in = raw_in + 1 == L::NR ? 0 : raw_in + 1;
-          }
-          cp_commit();
+            cp_commit();
 #pragma unroll
-          for (int i = L::NR - 1; i > 0; --i) rows_in[i] = rows_in[i - 1];
-          rows_in[0] = have_rows;
-        };
+            for (int i = NR - 1; i > 0; --i) rows_in[i] = rows_in[i - 1];
+            rows_in[0] = have_rows;
+          };
 #pragma unroll 1
-        for (int i = 0; i < L::NR - 1; ++i) stage();
-        for (int e = 0; ok && e < 2 * u.n; ++e) {
-          stage();
-          if (boxes) {
-            if (!wait(landed(raw_out, w), raw_turns / L::NR)) break;
-          } else {
-            cp_wait<L::NR - 1>();
+          for (int i = 0; i < NR; ++i) stage();
+#pragma unroll 1
+          for (int e = 0; ok && e < 2 * u.n; ++e) {
+            cp_wait<NR - 1>();
+            if (!wait(empty(slot), phase)) break;
+            convert(rows_in[NR - 1]);
+            raw_out = raw_out + 1 == NR ? 0 : raw_out + 1;
+            stage();
           }
-          ++raw_turns;
-          if (!wait(empty(slot), phase)) break;
-          const uint32_t tile = sbase + L::KV + slot * L::TILE_KV;
-          // Values that no row sees have to be zeros (whatever is in their slots).
-          const unsigned have_rows = is_key(e) ? 0xffffffffu : rows_in[L::NR - 1];
-          const bool all = (RPW == 32 ? ~have_rows : ~have_rows & ((1u << RPW) - 1)) == 0;
-#pragma unroll
-          for (int i = 0; i < N8; ++i) {
-            const int lr = i * RP8 + lane / CP8, c = 2 * (lane % CP8), rr = w * RPW + lr;
-            uint4 v;
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(raw + raw_out * L::TILE_RAW + (i * 32 + lane) * 16)
-                         : "memory");
-            if (!all && !(have_rows >> lr & 1)) v = make_uint4(0, 0, 0, 0);
-            const uint2 a = e4m3x4_f16(v.x), b = e4m3x4_f16(v.y), f = e4m3x4_f16(v.z), g = e4m3x4_f16(v.w);
-            const uint32_t row = tile + (c >> 3) * L::CHUNK_KV + rr * 128;
-            st_shared_v4(row + (((c & 7) ^ (rr & 7)) << 4), a.x, a.y, b.x, b.y);
-            st_shared_v4(row + ((((c & 7) + 1) ^ (rr & 7)) << 4), f.x, f.y, g.x, g.y);
-          }
-          raw_out = raw_out + 1 == L::NR ? 0 : raw_out + 1;
-          arrive(full(slot));
-          next_slot();
         }
       }
     }
     cp_wait<0>();
     if (!ok) {   // after an abort, what has been asked for lands before the block ends
       volatile int no_abort = 0;
-      if constexpr (E4M3) {
-        if (p.box_rows > 0)
-          for (int i = raw_turns; i < raw_turns + L::NR; ++i)
-            mbar_wait(landed(i % L::NR, w), (i / L::NR) & 1, &no_abort, status, 100000000ull);
-      } else {
+      if constexpr (!E4M3)
         for (int i = max(0, tiles - NS); i < tiles; ++i)
           mbar_wait(full(i % NS), (i / NS) & 1, &no_abort, status, 100000000ull);
-      }
     }
   } else if (warp < 4 * TILES) {
     // ------------------------------------------------------------ softmax and output
@@ -892,7 +971,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             x[e + 1] = a.y;
           }
         }
-        if (key0 < lo_most || key0 + BK > hi_least || (missing.x | missing.y | missing.z | missing.w)) {
+        if (key0 < lo_most || key0 + BK > hi_least || (missing.x | missing.y | (BK == 128 ? missing.z | missing.w : 0u))) {
           const int c_lo = max(lo - key0, 0), c_hi = min(max(hi - key0, 0), BK);
           const uint32_t words[4] = {missing.x, missing.y, missing.z, missing.w};
 #pragma unroll
@@ -900,7 +979,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             // columns [c_lo, c_hi) but the missing ones, of these 32
             const int from = min(max(c_lo - 32 * c, 0), 32), to = min(max(c_hi - 32 * c, 0), 32);
             uint32_t seen = from < to ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
-            seen &= ~(BK == 128 ? words[c] : words[(2 * c) & 3] | words[(2 * c + 1) & 3] << 16);
+            seen &= ~words[c];
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[c * 32 + e] = seen >> e & 1 ? x[c * 32 + e] : -INFINITY;
           }
@@ -1073,7 +1152,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         continue;
       }
 #pragma unroll 1
-      for (int r0 = w * 32; r0 < tiles * 128; r0 += 64) {
+      for (int r0 = w * 32; r0 < u.rows; r0 += 64) {
         const int r = r0 + lane, row = u.row_first + r, tok = p.group_div.quotient(row);
         const long long from = (u.token0 + tok) * p.q_row_stride + (u.head_kv * group + row - tok * group) * D;
         const unsigned valid = __ballot_sync(0xffffffffu, r < u.rows);
@@ -1084,26 +1163,55 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           const bool have = valid >> lr & 1;
           const uint32_t dst = sbase + L::Q + (rr >> 7) * L::TILE_Q + (c >> 3) * L::CHUNK_Q + (rr & 127) * 128 +
                                (((c & 7) ^ (rr & 7)) << 4);
-          if constexpr (!E4M3) {
-            cp_async16(dst, p.q + (have ? o + c * 8 : 0), have);
-          } else {
-            // as fp16, the row times a power of two that puts its largest value just below 2^15
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (have) v = ldg_stream(p.q + o + c * 8);
-            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-            uint32_t top = 0;
+          cp_async16(dst, p.q + (have ? o + c * 8 : 0), have);
+        }
+      }
+      if constexpr (E4M3) {
+        // To fp16 in place (every thread the pieces that it has copied), a row times a
+        // power of two that puts its largest value just below 2^15.
+        cp_commit();
+        cp_wait<0>();
+#pragma unroll 1
+        for (int r0 = w * 32; r0 < u.rows; r0 += 64) {
+          constexpr int NB = 4;   // steps at a time
+          const int c = lane % CPR;
+          auto place = [&](int i) {
+            const int rr = r0 + i * RPI + lane / CPR;
+            return sbase + L::Q + (rr >> 7) * L::TILE_Q + (c >> 3) * L::CHUNK_Q + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4);
+          };
+#pragma unroll 1
+          for (int i0 = 0; i0 < 32 / RPI; i0 += NB) {
+            uint32_t words[NB][4], top[NB];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(words[e] << 16 & 0x7FFF0000u, words[e] & 0x7FFF0000u));
+            for (int i = 0; i < NB; ++i)
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(words[i][0]), "=r"(words[i][1]), "=r"(words[i][2]), "=r"(words[i][3])
+                           : "r"(place(i0 + i))
+                           : "memory");
 #pragma unroll
-            for (int x = CPR / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-            // exponent field of the factor: 127 + 14 - (top's - 127), kept a normal number
-            const int ex = min(max(268 - static_cast<int>(top >> 23), 1), 254);
-            const float f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
-            uint32_t out[4];
+            for (int i = 0; i < NB; ++i) {
+              top[i] = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) out[e] = pack_f16x2(bf_lo(words[e]) * f, bf_hi(words[e]) * f);
-            st_shared_v4(dst, out[0], out[1], out[2], out[3]);
-            if (c == 0) q_scale[(count & 1) * ROWS + rr] = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+              for (int e = 0; e < 4; ++e)
+                top[i] = max(top[i], max(words[i][e] << 16 & 0x7FFF0000u, words[i][e] & 0x7FFF0000u));
+            }
+#pragma unroll
+            for (int x = CPR / 2; x > 0; x >>= 1)
+#pragma unroll
+              for (int i = 0; i < NB; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], x));
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              // exponent field of the factor: 127 + 14 - (top's - 127), kept a normal number
+              const int ex = min(max(268 - static_cast<int>(top[i] >> 23), 1), 254);
+              const float f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+              uint32_t out[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) out[e] = pack_f16x2(bf_lo(words[i][e]) * f, bf_hi(words[i][e]) * f);
+              st_shared_v4(place(i0 + i), out[0], out[1], out[2], out[3]);
+              if (c == 0)
+                q_scale[(count & 1) * ROWS + r0 + (i0 + i) * RPI + lane / CPR] =
+                    __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+            }
           }
         }
       }
@@ -1243,12 +1351,13 @@ cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
   const long long units = (p.num_tokens * group / S::kRows + p.batch) * p.kv.heads_kv;
   p.cost_shift = S::kKeys == 128 ? 7 : 6;
   while (units >= (1ll << 30) / ((keys >> p.cost_shift) + 8)) ++p.cost_shift;
-  // Boxes of the largest power of two that divides a page, up to a warp's keys.
+  // Boxes of the largest power of two that divides a page, up to a warp's keys (8-bit
+  // caches: a block's).
   p.box_rows = 0;
   const long long most = std::max({p.kv.page_stride, p.kv.slot_stride, p.kv.head_stride});
   if (p.kv.page_size % 8 == 0 && p.max_pages > 0 && most < (1ll << 39)) {
     int rows = 8;
-    while (rows < S::kKeys / 4 && p.kv.page_size % (2 * rows) == 0) rows *= 2;
+    while (rows < (E4M3 ? S::kKeys : S::kKeys / L::LOAD_WARPS) && p.kv.page_size % (2 * rows) == 0) rows *= 2;
     if (!make_page_map(&p.tm_k, p.kv, p.kv.k, rows) || !make_page_map(&p.tm_v, p.kv, p.kv.v, rows))
       return cudaErrorInvalidValue;
     p.box_rows = rows;
