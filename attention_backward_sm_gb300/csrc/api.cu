@@ -557,12 +557,13 @@ int fa_selftest_wait_timeout(fa_stream_t stream) {
 }
 
 int fa_check_device_status(fa_stream_t stream) {
-  int st = 0, st256 = 0, st_dq = 0, st_fwd = 0, st_ext = 0;
+  int st = 0, st256 = 0, st_dq = 0, st_fwd = 0, st_ext = 0, st_rope = 0;
   int e = fa::bwd_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st);
   if (e == 0) e = fa::bwd256_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st256);
   if (e == 0) e = fa::dq_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st_dq);
   if (e == 0) e = fa::fwd_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st_fwd);
   if (e == 0) e = fa::extend_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st_ext);
+  if (e == 0) e = fa::rope_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st_rope);
   if (st == 0) st = st256;
   if (st == 0) st = st_dq;
   if (e != 0) return cuda_fail(static_cast<cudaError_t>(e), "fa_check_device_status");
@@ -572,6 +573,7 @@ int fa_check_device_status(fa_stream_t stream) {
   if (st_fwd != 0) return fail(FA_ERR_CUDA, "the forward recorded device status %d", st_fwd);
   if (st_ext == 4) return fail(FA_ERR_TIMEOUT, "a device-side wait in fa_extend ran out of time (status %d)", st_ext);
   if (st_ext != 0) return fail(FA_ERR_CUDA, "fa_extend recorded device status %d", st_ext);
+  if (st_rope != 0) return fail(FA_ERR_TIMEOUT, "a device-side wait in fa_qk_rope ran out of time (status %d)", st_rope);
   return ok();
 }
 

@@ -72,7 +72,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // smallest step 2^-24 counts 2^-31 beside the row's largest weight.
 constexpr float kF16Shift = 7.f;
 constexpr int kPieces = 4;     // pieces of the run that the walker is ahead
-constexpr int kLeastRun = 2;   // costs
+constexpr int kLeastRun = 4;   // costs
 constexpr int kMarks = 8;      // blocks whose missing pages are kept
 constexpr int kLag = 2;        // loads in flight behind the newest
 
@@ -180,41 +180,23 @@ __device__ __forceinline__ uint2 e4m3x4_f16(uint32_t x) {
       : "r"(x));
   return r;
 }
-// (a.x, a.y) * m + c, both halves
-__device__ __forceinline__ float2 fma2(float2 a, float2 m, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, m, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 m, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, m, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(m.x), "f"(m.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-
 // ------------------------------------------------------------------ partition
-// A request's numbers, and the cost of its units.  Tile x costs kUnitCost and one
-// for every 2^cost_shift keys that its last row sees (as if none were missing),
-// summed over tiles in closed form: costs only share out the work, so they are
-// rounded as suits, but every block has to come to the same ones.  Plain 32-bit
-// integers, without a division: the walk to a block's run is on the way of short
-// calls.
+// A request's numbers, and the cost of its units.  Tile x costs kUnitCost and
+// kBlockCost (a last tile of at most 128 rows: kShortCost) for every 2^cost_shift
+// keys that its last row sees (as if none were missing), summed over tiles in closed
+// form: costs only share out the work, so they are rounded as suits, but every block
+// has to come to the same ones.  Plain 32-bit integers, without a division: the walk
+// to a block's run is on the way of short calls.
 template <int D>
 struct Request {
   using S = Shape<D>;
-  static constexpr int kUnitCost = 2;
+  static constexpr int kUnitCost = S::kTiles == 2 ? 6 : 12, kBlockCost = S::kTiles == 2 ? 3 : 2, kShortCost = 2;
   static constexpr int kRowBits = S::kRows == 256 ? 8 : 7;
   int token0, len, pos0, base, rows;   // rows: tokens * group
   int tiles;
   int ramp;   // tiles that see less than the window
   int most;   // with a window: what a tile costs at most
-  int last;   // what the last tile costs
+  int last_block, last;   // what a block of the last tile costs, and the tile
   int cost;   // of all tiles, for one key/value head
   __device__ __forceinline__ Request(const ExtendParams& p, int b, int group) {
     const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1];
@@ -227,13 +209,15 @@ struct Request {
     tiles = (rows + S::kRows - 1) >> kRowBits;
     base = max(pos0, 0);
     ramp = tiles;
-    last = kUnitCost + ((base + end - token0) >> p.cost_shift);
+    last_block = S::kTiles == 2 && rows - (tiles - 1) * S::kRows <= 128 ? kShortCost : kBlockCost;
+    last = kUnitCost + last_block * ((base + end - token0) >> p.cost_shift);
     most = 0x7fffffff;
     if (p.window > 0) {
       const long long seen = static_cast<long long>(p.window) + p.tile_tokens;
       ramp = seen > base ? static_cast<int>(min(((seen - base) * group) >> kRowBits, static_cast<long long>(tiles))) : 0;
-      most = kUnitCost + 1 + static_cast<int>(min(seen, 0x7fffffffll) >> p.cost_shift);
-      last = min(last, most);
+      const int blocks = 1 + static_cast<int>(min(seen, 0x7fffffffll) >> p.cost_shift);
+      most = kUnitCost + kBlockCost * blocks;
+      last = min(last, kUnitCost + last_block * blocks);
     }
     cost = tiles > 0 ? full(p, tiles - 1) + last : 0;
   }
@@ -242,7 +226,7 @@ struct Request {
   __device__ __forceinline__ int full(const ExtendParams& p, int x) const {
     const long long y = min(x, ramp);   // the sum of base + (i + 1) rows / group over i < y, in 32nds
     const long long keys = y * base * 32 + y * (y + 1) * p.tile_keys16;
-    return x * kUnitCost + static_cast<int>(keys >> (p.cost_shift + 5)) + (x - static_cast<int>(y)) * (most - kUnitCost);
+    return x * kUnitCost + static_cast<int>((kBlockCost * keys) >> (p.cost_shift + 5)) + (x - static_cast<int>(y)) * (most - kUnitCost);
   }
 };
 
@@ -482,9 +466,11 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             u.key_lo = p.window > 0 ? min(max(first - p.window + 1, 0), u.key_hi) : 0;
             const int kb = u.key_lo / BK;
             const int nblk = max(1, (u.key_hi + BK - 1) / BK - kb);   // a unit that sees nothing has one (masked) block
-            // Block j starts at c + min(j >> spare, w - 1).  Those in [run_start, run_end):
-            const int j0 = run_start <= c ? 0 : min((run_start - c) << spare, nblk);
-            const int j1 = run_end >= c + w ? nblk : min((run_end - c) << spare, nblk);
+            // Block j starts at c + min(j cost >> spare, w - 1).  Those in [run_start, run_end):
+            const int cost = x + 1 == r.tiles ? r.last_block : Request<D>::kBlockCost;
+            auto first_from = [&](int place) { return min((((place - c) << spare) + cost - 1) / cost, nblk); };
+            const int j0 = run_start <= c ? 0 : first_from(run_start);
+            const int j1 = run_end >= c + w ? nblk : first_from(run_end);
             if (j1 <= j0) {
               // inside a unit, but none of its blocks starts here: no partial result
               if (j0 > 0 && j0 < nblk) {
@@ -503,7 +489,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
               cut.row_first = u.row_first;
               cut.token0 = r.token0;
               cut.head_kv = hk;
-              cut.last = min(runs.of(c + min((nblk - 1) >> spare, w - 1)), runs.runs - 1);
+              cut.last = min(runs.of(c + min(((nblk - 1) * cost) >> spare, w - 1)), runs.runs - 1);
             }
             emit(u);
           }
@@ -1008,6 +994,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           }
           return (sum0.x + sum0.y) + (sum1.x + sum1.y);
         };
+        const bool first = __any_sync(0xffffffffu, fresh);
         float rest0 = x[BK / 2], rest1 = x[BK / 2 + 1];   // largest a of the second half
 #pragma unroll
         for (int e = BK / 2 + 2; e < BK; e += 4) {
@@ -1015,7 +1002,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           if (e + 2 < BK) rest1 = fmaxf(fmaxf(x[e + 2], x[e + 3]), rest1);
         }
         for (int round = 0;; ++round) {
-          sum = half(std::integral_constant<int, 0>());
+          if (round > 0 || !first) sum = half(std::integral_constant<int, 0>());
           const bool move = valid && (fresh || !(sum <= kMostSum) || fmaxf(rest0, rest1) > kMostLog);
           // (a reference in the 2^30s is off by more than the range allows for: a few rounds)
           if (!__any_sync(0xffffffffu, move) || round == 4) break;
@@ -1347,10 +1334,10 @@ cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
   const long long keys = static_cast<long long>(p.max_pages) * p.kv.page_size + p.num_tokens;   // as the costs have it
   p.tile_keys16 = static_cast<int>(S::kRows * 16 / group);
   p.tile_tokens = static_cast<int>(S::kRows / group + 1);
-  // A cost for a block of keys, or for as many as keep the sum of any lengths below 2^30.
+  // Costs per block of keys, or for as many as keep the sum of any lengths below 2^30.
   const long long units = (p.num_tokens * group / S::kRows + p.batch) * p.kv.heads_kv;
   p.cost_shift = S::kKeys == 128 ? 7 : 6;
-  while (units >= (1ll << 30) / ((keys >> p.cost_shift) + 8)) ++p.cost_shift;
+  while (units >= (1ll << 30) / (3 * (keys >> p.cost_shift) + 32)) ++p.cost_shift;
   // Boxes of the largest power of two that divides a page, up to a warp's keys (8-bit
   // caches: a block's).
   p.box_rows = 0;

@@ -94,6 +94,7 @@ struct FwdTcParams {
 };
 cudaError_t launch_fwd_main(const FwdTcParams& p, int head_dim, int batch, int max_q_blocks, cudaStream_t s);
 int fwd_read_and_clear_status(cudaStream_t s, int* status);
+int rope_read_and_clear_status(cudaStream_t s, int* status);
 
 // Sets a kernel's dynamic shared-memory limit once per device (the first
 // call with that device current); `done` is the kernel's per-device mask.

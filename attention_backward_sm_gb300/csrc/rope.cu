@@ -18,9 +18,10 @@
 //
 // All of it is one pass over the rows, bound by HBM: a thread holds 16 values
 // of a head (two pieces of 16 bytes that belong together under the rotation),
-// d / 16 threads make a head, and the sines and cosines of a block's tokens are
-// worked out once, in shared memory, for all of their heads.  Everything
-// between the loads and the one rounding at the end is fp32.
+// d / 16 lanes make a head, and a warp (few tokens: several) goes through the heads
+// of a token, whose sines and cosines it works out once and keeps in registers, as
+// it does a tensor's weights.  Everything between the loads and the one rounding at
+// the end is fp32.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -41,10 +42,15 @@ namespace {
 using namespace fa;
 
 constexpr int kThreads = 256;
-constexpr int kMostTokens = 8;       // of a block at a time
+constexpr int kMostPairs = 128;
 constexpr int kReduceThreads = 256;
-constexpr int kBwdBlocksPerSm = 3;   // blocks that walk through the tokens, each leaves one partial sum of the weights' gradients
 constexpr int kMostSms = 152;
+
+__device__ __forceinline__ void load4(const float* from, float2* x) {
+  const float4 a = *reinterpret_cast<const float4*>(from);
+  x[0] = make_float2(a.x, a.y);
+  x[1] = make_float2(a.z, a.w);
+}
 
 struct Rows {
   const uint16_t* in;    // [tokens, heads, d], rows in_stride elements apart
@@ -66,7 +72,6 @@ struct RopeParams {
   PagedCache kv;
   const int64_t* slots;
   FastDiv page_div;
-  FastDiv head_div;      // by the heads of a token, of all kinds
   int rotary;
   int half;              // pairs (i, i + rotary / 2), else (2i, 2i + 1)
   int weight_f32;
@@ -74,29 +79,35 @@ struct RopeParams {
   float sin_scale;       // mscale, or -mscale to turn back
   float eps;
   int num_tokens;
-  int tokens_per_block;
+  int split, split_bits; // warps that share a token, and log2 of it
   int heads;
   int heads_kv;
 };
 
-// cos and sin of a block's tokens: [2][tokens][rotary / 2].
-__device__ __forceinline__ void fill_turns(const RopeParams& p, long long t0, int tokens, float* turns) {
-  const int pairs = p.rotary / 2, total = tokens * pairs;
-  float* const sines = turns + p.tokens_per_block * pairs;
-  for (int i = threadIdx.x; i < total; i += kThreads) {
-    const int t = i / pairs;
-    const unsigned long long phase =
-        static_cast<unsigned long long>(static_cast<long long>(p.positions[t0 + t])) * p.freqs[i - t * pairs];
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &s, &c);
-    turns[i] = c * p.mscale;
-    sines[i] = s * p.sin_scale;
+// cos and sin of a token, worked out by a warp: c and s of the lane's 8 pairs
+// (of the u-th eight).  In shared memory the halves of an eight lie apart, so that
+// lanes read them from different banks.
+__device__ __forceinline__ void token_turns(const RopeParams& p, const unsigned long long* freqs, int at_position, int u,
+                                            float* turns, float2* c, float2* s) {
+  const int pairs = p.rotary / 2, lane = threadIdx.x % 32;
+  const unsigned long long position = static_cast<unsigned long long>(static_cast<long long>(at_position));
+  __syncwarp();   // the token before is done with the place
+  for (int i = lane; i < pairs; i += 32) {
+    const unsigned long long phase = position * freqs[i];
+    float sine, cosine;
+    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &sine, &cosine);
+    const int at = (i >> 2 & 1) * (pairs / 2) + (i >> 3) * 4 + (i & 3);
+    turns[at] = cosine * p.mscale;
+    turns[kMostPairs + at] = sine * p.sin_scale;
   }
-}
-
-__device__ __forceinline__ float weight_at(const void* w, int f32, int i) {
-  return f32 ? static_cast<const float*>(w)[i]
-             : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(w)[i]) << 16);
+  __syncwarp();
+  if (u < pairs / 8) {
+    const float* const from = turns + u * 4;
+    load4(from, c);
+    load4(from + pairs / 2, c + 2);
+    load4(from + kMostPairs, s);
+    load4(from + kMostPairs + pairs / 2, s + 2);
+  }
 }
 
 // A thread's place in a head: its two pieces of 8 values and its 8 pairs.
@@ -118,39 +129,91 @@ struct Place {
   }
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
+// 8 values, two to a float2.
+__device__ __forceinline__ void unpack8(const uint4& v, float2* x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf_lo(w[i]);
-    x[2 * i + 1] = bf_hi(w[i]);
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(bf_lo(w[i]), bf_hi(w[i]));
+}
+__device__ __forceinline__ uint4 pack8(const float2* x) {
+  return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                    pack_bf16x2(x[3].x, x[3].y));
+}
+__device__ __forceinline__ uint2 pack8_e4m3(const float2* x) {
+  return make_uint2(e4m3x2(x[0].x, x[0].y) | e4m3x2(x[1].x, x[1].y) << 16,
+                    e4m3x2(x[2].x, x[2].y) | e4m3x2(x[3].x, x[3].y) << 16);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// Sum of the products of 16 values with 16 others.
+__device__ __forceinline__ float dot16(const float2* x, const float2* y) {
+  float2 a = make_float2(0.f, 0.f), b = a;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    a = fma2(x[i], y[i], a);
+    b = fma2(x[i + 1], y[i + 1], b);
   }
+  a = add2(a, b);
+  return a.x + a.y;
 }
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
-}
-__device__ __forceinline__ void load8(const float* from, float* x) {
-  const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+// Positions (and slots) of 32 consecutive tokens, a lane each.
+template <bool SLOTS>
+struct Tokens {
+  int first = 0, position = 0;
+  long long slot = 0;
+  __device__ __forceinline__ void load(const RopeParams& p, int t) {
+    first = t;
+    const int at = min(t + static_cast<int>(threadIdx.x % 32), p.num_tokens - 1);
+    if (p.rotary > 0) position = p.positions[at];
+    if constexpr (SLOTS) slot = p.slots[at];
+  }
+  __device__ __forceinline__ int lane(const RopeParams& p, int t) {   // t >= first, of the whole warp
+    if (t - first >= 32) load(p, t);
+    return t - first;
+  }
+};
 
-// x[0..7] is piece a, x[8..15] piece b; c and s of the thread's 8 pairs.
-__device__ __forceinline__ void turn16(float* x, const float* c, const float* s, bool half) {
+// The weights of the lane's 16 values.
+__device__ __forceinline__ float weight_at(const void* w, int f32, int i) {
+  return f32 ? static_cast<const float*>(w)[i]
+             : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(w)[i]) << 16);
+}
+__device__ __forceinline__ void load_weights(const float* weights, const Place& at, float2* x) {
+  load4(weights + at.a, x);
+  load4(weights + at.a + 4, x + 2);
+  load4(weights + at.b, x + 4);
+  load4(weights + at.b + 4, x + 6);
+}
+// What the tokens share, in shared memory: both tensors' weights as fp32 (1 without
+// a norm), and the frequencies.
+struct Shared {
+  unsigned long long freqs[kMostPairs];
+  float weights[2 * 256];   // [2][D]
+  template <int D>
+  __device__ __forceinline__ void stage(const RopeParams& p, bool norm) {   // by the block
+    if (norm)
+      for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
+        const void* const w = i < D ? p.q.weight : p.k.weight;
+        weights[i] = w ? weight_at(w, p.weight_f32, i % D) : 1.f;
+      }
+    for (int i = threadIdx.x; i < p.rotary / 2; i += blockDim.x) freqs[i] = p.freqs[i];
+  }
+};
+
+// x[0..3] is piece a, x[4..7] piece b; c and s of the thread's 8 pairs.
+__device__ __forceinline__ void turn16(float2* x, const float2* c, const float2* s, bool half) {
   if (half) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = x[i], b = x[8 + i];
-      x[i] = a * c[i] - b * s[i];
-      x[8 + i] = b * c[i] + a * s[i];
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = x[i], b = x[4 + i];
+      x[i] = fma2(b, make_float2(-s[i].x, -s[i].y), mul2(a, c[i]));
+      x[4 + i] = fma2(a, s[i], mul2(b, c[i]));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = a * c[i] - b * s[i];
-      x[2 * i + 1] = b * c[i] + a * s[i];
+      const float2 a = x[i];
+      const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
+      x[i] = make_float2(a.x * ci - a.y * si, a.y * ci + a.x * si);
     }
   }
 }
@@ -166,233 +229,430 @@ __device__ __forceinline__ float head_sum(float v) {
 __device__ __forceinline__ uint4 load16(const uint16_t* p) { return ldg_stream(p); }
 
 // ---------------------------------------------------------------- forward
-template <int D, bool NORM, bool CACHE>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-  constexpr int TPH = D / 16, SLOTS = kThreads / TPH;
-  extern __shared__ __align__(16) float turns[];
-  __shared__ __align__(16) float weights[NORM ? 2 * D : 4];
-  const int u = threadIdx.x % TPH, slot = threadIdx.x / TPH;
-  const Place at(p, u);
-  const int per_token = p.heads + (CACHE ? 2 : 1) * p.heads_kv;
-  const long long t0 = static_cast<long long>(blockIdx.x) * p.tokens_per_block;
-  const int tokens = static_cast<int>(min(static_cast<long long>(p.tokens_per_block), p.num_tokens - t0));
-  const int items = tokens * per_token;
-  pdl_wait();
+// A pass is 512 / D heads of one tensor of a token: 1 KB, D / 16 lanes a head.  The
+// passes of a token are those of its queries, then its keys, then (with a cache) its
+// values.
 
-  struct Item {
-    uint4 a, b;
-    int t, h;
-  };
-  auto load = [&](int n, Item& it) {
-    it.t = -1;
-    it.a = it.b = make_uint4(0, 0, 0, 0);
-    if (n >= items) return;
-    it.t = p.head_div.quotient(n);
-    it.h = n - it.t * per_token;
-    const long long t = t0 + it.t;
-    const uint16_t* from;
-    if (it.h < p.heads) from = p.q.in + t * p.q.in_stride + it.h * D;
-    else if (!CACHE || it.h < p.heads + p.heads_kv) from = p.k.in + t * p.k.in_stride + (it.h - p.heads) * D;
-    else from = p.v + t * p.v_stride + (it.h - p.heads - p.heads_kv) * D;
-    it.a = load16(from + at.a);
-    it.b = load16(from + at.b);
-  };
-  Item next;
-  load(slot, next);   // on its way while the sines are worked out
-  if constexpr (NORM) {
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-      const void* const w = i < D ? p.q.weight : p.k.weight;
-      weights[i] = w ? weight_at(w, p.weight_f32, i % D) : 1.f;
+// What a warp keeps of the token and the tensor that it is at.
+template <int D, bool NORM, bool CACHE>
+struct Forward {
+  const RopeParams& p;
+  const Place at;
+  int t = -1, tensor = -1;
+  float2 c[4], s[4], w[NORM ? 8 : 1];
+  long long place = -1;   // of the slot in the cache, -1: not in it
+  const Shared* shared;   // nullptr: nothing is shared, weights and frequencies come from memory
+  Tokens<CACHE> tokens;
+  __device__ __forceinline__ Forward(const RopeParams& params, int u, const Shared* sh) : p(params), at(params, u), shared(sh) {}
+  __device__ __forceinline__ int heads(int tensor) const { return tensor == 0 ? p.heads : p.heads_kv; }
+  __device__ __forceinline__ const uint16_t* row(int tensor, int t) const {
+    return tensor == 0 ? p.q.in + t * p.q.in_stride : !CACHE || tensor == 1 ? p.k.in + t * p.k.in_stride : p.v + t * p.v_stride;
+  }
+  __device__ __forceinline__ void token(int next, int u, float* turns) {
+    t = next;
+    int position = 0;
+    [[maybe_unused]] long long slot = -1;
+    if (shared) {
+      const int lane = tokens.lane(p, t);
+      position = __shfl_sync(0xffffffffu, tokens.position, lane);
+      if constexpr (CACHE) slot = __shfl_sync(0xffffffffu, tokens.slot, lane);
+    } else {
+      if (p.rotary > 0) position = p.positions[t];
+      if constexpr (CACHE) slot = p.slots[t];
+    }
+    token_turns(p, shared ? shared->freqs : p.freqs, position, u, turns, c, s);
+    if constexpr (CACHE) {
+      const long long num_slots = static_cast<long long>(p.kv.num_pages) * p.kv.page_size;
+      place = -1;
+      if (slot >= 0 && slot < num_slots) {
+        const long long page = slot <= 0x7fffffffll ? p.page_div.quotient(static_cast<int>(slot)) : slot / p.kv.page_size;
+        place = page * p.kv.page_stride + (slot - page * p.kv.page_size) * p.kv.slot_stride;
+      }
     }
   }
-  fill_turns(p, t0, tokens, turns);
-  __syncthreads();
-
-  const int pairs = p.rotary / 2;
-  for (int n0 = 0; n0 < items; n0 += SLOTS) {
-    const Item it = next;
-    load(n0 + SLOTS + slot, next);
-    const bool is_q = it.h < p.heads, is_v = CACHE && it.h >= p.heads + p.heads_kv;
-    float x[16];
-    unpack8(it.a, x);
-    unpack8(it.b, x + 8);
+  __device__ __forceinline__ void of(int next) {
+    tensor = next;
     if constexpr (NORM) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
-      sum = head_sum<D>(sum);
-      if (!is_v && (is_q ? p.q.weight : p.k.weight) != nullptr) {
-        const float inv = rsqrtf(fmaf(sum, 1.f / D, p.eps));
-        float w[16];
-        load8(weights + (is_q ? 0 : D) + at.a, w);
-        load8(weights + (is_q ? 0 : D) + at.b, w + 8);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= inv * w[i];
-      }
-    }
-    if (it.t < 0) continue;
-    if (at.turned && !is_v) {
-      float c[8], s[8];
-      const float* const from = turns + it.t * pairs + 8 * u;
-      load8(from, c);
-      load8(from + p.tokens_per_block * pairs, s);
-      turn16(x, c, s, p.half);
-    }
-    const long long t = t0 + it.t;
-    if (!CACHE || is_q) {
-      uint16_t* const to = is_q ? p.q.out + t * p.q.out_stride + it.h * D
-                                : p.k.out + t * p.k.out_stride + (it.h - p.heads) * D;
-      *reinterpret_cast<uint4*>(to + at.a) = pack8(x);
-      *reinterpret_cast<uint4*>(to + at.b) = pack8(x + 8);
-    } else {
-      const long long s = p.slots[t], num_slots = static_cast<long long>(p.kv.num_pages) * p.kv.page_size;
-      if (s < 0 || s >= num_slots) continue;
-      const long long page = s <= 0x7fffffffll ? p.page_div.quotient(static_cast<int>(s)) : s / p.kv.page_size;
-      const int h = it.h - p.heads - (is_v ? p.heads_kv : 0);
-      const long long e = page * p.kv.page_stride + (s - page * p.kv.page_size) * p.kv.slot_stride + h * p.kv.head_stride;
-      void* const cache = is_v ? p.kv.v : p.kv.k;
-      if (p.kv.e4m3) {
-        uint8_t* const to = static_cast<uint8_t*>(cache) + e;
-        const float* const scales = is_v ? p.kv.v_scale : p.kv.k_scale;
-        uint2 a, b;
-        if (is_v) {   // as fa_kv_append stores them
-          const Scale sc(scales, h);
-          a = quantise8(it.a, sc);
-          b = quantise8(it.b, sc);
+      const void* const weight = tensor == 0 ? p.q.weight : p.k.weight;
+      if (tensor < 2 && weight) {
+        if (shared) {
+          load_weights(shared->weights + tensor * D, at, w);
         } else {
-          // rounded once: the turned values do not pass through bf16
-          const float sc = scales ? scales[h] : 1.f;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], sc);
-          a = make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16, e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
-          b = make_uint2(e4m3x2(x[8], x[9]) | e4m3x2(x[10], x[11]) << 16,
-                         e4m3x2(x[12], x[13]) | e4m3x2(x[14], x[15]) << 16);
+          for (int i = 0; i < 4; ++i) {
+            w[i] = make_float2(weight_at(weight, p.weight_f32, at.a + 2 * i), weight_at(weight, p.weight_f32, at.a + 2 * i + 1));
+            w[4 + i] = make_float2(weight_at(weight, p.weight_f32, at.b + 2 * i), weight_at(weight, p.weight_f32, at.b + 2 * i + 1));
+          }
         }
-        *reinterpret_cast<uint2*>(to + at.a) = a;
-        *reinterpret_cast<uint2*>(to + at.b) = b;
-      } else {
-        uint16_t* const to = static_cast<uint16_t*>(cache) + e;
-        *reinterpret_cast<uint4*>(to + at.a) = is_v ? it.a : pack8(x);
-        *reinterpret_cast<uint4*>(to + at.b) = is_v ? it.b : pack8(x + 8);
       }
+    }
+  }
+  // 16 values of head h (there: it exists) to where they belong.
+  __device__ __forceinline__ void finish(const uint4& a, const uint4& b, int h, bool there) const {
+    if (CACHE && tensor == 2) {
+      if (!there || place < 0) return;
+      if (p.kv.e4m3) {   // as fa_kv_append stores them
+        const Scale sc(p.kv.v_scale, h);
+        uint8_t* const to = static_cast<uint8_t*>(p.kv.v) + place + h * p.kv.head_stride;
+        *reinterpret_cast<uint2*>(to + at.a) = quantise8(a, sc);
+        *reinterpret_cast<uint2*>(to + at.b) = quantise8(b, sc);
+      } else {
+        uint16_t* const to = static_cast<uint16_t*>(p.kv.v) + place + h * p.kv.head_stride;
+        *reinterpret_cast<uint4*>(to + at.a) = a;
+        *reinterpret_cast<uint4*>(to + at.b) = b;
+      }
+      return;
+    }
+    float2 x[8];
+    unpack8(a, x);
+    unpack8(b, x + 4);
+    if constexpr (NORM) {
+      if (tensor == 0 ? p.q.weight != nullptr : p.k.weight != nullptr) {
+        const float2 inv = both(rsqrtf(fmaf(head_sum<D>(dot16(x, x)), 1.f / D, p.eps)));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(inv, w[i]));
+      }
+    }
+    if (at.turned) turn16(x, c, s, p.half);
+    if (!there) return;
+    if (!CACHE || tensor == 0) {
+      uint16_t* const to = (tensor == 0 ? p.q.out + t * p.q.out_stride : p.k.out + t * p.k.out_stride) + h * D;
+      *reinterpret_cast<uint4*>(to + at.a) = pack8(x);
+      *reinterpret_cast<uint4*>(to + at.b) = pack8(x + 4);
+    } else if (place < 0) {
+      return;
+    } else if (p.kv.e4m3) {
+      // Rounded once: the turned values do not pass through bf16.  (A product with the
+      // reciprocal is within their fp32 error of the quotient.)
+      const Scale sc(p.kv.k_scale, h);
+      if (sc.lo > 0.f) {
+        const float2 inv = both(__frcp_rn(sc.s));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], inv);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = make_float2(__fdiv_rn(x[i].x, sc.s), __fdiv_rn(x[i].y, sc.s));
+      }
+      uint8_t* const to = static_cast<uint8_t*>(p.kv.k) + place + h * p.kv.head_stride;
+      *reinterpret_cast<uint2*>(to + at.a) = pack8_e4m3(x);
+      *reinterpret_cast<uint2*>(to + at.b) = pack8_e4m3(x + 4);
+    } else {
+      uint16_t* const to = static_cast<uint16_t*>(p.kv.k) + place + h * p.kv.head_stride;
+      *reinterpret_cast<uint4*>(to + at.a) = pack8(x);
+      *reinterpret_cast<uint4*>(to + at.b) = pack8(x + 4);
+    }
+  }
+};
+
+// A warp (few tokens: p.split warps) takes the passes of a token, two at a time, the
+// first loads before the sines are worked out.
+template <int D, bool NORM, bool CACHE>
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
+  constexpr int TPH = D / 16, HP = 512 / D;
+  __shared__ __align__(16) float turns[kThreads / 32][2 * kMostPairs];
+  const int warp = threadIdx.x / 32, u = threadIdx.x % TPH, hl = threadIdx.x % 32 / TPH;
+  const long long job = blockIdx.x * static_cast<long long>(kThreads / 32) + warp;
+  const long long t_long = job >> p.split_bits;
+  const int t = static_cast<int>(t_long), part = static_cast<int>(job) & (p.split - 1);
+  pdl_wait();
+  if (t_long >= p.num_tokens) return;
+  Forward<D, NORM, CACHE> f(p, u, nullptr);
+  uint4 a[2], b[2];
+  auto load = [&](const uint16_t* row, int heads, int pass) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int h = (pass + i * p.split) * HP + hl;
+      a[i] = b[i] = make_uint4(0, 0, 0, 0);
+      if (h < heads) {
+        a[i] = load16(row + h * D + f.at.a);
+        b[i] = load16(row + h * D + f.at.b);
+      }
+    }
+  };
+  int before = 0;   // passes of the tensors before, which the warps of a token share in turn
+#pragma unroll
+  for (int tensor = 0; tensor < (CACHE ? 3 : 2); ++tensor) {
+    const int heads = f.heads(tensor), n = (heads + HP - 1) / HP;
+    const uint16_t* const row = f.row(tensor, t);
+    const int first = (part - before) & (p.split - 1);
+    if (first < n) load(row, heads, first);
+    if (tensor == 0) f.token(t, u, turns[warp]);
+    if (first < n) f.of(tensor);
+    for (int pass = first; pass < n; pass += 2 * p.split) {
+      if (pass != first) load(row, heads, pass);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (pass + i * p.split >= n) break;
+        const int h = (pass + i * p.split) * HP + hl;
+        f.finish(a[i], b[i], h, h < heads);
+      }
+    }
+    before += n;
+  }
+}
+
+// Where a warp is in its run of jobs: chunk `chunk` of token t, PASSES passes of one
+// tensor each (the last of a tensor may be shorter).
+template <int D, int PASSES>
+struct Job {
+  int t, chunk;
+  static constexpr int kHeads = PASSES * (512 / D);
+  __device__ __forceinline__ void next(int chunks) {
+    if (++chunk == chunks) {
+      chunk = 0;
+      ++t;
+    }
+  }
+};
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, int bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// Many tokens: every warp walks through a run of jobs, whose rows come by bulk copies
+// into a ring of its own, kRing jobs ahead: what is in flight takes no registers,
+// and 16 warps keep 192 KB per SM on their way (with loads to registers, two passes
+constexpr int kRing = 3;
+constexpr int kStreamThreads = 512;
+constexpr int kStreamWarps = kStreamThreads / 32;
+struct Stream {
+  static constexpr int kSlot = 4096;   // bytes
+  static constexpr int kTurns = kStreamWarps * kRing * kSlot;
+  static constexpr int kShared = kTurns + kStreamWarps * 2 * kMostPairs * 4;
+  static constexpr int kBars = kShared + sizeof(Shared);
+  static constexpr int kMisc = kBars + kStreamWarps * kRing * 8;
+  static constexpr int kBytes = kMisc + 16;
+};
+
+__device__ int g_rope_status = 0;
+
+// Calls body(job, slot address) for the jobs [first, last) of this warp, once their
+// copies, which copy(job, address, barrier) issues, have landed.
+template <class J, class Copy, class Body>
+__device__ __forceinline__ void stream(uint8_t* smem, J job, long long count, int chunks, Copy copy, Body body) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t base = smem_u32(smem), slots = base + warp * kRing * Stream::kSlot, bars = base + Stream::kBars + warp * kRing * 8;
+  volatile int* const abort = reinterpret_cast<volatile int*>(smem + Stream::kMisc);
+  J ahead = job;
+  long long asked = 0;
+  auto ask = [&](int r) {
+    if (asked < count) {
+      if (lane == 0) copy(ahead, slots + r * Stream::kSlot, bars + 8 * r);
+      ahead.next(chunks);
+      ++asked;
+    }
+  };
+  for (int r = 0; r < kRing; ++r) ask(r);
+  int r = 0, phase = 0;
+  for (long long i = 0; i < count; ++i) {
+    const bool ok = mbar_wait(bars + 8 * r, phase, abort, &g_rope_status);
+    if (!__all_sync(0xffffffffu, ok)) {
+      // what has been asked for lands before the block ends
+      volatile int no_abort = 0;
+      for (; i < asked; ++i) {
+        mbar_wait(bars + 8 * r, phase, &no_abort, &g_rope_status, 100000000ull);
+        if (++r == kRing) {
+          r = 0;
+          phase ^= 1;
+        }
+      }
+      return;
+    }
+    body(job, slots + r * Stream::kSlot);
+    job.next(chunks);
+    __syncwarp();   // every lane has read the slot
+    ask(r);
+    if (++r == kRing) {
+      r = 0;
+      phase ^= 1;
     }
   }
 }
 
-// ---------------------------------------------------------------- gradient
-// Blocks walk through the tokens, the query heads of all of theirs first, then
-// the key heads, so that one set of 16 sums per thread is enough for the
-// weights' gradients.  Each block leaves one partial sum per weight;
-// weight_kernel adds them in a fixed order.
 template <int D>
-__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(const RopeParams p) {
-  constexpr int TPH = D / 16, SLOTS = kThreads / TPH, WARPS = kThreads / 32;
-  extern __shared__ __align__(16) float turns[];
-  __shared__ __align__(16) float weights[D];
-  __shared__ __align__(16) float sums[WARPS][D];
-  const int u = threadIdx.x % TPH, slot = threadIdx.x / TPH, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const Place at(p, u);
-  const int pairs = p.rotary / 2;
+__device__ __forceinline__ void stream_start(const RopeParams& p, uint8_t* smem) {
+  if (threadIdx.x == 0) {
+    *reinterpret_cast<volatile int*>(smem + Stream::kMisc) = 0;
+    for (int i = 0; i < kStreamWarps * kRing; ++i) mbar_init(smem_u32(smem) + Stream::kBars + 8 * i, 1);
+    mbar_init_fence();
+  }
   pdl_wait();
+  reinterpret_cast<Shared*>(smem + Stream::kShared)->stage<D>(p, true);
+  __syncthreads();
+}
+// The run of this warp among so many jobs.
+__device__ __forceinline__ void stream_run(long long jobs, long long& first, long long& count) {
+  const long long warps = static_cast<long long>(gridDim.x) * kStreamWarps, w = static_cast<long long>(blockIdx.x) * kStreamWarps + threadIdx.x / 32;
+  const long long each = jobs / warps, rest = jobs - each * warps;
+  first = w * each + min(w, rest);
+  count = each + (w < rest ? 1 : 0);
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+template <int D, bool NORM, bool CACHE>
+__global__ void __launch_bounds__(kStreamThreads, 1) rope_stream_kernel(const RopeParams p) {
+  constexpr int TPH = D / 16, HP = 512 / D, PASSES = 4;
+  using J = Job<D, PASSES>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int u = threadIdx.x % TPH, hl = threadIdx.x % 32 / TPH;
+  float* const turns = reinterpret_cast<float*>(smem + Stream::kTurns) + threadIdx.x / 32 * 2 * kMostPairs;
+  stream_start<D>(p, smem);
+  Forward<D, NORM, CACHE> f(p, u, reinterpret_cast<const Shared*>(smem + Stream::kShared));
+  const int cq = (p.heads + J::kHeads - 1) / J::kHeads, ck = (p.heads_kv + J::kHeads - 1) / J::kHeads;
+  const int chunks = cq + (CACHE ? 2 : 1) * ck;
+  long long first, count;
+  stream_run(static_cast<long long>(p.num_tokens) * chunks, first, count);
+  auto tensor_of = [&](int chunk) { return chunk < cq ? 0 : chunk < cq + ck ? 1 : 2; };
+  auto first_head = [&](int chunk, int tensor) { return (chunk - (tensor == 0 ? 0 : tensor == 1 ? cq : cq + ck)) * J::kHeads; };
+  J job;
+  job.t = static_cast<int>(first / chunks);
+  job.chunk = static_cast<int>(first - static_cast<long long>(job.t) * chunks);
+  if (count > 0) f.tokens.load(p, job.t);
+  stream(smem, job, count, chunks,
+         [&](const J& j, uint32_t to, uint32_t bar) {
+           const int tensor = tensor_of(j.chunk), h = first_head(j.chunk, tensor), n = min(f.heads(tensor) - h, J::kHeads);
+           mbar_arrive_expect_tx(bar, n * D * 2);
+           bulk_copy(to, f.row(tensor, j.t) + h * D, n * D * 2, bar);
+         },
+         [&](const J& j, uint32_t from) {
+           if (j.t != f.t) f.token(j.t, u, turns);
+           const int tensor = tensor_of(j.chunk), h0 = first_head(j.chunk, tensor), n = min(f.heads(tensor) - h0, J::kHeads);
+           if (tensor != f.tensor) f.of(tensor);
+#pragma unroll 2
+           for (int i = 0; i < n; i += HP) {
+             const int h = i + hl;
+             const uint32_t row = from + h * D * 2;   // of a head past the last: in the slot, but not used
+             const uint4 a = lds16(row + f.at.a * 2), b = lds16(row + f.at.b * 2);
+             f.finish(a, b, h0 + h, h < n);
+           }
+         });
+}
+
+// ---------------------------------------------------------------- gradient
+// As the stream above, with two rows per job and 16 sums per lane for each weight's
+// gradient.  Each block leaves one partial sum per weight; weight_kernel adds them
+// in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(kStreamThreads, 1) rope_bwd_kernel(const RopeParams p) {
+  constexpr int TPH = D / 16, HP = 512 / D, PASSES = 2;
+  using J = Job<D, PASSES>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, u = lane % TPH, hl = lane / TPH;
+  float* const turns = reinterpret_cast<float*>(smem + Stream::kTurns) + warp * 2 * kMostPairs;
+  const Place at(p, u);
+  stream_start<D>(p, smem);
   pdl_launch();
-  for (int tensor = 0; tensor < 2; ++tensor) {
-    const Rows& r = tensor ? p.k : p.q;
-    const int heads = tensor ? p.heads_kv : p.heads;
-    const bool norm = r.weight != nullptr;
-    float acc[16];
+  const Shared& shared = *reinterpret_cast<const Shared*>(smem + Stream::kShared);
+  float2 acc_q[8], acc_k[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int i = 0; i < 8; ++i) acc_q[i] = acc_k[i] = make_float2(0.f, 0.f);
+  const int cq = (p.heads + J::kHeads - 1) / J::kHeads, chunks = cq + (p.heads_kv + J::kHeads - 1) / J::kHeads;
+  long long first, count;
+  stream_run(static_cast<long long>(p.num_tokens) * chunks, first, count);
+  J job;
+  job.t = chunks > 0 ? static_cast<int>(first / chunks) : 0;
+  job.chunk = static_cast<int>(first - static_cast<long long>(job.t) * chunks);
+  int t = -1, tensor = -1;
+  float2 c[4], s[4], w[8];
+  const bool q_norm = p.q.weight != nullptr, k_norm = p.k.weight != nullptr;
+  bool norm = false;
+  uint16_t* to = nullptr;
+  Tokens<false> tokens;
+  if (count > 0) tokens.load(p, job.t);
+  stream(smem, job, count, chunks,
+         [&](const J& j, uint32_t to, uint32_t bar) {
+           const bool is_q = j.chunk < cq, two = is_q ? q_norm : k_norm;
+           const int h = (is_q ? j.chunk : j.chunk - cq) * J::kHeads, n = min((is_q ? p.heads : p.heads_kv) - h, J::kHeads);
+           const int bytes = n * D * 2;
+           mbar_arrive_expect_tx(bar, two ? 2 * bytes : bytes);
+           bulk_copy(to, (is_q ? p.q.in + j.t * p.q.in_stride : p.k.in + j.t * p.k.in_stride) + h * D, bytes, bar);
+           if (two)
+             bulk_copy(to + Stream::kSlot / 2, (is_q ? p.q.x + j.t * p.q.x_stride : p.k.x + j.t * p.k.x_stride) + h * D, bytes, bar);
+         },
+         [&](const J& j, uint32_t from) {
+           const bool is_q = j.chunk < cq;
+           const int h0 = (is_q ? j.chunk : j.chunk - cq) * J::kHeads, n = min((is_q ? p.heads : p.heads_kv) - h0, J::kHeads);
+           if (j.t != t) {
+             const int at_lane = tokens.lane(p, j.t);
+             token_turns(p, shared.freqs, __shfl_sync(0xffffffffu, tokens.position, at_lane), u, turns, c, s);
+             tensor = -1;
+           }
+           t = j.t;
+           if (tensor != (is_q ? 0 : 1)) {
+             tensor = is_q ? 0 : 1;
+             norm = is_q ? q_norm : k_norm;
+             to = is_q ? p.q.out + t * p.q.out_stride : p.k.out + t * p.k.out_stride;
+             load_weights(shared.weights + (is_q ? 0 : D), at, w);
+           }
+#pragma unroll
+           for (int i = 0; i < PASSES * HP; i += HP) {
+             if (i >= n) break;
+             const int h = i + hl;
+             const uint32_t row = from + h * D * 2;   // of a head past the last: in the slot, but not used
+             float2 g[8];
+             unpack8(lds16(row + at.a * 2), g);
+             unpack8(lds16(row + at.b * 2), g + 4);
+             if (at.turned) turn16(g, c, s, p.half);
+             if (norm) {
+               float2 x[8];
+               unpack8(lds16(row + Stream::kSlot / 2 + at.a * 2), x);
+               unpack8(lds16(row + Stream::kSlot / 2 + at.b * 2), x + 4);
+               const float inv = rsqrtf(fmaf(head_sum<D>(dot16(x, x)), 1.f / D, p.eps));
+#pragma unroll
+               for (int k = 0; k < 8; ++k) x[k] = mul2(x[k], both(inv));
+               if (h < n) {
+                 if (is_q) {
+#pragma unroll
+                   for (int k = 0; k < 8; ++k) acc_q[k] = fma2(g[k], x[k], acc_q[k]);
+                 } else {
+#pragma unroll
+                   for (int k = 0; k < 8; ++k) acc_k[k] = fma2(g[k], x[k], acc_k[k]);
+                 }
+               }
+#pragma unroll
+               for (int k = 0; k < 8; ++k) g[k] = mul2(g[k], w[k]);
+               const float2 along = both(head_sum<D>(dot16(g, x)) * (-1.f / D));
+#pragma unroll
+               for (int k = 0; k < 8; ++k) g[k] = mul2(both(inv), fma2(x[k], along, g[k]));
+             }
+             if (h >= n) continue;
+             uint16_t* const row_to = to + (h0 + h) * D;
+             *reinterpret_cast<uint4*>(row_to + at.a) = pack8(g);
+             *reinterpret_cast<uint4*>(row_to + at.b) = pack8(g + 4);
+           }
+         });
+  // the heads of a warp, then the warps, in order; the rings are free
+  float* const sums = reinterpret_cast<float*>(smem);   // [warps][D]
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float2* const acc = k == 0 ? acc_q : acc_k;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int off = TPH; off < 32; off <<= 1) {
+        acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, off);
+        acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, off);
+      }
     __syncthreads();
-    if (norm)
-      for (int i = threadIdx.x; i < D; i += kThreads) weights[i] = weight_at(r.weight, p.weight_f32, i);
-    for (long long t0 = static_cast<long long>(blockIdx.x) * p.tokens_per_block; heads > 0 && t0 < p.num_tokens;
-         t0 += static_cast<long long>(gridDim.x) * p.tokens_per_block) {
-      const int tokens = static_cast<int>(min(static_cast<long long>(p.tokens_per_block), p.num_tokens - t0));
-      const int items = tokens * heads;
-      struct Item {
-        uint4 ga, gb, xa, xb;
-        int t, h;
-      };
-      auto load = [&](int n, Item& it) {
-        it.t = -1;
-        it.ga = it.gb = it.xa = it.xb = make_uint4(0, 0, 0, 0);
-        if (n >= items) return;
-        it.t = n / heads;
-        it.h = n - it.t * heads;
-        const uint16_t* const g = r.in + (t0 + it.t) * r.in_stride + it.h * D;
-        it.ga = load16(g + at.a);
-        it.gb = load16(g + at.b);
-        if (norm) {
-          const uint16_t* const x = r.x + (t0 + it.t) * r.x_stride + it.h * D;
-          it.xa = load16(x + at.a);
-          it.xb = load16(x + at.b);
-        }
-      };
-      Item next;
-      load(slot, next);
-      __syncthreads();   // the tokens before are done with their turns
-      fill_turns(p, t0, tokens, turns);
-      __syncthreads();
-      for (int n0 = 0; n0 < items; n0 += SLOTS) {
-        const Item it = next;
-        load(n0 + SLOTS + slot, next);
-        float g[16], x[16];
-        unpack8(it.ga, g);
-        unpack8(it.gb, g + 8);
-        if (at.turned && it.t >= 0) {
-          float c[8], s[8];
-          const float* const from = turns + it.t * pairs + 8 * u;
-          load8(from, c);
-          load8(from + p.tokens_per_block * pairs, s);
-          turn16(g, c, s, p.half);
-        }
-        if (norm) {
-          unpack8(it.xa, x);
-          unpack8(it.xb, x + 8);
-          float sum = 0.f;
+    if (lane < TPH) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
-          const float inv = rsqrtf(fmaf(head_sum<D>(sum), 1.f / D, p.eps));
-          float w[16], along = 0.f;
-          load8(weights + at.a, w);
-          load8(weights + at.b, w + 8);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            x[i] *= inv;
-            if (it.t >= 0) acc[i] = fmaf(g[i], x[i], acc[i]);
-            g[i] *= w[i];
-            along = fmaf(g[i], x[i], along);
-          }
-          along = head_sum<D>(along) * (1.f / D);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) g[i] = inv * fmaf(-x[i], along, g[i]);
-        }
-        if (it.t < 0) continue;
-        uint16_t* const to = r.out + (t0 + it.t) * r.out_stride + it.h * D;
-        *reinterpret_cast<uint4*>(to + at.a) = pack8(g);
-        *reinterpret_cast<uint4*>(to + at.b) = pack8(g + 8);
+      for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<float2*>(sums + warp * D + at.a + 2 * i) = acc[i];
+        *reinterpret_cast<float2*>(sums + warp * D + at.b + 2 * i) = acc[4 + i];
       }
     }
-    if (norm) {
-      // the heads of a warp, then the warps, in order
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += kStreamThreads) {
+      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int off = TPH; off < 32; off <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
-      if (lane < TPH) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sums[warp][at.a + i] = acc[i];
-          sums[warp][at.b + i] = acc[8 + i];
-        }
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < D; i += kThreads) {
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) sum += sums[w][i];
-        p.partial[(static_cast<long long>(blockIdx.x) * 2 + tensor) * D + i] = sum;
-      }
+      for (int v = 0; v < kStreamWarps; ++v) sum += sums[v * D + i];
+      p.partial[(static_cast<long long>(blockIdx.x) * 2 + k) * D + i] = sum;
     }
   }
 }
@@ -518,23 +778,47 @@ RopeParams make_params(const void* positions, const void* freqs, int rotary, int
 }
 
 cudaError_t launch_forward(RopeParams& p, int head_dim, bool cache, const Device& dev, cudaStream_t s) {
-  const int per_token = p.heads + (cache ? 2 : 1) * p.heads_kv;
-  // One token per block until every SM has four blocks.
-  const int per = p.num_tokens / (4 * dev.sms);
-  p.tokens_per_block = per < 1 ? 1 : per > kMostTokens ? kMostTokens : per;
-  p.head_div = FastDiv(static_cast<uint32_t>(per_token));
-  const int grid = (p.num_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
-  const size_t smem = static_cast<size_t>(p.tokens_per_block) * p.rotary * sizeof(float);
+  const int hp = 512 / head_dim, q = (p.heads + hp - 1) / hp, k = (p.heads_kv + hp - 1) / hp;
+  const int passes = q + (cache ? 2 : 1) * k, warps = kThreads / 32;
   const bool norm = p.q.weight || p.k.weight;
+  // With a cache, from 8 passes for each of the warps of a stream on, the stream.
+  const bool many = cache && static_cast<long long>(p.num_tokens) * passes >= 8ll * kStreamWarps * dev.sms;
   return with_dim(head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
+    if (many) {
+      static std::atomic<unsigned long long> done[4];
+      auto* const kernel = cache ? (norm ? rope_stream_kernel<D, true, true> : rope_stream_kernel<D, false, true>)
+                                 : (norm ? rope_stream_kernel<D, true, false> : rope_stream_kernel<D, false, false>);
+      cudaError_t e = prepare_once(reinterpret_cast<const void*>(kernel), Stream::kBytes, dev.id, done[2 * cache + norm]);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(kernel, dim3(dev.sms), dim3(kStreamThreads), Stream::kBytes, s, p);
+    }
     auto* const kernel = cache ? (norm ? rope_kernel<D, true, true> : rope_kernel<D, false, true>)
                                : (norm ? rope_kernel<D, true, false> : rope_kernel<D, false, false>);
-    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, p);
+    // as many warps per token as have two passes each, up to what runs at once
+    const int most = 3 * dev.sms;   // blocks
+    p.split = 1;
+    p.split_bits = 0;
+    while (p.split < warps && 2 * p.split < passes && static_cast<long long>(p.num_tokens) * p.split < most * warps) {
+      p.split *= 2;
+      ++p.split_bits;
+    }
+    const long long want = (static_cast<long long>(p.num_tokens) * p.split + warps - 1) / warps;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(want)), dim3(kThreads), 0, s, p);
   });
 }
 
 }  // namespace
+
+namespace fa {
+int rope_read_and_clear_status(cudaStream_t s, int* status) {
+  int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_rope_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_rope_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return static_cast<int>(e);
+}
+}  // namespace fa
 
 extern "C" {
 
@@ -603,7 +887,7 @@ size_t fa_qk_rope_bwd_workspace_size(int head_dim) {
     return 0;
   }
   ok();
-  return static_cast<size_t>(kMostSms) * kBwdBlocksPerSm * 2 * head_dim * sizeof(float);
+  return static_cast<size_t>(kMostSms) * 2 * head_dim * sizeof(float);
 }
 
 int fa_qk_rope_bwd(const fa_bf16* dq_out, const fa_bf16* dk_out, long long dq_out_row_stride,
@@ -646,15 +930,16 @@ int fa_qk_rope_bwd(const fa_bf16* dq_out, const fa_bf16* dk_out, long long dq_ou
   p.q.x = q, p.q.x_stride = q_row_stride;
   p.k.x = k, p.k.x_stride = k_row_stride;
   p.partial = static_cast<float*>(workspace);
-  const int most = kBwdBlocksPerSm * (dev.sms < kMostSms ? dev.sms : kMostSms);
-  const int per = num_tokens / most;
-  p.tokens_per_block = per < 1 ? 1 : per > kMostTokens ? kMostTokens : per;
-  const int chunks = (num_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
-  const int blocks = chunks < 1 ? 1 : chunks < most ? chunks : most;   // without tokens the weights' gradients are 0
-  const size_t smem = static_cast<size_t>(p.tokens_per_block) * rotary_dim * sizeof(float);
+  const int most = dev.sms < kMostSms ? dev.sms : kMostSms, hp = 512 / head_dim;
+  // a job for every warp at least; without tokens the weights' gradients are 0
+  const long long jobs = static_cast<long long>(num_tokens) * ((heads + 2 * hp - 1) / (2 * hp) + (heads_kv + 2 * hp - 1) / (2 * hp));
+  const long long want = (jobs + kStreamWarps - 1) / kStreamWarps;
+  const int blocks = want < 1 ? 1 : want < most ? static_cast<int>(want) : most;
   cudaError_t e = with_dim(head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    cudaError_t e = launch_pdl(rope_bwd_kernel<D>, dim3(blocks), dim3(kThreads), smem, s, p);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = prepare_once(reinterpret_cast<const void*>(rope_bwd_kernel<D>), Stream::kBytes, dev.id, done);
+    if (e == cudaSuccess) e = launch_pdl(rope_bwd_kernel<D>, dim3(blocks), dim3(kStreamThreads), Stream::kBytes, s, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(weight_kernel<D>, dim3(2 * D / 8), dim3(kReduceThreads), 0, s,
                       static_cast<const float*>(p.partial), blocks, q_weight ? dq_weight : nullptr,
