@@ -345,7 +345,10 @@ struct Forward {
 };
 
 // A warp (few tokens: p.split warps) takes the passes of a token, two at a time, the
-// first loads before the sines are worked out.
+// first loads before the sines are worked out.  32768 rows of 32 / 8 heads of 128 with
+// norms (671 MB): 114 us, 88 % of a copy's rate; 8191 rows of 16 / 4 heads of 64, half
+// of each rotated (42 MB): 9.6 us, 65 %; 64 rows of 32 / 8 heads of 128: 3 us, the
+// launch and three dependent reads.
 template <int D, bool NORM, bool CACHE>
 __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
   constexpr int TPH = D / 16, HP = 512 / D;
@@ -410,9 +413,9 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, int byt
                : "memory");
 }
 
-// Many tokens: every warp walks through a run of jobs, whose rows come by bulk copies
-// into a ring of its own, kRing jobs ahead: what is in flight takes no registers,
-// and 16 warps keep 192 KB per SM on their way (with loads to registers, two passes
+// Streams: every warp walks through a run of jobs, whose rows come by bulk copies into
+// a ring of its own, kRing jobs ahead: what is in flight takes no registers, and 16
+// warps keep 192 KB per SM on their way.
 constexpr int kRing = 3;
 constexpr int kStreamThreads = 512;
 constexpr int kStreamWarps = kStreamThreads / 32;
@@ -495,7 +498,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
   return v;
 }
 
-template <int D, bool NORM, bool CACHE>
+// Many tokens into a cache.  8191 rows of 32 / 8 heads of 128 with norms to e4m3 (185
+// MB): 36 us, 77 % of a copy's rate (rope_kernel: 43).
+template <int D, bool NORM>
 __global__ void __launch_bounds__(kStreamThreads, 1) rope_stream_kernel(const RopeParams p) {
   constexpr int TPH = D / 16, HP = 512 / D, PASSES = 4;
   using J = Job<D, PASSES>;
@@ -503,9 +508,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) rope_stream_kernel(const Ro
   const int u = threadIdx.x % TPH, hl = threadIdx.x % 32 / TPH;
   float* const turns = reinterpret_cast<float*>(smem + Stream::kTurns) + threadIdx.x / 32 * 2 * kMostPairs;
   stream_start<D>(p, smem);
-  Forward<D, NORM, CACHE> f(p, u, reinterpret_cast<const Shared*>(smem + Stream::kShared));
+  Forward<D, NORM, true> f(p, u, reinterpret_cast<const Shared*>(smem + Stream::kShared));
   const int cq = (p.heads + J::kHeads - 1) / J::kHeads, ck = (p.heads_kv + J::kHeads - 1) / J::kHeads;
-  const int chunks = cq + (CACHE ? 2 : 1) * ck;
+  const int chunks = cq + 2 * ck;
   long long first, count;
   stream_run(static_cast<long long>(p.num_tokens) * chunks, first, count);
   auto tensor_of = [&](int chunk) { return chunk < cq ? 0 : chunk < cq + ck ? 1 : 2; };
@@ -537,7 +542,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1) rope_stream_kernel(const Ro
 // ---------------------------------------------------------------- gradient
 // As the stream above, with two rows per job and 16 sums per lane for each weight's
 // gradient.  Each block leaves one partial sum per weight; weight_kernel adds them
-// in a fixed order.
+// in a fixed order.  16384 rows of 16 / 16 heads of 128 (403 MB): 81 us, 74 % of a
+// copy's rate; 5001 rows of 8 / 1 heads of 256 (69 MB): 25.7 us, 40 %.  Bound by its
+// instructions: 300 for a pass of 1 KB, their slots 44 % busy with 16 warps per SM,
+// which is what the rings and 128 registers leave (without the stores 62 us, without
+// the sines 73).
 template <int D>
 __global__ void __launch_bounds__(kStreamThreads, 1) rope_bwd_kernel(const RopeParams p) {
   constexpr int TPH = D / 16, HP = 512 / D, PASSES = 2;
@@ -781,15 +790,17 @@ cudaError_t launch_forward(RopeParams& p, int head_dim, bool cache, const Device
   const int hp = 512 / head_dim, q = (p.heads + hp - 1) / hp, k = (p.heads_kv + hp - 1) / hp;
   const int passes = q + (cache ? 2 : 1) * k, warps = kThreads / 32;
   const bool norm = p.q.weight || p.k.weight;
-  // With a cache, from 8 passes for each of the warps of a stream on, the stream.
+  // Into a cache, from 8 passes for each of the warps of a stream on, the stream (8191
+  // rows of 32 / 8 heads of 128 to e4m3: 36 us, 43 without it; 64 rows: 3.2 us
+  // without it, of which its rings would not see a second job).  Rows to rows go
+  // without it: 32768 of 32 / 8 heads of 128 with norms 114 us, as a stream 125.
   const bool many = cache && static_cast<long long>(p.num_tokens) * passes >= 8ll * kStreamWarps * dev.sms;
   return with_dim(head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
     if (many) {
-      static std::atomic<unsigned long long> done[4];
-      auto* const kernel = cache ? (norm ? rope_stream_kernel<D, true, true> : rope_stream_kernel<D, false, true>)
-                                 : (norm ? rope_stream_kernel<D, true, false> : rope_stream_kernel<D, false, false>);
-      cudaError_t e = prepare_once(reinterpret_cast<const void*>(kernel), Stream::kBytes, dev.id, done[2 * cache + norm]);
+      static std::atomic<unsigned long long> done[2];
+      auto* const kernel = norm ? rope_stream_kernel<D, true> : rope_stream_kernel<D, false>;
+      cudaError_t e = prepare_once(reinterpret_cast<const void*>(kernel), Stream::kBytes, dev.id, done[norm]);
       if (e != cudaSuccess) return e;
       return launch_pdl(kernel, dim3(dev.sms), dim3(kStreamThreads), Stream::kBytes, s, p);
     }

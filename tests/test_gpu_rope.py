@@ -254,7 +254,10 @@ def cache_of(pages, page, Hkv, d, kv, layout="plain"):
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("norm", ["", "qk"])
 @pytest.mark.parametrize("shape", [(1, 4, 1, 64, 64), (64, 32, 8, 128, 128), (77, 3, 3, 256, 64), (2500, 8, 2, 64, 32),
-                                   (1300, 6, 6, 128, 112)], ids=str)
+                                   (1300, 6, 6, 128, 112),
+                                   # enough for the stream: whole and part chunks, more than 32 tokens to a warp
+                                   (6500, 8, 4, 128, 128), (5001, 5, 3, 256, 128), (7001, 36, 9, 64, 64),
+                                   (90001, 2, 1, 64, 32)], ids=str)
 def test_append_is_rotation_then_append(shape, norm, kv, layout):
     T, H, Hkv, d, rotary = shape
     p = Problem(*shape, half=T % 2 == 0, norm=norm, seed=T)
