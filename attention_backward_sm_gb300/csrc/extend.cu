@@ -97,7 +97,7 @@ struct Piece {
 // one behind it: tile 1's warps, which take no part in units of one tile, have
 // barriers of their own, and so has the end of a piece (O_LAST; O_DONE is of every
 // block).
-enum { B_Q_FULL = 0, B_Q_EMPTY, B_S_FULL, B_P_READY = B_S_FULL + 3, B_P_HALF = B_P_READY + 3, B_O_DONE = B_P_HALF + 2, B_O_LAST = B_O_DONE + 2,
+enum { B_Q_FULL = 0, B_Q_EMPTY, B_Q_RAW, B_S_FULL, B_P_READY = B_S_FULL + 3, B_P_HALF = B_P_READY + 3, B_O_DONE = B_P_HALF + 2, B_O_LAST = B_O_DONE + 2,
        B_O_FREE = B_O_LAST + 2, B_PIECE_FULL = B_O_FREE + 2, B_PIECE_EMPTY = B_PIECE_FULL + kPieces, B_TEARDOWN = B_PIECE_EMPTY + kPieces,
        B_FULL };
 
@@ -126,6 +126,11 @@ struct Layout {
   static constexpr uint32_t BYTES = MISC + 16;
   static constexpr uint32_t COL_O = 2 * BK;              // after two score buffers
   static constexpr int LOAD_WARPS = E4M3 && S::kTiles == 1 ? 8 : 4;
+  // Who makes fp16 of the queries of an 8-bit cache: the loading warps, or at heads of 64,
+  // whose tiles of keys are the smallest, the query warps.  (4 chunks of 2048 over cached
+  // rows, 32 / 8 heads of 128: 960 us, and 1166 by the query warps; 32 / 8 heads of 64: 811,
+  // and 757 by the query warps; 64 requests of 1 to 8 tokens 124, and 105.)
+  static constexpr bool LOADERS_CONVERT_Q = E4M3 && D > 64;
   static constexpr int WARPS = 4 * S::kTiles + LOAD_WARPS + 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int LOAD_WARP = 4 * S::kTiles;
@@ -259,6 +264,51 @@ __device__ __forceinline__ bool is_key(int e, int n, bool two) {
 // Values of the block before the newest key's.
 __device__ __forceinline__ bool is_old(int e, int n, bool two) { return !two && e + 1 < 2 * n; }
 
+// Queries of an 8-bit cache from bf16 to fp16 in place, a row times a power of two that
+// puts its largest value just below 2^15; scale has the power's inverse.  Warp w of
+// `warps`, NB rows (or pairs, fours of them) in flight.
+template <int D, int NB>
+__device__ __forceinline__ void convert_queries(uint32_t q, float* scale, int rows, int w, int warps, int lane) {
+  constexpr int QPR = D / 8, QPI = 32 / QPR;   // pieces per row, rows per step
+  const int c = lane % QPR;
+#pragma unroll 1
+  for (int r0 = w * (NB * QPI); r0 < rows; r0 += warps * NB * QPI) {
+    auto place = [&](int i) {
+      const int rr = r0 + i * QPI + lane / QPR;
+      return q + (rr >> 7) * (128 * D * 2) + (c >> 3) * (128 * 128) + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4);
+    };
+    uint32_t words[NB][4], top[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(words[i][0]), "=r"(words[i][1]), "=r"(words[i][2]), "=r"(words[i][3])
+                   : "r"(place(i))
+                   : "memory");
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      top[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        top[i] = max(top[i], max(words[i][e] << 16 & 0x7FFF0000u, words[i][e] & 0x7FFF0000u));
+    }
+#pragma unroll
+    for (int x = QPR / 2; x > 0; x >>= 1)
+#pragma unroll
+      for (int i = 0; i < NB; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], x));
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      // exponent field of the factor: 127 + 14 - (top's - 127), kept a normal number
+      const int ex = min(max(268 - static_cast<int>(top[i] >> 23), 1), 254);
+      const float f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+      uint32_t out[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = pack_f16x2(bf_lo(words[i][e]) * f, bf_hi(words[i][e]) * f);
+      st_shared_v4(place(i), out[0], out[1], out[2], out[3]);
+      if (c == 0) scale[r0 + i * QPI + lane / QPR] = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ main kernel
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(const __grid_constant__ ExtendParams p) {
@@ -287,9 +337,11 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     if (threadIdx.x == 0) atomicCAS(status, 0, 99);
     return;
   }
+  const bool boxed = E4M3 && p.box_rows > 0;
   if (threadIdx.x == 0) {
     *abort = 0;
-    mbar_init(bar(B_Q_FULL), 2);   // a lane of every warp, here and below
+    mbar_init(bar(B_Q_FULL), L::LOADERS_CONVERT_Q ? L::LOAD_WARPS : 2);   // a lane of every warp, here and below
+    mbar_init(bar(B_Q_RAW), 2);
     mbar_init(bar(B_Q_EMPTY), 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(bar(B_S_FULL + i), 1);
@@ -306,13 +358,13 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       mbar_init(bar(B_PIECE_EMPTY + i), 4 * TILES + L::LOAD_WARPS + 3);   // all warps but the walker
     }
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full(i), L::LOAD_WARPS);
+      mbar_init(full(i), boxed ? 4 : L::LOAD_WARPS);
       mbar_init(empty(i), 1);
     }
     if constexpr (E4M3)
       for (int i = 0; i < NR; ++i) {
         mbar_init(landed(i), 1);
-        mbar_init(taken(i), L::LOAD_WARPS);
+        mbar_init(taken(i), 4);
       }
     mbar_init(bar(B_TEARDOWN), 1);
     mbar_init_fence();
@@ -645,8 +697,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     int slot = 0, phase = 1;                 // of the ring: the first pass finds every slot empty
     uint32_t pending[kLag] = {};             // barriers of the copies in flight, oldest last (0: none)
     int block = 0, raw_in = 0, raw_out = 0;  // blocks of keys so far; places in the ring of cached rows
-    int tiles = 0;                           // asked for so far
-    [[maybe_unused]] int raw_turns = 0;      // tiles of cached rows taken so far
+    int tiles = 0;                           // so far
     bool ok = true;
     auto wait = [&](uint32_t b, int parity) {
       if (ok && !mbar_wait(b, parity & 1, abort, status)) ok = false;
@@ -772,59 +823,72 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         }
         drain();   // the products to come wait for them, and these loads for the products
       } else {
-        constexpr int CP8 = D / 16, RP8 = 32 / CP8, N8 = RPW / RP8;   // pieces per cached row, rows per step, steps
-        const uint32_t raw = sbase + L::RAW + w * (RPW * D);
-        // This warp's rows of a tile from the ring of cached rows, as fp16; zeros where
-        // have_rows says so (of values that no row sees, whatever is in their slots).
-        auto convert = [&](unsigned have_rows) {
-          const uint32_t from = raw + raw_out * L::TILE_RAW + lane * 16, tile = sbase + L::KV + slot * L::TILE_KV;
-          const bool all = (RPW == 32 ? ~have_rows : ~have_rows & ((1u << (RPW & 31)) - 1)) == 0;
-          constexpr int NB = N8 < 4 ? N8 : 4;   // loads in flight
+        constexpr int CP8 = D / 16, RP8 = 32 / CP8;   // pieces per cached row, rows per step
+        // N rows of a tile, from row0 on, from the ring of cached rows as fp16; zeros where
+        // `have` says so (of values that no row sees, whatever is in their slots).
+        auto convert = [&](auto rows, uint32_t raw, uint32_t tile, int row0, unsigned have) {
+          constexpr int N = decltype(rows)::value, STEPS = N / RP8, NB = STEPS < 4 ? STEPS : 4;   // NB loads in flight
+          const bool all = (~have & (0xffffffffu >> (32 - N))) == 0;
           const int c = 2 * (lane % CP8);
-#pragma unroll
-          for (int i0 = 0; i0 < N8; i0 += NB) {
+#pragma unroll 1
+          for (int i0 = 0; i0 < STEPS; i0 += NB) {
             uint4 v[NB];
 #pragma unroll
             for (int i = 0; i < NB; ++i)
               asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                            : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                           : "r"(from + (i0 + i) * 512)
+                           : "r"(raw + row0 * D + ((i0 + i) * 32 + lane) * 16)
                            : "memory");
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-              const int lr = (i0 + i) * RP8 + lane / CP8, rr = w * RPW + lr;
-              if (!all && !(have_rows >> lr & 1)) v[i] = make_uint4(0, 0, 0, 0);
+              const int lr = (i0 + i) * RP8 + lane / CP8, rr = row0 + lr;
+              if (!all && !(have >> lr & 1)) v[i] = make_uint4(0, 0, 0, 0);
               const uint2 a = e4m3x4_f16(v[i].x), b = e4m3x4_f16(v[i].y), f = e4m3x4_f16(v[i].z), g = e4m3x4_f16(v[i].w);
               const uint32_t row = tile + (c >> 3) * L::CHUNK_KV + rr * 128;
               st_shared_v4(row + (((c & 7) ^ (rr & 7)) << 4), a.x, a.y, b.x, b.y);
               st_shared_v4(row + ((((c & 7) + 1) ^ (rr & 7)) << 4), f.x, f.y, g.x, g.y);
             }
           }
-          arrive(full(slot));
-          next_slot();
         };
-        if (p.box_rows > 0) {   // the walker fills the ring
-          int values = 0;       // blocks whose values have been converted
+        // This warp's share of Q, which the query warps have brought
+        auto convert_q = [&] {
+          if constexpr (L::LOADERS_CONVERT_Q) {
+            if (!wait(bar(B_Q_RAW), count)) return;
+            convert_queries<D, 2>(sbase + L::Q, q_scale + (count & 1) * ROWS, u.rows, w, L::LOAD_WARPS, lane);
+            arrive(bar(B_Q_FULL));
+          }
+        };
+        if (boxed) {
+          // The walker fills the ring; group `mine` of four warps takes every GROUPS-th tile:
+          // a tile's waits and fences come half as often to each of two.  (With four warps in
+          // all it does not pay: 64 requests of 1 to 8 tokens, 32 / 8 heads of 64, 108 us, and
+          // 125 as two pairs; with eight, 24 chunks over heads of 256, 115 us and 99 in groups.)
+          constexpr int N = BK / 4, GROUPS = L::LOAD_WARPS / 4;
+          const int mine = w / 4, row0 = w % 4 * N;
+          if (mine > 0) convert_q();
 #pragma unroll 1
-          for (int e = 0; ok && e < 2 * u.n; ++e) {
-            unsigned have_rows = 0xffffffffu;
-            if (!wait(landed(raw_out), raw_turns / NR) || !wait(empty(slot), phase)) break;
-            ++raw_turns;
+          for (int e = mine; ok && e < 2 * u.n; e += GROUPS) {
+            const int i = tiles + e, at = i % NS, raw_at = i % NR;
+            if (!wait(landed(raw_at), i / NR) || !wait(empty(at), i / NS + 1)) break;
+            unsigned have = 0xffffffffu;
             if (!is_key(e, u.n, two)) {
               // rows [key_lo, key_hi) of this warp's, without missing pages
-              const int k0 = (u.kb0 + values) * BK + w * RPW;
-              const int a = min(max(u.key_lo - k0, 0), RPW), b = min(max(u.key_hi - k0, 0), RPW);
-              have_rows = a < b ? (0xffffffffu >> (32 - (b - a))) << a : 0u;
-              have_rows &= ~(marks[((block + values) % kMarks) * 4 + w * RPW / 32] >> (w * RPW % 32));
-              ++values;
+              const int j = two ? e / 2 : e + 1 == 2 * u.n ? u.n - 1 : e / 2 - 1, k0 = (u.kb0 + j) * BK + row0;
+              const int a = min(max(u.key_lo - k0, 0), N), b = min(max(u.key_hi - k0, 0), N);
+              have = a < b ? (0xffffffffu >> (32 - (b - a))) << a : 0u;
+              have &= ~(marks[((block + j) % kMarks) * 4 + row0 / 32] >> row0 % 32);
             }
-            convert(have_rows);
-            if (lane == 0) mbar_arrive(taken(raw_out));
-            raw_out = raw_out + 1 == NR ? 0 : raw_out + 1;
+            convert(std::integral_constant<int, N>(), sbase + L::RAW + raw_at * L::TILE_RAW, sbase + L::KV + at * L::TILE_KV, row0, have);
+            arrive(full(at));
+            if (lane == 0) mbar_arrive(taken(raw_at));
+            if (e == 0) convert_q();
           }
+          tiles += 2 * u.n;
           block += u.n;
         } else {
           // Every thread copies the pieces that it later converts, NR tiles ahead.
+          constexpr int N8 = RPW / RP8;   // steps
+          const uint32_t raw = sbase + L::RAW + w * (RPW * D);
           int staged = 0;
           unsigned rows_in[NR];   // which rows of the tiles on their way are there, newest first
           auto stage = [&] {
@@ -854,11 +918,15 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           };
 #pragma unroll 1
           for (int i = 0; i < NR; ++i) stage();
+          convert_q();
 #pragma unroll 1
           for (int e = 0; ok && e < 2 * u.n; ++e) {
             cp_wait<NR - 1>();
             if (!wait(empty(slot), phase)) break;
-            convert(rows_in[NR - 1]);
+            convert(std::integral_constant<int, RPW>(), sbase + L::RAW + raw_out * L::TILE_RAW, sbase + L::KV + slot * L::TILE_KV,
+                    w * RPW, rows_in[NR - 1]);
+            arrive(full(slot));
+            next_slot();
             raw_out = raw_out + 1 == NR ? 0 : raw_out + 1;
             stage();
           }
@@ -994,7 +1062,6 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           }
           return (sum0.x + sum0.y) + (sum1.x + sum1.y);
         };
-        const bool first = __any_sync(0xffffffffu, fresh);
         float rest0 = x[BK / 2], rest1 = x[BK / 2 + 1];   // largest a of the second half
 #pragma unroll
         for (int e = BK / 2 + 2; e < BK; e += 4) {
@@ -1002,7 +1069,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           if (e + 2 < BK) rest1 = fmaxf(fmaxf(x[e + 2], x[e + 3]), rest1);
         }
         for (int round = 0;; ++round) {
-          if (round > 0 || !first) sum = half(std::integral_constant<int, 0>());
+          sum = half(std::integral_constant<int, 0>());
           const bool move = valid && (fresh || !(sum <= kMostSum) || fmaxf(rest0, rest1) > kMostLog);
           // (a reference in the 2^30s is off by more than the range allows for: a few rounds)
           if (!__any_sync(0xffffffffu, move) || round == 4) break;
@@ -1120,26 +1187,25 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         ok = mbar_wait(bar(B_Q_EMPTY), (count - 1) & 1, abort, status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
-      if (!E4M3 && p.q_boxes) {
+      const uint32_t q_there = bar(E4M3 ? B_Q_RAW : B_Q_FULL);   // queries to be made fp16 get there first
+      if (p.q_boxes) {
         // 128 rows are whole tokens: a box of the group's heads for 128 / group tokens
         if (lane == 0) {
           if (w == 0) {
-            mbar_arrive_expect_tx(bar(B_Q_FULL), tiles * L::TILE_Q);
+            mbar_arrive_expect_tx(q_there, tiles * L::TILE_Q);
             for (int t = 0; t < tiles; ++t)
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
                 tma_load_3d(sbase + L::Q + t * L::TILE_Q + c * L::CHUNK_Q, &p.tm_q, c * 64, u.head_kv * group,
-                            u.token0 + p.group_div.quotient(u.row_first + t * 128), bar(B_Q_FULL));
+                            u.token0 + p.group_div.quotient(u.row_first + t * 128), q_there);
           } else {
-            mbar_arrive(bar(B_Q_FULL));
+            mbar_arrive(q_there);
           }
         }
-        __syncwarp();
         asked = count + 1;
-        continue;
       }
 #pragma unroll 1
-      for (int r0 = w * 32; r0 < u.rows; r0 += 64) {
+      for (int r0 = w * 32; !p.q_boxes && r0 < u.rows; r0 += 64) {
         const int r = r0 + lane, row = u.row_first + r, tok = p.group_div.quotient(row);
         const long long from = (u.token0 + tok) * p.q_row_stride + (u.head_kv * group + row - tok * group) * D;
         const unsigned valid = __ballot_sync(0xffffffffu, r < u.rows);
@@ -1153,64 +1219,25 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
           cp_async16(dst, p.q + (have ? o + c * 8 : 0), have);
         }
       }
-      if constexpr (E4M3) {
-        // To fp16 in place (every thread the pieces that it has copied), a row times a
-        // power of two that puts its largest value just below 2^15.
+      if (!p.q_boxes) {
         cp_commit();
         cp_wait<0>();
-#pragma unroll 1
-        for (int r0 = w * 32; r0 < u.rows; r0 += 64) {
-          constexpr int NB = 4;   // steps at a time
-          const int c = lane % CPR;
-          auto place = [&](int i) {
-            const int rr = r0 + i * RPI + lane / CPR;
-            return sbase + L::Q + (rr >> 7) * L::TILE_Q + (c >> 3) * L::CHUNK_Q + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4);
-          };
-#pragma unroll 1
-          for (int i0 = 0; i0 < 32 / RPI; i0 += NB) {
-            uint32_t words[NB][4], top[NB];
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(words[i][0]), "=r"(words[i][1]), "=r"(words[i][2]), "=r"(words[i][3])
-                           : "r"(place(i0 + i))
-                           : "memory");
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-              top[i] = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                top[i] = max(top[i], max(words[i][e] << 16 & 0x7FFF0000u, words[i][e] & 0x7FFF0000u));
-            }
-#pragma unroll
-            for (int x = CPR / 2; x > 0; x >>= 1)
-#pragma unroll
-              for (int i = 0; i < NB; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], x));
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-              // exponent field of the factor: 127 + 14 - (top's - 127), kept a normal number
-              const int ex = min(max(268 - static_cast<int>(top[i] >> 23), 1), 254);
-              const float f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
-              uint32_t out[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) out[e] = pack_f16x2(bf_lo(words[i][e]) * f, bf_hi(words[i][e]) * f);
-              st_shared_v4(place(i0 + i), out[0], out[1], out[2], out[3]);
-              if (c == 0)
-                q_scale[(count & 1) * ROWS + r0 + (i0 + i) * RPI + lane / CPR] =
-                    __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-            }
-          }
-        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_there);
       }
-      cp_commit();
-      cp_wait<0>();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_Q_FULL));
+      if constexpr (E4M3 && !L::LOADERS_CONVERT_Q) {
+        ok = mbar_wait(q_there, count & 1, abort, status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        convert_queries<D, 4>(sbase + L::Q, q_scale + (count & 1) * ROWS, u.rows, w, 2, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_Q_FULL));
+      }
     }
     if (!ok && asked > 0) {   // after an abort, what has been asked for lands before the block ends
       volatile int no_abort = 0;
-      mbar_wait(bar(B_Q_FULL), (asked - 1) & 1, &no_abort, status, 100000000ull);
+      mbar_wait(bar(E4M3 ? B_Q_RAW : B_Q_FULL), (asked - 1) & 1, &no_abort, status, 100000000ull);
     }
   }
 
@@ -1351,7 +1378,7 @@ cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
   }
   // Queries in boxes where 128 rows are whole tokens.
   p.q_boxes = 0;
-  if (!E4M3 && group <= 128 && (group & (group - 1)) == 0 && p.q_row_stride < (1ll << 39)) {
+  if (group <= 128 && (group & (group - 1)) == 0 && p.q_row_stride < (1ll << 39)) {
     if (!make_query_map(&p.tm_q, p, static_cast<int>(group))) return cudaErrorInvalidValue;
     p.q_boxes = 1;
   }
