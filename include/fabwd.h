@@ -386,7 +386,9 @@ size_t fa_extend_workspace_size(int head_dim);
  * num_tokens (a request cut off by num_tokens keeps its positions).  A row that
  * sees no key, and one that belongs to no request (from cu_new[batch] on; a
  * padded batch), gets o = 0, lse = -inf.  Contents of slots that no row of a
- * request sees do not matter (NaN included).  The weights exp(x - max) are
+ * request sees do not matter (NaN included); a value that is not finite and that
+ * some of a request's rows see may make NaN of others' outputs (0 times it), as
+ * in fa_fwd_*.  The weights exp(x - max) are
  * rounded to bf16 beside a bf16 cache (as in fa_fwd_*), to fp16 beside an e4m3
  * one; sums are fp32.  o must not overlap q.  workspace: 16-byte aligned,
  * contents arbitrary; calls whose work overlaps on the GPU need one each.

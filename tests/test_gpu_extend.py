@@ -210,6 +210,28 @@ def test_sizes_of_queries(q_scale, kv):
     p.check(*p.run())
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("course", ["climb", "fall", "turns", "last", "first", "zigzag"])
+def test_scores_far_apart(course, dim, kv):
+    """Scores along the keys that a weight of 32 bits cannot hold beside each
+    other, in every order: q . k = d a_j b with b the row's, a_j the key's."""
+    p = Problem([700, 130, 40], [9, 200, 300], 6, 2, dim, 24, kv, seed=dim)
+    base = p.k_scale.mean().item() * 448 if kv == "e4m3" else 8.0   # the most that a key may hold
+    span = p.table.shape[1] * 24
+    j = torch.arange(span)
+    a = {"climb": j / 700 - 0.2, "fall": 0.8 - j / 700, "turns": torch.where(j // 70 % 2 == 0, 1.0, -1.0) * (j + 1) / 1000,
+         "last": torch.where(j % 127 == 126, 1.0, -0.5), "first": torch.where(j == 0, 1.0, -0.5),
+         "zigzag": torch.where(j % 2 == 0, 1.0, -1.0) * (j + 1) / 1000}[course] * base * 0.9
+    scale = p.k_scale[:, None] if kv == "e4m3" else torch.ones(1)
+    for b, n in enumerate(p.lens.tolist()):
+        t = torch.arange(n)
+        p.k[p.table[b, t // 24].long(), t % 24] = (a[t, None, None] / scale).clamp(-448, 448).expand(n, 2, dim).to(p.k.dtype)
+    rows = torch.linspace(-12, 12, p.q.shape[0] * 6).reshape(-1, 6, 1)
+    p.q = rows.expand(p.q.shape).bfloat16().contiguous()
+    p.check(*p.run())
+
+
 def test_lengths_that_do_not_fit():
     """Lengths below 0 and below the number of new tokens (their first rows see
     nothing), past the table, and a request cut off by the rows of q."""
