@@ -20,17 +20,19 @@
 //
 // Work.  The units of all requests (requests in order, key/value heads, tiles
 // of rows) and their blocks of keys are laid out on a line by what they cost
-// (keys seen, and as much as a block for a unit's start and end), and the line
-// is cut into runs of equal length, one per SM: ragged lengths, one long
-// document and a causal mask's short first rows all load every SM alike, and
-// the host needs no lengths.  A unit that lies in several runs leaves partial
+// (keys seen, and what a unit's start and end take), and the line is cut into
+// runs of equal length, one per SM: ragged lengths, one long document and a
+// causal mask's short first rows all load every SM alike, and the host needs no
+// lengths.  A unit that lies in several runs leaves partial
 // results (at most two per run), which a second kernel joins in a fixed order.
 // The costs are closed forms of a request's numbers, so that every block finds
 // its run with one scan over the requests.
 //
 // Warps: per tile of 128 rows four for the softmax and the output, then four
-// that load keys and values, one that issues the products, one that walks along
-// the run and tells the others what is next, two that load queries.
+// that load keys and values (beside an 8-bit cache they make fp16 of them, eight
+// at head_dim 256), one that issues the products, one that walks along the run,
+// tells the others what is next and starts the copies by TMA, two that load
+// queries.
 //   Two tiles: the products of one run while the softmax works on the other,
 //   in the order P_A V, S_A (of the next block), P_B V, S_B.
 //   One tile (at most 128 rows): two score buffers, S of the next block is
@@ -192,6 +194,10 @@ __device__ __forceinline__ uint2 e4m3x4_f16(uint32_t x) {
 // form: costs only share out the work, so they are rounded as suits, but every block
 // has to come to the same ones.  Plain 32-bit integers, without a division: the walk
 // to a block's run is on the way of short calls.
+// A unit's start and end cost as much as two blocks of keys (one tile of rows: six):
+// with a cost of 1 for them 64 requests of 1 to 8 tokens take 125 us instead of 105,
+// 37 ragged ones with a window of 1024 113 instead of 83.  A block of one tile of rows
+// where the unit has room for two: as much as one of two, the ragged ones take 112.
 template <int D>
 struct Request {
   using S = Shape<D>;
@@ -1366,7 +1372,10 @@ cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
   p.cost_shift = S::kKeys == 128 ? 7 : 6;
   while (units >= (1ll << 30) / (3 * (keys >> p.cost_shift) + 32)) ++p.cost_shift;
   // Boxes of the largest power of two that divides a page, up to a warp's keys (8-bit
-  // caches: a block's).
+  // caches: a block's).  Without boxes, 16 bytes a thread at a time: 64 requests of 1 to
+  // 8 tokens 116 us instead of 105, chunks of 2048 985 instead of 909, 24 chunks over
+  // e4m3 heads of 256 132 instead of 99.  Boxes of less than 8 rows would be smaller than
+  // the swizzle's pattern.
   p.box_rows = 0;
   const long long most = std::max({p.kv.page_stride, p.kv.slot_stride, p.kv.head_stride});
   if (p.kv.page_size % 8 == 0 && p.max_pages > 0 && most < (1ll << 39)) {
@@ -1376,7 +1385,8 @@ cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
       return cudaErrorInvalidValue;
     p.box_rows = rows;
   }
-  // Queries in boxes where 128 rows are whole tokens.
+  // Queries in boxes where 128 rows are whole tokens (37 ragged requests with a window of
+  // 1024, 16 heads of 64: 94 us without, 83 with).
   p.q_boxes = 0;
   if (group <= 128 && (group & (group - 1)) == 0 && p.q_row_stride < (1ll << 39)) {
     if (!make_query_map(&p.tm_q, p, static_cast<int>(group))) return cudaErrorInvalidValue;
