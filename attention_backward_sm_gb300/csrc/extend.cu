@@ -1339,9 +1339,16 @@ bool make_page_map(CUtensorMap* m, const PagedCache& c, const void* base, int ro
                                  stride(c.page_stride, c.num_pages)};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.e4m3 ? c.head_dim : 64), 1, static_cast<cuuint32_t>(rows), 1};
   const cuuint32_t steps[4] = {1, 1, 1, 1};
+  // What a miss brings into the L2: no more than a head's row, since the next head's is
+  // read by another SM, much later (64 requests of 4 tokens over 8192 keys, 32 / 8 heads
+  // of 64: 261 us with 256 bytes, 221 so).
+  const int row = c.head_dim * (c.e4m3 ? 1 : 2);   // bytes
+  const auto promotion = row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                         : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                      : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   return enc(m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
              dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             c.e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             c.e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, promotion,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
