@@ -388,12 +388,12 @@ size_t fa_extend_workspace_size(int head_dim);
  * padded batch), gets o = 0, lse = -inf.  Contents of slots that no row of a
  * request sees do not matter (NaN included); a value that is not finite and that
  * some of a request's rows see may make NaN of others' outputs (0 times it), as
- * in fa_fwd_*.  The weights exp(x - max) are
- * rounded to bf16 beside a bf16 cache (as in fa_fwd_*), to fp16 beside an e4m3
- * one; sums are fp32.  o must not overlap q.  workspace: 16-byte aligned,
- * contents arbitrary; calls whose work overlaps on the GPU need one each.
- * Results do not depend on timing: the same call gives the same bits.  Waits
- * inside are bounded: fa_check_device_status reports one that ran out. */
+ * in fa_fwd_*.  The weights exp(x - max) are rounded to bf16 beside a bf16 cache
+ * (as in fa_fwd_*), to fp16 beside an e4m3 one; sums are fp32.  o must not
+ * overlap q.  workspace: 16-byte aligned, contents arbitrary; calls whose work
+ * overlaps on the GPU need one each.  Results do not depend on timing: the same
+ * call gives the same bits.  Waits inside are bounded: fa_check_device_status
+ * reports one that ran out. */
 int fa_extend(const fa_bf16* q, long long q_row_stride,
               const void* k_cache, const void* v_cache, int kv_type, const float* k_scale, const float* v_scale,
               long long page_stride, long long slot_stride, long long head_stride,
@@ -422,6 +422,8 @@ int fa_extend(const fa_bf16* q, long long q_row_stride,
  * q [num_tokens, H, d], k [num_tokens, Hkv, d] bf16, rows row_stride elements
  * apart (multiples of 8: slices of a fused projection need no copy), 16-byte
  * aligned; H or Hkv may be 0 (the tensor may then be NULL).  d 64, 128 or 256.
+ * The gradient, and many rows into a cache, wait inside for copies, bounded:
+ * fa_check_device_status reports a wait that ran out.
  * ------------------------------------------------------------------------ */
 enum fa_rope_layout {
     FA_ROPE_HALF = 0,         /* pairs (i, i + rotary_dim / 2) */
