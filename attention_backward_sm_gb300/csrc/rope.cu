@@ -938,6 +938,9 @@ int fa_qk_rope_bwd(const fa_bf16* dq_out, const fa_bf16* dk_out, long long dq_ou
     if (e != cudaSuccess) return cuda_fail(e, "rope gradient launch");
     return ok();
   }
+  // Without tokens only the weights' gradients are written; positions and freqs, which
+  // may then be NULL, are not read.
+  if (num_tokens == 0) p.rotary = 0;
   p.q.x = q, p.q.x_stride = q_row_stride;
   p.k.x = k, p.k.x_stride = k_row_stride;
   p.partial = static_cast<float*>(workspace);

@@ -242,6 +242,23 @@ def test_offsets_past_32_bits():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_weights_without_tokens_need_no_positions(dim):
+    """The C entry with weights and no tokens: zeros as the weights' gradients;
+    everything that belongs to tokens may be NULL."""
+    from attention_backward_sm_gb300._lib import load
+    f32, at = fab().FA_WEIGHT_F32, lambda t: t.data_ptr()  # noqa: E731
+    w = torch.ones(2, dim, device=DEV)
+    dw = torch.full((2, dim), 9.0, device=DEV)
+    size = fab().fa_qk_rope_bwd_workspace_size(dim)
+    work = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    rc = load().fa_qk_rope_bwd(None, None, 0, 0, None, None, 0, 0, None, None, dim, 0, 1.0, at(w[0]), at(w[1]), f32, 1e-6,
+                               0, 4, 2, dim, None, None, 0, 0, at(dw[0]), at(dw[1]), at(work), size,
+                               torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    assert torch.all(dw == 0)
+
+
 # ------------------------------------------------------------------ into the cache
 def cache_of(pages, page, Hkv, d, kv, layout="plain"):
     t = torch.full((pages, page, Hkv, d), -2.0, device=DEV).to(torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn)
