@@ -27,7 +27,7 @@ HOST_TAG = os.path.join(BUILD, "host_torch")   # the PyTorch that HOST was built
 SOURCES = ["api.cu", "small_kernels.cu", "fwd_main.cu", "bwd_main.cu", "bwd_d256.cu", "dq_main.cu", "noalloc.cu",
            "paged.cu", "rope.cu", "extend.cu", "decode.cu", "decode_d64.cu", "decode_d128.cu", "decode_d256.cu"]
 HEADERS = ["internal.h", "sm103.cuh", "paged.h", "decode.cuh", "decode_shape.h", "checks.h",
-           "quantise.cuh", "extend.h"]
+           "quantise.cuh", "extend.h", "extend_shape.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I" + os.path.join(ROOT, "include")]

@@ -1374,10 +1374,7 @@ cudaError_t launch_dim(ExtendParams p, const Device& dev, cudaStream_t s) {
   const long long keys = static_cast<long long>(p.max_pages) * p.kv.page_size + p.num_tokens;   // as the costs have it
   p.tile_keys16 = static_cast<int>(S::kRows * 16 / group);
   p.tile_tokens = static_cast<int>(S::kRows / group + 1);
-  // Costs per block of keys, or for as many as keep the sum of any lengths below 2^30.
-  const long long units = (p.num_tokens * group / S::kRows + p.batch) * p.kv.heads_kv;
-  p.cost_shift = S::kKeys == 128 ? 7 : 6;
-  while (units >= (1ll << 30) / (3 * (keys >> p.cost_shift) + 32)) ++p.cost_shift;
+  p.cost_shift = cost_shift(most_units(p.num_tokens, p.batch, p.heads, p.kv.heads_kv, D), keys, S::kKeys == 128 ? 7 : 6);
   // Boxes of the largest power of two that divides a page, up to a warp's keys (8-bit
   // caches: a block's).  Without boxes, 16 bytes a thread at a time: 64 requests of 1 to
   // 8 tokens 116 us instead of 105, chunks of 2048 985 instead of 909, 24 chunks over

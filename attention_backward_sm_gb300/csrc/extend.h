@@ -6,6 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "extend_shape.h"
 #include "paged.h"
 
 namespace fa {

@@ -481,8 +481,10 @@ int fa_extend(const fa_bf16* q, long long q_row_stride, const void* k_cache, con
                           heads, heads_kv);
   if (static_cast<long long>(heads) * head_dim > 65535 * 64)
     return set_last_error(FA_ERR_UNSUPPORTED, "heads * head_dim too large (%d * %d)", heads, head_dim);
-  // Rows (tokens by heads) and units (of a request and a key/value head) are counted with 32 bits.
-  if (static_cast<long long>(num_tokens) * heads > 0x7ff00000ll || static_cast<long long>(batch) * heads_kv > 0x7fffffffll)
+  // Rows (tokens by heads) and the costs of units are counted with 32 bits; every block
+  // looks at all requests (2^20 of them 8 ms) while others wait for it, 20 s at most.
+  if (batch > 1 << 28 || static_cast<long long>(num_tokens) * heads > 0x7ff00000ll ||
+      fa::extend::most_units(num_tokens, batch, heads, heads_kv, head_dim) >= fa::extend::kMostUnits)
     return set_last_error(FA_ERR_UNSUPPORTED, "%d tokens of %d requests and %d heads are too many", num_tokens, batch,
                           heads);
   if (window < 0) return set_last_error(FA_ERR_INVALID_ARG, "window must be >= 0, got %d", window);

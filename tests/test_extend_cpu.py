@@ -2,6 +2,8 @@
 oracle's pins and the refusals of the C entry point (before anything touches the
 device)."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -73,6 +75,53 @@ def _rc(lib, **kw):
 def test_refusals(lib, kw, code, word):
     assert _rc(lib, **kw) == code
     assert word in lib.fa_last_error()
+
+
+def test_units_that_the_costs_have_no_room_for(lib):
+    """From 2^25 units on (a request with tokens and a key/value head, at least one
+    each) the call is refused; requests without tokens, a padded batch's, are no
+    units."""
+    many = dict(heads=32, heads_kv=32, qs=4096, batch=1 << 20)
+    assert _rc(lib, **many, n=1 << 20) == 2 and b"too many" in lib.fa_last_error()
+    assert _rc(lib, **{**many, "batch": 1 << 25, "heads": 1, "heads_kv": 1, "qs": 128}, n=1 << 25) == 2
+    assert b"too many" in lib.fa_last_error()
+    for batch in (1 << 28 | 1, (1 << 31) - 1):   # nor can so many be looked at
+        assert _rc(lib, **{**many, "batch": batch}, n=100) == 2 and b"too many" in lib.fa_last_error()
+    for batch in (1 << 20, 1 << 28):
+        # passes, to the next refusal
+        assert _rc(lib, **{**many, "batch": batch}, n=100, window=-1) == 1 and b"window" in lib.fa_last_error()
+
+
+SHIFT = """
+#include <cstdio>
+#include "extend_shape.h"
+int main() {
+  long long units, keys;
+  int bits;
+  while (std::scanf("%lld %lld %d", &units, &keys, &bits) == 3) std::printf("%d\\n", fa::extend::cost_shift(units, keys, bits));
+}
+"""
+
+
+def test_costs_of_any_call_fit(tmp_path):
+    """The smallest step from a block's keys on with which the costs of all units
+    that are not refused stay below 2^30."""
+    (tmp_path / "main.cpp").write_text(SHIFT)
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "attention_backward_sm_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I" + csrc, str(tmp_path / "main.cpp"), "-o",
+                    str(tmp_path / "main")], check=True)
+    units = [0, 1, 2, 1000, 1 << 20, (1 << 24) - 1, 1 << 24, (1 << 25) - 1]
+    keys = [0, 1, 127, 128, 5000, 1 << 20, 0x7fff0000, 0x7fff0000 + 0x7ff00000]
+    calls = [(u, k, b) for u in units for k in keys for b in (6, 7)]
+    text = "".join("%d %d %d\n" % c for c in calls)
+    out = subprocess.run([str(tmp_path / "main")], input=text, capture_output=True, text=True, check=True, timeout=20)
+    shifts = [int(x) for x in out.stdout.split()]
+    assert len(shifts) == len(calls)
+    for (u, k, b), s in zip(calls, shifts):
+        most = lambda shift: u * (3 * (k >> shift) + 32)  # noqa: E731
+        assert most(s) < 1 << 30 and b <= s <= 63
+        # one less would not do (the quotient is rounded down: as much as a unit's cost away)
+        assert s == b or most(s - 1) + 3 * (k >> (s - 1)) + 32 >= 1 << 30
 
 
 def test_nothing_succeeds(lib):

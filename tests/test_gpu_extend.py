@@ -232,6 +232,25 @@ def test_scores_far_apart(course, dim, kv):
     p.check(*p.run())
 
 
+def test_a_padded_batch_of_a_million_requests():
+    """Requests without tokens are no units, however many there are."""
+    p = Problem([40, 3, 200], [3, 1, 2], 32, 32, 64, 16, seed=18, extra_width=0)
+    want = p.run()
+    a = p.device()
+    batch = 1 << 20
+    lens = torch.zeros(batch, dtype=torch.int32, device=DEV)
+    lens[:2], lens[batch - 1] = a["seq_lens"][:2], a["seq_lens"][2]
+    cu = torch.full((batch + 1,), 4, dtype=torch.int32, device=DEV)
+    cu[:2], cu[batch] = a["cu_new"][:2], a["cu_new"][3]
+    table = torch.full((batch, p.table.shape[1]), -1, dtype=torch.int32, device=DEV)
+    table[:2], table[batch - 1] = a["block_table"][:2], a["block_table"][2]
+    a.update(seq_lens=lens, cu_new=cu, block_table=table)
+    o, lse = fab().extend(**a)
+    fab().fa_check_device_status()
+    p.check(o, lse)
+    assert o.shape == want[0].shape
+
+
 def test_lengths_that_do_not_fit():
     """Lengths below 0 and below the number of new tokens (their first rows see
     nothing), past the table, and a request cut off by the rows of q."""
