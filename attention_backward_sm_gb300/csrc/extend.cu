@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
             const int first = r.pos0 + p.group_div.quotient(u.row_first);
             const int last = r.pos0 + p.group_div.quotient(u.row_first + u.rows - 1);
             u.key_hi = max(last + 1, 0);
-            u.key_lo = p.window > 0 ? min(max(first - p.window + 1, 0), u.key_hi) : 0;
+            u.key_lo = p.window > 0 ? min(max(max(first, 0) - p.window + 1, 0), u.key_hi) : 0;   // (tokens before 0 see nothing)
             const int kb = u.key_lo / BK;
             const int nblk = max(1, (u.key_hi + BK - 1) / BK - kb);   // a unit that sees nothing has one (masked) block
             // Block j starts at c + min(j cost >> spare, w - 1).  Those in [run_start, run_end):
@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
       // Visible keys [lo, hi), and of the warp's rows the largest lo and the smallest
       // hi; rows past the unit's are computed like any and not written.
       const int hi = valid ? pos + 1 : 0x7fffffff;
-      const int lo = valid && p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+      const int lo = valid && p.window > 0 ? max(max(pos, 0) - p.window + 1, 0) : 0;
       const int lo_most = __reduce_max_sync(0xffffffffu, lo), hi_least = __reduce_min_sync(0xffffffffu, hi);
       const float k_scale = E4M3 && p.kv.k_scale ? p.kv.k_scale[u.head_kv] : 1.f;
       float sl2 = 0.f;   // set once Q is there

@@ -232,6 +232,17 @@ def test_scores_far_apart(course, dim, kv):
     p.check(*p.run())
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 40, 30])
+def test_windows_before_the_first_key(window, dim, kv):
+    """Requests with fewer keys than new tokens, whose first rows lie before all
+    keys: no window, however wide, shifts what the others see."""
+    p = Problem([0, 0, 90], [60, 200, 70], 4, 2, dim, 16, kv, seed=19, window=window)
+    p.lens[0], p.lens[1], p.lens[2] = 50, 7, 40
+    p.check(*p.run())
+
+
 def test_a_padded_batch_of_a_million_requests():
     """Requests without tokens are no units, however many there are."""
     p = Problem([40, 3, 200], [3, 1, 2], 32, 32, 64, 16, seed=18, extra_width=0)
