@@ -412,6 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const __grid_constant_
         }
         fence_proxy_async_smem();
       }
+      // The epilogue waits for the last product by parity, so the one before it has
+      // to be over by then; the scores of this block do not tell, they are issued
+      // ahead of it.  (Once this warp has arrived below, its phase may pass, too.)
+      if (j > 0 && j + 1 == n && !mbar_wait(bar(B_O_DONE), (j - 1) & 1, abort, status)) { ok = false; break; }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar(B_P_READY0 + s));

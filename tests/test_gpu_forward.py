@@ -67,6 +67,25 @@ def test_forward_running_max_moves(grow):
     check_forward(case, q, k, v)
 
 
+@pytest.mark.parametrize("late", [0, 3], ids=["first_rows", "last_rows"])
+@pytest.mark.parametrize("keys", [64, 100, 128, 190, 256, 330, 384, 500])
+@pytest.mark.parametrize("d", [64, 256])
+def test_forward_rows_that_fall_behind(d, keys, late):
+    """Of four softmax warps one rescales O in every block (its rows' scores climb
+    from block to block by more than the reference's slack), the others never: they
+    end up to a block earlier, and must not take O before the last products."""
+    case = si.fixed("fwd_uneven_warps", 2, 64, d, 256, keys, False, 221, scale=d ** -0.5)
+    q, k, v, _ = case.tensors()
+    bk = 64 if d == 256 else 128
+    climb = 6.0 * (1 + torch.arange(keys) // bk).float()
+    k[..., 0] = climb.repeat(2)[:, None].to(torch.bfloat16)
+    # log2 of the weights grows by 12 a block where q's first value says so, else not
+    step = 12 / 1.4426950408889634 / 6.0 * d ** 0.5
+    row = torch.arange(q.shape[0]) % 128 // 32
+    q[..., 0] = torch.where(row == late, step, 0.0)[:, None].to(torch.bfloat16)
+    check_forward(case, q, k, v)
+
+
 # Causal grids whose tiles see very different numbers of keys launch in
 # chunks of (sequence, query head) units, longest tiles first; these shapes
 # leave a short last chunk (32 MiB of K and V per chunk), whose heads are
