@@ -68,8 +68,10 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A row's reference for the exponents moves where the weights of half a block add
-// up to more than kMostSum, or one of them exceeds 2^kMostLog.  bf16 weights and
-// the fp32 sums of 2^31 of them times values have room up to 2^127.
+// up to more than kMostSum, or one of them exceeds 2^kMostLog: fp16 weights have to stay
+// in their type's range, and beside bf16 ones the fp32 sums of n weights times values
+// have room for values up to 2^113 / n.
+constexpr float kMostLog = 14.5f, kMostSum = 0x1p15f;
 // fp16 weights (8-bit caches) are stored times 2^7: at most 2^15, and the
 // smallest step 2^-24 counts 2^-31 beside the row's largest weight.
 constexpr float kF16Shift = 7.f;
@@ -953,7 +955,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
     const int r = (warp & 3) * 32 + lane;                 // row of the tile (TMEM lane)
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lane_addr + L::COL_O + t * D;
-    constexpr float kShift = E4M3 ? kF16Shift : 0.f, kMostLog = E4M3 ? 14.5f : 60.f, kMostSum = E4M3 ? 0x1p15f : 0x1p60f;
+    constexpr float kShift = E4M3 ? kF16Shift : 0.f;
     // phases seen of S_FULL, of its third, of O_DONE, of O_LAST; blocks
     int s_used = 0, s_odd = 0, o_used = 0, done = 0, block = 0;
     // Rows that belong to no request, while there is nothing else to do.
@@ -1046,7 +1048,7 @@ __global__ void __launch_bounds__(Layout<D, E4M3>::THREADS, 1) extend_kernel(con
         }
         // The reference is that of the blocks before: floating-point weights may be
         // far above 1.  It moves only where a row has none yet and where its weights
-        // would come near the end of their type's range: then, rarely, the largest a
+        // would grow past kMostSum or 2^kMostLog: then, rarely, the largest a
         // is looked for and the first half is worked out again.  So the exponentials
         // wait for no maximum.
         float sum = 0.f;

@@ -232,6 +232,24 @@ def test_scores_far_apart(course, dim, kv):
     p.check(*p.run())
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("climb", [0.03, 0.3, 3.0])
+def test_large_values_behind_climbing_scores(climb, dim):
+    """Values of up to 2^100 and scores that climb along the keys, slowly and by more
+    than a block's slack: weights against an old reference do not carry the sums out
+    of the range of 32 bits."""
+    p = Problem([700, 130, 40], [9, 200, 300], 6, 2, dim, 24, seed=dim + 1, scale=1.0)
+    span = p.table.shape[1] * 24
+    j = torch.arange(span)
+    for b, n in enumerate(p.lens.tolist()):
+        t = torch.arange(n)
+        at = p.table[b, t // 24].long(), t % 24
+        p.k[at] = (climb * j[:n, None, None] / dim).expand(n, 2, dim).bfloat16()
+        p.v[at] = (p.v[at].float().clamp(-4, 4) * 2.0 ** 98).bfloat16()
+    p.q = torch.ones_like(p.q)
+    p.check(*p.run())
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("dim", [64, 256])
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 40, 30])
