@@ -225,8 +225,8 @@ def fa_bwd_noalloc(q, k, v, o, do, m, l, dq, dk, dv, cu_q_dev, cu_kv_dev, cu_q_h
 
 
 def fa_selftest_wait_timeout(stream=None):
-    """Launches a block whose bounded wait runs out (after 1 s); the next
-    fa_check_device_status raises FabwdError with FA_ERR_TIMEOUT."""
+    """Launches a block per status word whose bounded wait runs out (after 1 s);
+    the next fa_check_device_status raises FabwdError with FA_ERR_TIMEOUT."""
     _check(lib().fa_selftest_wait_timeout(_stream(stream)))
 
 

@@ -200,6 +200,21 @@ int check_device() {
   return FA_OK;
 }
 
+// The words in which bounded waits record that they ran out, and whose they are
+// (words of one caller one after the other).
+constexpr char kBackward[] = "fa_bwd";
+const struct {
+  const char* name;
+  cudaError_t (*word)(int**);
+  int (*read_and_clear)(cudaStream_t, int*);
+} kStatus[fa::kStatusWords] = {
+    {kBackward, fa::bwd_status_word, fa::bwd_read_and_clear_status},
+    {kBackward, fa::bwd256_status_word, fa::bwd256_read_and_clear_status},
+    {kBackward, fa::dq_status_word, fa::dq_read_and_clear_status},
+    {"the forward", fa::fwd_status_word, fa::fwd_read_and_clear_status},
+    {"fa_extend", fa::extend_status_word, fa::extend_read_and_clear_status},
+    {"fa_qk_rope_bwd or fa_qk_rope_append", fa::rope_status_word, fa::rope_read_and_clear_status}};
+
 }  // namespace
 
 namespace fa {
@@ -551,30 +566,35 @@ int fa_bwd_dq_finalize(const float* dq_acc, fa_bf16* dq, int total_q, int heads,
 int fa_selftest_wait_timeout(fa_stream_t stream) {
   int rc = check_device();
   if (rc) return rc;
-  cudaError_t e = fa::launch_wait_timeout(reinterpret_cast<cudaStream_t>(stream));
+  fa::StatusWords words;
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < fa::kStatusWords && e == cudaSuccess; ++i) e = kStatus[i].word(&words.at[i]);
+  if (e == cudaSuccess) e = fa::launch_wait_timeout(words, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "self-test launch");
   return ok();
 }
 
 int fa_check_device_status(fa_stream_t stream) {
-  int st = 0, st256 = 0, st_dq = 0, st_fwd = 0, st_ext = 0, st_rope = 0;
-  int e = fa::bwd_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st);
-  if (e == 0) e = fa::bwd256_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st256);
-  if (e == 0) e = fa::dq_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st_dq);
-  if (e == 0) e = fa::fwd_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st_fwd);
-  if (e == 0) e = fa::extend_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st_ext);
-  if (e == 0) e = fa::rope_read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &st_rope);
-  if (st == 0) st = st256;
-  if (st == 0) st = st_dq;
+  int st[fa::kStatusWords] = {};
+  int e = 0;
+  for (int i = 0; i < fa::kStatusWords && e == 0; ++i)
+    e = kStatus[i].read_and_clear(reinterpret_cast<cudaStream_t>(stream), &st[i]);
   if (e != 0) return cuda_fail(static_cast<cudaError_t>(e), "fa_check_device_status");
-  if (st == 4) return fail(FA_ERR_TIMEOUT, "a device-side wait in fa_bwd ran out of time (status %d)", st);
-  if (st != 0) return fail(FA_ERR_CUDA, "fa_bwd recorded device status %d", st);
-  if (st_fwd == 4) return fail(FA_ERR_TIMEOUT, "a device-side wait in the forward ran out of time (status %d)", st_fwd);
-  if (st_fwd != 0) return fail(FA_ERR_CUDA, "the forward recorded device status %d", st_fwd);
-  if (st_ext == 4) return fail(FA_ERR_TIMEOUT, "a device-side wait in fa_extend ran out of time (status %d)", st_ext);
-  if (st_ext != 0) return fail(FA_ERR_CUDA, "fa_extend recorded device status %d", st_ext);
-  if (st_rope != 0) return fail(FA_ERR_TIMEOUT, "a device-side wait in fa_qk_rope ran out of time (status %d)", st_rope);
-  return ok();
+  // all words are cleared now: the message names every caller that set one
+  int code = FA_OK;
+  char text[400] = "";
+  size_t at = 0;
+  const char* named = nullptr;
+  for (int i = 0; i < fa::kStatusWords; ++i) {
+    if (st[i] == 0 || kStatus[i].name == named) continue;
+    named = kStatus[i].name;
+    const bool timeout = st[i] == 4;
+    if (code == FA_OK) code = timeout ? FA_ERR_TIMEOUT : FA_ERR_CUDA;
+    at += snprintf(text + at, sizeof(text) - at,
+                   timeout ? "%sa device-side wait in %s ran out of time (status %d)" : "%s%s recorded device status %d",
+                   at ? "; " : "", kStatus[i].name, st[i]);
+  }
+  return code == FA_OK ? ok() : fail(code, "%s", text);
 }
 
 }  // extern "C"

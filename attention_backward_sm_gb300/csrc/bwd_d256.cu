@@ -808,6 +808,8 @@ cudaError_t launch_bwd256(const BwdParams& p, int batch, int max_kv_blocks, cuda
   return cudaGetLastError();
 }
 
+cudaError_t bwd256_status_word(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_bwd256_status); }
+
 int bwd256_read_and_clear_status(cudaStream_t s, int* status) {
   int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_bwd256_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);

@@ -1078,8 +1078,8 @@ namespace {
 // Waits, through the kernels' own bounded mbarrier wait, on a barrier that
 // nothing arrives on: the wait gives up after its time limit (1 s here,
 // shorter than the kernels' own) and records the timeout code in the
-// status word, and the kernel returns normally.
-__global__ void wait_timeout_kernel() {
+// block's status word, and the kernel returns normally.
+__global__ void wait_timeout_kernel(const StatusWords words) {
   __shared__ __align__(8) uint64_t never;
   __shared__ int abort_flag;
   if (threadIdx.x == 0) {
@@ -1088,15 +1088,17 @@ __global__ void wait_timeout_kernel() {
     mbar_init_fence();
   }
   __syncthreads();
-  if (threadIdx.x == 0) mbar_wait(smem_u32(&never), 0, &abort_flag, &g_bwd_status, 1000000000ull);
+  if (threadIdx.x == 0) mbar_wait(smem_u32(&never), 0, &abort_flag, words.at[blockIdx.x], 1000000000ull);
 }
 
 }  // namespace
 
-cudaError_t launch_wait_timeout(cudaStream_t s) {
-  wait_timeout_kernel<<<1, 32, 0, s>>>();
+cudaError_t launch_wait_timeout(const StatusWords& words, cudaStream_t s) {
+  wait_timeout_kernel<<<kStatusWords, 32, 0, s>>>(words);
   return cudaGetLastError();
 }
+
+cudaError_t bwd_status_word(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_bwd_status); }
 
 int bwd_read_and_clear_status(cudaStream_t s, int* status) {
   int zero = 0;

@@ -605,6 +605,8 @@ cudaError_t launch_dq(const BwdParams& p, int head_dim, int batch, int max_kv, c
   return head_dim == 64 ? launch_d<64>(p, batch, max_kv, s) : launch_d<128>(p, batch, max_kv, s);
 }
 
+cudaError_t dq_status_word(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_dq_status); }
+
 int dq_read_and_clear_status(cudaStream_t s, int* status) {
   int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_dq_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);

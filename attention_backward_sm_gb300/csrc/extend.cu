@@ -1426,6 +1426,8 @@ cudaError_t launch_extend(const ExtendParams& p, const Device& dev, cudaStream_t
                                 : launch_dim<256, false>(p, dev, s);
 }
 
+cudaError_t extend_status_word(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_extend_status); }
+
 int extend_read_and_clear_status(cudaStream_t s, int* status) {
   int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_extend_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);

@@ -77,5 +77,6 @@ inline size_t workspace_bytes(int head_dim) {
 
 cudaError_t launch_extend(const ExtendParams& p, const Device& dev, cudaStream_t s);
 int extend_read_and_clear_status(cudaStream_t s, int* status);
+cudaError_t extend_status_word(int** word);
 
 }  // namespace fa

@@ -907,6 +907,8 @@ cudaError_t launch_fwd_main(const FwdTcParams& p, int head_dim, int batch, int m
   return launch_d2<128>(p, batch, max_q_blocks, s);
 }
 
+cudaError_t fwd_status_word(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_fwd_status); }
+
 int fwd_read_and_clear_status(cudaStream_t s, int* status) {
   int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_fwd_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);

@@ -57,14 +57,22 @@ cudaError_t launch_bwd_main(const BwdParams& p, int head_dim, int batch, int max
 // dS K sums of every query row into dq_acc, one CTA per query block.
 cudaError_t launch_dq(const BwdParams& p, int head_dim, int batch, int max_kv, cudaStream_t s);
 int dq_read_and_clear_status(cudaStream_t s, int* status);
+cudaError_t dq_status_word(int** word);
 // (sequence, key/value head) units per launch-order chunk of a backward grid
 // with n_kvb key blocks of bm rows and query blocks of bn rows.
 int launch_head_chunk(const BwdParams& p, int batch, int n_kvb, int bm, int bn, int head_dim);
 // head_dim 256 (bwd_d256.cu): tm_q / tm_do with 64-row boxes, max_q_blocks in 64-row blocks
 cudaError_t launch_bwd256(const BwdParams& p, int batch, int max_kv_blocks, cudaStream_t s);
 int bwd256_read_and_clear_status(cudaStream_t s, int* status);
+cudaError_t bwd256_status_word(int** word);
 int bwd_read_and_clear_status(cudaStream_t s, int* status);
-cudaError_t launch_wait_timeout(cudaStream_t s);
+cudaError_t bwd_status_word(int** word);
+// One block per status word, each with a wait that runs out.
+constexpr int kStatusWords = 6;
+struct StatusWords {
+  int* at[kStatusWords];
+};
+cudaError_t launch_wait_timeout(const StatusWords& words, cudaStream_t s);
 
 cudaError_t launch_preprocess(const uint16_t* o, const uint16_t* dout, float* D, float* dq_acc, long long rows,
                               int head_dim, cudaStream_t s);
@@ -94,7 +102,9 @@ struct FwdTcParams {
 };
 cudaError_t launch_fwd_main(const FwdTcParams& p, int head_dim, int batch, int max_q_blocks, cudaStream_t s);
 int fwd_read_and_clear_status(cudaStream_t s, int* status);
+cudaError_t fwd_status_word(int** word);
 int rope_read_and_clear_status(cudaStream_t s, int* status);
+cudaError_t rope_status_word(int** word);
 
 // Sets a kernel's dynamic shared-memory limit once per device (the first
 // call with that device current); `done` is the kernel's per-device mask.

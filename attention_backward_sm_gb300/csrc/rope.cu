@@ -822,6 +822,8 @@ cudaError_t launch_forward(RopeParams& p, int head_dim, bool cache, const Device
 }  // namespace
 
 namespace fa {
+cudaError_t rope_status_word(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_rope_status); }
+
 int rope_read_and_clear_status(cudaStream_t s, int* status) {
   int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_rope_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);

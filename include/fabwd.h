@@ -480,21 +480,25 @@ int fa_qk_rope_append(const fa_bf16* q, const fa_bf16* k, const fa_bf16* v, long
                       long long page_stride, long long slot_stride, long long head_stride,
                       int num_pages, int page_size, int heads_kv, int head_dim, fa_stream_t stream);
 
-/* Diagnostic (the pages have no counterpart): launches one block that
+/* Diagnostic (the pages have no counterpart): launches a block for every
+ * status word (the backward's, the forward's, fa_extend's, the rotation's) that
  * waits, through the same bounded mbarrier wait the kernels use, on a
  * barrier nothing arrives on.  After its own short limit (1 s; the
  * kernels' waits give up after 20 s) it records
- * FA_ERR_TIMEOUT in the device status word and returns; nothing faults and
+ * FA_ERR_TIMEOUT in the status word and returns; nothing faults and
  * the context stays usable.  The next fa_check_device_status on `stream`
  * then returns FA_ERR_TIMEOUT.  Lets a caller test its handling of a timed
  * out kernel. */
 int fa_selftest_wait_timeout(fa_stream_t stream);
 
-/* Synchronises `stream`, then reads and clears the device status word
- * that bounded waits set.  Returns FA_OK, FA_ERR_TIMEOUT or FA_ERR_CUDA.
+/* Synchronises `stream`, then reads and clears the device status words
+ * that bounded waits set.  Returns FA_OK, FA_ERR_TIMEOUT or FA_ERR_CUDA; the
+ * message names every call whose word was set.
  * The outputs of the kernels launched before it are complete and valid
  * only when it returns FA_OK: after FA_ERR_TIMEOUT some CTAs stopped early
- * and dq_acc, dk, dv (or o, m, l) may be partial. */
+ * and their outputs (dq_acc, dk, dv; o, m, l; fa_extend's o and lse; dq, dk and
+ * the weights' gradients of fa_qk_rope_bwd; q_out and the cache's slots of
+ * fa_qk_rope_append) may be partial. */
 int fa_check_device_status(fa_stream_t stream);
 
 /* Message describing the last error returned on the calling thread

@@ -92,3 +92,27 @@ def test_bounded_wait_times_out_into_a_status_code():
     torch.cuda.synchronize()
     fab.fa_check_device_status()
     assert torch.isfinite(dq.float()).all() and torch.isfinite(dk.float()).all()
+
+
+def test_waits_of_all_calls_are_reported_together():
+    """Every call's status word is read, named and cleared, also where several
+    are set; each call works afterwards."""
+    import attention_backward_sm_gb300 as fab
+    fab.fa_check_device_status()
+    fab.fa_selftest_wait_timeout()
+    with pytest.raises(fab.FabwdError) as e:
+        fab.fa_check_device_status()
+    assert e.value.code == fab.FA_ERR_TIMEOUT
+    for name in ("fa_bwd", "the forward", "fa_extend", "fa_qk_rope_bwd or fa_qk_rope_append"):
+        assert str(e.value).count(f"wait in {name} ran out") == 1, str(e.value)
+    fab.fa_check_device_status()
+    T, d = 40, 64
+    x = torch.randn(T, 2, d, device="cuda").bfloat16()
+    positions, freqs = torch.arange(T, dtype=torch.int32, device="cuda"), fab.rope_freqs(d)
+    w = torch.ones(d, device="cuda")
+    cache = torch.zeros(4, 16, 2, d, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    fab.qk_rope_backward(x, x, positions, freqs, q=x, k=x, q_weight=w, k_weight=w)
+    fab.qk_rope_append(x, x, x, positions, freqs, cache, cache.clone(), torch.arange(T, device="cuda"))
+    fab.extend(x, cache, cache, torch.arange(4, **i32)[None], torch.tensor([T], **i32), torch.tensor([0, T], **i32), 0.1)
+    fab.fa_check_device_status()
