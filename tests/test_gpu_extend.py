@@ -153,6 +153,32 @@ def test_units_in_several_runs(old, new, heads, heads_kv, dim, kv):
     p.check(*p.run())
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,heads_kv,dim", [(40, 2, 64), (24, 1, 128), (128, 1, 64), (130, 1, 128), (300, 1, 64),
+                                                (144, 2, 256)])
+def test_large_groups(heads, heads_kv, dim, kv):
+    """Tiles that hold part of a token's heads, or several tokens and a part."""
+    p = Problem([37, 300, 0], [5, 1, 9], heads, heads_kv, dim, 16, kv, seed=heads)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_costs_counted_coarsely(dim, window, kv):
+    """Tables for 2^31 keys a request: costs count hundreds of keys at a time, so
+    that those of full tables would fit, and cut the few blocks there are."""
+    p = Problem([900, 0, 5, 2500] * 2, [20, 150, 1, 30] * 2, 8, 8, dim, 128, kv, window=window, seed=dim)
+    p.check(*p.run())
+    a = p.device()
+    width, rows = 0x7fff0000 // 128, p.table.shape[1]
+    flat = torch.full((width + 8 * rows,), -1, dtype=torch.int32, device=DEV)
+    flat[:8 * rows] = a["block_table"].flatten()
+    a["block_table"] = flat.as_strided((8, width), (rows, 1))   # entries past a request's own are not read
+    p.check(*fab().extend(**a))
+    fab().fa_check_device_status()
+
+
 def test_many_requests():
     rng = np.random.default_rng(5)
     new = [int(x) for x in rng.integers(0, 4, 1300)]

@@ -313,6 +313,33 @@ def test_append_is_rotation_then_append(shape, norm, kv, layout):
     assert torch.all(kc.reshape(-1, Hkv, d)[rest.to(DEV)].float() == -2)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("weight", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("norm", ["q", "k"])
+@pytest.mark.parametrize("T,H,Hkv,d,rotary", [(64, 8, 2, 128, 128), (5000, 12, 4, 128, 96), (6001, 4, 4, 256, 256),
+                                              (9000, 16, 2, 64, 64)])
+def test_append_with_one_norm(T, H, Hkv, d, rotary, norm, weight, kv):
+    """A norm of one tensor only, either type of weights, outputs scaled: few rows
+    and enough for the stream, which keep these in different places."""
+    p = Problem(T, H, Hkv, d, rotary, half=T % 2 == 0, norm=norm, weight=weight, mscale=1.25, seed=T + d)
+    page, pages = 16, T // 16 + 1
+    slots = torch.arange(T, device=DEV)
+    scales = {} if kv == "bf16" else {n: 0.01 + 0.01 * torch.rand(Hkv, device=DEV) for n in ("k_scale", "v_scale")}
+    kc, vc = (cache_of(pages, page, Hkv, d, kv) for _ in range(2))
+    q, k, v = p.on()
+    pos, freqs, kw = p.args()
+    p.check(fab().qk_rope_append(q, k, v, pos, freqs, kc, vc, slots, **scales, **kw), "q")
+    held = kc.reshape(-1, Hkv, d)[:T]
+    if kv == "bf16":
+        p.check(held, "k")
+        return
+    ref, s = p.want("k")
+    scale = f64(scales["k_scale"])[:, None]
+    ref, s = ref / scale, s / scale
+    err = np.abs(f64(held.float()) - np.clip(ref, -448, 448))
+    assert np.all(err <= np.maximum(np.abs(ref) * 2.0 ** -4, 2.0 ** -10) + 2.0 ** -18 * s)
+
+
 def test_append_in_place_and_without_pages():
     p = Problem(9, 2, 2, 64, 64, seed=9)
     pos, freqs, kw = p.args()
