@@ -322,8 +322,11 @@ struct Forward {
     } else if (place < 0) {
       return;
     } else if (p.kv.e4m3) {
-      // Rounded once: the turned values do not pass through bf16.  (A product with the
-      // reciprocal is within their fp32 error of the quotient.)
+      // Rounded to 8 bits once: the turned values do not pass through bf16.  The product
+      // with the rounded reciprocal is off by 2^-23 of the quotient at most, a fraction
+      // of the turned values' own fp32 error, so only values that lie that near to the border
+      // of two 8-bit ones may take the other (with the rounded quotient the values that
+      // differ from 64-bit arithmetic's are as many, 3 in 10^6, and 8191 rows 36.6 -> 37.2 us).
       const Scale sc(p.kv.k_scale, h);
       if (sc.lo > 0.f) {
         const float2 inv = both(__frcp_rn(sc.s));
@@ -499,7 +502,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
 }
 
 // Many tokens into a cache.  8191 rows of 32 / 8 heads of 128 with norms to e4m3 (185
-// MB): 36 us, 77 % of a copy's rate (rope_kernel: 43).
+// MB): 36.6 us, 75 % of a copy's rate (rope_kernel: 43).
 template <int D, bool NORM>
 __global__ void __launch_bounds__(kStreamThreads, 1) rope_stream_kernel(const RopeParams p) {
   constexpr int TPH = D / 16, HP = 512 / D, PASSES = 4;
@@ -542,11 +545,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) rope_stream_kernel(const Ro
 // ---------------------------------------------------------------- gradient
 // As the stream above, with two rows per job and 16 sums per lane for each weight's
 // gradient.  Each block leaves one partial sum per weight; weight_kernel adds them
-// in a fixed order.  16384 rows of 16 / 16 heads of 128 (403 MB): 81 us, 74 % of a
-// copy's rate; 5001 rows of 8 / 1 heads of 256 (69 MB): 25.7 us, 40 %.  Bound by its
-// instructions: 300 for a pass of 1 KB, their slots 44 % busy with 16 warps per SM,
-// which is what the rings and 128 registers leave (without the stores 62 us, without
-// the sines 73).
+// in a fixed order.  16384 rows of 16 / 16 heads of 128 (403 MB): 80 us, 75 % of a
+// copy's rate; 5001 rows of 8 / 1 heads of 256 (69 MB): 25.9 us, 40 %.  Bound by
+// latency: a pass of 1 KB is a chain of 300 instructions (two sums over a head's lanes
+// among them), and the 16 warps per SM that the rings and 128 registers leave keep the
+// issue slots 44 % busy (38 % at heads of 256).  Without the stores 62 us, without the
+// sines 73.
 template <int D>
 __global__ void __launch_bounds__(kStreamThreads, 1) rope_bwd_kernel(const RopeParams p) {
   constexpr int TPH = D / 16, HP = 512 / D, PASSES = 2;

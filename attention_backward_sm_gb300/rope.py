@@ -32,7 +32,8 @@ def _host():
 def rope_freqs(rotary_dim: int, base: float = 10000.0, factor: float = 1.0, original_len: int = 0, low: float = 1.0,
                high: float = 32.0, inv_freq=None, device="cuda") -> torch.Tensor:
     """Frequencies of rotary_dim / 2 pairs, int64 [rotary_dim / 2] on device:
-    theta_i = base^(-2i / rotary_dim) in turns per position times 2^64.
+    theta_i = base^(-2i / rotary_dim) in turns per position times 2^64, with the
+    53 significant bits of the float64 numbers they are computed in.
 
     For contexts longer than the trained one: factor alone divides every
     frequency (positions are interpolated).  With original_len, the trained

@@ -388,8 +388,10 @@ size_t fa_extend_workspace_size(int head_dim);
  * padded batch), gets o = 0, lse = -inf.  Contents of slots that no row of a
  * request sees do not matter (NaN included); a value that is not finite and that
  * some of a request's rows see may make NaN of others' outputs (0 times it), as
- * in fa_fwd_*.  The weights exp(x - max) are rounded to bf16 beside a bf16 cache
- * (as in fa_fwd_*), to fp16 beside an e4m3 one; sums are fp32.  o must not
+ * in fa_fwd_*.  The weights exp(x - r), where a row's r is at most 10.4 below its
+ * largest x, are rounded to bf16 beside a bf16 cache (as in fa_fwd_*; fa_decode
+ * keeps 16 bits of them), to fp16 beside an e4m3 one; sums are fp32, so
+ * values up to 2^113 over the number of keys cannot overflow.  o must not
  * overlap q.  workspace: 16-byte aligned, contents arbitrary; calls whose work
  * overlaps on the GPU need one each.  Results do not depend on timing: the same
  * call gives the same bits.  Waits inside are bounded: fa_check_device_status
@@ -414,10 +416,12 @@ int fa_extend(const fa_bf16* q, long long q_row_stride,
  *   rotary_dim  a multiple of 16 from 0 (the norm alone) to d
  *   positions   [num_tokens] int32 on the device (fa_kv_plan's), any value
  *   freqs       [rotary_dim / 2] on the device: theta_i / (2 pi) mod 1 as a
- *               64-bit fixed-point fraction of a turn (rounded times 2^64), which
- *               keeps the angle of any position exact to 2^-32 turns.  Stretched
- *               positions are other frequencies; mscale carries a factor of the
- *               outputs that goes with them (1 otherwise).
+ *               64-bit fixed-point fraction of a turn (rounded times 2^64).  The
+ *               product with a position loses nothing, whatever the position: an
+ *               angle is off by the frequency's own rounding times the position
+ *               and by about 2^-26 turns where it becomes fp32 for sine and
+ *               cosine.  Stretched positions are other frequencies; mscale carries
+ *               a factor of the outputs that goes with them (1 otherwise).
  *   weights     [d] of weight_type on the device, or NULL: no norm of this tensor
  * q [num_tokens, H, d], k [num_tokens, Hkv, d] bf16, rows row_stride elements
  * apart (multiples of 8: slices of a fused projection need no copy), 16-byte
@@ -468,7 +472,9 @@ int fa_qk_rope_bwd(const fa_bf16* dq_out, const fa_bf16* dk_out, long long dq_ou
  * q_out, k likewise into the cache, v goes into the cache as it is.  Cache,
  * slots (rows whose slot is outside the cache are skipped in the cache, their
  * q_out row is written) and scales as in fa_kv_append.  To an e4m3 cache a
- * rotated key is rounded once, as e4m3(y / k_scale[head]); values are stored as
+ * rotated key is rounded once, e4m3(y / k_scale[head]) of y in fp32, where y times
+ * the scale's fp32 reciprocal stands for the quotient (next to the border of two
+ * 8-bit values it may fall on the other side); values are stored as
  * fa_kv_append stores them.  q, k, v must not overlap the cache or q_out
  * (which may be q with the same stride). */
 int fa_qk_rope_append(const fa_bf16* q, const fa_bf16* k, const fa_bf16* v, long long q_row_stride,
