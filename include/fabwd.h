@@ -419,8 +419,7 @@ int fa_extend(const fa_bf16* q, long long q_row_stride,
  *               64-bit fixed-point fraction of a turn (rounded times 2^64).  The
  *               product with a position loses nothing, whatever the position: an
  *               angle is off by the frequency's own rounding times the position
- *               and by about 2^-26 turns where it becomes fp32 for sine and
- *               cosine.  Stretched positions are other frequencies; mscale carries
+ *               and by 2^-32 turns.  Stretched positions are other frequencies; mscale carries
  *               a factor of the outputs that goes with them (1 otherwise).
  *   weights     [d] of weight_type on the device, or NULL: no norm of this tensor
  * q [num_tokens, H, d], k [num_tokens, Hkv, d] bf16, rows row_stride elements

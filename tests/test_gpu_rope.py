@@ -144,6 +144,35 @@ def test_far_positions_and_scaled_frequencies(kw):
         p.check(got, n)
 
 
+@pytest.mark.parametrize("half", [True, False], ids=["half", "interleaved"])
+def test_angles_are_finer_than_32_bits(half):
+    """The weights' gradient of one row shows sines and cosines in fp32: with x = 1
+    and dy = 1 in the first value of every pair they are cos t and -sin t.  Where
+    they are small, an angle rounded to 24 bits (9e-8 radians) would stand out:
+    off by 2^-20 of the value (the norm's factor and five roundings) and by 2^-32
+    turns, of which 2^-28 radians leaves twice the room."""
+    d = 256
+    freqs, w = fab().rope_freqs(d), torch.ones(d, device=DEV)
+    x = torch.ones(1, 1, d, dtype=torch.bfloat16, device=DEV)
+    first = torch.arange(d) < d // 2 if half else torch.arange(d) % 2 == 0
+    dy = first.bfloat16().to(DEV).view(1, 1, d)
+    layout = fab().FA_ROPE_HALF if half else fab().FA_ROPE_INTERLEAVED
+    seen = 0
+    for position in (1, 7, 100, -1000, 4095, 50021, 65535):
+        pos = torch.tensor([position], dtype=torch.int32, device=DEV)
+        got = f64(fab().qk_rope_backward(dy, None, pos, freqs, layout=layout, q=x, q_weight=w)[2])
+        t = position * rope.frequencies(d)
+        ref = np.empty(d)
+        ref[first.numpy()], ref[~first.numpy()] = np.cos(t), -np.sin(t)
+        ref /= np.sqrt(1 + 1e-6)
+        small = np.abs(ref) < 2.0 ** -5
+        seen += small.sum()
+        err = np.abs(got - ref)
+        assert np.all(err[small] <= 2.0 ** -20 * np.abs(ref[small]) + 2.0 ** -28), f"off by {err[small].max():.3e}"
+        assert np.all(err <= 2.0 ** -20)
+    assert seen > 150
+
+
 def test_one_tensor_alone():
     p = Problem(70, 4, 2, 128, 128, norm="qk", seed=4)
     q, k, _ = p.on()
